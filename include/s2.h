@@ -18,7 +18,7 @@
  *
  * Common conventions
  *  - Every pointer argument is DEVICE memory owned by the caller, except the
- *    host_* arguments of s2_pipeline_dense_host. The library allocates
+ *    host_* arguments of s2_pipeline_dense_host and s2_wait_faults. The library allocates
  *    nothing and keeps no pointer after a call returns.
  *  - Every call is asynchronous on `stream` (NULL = the legacy default
  *    stream) and never synchronises the host. Validation errors are returned
@@ -365,6 +365,70 @@ S2_API s2_status s2_pipeline_workspace_size(s2_dtype dt, uint32_t W, uint64_t n,
 S2_API s2_status s2_pipeline_dense_host(const void *host_grad, s2_dtype dt, uint32_t W, uint64_t n,
                                  s2_params p, float scale, float *host_out, void *workspace,
                                  size_t workspace_bytes, s2_stream_t stream);
+
+/*
+ * The 8-bit layer -- the step that makes the gradients the calls above
+ * compress. A layer's activations and weights are kept in 8 bits, multiplied
+ * in 8 bits, and the weight gradient is taken from the 8-bit activations
+ * straight into a worker's row of grad[W][n].
+ *
+ * Packed matrix: codes [rows][cols], one byte each, row stride in elements,
+ * base 16-byte aligned and row stride a multiple of 16 (S2_ERR_ALIGNMENT;
+ * bytes between a row's end and the next row are neither read nor written),
+ * and scale bytes, contiguous. A code is an e4m3 number (sign, 4 exponent bits
+ * with bias 7, 3 mantissa bits; subnormals; 0x7f and 0xff are NaN, there is
+ * no infinity, the largest is 448); the byte b of its block scales it by
+ * 2^(b - 127). nblk = ceil(cols / 128):
+ *   S2_SCALE_ROWS:  scales [rows][nblk], a block is 128 elements of one row
+ *                   (activations, gradients of outputs);
+ *   S2_SCALE_TILES: scales [ceil(rows/128)][nblk], a block is 128 x 128
+ *                   elements (weights: the transpose has the same values).
+ * Sizes up to 2^31 - 1 (S2_ERR_UNSUPPORTED). Row strides of the other
+ * matrices are in elements and need only cover a row. A size of zero is valid.
+ */
+typedef enum {
+    S2_SCALE_ROWS = 0,
+    S2_SCALE_TILES = 1
+} s2_scale_layout;
+
+/*
+ * s2_pack8 -- x [rows][cols] of type dt to codes and scales. A block's scale
+ * is the least 2^e, e >= -117, with no finite element above 448 * 2^e; a code
+ * is its element divided by the scale, rounded to nearest, ties to even. NaN
+ * and infinities become NaN codes and leave their block's scale alone. (So
+ * the bytes are 10..247 and code * scale is exact in float32 and bfloat16.)
+ * codes_t / scales_t (both or neither; S2_SCALE_TILES only): also the
+ * transposed matrix, codes_t [cols][rows] with row stride ldct, scales_t
+ * [ceil(cols/128)][ceil(rows/128)], for the product with the weight's
+ * transpose (the gradient of a layer's input).
+ * rows * nblk must be below 2^32 (S2_ERR_UNSUPPORTED).
+ */
+S2_API s2_status s2_pack8(const void *x, s2_dtype dt, uint64_t rows, uint64_t cols, uint64_t ldx,
+                          s2_scale_layout layout, uint8_t *codes, uint64_t ldc, uint8_t *scales, uint8_t *codes_t,
+                          uint64_t ldct, uint8_t *scales_t, s2_stream_t stream);
+
+/* s2_unpack8 -- the values of a packed matrix: out [rows][cols] of type dt, row stride ldo. */
+S2_API s2_status s2_unpack8(const uint8_t *codes, uint64_t ldc, const uint8_t *scales, s2_scale_layout layout,
+                            uint64_t rows, uint64_t cols, void *out, s2_dtype dt, uint64_t ldo, s2_stream_t stream);
+
+/*
+ * s2_matmul8 -- y[m][n] = sum over k of X[m][k] * W[n][k], of type dt, with
+ *   X [M][K] packed with S2_SCALE_ROWS (a layer's input, or the gradient of
+ *   its output) and W [N][K] packed with either layout (its weight, or the
+ *   transposed weight). Sums are float32; one rounding to dt. The result does
+ *   not depend on timing. Serves one token (M = 1) as well as a batch.
+ */
+S2_API s2_status s2_matmul8(const uint8_t *x, uint64_t ldx, const uint8_t *x_scales, const uint8_t *w, uint64_t ldw,
+                            const uint8_t *w_scales, s2_scale_layout w_layout, uint64_t M, uint64_t N, uint64_t K,
+                            void *y, s2_dtype dt, uint64_t ldy, s2_stream_t stream);
+
+/*
+ * s2_wait_faults -- how many waits inside s2_matmul8 and s2_wgrad8 kernels
+ * ran out on the current device since the library was loaded (0 unless
+ * something is broken; outputs of the call concerned are not valid then).
+ * host_count is HOST memory; this call, a diagnostic, waits for the device.
+ */
+S2_API s2_status s2_wait_faults(uint32_t *host_count);
 
 /* Human-readable name of a status code (static string). */
 S2_API const char *s2_status_string(s2_status st);

@@ -46,6 +46,12 @@ __all__ = [
     "s2_hash",
     "s2_pipeline_workspace_size",
     "s2_pipeline_dense_host",
+    "s2_pack8",
+    "s2_unpack8",
+    "s2_matmul8",
+    "s2_wait_faults",
+    "S2_SCALE_ROWS",
+    "S2_SCALE_TILES",
     "s2_status_string",
     "s2_version",
     "S2_F32",
@@ -89,6 +95,10 @@ _SIGS = {
     "s2_hash": ([_vp, _u64, Params, _vp, _vp, _vp], _i32),
     "s2_pipeline_workspace_size": ([_i32, _u32, _u64, Params, ctypes.POINTER(_sz)], _i32),
     "s2_pipeline_dense_host": ([_vp, _i32, _u32, _u64, Params, _f32, _vp, _vp, _sz, _vp], _i32),
+    "s2_pack8": ([_vp, _i32, _u64, _u64, _u64, _i32, _vp, _u64, _vp, _vp, _u64, _vp, _vp], _i32),
+    "s2_unpack8": ([_vp, _u64, _vp, _i32, _u64, _u64, _vp, _i32, _u64, _vp], _i32),
+    "s2_matmul8": ([_vp, _u64, _vp, _vp, _u64, _vp, _i32, _u64, _u64, _u64, _vp, _i32, _u64, _vp], _i32),
+    "s2_wait_faults": ([ctypes.POINTER(_u32)], _i32),
     "s2_status_string": ([_i32], ctypes.c_char_p),
     "s2_version": ([], ctypes.c_char_p),
 }
@@ -392,9 +402,94 @@ def s2_pipeline_dense_host(host_grad: torch.Tensor, d: int, w: int, seed: int, h
                  _stream(stream)), "s2_pipeline_dense_host")
 
 
+# ---- the 8-bit layer ----
+
+S2_SCALE_ROWS, S2_SCALE_TILES = 0, 1
+_LAYOUTS = {"rows": S2_SCALE_ROWS, "tiles": S2_SCALE_TILES}
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+_BYTES = (torch.uint8,)
+
+
+def _mat(t: torch.Tensor, name: str, dtypes, rows: int = -1, cols: int = -1):
+    """Pointer, shape and row stride of a matrix whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    r, c = t.shape
+    if (rows >= 0 and r != rows) or (cols >= 0 and c != cols):
+        raise ValueError(f"{name} is {r} x {c}, expected {rows if rows >= 0 else r} x {cols if cols >= 0 else c}")
+    ld, one = t.stride()
+    if one != 1 and c > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), r, c, ld
+
+
+def _scales(t: torch.Tensor, name: str, rows: int, cols: int, layout: int):
+    n = ((rows + 127) // 128 if layout else rows) * ((cols + 127) // 128)
+    return _dev(t, name, _BYTES, n)
+
+
+def _layout(layout) -> int:
+    return _LAYOUTS[layout] if isinstance(layout, str) else int(layout)
+
+
+def s2_pack8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, layout="rows",
+             codes_t: Optional[torch.Tensor] = None, scales_t: Optional[torch.Tensor] = None, stream=None) -> None:
+    """x [rows, cols] -> codes [rows, cols] and scale bytes; "rows": a scale for each 128 elements of a row,
+    "tiles": for each 128 x 128 elements, and then also the transposed codes_t [cols, rows] and scales_t."""
+    lay = _layout(layout)
+    px, rows, cols, ldx = _mat(x, "x", _GRAD)
+    pc, _, _, ldc = _mat(codes, "codes", _CODES, rows, cols)
+    pt, ldt, pst = None, 0, None
+    if codes_t is not None:
+        pt, _, _, ldt = _mat(codes_t, "codes_t", _CODES, cols, rows)
+    if scales_t is not None:
+        pst = _scales(scales_t, "scales_t", cols, rows, lay)
+    _check(_f("s2_pack8")(px, _dtype_code(x), rows, cols, ldx, lay, pc, ldc, _scales(scales, "scales", rows, cols, lay),
+                          pt, ldt, pst, _stream(stream)), "s2_pack8")
+
+
+def s2_unpack8(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor, layout="rows", stream=None) -> None:
+    """The values of a packed matrix: codes [rows, cols] and scale bytes -> out [rows, cols]."""
+    lay = _layout(layout)
+    pc, rows, cols, ldc = _mat(codes, "codes", _CODES)
+    po, _, _, ldo = _mat(out, "out", _GRAD, rows, cols)
+    _check(_f("s2_unpack8")(pc, ldc, _scales(scales, "scales", rows, cols, lay), lay, rows, cols, po, _dtype_code(out),
+                            ldo, _stream(stream)), "s2_unpack8")
+
+
+def s2_matmul8(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, y: torch.Tensor,
+               w_layout="tiles", stream=None) -> None:
+    """y [M, N] = X W^T of packed X [M, K] (layout "rows") and W [N, K]."""
+    lay = _layout(w_layout)
+    px, M, K, ldx = _mat(x, "x", _CODES)
+    pw, N, _, ldw = _mat(w, "w", _CODES, -1, K)
+    py, _, _, ldy = _mat(y, "y", _GRAD, M, N)
+    _check(_f("s2_matmul8")(px, ldx, _scales(x_scales, "x_scales", M, K, 0), pw, ldw,
+                            _scales(w_scales, "w_scales", N, K, lay), lay, M, N, K, py, _dtype_code(y), ldy,
+                            _stream(stream)), "s2_matmul8")
+
+
+def s2_wait_faults() -> int:
+    """Waits of the tensor-core kernels that ran out on the current device (waits for the device)."""
+    c = _u32()
+    _check(_f("s2_wait_faults")(ctypes.byref(c)), "s2_wait_faults")
+    return int(c.value)
+
+
 # ---- allocation helpers (torch owns the memory; the library never allocates) ----
 
 def alloc_encode_outputs(W: int, n: int, d: int, w: int, device="cuda") -> Tuple[torch.Tensor, torch.Tensor]:
     return (torch.empty((W, nwords(n)), dtype=torch.int32, device=device),
             torch.empty((W, d, w), dtype=torch.float32, device=device))
 
+
+
+def alloc_pack8(rows: int, cols: int, layout="rows", device="cuda") -> Tuple[torch.Tensor, torch.Tensor]:
+    """Codes [rows, cols] whose rows start on 16 bytes, and scale bytes, for s2_pack8."""
+    codes = torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.uint8, device=device)[:, :cols]
+    srows = (rows + 127) // 128 if _layout(layout) == S2_SCALE_TILES else rows
+    return codes, torch.empty((srows, (cols + 127) // 128), dtype=torch.uint8, device=device)

@@ -2,6 +2,7 @@
 // entry point checks its arguments completely before anything is launched,
 // then queues its kernels on the caller's stream and returns.
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "s2.h"  // include/ is on the include path
@@ -297,6 +298,52 @@ PipelineLayout pipeline_layout(s2_dtype dt, uint32_t W, uint64_t n, s2_params p)
     off += round256(dense_workspace_bytes(n, p.d));
     L.total = off;
     return L;
+}
+
+// ---- 8-bit layer ----
+constexpr uint64_t kMaxDim8 = 0x7fffffffull;  // sizes travel as 32-bit coordinates
+
+inline uint64_t blocks8(uint64_t n) { return (n + 127) / 128; }
+inline uint64_t size_of(s2_dtype dt) { return dt == S2_F32 ? 4 : 2; }
+inline bool dtype_ok(s2_dtype dt) { return dt == S2_F32 || dt == S2_BF16; }
+inline bool layout_ok(s2_scale_layout l) { return l == S2_SCALE_ROWS || l == S2_SCALE_TILES; }
+
+// Bytes from the first to the last element of `rows` rows, `ld` elements apart.
+inline uint64_t extent(uint64_t rows, uint64_t cols, uint64_t ld, uint64_t esz) {
+    return rows && cols ? ((rows - 1) * ld + cols) * esz : 0;
+}
+
+// A matrix argument: its row stride covers a row and its bytes are addressable.
+inline s2_status check_matrix(uint64_t rows, uint64_t cols, uint64_t ld) {
+    if (rows > kMaxDim8 || cols > kMaxDim8 || ld >= (1ull << 38)) return S2_ERR_UNSUPPORTED;
+    return rows > 1 && ld < cols ? S2_ERR_INVALID_ARG : S2_OK;
+}
+
+// Codes: rows start on 16 bytes, as the tiled copies need them.
+inline s2_status check_codes(const void* codes, uint64_t rows, uint64_t cols, uint64_t ld) {
+    const s2_status st = check_matrix(rows, cols, ld);
+    if (st != S2_OK) return st;
+    if (!codes) return S2_ERR_INVALID_ARG;
+    return aligned(codes, 16) && (rows <= 1 || ld % 16 == 0) ? S2_OK : S2_ERR_ALIGNMENT;
+}
+
+inline s2_status first_error(std::initializer_list<s2_status> all) {
+    for (s2_status st : all)
+        if (st != S2_OK) return st;
+    return S2_OK;
+}
+
+struct Span {
+    const void* p;
+    uint64_t bytes;
+};
+// Some output overlaps an input or another output (the first `outs` spans are outputs).
+inline bool clash(std::initializer_list<Span> spans, size_t outs) {
+    for (size_t i = 0; i < outs; ++i)
+        for (size_t j = i + 1; j < spans.size(); ++j)
+            if (overlap(spans.begin()[i].p, spans.begin()[i].bytes, spans.begin()[j].p, spans.begin()[j].bytes))
+                return true;
+    return false;
 }
 
 }  // namespace
@@ -658,6 +705,80 @@ s2_status s2_pipeline_dense_host(const void* host_grad, s2_dtype dt, uint32_t W,
         cudaMemcpyAsync(host_out, d_out, (size_t)n * 4, cudaMemcpyDeviceToHost, s) != cudaSuccess)
         return S2_ERR_CUDA;
     return S2_OK;
+}
+
+s2_status s2_pack8(const void* x, s2_dtype dt, uint64_t rows, uint64_t cols, uint64_t ldx, s2_scale_layout layout,
+                   uint8_t* codes, uint64_t ldc, uint8_t* scales, uint8_t* codes_t, uint64_t ldct, uint8_t* scales_t,
+                   s2_stream_t stream) {
+    if (!dtype_ok(dt) || !layout_ok(layout)) return S2_ERR_INVALID_ARG;
+    const bool tiles = layout == S2_SCALE_TILES;
+    if ((codes_t != nullptr) != (scales_t != nullptr) || (codes_t && !tiles)) return S2_ERR_INVALID_ARG;
+    s2_status st = check_matrix(rows, cols, ldx);
+    if (st != S2_OK) return st;
+    const uint64_t nblk = blocks8(cols), nrow = blocks8(rows);
+    if (rows * nblk > 0xffffffffull || (tiles && nrow * nblk > kMaxDim8)) return S2_ERR_UNSUPPORTED;
+    if (rows == 0 || cols == 0) return S2_OK;
+    if (!x || !scales) return S2_ERR_INVALID_ARG;
+    st = first_error({check_codes(codes, rows, cols, ldc), codes_t ? check_codes(codes_t, cols, rows, ldct) : S2_OK});
+    if (st != S2_OK) return st;
+    if (!aligned(x, size_of(dt))) return S2_ERR_ALIGNMENT;
+    const uint64_t ns = (tiles ? nrow : rows) * nblk;
+    if (clash({{codes, extent(rows, cols, ldc, 1)}, {scales, ns}, {codes_t, extent(cols, rows, ldct, 1)},
+               {scales_t, ns}, {x, extent(rows, cols, ldx, size_of(dt))}}, 4))
+        return S2_ERR_INVALID_ARG;
+    Pack8Args a{x, ldx, codes, ldc, scales, codes_t, ldct, scales_t, rows, (uint32_t)cols, (uint32_t)nblk,
+                (uint32_t)nrow, (uint32_t)(rows * nblk)};
+    return cuda_status(launch_pack8(a, dt == S2_F32 ? 0 : 1, tiles, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+s2_status s2_unpack8(const uint8_t* codes, uint64_t ldc, const uint8_t* scales, s2_scale_layout layout, uint64_t rows,
+                     uint64_t cols, void* out, s2_dtype dt, uint64_t ldo, s2_stream_t stream) {
+    if (!dtype_ok(dt) || !layout_ok(layout)) return S2_ERR_INVALID_ARG;
+    s2_status st = check_matrix(rows, cols, ldo);
+    if (st != S2_OK) return st;
+    const uint64_t nblk = blocks8(cols);
+    if (rows * nblk > 0xffffffffull) return S2_ERR_UNSUPPORTED;
+    if (rows == 0 || cols == 0) return S2_OK;
+    if (!out || !scales) return S2_ERR_INVALID_ARG;
+    st = check_codes(codes, rows, cols, ldc);
+    if (st != S2_OK) return st;
+    if (!aligned(out, size_of(dt))) return S2_ERR_ALIGNMENT;
+    const uint64_t ns = (layout == S2_SCALE_TILES ? blocks8(rows) : rows) * nblk;
+    if (clash({{out, extent(rows, cols, ldo, size_of(dt))}, {codes, extent(rows, cols, ldc, 1)}, {scales, ns}}, 1))
+        return S2_ERR_INVALID_ARG;
+    Unpack8Args a{codes, ldc, scales, layout == S2_SCALE_TILES ? 7u : 0u, out, ldo, (uint32_t)cols, (uint32_t)nblk,
+                  (uint32_t)(rows * nblk)};
+    return cuda_status(launch_unpack8(a, dt == S2_F32 ? 0 : 1, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+s2_status s2_matmul8(const uint8_t* x, uint64_t ldx, const uint8_t* x_scales, const uint8_t* w, uint64_t ldw,
+                     const uint8_t* w_scales, s2_scale_layout w_layout, uint64_t M, uint64_t N, uint64_t K, void* y,
+                     s2_dtype dt, uint64_t ldy, s2_stream_t stream) {
+    if (!dtype_ok(dt) || !layout_ok(w_layout)) return S2_ERR_INVALID_ARG;
+    s2_status st = first_error({check_matrix(M, N, ldy), check_matrix(M, K, ldx), check_matrix(N, K, ldw)});
+    if (st != S2_OK) return st;
+    if (M == 0 || N == 0) return S2_OK;
+    if (!y) return S2_ERR_INVALID_ARG;
+    const uint64_t esz = size_of(dt);
+    if (!aligned(y, esz)) return S2_ERR_ALIGNMENT;
+    if (K == 0)  // an empty sum
+        return cuda_status(cudaMemset2DAsync(y, (M > 1 ? ldy : N) * esz, 0, N * esz, M,
+                                             reinterpret_cast<cudaStream_t>(stream)));
+    if (!x_scales || !w_scales) return S2_ERR_INVALID_ARG;
+    st = first_error({check_codes(x, M, K, ldx), check_codes(w, N, K, ldw)});
+    if (st != S2_OK) return st;
+    const uint64_t nblk = blocks8(K);
+    if (clash({{y, extent(M, N, ldy, esz)}, {x, extent(M, K, ldx, 1)}, {x_scales, M * nblk}, {w, extent(N, K, ldw, 1)},
+               {w_scales, (w_layout == S2_SCALE_TILES ? blocks8(N) : N) * nblk}}, 1))
+        return S2_ERR_INVALID_ARG;
+    Matmul8Args a{x, x_scales, w, w_scales, y, M > 1 ? ldx : (K + 15) / 16 * 16, N > 1 ? ldw : (K + 15) / 16 * 16, ldy,
+                  (uint32_t)M, (uint32_t)N, (uint32_t)K, w_layout == S2_SCALE_TILES ? 7u : 0u, dt == S2_F32 ? 0 : 1};
+    return cuda_status(launch_matmul8(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+s2_status s2_wait_faults(uint32_t* host_count) {
+    if (!host_count) return S2_ERR_INVALID_ARG;
+    return cuda_status(read_wait_faults(host_count));
 }
 
 const char* s2_status_string(s2_status st) {

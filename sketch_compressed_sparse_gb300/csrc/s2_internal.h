@@ -129,6 +129,65 @@ cudaError_t noalloc_compact_scratch(uint32_t** counts, uint32_t** offsets);
 cudaError_t launch_hash(const uint32_t* idx, uint64_t m, uint32_t d, uint32_t w, RowKeys keys,
                         uint32_t* bucket_out, int8_t* sign_out, cudaStream_t s);
 
+// ---- 8-bit layer: packing, products of packed matrices ----------------------
+struct Pack8Args {
+    const void* x;
+    uint64_t ldx;
+    uint8_t* codes;
+    uint64_t ldc;
+    uint8_t* scales;
+    uint8_t* codes_t;  // transposed copy of the codes (tiles only), or nullptr
+    uint64_t ldct;
+    uint8_t* scales_t;
+    uint64_t rows;
+    uint32_t cols;
+    uint32_t nblk;      // blocks per row
+    uint32_t nrow_blk;  // row blocks (tiles only)
+    uint32_t items;     // rows * nblk
+};
+struct Unpack8Args {
+    const uint8_t* codes;
+    uint64_t ldc;
+    const uint8_t* scales;
+    uint32_t row_shift;  // 0: a scale per row, 7: per 128 rows
+    void* out;
+    uint64_t ldo;
+    uint32_t cols;
+    uint32_t nblk;
+    uint32_t items;  // rows * nblk
+};
+// dtype: 0 = f32, 1 = bf16; at least one element.
+cudaError_t launch_pack8(const Pack8Args& a, int dtype, bool tiles, cudaStream_t s);
+cudaError_t launch_unpack8(const Unpack8Args& a, int dtype, cudaStream_t s);
+
+struct Matmul8Args {
+    const uint8_t* x;  // [M][K] codes, row stride ldx
+    const uint8_t* xs;
+    const uint8_t* w;  // [N][K] codes, row stride ldw
+    const uint8_t* ws;
+    void* y;  // [M][N], row stride ldy
+    uint64_t ldx, ldw, ldy;
+    uint32_t M, N, K;
+    uint32_t w_shift;  // 0: w has a scale per row and block, 7: per 128 x 128 tile
+    int dtype;         // of y: 0 = f32, 1 = bf16
+};
+cudaError_t launch_matmul8(const Matmul8Args& a, cudaStream_t s);
+
+struct Wgrad8Args {
+    const void* dy;  // [T][N] bf16, row stride lddy
+    const uint8_t* x;  // [T][K] codes, row stride ldx
+    const uint8_t* xs;
+    void* dw;  // [N][K], row stride lddw
+    uint64_t lddy, ldx, lddw;
+    uint32_t T, N, K;
+    int dtype;  // of dw: 0 = f32, 1 = bf16
+    int accumulate;
+};
+cudaError_t launch_wgrad8(const Wgrad8Args& a, cudaStream_t s);
+
+// Waits of the tensor-core kernels that ran out on the current device.
+cudaError_t read_wait_faults(uint32_t* count);
+
 // Resident blocks per SM of kernel `fn` (occupancy calculator, cached per
 // device, kernel, block size and dynamic shared memory); at least 1.
 int blocks_per_sm(const void* fn, int threads, size_t smem);

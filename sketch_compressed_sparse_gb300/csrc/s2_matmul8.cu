@@ -1,0 +1,334 @@
+// Y[m][n] = sum_k X[m][k] * W[n][k] for two 8-bit packed matrices.
+//
+// The scales are powers of two, one byte each, which is what the tensor cores'
+// block scaling takes: every product of 32 k is scaled by both bytes and added
+// to one float32 accumulator in tensor memory, so a tile needs no pass over
+// its sums between the blocks of K. The hardware takes a byte for each 32
+// elements; a block of 128 gives the same byte to four products.
+//
+// A tile is 128 features (rows of W, the accumulator's lanes) by NT tokens
+// (rows of X, its columns): neighbouring lanes hold neighbouring features, so
+// stores to Y run along its rows whatever its alignment, and few tokens cost a
+// small NT instead of an idle part of the tile.
+#include "s2_internal.h"
+#include "s2_tc.cuh"
+
+namespace s2 {
+namespace {
+
+using namespace tc;
+
+constexpr int kBK = 128;                 // bytes (= elements) of K per stage
+constexpr int kBF = 128;                 // features per tile
+constexpr int kGroup = 4;                // K blocks whose scale bytes share a 32-bit word
+constexpr int kWarps = 10;               // 0-3 store, 4-7 scales, 8 copies, 9 products
+constexpr uint32_t kABytes = kBF * kBK;  // W part of a stage
+
+struct Args {
+    const uint8_t *xs, *ws;
+    void* y;
+    uint64_t ldy;
+    uint32_t M, N, nblk, w_shift;
+    int dtype;
+    uint32_t tiles_f, tiles_t;
+    uint32_t tokens_inner;  // tiles of one feature range are neighbours in the order
+    uint32_t split;         // blocks (one cluster) per tile, each with a part of K
+    uint32_t* faults;
+};
+
+template <int NT>
+struct Shape {
+    static constexpr uint32_t kStage = kABytes + NT * kBK;
+    static constexpr int kStages = (int)(200 * 1024 / kStage) < 10 ? (int)(200 * 1024 / kStage) : 10;
+    static constexpr int kAcc = 2;                          // accumulators in tensor memory
+    static constexpr int kScaleB = (NT + 127) / 128 * 4;    // columns of X's scales, in fours
+    static constexpr int kScaleCols = 4 + kScaleB;          // columns of one group's scales
+    static constexpr int kRing = 2;                         // groups of scales in tensor memory
+    static constexpr uint32_t kUsed = kAcc * NT + kRing * kScaleCols;
+    static constexpr uint32_t kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+    static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
+    static_assert(kUsed <= 512, "tensor memory");
+    static_assert((size_t)NT * kBF * 4 <= (size_t)kStages * kStage, "a partial tile fits where the stages were");
+};
+
+__device__ __forceinline__ void store(void* y, int dtype, uint64_t at, float v) {
+    if (dtype == 0) {
+        static_cast<float*>(y)[at] = v;
+    } else {
+        uint16_t h;  // the one rounding to 16 bits: Y's own type
+        asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(v));
+        static_cast<uint16_t*>(y)[at] = h;
+    }
+}
+
+// The scale bytes of K blocks kb..kb+3 of one row as a word; blocks past the
+// end repeat 1.0, which no product uses.
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* s, uint32_t kb, uint32_t nblk) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) w |= (kb + i < nblk ? (uint32_t)__ldg(s + kb + i) : 127u) << (8 * i);
+    return w;
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kWarps * 32, 1)
+    matmul8_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, const Args a) {
+    using S = Shape<NT>;
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t bars[2 * S::kStages + 2 * S::kRing + 2 * S::kAcc + 1];
+    __shared__ uint32_t tmem_slot;
+    __shared__ uint32_t dead;
+
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t bar0 = smem_u32(bars);
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (S::kStages + s); };
+    auto sf_full = [&](int s) { return bar0 + 8u * (2 * S::kStages + s); };
+    auto sf_empty = [&](int s) { return bar0 + 8u * (2 * S::kStages + S::kRing + s); };
+    auto acc_full = [&](int s) { return bar0 + 8u * (2 * S::kStages + 2 * S::kRing + s); };
+    auto acc_empty = [&](int s) { return bar0 + 8u * (2 * S::kStages + 2 * S::kRing + S::kAcc + s); };
+    const uint32_t drain = bar0 + 8u * (2 * S::kStages + 2 * S::kRing + 2 * S::kAcc);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S::kStages; ++s) {
+            bar_init(full(s), 1);
+            bar_init(empty(s), 1);
+        }
+        for (int s = 0; s < S::kRing; ++s) {
+            bar_init(sf_full(s), 4);
+            bar_init(sf_empty(s), 1);
+        }
+        for (int s = 0; s < S::kAcc; ++s) {
+            bar_init(acc_full(s), 1);
+            bar_init(acc_empty(s), 4);
+        }
+        bar_init(drain, 1);
+        dead = 0;
+        bar_fence_init();
+    }
+    if (warp == 9) tmem_alloc(smem_u32(&tmem_slot), S::kCols);
+    if (threadIdx.x == 8 * 32) {
+        tma_prefetch(&wmap);
+        tma_prefetch(&xmap);
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = tmem_slot;
+    const Wait wt{&dead, a.faults};
+
+    const uint32_t rank = a.split > 1 ? cluster_rank() : 0;
+    const uint32_t first = blockIdx.x / a.split, step = gridDim.x / a.split, tiles = a.tiles_f * a.tiles_t;
+    const uint32_t kb0 = (uint32_t)((uint64_t)a.nblk * rank / a.split);
+    const uint32_t kb1 = (uint32_t)((uint64_t)a.nblk * (rank + 1) / a.split);
+    auto place = [&](uint32_t tile, uint32_t& f0, uint32_t& t0) {
+        const uint32_t inner = a.tokens_inner ? a.tiles_t : a.tiles_f, o = tile / inner, i = tile - o * inner;
+        f0 = (a.tokens_inner ? o : i) * kBF;
+        t0 = (a.tokens_inner ? i : o) * NT;
+    };
+
+    if (warp == 8) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (uint32_t tile = first; ok && tile < tiles; tile += step) {
+                uint32_t f0, t0;
+                place(tile, f0, t0);
+                for (uint32_t kb = kb0; kb < kb1; ++kb, ++it) {
+                    const int s = it % S::kStages;
+                    if (!(ok = bar_wait(empty(s), ((it / S::kStages) & 1) ^ 1, wt))) break;
+                    bar_expect(full(s), S::kStage);
+                    const uint32_t dst = base + s * S::kStage;
+                    tma_2d(dst, &wmap, full(s), (int)(kb * kBK), (int)f0);
+                    tma_2d(dst + kABytes, &xmap, full(s), (int)(kb * kBK), (int)t0);
+                }
+            }
+            // nothing of this block's may still be on its way when it ends
+            if (dead)
+                for (uint32_t j = it > (uint32_t)S::kStages ? it - S::kStages : 0; j < it; ++j)
+                    bar_drain(full(j % S::kStages), (j / S::kStages) & 1);
+        }
+    } else if (warp == 9) {
+        if (lane == 0) {
+            // D float32, A and B e4m3, both along K, UE8M0 scales, N = NT, M = 128
+            const uint32_t idesc = (uint32_t)(NT / 8) << 17 | 1u << 23 | (uint32_t)(kBF / 16) << 24;
+            uint32_t it = 0, grp = 0, n = 0;
+            bool ok = true;
+            for (uint32_t tile = first; ok && tile < tiles; tile += step, ++n) {
+                const int buf = n % S::kAcc;
+                if (!(ok = bar_wait(acc_empty(buf), ((n / S::kAcc) & 1) ^ 1, wt))) break;
+                fence_after();
+                const uint32_t d = tmem + buf * NT;
+                for (uint32_t kb = kb0; kb < kb1; ++kb, ++it) {
+                    const uint32_t i = kb - kb0;
+                    const uint32_t sf = tmem + S::kAcc * NT + (grp % S::kRing) * S::kScaleCols;
+                    if (i % kGroup == 0 && !(ok = bar_wait(sf_full(grp % S::kRing), (grp / S::kRing) & 1, wt))) break;
+                    const int s = it % S::kStages;
+                    if (!(ok = bar_wait(full(s), (it / S::kStages) & 1, wt))) break;
+                    fence_after();
+                    const uint64_t ad = smem_desc(base + s * S::kStage, 16, 1024);
+                    const uint64_t bd = smem_desc(base + s * S::kStage + kABytes, 16, 1024);
+                    const uint32_t id = idesc | (i % kGroup) << 4 | (i % kGroup) << 29;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)  // 32 bytes of K each
+                        mma_mx8(d, ad + 2 * j, bd + 2 * j, id, sf, sf + 4, i > 0 || j > 0);
+                    mma_commit(empty(s));
+                    if (i % kGroup == kGroup - 1 || kb + 1 == kb1) {
+                        mma_commit(sf_empty(grp % S::kRing));
+                        ++grp;
+                    }
+                }
+                if (ok) mma_commit(acc_full(buf));
+            }
+            if (dead) {  // products in flight still read this block's memory
+                mma_commit(drain);
+                bar_drain(drain, 0);
+            }
+        }
+    } else if (warp >= 4) {
+        // Each of the four warps writes the same words to its own 32 lanes:
+        // word c of lane l holds the bytes of row 32c + l.
+        uint32_t grp = 0;
+        bool ok = true;
+        const uint32_t quarter = (uint32_t)(warp % 4) << 21;  // lane 32 * (warp % 4)
+        for (uint32_t tile = first; ok && tile < tiles; tile += step) {
+            uint32_t f0, t0;
+            place(tile, f0, t0);
+            for (uint32_t kb = kb0; kb < kb1; kb += kGroup, ++grp) {
+                uint32_t wa[4], wb[S::kScaleB];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t f = f0 + 32 * c + lane;
+                    wa[c] = f < a.N ? scale_word(a.ws + (uint64_t)(f >> a.w_shift) * a.nblk, kb, a.nblk) : 0x7f7f7f7fu;
+                }
+#pragma unroll
+                for (int c = 0; c < S::kScaleB; ++c) {
+                    const uint32_t t = t0 + 32 * c + lane;
+                    wb[c] = 32 * c < NT && t < a.M ? scale_word(a.xs + (uint64_t)t * a.nblk, kb, a.nblk) : 0x7f7f7f7fu;
+                }
+                if (!(ok = __all_sync(kFull, bar_wait(sf_empty(grp % S::kRing), ((grp / S::kRing) & 1) ^ 1, wt)))) break;
+                fence_after();
+                const uint32_t sf = tmem + quarter + S::kAcc * NT + (grp % S::kRing) * S::kScaleCols;
+                tmem_st4(sf, wa[0], wa[1], wa[2], wa[3]);
+#pragma unroll
+                for (int c = 0; c < S::kScaleB; c += 4) tmem_st4(sf + 4 + c, wb[c], wb[c + 1], wb[c + 2], wb[c + 3]);
+                wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(sf_full(grp % S::kRing));
+            }
+        }
+    } else {
+        uint32_t n = 0;
+        for (uint32_t tile = first; tile < tiles; tile += step, ++n) {
+            const int buf = n % S::kAcc;
+            if (!__all_sync(kFull, bar_wait(acc_full(buf), (n / S::kAcc) & 1, wt))) break;
+            fence_after();
+            uint32_t f0, t0;
+            place(tile, f0, t0);
+            const uint32_t f = f0 + warp * 32 + lane;
+#pragma unroll 1
+            for (int c = 0; c < NT; c += 16) {
+                uint32_t r[16];
+                tmem_ld16(tmem + ((uint32_t)warp << 21) + buf * NT + c, r);
+                wait_ld();
+                if (a.split > 1) {
+                    // this block's part of the sums, where the stages were
+                    float* part = reinterpret_cast<float*>(raw + (base - smem_u32(raw)));
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) part[(c + j) * kBF + warp * 32 + lane] = __uint_as_float(r[j]);
+                } else if (f < a.N) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (t0 + c + j < a.M) store(a.y, a.dtype, (uint64_t)(t0 + c + j) * a.ldy + f, __uint_as_float(r[j]));
+                }
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(acc_empty(buf));
+        }
+    }
+
+    __syncwarp();
+    if (a.split > 1) {
+        // One tile per cluster: every block adds the parts of its own columns
+        // in the order of the ranks, so the sums do not depend on timing.
+        cluster_sync();
+        uint32_t f0, t0;
+        place(first, f0, t0);
+        const uint32_t f = f0 + threadIdx.x % kBF;
+        const uint32_t c0 = NT * rank / a.split, c1 = NT * (rank + 1) / a.split;
+        if (!dead && threadIdx.x < 2 * kBF) {
+            for (uint32_t c = c0 + threadIdx.x / kBF; c < c1 && t0 + c < a.M; c += 2) {
+                float v = 0.0f;
+                for (uint32_t r = 0; r < a.split; ++r) v += ld_peer(base + (c * kBF + threadIdx.x % kBF) * 4, r);
+                if (f < a.N) store(a.y, a.dtype, (uint64_t)(t0 + c) * a.ldy + f, v);
+            }
+        }
+        cluster_sync();
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == 9) tmem_free(tmem, S::kCols);
+}
+
+template <int NT>
+cudaError_t launch(const Matmul8Args& m, Args a, cudaStream_t s) {
+    using S = Shape<NT>;
+    DeviceInfo di{};
+    cudaError_t e = device_info(&di);
+    if (e != cudaSuccess) return e;
+    CUtensorMap wmap, xmap;
+    e = make_map(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, m.w, m.K, m.N, m.ldw, kBK, kBF);
+    if (e != cudaSuccess) return e;
+    e = make_map(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, m.x, m.K, m.M, m.ldx, kBK, NT);
+    if (e != cudaSuccess) return e;
+    a.tiles_f = (m.N + kBF - 1) / kBF;
+    a.tiles_t = (m.M + NT - 1) / NT;
+    const uint64_t tiles = (uint64_t)a.tiles_f * a.tiles_t;
+    if (tiles > 0x7fffffffull) return cudaErrorInvalidValue;
+    // the operand with the fewer bytes is the one that tiles in a row re-read
+    a.tokens_inner = m.M <= m.N;
+    a.split = 1;
+    while (a.split < 8 && tiles * a.split * 2 <= (uint64_t)di.sms && a.split * 2 <= a.nblk) a.split *= 2;
+    auto kernel = matmul8_kernel<NT>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(a.split > 1 ? tiles * a.split : tiles < (uint64_t)di.sms ? tiles : di.sms));
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = a.split;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = a.split > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, a);
+}
+
+}  // namespace
+
+cudaError_t launch_matmul8(const Matmul8Args& m, cudaStream_t s) {
+    Args a{};
+    a.xs = m.xs;
+    a.ws = m.ws;
+    a.y = m.y;
+    a.ldy = m.ldy;
+    a.M = m.M;
+    a.N = m.N;
+    a.nblk = (m.K + kBK - 1) / kBK;
+    a.w_shift = m.w_shift;
+    a.dtype = m.dtype;
+    cudaError_t e = wait_fault_word(&a.faults);
+    if (e != cudaSuccess) return e;
+    if (m.M <= 16) return launch<16>(m, a, s);
+    if (m.M <= 32) return launch<32>(m, a, s);
+    if (m.M <= 64) return launch<64>(m, a, s);
+    if (m.M <= 128) return launch<128>(m, a, s);
+    return launch<224>(m, a, s);
+}
+
+}  // namespace s2

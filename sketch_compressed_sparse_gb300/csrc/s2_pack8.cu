@@ -1,0 +1,345 @@
+// 8-bit packing: e4m3 codes with one power-of-two scale for each block of 128
+// elements of a row, or of 128 x 128 elements, and the way back.
+//
+// The scale of a block is 2^e with the least e >= -117 for which no finite
+// element of the block exceeds 448 * 2^e (448 is e4m3's largest number). With
+// the float's bits (1.m * 2^(E-127)) that is e = E - 135, plus 1 where 1.m
+// exceeds 1.75 = 448 / 2^8, and the stored byte is e + 127. A power of two
+// makes x * 2^-e exact, so a code is one rounding away from its element, and
+// makes code * 2^e exact in float32 and in bfloat16 (the bound -117 keeps the
+// smallest code times 2^e a normal number).
+//
+// Both directions are bound by HBM: an element is read once and written once
+// and costs a handful of instructions. Sixteen lanes hold one row's block,
+// eight neighbouring elements each, so that the largest is found with four
+// shuffles and bfloat16 rows move 16 bytes a lane.
+#include "s2_internal.h"
+
+namespace s2 {
+namespace {
+
+constexpr int kBlk = 128;
+constexpr int kPer = 8;               // elements per lane
+constexpr int kLanes = kBlk / kPer;   // lanes per block of a row
+constexpr int kMinByte = 10;          // e >= -117
+
+struct Vals {
+    float v[kPer];
+};
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T x);
+template <>
+__device__ __forceinline__ float to_f32<float>(float x) {
+    return x;
+}
+template <>
+__device__ __forceinline__ float to_f32<uint16_t>(uint16_t x) {
+    return __uint_as_float((uint32_t)x << 16);
+}
+
+// Eight elements from p; only the first `valid` exist (the others read as 0).
+// VEC: p is 16-byte aligned.
+template <typename T, bool VEC>
+__device__ __forceinline__ Vals load8(const T* p, int valid) {
+    Vals r;
+    if (VEC && valid >= kPer) {
+        if constexpr (sizeof(T) == 4) {
+            const uint4 a = ld_stream_u4(p), b = ld_stream_u4(p + 4);
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) r.v[i] = __uint_as_float(w[i]);
+        } else {
+            const uint4 a = ld_stream_u4(p);
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                r.v[2 * i] = __uint_as_float(w[i] << 16);
+                r.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+        return r;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) r.v[i] = i < valid ? to_f32<T>(p[i]) : 0.0f;
+    return r;
+}
+
+// Bits of the largest finite magnitude among the eight.
+__device__ __forceinline__ uint32_t amax_bits(const Vals& x) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const uint32_t b = __float_as_uint(x.v[i]) & 0x7fffffffu;
+        m = max(m, b < 0x7f800000u ? b : 0u);
+    }
+    return m;
+}
+
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
+    return (uint32_t)max((int)((amax + 0x1fffffu) >> 23) - 8, kMinByte);
+}
+
+// The eight codes of a block with scale byte b, lowest element first. A code
+// is e4m3's nearest (ties to even); NaN and infinities become NaN.
+__device__ __forceinline__ uint2 codes8(const Vals& x, uint32_t b) {
+    const float inv = __uint_as_float((254u - b) << 23);
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float lo = x.v[2 * i] * inv, hi = x.v[2 * i + 1] * inv;
+        // the conversion saturates, so infinities are made NaN first
+        if ((__float_as_uint(lo) & 0x7fffffffu) == 0x7f800000u) lo = __uint_as_float(0x7fffffffu);
+        if ((__float_as_uint(hi) & 0x7fffffffu) == 0x7f800000u) hi = __uint_as_float(0x7fffffffu);
+        uint16_t q;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(q) : "f"(hi), "f"(lo));
+        h[i] = q;
+    }
+    return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+
+// Codes to p (8-byte aligned), the first `valid` of them.
+__device__ __forceinline__ void store_codes(uint8_t* p, uint2 c, int valid) {
+    if (valid >= kPer) {
+        *reinterpret_cast<uint2*>(p) = c;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        if (i < valid) p[i] = (uint8_t)((i < 4 ? c.x >> (8 * i) : c.y >> (8 * (i - 4))) & 0xffu);
+}
+
+constexpr int kItems = 4;  // blocks of a row in flight per half-warp
+
+// One half-warp per block of a row, kItems of them in flight.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads) pack_rows_kernel(Pack8Args a) {
+    const uint32_t sub = threadIdx.x % kLanes;
+    const uint32_t group = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
+    const uint64_t first = (uint64_t)group * kItems;
+    const T* x = static_cast<const T*>(a.x);
+    Vals v[kItems];
+    uint64_t row[kItems];
+    uint32_t blk[kItems];
+    int valid[kItems];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        const uint64_t item = first + i;
+        const bool live = item < (uint64_t)a.items;
+        const uint32_t it = live ? (uint32_t)item : 0u;
+        row[i] = it / a.nblk;
+        blk[i] = it - (uint32_t)row[i] * a.nblk;
+        const uint32_t c0 = blk[i] * kBlk + sub * kPer;
+        valid[i] = live ? min(max((int)a.cols - (int)c0, 0), kPer) : 0;
+        v[i] = load8<T, VEC>(x + row[i] * a.ldx + c0, valid[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        uint32_t m = amax_bits(v[i]);
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+        const uint32_t b = scale_byte(m);
+        store_codes(a.codes + row[i] * a.ldc + blk[i] * kBlk + sub * kPer, codes8(v[i], b), valid[i]);
+        if (sub == 0 && first + i < (uint64_t)a.items) a.scales[first + i] = (uint8_t)b;
+    }
+}
+
+// 4 x 4 bytes: word i holds row i; afterwards word j holds column j.
+__device__ __forceinline__ void transpose4(uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+    const uint32_t a = __byte_perm(r0, r1, 0x5140), b = __byte_perm(r2, r3, 0x5140);
+    const uint32_t c = __byte_perm(r0, r1, 0x7362), d = __byte_perm(r2, r3, 0x7362);
+    r0 = __byte_perm(a, b, 0x5410);
+    r1 = __byte_perm(a, b, 0x7632);
+    r2 = __byte_perm(c, d, 0x5410);
+    r3 = __byte_perm(c, d, 0x7632);
+}
+
+constexpr int kTileLd = kBlk + 16;  // row length of the transposed tile in shared memory, in bytes
+
+// One block of threads per 128 x 128 tile: each half-warp holds eight whole
+// rows of it in registers, so the tile is read once; the transposed codes
+// turn 8 x 8 bytes in registers and pass through shared memory.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads) pack_tiles_kernel(Pack8Args a) {
+    __shared__ uint32_t warp_max[kThreads / 32];
+    __shared__ __align__(16) uint8_t turned[kBlk * kTileLd];
+    const uint32_t sub = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
+    const uint32_t trow = blockIdx.x / a.nblk, tcol = blockIdx.x - trow * a.nblk;
+    const uint64_t r0 = (uint64_t)trow * kBlk + grp * kPer;
+    const uint32_t c0 = tcol * kBlk + sub * kPer;
+    const int cvalid = min(max((int)a.cols - (int)c0, 0), kPer);
+    const int rvalid = (int)min((uint64_t)kPer, a.rows > r0 ? a.rows - r0 : 0);
+    const T* x = static_cast<const T*>(a.x) + r0 * a.ldx + c0;
+    Vals v[kPer];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i] = load8<T, VEC>(x + (i < rvalid ? i : 0) * a.ldx, i < rvalid ? cvalid : 0);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) m = max(m, amax_bits(v[i]));
+    m = __reduce_max_sync(kFull, m);
+    if (threadIdx.x % 32 == 0) warp_max[threadIdx.x / 32] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) m = max(m, warp_max[i]);
+    const uint32_t b = scale_byte(m);
+    uint2 c[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        c[i] = codes8(v[i], b);
+        if (i < rvalid) store_codes(a.codes + (r0 + i) * a.ldc + c0, c[i], cvalid);
+    }
+    if (threadIdx.x == 0) {
+        a.scales[(uint64_t)trow * a.nblk + tcol] = (uint8_t)b;
+        if (a.codes_t) a.scales_t[(uint64_t)tcol * a.nrow_blk + trow] = (uint8_t)b;
+    }
+    if (!a.codes_t) return;
+    transpose4(c[0].x, c[1].x, c[2].x, c[3].x);
+    transpose4(c[4].x, c[5].x, c[6].x, c[7].x);
+    transpose4(c[0].y, c[1].y, c[2].y, c[3].y);
+    transpose4(c[4].y, c[5].y, c[6].y, c[7].y);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const uint2 w = j < 4 ? make_uint2(c[j].x, c[j + 4].x) : make_uint2(c[j - 4].y, c[j].y);
+        *reinterpret_cast<uint2*>(turned + (sub * kPer + j) * kTileLd + grp * kPer) = w;
+    }
+    __syncthreads();
+    const int left = (int)min((uint64_t)kBlk, a.rows - (uint64_t)trow * kBlk);
+#pragma unroll
+    for (int i = 0; i < kBlk * kBlk / 16 / kThreads; ++i) {
+        const uint32_t t = threadIdx.x + i * kThreads, col = t / 8, at = (t % 8) * 16;
+        if (tcol * kBlk + col >= a.cols) continue;
+        const uint8_t* s = turned + col * kTileLd + at;
+        uint8_t* d = a.codes_t + (uint64_t)(tcol * kBlk + col) * a.ldct + (uint64_t)trow * kBlk + at;
+        if ((int)at + 16 <= left) {
+            *reinterpret_cast<uint4*>(d) = *reinterpret_cast<const uint4*>(s);
+        } else {
+            for (int j = 0; (int)at + j < left; ++j) d[j] = s[j];
+        }
+    }
+}
+
+// Two e4m3 codes to two floats, exactly.
+__device__ __forceinline__ float2 decode2(uint32_t two) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
+    float2 f;
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}" : "=f"(f.x), "=f"(f.y) : "r"(h));
+    return f;
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads) unpack_kernel(Unpack8Args a) {
+    const uint32_t sub = threadIdx.x % kLanes;
+    const uint32_t group = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
+    const uint64_t first = (uint64_t)group * kItems;
+    T* out = static_cast<T*>(a.out);
+    uint2 c[kItems];
+    uint32_t b[kItems];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        const uint64_t item = first + i;
+        c[i] = make_uint2(0, 0);
+        b[i] = 127;
+        if (item >= (uint64_t)a.items) continue;
+        const uint32_t it = (uint32_t)item, row = it / a.nblk, blk = it - row * a.nblk;
+        const uint32_t c0 = blk * kBlk + sub * kPer;
+        const int valid = min(max((int)a.cols - (int)c0, 0), kPer);
+        const uint8_t* p = a.codes + (uint64_t)row * a.ldc + c0;
+        if (valid == kPer) {
+            c[i] = *reinterpret_cast<const uint2*>(p);
+        } else {
+            for (int j = 0; j < valid; ++j) (j < 4 ? c[i].x : c[i].y) |= (uint32_t)p[j] << (8 * (j % 4));
+        }
+        b[i] = a.scales[(uint64_t)(row >> a.row_shift) * a.nblk + blk];
+    }
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        const uint64_t item = first + i;
+        if (item >= (uint64_t)a.items) continue;
+        const uint32_t it = (uint32_t)item, row = it / a.nblk, blk = it - row * a.nblk;
+        const uint32_t c0 = blk * kBlk + sub * kPer;
+        const int valid = min(max((int)a.cols - (int)c0, 0), kPer);
+        // byte 0 stands for 2^-127, a subnormal float; byte 255 for NaN
+        const float s = __uint_as_float(b[i] == 0 ? 0x00400000u : b[i] == 255 ? 0x7fffffffu : b[i] << 23);
+        float f[kPer];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 d = decode2((j < 2 ? c[i].x : c[i].y) >> (16 * (j % 2)));
+            f[2 * j] = d.x * s;
+            f[2 * j + 1] = d.y * s;
+        }
+        T* o = out + (uint64_t)row * a.ldo + c0;
+        if constexpr (sizeof(T) == 4) {
+            if (VEC && valid == kPer) {
+                reinterpret_cast<float4*>(o)[0] = make_float4(f[0], f[1], f[2], f[3]);
+                reinterpret_cast<float4*>(o)[1] = make_float4(f[4], f[5], f[6], f[7]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kPer; ++j)
+                    if (j < valid) o[j] = f[j];
+            }
+        } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = bf16x2(f[2 * j], f[2 * j + 1]);
+            if (VEC && valid == kPer) {
+                *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kPer; ++j)
+                    if (j < valid) o[j] = (uint16_t)(w[j / 2] >> (16 * (j % 2)));
+            }
+        }
+    }
+}
+
+inline bool vec16(const void* p, uint64_t ld, size_t esz) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * esz % 16 == 0;
+}
+
+}  // namespace
+
+cudaError_t launch_pack8(const Pack8Args& a, int dtype, bool tiles, cudaStream_t s) {
+    const bool vec = vec16(a.x, a.ldx, dtype == 0 ? 4 : 2);
+    if (tiles) {
+        const uint32_t grid = a.nrow_blk * a.nblk;
+        if (dtype == 0) {
+            if (vec) pack_tiles_kernel<float, true><<<grid, kThreads, 0, s>>>(a);
+            else pack_tiles_kernel<float, false><<<grid, kThreads, 0, s>>>(a);
+        } else {
+            if (vec) pack_tiles_kernel<uint16_t, true><<<grid, kThreads, 0, s>>>(a);
+            else pack_tiles_kernel<uint16_t, false><<<grid, kThreads, 0, s>>>(a);
+        }
+        return cudaGetLastError();
+    }
+    const uint32_t per = (uint32_t)(kThreads / kLanes * kItems), grid = (a.items - 1) / per + 1;
+    if (dtype == 0) {
+        if (vec) pack_rows_kernel<float, true><<<grid, kThreads, 0, s>>>(a);
+        else pack_rows_kernel<float, false><<<grid, kThreads, 0, s>>>(a);
+    } else {
+        if (vec) pack_rows_kernel<uint16_t, true><<<grid, kThreads, 0, s>>>(a);
+        else pack_rows_kernel<uint16_t, false><<<grid, kThreads, 0, s>>>(a);
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_unpack8(const Unpack8Args& a, int dtype, cudaStream_t s) {
+    const bool vec = vec16(a.out, a.ldo, dtype == 0 ? 4 : 2);
+    const uint32_t per = (uint32_t)(kThreads / kLanes * kItems), grid = (a.items - 1) / per + 1;
+    if (dtype == 0) {
+        if (vec) unpack_kernel<float, true><<<grid, kThreads, 0, s>>>(a);
+        else unpack_kernel<float, false><<<grid, kThreads, 0, s>>>(a);
+    } else {
+        if (vec) unpack_kernel<uint16_t, true><<<grid, kThreads, 0, s>>>(a);
+        else unpack_kernel<uint16_t, false><<<grid, kThreads, 0, s>>>(a);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace s2

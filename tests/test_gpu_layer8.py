@@ -1,0 +1,282 @@
+"""GPU tests of the 8-bit layer: packing, unpacking and the product of packed
+matrices, against the plain float64 implementation in tests/_layer8.py.
+
+Codes and scale bytes are compared bit for bit, unpacked values exactly.
+
+Products: with x_k, w_k the exact values, the products x_k w_k are exact in
+the tensor core (two 4-bit significands) and are added to float32
+accumulators. Let A = sum |x_k w_k|. A step adds 32 products and the
+accumulator; each of its terms may lose less than one unit in the last place
+of float32 at the step's largest term, so a step loses less than
+33 * 2^-23 * (largest partial magnitude <= A). That would give a bound of
+33 * K/32 * 2^-23 * A; terms lost from below the accumulator's last place are
+of random sign, but no use is made of that. Splitting K among up to eight
+blocks adds eight float32 roundings. So
+    |y - exact| <= (K + 33 + 8) * 2^-23 * A          (float32)
+A bfloat16 result is the float32 result rounded once to nearest, and is
+compared with that bit for bit.
+"""
+import numpy as np
+import pytest
+import torch
+
+from tests import _layer8 as ref
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import sketch_compressed_sparse_gb300 as s2
+
+DEV = "cuda"
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+SENTINEL = 0xA5
+
+
+def make(rows, cols, tag, dtype="f32", kind="normal"):
+    rng = np.random.default_rng(tag)
+    x = rng.normal(size=(rows, cols))
+    if kind == "wide":  # magnitudes over the whole float range, zero blocks, signed zeros
+        x *= 10.0 ** rng.uniform(-44, 37, size=x.shape)
+        x[rng.random(x.shape) < 0.1] = -0.0
+        x[::3] = 0.0
+    t = torch.from_numpy(x.astype(np.float32)).to(DT[dtype])
+    return t
+
+
+def padded(rows, cols, extra=16, dtype=torch.uint8, fill=SENTINEL):
+    """A matrix inside a larger one, filled, so that writes outside it show."""
+    ld = -(-cols // 16) * 16 + extra
+    whole = torch.full((rows + 1, ld), fill, dtype=dtype, device=DEV)
+    return whole, whole[:rows, :cols]
+
+
+def untouched(whole, rows, cols, fill=SENTINEL):
+    w = whole.clone()
+    w[:rows, :cols] = fill
+    return bool((w == fill).all())
+
+
+SIZES = [(1, 1), (1, 1024), (3, 127), (5, 128), (2, 129), (64, 7), (127, 300), (128, 128), (130, 257), (1000, 72),
+         (257, 1031)]
+
+
+@pytest.mark.parametrize("tiles", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,cols", SIZES)
+def test_pack_and_unpack(rows, cols, dtype, tiles):
+    lay = "tiles" if tiles else "rows"
+    for kind in ("normal", "wide"):
+        x = make(rows, cols, rows * 7 + cols, dtype, kind)
+        want, want_s = ref.pack(x.double().numpy(), tiles)
+        whole, codes = padded(rows, cols)
+        scales = torch.full((want_s.size + 3,), SENTINEL, dtype=torch.uint8, device=DEV)
+        extra = {}
+        if tiles:
+            whole_t, codes_t = padded(cols, rows)
+            scales_t = torch.full((want_s.size + 3,), SENTINEL, dtype=torch.uint8, device=DEV)
+            extra = {"codes_t": codes_t, "scales_t": scales_t}
+        s2.s2_pack8(x.to(DEV), codes, scales, lay, **extra)
+        np.testing.assert_array_equal(codes.cpu().numpy(), want)
+        np.testing.assert_array_equal(scales[:want_s.size].cpu().numpy(), want_s.reshape(-1))
+        assert untouched(whole, rows, cols) and bool((scales[want_s.size:] == SENTINEL).all())
+        if tiles:
+            np.testing.assert_array_equal(codes_t.cpu().numpy(), want.T)
+            np.testing.assert_array_equal(scales_t[:want_s.size].cpu().numpy(), want_s.T.reshape(-1))
+            assert untouched(whole_t, cols, rows) and bool((scales_t[want_s.size:] == SENTINEL).all())
+        # and back, exactly, in both types (a code times its scale has 4 significant bits)
+        for out_t in (torch.float32, torch.bfloat16):
+            wo, out = padded(rows, cols, extra=3, dtype=out_t, fill=7.0)
+            s2.s2_unpack8(codes, scales, out, lay)
+            np.testing.assert_array_equal(out.double().cpu().numpy(), ref.unpack(want, want_s, tiles))
+            assert untouched(wo, rows, cols, 7.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("ld,off", [(300, 0), (301, 0), (304, 1), (304, 8), (333, 3)])
+def test_pack_strides_and_offsets(dtype, ld, off):
+    """Rows of a larger matrix, at any offset and row length."""
+    rows, cols = 70, 290
+    big = make(rows, ld + off, ld, dtype).to(DEV)
+    x = big.reshape(-1)[off:off + rows * ld].reshape(rows, ld)[:, :cols]
+    for lay in ("rows", "tiles"):
+        codes, scales = s2.alloc_pack8(rows, cols, lay)
+        s2.s2_pack8(x, codes, scales, lay)
+        want, want_s = ref.pack(x.double().cpu().numpy(), lay == "tiles")
+        np.testing.assert_array_equal(codes.cpu().numpy(), want)
+        np.testing.assert_array_equal(scales.cpu().numpy(), want_s)
+        flat = torch.zeros(off + rows * ld, device=DEV, dtype=DT[dtype])
+        out = flat[off:].reshape(rows, ld)[:, :cols]
+        s2.s2_unpack8(codes, scales, out, lay)
+        np.testing.assert_array_equal(out.double().cpu().numpy(), ref.unpack(want, want_s, lay == "tiles"))
+
+
+@pytest.mark.parametrize("tiles", [False, True])
+def test_pack_not_finite(tiles):
+    """NaN and infinities become NaN codes; the rest of their block is as without them."""
+    x = make(130, 260, 5)
+    bad = torch.zeros_like(x, dtype=torch.bool)
+    bad[3, 5] = bad[4, 200] = bad[129, 259] = bad[7, 128:256] = True
+    y = x.clone()
+    y[bad] = torch.tensor([float("nan"), float("inf"), float("-inf")]).repeat(100)[:int(bad.sum())]
+    y[7, 128:256] = float("inf")  # a row's block with nothing finite
+    codes, scales = s2.alloc_pack8(130, 260, "tiles" if tiles else "rows")
+    s2.s2_pack8(y.to(DEV), codes, scales, "tiles" if tiles else "rows")
+    want, want_s = ref.pack(y.double().numpy(), tiles)
+    np.testing.assert_array_equal(codes.cpu().numpy(), want)
+    np.testing.assert_array_equal(scales.cpu().numpy(), want_s)
+    out = torch.empty((130, 260), device=DEV)
+    s2.s2_unpack8(codes, scales, out, "tiles" if tiles else "rows")
+    assert torch.equal(torch.isnan(out).cpu(), bad)
+
+
+def test_unpack_every_code_and_byte():
+    """All 256 codes under every scale byte whose values float32 holds exactly (2^-9 * 2^(b-127) normal), and byte 255."""
+    codes = torch.arange(256, dtype=torch.int32).to(torch.uint8).reshape(1, 256).repeat(246, 1).contiguous().to(DEV)
+    sb = torch.arange(10, 256, dtype=torch.int32).to(torch.uint8)
+    scales = sb.reshape(-1, 1).repeat(1, 2).contiguous().to(DEV)
+    out = torch.empty((246, 256), device=DEV)
+    s2.s2_unpack8(codes, scales, out)
+    want = ref.VALUES[None, :] * np.exp2(sb.numpy().astype(np.float64) - 127)[:, None]
+    want[-1] = np.nan
+    with np.errstate(over="ignore"):
+        np.testing.assert_array_equal(out.cpu().numpy(), want.astype(np.float32))
+
+
+def packed(x, lay):
+    codes, scales = s2.alloc_pack8(*x.shape, lay)
+    c, s = ref.pack(x.double().numpy(), lay == "tiles")
+    codes.copy_(torch.from_numpy(c))
+    scales.copy_(torch.from_numpy(s))
+    return codes, scales, ref.unpack(c, s, lay == "tiles")
+
+
+def bound(K, A):
+    return (K + 41) * 2.0 ** -23 * A + 2.0 ** -149
+
+
+def check_matmul(M, N, K, dtype, w_lay, kind="normal", ldy_extra=0):
+    x, w = make(M, K, M + 3 * K), make(N, K, N + 5 * K + 1)
+    if kind == "mixed":  # block scales that differ by row and by block of K
+        rng = np.random.default_rng(K)
+        x = x * torch.from_numpy(2.0 ** rng.integers(-12, 12, size=(M, ref.blocks(K))).repeat(128, 1)[:, :K]).float()
+        w = w * torch.from_numpy(2.0 ** rng.integers(-12, 12, size=(N, ref.blocks(K))).repeat(128, 1)[:, :K]).float()
+        x[::4] = 0
+    xc, xs, xv = packed(x, "rows")
+    wc, ws, wv = packed(w, w_lay)
+    flat = torch.full((M * (N + ldy_extra) + 5,), 3.0, dtype=DT[dtype], device=DEV)
+    y = flat[1:1 + M * (N + ldy_extra)].reshape(M, N + ldy_extra)[:, :N]
+    s2.s2_matmul8(xc, xs, wc, ws, y, w_lay)
+    y32 = y
+    if dtype == "bf16":
+        y32 = torch.empty((M, N), device=DEV)
+        s2.s2_matmul8(xc, xs, wc, ws, y32, w_lay)
+        assert torch.equal(y, y32.to(torch.bfloat16))
+    got = y32.double().cpu().numpy()
+    want, A = xv @ wv.T, np.abs(xv) @ np.abs(wv).T
+    err = np.abs(got - want)
+    tol = bound(K, A)
+    assert (err <= tol).all(), f"worst {np.max(err / np.maximum(tol, 1e-300))} of the bound"
+    y.fill_(3.0)
+    assert bool((flat == 3.0).all()), "wrote outside y"
+    assert s2.s2_wait_faults() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M", [1, 2, 15, 16, 17, 33, 64, 65, 100, 128, 129, 225, 300])
+def test_matmul_tokens(M, dtype):
+    """Every choice of the token tile, one token among them."""
+    check_matmul(M, 300, 650, dtype, "tiles")
+
+
+@pytest.mark.parametrize("N,K", [(1, 1), (1, 128), (7, 31), (128, 127), (129, 129), (64, 16), (130, 512), (1000, 513),
+                                 (333, 1024), (2000, 2056), (50, 5000)])
+@pytest.mark.parametrize("M", [1, 40, 260])
+def test_matmul_sizes(M, N, K):
+    check_matmul(M, N, K, "f32", "tiles", ldy_extra=N % 3)
+
+
+@pytest.mark.parametrize("w_lay", ["rows", "tiles"])
+@pytest.mark.parametrize("M,N,K", [(1, 256, 2048), (20, 500, 1100), (250, 400, 900)])
+def test_matmul_scales(M, N, K, w_lay):
+    """Scales that differ from row to row and block to block, and zero rows."""
+    check_matmul(M, N, K, "f32", w_lay, kind="mixed")
+
+
+def test_matmul_many_tiles():
+    """More tiles than SMs: every block takes several, in both tile orders."""
+    check_matmul(3, 40000, 200, "bf16", "tiles")
+    check_matmul(2000, 2100, 300, "f32", "tiles")
+    check_matmul(5000, 700, 256, "bf16", "tiles")
+
+
+def test_matmul_empty():
+    codes = torch.zeros((4, 16), dtype=torch.uint8, device=DEV)
+    none = codes[:, :0]
+    y = torch.full((4, 6), 5.0, device=DEV)[:, :4]
+    nos = torch.zeros(0, dtype=torch.uint8, device=DEV)
+    s2.s2_matmul8(none, nos, none, nos, y)  # K = 0: an empty sum
+    assert bool((y == 0).all())
+    s2.s2_matmul8(codes[:0], nos, codes, torch.zeros((1, 1), dtype=torch.uint8, device=DEV), y[:0])
+
+
+def test_matmul_not_finite():
+    """A NaN code reaches the outputs of its row and no other."""
+    xc, xs, _ = packed(make(40, 300, 1), "rows")
+    wc, ws, _ = packed(make(50, 300, 2), "tiles")
+    xc[7, 290] = 0x7f
+    wc[11, 3] = 0xff
+    y = torch.empty((40, 50), device=DEV)
+    s2.s2_matmul8(xc, xs, wc, ws, y)
+    bad = torch.isnan(y).cpu()
+    want = torch.zeros((40, 50), dtype=torch.bool)
+    want[7] = True
+    want[:, 11] = True
+    assert torch.equal(bad, want)
+
+
+def test_matmul_repeats_and_streams():
+    """The same bits on every run, and on a side stream."""
+    xc, xs, _ = packed(make(9, 4096, 1), "rows")
+    wc, ws, _ = packed(make(1024, 4096, 2), "tiles")
+    outs = []
+    for i in range(4):
+        y = torch.empty((9, 1024), device=DEV)
+        st = torch.cuda.Stream() if i % 2 else torch.cuda.current_stream()
+        st.wait_stream(torch.cuda.current_stream())
+        s2.s2_matmul8(xc, xs, wc, ws, y, stream=st)
+        torch.cuda.synchronize()
+        outs.append(y)
+    assert all(torch.equal(o, outs[0]) for o in outs)
+
+
+def test_input_gradient_from_transposed_weight():
+    """dX = dY W from the transposed codes that packing a weight by tiles also writes."""
+    T, N, K = 70, 300, 200
+    w = make(N, K, 3)
+    codes, scales = s2.alloc_pack8(N, K, "tiles")
+    codes_t, scales_t = s2.alloc_pack8(K, N, "tiles")
+    s2.s2_pack8(w.to(DEV), codes, scales, "tiles", codes_t, scales_t)
+    gc, gs, gv = packed(make(T, N, 4), "rows")
+    dx = torch.empty((T, K), device=DEV)
+    s2.s2_matmul8(gc, gs, codes_t, scales_t, dx)
+    wv = ref.unpack(*ref.pack(w.double().numpy(), True), True)
+    want, A = gv @ wv, np.abs(gv) @ np.abs(wv)
+    assert (np.abs(dx.double().cpu().numpy() - want) <= bound(N, A)).all()
+
+
+def test_binding_refusals():
+    codes, scales = s2.alloc_pack8(8, 64)
+    x = torch.zeros((8, 64), device=DEV)
+    with pytest.raises(TypeError):
+        s2.s2_pack8(x.half(), codes, scales)
+    with pytest.raises(ValueError):
+        s2.s2_pack8(x.t(), codes, scales)
+    with pytest.raises(ValueError):
+        s2.s2_pack8(x[:7], codes, scales)
+    with pytest.raises(ValueError):
+        s2.s2_pack8(x, codes, scales[:4])
+    with pytest.raises(s2.S2Error) as e:
+        s2.s2_pack8(x[:, :40], codes.reshape(-1)[:8 * 40].reshape(8, 40), scales)
+    assert e.value.status == 2
+    with pytest.raises(ValueError):
+        s2.s2_matmul8(codes, scales, codes[:, :48], scales, x)
