@@ -23,7 +23,8 @@
  *  - Every call is asynchronous on `stream` (NULL = the legacy default
  *    stream) and never synchronises the host. Validation errors are returned
  *    before anything is launched; a failed launch returns S2_ERR_CUDA.
- *  - Outputs are overwritten, never accumulated into. Outputs must not
+ *  - Outputs are overwritten, never accumulated into (unless s2_wgrad8 is
+ *    asked to). Outputs must not
  *    overlap inputs (S2_ERR_INVALID_ARG).
  *  - Gradient, bitmap, sketch and dense-output base pointers must be 16-byte
  *    aligned (S2_ERR_ALIGNMENT). Other arrays need their natural alignment.
@@ -421,6 +422,22 @@ S2_API s2_status s2_unpack8(const uint8_t *codes, uint64_t ldc, const uint8_t *s
 S2_API s2_status s2_matmul8(const uint8_t *x, uint64_t ldx, const uint8_t *x_scales, const uint8_t *w, uint64_t ldw,
                             const uint8_t *w_scales, s2_scale_layout w_layout, uint64_t M, uint64_t N, uint64_t K,
                             void *y, s2_dtype dt, uint64_t ldy, s2_stream_t stream);
+
+/*
+ * s2_wgrad8 -- a layer's weight gradient from its 8-bit activations:
+ *   dw[n][k] = sum over t of dy[t][n] * X[t][k], of type dt, with
+ *   dy [T][N] bfloat16 (row stride lddy, any alignment) and X [T][K] packed
+ *   with S2_SCALE_ROWS. X's values are exact in bfloat16 (scale bytes 10 to
+ *   247, as s2_pack8 writes them; others are rounded), the sums are float32.
+ *   accumulate != 0: dw += the sum instead (one more rounding), for a
+ *   gradient taken over several batches. The result does not depend on
+ *   timing. dw may be a worker's row of grad[W][n], which s2_encode_batched
+ *   and s2_block_topk read. Where base or row stride of dy misses 16 bytes
+ *   the rows are fetched through registers (slower than aligned rows).
+ */
+S2_API s2_status s2_wgrad8(const void *dy, uint64_t lddy, const uint8_t *x, uint64_t ldx, const uint8_t *x_scales,
+                           uint64_t T, uint64_t N, uint64_t K, void *dw, s2_dtype dt, uint64_t lddw, int accumulate,
+                           s2_stream_t stream);
 
 /*
  * s2_wait_faults -- how many waits inside s2_matmul8 and s2_wgrad8 kernels

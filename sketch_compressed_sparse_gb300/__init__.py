@@ -49,6 +49,7 @@ __all__ = [
     "s2_pack8",
     "s2_unpack8",
     "s2_matmul8",
+    "s2_wgrad8",
     "s2_wait_faults",
     "S2_SCALE_ROWS",
     "S2_SCALE_TILES",
@@ -98,6 +99,7 @@ _SIGS = {
     "s2_pack8": ([_vp, _i32, _u64, _u64, _u64, _i32, _vp, _u64, _vp, _vp, _u64, _vp, _vp], _i32),
     "s2_unpack8": ([_vp, _u64, _vp, _i32, _u64, _u64, _vp, _i32, _u64, _vp], _i32),
     "s2_matmul8": ([_vp, _u64, _vp, _vp, _u64, _vp, _i32, _u64, _u64, _u64, _vp, _i32, _u64, _vp], _i32),
+    "s2_wgrad8": ([_vp, _u64, _vp, _u64, _vp, _u64, _u64, _u64, _vp, _i32, _u64, _i32, _vp], _i32),
     "s2_wait_faults": ([ctypes.POINTER(_u32)], _i32),
     "s2_status_string": ([_i32], ctypes.c_char_p),
     "s2_version": ([], ctypes.c_char_p),
@@ -471,6 +473,16 @@ def s2_matmul8(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
     _check(_f("s2_matmul8")(px, ldx, _scales(x_scales, "x_scales", M, K, 0), pw, ldw,
                             _scales(w_scales, "w_scales", N, K, lay), lay, M, N, K, py, _dtype_code(y), ldy,
                             _stream(stream)), "s2_matmul8")
+
+
+def s2_wgrad8(dy: torch.Tensor, x: torch.Tensor, x_scales: torch.Tensor, dw: torch.Tensor, accumulate: bool = False,
+              stream=None) -> None:
+    """dw [N, K] = dY^T X (or += with accumulate) of dy [T, N] bfloat16 and packed X [T, K] (layout "rows")."""
+    py, T, N, ldy = _mat(dy, "dy", (torch.bfloat16,))
+    px, _, K, ldx = _mat(x, "x", _CODES, T)
+    pw, _, _, ldw = _mat(dw, "dw", _GRAD, N, K)
+    _check(_f("s2_wgrad8")(py, ldy, px, ldx, _scales(x_scales, "x_scales", T, K, 0), T, N, K, pw, _dtype_code(dw), ldw,
+                           1 if accumulate else 0, _stream(stream)), "s2_wgrad8")
 
 
 def s2_wait_faults() -> int:

@@ -776,6 +776,31 @@ s2_status s2_matmul8(const uint8_t* x, uint64_t ldx, const uint8_t* x_scales, co
     return cuda_status(launch_matmul8(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+s2_status s2_wgrad8(const void* dy, uint64_t lddy, const uint8_t* x, uint64_t ldx, const uint8_t* x_scales, uint64_t T,
+                    uint64_t N, uint64_t K, void* dw, s2_dtype dt, uint64_t lddw, int accumulate, s2_stream_t stream) {
+    if (!dtype_ok(dt)) return S2_ERR_INVALID_ARG;
+    s2_status st = first_error({check_matrix(T, N, lddy), check_matrix(T, K, ldx), check_matrix(N, K, lddw)});
+    if (st != S2_OK) return st;
+    if (N == 0 || K == 0) return S2_OK;
+    if (!dw) return S2_ERR_INVALID_ARG;
+    const uint64_t esz = size_of(dt);
+    if (!aligned(dw, esz)) return S2_ERR_ALIGNMENT;
+    if (T == 0)  // an empty sum
+        return accumulate ? S2_OK
+                          : cuda_status(cudaMemset2DAsync(dw, (N > 1 ? lddw : K) * esz, 0, K * esz, N,
+                                                          reinterpret_cast<cudaStream_t>(stream)));
+    if (!dy || !x_scales) return S2_ERR_INVALID_ARG;
+    st = check_codes(x, T, K, ldx);
+    if (st != S2_OK) return st;
+    if (!aligned(dy, 2)) return S2_ERR_ALIGNMENT;
+    if (clash({{dw, extent(N, K, lddw, esz)}, {dy, extent(T, N, lddy, 2)}, {x, extent(T, K, ldx, 1)},
+               {x_scales, T * blocks8(K)}}, 1))
+        return S2_ERR_INVALID_ARG;
+    Wgrad8Args a{dy, x, x_scales, dw, T > 1 ? lddy : (N + 7) / 8 * 8, ldx, lddw, (uint32_t)T, (uint32_t)N, (uint32_t)K,
+                 dt == S2_F32 ? 0 : 1, accumulate != 0};
+    return cuda_status(launch_wgrad8(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 s2_status s2_wait_faults(uint32_t* host_count) {
     if (!host_count) return S2_ERR_INVALID_ARG;
     return cuda_status(read_wait_faults(host_count));

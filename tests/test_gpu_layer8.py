@@ -15,6 +15,11 @@ blocks adds eight float32 roundings. So
     |y - exact| <= (K + 33 + 8) * 2^-23 * A          (float32)
 A bfloat16 result is the float32 result rounded once to nearest, and is
 compared with that bit for bit.
+
+Weight gradients: the products dy x (8 and 4 significant bits) are exact, a
+step adds 16 of them and the accumulator, so likewise
+    |dw - exact| <= (17/16 T + 17 + 8 + 2) * 2^-23 * (A + |what was there|),
+the last two for the addition to what was there.
 """
 import numpy as np
 import pytest
@@ -262,6 +267,158 @@ def test_input_gradient_from_transposed_weight():
     wv = ref.unpack(*ref.pack(w.double().numpy(), True), True)
     want, A = gv @ wv, np.abs(gv) @ np.abs(wv)
     assert (np.abs(dx.double().cpu().numpy() - want) <= bound(N, A)).all()
+
+
+def check_wgrad(T, N, K, dtype="f32", dy_off=0, dy_extra=0, dw_extra=0, accumulate=False, kind="normal"):
+    xc, xs, xv = packed(make(T, K, T + K, kind=kind), "rows")
+    ld = N + dy_extra
+    flat = torch.full((dy_off + T * ld,), float("nan"), dtype=torch.bfloat16, device=DEV)
+    dy = flat[dy_off:].reshape(T, ld)[:, :N]
+    dy.copy_(make(T, N, T + N + 1, "bf16"))
+    out = torch.full((N * (K + dw_extra) + 5,), 3.0, dtype=DT[dtype], device=DEV)
+    dw = out[1:1 + N * (K + dw_extra)].reshape(N, K + dw_extra)[:, :K]
+    prior = np.zeros((N, K))
+    if accumulate:
+        dw.copy_(make(N, K, 9, dtype))
+        prior = dw.double().cpu().numpy()
+    dw32 = dw.float() if dtype == "bf16" else dw
+    s2.s2_wgrad8(dy, xc, xs, dw, accumulate)
+    if dtype == "bf16":
+        s2.s2_wgrad8(dy, xc, xs, dw32, accumulate)
+        assert torch.equal(dw, dw32.to(torch.bfloat16))
+    yv = dy.double().cpu().numpy()
+    want, A = yv.T @ xv + prior, np.abs(yv).T @ np.abs(xv) + np.abs(prior)
+    err = np.abs(dw32.double().cpu().numpy() - want)
+    tol = (17 / 16 * T + 27) * 2.0 ** -23 * A + 2.0 ** -149
+    assert (err <= tol).all(), f"worst {np.max(err / np.maximum(tol, 1e-300))} of the bound"
+    dw.fill_(3.0)
+    assert bool((out == 3.0).all()), "wrote outside dw"
+    assert s2.s2_wait_faults() == 0
+
+
+@pytest.mark.parametrize("T", [1, 2, 15, 16, 63, 64, 65, 130, 511, 1000])
+@pytest.mark.parametrize("N,K", [(1, 1), (8, 16), (64, 128), (65, 129), (7, 300), (200, 96), (333, 257)])
+def test_wgrad_sizes(T, N, K):
+    check_wgrad(T, N, K, dw_extra=N % 2)
+
+
+@pytest.mark.parametrize("off,extra", [(0, 0), (0, 1), (1, 0), (3, 2), (5, 3), (7, 7), (8, 4), (2, 8), (0, 8)])
+@pytest.mark.parametrize("N", [300, 328])
+def test_wgrad_strides(N, off, extra):
+    """dY at every kind of misalignment; what lies between its rows is NaN and must not matter."""
+    check_wgrad(150, N, 200, dy_off=off, dy_extra=extra)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("N", [104, 333])
+def test_wgrad_types(N, accumulate, dtype):
+    check_wgrad(300, N, 250, dtype, accumulate=accumulate)
+
+
+@pytest.mark.parametrize("N,extra", [(2500, 0), (2501, 0), (2049, 3)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_wgrad_many_tiles(N, extra, accumulate):
+    """More tiles than SMs, in aligned and unaligned rows."""
+    check_wgrad(200, N, 4000, dy_extra=extra, accumulate=accumulate)
+    check_wgrad(70, 40 * N, 128, "bf16", dy_extra=extra, accumulate=accumulate)
+
+
+def test_wgrad_empty():
+    dw = torch.full((5, 7), 2.0, device=DEV)[:, :6]
+    dy = torch.zeros((0, 5), dtype=torch.bfloat16, device=DEV)
+    x = torch.zeros((0, 6), dtype=torch.uint8, device=DEV)
+    nos = torch.zeros(0, dtype=torch.uint8, device=DEV)
+    s2.s2_wgrad8(dy, x, nos, dw, True)
+    assert bool((dw == 2).all())
+    s2.s2_wgrad8(dy, x, nos, dw)
+    assert bool((dw == 0).all())
+
+
+def test_wgrad_masked_tokens():
+    """Tokens without gradient, among them whole blocks of 64, and without activation."""
+    T, N, K = 400, 130, 140
+    x = make(T, K, 1)
+    x[5:9] = 0
+    dy = make(T, N, 2, "bf16")
+    dy[64:200] = 0
+    xc, xs, xv = packed(x, "rows")
+    dw = torch.empty((N, K), device=DEV)
+    s2.s2_wgrad8(dy.to(DEV), xc, xs, dw)
+    yv = dy.double().numpy()
+    tol = (17 / 16 * T + 27) * 2.0 ** -23 * (np.abs(yv).T @ np.abs(xv))
+    assert (np.abs(dw.double().cpu().numpy() - yv.T @ xv) <= tol + 2.0 ** -149).all()
+    s2.s2_wgrad8(torch.zeros_like(dy).to(DEV), xc, xs, dw)
+    assert bool((dw == 0).all())
+
+
+@pytest.mark.parametrize("N", [128, 129])
+def test_wgrad_not_finite(N):
+    """A NaN activation reaches its column of dW, a NaN gradient its row, and nothing else."""
+    xc, xs, _ = packed(make(100, 200, 1), "rows")
+    xc[33, 150] = 0x7f
+    dy = make(100, N, 2, "bf16").to(DEV)
+    dy[70, 11] = float("nan")
+    dw = torch.empty((N, 200), device=DEV)
+    s2.s2_wgrad8(dy, xc, xs, dw)
+    want = torch.zeros((N, 200), dtype=torch.bool)
+    want[:, 150] = True
+    want[11] = True
+    assert torch.equal(torch.isnan(dw).cpu(), want)
+
+
+def test_wgrad_scale_range():
+    """Activations over the whole range of the scales: 2^-117 and 2^120 are exact in bfloat16."""
+    x = torch.zeros((2, 256))
+    x[0, :128], x[0, 128:] = 3.0e38, 1.0e-38
+    x[1, :128], x[1, 128:] = 1.0, 2.0 ** -126
+    codes, scales = s2.alloc_pack8(2, 256)
+    s2.s2_pack8(x.to(DEV), codes, scales)
+    assert scales.cpu().tolist() == [[247, 10], [119, 10]]
+    v = torch.empty((2, 256), device=DEV)
+    s2.s2_unpack8(codes, scales, v)
+    dw = torch.empty((2, 256), device=DEV)
+    s2.s2_wgrad8(torch.eye(2, dtype=torch.bfloat16, device=DEV), codes, scales, dw)
+    assert torch.equal(dw, v)
+
+
+@pytest.mark.parametrize("N", [512, 515])
+def test_wgrad_repeats_and_streams(N):
+    xc, xs, _ = packed(make(1000, 500, 1), "rows")
+    dy = make(1000, N, 2, "bf16").to(DEV)
+    outs = []
+    for i in range(4):
+        dw = torch.empty((N, 500), device=DEV)
+        st = torch.cuda.Stream() if i % 2 else torch.cuda.current_stream()
+        st.wait_stream(torch.cuda.current_stream())
+        s2.s2_wgrad8(dy, xc, xs, dw, stream=st)
+        torch.cuda.synchronize()
+        outs.append(dw)
+    assert all(torch.equal(o, outs[0]) for o in outs)
+
+
+def test_wgrad_against_differences():
+    """L(W) = sum(G * (X W^T)) is linear in W: its central difference along a direction D of packed
+    weights is <dL/dW, D>. Both sides in float64 from the operators' float32 outputs:
+    each y is off by at most (K + 41) 2^-23 A_y and each dw by (17/16 T + 27) 2^-23 A_w."""
+    T, N, K = 90, 70, 200
+    xc, xs, xv = packed(make(T, K, 1), "rows")
+    g = make(T, N, 2, "bf16")
+    w, d = make(N, K, 3), make(N, K, 4)
+    gv = g.double().numpy()
+    dw = torch.empty((N, K), device=DEV)
+    s2.s2_wgrad8(g.to(DEV), xc, xs, dw)
+    loss, wv, room = [], [], 0.0
+    for sign in (1, -1):
+        wc, ws, v = packed(w + sign * d, "tiles")
+        y = torch.empty((T, N), device=DEV)
+        s2.s2_matmul8(xc, xs, wc, ws, y)
+        loss.append((gv * y.double().cpu().numpy()).sum())
+        wv.append(v)
+        room += (np.abs(gv) * bound(K, np.abs(xv) @ np.abs(v).T)).sum()
+    step = wv[0] - wv[1]
+    room += (np.abs(step) * (17 / 16 * T + 27) * 2.0 ** -23 * (np.abs(gv).T @ np.abs(xv))).sum()
+    assert abs((loss[0] - loss[1]) - (dw.double().cpu().numpy() * step).sum()) <= room
 
 
 def test_binding_refusals():

@@ -118,6 +118,25 @@ def test_matmul_refusals(lib):
     assert call(M=0) == OK and call(N=0) == OK
 
 
+def test_wgrad_refusals(lib):
+    f = _fn(lib, "s2_wgrad8", [VP, U64, VP, U64, VP, U64, U64, U64, VP, I32, U64, I32, VP])
+
+    def call(dy=A, lddy=30, x=A + G, ldx=256, xs=A + 2 * G, T=10, N=30, K=250, dw=A + 3 * G, dt=F32, lddw=250, acc=0):
+        return f(dy, lddy, x, ldx, xs, T, N, K, dw, dt, lddw, acc, None)
+
+    assert call(dt=2) == INVALID
+    assert call(lddy=29) == INVALID and call(ldx=240) == INVALID and call(lddw=249) == INVALID
+    assert call(ldx=250) == ALIGN and call(x=A + G + 4) == ALIGN
+    assert call(dy=A + 1) == ALIGN and call(dw=A + 3 * G + 2) == ALIGN
+    for k in ("dy", "x", "xs", "dw"):
+        assert call(**{k: None}) == INVALID
+    assert call(dw=A + 100) == INVALID           # over dY
+    assert call(dw=A + G) == INVALID and call(dw=A + 2 * G) == INVALID
+    assert call(T=1 << 31) == UNSUP and call(K=1 << 31, ldx=1 << 31, lddw=1 << 31) == UNSUP
+    assert call(N=0) == OK and call(K=0) == OK
+    assert call(T=0, acc=1) == OK                # adds nothing
+
+
 def test_binding_checks():
     import sketch_compressed_sparse_gb300 as s2
 
