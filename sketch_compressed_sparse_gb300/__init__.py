@@ -158,8 +158,10 @@ def _check(status: int, where: str):
 
 
 def _stream(stream: Optional[torch.cuda.Stream]) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # torch.cuda.current_stream().cuda_stream without building a Stream object (0.2 us instead of 2.9 us)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _dev(t: Optional[torch.Tensor], name: str, dtypes, numel: Optional[int] = None):

@@ -148,6 +148,36 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
         : "memory");
 }
 
+// ---- pairs of blocks (a cluster of two on one tile) -----------------------------
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t slot, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free_pair(uint32_t addr, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+}
+// Arrives at `bar` of both blocks once the products issued by this thread so far are done.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{.reg .pred p; setp.ne.u32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+// Arrives at the barrier that lies at `bar` in the first block of the pair.
+__device__ __forceinline__ void bar_arrive_first(uint32_t bar) {
+    asm volatile(
+        "{.reg .b32 p; mapa.shared::cluster.u32 p, %0, 0;\n"
+        "mbarrier.arrive.shared::cluster.b64 _, [p];}" ::"r"(bar)
+        : "memory");
+}
+
 // ---- clusters ----------------------------------------------------------------
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -169,8 +199,13 @@ __device__ __forceinline__ float ld_peer(uint32_t addr, uint32_t rank) {
 // Two-dimensional map of `rows` rows of `cols` elements, `stride` bytes apart,
 // copied in boxes of box_rows x box_cols under the 128-byte swizzle; what lies
 // outside reads as zero. Base 16-byte aligned, stride a multiple of 16.
+// (swizzle = false: rows of the box lie one after the other.)
 cudaError_t make_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t cols, uint64_t rows,
-                     uint64_t stride, uint32_t box_cols, uint32_t box_rows);
+                     uint64_t stride, uint32_t box_cols, uint32_t box_rows, bool swizzle = true);
+
+// Pairs of blocks of kernel `fn` that the device holds at once (cached); also
+// lets the kernel use `smem` bytes of dynamic shared memory.
+cudaError_t max_pairs(const void* fn, int threads, size_t smem, int* pairs);
 
 // Device word that counts waits that ran out.
 cudaError_t wait_fault_word(uint32_t** word);

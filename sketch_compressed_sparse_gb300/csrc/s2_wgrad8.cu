@@ -54,28 +54,62 @@ struct Shape {
     static_assert((size_t)NT * kBF * 4 <= (size_t)kStages * kStage, "a partial tile fits where the stages were");
 };
 
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+// A scale byte as two bfloat16 factors (each twice in a word) that together
+// are 2^(120 + e): see widen16.
+struct Factors {
+    uint32_t first, second;
+};
+__device__ __forceinline__ Factors factors_of(uint32_t b) {
+    const int up = (int)b - 7;  // 120 + e; the byte 0 to 7 gives less than 2^0
+    const int one = min(up, 127), two = up - one;
+    // 2^one and 2^two from their exponent fields; the byte 255 stands for NaN
+    const uint32_t f = (uint32_t)(127 + one) << 7, g = b == 255 ? 0x7fffu : (uint32_t)(127 + two) << 7;
+    return {f | f << 16, g | g << 16};
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    asm("mul.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
-// Four codes times 2^e to four bfloat16, exactly (NaN stays NaN).
-__device__ __forceinline__ uint2 widen4(uint32_t codes, float scale) {
-    uint32_t h[2];
-    asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b;}"
-        : "=r"(h[0]), "=r"(h[1])
-        : "r"(codes));
-    uint32_t o[2];
+// Two e4m3 codes, each in the upper byte of its half, to bfloat16. The code's
+// bits at bfloat16's places are the number times 2^-120 (the exponents' biases
+// are 7 and 127; subnormal codes become subnormal numbers), and the factors
+// bring it to its value: exact, as 2^e >= 2^-117 keeps it normal. (Conversion
+// instructions run at a quarter of this arithmetic's rate or less.)
+__device__ __forceinline__ uint32_t widen2(uint32_t x, Factors f) {
+    const uint32_t y = ((x & 0x7f007f00u) >> 4) | (x & 0x80008000u);
+    return mul_bf16x2(mul_bf16x2(y, f.first), f.second);
+}
+
+__device__ __noinline__ uint32_t nan_fixed(uint32_t codes, uint32_t wide) {  // two codes, in the upper bytes
+    if ((codes & 0x7f00u) == 0x7f00u) wide |= 0x7fffu;
+    if ((codes & 0x7f000000u) == 0x7f000000u) wide |= 0x7fff0000u;
+    return wide;
+}
+
+// Sixteen codes to bfloat16, in order.
+__device__ __forceinline__ void widen16(const uint4& c, Factors f, uint4& lo, uint4& hi) {
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    uint32_t x[8], o[8];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        float lo, hi;
-        asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b;}"
-            : "=f"(lo), "=f"(hi)
-            : "r"(h[i]));
-        o[i] = bf16x2(lo * scale, hi * scale);
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __byte_perm(w[i], 0, 0x1404);
+        x[2 * i + 1] = __byte_perm(w[i], 0, 0x3424);
     }
-    return make_uint2(o[0], o[1]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = widen2(x[i], f);
+    // a byte 0x7f or 0xff carries into its top bit
+    uint32_t nan = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) nan |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;
+    if (nan & 0x80808080u) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = nan_fixed(x[i], o[i]);
+    }
+    lo = make_uint4(o[0], o[1], o[2], o[3]);
+    hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 __device__ __forceinline__ void st_shared(uint32_t addr, uint4 v) {
@@ -289,16 +323,15 @@ __global__ void __launch_bounds__(Shape<NT, TMA>::kWarps * 32, 1)
             const uint32_t kb = tile % a.tiles_k;
             for (uint32_t tb = g.tb0; tb < g.tb1; ++tb, ++it) {
                 uint4 c[kPieces];
-                float sc[kPieces];
+                uint32_t sc[kPieces];
 #pragma unroll
                 for (int i = 0; i < kPieces; ++i) {
                     const uint32_t t = tb * kBT + (w * 2 + i / 2) * 8 + tsub, k = kb * kBF + (i % 2) * 64 + piece * 16;
                     c[i] = make_uint4(0, 0, 0, 0);
-                    sc[i] = 0.0f;
+                    sc[i] = 127;
                     if (t < a.T) {
                         const uint8_t* p = a.x + (uint64_t)t * a.ldx + k;
-                        const uint32_t b = __ldg(a.xs + (uint64_t)t * a.nblk + kb);
-                        sc[i] = __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7fffffffu : b << 23);
+                        sc[i] = __ldg(a.xs + (uint64_t)t * a.nblk + kb);
                         if (k + 16 <= a.K) {
                             c[i] = __ldg(reinterpret_cast<const uint4*>(p));
                         } else {
@@ -316,10 +349,10 @@ __global__ void __launch_bounds__(Shape<NT, TMA>::kWarps * 32, 1)
                 for (int i = 0; i < kPieces; ++i) {
                     const uint32_t row = (w * 2 + i / 2) * 8 + tsub;  // row % 8 == tsub
                     const uint32_t at = base + s * S::kStage + (i % 2) * kGroupBytes + row * 128;
-                    const uint2 p0 = widen4(c[i].x, sc[i]), p1 = widen4(c[i].y, sc[i]);
-                    const uint2 p2 = widen4(c[i].z, sc[i]), p3 = widen4(c[i].w, sc[i]);
-                    st_shared(at + ((2 * piece) ^ tsub) * 16, make_uint4(p0.x, p0.y, p1.x, p1.y));
-                    st_shared(at + ((2 * piece + 1) ^ tsub) * 16, make_uint4(p2.x, p2.y, p3.x, p3.y));
+                    uint4 lo, up;
+                    widen16(c[i], factors_of(sc[i]), lo, up);
+                    st_shared(at + ((2 * piece) ^ tsub) * 16, lo);
+                    st_shared(at + ((2 * piece + 1) ^ tsub) * 16, up);
                 }
                 fence_async();
                 __syncwarp();
@@ -405,6 +438,321 @@ cudaError_t launch(const Wgrad8Args& m, Args a, int sms, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, kernel, ymap, a);
 }
 
+// ---- the wide form: a pair of blocks per tile ----------------------------------
+
+// A tile is 256 features by 256 outputs on two SMs: each block widens its own
+// 128 features and fetches 128 of the outputs, and the pair's product reads
+// both blocks' shared memory, so dY's part of a stage is half of what one
+// block would need for tiles of the same size.
+constexpr int kPairN = 256;            // outputs per tile
+constexpr int kHalfN = kPairN / 2;     // of which a block fetches half
+constexpr int kTeams = 4;              // teams of four warps that widen X, a stage each in turn
+constexpr int kWideners = 4 * kTeams;
+constexpr uint32_t kXRaw = kBT * kBF;  // 8-bit part of a stage
+constexpr uint32_t kBBytes = kHalfN / 64 * kGroupBytes;
+constexpr uint32_t kRowRaw = (kHalfN + 8) * 2;     // a misaligned row's piece: 8 elements more
+constexpr uint32_t kYRaw = kBT * kRowRaw;
+
+struct YMaps {
+    CUtensorMap m[8];  // aligned rows: m[0]; else the rows t = r mod 8 for each r
+};
+
+template <bool ALIGNED>
+struct Pair {
+    static constexpr uint32_t kRaw = kXRaw + (ALIGNED ? 0 : kYRaw);
+    static constexpr uint32_t kOperands = kABytes + kBBytes;
+    static constexpr int kRawStages = ALIGNED ? 6 : 4;
+    static constexpr int kStages = ALIGNED ? 5 : 3;
+    static constexpr int kAcc = 2;
+    static constexpr uint32_t kCols = kAcc * kPairN;
+    static constexpr int kWarps = 4 + kWideners + 2 + (ALIGNED ? 0 : kLoaders);
+    static constexpr size_t kSmem = (size_t)kStages * kOperands + (size_t)kRawStages * kRaw + 1024;
+    static_assert(kRaw % 1024 == 0, "a stage of raw rows starts on the swizzle's period");
+    static_assert(kSmem <= 226 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ uint4 ld_shared(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+
+// Shifts one warp's rows of every stage into place: row q of residue r goes to
+// row 8r + q of the operand (the tokens of a stage may lie in any order as
+// long as both operands agree), which also keeps the stores free of bank conflicts.
+template <int SHIFT>
+__device__ __forceinline__ void realign(uint32_t stages, uint32_t raw0, uint32_t op0, uint32_t rfull, uint32_t rempty,
+                                        uint32_t ofull, uint32_t oempty, const Wait& wt, uint32_t r, uint32_t lane) {
+    using P = Pair<false>;
+    const uint32_t q = lane % 8, c0 = lane / 8 * 4;
+    for (uint32_t it = 0; it < stages; ++it) {
+        const uint32_t rs = it % P::kRawStages, s = it % P::kStages;
+        if (!__all_sync(kFull, bar_wait(rfull + 8 * rs, (it / P::kRawStages) & 1, wt))) return;
+        const uint32_t src = raw0 + rs * P::kRaw + kXRaw + (r * 8 + q) * kRowRaw + c0 * 16;
+        uint4 v[5];
+#pragma unroll
+        for (int i = 0; i < (SHIFT ? 5 : 4); ++i) v[i] = ld_shared(src + 16 * i);
+        if (!__all_sync(kFull, bar_wait(oempty + 8 * s, ((it / P::kStages) & 1) ^ 1, wt))) return;
+        const uint32_t dst = op0 + s * P::kOperands + kABytes + (r * 8 + q) * 128;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t c = c0 + i;
+            st_shared(dst + c / 8 * kGroupBytes + ((c % 8) ^ q) * 16, SHIFT ? shifted<SHIFT>(v[i], v[i + 1]) : v[i]);
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) {
+            bar_arrive(rempty + 8 * rs);
+            bar_arrive_first(ofull + 8 * s);
+        }
+    }
+}
+
+template <bool ALIGNED>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarps * 32, 1)
+    wgrad8_pair_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ YMaps ymaps, const Args a) {
+    using P = Pair<ALIGNED>;
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t bars[2 * P::kRawStages + 3 * P::kStages + 2 * P::kAcc + 1];
+    __shared__ uint32_t tmem_slot;
+    __shared__ uint32_t dead;
+
+    const uint32_t op0 = (smem_u32(raw) + 1023u) & ~1023u, raw0 = op0 + P::kStages * P::kOperands;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = cluster_rank();
+    const uint32_t rfull = smem_u32(bars), rempty = rfull + 8 * P::kRawStages;
+    const uint32_t ofull = rempty + 8 * P::kRawStages, oempty = ofull + 8 * P::kStages, copied = oempty + 8 * P::kStages;
+    const uint32_t acc_full = copied + 8 * P::kStages, acc_empty = acc_full + 8 * P::kAcc, drain = acc_empty + 8 * P::kAcc;
+    constexpr int kFillers = 4 + (ALIGNED ? 0 : kLoaders);  // warps that fill a stage
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < P::kRawStages; ++s) {
+            bar_init(rfull + 8 * s, 1);
+            bar_init(rempty + 8 * s, kFillers);
+        }
+        for (int s = 0; s < P::kStages; ++s) {
+            bar_init(ofull + 8 * s, 2 * kFillers);
+            bar_init(oempty + 8 * s, 1);
+            bar_init(copied + 8 * s, 1);
+        }
+        for (int s = 0; s < P::kAcc; ++s) {
+            bar_init(acc_full + 8 * s, 1);
+            bar_init(acc_empty + 8 * s, 8);
+        }
+        bar_init(drain, 1);
+        dead = 0;
+        bar_fence_init();
+    }
+    constexpr int kCopier = 4 + kWideners, kIssuer = kCopier + 1;
+    if (warp == kIssuer) tmem_alloc_pair(smem_u32(&tmem_slot), P::kCols);
+    fence_before();
+    cluster_sync();
+    fence_after();
+    const uint32_t tmem = tmem_slot;
+    const Wait wt{&dead, a.faults};
+    const uint32_t first = blockIdx.x / 2, step = gridDim.x / 2, tiles = a.tiles_k * a.tiles_n;
+    const uint32_t tblocks = (a.T + kBT - 1) / kBT;
+    const uint32_t mine = first < tiles ? (tiles - first - 1) / step + 1 : 0, stages = mine * tblocks;
+
+    if (warp == kCopier) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (uint32_t tile = first; ok && tile < tiles; tile += step) {
+                const int k0 = (int)((tile % a.tiles_k * 2 + rank) * kBF);
+                const int n0 = (int)(tile / a.tiles_k * kPairN + rank * kHalfN);
+                for (uint32_t tb = 0; tb < tblocks; ++tb, ++it) {
+                    const uint32_t rs = it % P::kRawStages, s = it % P::kStages;
+                    if (!(ok = bar_wait(rempty + 8 * rs, ((it / P::kRawStages) & 1) ^ 1, wt))) break;
+                    bar_expect(rfull + 8 * rs, P::kRaw);
+                    const uint32_t dst = raw0 + rs * P::kRaw;
+                    tma_2d(dst, &xmap, rfull + 8 * rs, k0, (int)(tb * kBT));
+                    if (ALIGNED) {
+                        if (!(ok = bar_wait(oempty + 8 * s, ((it / P::kStages) & 1) ^ 1, wt))) {
+                            ++it;  // the copy of X is on its way
+                            break;
+                        }
+                        bar_expect(copied + 8 * s, kBBytes);
+#pragma unroll
+                        for (int c = 0; c < kHalfN / 64; ++c)
+                            tma_2d(op0 + s * P::kOperands + kABytes + c * kGroupBytes, &ymaps.m[0], copied + 8 * s,
+                                   n0 + 64 * c, (int)(tb * kBT));
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < 8; ++r)
+                            tma_2d(dst + kXRaw + r * 8 * kRowRaw, &ymaps.m[r], rfull + 8 * rs, n0, (int)(tb * kBT / 8));
+                    }
+                }
+            }
+            // nothing of this block's may still be on its way when it ends
+            if (dead) {
+                for (uint32_t j = it > (uint32_t)P::kRawStages ? it - P::kRawStages : 0; j < it; ++j)
+                    bar_drain(rfull + 8 * (j % P::kRawStages), (j / P::kRawStages) & 1);
+                if (ALIGNED)
+                    for (uint32_t j = it > (uint32_t)P::kStages ? it - P::kStages : 0; j < it; ++j)
+                        bar_drain(copied + 8 * (j % P::kStages), (j / P::kStages) & 1);
+            }
+        }
+    } else if (warp == kIssuer) {
+        if (lane == 0 && rank == 0) {
+            // D float32, A and B bfloat16, both with rows along M (256) and N (256)
+            constexpr uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | 1u << 15 | 1u << 16 | (kPairN / 8) << 17 |
+                                       (2 * kBF / 16) << 24;
+            uint32_t it = 0, n = 0;
+            bool ok = true;
+            for (uint32_t tile = first; ok && tile < tiles; tile += step, ++n) {
+                const uint32_t buf = n % P::kAcc;
+                if (!(ok = bar_wait(acc_empty + 8 * buf, ((n / P::kAcc) & 1) ^ 1, wt))) break;
+                fence_after();
+                for (uint32_t tb = 0; tb < tblocks; ++tb, ++it) {
+                    const uint32_t s = it % P::kStages;
+                    if (!(ok = bar_wait(ofull + 8 * s, (it / P::kStages) & 1, wt))) break;
+                    fence_after();
+                    const uint64_t ad = smem_desc(op0 + s * P::kOperands, kGroupBytes, 1024);
+                    const uint64_t bd = smem_desc(op0 + s * P::kOperands + kABytes, kGroupBytes, 1024);
+#pragma unroll
+                    for (int j = 0; j < kBT / 16; ++j)
+                        mma_bf16_pair(tmem + buf * kPairN, ad + 128 * j, bd + 128 * j, idesc, tb > 0 || j > 0);
+                    mma_commit_pair(oempty + 8 * s);
+                }
+                if (ok) mma_commit_pair(acc_full + 8 * buf);
+            }
+            if (dead) {
+                mma_commit_pair(drain);
+                bar_drain(drain, 0);
+            }
+        }
+    } else if (warp > kIssuer) {
+        const uint32_t r = warp - kIssuer - 1;
+        switch ((reinterpret_cast<uintptr_t>(a.dy) + (uint64_t)r * a.lddy * 2) % 16 / 2) {
+            case 0: realign<0>(stages, raw0, op0, rfull, rempty, ofull, oempty, wt, r, lane); break;
+            case 1: realign<2>(stages, raw0, op0, rfull, rempty, ofull, oempty, wt, r, lane); break;
+            case 2: realign<4>(stages, raw0, op0, rfull, rempty, ofull, oempty, wt, r, lane); break;
+            case 3: realign<6>(stages, raw0, op0, rfull, rempty, ofull, oempty, wt, r, lane); break;
+            case 4: realign<8>(stages, raw0, op0, rfull, rempty, ofull, oempty, wt, r, lane); break;
+            case 5: realign<10>(stages, raw0, op0, rfull, rempty, ofull, oempty, wt, r, lane); break;
+            case 6: realign<12>(stages, raw0, op0, rfull, rempty, ofull, oempty, wt, r, lane); break;
+            default: realign<14>(stages, raw0, op0, rfull, rempty, ofull, oempty, wt, r, lane); break;
+        }
+    } else if (warp >= 4) {
+        // Widen X: a warp takes sixteen tokens, eight tokens by 64 features at a
+        // step, four lanes a token. Eight neighbouring lanes hold tokens t and
+        // t + 4, whose swizzled pieces lie in different banks; the second four
+        // store their two pieces in the other order for the same reason. The
+        // teams take the stages in turn: a stage's chain of waits, loads and
+        // fences is several times as long as its product.
+        const uint32_t team = (warp - 4) / 4, w = warp % 4, piece = lane % 4, hi = lane / 4 % 2, sub = lane / 8 + 4 * hi;
+        uint32_t it = 0;
+        bool ok = true;
+        // scale bytes are fetched one turn ahead
+        uint32_t ahead = team;
+        auto next_scales = [&]() -> uint32_t {
+            uint32_t b = 127, b8 = 127;
+            if (ahead < stages) {
+                const uint32_t i = ahead / tblocks, kb = (first + i * step) % a.tiles_k * 2 + rank;
+                const uint32_t t = (ahead - i * tblocks) * kBT + w * 16 + sub;
+                if (kb < a.nblk && t < a.T) b = __ldg(a.xs + (uint64_t)t * a.nblk + kb);
+                if (kb < a.nblk && t + 8 < a.T) b8 = __ldg(a.xs + (uint64_t)(t + 8) * a.nblk + kb);
+                b |= b8 << 8;
+            }
+            ahead += kTeams;
+            return b;
+        };
+        uint32_t b0 = next_scales();
+        for (it = team; ok && it < stages; it += kTeams) {
+            const uint32_t b = b0;
+            b0 = next_scales();
+            const uint32_t rs = it % P::kRawStages, s = it % P::kStages;
+            if (!(ok = __all_sync(kFull, bar_wait(rfull + 8 * rs, (it / P::kRawStages) & 1, wt)))) break;
+            uint4 c[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t from = w * 16 + i / 2 * 8 + sub;
+                c[i] = ld_shared(raw0 + rs * P::kRaw + from * 128 + ((i % 2 * 4 + piece) ^ sub) * 16);
+            }
+            if (!(ok = __all_sync(kFull, bar_wait(oempty + 8 * s, ((it / P::kStages) & 1) ^ 1, wt)))) break;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t from = w * 16 + i / 2 * 8 + sub;
+                const uint32_t to = ALIGNED ? from : sub * 8 + w * 2 + i / 2;  // token's row in the operand
+                const uint32_t at = op0 + s * P::kOperands + i % 2 * kGroupBytes + to * 128;
+                uint4 lo, up;
+                widen16(c[i], factors_of(i / 2 ? b >> 8 : b & 255), lo, up);
+                const uint32_t at_lo = at + ((2 * piece) ^ (to % 8)) * 16, at_up = at + ((2 * piece + 1) ^ (to % 8)) * 16;
+                st_shared(hi ? at_up : at_lo, hi ? up : lo);
+                st_shared(hi ? at_lo : at_up, hi ? lo : up);
+            }
+            fence_async();
+            if (ALIGNED && !(ok = __all_sync(kFull, bar_wait(copied + 8 * s, (it / P::kStages) & 1, wt)))) break;
+            __syncwarp();
+            if (lane == 0) {
+                bar_arrive(rempty + 8 * rs);
+                bar_arrive_first(ofull + 8 * s);
+            }
+        }
+    } else {
+        uint32_t n = 0;
+        for (uint32_t tile = first; tile < tiles; tile += step, ++n) {
+            const uint32_t buf = n % P::kAcc;
+            if (!__all_sync(kFull, bar_wait(acc_full + 8 * buf, (n / P::kAcc) & 1, wt))) break;
+            fence_after();
+            const uint32_t k = (tile % a.tiles_k * 2 + rank) * kBF + warp * 32 + lane, n0 = tile / a.tiles_k * kPairN;
+#pragma unroll 1
+            for (int c = 0; c < kPairN; c += 16) {
+                uint32_t r[16];
+                tmem_ld16(tmem + ((uint32_t)warp << 21) + buf * kPairN + c, r);
+                wait_ld();
+                if (k < a.K) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (n0 + c + j < a.N) store(a, n0 + c + j, k, __uint_as_float(r[j]));
+                }
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive_first(acc_empty + 8 * buf);
+        }
+    }
+
+    __syncwarp();
+    fence_before();
+    cluster_sync();  // the other block's products and arrivals reach into this one
+    if (warp == kIssuer) tmem_free_pair(tmem, P::kCols);
+}
+
+template <bool ALIGNED>
+cudaError_t launch_pair(const Wgrad8Args& m, Args a, cudaStream_t s) {
+    using P = Pair<ALIGNED>;
+    CUtensorMap xmap;
+    YMaps ymaps{};
+    cudaError_t e = make_map(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, m.x, m.K, m.T, m.ldx, kBF, kBT);
+    if (e != cudaSuccess) return e;
+    if (ALIGNED) {
+        e = make_map(&ymaps.m[0], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, m.dy, m.N, m.T, m.lddy * 2, 64, kBT);
+        if (e != cudaSuccess) return e;
+    } else {
+        for (uint32_t r = 0; r < 8; ++r) {
+            // row r rounded down to 16 bytes and every eighth row from there: the same shift in all of them
+            const uintptr_t row = reinterpret_cast<uintptr_t>(m.dy) + (uint64_t)r * m.lddy * 2;
+            const uint32_t shift = row % 16;
+            e = make_map(&ymaps.m[r], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, reinterpret_cast<const void*>(row - shift),
+                         m.N + shift / 2, (m.T - r + 7) / 8, m.lddy * 16, kHalfN + 8, kBT / 8, false);
+            if (e != cudaSuccess) return e;
+        }
+    }
+    a.tiles_k = (m.K + 2 * kBF - 1) / (2 * kBF);
+    a.tiles_n = (m.N + kPairN - 1) / kPairN;
+    const uint64_t tiles = (uint64_t)a.tiles_k * a.tiles_n;
+    if (tiles * ((m.T + kBT - 1) / kBT) > 0xffffffffull) return cudaErrorInvalidValue;
+    auto kernel = wgrad8_pair_kernel<ALIGNED>;
+    int pairs = 0;
+    e = max_pairs(reinterpret_cast<const void*>(kernel), P::kWarps * 32, P::kSmem, &pairs);
+    if (e != cudaSuccess) return e;
+    const uint32_t grid = 2 * (uint32_t)(tiles < (uint64_t)pairs ? tiles : pairs);
+    kernel<<<grid, P::kWarps * 32, P::kSmem, s>>>(xmap, ymaps, a);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_wgrad8(const Wgrad8Args& m, cudaStream_t s) {
@@ -428,9 +776,9 @@ cudaError_t launch_wgrad8(const Wgrad8Args& m, cudaStream_t s) {
     e = tc::wait_fault_word(&a.faults);
     if (e != cudaSuccess) return e;
     const bool tma = reinterpret_cast<uintptr_t>(m.dy) % 16 == 0 && m.lddy % 8 == 0;
-    const bool wide = (uint64_t)a.tiles_k * ((m.N + 255) / 256) >= (uint64_t)di.sms;
-    if (tma) return wide ? launch<256, true>(m, a, di.sms, s) : launch<64, true>(m, a, di.sms, s);
-    return wide ? launch<256, false>(m, a, di.sms, s) : launch<64, false>(m, a, di.sms, s);
+    const bool wide = (uint64_t)((m.K + 255) / 256) * ((m.N + 255) / 256) * 2 >= (uint64_t)di.sms && m.T >= 8;
+    if (wide) return tma ? launch_pair<true>(m, a, s) : launch_pair<false>(m, a, s);
+    return tma ? launch<64, true>(m, a, di.sms, s) : launch<64, false>(m, a, di.sms, s);
 }
 
 }  // namespace s2

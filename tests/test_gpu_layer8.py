@@ -382,6 +382,26 @@ def test_wgrad_scale_range():
     assert torch.equal(dw, v)
 
 
+@pytest.mark.parametrize("extra", [0, 1])
+def test_wgrad_every_code_and_byte(extra):
+    """dY = 1: dW holds X's values exactly, for every code (NaN aside) under every byte that packing writes."""
+    n = 238
+    codes = torch.arange(256, dtype=torch.int32).to(torch.uint8).repeat(n, 1)
+    codes[:, [0x7f, 0xff]] = 0
+    scales = torch.arange(10, 248, dtype=torch.int32).to(torch.uint8).reshape(-1, 1).repeat(1, 2).contiguous()
+    want = ref.unpack(codes.numpy(), scales.numpy(), False)
+    with np.errstate(over="ignore"):
+        want = np.where(np.abs(want) >= 2.0 ** 128, 0.0, want)  # past float32: left out
+    codes = torch.where(torch.from_numpy(want == 0), torch.zeros_like(codes), codes)
+    dy = torch.zeros((n, 20000 + extra), dtype=torch.bfloat16, device=DEV)  # wide enough for every form
+    dy[:, :n] = torch.eye(n)
+    for N in (n + extra, 20000 + extra):
+        dw = torch.empty((N, 256), device=DEV)
+        s2.s2_wgrad8(dy[:, :N] if extra else dy[:, :N].contiguous(), codes.to(DEV), scales.to(DEV), dw)
+        np.testing.assert_array_equal(dw[:n].double().cpu().numpy(), want)
+        assert bool((dw[n:] == 0).all())
+
+
 @pytest.mark.parametrize("N", [512, 515])
 def test_wgrad_repeats_and_streams(N):
     xc, xs, _ = packed(make(1000, 500, 1), "rows")
