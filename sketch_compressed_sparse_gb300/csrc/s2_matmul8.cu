@@ -129,7 +129,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     };
 
     if (warp == 8) {
-        if (lane == 0) {
+        {
+            const bool leader = elect();
             uint32_t it = 0;
             bool ok = true;
             for (uint32_t tile = first; ok && tile < tiles; tile += step) {
@@ -138,10 +139,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 for (uint32_t kb = kb0; kb < kb1; ++kb, ++it) {
                     const int s = it % S::kStages;
                     if (!(ok = bar_wait(empty(s), ((it / S::kStages) & 1) ^ 1, wt))) break;
-                    bar_expect(full(s), S::kStage);
                     const uint32_t dst = base + s * S::kStage;
-                    tma_2d(dst, &wmap, full(s), (int)(kb * kBK), (int)f0);
-                    tma_2d(dst + kABytes, &xmap, full(s), (int)(kb * kBK), (int)t0);
+                    if (leader) {
+                        bar_expect(full(s), S::kStage);
+                        tma_2d(dst, &wmap, full(s), (int)(kb * kBK), (int)f0);
+                        tma_2d(dst + kABytes, &xmap, full(s), (int)(kb * kBK), (int)t0);
+                    }
                 }
             }
             // nothing of this block's may still be on its way when it ends
@@ -150,7 +153,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     bar_drain(full(j % S::kStages), (j / S::kStages) & 1);
         }
     } else if (warp == 9) {
-        if (lane == 0) {
+        {
+            const bool leader = elect();  // the thread that issues the products also commits them
             // D float32, A and B e4m3, both along K, UE8M0 scales, N = NT, M = 128
             const uint32_t idesc = (uint32_t)(NT / 8) << 17 | 1u << 23 | (uint32_t)(kBF / 16) << 24;
             uint32_t it = 0, grp = 0, n = 0;
@@ -170,18 +174,19 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     const uint64_t ad = smem_desc(base + s * S::kStage, 16, 1024);
                     const uint64_t bd = smem_desc(base + s * S::kStage + kABytes, 16, 1024);
                     const uint32_t id = idesc | (i % kGroup) << 4 | (i % kGroup) << 29;
+                    const bool last = i % kGroup == kGroup - 1 || kb + 1 == kb1;
+                    if (leader) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)  // 32 bytes of K each
-                        mma_mx8(d, ad + 2 * j, bd + 2 * j, id, sf, sf + 4, i > 0 || j > 0);
-                    mma_commit(empty(s));
-                    if (i % kGroup == kGroup - 1 || kb + 1 == kb1) {
-                        mma_commit(sf_empty(grp % S::kRing));
-                        ++grp;
+                        for (int j = 0; j < 4; ++j)  // 32 bytes of K each
+                            mma_mx8(d, ad + 2 * j, bd + 2 * j, id, sf, sf + 4, i > 0 || j > 0);
+                        mma_commit(empty(s));
+                        if (last) mma_commit(sf_empty(grp % S::kRing));
                     }
+                    if (last) ++grp;
                 }
-                if (ok) mma_commit(acc_full(buf));
+                if (ok && leader) mma_commit(acc_full(buf));
             }
-            if (dead) {  // products in flight still read this block's memory
+            if (dead && leader) {  // products in flight still read this block's memory
                 mma_commit(drain);
                 bar_drain(drain, 0);
             }
@@ -207,7 +212,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     const uint32_t t = t0 + 32 * c + lane;
                     wb[c] = 32 * c < NT && t < a.M ? scale_word(a.xs + (uint64_t)t * a.nblk, kb, a.nblk) : 0x7f7f7f7fu;
                 }
-                if (!(ok = __all_sync(kFull, bar_wait(sf_empty(grp % S::kRing), ((grp / S::kRing) & 1) ^ 1, wt)))) break;
+                if (!(ok = bar_wait(sf_empty(grp % S::kRing), ((grp / S::kRing) & 1) ^ 1, wt))) break;
                 fence_after();
                 const uint32_t sf = tmem + quarter + S::kAcc * NT + (grp % S::kRing) * S::kScaleCols;
                 tmem_st4(sf, wa[0], wa[1], wa[2], wa[3]);
@@ -223,7 +228,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         uint32_t n = 0;
         for (uint32_t tile = first; tile < tiles; tile += step, ++n) {
             const int buf = n % S::kAcc;
-            if (!__all_sync(kFull, bar_wait(acc_full(buf), (n / S::kAcc) & 1, wt))) break;
+            if (!bar_wait(acc_full(buf), (n / S::kAcc) & 1, wt)) break;
             fence_after();
             uint32_t f0, t0;
             place(tile, f0, t0);

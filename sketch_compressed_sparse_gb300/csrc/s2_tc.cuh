@@ -13,6 +13,15 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return (uint32_t)__cvta_generic_to_shared(p);
 }
 
+// True in one lane of a converged warp. The warps that issue copies and
+// products stay converged and issue under this predicate: their loop counters
+// and addresses are then uniform, which those instructions' operands have to be.
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{.reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p;}" : "=r"(p));
+    return p != 0;
+}
+
 // ---- mbarriers ---------------------------------------------------------------
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
@@ -65,11 +74,13 @@ static __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity,
         }
     }
 }
+// Whole warp, converged; the answer is the same in every lane.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const Wait& w) {
+    if (__all_sync(0xffffffffu, bar_try(bar, parity))) return true;
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
-        if (bar_try(bar, parity)) return true;
-    return bar_wait_slow(bar, parity, w);
+        if (__all_sync(0xffffffffu, bar_try(bar, parity))) return true;
+    return __all_sync(0xffffffffu, bar_wait_slow(bar, parity, w));
 }
 // For the copies in flight of a block that gave up: no `dead` word ends it.
 static __device__ __noinline__ void bar_drain(uint32_t bar, uint32_t parity) {

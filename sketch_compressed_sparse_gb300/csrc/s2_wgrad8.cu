@@ -76,11 +76,14 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 // Two e4m3 codes, each in the upper byte of its half, to bfloat16. The code's
 // bits at bfloat16's places are the number times 2^-120 (the exponents' biases
 // are 7 and 127; subnormal codes become subnormal numbers), and the factors
-// bring it to its value: exact, as 2^e >= 2^-117 keeps it normal. (Conversion
-// instructions run at a quarter of this arithmetic's rate or less.)
+// bring it to its value: exact, as 2^e >= 2^-117 keeps it normal. ONE: the
+// second factor is 1. (Conversion instructions run at a quarter of this
+// arithmetic's rate or less: the wide form takes 0.55 of the time it took with them.)
+template <bool ONE>
 __device__ __forceinline__ uint32_t widen2(uint32_t x, Factors f) {
     const uint32_t y = ((x & 0x7f007f00u) >> 4) | (x & 0x80008000u);
-    return mul_bf16x2(mul_bf16x2(y, f.first), f.second);
+    const uint32_t v = mul_bf16x2(y, f.first);
+    return ONE ? v : mul_bf16x2(v, f.second);
 }
 
 __device__ __noinline__ uint32_t nan_fixed(uint32_t codes, uint32_t wide) {  // two codes, in the upper bytes
@@ -90,6 +93,7 @@ __device__ __noinline__ uint32_t nan_fixed(uint32_t codes, uint32_t wide) {  // 
 }
 
 // Sixteen codes to bfloat16, in order.
+template <bool ONE>
 __device__ __forceinline__ void widen16(const uint4& c, Factors f, uint4& lo, uint4& hi) {
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
     uint32_t x[8], o[8];
@@ -99,7 +103,7 @@ __device__ __forceinline__ void widen16(const uint4& c, Factors f, uint4& lo, ui
         x[2 * i + 1] = __byte_perm(w[i], 0, 0x3424);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = widen2(x[i], f);
+    for (int i = 0; i < 8; ++i) o[i] = widen2<ONE>(x[i], f);
     // a byte 0x7f or 0xff carries into its top bit
     uint32_t nan = 0;
 #pragma unroll
@@ -185,7 +189,7 @@ __device__ __forceinline__ void load_rows(const Args& a, const Ring& g, const Wa
                 }
             }
             const int s = it % S::kStages;
-            if (!__all_sync(kFull, bar_wait(g.bar0 + 8u * (S::kStages + s), ((it / S::kStages) & 1) ^ 1, wt))) return;
+            if (!bar_wait(g.bar0 + 8u * (S::kStages + s), ((it / S::kStages) & 1) ^ 1, wt)) return;
 #pragma unroll
             for (int j = 0; j < kLoads; ++j) {
                 const uint32_t t = w + 8 * (j * kRows + sub);  // t % 8 == w
@@ -250,7 +254,8 @@ __global__ void __launch_bounds__(Shape<NT, TMA>::kWarps * 32, 1)
     g.tb1 = (uint32_t)((uint64_t)tblocks * (rank + 1) / a.split);
 
     if (warp == 8) {
-        if (TMA && lane == 0) {
+        if (TMA) {
+            const bool leader = elect();
             uint32_t it = 0;
             bool ok = true;
             for (uint32_t tile = g.first; ok && tile < g.tiles; tile += g.step) {
@@ -258,11 +263,13 @@ __global__ void __launch_bounds__(Shape<NT, TMA>::kWarps * 32, 1)
                 for (uint32_t tb = g.tb0; tb < g.tb1; ++tb, ++it) {
                     const int s = it % S::kStages;
                     if (!(ok = bar_wait(empty(s), ((it / S::kStages) & 1) ^ 1, wt))) break;
-                    bar_expect(copied(s), NT / 64 * kGroupBytes);
+                    if (leader) {
+                        bar_expect(copied(s), NT / 64 * kGroupBytes);
 #pragma unroll
-                    for (int c = 0; c < NT / 64; ++c)
-                        tma_2d(base + s * S::kStage + kABytes + c * kGroupBytes, &ymap, copied(s), (int)(n0 + 64 * c),
-                               (int)(tb * kBT));
+                        for (int c = 0; c < NT / 64; ++c)
+                            tma_2d(base + s * S::kStage + kABytes + c * kGroupBytes, &ymap, copied(s), (int)(n0 + 64 * c),
+                                   (int)(tb * kBT));
+                    }
                 }
             }
             // nothing of this block's may still be on its way when it ends
@@ -271,7 +278,8 @@ __global__ void __launch_bounds__(Shape<NT, TMA>::kWarps * 32, 1)
                     bar_drain(copied(j % S::kStages), (j / S::kStages) & 1);
         }
     } else if (warp == 9) {
-        if (lane == 0) {
+        {
+            const bool leader = elect();  // the thread that issues the products also commits them
             // D float32, A and B bfloat16, both with rows along M and N
             const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | 1u << 15 | 1u << 16 | (uint32_t)(NT / 8) << 17 |
                                    (uint32_t)(kBF / 16) << 24;
@@ -288,14 +296,16 @@ __global__ void __launch_bounds__(Shape<NT, TMA>::kWarps * 32, 1)
                     fence_after();
                     const uint64_t ad = smem_desc(base + s * S::kStage, kGroupBytes, 1024);
                     const uint64_t bd = smem_desc(base + s * S::kStage + kABytes, kGroupBytes, 1024);
+                    if (leader) {
 #pragma unroll
-                    for (int j = 0; j < kBT / 16; ++j)  // 16 tokens: two groups of eight rows
-                        mma_bf16(tmem + buf * NT, ad + 128 * j, bd + 128 * j, idesc, tb > g.tb0 || j > 0);
-                    mma_commit(empty(s));
+                        for (int j = 0; j < kBT / 16; ++j)  // 16 tokens: two groups of eight rows
+                            mma_bf16(tmem + buf * NT, ad + 128 * j, bd + 128 * j, idesc, tb > g.tb0 || j > 0);
+                        mma_commit(empty(s));
+                    }
                 }
-                if (ok) mma_commit(acc_full(buf));
+                if (ok && leader) mma_commit(acc_full(buf));
             }
-            if (dead) {
+            if (dead && leader) {
                 mma_commit(drain);
                 bar_drain(drain, 0);
             }
@@ -344,13 +354,13 @@ __global__ void __launch_bounds__(Shape<NT, TMA>::kWarps * 32, 1)
                     }
                 }
                 const int s = it % S::kStages;
-                if (!(ok = __all_sync(kFull, bar_wait(empty(s), ((it / S::kStages) & 1) ^ 1, wt)))) break;
+                if (!(ok = bar_wait(empty(s), ((it / S::kStages) & 1) ^ 1, wt))) break;
 #pragma unroll
                 for (int i = 0; i < kPieces; ++i) {
                     const uint32_t row = (w * 2 + i / 2) * 8 + tsub;  // row % 8 == tsub
                     const uint32_t at = base + s * S::kStage + (i % 2) * kGroupBytes + row * 128;
                     uint4 lo, up;
-                    widen16(c[i], factors_of(sc[i]), lo, up);
+                    widen16<false>(c[i], factors_of(sc[i]), lo, up);
                     st_shared(at + ((2 * piece) ^ tsub) * 16, lo);
                     st_shared(at + ((2 * piece + 1) ^ tsub) * 16, up);
                 }
@@ -363,7 +373,7 @@ __global__ void __launch_bounds__(Shape<NT, TMA>::kWarps * 32, 1)
         uint32_t n = 0;
         for (uint32_t tile = g.first; tile < g.tiles; tile += g.step, ++n) {
             const int buf = n % S::kAcc;
-            if (!__all_sync(kFull, bar_wait(acc_full(buf), (n / S::kAcc) & 1, wt))) break;
+            if (!bar_wait(acc_full(buf), (n / S::kAcc) & 1, wt)) break;
             fence_after();
             const uint32_t k = tile % a.tiles_k * kBF + warp * 32 + lane, n0 = tile / a.tiles_k * NT;
 #pragma unroll 1
@@ -478,8 +488,9 @@ __device__ __forceinline__ uint4 ld_shared(uint32_t addr) {
 }
 
 // Shifts one warp's rows of every stage into place: row q of residue r goes to
-// row 8r + q of the operand (the tokens of a stage may lie in any order as
-// long as both operands agree), which also keeps the stores free of bank conflicts.
+// row 8r + (q ^ r % 2) of the operand (the tokens of a stage may lie in any
+// order as long as both operands agree), which keeps this warp's and the
+// wideners' stores free of bank conflicts.
 template <int SHIFT>
 __device__ __forceinline__ void realign(uint32_t stages, uint32_t raw0, uint32_t op0, uint32_t rfull, uint32_t rempty,
                                         uint32_t ofull, uint32_t oempty, const Wait& wt, uint32_t r, uint32_t lane) {
@@ -487,17 +498,17 @@ __device__ __forceinline__ void realign(uint32_t stages, uint32_t raw0, uint32_t
     const uint32_t q = lane % 8, c0 = lane / 8 * 4;
     for (uint32_t it = 0; it < stages; ++it) {
         const uint32_t rs = it % P::kRawStages, s = it % P::kStages;
-        if (!__all_sync(kFull, bar_wait(rfull + 8 * rs, (it / P::kRawStages) & 1, wt))) return;
+        if (!bar_wait(rfull + 8 * rs, (it / P::kRawStages) & 1, wt)) return;
         const uint32_t src = raw0 + rs * P::kRaw + kXRaw + (r * 8 + q) * kRowRaw + c0 * 16;
         uint4 v[5];
 #pragma unroll
         for (int i = 0; i < (SHIFT ? 5 : 4); ++i) v[i] = ld_shared(src + 16 * i);
-        if (!__all_sync(kFull, bar_wait(oempty + 8 * s, ((it / P::kStages) & 1) ^ 1, wt))) return;
-        const uint32_t dst = op0 + s * P::kOperands + kABytes + (r * 8 + q) * 128;
+        if (!bar_wait(oempty + 8 * s, ((it / P::kStages) & 1) ^ 1, wt)) return;
+        const uint32_t row = q ^ (r % 2), dst = op0 + s * P::kOperands + kABytes + (r * 8 + row) * 128;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t c = c0 + i;
-            st_shared(dst + c / 8 * kGroupBytes + ((c % 8) ^ q) * 16, SHIFT ? shifted<SHIFT>(v[i], v[i + 1]) : v[i]);
+            st_shared(dst + c / 8 * kGroupBytes + ((c % 8) ^ row) * 16, SHIFT ? shifted<SHIFT>(v[i], v[i + 1]) : v[i]);
         }
         fence_async();
         __syncwarp();
@@ -555,7 +566,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
     const uint32_t mine = first < tiles ? (tiles - first - 1) / step + 1 : 0, stages = mine * tblocks;
 
     if (warp == kCopier) {
-        if (lane == 0) {
+        {
+            const bool leader = elect();
             uint32_t it = 0;
             bool ok = true;
             for (uint32_t tile = first; ok && tile < tiles; tile += step) {
@@ -564,23 +576,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
                 for (uint32_t tb = 0; tb < tblocks; ++tb, ++it) {
                     const uint32_t rs = it % P::kRawStages, s = it % P::kStages;
                     if (!(ok = bar_wait(rempty + 8 * rs, ((it / P::kRawStages) & 1) ^ 1, wt))) break;
-                    bar_expect(rfull + 8 * rs, P::kRaw);
                     const uint32_t dst = raw0 + rs * P::kRaw;
-                    tma_2d(dst, &xmap, rfull + 8 * rs, k0, (int)(tb * kBT));
+                    if (leader) {
+                        bar_expect(rfull + 8 * rs, P::kRaw);
+                        tma_2d(dst, &xmap, rfull + 8 * rs, k0, (int)(tb * kBT));
+                        if (!ALIGNED) {
+#pragma unroll
+                            for (int r = 0; r < 8; ++r)
+                                tma_2d(dst + kXRaw + r * 8 * kRowRaw, &ymaps.m[r], rfull + 8 * rs, n0, (int)(tb * kBT / 8));
+                        }
+                    }
                     if (ALIGNED) {
                         if (!(ok = bar_wait(oempty + 8 * s, ((it / P::kStages) & 1) ^ 1, wt))) {
                             ++it;  // the copy of X is on its way
                             break;
                         }
-                        bar_expect(copied + 8 * s, kBBytes);
+                        if (leader) {
+                            bar_expect(copied + 8 * s, kBBytes);
 #pragma unroll
-                        for (int c = 0; c < kHalfN / 64; ++c)
-                            tma_2d(op0 + s * P::kOperands + kABytes + c * kGroupBytes, &ymaps.m[0], copied + 8 * s,
-                                   n0 + 64 * c, (int)(tb * kBT));
-                    } else {
-#pragma unroll
-                        for (int r = 0; r < 8; ++r)
-                            tma_2d(dst + kXRaw + r * 8 * kRowRaw, &ymaps.m[r], rfull + 8 * rs, n0, (int)(tb * kBT / 8));
+                            for (int c = 0; c < kHalfN / 64; ++c)
+                                tma_2d(op0 + s * P::kOperands + kABytes + c * kGroupBytes, &ymaps.m[0], copied + 8 * s,
+                                       n0 + 64 * c, (int)(tb * kBT));
+                        }
                     }
                 }
             }
@@ -594,7 +611,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
             }
         }
     } else if (warp == kIssuer) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
+            const bool leader = elect();  // the thread that issues the products also commits them
             // D float32, A and B bfloat16, both with rows along M (256) and N (256)
             constexpr uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | 1u << 15 | 1u << 16 | (kPairN / 8) << 17 |
                                        (2 * kBF / 16) << 24;
@@ -610,14 +628,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
                     fence_after();
                     const uint64_t ad = smem_desc(op0 + s * P::kOperands, kGroupBytes, 1024);
                     const uint64_t bd = smem_desc(op0 + s * P::kOperands + kABytes, kGroupBytes, 1024);
+                    if (leader) {
 #pragma unroll
-                    for (int j = 0; j < kBT / 16; ++j)
-                        mma_bf16_pair(tmem + buf * kPairN, ad + 128 * j, bd + 128 * j, idesc, tb > 0 || j > 0);
-                    mma_commit_pair(oempty + 8 * s);
+                        for (int j = 0; j < kBT / 16; ++j)
+                            mma_bf16_pair(tmem + buf * kPairN, ad + 128 * j, bd + 128 * j, idesc, tb > 0 || j > 0);
+                        mma_commit_pair(oempty + 8 * s);
+                    }
                 }
-                if (ok) mma_commit_pair(acc_full + 8 * buf);
+                if (ok && leader) mma_commit_pair(acc_full + 8 * buf);
             }
-            if (dead) {
+            if (dead && leader) {
                 mma_commit_pair(drain);
                 bar_drain(drain, 0);
             }
@@ -636,54 +656,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
         }
     } else if (warp >= 4) {
         // Widen X: a warp takes sixteen tokens, eight tokens by 64 features at a
-        // step, four lanes a token. Eight neighbouring lanes hold tokens t and
-        // t + 4, whose swizzled pieces lie in different banks; the second four
-        // store their two pieces in the other order for the same reason. The
-        // teams take the stages in turn: a stage's chain of waits, loads and
-        // fences is several times as long as its product.
-        const uint32_t team = (warp - 4) / 4, w = warp % 4, piece = lane % 4, hi = lane / 4 % 2, sub = lane / 8 + 4 * hi;
-        uint32_t it = 0;
+        // step, four lanes a token. Neighbouring tokens take the halves of the
+        // features in opposite order, so that the pieces of eight neighbouring
+        // lanes lie in different banks on both sides. The teams take the stages
+        // in turn: a stage's chain of waits, loads and fences is several times
+        // as long as its product.
+        const uint32_t team = (warp - 4) / 4, w = warp % 4, piece = lane % 4, odd = lane / 4 % 2, sub = lane / 8 * 2 + odd;
+        const uint32_t from = (w * 16 + sub) * 128 + ((odd * 4 + piece) ^ sub) * 16;
+        uint32_t to[2];  // token's row in the operand, and its first piece; the other is 16 bytes up or down
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t row = ALIGNED ? w * 16 + i * 8 + sub : sub * 8 + ((w * 2 + i) ^ odd);
+            to[i] = row * 128 + ((2 * piece) ^ (row % 8)) * 16;
+        }
         bool ok = true;
         // scale bytes are fetched one turn ahead
-        uint32_t ahead = team;
-        auto next_scales = [&]() -> uint32_t {
-            uint32_t b = 127, b8 = 127;
-            if (ahead < stages) {
-                const uint32_t i = ahead / tblocks, kb = (first + i * step) % a.tiles_k * 2 + rank;
-                const uint32_t t = (ahead - i * tblocks) * kBT + w * 16 + sub;
-                if (kb < a.nblk && t < a.T) b = __ldg(a.xs + (uint64_t)t * a.nblk + kb);
-                if (kb < a.nblk && t + 8 < a.T) b8 = __ldg(a.xs + (uint64_t)(t + 8) * a.nblk + kb);
-                b |= b8 << 8;
+        uint32_t ahead = first, ahead_tb = team, kb = first % a.tiles_k * 2 + rank;
+        auto next_scales = [&](uint32_t* b) {
+            while (ahead_tb >= tblocks && ahead < tiles) {
+                ahead_tb -= tblocks;
+                ahead += step;
+                kb = ahead % a.tiles_k * 2 + rank;
             }
-            ahead += kTeams;
-            return b;
+            b[0] = b[1] = 127;
+            if (ahead < tiles && kb < a.nblk) {
+                const uint32_t t = ahead_tb * kBT + w * 16 + sub;
+                const uint8_t* p = a.xs + (uint64_t)t * a.nblk + kb;
+                if (t < a.T) b[0] = __ldg(p);
+                if (t + 8 < a.T) b[1] = __ldg(p + 8 * a.nblk);
+            }
+            ahead_tb += kTeams;
         };
-        uint32_t b0 = next_scales();
-        for (it = team; ok && it < stages; it += kTeams) {
-            const uint32_t b = b0;
-            b0 = next_scales();
+        uint32_t b0[2], b1[2];
+        next_scales(b1);
+        for (uint32_t it = team; ok && it < stages; it += kTeams) {
+            b0[0] = b1[0];
+            b0[1] = b1[1];
+            next_scales(b1);
             const uint32_t rs = it % P::kRawStages, s = it % P::kStages;
-            if (!(ok = __all_sync(kFull, bar_wait(rfull + 8 * rs, (it / P::kRawStages) & 1, wt)))) break;
+            if (!(ok = bar_wait(rfull + 8 * rs, (it / P::kRawStages) & 1, wt))) break;
             uint4 c[4];
+            const uint32_t src = raw0 + rs * P::kRaw + from;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[i] = ld_shared((src ^ (i % 2 * 64)) + i / 2 * 1024);
+            if (!(ok = bar_wait(oempty + 8 * s, ((it / P::kStages) & 1) ^ 1, wt))) break;
+            const uint32_t dst = op0 + s * P::kOperands + odd * kGroupBytes;
+            const bool one = __all_sync(kFull, max(b0[0], b0[1]) <= 134);  // no scale above 2^7
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t from = w * 16 + i / 2 * 8 + sub;
-                c[i] = ld_shared(raw0 + rs * P::kRaw + from * 128 + ((i % 2 * 4 + piece) ^ sub) * 16);
-            }
-            if (!(ok = __all_sync(kFull, bar_wait(oempty + 8 * s, ((it / P::kStages) & 1) ^ 1, wt)))) break;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t from = w * 16 + i / 2 * 8 + sub;
-                const uint32_t to = ALIGNED ? from : sub * 8 + w * 2 + i / 2;  // token's row in the operand
-                const uint32_t at = op0 + s * P::kOperands + i % 2 * kGroupBytes + to * 128;
                 uint4 lo, up;
-                widen16(c[i], factors_of(i / 2 ? b >> 8 : b & 255), lo, up);
-                const uint32_t at_lo = at + ((2 * piece) ^ (to % 8)) * 16, at_up = at + ((2 * piece + 1) ^ (to % 8)) * 16;
-                st_shared(hi ? at_up : at_lo, hi ? up : lo);
-                st_shared(hi ? at_lo : at_up, hi ? lo : up);
+                if (one) widen16<true>(c[i], factors_of(b0[i / 2]), lo, up);
+                else widen16<false>(c[i], factors_of(b0[i / 2]), lo, up);
+                const uint32_t at = dst + to[i / 2] + (i % 2 ? (odd ? -kGroupBytes : kGroupBytes) : 0);
+                st_shared(at, lo);
+                st_shared(at ^ 16, up);
             }
             fence_async();
-            if (ALIGNED && !(ok = __all_sync(kFull, bar_wait(copied + 8 * s, (it / P::kStages) & 1, wt)))) break;
+            if (ALIGNED && !(ok = bar_wait(copied + 8 * s, (it / P::kStages) & 1, wt))) break;
             __syncwarp();
             if (lane == 0) {
                 bar_arrive(rempty + 8 * rs);
@@ -694,7 +723,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
         uint32_t n = 0;
         for (uint32_t tile = first; tile < tiles; tile += step, ++n) {
             const uint32_t buf = n % P::kAcc;
-            if (!__all_sync(kFull, bar_wait(acc_full + 8 * buf, (n / P::kAcc) & 1, wt))) break;
+            if (!bar_wait(acc_full + 8 * buf, (n / P::kAcc) & 1, wt)) break;
             fence_after();
             const uint32_t k = (tile % a.tiles_k * 2 + rank) * kBF + warp * 32 + lane, n0 = tile / a.tiles_k * kPairN;
 #pragma unroll 1
