@@ -39,6 +39,7 @@ struct Args {
     uint32_t T, N, K, nblk;
     uint32_t tiles_k, tiles_n;
     uint32_t split;
+    uint32_t nt;  // outputs per tile of the wide form, a multiple of 32
     int dtype, accumulate;
     uint32_t* faults;
 };
@@ -54,63 +55,34 @@ struct Shape {
     static_assert((size_t)NT * kBF * 4 <= (size_t)kStages * kStage, "a partial tile fits where the stages were");
 };
 
-// A scale byte as two bfloat16 factors (each twice in a word) that together
-// are 2^(120 + e): see widen16.
-struct Factors {
-    uint32_t first, second;
-};
-__device__ __forceinline__ Factors factors_of(uint32_t b) {
-    const int up = (int)b - 7;  // 120 + e; the byte 0 to 7 gives less than 2^0
-    const int one = min(up, 127), two = up - one;
-    // 2^one and 2^two from their exponent fields; the byte 255 stands for NaN
-    const uint32_t f = (uint32_t)(127 + one) << 7, g = b == 255 ? 0x7fffu : (uint32_t)(127 + two) << 7;
-    return {f | f << 16, g | g << 16};
+// The scale 2^(b - 127) as a bfloat16, twice in a word (the byte 0 is a
+// subnormal number, 255 stands for NaN).
+__device__ __forceinline__ uint32_t factor_of(uint32_t b) {
+    const uint32_t f = b == 0 ? 0x0040u : b == 255 ? 0x7fffu : b << 7;
+    return f | f << 16;
 }
 
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-// Two e4m3 codes, each in the upper byte of its half, to bfloat16. The code's
-// bits at bfloat16's places are the number times 2^-120 (the exponents' biases
-// are 7 and 127; subnormal codes become subnormal numbers), and the factors
-// bring it to its value: exact, as 2^e >= 2^-117 keeps it normal. ONE: the
-// second factor is 1. (Conversion instructions run at a quarter of this
-// arithmetic's rate or less: the wide form takes 0.55 of the time it took with them.)
-template <bool ONE>
-__device__ __forceinline__ uint32_t widen2(uint32_t x, Factors f) {
-    const uint32_t y = ((x & 0x7f007f00u) >> 4) | (x & 0x80008000u);
-    const uint32_t v = mul_bf16x2(y, f.first);
-    return ONE ? v : mul_bf16x2(v, f.second);
-}
-
-__device__ __noinline__ uint32_t nan_fixed(uint32_t codes, uint32_t wide) {  // two codes, in the upper bytes
-    if ((codes & 0x7f00u) == 0x7f00u) wide |= 0x7fffu;
-    if ((codes & 0x7f000000u) == 0x7f000000u) wide |= 0x7fff0000u;
-    return wide;
-}
-
-// Sixteen codes to bfloat16, in order.
-template <bool ONE>
-__device__ __forceinline__ void widen16(const uint4& c, Factors f, uint4& lo, uint4& hi) {
+// Sixteen codes times their scale to bfloat16, in order. Every step is exact
+// (a code has four significant bits; scales from 2^-117 on keep it normal), and
+// NaN stays NaN. Arithmetic on the bits with a check for NaN instead of the
+// conversions measured 211 us for 198 us (8192 tokens, 4096 x 4096).
+__device__ __forceinline__ void widen16(const uint4& c, uint32_t factor, uint4& lo, uint4& hi) {
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-    uint32_t x[8], o[8];
+    uint32_t o[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __byte_perm(w[i], 0, 0x1404);
-        x[2 * i + 1] = __byte_perm(w[i], 0, 0x3424);
-    }
+        uint32_t h[2];
+        asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b;}"
+            : "=r"(h[0]), "=r"(h[1])
+            : "r"(w[i]));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = widen2<ONE>(x[i], f);
-    // a byte 0x7f or 0xff carries into its top bit
-    uint32_t nan = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) nan |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;
-    if (nan & 0x80808080u) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = nan_fixed(x[i], o[i]);
+        for (int j = 0; j < 2; ++j) {
+            float l, u;
+            uint32_t p;
+            asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b;}" : "=f"(l), "=f"(u) : "r"(h[j]));
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p) : "f"(u), "f"(l));
+            asm("mul.bf16x2 %0, %1, %2;" : "=r"(o[2 * i + j]) : "r"(p), "r"(factor));
+        }
     }
     lo = make_uint4(o[0], o[1], o[2], o[3]);
     hi = make_uint4(o[4], o[5], o[6], o[7]);
@@ -360,7 +332,7 @@ __global__ void __launch_bounds__(Shape<NT, TMA>::kWarps * 32, 1)
                     const uint32_t row = (w * 2 + i / 2) * 8 + tsub;  // row % 8 == tsub
                     const uint32_t at = base + s * S::kStage + (i % 2) * kGroupBytes + row * 128;
                     uint4 lo, up;
-                    widen16<false>(c[i], factors_of(sc[i]), lo, up);
+                    widen16(c[i], factor_of(sc[i]), lo, up);
                     st_shared(at + ((2 * piece) ^ tsub) * 16, lo);
                     st_shared(at + ((2 * piece + 1) ^ tsub) * 16, up);
                 }
@@ -454,10 +426,8 @@ cudaError_t launch(const Wgrad8Args& m, Args a, int sms, cudaStream_t s) {
 // 128 features and fetches 128 of the outputs, and the pair's product reads
 // both blocks' shared memory, so dY's part of a stage is half of what one
 // block would need for tiles of the same size.
-constexpr int kPairN = 256;            // outputs per tile
+constexpr int kPairN = 256;            // outputs per tile, at most (Args::nt)
 constexpr int kHalfN = kPairN / 2;     // of which a block fetches half
-constexpr int kTeams = 4;              // teams of four warps that widen X, a stage each in turn
-constexpr int kWideners = 4 * kTeams;
 constexpr uint32_t kXRaw = kBT * kBF;  // 8-bit part of a stage
 constexpr uint32_t kBBytes = kHalfN / 64 * kGroupBytes;
 constexpr uint32_t kRowRaw = (kHalfN + 8) * 2;     // a misaligned row's piece: 8 elements more
@@ -475,6 +445,8 @@ struct Pair {
     static constexpr int kStages = ALIGNED ? 5 : 3;
     static constexpr int kAcc = 2;
     static constexpr uint32_t kCols = kAcc * kPairN;
+    static constexpr int kTeams = ALIGNED ? 4 : 3;  // teams of four warps that widen X, a stage each in turn
+    static constexpr int kWideners = 4 * kTeams;
     static constexpr int kWarps = 4 + kWideners + 2 + (ALIGNED ? 0 : kLoaders);
     static constexpr size_t kSmem = (size_t)kStages * kOperands + (size_t)kRawStages * kRaw + 1024;
     static_assert(kRaw % 1024 == 0, "a stage of raw rows starts on the swizzle's period");
@@ -503,19 +475,21 @@ __device__ __forceinline__ void realign(uint32_t stages, uint32_t raw0, uint32_t
         uint4 v[5];
 #pragma unroll
         for (int i = 0; i < (SHIFT ? 5 : 4); ++i) v[i] = ld_shared(src + 16 * i);
+        __syncwarp();
+        if (lane == 0) bar_arrive(rempty + 8 * rs);
+        uint4 o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = SHIFT ? shifted<SHIFT>(v[i], v[i + 1]) : v[i];
         if (!bar_wait(oempty + 8 * s, ((it / P::kStages) & 1) ^ 1, wt)) return;
         const uint32_t row = q ^ (r % 2), dst = op0 + s * P::kOperands + kABytes + (r * 8 + row) * 128;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t c = c0 + i;
-            st_shared(dst + c / 8 * kGroupBytes + ((c % 8) ^ row) * 16, SHIFT ? shifted<SHIFT>(v[i], v[i + 1]) : v[i]);
+            st_shared(dst + c / 8 * kGroupBytes + ((c % 8) ^ row) * 16, o[i]);
         }
         fence_async();
         __syncwarp();
-        if (lane == 0) {
-            bar_arrive(rempty + 8 * rs);
-            bar_arrive_first(ofull + 8 * s);
-        }
+        if (lane == 0) bar_arrive_first(ofull + 8 * s);
     }
 }
 
@@ -554,7 +528,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
         dead = 0;
         bar_fence_init();
     }
-    constexpr int kCopier = 4 + kWideners, kIssuer = kCopier + 1;
+    constexpr int kCopier = 4 + P::kWideners, kIssuer = kCopier + 1;
     if (warp == kIssuer) tmem_alloc_pair(smem_u32(&tmem_slot), P::kCols);
     fence_before();
     cluster_sync();
@@ -572,7 +546,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
             bool ok = true;
             for (uint32_t tile = first; ok && tile < tiles; tile += step) {
                 const int k0 = (int)((tile % a.tiles_k * 2 + rank) * kBF);
-                const int n0 = (int)(tile / a.tiles_k * kPairN + rank * kHalfN);
+                const int n0 = (int)(tile / a.tiles_k * a.nt + rank * (a.nt / 2));
                 for (uint32_t tb = 0; tb < tblocks; ++tb, ++it) {
                     const uint32_t rs = it % P::kRawStages, s = it % P::kStages;
                     if (!(ok = bar_wait(rempty + 8 * rs, ((it / P::kRawStages) & 1) ^ 1, wt))) break;
@@ -613,9 +587,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
     } else if (warp == kIssuer) {
         if (rank == 0) {
             const bool leader = elect();  // the thread that issues the products also commits them
-            // D float32, A and B bfloat16, both with rows along M (256) and N (256)
-            constexpr uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | 1u << 15 | 1u << 16 | (kPairN / 8) << 17 |
-                                       (2 * kBF / 16) << 24;
+            // D float32, A and B bfloat16, both with rows along M (256) and N
+            const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | 1u << 15 | 1u << 16 | (a.nt / 8) << 17 |
+                                   (2 * kBF / 16) << 24;
             uint32_t it = 0, n = 0;
             bool ok = true;
             for (uint32_t tile = first; ok && tile < tiles; tile += step, ++n) {
@@ -685,11 +659,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
                 if (t < a.T) b[0] = __ldg(p);
                 if (t + 8 < a.T) b[1] = __ldg(p + 8 * a.nblk);
             }
-            ahead_tb += kTeams;
+            ahead_tb += P::kTeams;
         };
         uint32_t b0[2], b1[2];
         next_scales(b1);
-        for (uint32_t it = team; ok && it < stages; it += kTeams) {
+        for (uint32_t it = team; ok && it < stages; it += P::kTeams) {
             b0[0] = b1[0];
             b0[1] = b1[1];
             next_scales(b1);
@@ -699,25 +673,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
             const uint32_t src = raw0 + rs * P::kRaw + from;
 #pragma unroll
             for (int i = 0; i < 4; ++i) c[i] = ld_shared((src ^ (i % 2 * 64)) + i / 2 * 1024);
+            __syncwarp();
+            if (lane == 0) bar_arrive(rempty + 8 * rs);  // the raw rows are in registers
+            // all the arithmetic before the wait: only the stores lie between a
+            // stage's release and its next product
+            uint4 lo[4], up[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) widen16(c[i], factor_of(b0[i / 2]), lo[i], up[i]);
             if (!(ok = bar_wait(oempty + 8 * s, ((it / P::kStages) & 1) ^ 1, wt))) break;
             const uint32_t dst = op0 + s * P::kOperands + odd * kGroupBytes;
-            const bool one = __all_sync(kFull, max(b0[0], b0[1]) <= 134);  // no scale above 2^7
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint4 lo, up;
-                if (one) widen16<true>(c[i], factors_of(b0[i / 2]), lo, up);
-                else widen16<false>(c[i], factors_of(b0[i / 2]), lo, up);
                 const uint32_t at = dst + to[i / 2] + (i % 2 ? (odd ? -kGroupBytes : kGroupBytes) : 0);
-                st_shared(at, lo);
-                st_shared(at ^ 16, up);
+                st_shared(at, lo[i]);
+                st_shared(at ^ 16, up[i]);
             }
             fence_async();
             if (ALIGNED && !(ok = bar_wait(copied + 8 * s, (it / P::kStages) & 1, wt))) break;
             __syncwarp();
-            if (lane == 0) {
-                bar_arrive(rempty + 8 * rs);
-                bar_arrive_first(ofull + 8 * s);
-            }
+            if (lane == 0) bar_arrive_first(ofull + 8 * s);
         }
     } else {
         uint32_t n = 0;
@@ -725,9 +699,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
             const uint32_t buf = n % P::kAcc;
             if (!bar_wait(acc_full + 8 * buf, (n / P::kAcc) & 1, wt)) break;
             fence_after();
-            const uint32_t k = (tile % a.tiles_k * 2 + rank) * kBF + warp * 32 + lane, n0 = tile / a.tiles_k * kPairN;
+            const uint32_t k = (tile % a.tiles_k * 2 + rank) * kBF + warp * 32 + lane, n0 = tile / a.tiles_k * a.nt;
 #pragma unroll 1
-            for (int c = 0; c < kPairN; c += 16) {
+            for (uint32_t c = 0; c < a.nt; c += 16) {
                 uint32_t r[16];
                 tmem_ld16(tmem + ((uint32_t)warp << 21) + buf * kPairN + c, r);
                 wait_ld();
@@ -770,13 +744,25 @@ cudaError_t launch_pair(const Wgrad8Args& m, Args a, cudaStream_t s) {
         }
     }
     a.tiles_k = (m.K + 2 * kBF - 1) / (2 * kBF);
-    a.tiles_n = (m.N + kPairN - 1) / kPairN;
-    const uint64_t tiles = (uint64_t)a.tiles_k * a.tiles_n;
-    if (tiles * ((m.T + kBT - 1) / kBT) > 0xffffffffull) return cudaErrorInvalidValue;
     auto kernel = wgrad8_pair_kernel<ALIGNED>;
     int pairs = 0;
     e = max_pairs(reinterpret_cast<const void*>(kernel), P::kWarps * 32, P::kSmem, &pairs);
     if (e != cudaSuccess) return e;
+    // The width that leaves the least of the last round of tiles idle: time
+    // goes as rounds * (width + 40), the widening of X not getting shorter with
+    // the width (256 x 256 tiles of 4096 x 4096 fill 3.4 of 4 rounds, tiles of
+    // 224 all 4: 213 us became 207 us; 160 took longer wherever it was chosen).
+    uint64_t best = ~0ull;
+    for (uint32_t nt = kPairN; nt >= 224; nt -= 32) {
+        const uint64_t rounds = ((uint64_t)a.tiles_k * ((m.N + nt - 1) / nt) + pairs - 1) / pairs;
+        if (rounds * (nt + 40) < best) {
+            best = rounds * (nt + 40);
+            a.nt = nt;
+        }
+    }
+    a.tiles_n = (m.N + a.nt - 1) / a.nt;
+    const uint64_t tiles = (uint64_t)a.tiles_k * a.tiles_n;
+    if (tiles * ((m.T + kBT - 1) / kBT) > 0xffffffffull) return cudaErrorInvalidValue;
     const uint32_t grid = 2 * (uint32_t)(tiles < (uint64_t)pairs ? tiles : pairs);
     kernel<<<grid, P::kWarps * 32, P::kSmem, s>>>(xmap, ymaps, a);
     return cudaGetLastError();
