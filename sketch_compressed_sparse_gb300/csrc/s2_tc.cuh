@@ -62,25 +62,25 @@ struct Wait {
 };
 
 static __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, const Wait w) {
-    const uint64_t t0 = now_ns();
+    uint64_t t0 = 0;
     for (;;) {
+#pragma unroll 1
         for (int i = 0; i < 256; ++i)
-            if (bar_try(bar, parity)) return true;
-        if (*w.dead) return false;
-        if (now_ns() - t0 > kWaitNs) {
+            if (__all_sync(0xffffffffu, bar_try(bar, parity))) return true;
+        if (t0 == 0) t0 = now_ns();
+        const bool late = now_ns() - t0 > kWaitNs;
+        if (late && threadIdx.x % 32 == 0) {
             *w.dead = 1;
             atomicAdd(w.faults, 1u);
-            return false;
         }
+        if (__any_sync(0xffffffffu, late || *w.dead)) return false;
     }
 }
-// Whole warp, converged; the answer is the same in every lane.
+// Whole warp, converged; the answer is the same in every lane. (Kept small
+// where it is inlined: the warps of a block run many different loops, and their
+// instructions have to stay in the cache.)
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const Wait& w) {
-    if (__all_sync(0xffffffffu, bar_try(bar, parity))) return true;
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-        if (__all_sync(0xffffffffu, bar_try(bar, parity))) return true;
-    return __all_sync(0xffffffffu, bar_wait_slow(bar, parity, w));
+    return __all_sync(0xffffffffu, bar_try(bar, parity)) || bar_wait_slow(bar, parity, w);
 }
 // For the copies in flight of a block that gave up: no `dead` word ends it.
 static __device__ __noinline__ void bar_drain(uint32_t bar, uint32_t parity) {

@@ -94,6 +94,7 @@ __device__ __forceinline__ void st_shared(uint32_t addr, uint4 v) {
 // Makes this thread's shared-memory stores visible to the tensor cores.
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// Sixteen neighbouring outputs of feature k, from n on.
 __device__ __forceinline__ void store(const Args& a, uint32_t n, uint32_t k, float v) {
     const uint64_t at = (uint64_t)n * a.lddw + k;
     if (a.dtype == 0) {
@@ -103,6 +104,21 @@ __device__ __forceinline__ void store(const Args& a, uint32_t n, uint32_t k, flo
         uint16_t* p = static_cast<uint16_t*>(a.dw) + at;
         if (a.accumulate) v += __uint_as_float((uint32_t)*p << 16);
         asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(*p) : "f"(v));  // the one rounding to 16 bits: dW's own type
+    }
+}
+__device__ __forceinline__ void store16(const Args& a, uint32_t n, uint32_t k, const uint32_t* r) {
+    if (a.accumulate || n + 16 > a.N) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (n + j < a.N) store(a, n + j, k, __uint_as_float(r[j]));
+    } else if (a.dtype == 0) {
+        float* p = static_cast<float*>(a.dw) + (uint64_t)n * a.lddw + k;
+#pragma unroll
+        for (int j = 0; j < 16; ++j, p += a.lddw) *p = __uint_as_float(r[j]);
+    } else {
+        uint16_t* p = static_cast<uint16_t*>(a.dw) + (uint64_t)n * a.lddw + k;
+#pragma unroll
+        for (int j = 0; j < 16; ++j, p += a.lddw) asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(*p) : "f"(__uint_as_float(r[j])));
     }
 }
 
@@ -120,14 +136,17 @@ __device__ __forceinline__ uint4 load_piece(const uint8_t* q, const uint8_t* lo,
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int SHIFT>
-__device__ __forceinline__ uint4 shifted(uint4 a, uint4 b) {
+// Sixteen bytes from byte `shift` (even, below 16) of a and b on: whole words
+// by the (warp-uniform) branch, half a word by the funnel.
+template <int WORDS>
+__device__ __forceinline__ uint4 from_word(const uint4& a, const uint4& b, uint32_t bits) {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    constexpr int k = SHIFT / 4, r = SHIFT % 4 * 8;
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = r ? __funnelshift_r(w[i + k], w[(i + k + 1) % 8], r) : w[i + k];
-    return make_uint4(o[0], o[1], o[2], o[3]);
+    uint4 o;
+    o.x = __funnelshift_r(w[WORDS], w[WORDS + 1], bits);
+    o.y = __funnelshift_r(w[WORDS + 1], w[WORDS + 2], bits);
+    o.z = __funnelshift_r(w[WORDS + 2], w[WORDS + 3], bits);
+    o.w = __funnelshift_r(w[WORDS + 3], w[(WORDS + 4) % 8], bits);
+    return o;
 }
 
 struct Ring {
@@ -135,9 +154,10 @@ struct Ring {
     uint32_t tb0, tb1;  // this block's token blocks
 };
 
-// One loader warp's rows of every tile: t = w mod 8, SHIFT bytes past a boundary.
-template <int NT, int SHIFT>
-__device__ __forceinline__ void load_rows(const Args& a, const Ring& g, const Wait& wt, uint32_t w, uint32_t lane) {
+// One loader warp's rows of every tile: t = w mod 8, `shift` bytes past a boundary.
+template <int NT>
+__device__ __forceinline__ void load_rows(const Args& a, const Ring& g, const Wait& wt, uint32_t w, uint32_t lane,
+                                          uint32_t shift) {
     using S = Shape<NT, false>;
     constexpr int kChunks = NT / 8;               // 16-byte pieces of a row
     constexpr int kRows = 32 / kChunks;           // rows of one load
@@ -155,9 +175,16 @@ __device__ __forceinline__ void load_rows(const Args& a, const Ring& g, const Wa
                 const uint32_t t = tb * kBT + w + 8 * (j * kRows + sub);
                 v[j] = make_uint4(0, 0, 0, 0);
                 if (t < a.T && n < a.N) {
-                    const uint8_t* q = lo + ((uint64_t)t * a.lddy + n) * 2 - SHIFT;
+                    const uint8_t* q = lo + ((uint64_t)t * a.lddy + n) * 2 - shift;
                     const uint4 b0 = load_piece(q, lo, hi);
-                    v[j] = SHIFT ? shifted<SHIFT>(b0, load_piece(q + 16, lo, hi)) : b0;
+                    const uint4 b1 = shift ? load_piece(q + 16, lo, hi) : b0;
+                    const uint32_t bits = shift % 4 * 8;
+                    switch (shift / 4) {
+                        case 0: v[j] = from_word<0>(b0, b1, bits); break;
+                        case 1: v[j] = from_word<1>(b0, b1, bits); break;
+                        case 2: v[j] = from_word<2>(b0, b1, bits); break;
+                        default: v[j] = from_word<3>(b0, b1, bits); break;
+                    }
                 }
             }
             const int s = it % S::kStages;
@@ -285,16 +312,7 @@ __global__ void __launch_bounds__(Shape<NT, TMA>::kWarps * 32, 1)
     } else if (warp >= 10) {
         // the same shift for every row t = w mod 8 and every tile: 8 rows and 8 outputs are multiples of 16 bytes
         const uint32_t w = warp - 10;
-        switch ((reinterpret_cast<uintptr_t>(a.dy) + (uint64_t)w * a.lddy * 2) % 16 / 2) {
-            case 0: load_rows<NT, 0>(a, g, wt, w, lane); break;
-            case 1: load_rows<NT, 2>(a, g, wt, w, lane); break;
-            case 2: load_rows<NT, 4>(a, g, wt, w, lane); break;
-            case 3: load_rows<NT, 6>(a, g, wt, w, lane); break;
-            case 4: load_rows<NT, 8>(a, g, wt, w, lane); break;
-            case 5: load_rows<NT, 10>(a, g, wt, w, lane); break;
-            case 6: load_rows<NT, 12>(a, g, wt, w, lane); break;
-            default: load_rows<NT, 14>(a, g, wt, w, lane); break;
-        }
+        load_rows<NT>(a, g, wt, w, lane, (uint32_t)((reinterpret_cast<uintptr_t>(a.dy) + (uint64_t)w * a.lddy * 2) % 16));
     } else if (warp >= 4) {
         // widen X: a warp takes eight tokens by 64 features at a time, four lanes a token
         constexpr int kPieces = 4;
@@ -358,9 +376,7 @@ __global__ void __launch_bounds__(Shape<NT, TMA>::kWarps * 32, 1)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) part[(c + j) * kBF + warp * 32 + lane] = __uint_as_float(r[j]);
                 } else if (k < a.K) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (n0 + c + j < a.N) store(a, n0 + c + j, k, __uint_as_float(r[j]));
+                    store16(a, n0 + c, k, r);
                 }
             }
             fence_before();
@@ -437,20 +453,38 @@ struct YMaps {
     CUtensorMap m[8];  // aligned rows: m[0]; else the rows t = r mod 8 for each r
 };
 
+// Four rings in shared memory: 8-bit rows of X, widened X (A), dY in place (B)
+// and, for misaligned rows, dY as it lies. B and the raw rows are the deeper
+// ones: they wait for HBM, A only for the arithmetic.
 template <bool ALIGNED>
 struct Pair {
-    static constexpr uint32_t kRaw = kXRaw + (ALIGNED ? 0 : kYRaw);
-    static constexpr uint32_t kOperands = kABytes + kBBytes;
-    static constexpr int kRawStages = ALIGNED ? 6 : 4;
-    static constexpr int kStages = ALIGNED ? 5 : 3;
+    // Teams of four warps widen X, a stage each in turn. A has a slot per team
+    // and the raw rows of X kXs, so that a team meets every use of its own
+    // slots and can tell their phases by one bit.
+    static constexpr int kTeams = ALIGNED ? 4 : 3, kXs = ALIGNED ? 1 : 2;
+    static constexpr int kA = kTeams, kX = kXs * kTeams, kB = ALIGNED ? 7 : 3, kY = ALIGNED ? 0 : 4;
+    static constexpr uint32_t kBAt = kA * kABytes, kXAt = kBAt + kB * kBBytes, kYAt = kXAt + kX * kXRaw;
+    static constexpr size_t kSmem = kYAt + kY * kYRaw + 1024;
     static constexpr int kAcc = 2;
     static constexpr uint32_t kCols = kAcc * kPairN;
-    static constexpr int kTeams = ALIGNED ? 4 : 3;  // teams of four warps that widen X, a stage each in turn
     static constexpr int kWideners = 4 * kTeams;
     static constexpr int kWarps = 4 + kWideners + 2 + (ALIGNED ? 0 : kLoaders);
-    static constexpr size_t kSmem = (size_t)kStages * kOperands + (size_t)kRawStages * kRaw + 1024;
-    static_assert(kRaw % 1024 == 0, "a stage of raw rows starts on the swizzle's period");
+    static constexpr int kBars = 2 * kX + 2 * kA + 3 * kB + 2 * kY + 2 * kAcc + 1;
+    static_assert(kYRaw % 1024 == 0, "rings start on the swizzle's period");
+    static_assert(kB >= kA, "a stage's B outlives its A");
     static_assert(kSmem <= 226 * 1024, "shared memory");
+};
+
+// Position in a ring and the parity of the phase that its next use completes.
+template <int N>
+struct Slot {
+    uint32_t at = 0, phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++at == N) {
+            at = 0;
+            phase ^= 1;
+        }
+    }
 };
 
 __device__ __forceinline__ uint4 ld_shared(uint32_t addr) {
@@ -463,25 +497,42 @@ __device__ __forceinline__ uint4 ld_shared(uint32_t addr) {
 // row 8r + (q ^ r % 2) of the operand (the tokens of a stage may lie in any
 // order as long as both operands agree), which keeps this warp's and the
 // wideners' stores free of bank conflicts.
-template <int SHIFT>
-__device__ __forceinline__ void realign(uint32_t stages, uint32_t raw0, uint32_t op0, uint32_t rfull, uint32_t rempty,
-                                        uint32_t ofull, uint32_t oempty, const Wait& wt, uint32_t r, uint32_t lane) {
+__device__ __forceinline__ void realign(uint32_t stages, uint32_t y0, uint32_t b0, uint32_t yfull, uint32_t yempty,
+                                        uint32_t bfull, uint32_t bempty, const Wait& wt, uint32_t r, uint32_t lane,
+                                        uint32_t shift) {
     using P = Pair<false>;
-    const uint32_t q = lane % 8, c0 = lane / 8 * 4;
+    const uint32_t q = lane % 8, c0 = lane / 8 * 4, row = q ^ (r % 2), bits = shift % 4 * 8;
+    Slot<P::kY> ys;
+    Slot<P::kB> bs;
     for (uint32_t it = 0; it < stages; ++it) {
-        const uint32_t rs = it % P::kRawStages, s = it % P::kStages;
-        if (!bar_wait(rfull + 8 * rs, (it / P::kRawStages) & 1, wt)) return;
-        const uint32_t src = raw0 + rs * P::kRaw + kXRaw + (r * 8 + q) * kRowRaw + c0 * 16;
+        if (!bar_wait(yfull + 8 * ys.at, ys.phase, wt)) return;
+        const uint32_t src = y0 + ys.at * kYRaw + (r * 8 + q) * kRowRaw + c0 * 16;
         uint4 v[5];
 #pragma unroll
-        for (int i = 0; i < (SHIFT ? 5 : 4); ++i) v[i] = ld_shared(src + 16 * i);
+        for (int i = 0; i < 5; ++i) v[i] = ld_shared(src + 16 * i);
         __syncwarp();
-        if (lane == 0) bar_arrive(rempty + 8 * rs);
+        if (lane == 0) bar_arrive(yempty + 8 * ys.at);
+        ys.next();
         uint4 o[4];
+        switch (shift / 4) {
+            case 0:
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = SHIFT ? shifted<SHIFT>(v[i], v[i + 1]) : v[i];
-        if (!bar_wait(oempty + 8 * s, ((it / P::kStages) & 1) ^ 1, wt)) return;
-        const uint32_t row = q ^ (r % 2), dst = op0 + s * P::kOperands + kABytes + (r * 8 + row) * 128;
+                for (int i = 0; i < 4; ++i) o[i] = from_word<0>(v[i], v[i + 1], bits);
+                break;
+            case 1:
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[i] = from_word<1>(v[i], v[i + 1], bits);
+                break;
+            case 2:
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[i] = from_word<2>(v[i], v[i + 1], bits);
+                break;
+            default:
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[i] = from_word<3>(v[i], v[i + 1], bits);
+        }
+        if (!bar_wait(bempty + 8 * bs.at, bs.phase ^ 1, wt)) return;
+        const uint32_t dst = b0 + bs.at * kBBytes + (r * 8 + row) * 128;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t c = c0 + i;
@@ -489,7 +540,8 @@ __device__ __forceinline__ void realign(uint32_t stages, uint32_t raw0, uint32_t
         }
         fence_async();
         __syncwarp();
-        if (lane == 0) bar_arrive_first(ofull + 8 * s);
+        if (lane == 0) bar_arrive_first(bfull + 8 * bs.at);
+        bs.next();
     }
 }
 
@@ -498,27 +550,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
     wgrad8_pair_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ YMaps ymaps, const Args a) {
     using P = Pair<ALIGNED>;
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t bars[2 * P::kRawStages + 3 * P::kStages + 2 * P::kAcc + 1];
+    __shared__ __align__(8) uint64_t bars[P::kBars];
     __shared__ uint32_t tmem_slot;
     __shared__ uint32_t dead;
 
-    const uint32_t op0 = (smem_u32(raw) + 1023u) & ~1023u, raw0 = op0 + P::kStages * P::kOperands;
+    const uint32_t a0 = (smem_u32(raw) + 1023u) & ~1023u, b0 = a0 + P::kBAt, x0 = a0 + P::kXAt, y0 = a0 + P::kYAt;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = cluster_rank();
-    const uint32_t rfull = smem_u32(bars), rempty = rfull + 8 * P::kRawStages;
-    const uint32_t ofull = rempty + 8 * P::kRawStages, oempty = ofull + 8 * P::kStages, copied = oempty + 8 * P::kStages;
-    const uint32_t acc_full = copied + 8 * P::kStages, acc_empty = acc_full + 8 * P::kAcc, drain = acc_empty + 8 * P::kAcc;
-    constexpr int kFillers = 4 + (ALIGNED ? 0 : kLoaders);  // warps that fill a stage
+    const uint32_t xfull = smem_u32(bars), xempty = xfull + 8 * P::kX;
+    const uint32_t afull = xempty + 8 * P::kX, aempty = afull + 8 * P::kA;       // the first block's afull counts
+    const uint32_t bfull = aempty + 8 * P::kA, bempty = bfull + 8 * P::kB;       // both; the same for bfull
+    const uint32_t copied = bempty + 8 * P::kB;                                  // this block's B, by tiled copy
+    const uint32_t yfull = copied + 8 * P::kB, yempty = yfull + 8 * P::kY;
+    const uint32_t acc_full = yempty + 8 * P::kY, acc_empty = acc_full + 8 * P::kAcc, drain = acc_empty + 8 * P::kAcc;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < P::kRawStages; ++s) {
-            bar_init(rfull + 8 * s, 1);
-            bar_init(rempty + 8 * s, kFillers);
+        for (int s = 0; s < P::kX; ++s) {
+            bar_init(xfull + 8 * s, 1);
+            bar_init(xempty + 8 * s, 4);
         }
-        for (int s = 0; s < P::kStages; ++s) {
-            bar_init(ofull + 8 * s, 2 * kFillers);
-            bar_init(oempty + 8 * s, 1);
+        for (int s = 0; s < P::kA; ++s) {
+            bar_init(afull + 8 * s, 2 * 4);
+            bar_init(aempty + 8 * s, 1);
+        }
+        for (int s = 0; s < P::kB; ++s) {
+            bar_init(bfull + 8 * s, 2 * kLoaders);
+            bar_init(bempty + 8 * s, 1);
             bar_init(copied + 8 * s, 1);
+        }
+        for (int s = 0; s < P::kY; ++s) {
+            bar_init(yfull + 8 * s, 1);
+            bar_init(yempty + 8 * s, kLoaders);
         }
         for (int s = 0; s < P::kAcc; ++s) {
             bar_init(acc_full + 8 * s, 1);
@@ -540,49 +602,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
     const uint32_t mine = first < tiles ? (tiles - first - 1) / step + 1 : 0, stages = mine * tblocks;
 
     if (warp == kCopier) {
-        {
-            const bool leader = elect();
-            uint32_t it = 0;
-            bool ok = true;
-            for (uint32_t tile = first; ok && tile < tiles; tile += step) {
-                const int k0 = (int)((tile % a.tiles_k * 2 + rank) * kBF);
-                const int n0 = (int)(tile / a.tiles_k * a.nt + rank * (a.nt / 2));
-                for (uint32_t tb = 0; tb < tblocks; ++tb, ++it) {
-                    const uint32_t rs = it % P::kRawStages, s = it % P::kStages;
-                    if (!(ok = bar_wait(rempty + 8 * rs, ((it / P::kRawStages) & 1) ^ 1, wt))) break;
-                    const uint32_t dst = raw0 + rs * P::kRaw;
-                    if (leader) {
-                        bar_expect(rfull + 8 * rs, P::kRaw);
-                        tma_2d(dst, &xmap, rfull + 8 * rs, k0, (int)(tb * kBT));
-                        if (!ALIGNED) {
-#pragma unroll
-                            for (int r = 0; r < 8; ++r)
-                                tma_2d(dst + kXRaw + r * 8 * kRowRaw, &ymaps.m[r], rfull + 8 * rs, n0, (int)(tb * kBT / 8));
-                        }
-                    }
+        const bool leader = elect();
+        Slot<P::kX> xs;
+        Slot<ALIGNED ? P::kB : P::kY> ys;
+        uint32_t nx = 0, ny = 0;  // copies issued
+        bool ok = true;
+        for (uint32_t tile = first; ok && tile < tiles; tile += step) {
+            const int k0 = (int)((tile % a.tiles_k * 2 + rank) * kBF);
+            const int n0 = (int)(tile / a.tiles_k * a.nt + rank * (a.nt / 2));
+            for (uint32_t tb = 0; tb < tblocks; ++tb) {
+                if (!(ok = bar_wait(xempty + 8 * xs.at, xs.phase ^ 1, wt))) break;
+                if (leader) {
+                    bar_expect(xfull + 8 * xs.at, kXRaw);
+                    tma_2d(x0 + xs.at * kXRaw, &xmap, xfull + 8 * xs.at, k0, (int)(tb * kBT));
+                }
+                xs.next();
+                ++nx;
+                if (!(ok = bar_wait((ALIGNED ? bempty : yempty) + 8 * ys.at, ys.phase ^ 1, wt))) break;
+                if (leader) {
                     if (ALIGNED) {
-                        if (!(ok = bar_wait(oempty + 8 * s, ((it / P::kStages) & 1) ^ 1, wt))) {
-                            ++it;  // the copy of X is on its way
-                            break;
-                        }
-                        if (leader) {
-                            bar_expect(copied + 8 * s, kBBytes);
+                        bar_expect(copied + 8 * ys.at, kBBytes);
 #pragma unroll
-                            for (int c = 0; c < kHalfN / 64; ++c)
-                                tma_2d(op0 + s * P::kOperands + kABytes + c * kGroupBytes, &ymaps.m[0], copied + 8 * s,
-                                       n0 + 64 * c, (int)(tb * kBT));
-                        }
+                        for (int c = 0; c < kHalfN / 64; ++c)
+                            tma_2d(b0 + ys.at * kBBytes + c * kGroupBytes, &ymaps.m[0], copied + 8 * ys.at, n0 + 64 * c,
+                                   (int)(tb * kBT));
+                    } else {
+                        bar_expect(yfull + 8 * ys.at, kYRaw);
+#pragma unroll
+                        for (int r = 0; r < 8; ++r)
+                            tma_2d(y0 + ys.at * kYRaw + r * 8 * kRowRaw, &ymaps.m[r], yfull + 8 * ys.at, n0,
+                                   (int)(tb * kBT / 8));
                     }
                 }
+                ys.next();
+                ++ny;
             }
-            // nothing of this block's may still be on its way when it ends
-            if (dead) {
-                for (uint32_t j = it > (uint32_t)P::kRawStages ? it - P::kRawStages : 0; j < it; ++j)
-                    bar_drain(rfull + 8 * (j % P::kRawStages), (j / P::kRawStages) & 1);
-                if (ALIGNED)
-                    for (uint32_t j = it > (uint32_t)P::kStages ? it - P::kStages : 0; j < it; ++j)
-                        bar_drain(copied + 8 * (j % P::kStages), (j / P::kStages) & 1);
-            }
+        }
+        // nothing of this block's may still be on its way when it ends
+        if (dead && leader) {
+            constexpr uint32_t kYs = ALIGNED ? P::kB : P::kY;
+            for (uint32_t j = nx > (uint32_t)P::kX ? nx - P::kX : 0; j < nx; ++j)
+                bar_drain(xfull + 8 * (j % P::kX), (j / P::kX) & 1);
+            for (uint32_t j = ny > kYs ? ny - kYs : 0; j < ny; ++j)
+                bar_drain((ALIGNED ? copied : yfull) + 8 * (j % kYs), (j / kYs) & 1);
         }
     } else if (warp == kIssuer) {
         if (rank == 0) {
@@ -590,26 +652,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
             // D float32, A and B bfloat16, both with rows along M (256) and N
             const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | 1u << 15 | 1u << 16 | (a.nt / 8) << 17 |
                                    (2 * kBF / 16) << 24;
-            uint32_t it = 0, n = 0;
+            Slot<P::kA> as;
+            Slot<P::kB> bs;
+            Slot<P::kAcc> acc;
             bool ok = true;
-            for (uint32_t tile = first; ok && tile < tiles; tile += step, ++n) {
-                const uint32_t buf = n % P::kAcc;
-                if (!(ok = bar_wait(acc_empty + 8 * buf, ((n / P::kAcc) & 1) ^ 1, wt))) break;
+            for (uint32_t tile = first; ok && tile < tiles; tile += step) {
+                if (!(ok = bar_wait(acc_empty + 8 * acc.at, acc.phase ^ 1, wt))) break;
                 fence_after();
-                for (uint32_t tb = 0; tb < tblocks; ++tb, ++it) {
-                    const uint32_t s = it % P::kStages;
-                    if (!(ok = bar_wait(ofull + 8 * s, (it / P::kStages) & 1, wt))) break;
+                for (uint32_t tb = 0; tb < tblocks; ++tb) {
+                    if (!ALIGNED && !(ok = bar_wait(bfull + 8 * bs.at, bs.phase, wt))) break;
+                    if (!(ok = bar_wait(afull + 8 * as.at, as.phase, wt))) break;
                     fence_after();
-                    const uint64_t ad = smem_desc(op0 + s * P::kOperands, kGroupBytes, 1024);
-                    const uint64_t bd = smem_desc(op0 + s * P::kOperands + kABytes, kGroupBytes, 1024);
+                    const uint64_t ad = smem_desc(a0 + as.at * kABytes, kGroupBytes, 1024);
+                    const uint64_t bd = smem_desc(b0 + bs.at * kBBytes, kGroupBytes, 1024);
                     if (leader) {
 #pragma unroll
                         for (int j = 0; j < kBT / 16; ++j)
-                            mma_bf16_pair(tmem + buf * kPairN, ad + 128 * j, bd + 128 * j, idesc, tb > 0 || j > 0);
-                        mma_commit_pair(oempty + 8 * s);
+                            mma_bf16_pair(tmem + acc.at * kPairN, ad + 128 * j, bd + 128 * j, idesc, tb > 0 || j > 0);
+                        mma_commit_pair(aempty + 8 * as.at);
+                        mma_commit_pair(bempty + 8 * bs.at);
                     }
+                    as.next();
+                    bs.next();
                 }
-                if (ok && leader) mma_commit_pair(acc_full + 8 * buf);
+                if (ok && leader) mma_commit_pair(acc_full + 8 * acc.at);
+                acc.next();
             }
             if (dead && leader) {
                 mma_commit_pair(drain);
@@ -618,16 +685,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
         }
     } else if (warp > kIssuer) {
         const uint32_t r = warp - kIssuer - 1;
-        switch ((reinterpret_cast<uintptr_t>(a.dy) + (uint64_t)r * a.lddy * 2) % 16 / 2) {
-            case 0: realign<0>(stages, raw0, op0, rfull, rempty, ofull, oempty, wt, r, lane); break;
-            case 1: realign<2>(stages, raw0, op0, rfull, rempty, ofull, oempty, wt, r, lane); break;
-            case 2: realign<4>(stages, raw0, op0, rfull, rempty, ofull, oempty, wt, r, lane); break;
-            case 3: realign<6>(stages, raw0, op0, rfull, rempty, ofull, oempty, wt, r, lane); break;
-            case 4: realign<8>(stages, raw0, op0, rfull, rempty, ofull, oempty, wt, r, lane); break;
-            case 5: realign<10>(stages, raw0, op0, rfull, rempty, ofull, oempty, wt, r, lane); break;
-            case 6: realign<12>(stages, raw0, op0, rfull, rempty, ofull, oempty, wt, r, lane); break;
-            default: realign<14>(stages, raw0, op0, rfull, rempty, ofull, oempty, wt, r, lane); break;
-        }
+        realign(stages, y0, b0, yfull, yempty, bfull, bempty, wt, r, lane,
+                (uint32_t)((reinterpret_cast<uintptr_t>(a.dy) + (uint64_t)r * a.lddy * 2) % 16));
     } else if (warp >= 4) {
         // Widen X: a warp takes sixteen tokens, eight tokens by 64 features at a
         // step, four lanes a token. Neighbouring tokens take the halves of the
@@ -636,12 +695,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
         // in turn: a stage's chain of waits, loads and fences is several times
         // as long as its product.
         const uint32_t team = (warp - 4) / 4, w = warp % 4, piece = lane % 4, odd = lane / 4 % 2, sub = lane / 8 * 2 + odd;
-        const uint32_t from = (w * 16 + sub) * 128 + ((odd * 4 + piece) ^ sub) * 16;
+        const uint32_t src0 = x0 + team * kXRaw + (w * 16 + sub) * 128 + ((odd * 4 + piece) ^ sub) * 16;
+        const uint32_t dst = a0 + team * kABytes + odd * kGroupBytes;
         uint32_t to[2];  // token's row in the operand, and its first piece; the other is 16 bytes up or down
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const uint32_t row = ALIGNED ? w * 16 + i * 8 + sub : sub * 8 + ((w * 2 + i) ^ odd);
-            to[i] = row * 128 + ((2 * piece) ^ (row % 8)) * 16;
+            to[i] = dst + row * 128 + ((2 * piece) ^ (row % 8)) * 16;
         }
         bool ok = true;
         // scale bytes are fetched one turn ahead
@@ -661,59 +721,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
             }
             ahead_tb += P::kTeams;
         };
-        uint32_t b0[2], b1[2];
-        next_scales(b1);
-        for (uint32_t it = team; ok && it < stages; it += P::kTeams) {
-            b0[0] = b1[0];
-            b0[1] = b1[1];
-            next_scales(b1);
-            const uint32_t rs = it % P::kRawStages, s = it % P::kStages;
-            if (!(ok = bar_wait(rfull + 8 * rs, (it / P::kRawStages) & 1, wt))) break;
+        uint32_t now[2], then[2], phase = 0;
+        next_scales(then);
+        Slot<P::kXs> xs;
+        Slot<P::kB> bs;
+        for (uint32_t i = 0; i < team; ++i) bs.next();
+        for (uint32_t it = team; ok && it < stages; it += P::kTeams, phase ^= 1) {
+            now[0] = then[0];
+            now[1] = then[1];
+            next_scales(then);
+            const uint32_t x = team + xs.at * P::kTeams, src = src0 + xs.at * P::kTeams * kXRaw;
+            if (!(ok = bar_wait(xfull + 8 * x, xs.phase, wt))) break;
             uint4 c[4];
-            const uint32_t src = raw0 + rs * P::kRaw + from;
 #pragma unroll
             for (int i = 0; i < 4; ++i) c[i] = ld_shared((src ^ (i % 2 * 64)) + i / 2 * 1024);
             __syncwarp();
-            if (lane == 0) bar_arrive(rempty + 8 * rs);  // the raw rows are in registers
+            if (lane == 0) bar_arrive(xempty + 8 * x);  // the raw rows are in registers
+            xs.next();
             // all the arithmetic before the wait: only the stores lie between a
-            // stage's release and its next product
+            // slot's release and its next product
             uint4 lo[4], up[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) widen16(c[i], factor_of(b0[i / 2]), lo[i], up[i]);
-            if (!(ok = bar_wait(oempty + 8 * s, ((it / P::kStages) & 1) ^ 1, wt))) break;
-            const uint32_t dst = op0 + s * P::kOperands + odd * kGroupBytes;
+            for (int i = 0; i < 4; ++i) widen16(c[i], factor_of(now[i / 2]), lo[i], up[i]);
+            if (!(ok = bar_wait(aempty + 8 * team, phase ^ 1, wt))) break;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t at = dst + to[i / 2] + (i % 2 ? (odd ? -kGroupBytes : kGroupBytes) : 0);
+                const uint32_t at = to[i / 2] + (i % 2 ? (odd ? -kGroupBytes : kGroupBytes) : 0);
                 st_shared(at, lo[i]);
                 st_shared(at ^ 16, up[i]);
             }
             fence_async();
-            if (ALIGNED && !(ok = bar_wait(copied + 8 * s, (it / P::kStages) & 1, wt))) break;
+            // this arrival also tells the first block that this block's B has come
+            if (ALIGNED && !(ok = bar_wait(copied + 8 * bs.at, bs.phase, wt))) break;
             __syncwarp();
-            if (lane == 0) bar_arrive_first(ofull + 8 * s);
+            if (lane == 0) bar_arrive_first(afull + 8 * team);
+#pragma unroll
+            for (int i = 0; i < P::kTeams; ++i) bs.next();
         }
     } else {
-        uint32_t n = 0;
-        for (uint32_t tile = first; tile < tiles; tile += step, ++n) {
-            const uint32_t buf = n % P::kAcc;
-            if (!bar_wait(acc_full + 8 * buf, (n / P::kAcc) & 1, wt)) break;
+        Slot<P::kAcc> acc;
+        for (uint32_t tile = first; tile < tiles; tile += step) {
+            if (!bar_wait(acc_full + 8 * acc.at, acc.phase, wt)) break;
             fence_after();
             const uint32_t k = (tile % a.tiles_k * 2 + rank) * kBF + warp * 32 + lane, n0 = tile / a.tiles_k * a.nt;
 #pragma unroll 1
             for (uint32_t c = 0; c < a.nt; c += 16) {
                 uint32_t r[16];
-                tmem_ld16(tmem + ((uint32_t)warp << 21) + buf * kPairN + c, r);
+                tmem_ld16(tmem + ((uint32_t)warp << 21) + acc.at * kPairN + c, r);
                 wait_ld();
-                if (k < a.K) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (n0 + c + j < a.N) store(a, n0 + c + j, k, __uint_as_float(r[j]));
-                }
+                if (k < a.K) store16(a, n0 + c, k, r);
             }
             fence_before();
             __syncwarp();
-            if (lane == 0) bar_arrive_first(acc_empty + 8 * buf);
+            if (lane == 0) bar_arrive_first(acc_empty + 8 * acc.at);
+            acc.next();
         }
     }
 
