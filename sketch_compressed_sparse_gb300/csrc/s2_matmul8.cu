@@ -31,6 +31,7 @@ struct Args {
     uint32_t M, N, nblk, w_shift;
     int dtype;
     uint32_t tiles_f, tiles_t;
+    uint32_t nt;            // tokens per tile of the pair form, a multiple of 32
     uint32_t tokens_inner;  // tiles of one feature range are neighbours in the order
     uint32_t split;         // blocks (one cluster) per tile, each with a part of K
     uint32_t* faults;
@@ -51,23 +52,47 @@ struct Shape {
     static_assert((size_t)NT * kBF * 4 <= (size_t)kStages * kStage, "a partial tile fits where the stages were");
 };
 
-__device__ __forceinline__ void store(void* y, int dtype, uint64_t at, float v) {
-    if (dtype == 0) {
-        static_cast<float*>(y)[at] = v;
+__device__ __forceinline__ uint16_t to_bf16(float v) {
+    uint16_t h;  // the one rounding to 16 bits: Y's own type
+    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(v));
+    return h;
+}
+
+__device__ __forceinline__ void store(const Args& a, uint32_t t, uint32_t f, float v) {
+    const uint64_t at = (uint64_t)t * a.ldy + f;
+    if (a.dtype == 0) static_cast<float*>(a.y)[at] = v;
+    else static_cast<uint16_t*>(a.y)[at] = to_bf16(v);
+}
+
+// Feature f of sixteen neighbouring tokens, from t on.
+__device__ __forceinline__ void store16(const Args& a, uint32_t t, uint32_t f, const uint32_t* r) {
+    if (t + 16 > a.M) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (t + j < a.M) store(a, t + j, f, __uint_as_float(r[j]));
+    } else if (a.dtype == 0) {
+        float* p = static_cast<float*>(a.y) + (uint64_t)t * a.ldy + f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j, p += a.ldy) *p = __uint_as_float(r[j]);
     } else {
-        uint16_t h;  // the one rounding to 16 bits: Y's own type
-        asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(v));
-        static_cast<uint16_t*>(y)[at] = h;
+        uint16_t* p = static_cast<uint16_t*>(a.y) + (uint64_t)t * a.ldy + f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j, p += a.ldy) *p = to_bf16(__uint_as_float(r[j]));
     }
 }
 
 // The scale bytes of K blocks kb..kb+3 of one row as a word; blocks past the
-// end repeat 1.0, which no product uses.
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* s, uint32_t kb, uint32_t nblk) {
+// end repeat 1.0, which no product uses. Words: rows of bytes start on four
+// bytes and their number is a multiple of four.
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* s, uint32_t kb, uint32_t nblk, bool words) {
+    if (words) return __ldg(reinterpret_cast<const uint32_t*>(s + kb));
     uint32_t w = 0;
 #pragma unroll
     for (int i = 0; i < kGroup; ++i) w |= (kb + i < nblk ? (uint32_t)__ldg(s + kb + i) : 127u) << (8 * i);
     return w;
+}
+__device__ __forceinline__ bool in_words(const uint8_t* s, uint32_t nblk) {
+    return nblk % kGroup == 0 && reinterpret_cast<uintptr_t>(s) % kGroup == 0;
 }
 
 template <int NT>
@@ -197,6 +222,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         uint32_t grp = 0;
         bool ok = true;
         const uint32_t quarter = (uint32_t)(warp % 4) << 21;  // lane 32 * (warp % 4)
+        // (a block's part of K may begin between two words)
+        const bool w_words = in_words(a.ws, a.nblk) && kb0 % kGroup == 0, x_words = in_words(a.xs, a.nblk) && kb0 % kGroup == 0;
         for (uint32_t tile = first; ok && tile < tiles; tile += step) {
             uint32_t f0, t0;
             place(tile, f0, t0);
@@ -205,12 +232,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const uint32_t f = f0 + 32 * c + lane;
-                    wa[c] = f < a.N ? scale_word(a.ws + (uint64_t)(f >> a.w_shift) * a.nblk, kb, a.nblk) : 0x7f7f7f7fu;
+                    wa[c] = f < a.N ? scale_word(a.ws + (uint64_t)(f >> a.w_shift) * a.nblk, kb, a.nblk, w_words) : 0x7f7f7f7fu;
                 }
 #pragma unroll
                 for (int c = 0; c < S::kScaleB; ++c) {
                     const uint32_t t = t0 + 32 * c + lane;
-                    wb[c] = 32 * c < NT && t < a.M ? scale_word(a.xs + (uint64_t)t * a.nblk, kb, a.nblk) : 0x7f7f7f7fu;
+                    wb[c] = 32 * c < NT && t < a.M ? scale_word(a.xs + (uint64_t)t * a.nblk, kb, a.nblk, x_words) : 0x7f7f7f7fu;
                 }
                 if (!(ok = bar_wait(sf_empty(grp % S::kRing), ((grp / S::kRing) & 1) ^ 1, wt))) break;
                 fence_after();
@@ -244,9 +271,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) part[(c + j) * kBF + warp * 32 + lane] = __uint_as_float(r[j]);
                 } else if (f < a.N) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (t0 + c + j < a.M) store(a.y, a.dtype, (uint64_t)(t0 + c + j) * a.ldy + f, __uint_as_float(r[j]));
+                    store16(a, t0 + c, f, r);
                 }
             }
             fence_before();
@@ -268,7 +293,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             for (uint32_t c = c0 + threadIdx.x / kBF; c < c1 && t0 + c < a.M; c += 2) {
                 float v = 0.0f;
                 for (uint32_t r = 0; r < a.split; ++r) v += ld_peer(base + (c * kBF + threadIdx.x % kBF) * 4, r);
-                if (f < a.N) store(a.y, a.dtype, (uint64_t)(t0 + c) * a.ldy + f, v);
+                if (f < a.N) store(a, t0 + c, f, v);
             }
         }
         cluster_sync();
@@ -314,6 +339,229 @@ cudaError_t launch(const Matmul8Args& m, Args a, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, a);
 }
 
+// ---- a pair of blocks per tile ---------------------------------------------------
+
+// A tile is 256 features by up to 224 tokens on two SMs. Each block holds 128
+// of the features and half of the tokens' codes; the pair's product reads both,
+// so a block fetches 30 KB per 128 of K where a block by itself would fetch
+// 44 KB for the same rate. Two accumulators of 224 columns leave 64 columns of
+// tensor memory for the scales (256 would leave none).
+constexpr int kMaxNT = 224;
+
+struct Pair {
+    static constexpr uint32_t kHalf = kMaxNT / 2 * kBK;  // X part of a stage
+    static constexpr uint32_t kStage = kABytes + kHalf;
+    static constexpr int kStages = 7;
+    static constexpr int kAcc = 2;
+    static constexpr int kScaleCols = 12;  // 4 of W, 8 of X
+    static constexpr int kRing = 4;
+    static constexpr uint32_t kScaleAt = kAcc * kMaxNT;
+    static constexpr uint32_t kCols = 512;
+    static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
+    static_assert(kScaleAt + kRing * kScaleCols <= kCols, "tensor memory");
+    static_assert(kHalf % 1024 == 0, "stages start on the swizzle's period");
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWarps * 32, 1)
+    matmul8_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, const Args a) {
+    using S = Pair;
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t bars[2 * S::kStages + 2 * S::kRing + 2 * S::kAcc + 1];
+    __shared__ uint32_t tmem_slot;
+    __shared__ uint32_t dead;
+
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = cluster_rank();
+    // full, sf_full and acc_empty of the first block count both blocks
+    const uint32_t full = smem_u32(bars), empty = full + 8 * S::kStages;
+    const uint32_t sf_full = empty + 8 * S::kStages, sf_empty = sf_full + 8 * S::kRing;
+    const uint32_t acc_full = sf_empty + 8 * S::kRing, acc_empty = acc_full + 8 * S::kAcc, drain = acc_empty + 8 * S::kAcc;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S::kStages; ++s) {
+            bar_init(full + 8 * s, 1);
+            bar_init(empty + 8 * s, 1);
+        }
+        for (int s = 0; s < S::kRing; ++s) {
+            bar_init(sf_full + 8 * s, 8);
+            bar_init(sf_empty + 8 * s, 1);
+        }
+        for (int s = 0; s < S::kAcc; ++s) {
+            bar_init(acc_full + 8 * s, 1);
+            bar_init(acc_empty + 8 * s, 8);
+        }
+        bar_init(drain, 1);
+        dead = 0;
+        bar_fence_init();
+    }
+    if (warp == 9) tmem_alloc_pair(smem_u32(&tmem_slot), S::kCols);
+    fence_before();
+    cluster_sync();
+    fence_after();
+    const uint32_t tmem = tmem_slot;
+    const Wait wt{&dead, a.faults};
+    const uint32_t first = blockIdx.x / 2, step = gridDim.x / 2, tiles = a.tiles_f * a.tiles_t;
+    auto place = [&](uint32_t tile, uint32_t& f0, uint32_t& t0) {
+        const uint32_t inner = a.tokens_inner ? a.tiles_t : a.tiles_f, o = tile / inner, i = tile - o * inner;
+        f0 = (a.tokens_inner ? o : i) * (2 * kBF) + rank * kBF;
+        t0 = (a.tokens_inner ? i : o) * a.nt;
+    };
+
+    if (warp == 8) {
+        const bool leader = elect();
+        const uint32_t bytes = 2 * (kABytes + a.nt / 2 * kBK), full0 = in_first(full);
+        Slot<S::kStages> s;
+        uint32_t issued = 0;
+        bool ok = true;
+        for (uint32_t tile = first; ok && tile < tiles; tile += step) {
+            uint32_t f0, t0;
+            place(tile, f0, t0);
+            const int x_row = (int)(t0 + rank * (a.nt / 2));
+            for (uint32_t kb = 0; kb < a.nblk; ++kb) {
+                if (!(ok = bar_wait(empty + 8 * s.at, s.phase ^ 1, wt))) break;
+                const uint32_t dst = base + s.at * S::kStage;
+                if (leader) {
+                    if (rank == 0) bar_expect(full + 8 * s.at, bytes);
+                    tma_2d_pair(dst, &wmap, full0 + 8 * s.at, (int)(kb * kBK), (int)f0);
+                    tma_2d_pair(dst + kABytes, &xmap, full0 + 8 * s.at, (int)(kb * kBK), x_row);
+                }
+                s.next();
+                ++issued;
+            }
+        }
+        // nothing of the pair's may still be on its way when it ends
+        if (dead && leader && rank == 0)
+            for (uint32_t j = issued > (uint32_t)S::kStages ? issued - S::kStages : 0; j < issued; ++j)
+                bar_drain(full + 8 * (j % S::kStages), (j / S::kStages) & 1);
+    } else if (warp == 9) {
+        if (rank == 0) {
+            const bool leader = elect();  // the thread that issues the products also commits them
+            // D float32, A and B e4m3, both along K, UE8M0 scales, N = nt, M = 256
+            const uint32_t idesc = (a.nt / 8) << 17 | 1u << 23 | (uint32_t)(2 * kBF / 16) << 24;
+            Slot<S::kStages> s;
+            Slot<S::kRing> g;
+            Slot<S::kAcc> acc;
+            bool ok = true;
+            for (uint32_t tile = first; ok && tile < tiles; tile += step) {
+                if (!(ok = bar_wait(acc_empty + 8 * acc.at, acc.phase ^ 1, wt))) break;
+                fence_after();
+                const uint32_t d = tmem + acc.at * kMaxNT;
+                for (uint32_t kb = 0; kb < a.nblk; ++kb) {
+                    const uint32_t i = kb % kGroup;
+                    if (i == 0 && !(ok = bar_wait(sf_full + 8 * g.at, g.phase, wt))) break;
+                    if (!(ok = bar_wait(full + 8 * s.at, s.phase, wt))) break;
+                    fence_after();
+                    const uint64_t ad = smem_desc(base + s.at * S::kStage, 16, 1024);
+                    const uint64_t bd = smem_desc(base + s.at * S::kStage + kABytes, 16, 1024);
+                    const uint32_t id = idesc | i << 4 | i << 29, sf = tmem + S::kScaleAt + g.at * S::kScaleCols;
+                    const bool last = i == kGroup - 1 || kb + 1 == a.nblk;
+                    if (leader) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            mma_mx8_pair(d, ad + 2 * j, bd + 2 * j, id, sf, sf + 4, kb > 0 || j > 0);
+                        mma_commit_pair(empty + 8 * s.at);
+                        if (last) mma_commit_pair(sf_empty + 8 * g.at);
+                    }
+                    if (last) g.next();
+                    s.next();
+                }
+                if (ok && leader) mma_commit_pair(acc_full + 8 * acc.at);
+                acc.next();
+            }
+            if (dead && leader) {
+                mma_commit_pair(drain);
+                bar_drain(drain, 0);
+            }
+        }
+    } else if (warp >= 4) {
+        // As above; each block holds the scales of its own features and of all the tile's tokens.
+        Slot<S::kRing> g;
+        bool ok = true;
+        const uint32_t quarter = (uint32_t)(warp % 4) << 21;
+        const bool w_words = in_words(a.ws, a.nblk), x_words = in_words(a.xs, a.nblk);
+        for (uint32_t tile = first; ok && tile < tiles; tile += step) {
+            uint32_t f0, t0;
+            place(tile, f0, t0);
+            for (uint32_t kb = 0; kb < a.nblk; kb += kGroup) {
+                uint32_t wa[4], wb[8];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t f = f0 + 32 * c + lane;
+                    wa[c] = f < a.N ? scale_word(a.ws + (uint64_t)(f >> a.w_shift) * a.nblk, kb, a.nblk, w_words) : 0x7f7f7f7fu;
+                }
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const uint32_t t = t0 + 32 * c + lane;
+                    wb[c] = 32 * c < a.nt && t < a.M ? scale_word(a.xs + (uint64_t)t * a.nblk, kb, a.nblk, x_words) : 0x7f7f7f7fu;
+                }
+                if (!(ok = bar_wait(sf_empty + 8 * g.at, g.phase ^ 1, wt))) break;
+                fence_after();
+                const uint32_t sf = tmem + quarter + S::kScaleAt + g.at * S::kScaleCols;
+                tmem_st4(sf, wa[0], wa[1], wa[2], wa[3]);
+                tmem_st4(sf + 4, wb[0], wb[1], wb[2], wb[3]);
+                tmem_st4(sf + 8, wb[4], wb[5], wb[6], wb[7]);
+                wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive_first(sf_full + 8 * g.at);
+                g.next();
+            }
+        }
+    } else {
+        Slot<S::kAcc> acc;
+        for (uint32_t tile = first; tile < tiles; tile += step) {
+            if (!bar_wait(acc_full + 8 * acc.at, acc.phase, wt)) break;
+            fence_after();
+            uint32_t f0, t0;
+            place(tile, f0, t0);
+            const uint32_t f = f0 + warp * 32 + lane;
+#pragma unroll 1
+            for (uint32_t c = 0; c < a.nt; c += 16) {
+                uint32_t r[16];
+                tmem_ld16(tmem + ((uint32_t)warp << 21) + acc.at * kMaxNT + c, r);
+                wait_ld();
+                if (f < a.N) store16(a, t0 + c, f, r);
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive_first(acc_empty + 8 * acc.at);
+            acc.next();
+        }
+    }
+
+    __syncwarp();
+    fence_before();
+    cluster_sync();  // the other block's products, copies and arrivals reach into this one
+    if (warp == 9) tmem_free_pair(tmem, S::kCols);
+}
+
+cudaError_t launch_pair(const Matmul8Args& m, Args a, int pairs, cudaStream_t s) {
+    // the width that leaves the least of the last round of tiles idle
+    uint64_t best = ~0ull;
+    a.tiles_f = (m.N + 2 * kBF - 1) / (2 * kBF);
+    for (uint32_t nt = kMaxNT; nt >= 160; nt -= 32) {
+        const uint64_t rounds = ((uint64_t)a.tiles_f * ((m.M + nt - 1) / nt) + pairs - 1) / pairs;
+        if (rounds * (nt + 16) < best) {
+            best = rounds * (nt + 16);
+            a.nt = nt;
+        }
+    }
+    a.tiles_t = (m.M + a.nt - 1) / a.nt;
+    const uint64_t tiles = (uint64_t)a.tiles_f * a.tiles_t;
+    if (tiles > 0x7fffffffull) return cudaErrorInvalidValue;
+    a.tokens_inner = m.M <= m.N;
+    a.split = 1;
+    CUtensorMap wmap, xmap;
+    cudaError_t e = make_map(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, m.w, m.K, m.N, m.ldw, kBK, kBF);
+    if (e != cudaSuccess) return e;
+    e = make_map(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, m.x, m.K, m.M, m.ldx, kBK, a.nt / 2);
+    if (e != cudaSuccess) return e;
+    const uint32_t grid = 2 * (uint32_t)(tiles < (uint64_t)pairs ? tiles : pairs);
+    matmul8_pair_kernel<<<grid, kWarps * 32, Pair::kSmem, s>>>(wmap, xmap, a);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_matmul8(const Matmul8Args& m, cudaStream_t s) {
@@ -333,6 +581,11 @@ cudaError_t launch_matmul8(const Matmul8Args& m, cudaStream_t s) {
     if (m.M <= 32) return launch<32>(m, a, s);
     if (m.M <= 64) return launch<64>(m, a, s);
     if (m.M <= 128) return launch<128>(m, a, s);
+    int pairs = 0;
+    e = max_pairs(reinterpret_cast<const void*>(matmul8_pair_kernel), kWarps * 32, Pair::kSmem, &pairs);
+    if (e != cudaSuccess) return e;
+    const uint64_t wide = (uint64_t)((m.N + 2 * kBF - 1) / (2 * kBF)) * ((m.M + kMaxNT - 1) / kMaxNT);
+    if (wide >= (uint64_t)pairs) return launch_pair(m, a, pairs, s);
     return launch<224>(m, a, s);
 }
 

@@ -89,6 +89,18 @@ static __device__ __noinline__ void bar_drain(uint32_t bar, uint32_t parity) {
     }
 }
 
+// Position in a ring of N slots and the parity of the phase that its next use completes.
+template <int N>
+struct Slot {
+    uint32_t at = 0, phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++at == N) {
+            at = 0;
+            phase ^= 1;
+        }
+    }
+};
+
 // ---- TMA ---------------------------------------------------------------------
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
     asm volatile(
@@ -179,6 +191,27 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d, uint64_t a, uint64_t b
         "{.reg .pred p; setp.ne.u32 p, %4, 0;\n"
         "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void mma_mx8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                             uint32_t sfb, bool add) {
+    asm volatile(
+        "{.reg .pred p; setp.ne.u32 p, %6, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"((uint32_t)add)
+        : "memory");
+}
+// Address, in the cluster's window, of what lies at `addr` in the pair's first block.
+__device__ __forceinline__ uint32_t in_first(uint32_t addr) {
+    uint32_t p;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(p) : "r"(addr));
+    return p;
+}
+// Copy into this block's memory that reports to a barrier of the pair's first block (its cluster address).
+__device__ __forceinline__ void tma_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y)
         : "memory");
 }
 // Arrives at the barrier that lies at `bar` in the first block of the pair.

@@ -475,18 +475,6 @@ struct Pair {
     static_assert(kSmem <= 226 * 1024, "shared memory");
 };
 
-// Position in a ring and the parity of the phase that its next use completes.
-template <int N>
-struct Slot {
-    uint32_t at = 0, phase = 0;
-    __device__ __forceinline__ void next() {
-        if (++at == N) {
-            at = 0;
-            phase ^= 1;
-        }
-    }
-};
-
 __device__ __forceinline__ uint4 ld_shared(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
