@@ -9,10 +9,16 @@
 // makes code * 2^e exact in float32 and in bfloat16 (the bound -117 keeps the
 // smallest code times 2^e a normal number).
 //
-// Both directions are bound by HBM: an element is read once and written once
-// and costs a handful of instructions. Sixteen lanes hold one row's block,
-// eight neighbouring elements each, so that the largest is found with four
-// shuffles and bfloat16 rows move 16 bytes a lane.
+// Both directions are bound by HBM: an element is read once and written once.
+// They come near it only with few instructions per element, so the special
+// numbers cost nothing where there are none: maxima ignore NaN, and only a
+// block whose maximum is infinite goes through its elements again.
+//
+// Sixteen lanes hold one row's block. Where rows start on 16 bytes a lane holds
+// eight neighbouring elements, else every sixteenth one, so that its accesses
+// of two or four bytes still run along the row together with its neighbours'.
+#include <cuda_bf16.h>
+
 #include "s2_internal.h"
 
 namespace s2 {
@@ -22,56 +28,74 @@ constexpr int kBlk = 128;
 constexpr int kPer = 8;               // elements per lane
 constexpr int kLanes = kBlk / kPer;   // lanes per block of a row
 constexpr int kMinByte = 10;          // e >= -117
+constexpr uint32_t kInf = 0x7f800000u;
 
-struct Vals {
-    float v[kPer];
+// Eight elements as they lie in memory.
+template <typename T>
+struct Raw {
+    uint32_t w[2 * sizeof(T)];
 };
 
-template <typename T>
-__device__ __forceinline__ float to_f32(T x);
-template <>
-__device__ __forceinline__ float to_f32<float>(float x) {
-    return x;
+// Element i as a float.
+__device__ __forceinline__ float value(const Raw<float>& r, int i) { return __uint_as_float(r.w[i]); }
+__device__ __forceinline__ float value(const Raw<uint16_t>& r, int i) {
+    return __uint_as_float(i % 2 ? r.w[i / 2] & 0xffff0000u : r.w[i / 2] << 16);
 }
-template <>
-__device__ __forceinline__ float to_f32<uint16_t>(uint16_t x) {
-    return __uint_as_float((uint32_t)x << 16);
+__device__ __forceinline__ void put(Raw<float>& r, int i, float x) { r.w[i] = __float_as_uint(x); }
+__device__ __forceinline__ void put(Raw<uint16_t>& r, int i, uint16_t x) { r.w[i / 2] |= (uint32_t)x << (16 * (i % 2)); }
+
+// Column of a lane's element i within its block.
+template <bool VEC>
+__device__ __forceinline__ uint32_t column(uint32_t sub, int i) {
+    return VEC ? sub * kPer + i : sub + i * kLanes;
 }
 
-// Eight elements from p; only the first `valid` exist (the others read as 0).
-// VEC: p is 16-byte aligned.
+// A lane's elements of the block of a row that begins at p; `left` columns
+// exist from there on (the others read as 0). VEC: p is 16-byte aligned.
 template <typename T, bool VEC>
-__device__ __forceinline__ Vals load8(const T* p, int valid) {
-    Vals r;
-    if (VEC && valid >= kPer) {
-        if constexpr (sizeof(T) == 4) {
-            const uint4 a = ld_stream_u4(p), b = ld_stream_u4(p + 4);
-            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+__device__ __forceinline__ Raw<T> load8(const T* p, uint32_t sub, int left) {
+    Raw<T> r;
+    if (VEC && left >= (int)(sub + 1) * kPer) {
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) r.v[i] = __uint_as_float(w[i]);
-        } else {
-            const uint4 a = ld_stream_u4(p);
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                r.v[2 * i] = __uint_as_float(w[i] << 16);
-                r.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            }
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+            const uint4 a = ld_stream_u4(reinterpret_cast<const uint4*>(p + sub * kPer) + i);
+            r.w[4 * i] = a.x;
+            r.w[4 * i + 1] = a.y;
+            r.w[4 * i + 2] = a.z;
+            r.w[4 * i + 3] = a.w;
         }
         return r;
     }
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) r.v[i] = i < valid ? to_f32<T>(p[i]) : 0.0f;
+    for (int i = 0; i < (int)(2 * sizeof(T)); ++i) r.w[i] = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        if ((int)column<VEC>(sub, i) < left) put(r, i, p[column<VEC>(sub, i)]);
     return r;
 }
 
-// Bits of the largest finite magnitude among the eight.
-__device__ __forceinline__ uint32_t amax_bits(const Vals& x) {
+// Bits of the largest magnitude among the eight, NaN aside.
+__device__ __forceinline__ uint32_t amax_bits(const Raw<float>& r) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) m = fmaxf(m, fabsf(__uint_as_float(r.w[i])));
+    return __float_as_uint(m);
+}
+__device__ __forceinline__ uint32_t amax_bits(const Raw<uint16_t>& r) {
+    __nv_bfloat162 m = __float2bfloat162_rn(0.0f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&r.w[i])));
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(&m);
+    return max(w & 0xffff0000u, w << 16);
+}
+// Of the finite ones.
+template <typename T>
+__device__ __forceinline__ uint32_t finite_amax_bits(const Raw<T>& r) {
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const uint32_t b = __float_as_uint(x.v[i]) & 0x7fffffffu;
-        m = max(m, b < 0x7f800000u ? b : 0u);
+        const uint32_t b = __float_as_uint(value(r, i)) & 0x7fffffffu;
+        m = max(m, b < kInf ? b : 0u);
     }
     return m;
 }
@@ -80,17 +104,20 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
     return (uint32_t)max((int)((amax + 0x1fffffu) >> 23) - 8, kMinByte);
 }
 
-// The eight codes of a block with scale byte b, lowest element first. A code
-// is e4m3's nearest (ties to even); NaN and infinities become NaN.
-__device__ __forceinline__ uint2 codes8(const Vals& x, uint32_t b) {
+// The eight codes of a block with scale byte b. A code is e4m3's nearest (ties
+// to even); NaN becomes NaN, and so do infinities, which the conversion alone
+// would saturate (special: the block has some).
+template <typename T>
+__device__ __forceinline__ uint2 codes8(const Raw<T>& r, uint32_t b, bool special) {
     const float inv = __uint_as_float((254u - b) << 23);
     uint32_t h[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float lo = x.v[2 * i] * inv, hi = x.v[2 * i + 1] * inv;
-        // the conversion saturates, so infinities are made NaN first
-        if ((__float_as_uint(lo) & 0x7fffffffu) == 0x7f800000u) lo = __uint_as_float(0x7fffffffu);
-        if ((__float_as_uint(hi) & 0x7fffffffu) == 0x7f800000u) hi = __uint_as_float(0x7fffffffu);
+        float lo = value(r, 2 * i) * inv, hi = value(r, 2 * i + 1) * inv;
+        if (special) {
+            if (fabsf(lo) == __uint_as_float(kInf)) lo = __uint_as_float(0x7fffffffu);
+            if (fabsf(hi) == __uint_as_float(kInf)) hi = __uint_as_float(0x7fffffffu);
+        }
         uint16_t q;
         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(q) : "f"(hi), "f"(lo));
         h[i] = q;
@@ -98,49 +125,60 @@ __device__ __forceinline__ uint2 codes8(const Vals& x, uint32_t b) {
     return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
-// Codes to p (8-byte aligned), the first `valid` of them.
-__device__ __forceinline__ void store_codes(uint8_t* p, uint2 c, int valid) {
-    if (valid >= kPer) {
-        *reinterpret_cast<uint2*>(p) = c;
+__device__ __forceinline__ uint8_t byte_of(uint2 c, int i) { return (uint8_t)((i < 4 ? c.x : c.y) >> (8 * (i % 4))); }
+
+// A lane's codes to the block that begins at p (8-byte aligned).
+template <bool VEC>
+__device__ __forceinline__ void store_codes(uint8_t* p, uint2 c, uint32_t sub, int left) {
+    if (VEC && left >= (int)(sub + 1) * kPer) {
+        *reinterpret_cast<uint2*>(p + sub * kPer) = c;
         return;
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-        if (i < valid) p[i] = (uint8_t)((i < 4 ? c.x >> (8 * i) : c.y >> (8 * (i - 4))) & 0xffu);
+        if ((int)column<VEC>(sub, i) < left) p[column<VEC>(sub, i)] = byte_of(c, i);
 }
 
-constexpr int kItems = 4;  // blocks of a row in flight per half-warp
+// Blocks of a row in flight per half-warp. 8192 x 4096 bfloat16, times with L2
+// flushed: 31 us with two, 37 with four, 33 with one.
+constexpr int kItems = 2;
 
 // One half-warp per block of a row, kItems of them in flight.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) pack_rows_kernel(Pack8Args a) {
     const uint32_t sub = threadIdx.x % kLanes;
-    const uint32_t group = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
-    const uint64_t first = (uint64_t)group * kItems;
+    const uint64_t first = ((uint64_t)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes) * kItems;
     const T* x = static_cast<const T*>(a.x);
-    Vals v[kItems];
+    Raw<T> v[kItems];
     uint64_t row[kItems];
-    uint32_t blk[kItems];
-    int valid[kItems];
+    uint32_t col[kItems];
+    int left[kItems];
+    uint32_t r = first < a.items ? (uint32_t)first / a.nblk : 0, blk = first < a.items ? (uint32_t)first - r * a.nblk : 0;
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-        const uint64_t item = first + i;
-        const bool live = item < (uint64_t)a.items;
-        const uint32_t it = live ? (uint32_t)item : 0u;
-        row[i] = it / a.nblk;
-        blk[i] = it - (uint32_t)row[i] * a.nblk;
-        const uint32_t c0 = blk[i] * kBlk + sub * kPer;
-        valid[i] = live ? min(max((int)a.cols - (int)c0, 0), kPer) : 0;
-        v[i] = load8<T, VEC>(x + row[i] * a.ldx + c0, valid[i]);
+        row[i] = r;
+        col[i] = blk * kBlk;
+        left[i] = first + i < a.items ? (int)(a.cols - col[i]) : 0;
+        v[i] = load8<T, VEC>(x + row[i] * a.ldx + col[i], sub, left[i]);
+        if (++blk == a.nblk) {
+            blk = 0;
+            ++r;
+        }
     }
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
         uint32_t m = amax_bits(v[i]);
 #pragma unroll
         for (int o = kLanes / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+        const bool special = __any_sync(kFull, m == kInf);
+        if (special) {
+            m = finite_amax_bits(v[i]);
+#pragma unroll
+            for (int o = kLanes / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+        }
         const uint32_t b = scale_byte(m);
-        store_codes(a.codes + row[i] * a.ldc + blk[i] * kBlk + sub * kPer, codes8(v[i], b), valid[i]);
-        if (sub == 0 && first + i < (uint64_t)a.items) a.scales[first + i] = (uint8_t)b;
+        store_codes<VEC>(a.codes + row[i] * a.ldc + col[i], codes8(v[i], b, special), sub, left[i]);
+        if (sub == 0 && left[i]) a.scales[first + i] = (uint8_t)b;
     }
 }
 
@@ -166,14 +204,19 @@ __global__ void __launch_bounds__(kThreads) pack_tiles_kernel(Pack8Args a) {
     const uint32_t sub = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
     const uint32_t trow = blockIdx.x / a.nblk, tcol = blockIdx.x - trow * a.nblk;
     const uint64_t r0 = (uint64_t)trow * kBlk + grp * kPer;
-    const uint32_t c0 = tcol * kBlk + sub * kPer;
-    const int cvalid = min(max((int)a.cols - (int)c0, 0), kPer);
+    const int left = (int)(a.cols - tcol * kBlk);
     const int rvalid = (int)min((uint64_t)kPer, a.rows > r0 ? a.rows - r0 : 0);
-    const T* x = static_cast<const T*>(a.x) + r0 * a.ldx + c0;
-    Vals v[kPer];
+    const T* x = static_cast<const T*>(a.x) + (rvalid ? r0 : 0) * a.ldx + tcol * kBlk;
+    Raw<T> v[kPer];
     uint32_t m = 0;
+    // (the whole tile exists nearly always: its loads carry no conditions)
+    if (rvalid == kPer) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) v[i] = load8<T, VEC>(x + (i < rvalid ? i : 0) * a.ldx, i < rvalid ? cvalid : 0);
+        for (int i = 0; i < kPer; ++i) v[i] = load8<T, VEC>(x + i * a.ldx, sub, left);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) v[i] = load8<T, VEC>(x + (i < rvalid ? i : 0) * a.ldx, sub, i < rvalid ? left : 0);
+    }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) m = max(m, amax_bits(v[i]));
     m = __reduce_max_sync(kFull, m);
@@ -181,12 +224,22 @@ __global__ void __launch_bounds__(kThreads) pack_tiles_kernel(Pack8Args a) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kThreads / 32; ++i) m = max(m, warp_max[i]);
+    const bool special = m == kInf;  // the same in the whole block of threads
+    if (special) {
+        m = 0;
+        for (int i = 0; i < kPer; ++i) m = max(m, finite_amax_bits(v[i]));
+        m = __reduce_max_sync(kFull, m);
+        __syncthreads();
+        if (threadIdx.x % 32 == 0) warp_max[threadIdx.x / 32] = m;
+        __syncthreads();
+        for (int i = 0; i < kThreads / 32; ++i) m = max(m, warp_max[i]);
+    }
     const uint32_t b = scale_byte(m);
     uint2 c[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        c[i] = codes8(v[i], b);
-        if (i < rvalid) store_codes(a.codes + (r0 + i) * a.ldc + c0, c[i], cvalid);
+        c[i] = codes8(v[i], b, special);
+        if (i < rvalid) store_codes<VEC>(a.codes + (r0 + i) * a.ldc + tcol * kBlk, c[i], sub, left);
     }
     if (threadIdx.x == 0) {
         a.scales[(uint64_t)trow * a.nblk + tcol] = (uint8_t)b;
@@ -200,20 +253,20 @@ __global__ void __launch_bounds__(kThreads) pack_tiles_kernel(Pack8Args a) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         const uint2 w = j < 4 ? make_uint2(c[j].x, c[j + 4].x) : make_uint2(c[j - 4].y, c[j].y);
-        *reinterpret_cast<uint2*>(turned + (sub * kPer + j) * kTileLd + grp * kPer) = w;
+        *reinterpret_cast<uint2*>(turned + column<VEC>(sub, j) * kTileLd + grp * kPer) = w;
     }
     __syncthreads();
-    const int left = (int)min((uint64_t)kBlk, a.rows - (uint64_t)trow * kBlk);
+    const int down = (int)min((uint64_t)kBlk, a.rows - (uint64_t)trow * kBlk);
 #pragma unroll
     for (int i = 0; i < kBlk * kBlk / 16 / kThreads; ++i) {
         const uint32_t t = threadIdx.x + i * kThreads, col = t / 8, at = (t % 8) * 16;
         if (tcol * kBlk + col >= a.cols) continue;
         const uint8_t* s = turned + col * kTileLd + at;
         uint8_t* d = a.codes_t + (uint64_t)(tcol * kBlk + col) * a.ldct + (uint64_t)trow * kBlk + at;
-        if ((int)at + 16 <= left) {
+        if ((int)at + 16 <= down) {
             *reinterpret_cast<uint4*>(d) = *reinterpret_cast<const uint4*>(s);
         } else {
-            for (int j = 0; (int)at + j < left; ++j) d[j] = s[j];
+            for (int j = 0; (int)at + j < down; ++j) d[j] = s[j];
         }
     }
 }
@@ -236,35 +289,35 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) unpack_kernel(Unpack8Args a) {
     const uint32_t sub = threadIdx.x % kLanes;
-    const uint32_t group = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
-    const uint64_t first = (uint64_t)group * kItems;
+    const uint64_t first = ((uint64_t)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes) * kItems;
     T* out = static_cast<T*>(a.out);
     uint2 c[kItems];
-    uint32_t b[kItems];
+    uint32_t b[kItems], col[kItems];
+    uint64_t row[kItems];
+    int left[kItems];
+    uint32_t r = first < a.items ? (uint32_t)first / a.nblk : 0, blk = first < a.items ? (uint32_t)first - r * a.nblk : 0;
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-        const uint64_t item = first + i;
+        row[i] = r;
+        col[i] = blk * kBlk;
+        left[i] = first + i < a.items ? (int)(a.cols - col[i]) : 0;
+        const uint8_t* p = a.codes + row[i] * a.ldc + col[i];
         c[i] = make_uint2(0, 0);
-        b[i] = 127;
-        if (item >= (uint64_t)a.items) continue;
-        const uint32_t it = (uint32_t)item, row = it / a.nblk, blk = it - row * a.nblk;
-        const uint32_t c0 = blk * kBlk + sub * kPer;
-        const int valid = min(max((int)a.cols - (int)c0, 0), kPer);
-        const uint8_t* p = a.codes + (uint64_t)row * a.ldc + c0;
-        if (valid == kPer) {
-            c[i] = *reinterpret_cast<const uint2*>(p);
+        if (VEC && left[i] >= (int)(sub + 1) * kPer) {
+            c[i] = *reinterpret_cast<const uint2*>(p + sub * kPer);
         } else {
-            for (int j = 0; j < valid; ++j) (j < 4 ? c[i].x : c[i].y) |= (uint32_t)p[j] << (8 * (j % 4));
+#pragma unroll
+            for (int j = 0; j < kPer; ++j)
+                if ((int)column<VEC>(sub, j) < left[i]) (j < 4 ? c[i].x : c[i].y) |= (uint32_t)p[column<VEC>(sub, j)] << (8 * (j % 4));
         }
-        b[i] = a.scales[(uint64_t)(row >> a.row_shift) * a.nblk + blk];
+        b[i] = left[i] ? a.scales[(row[i] >> a.row_shift) * a.nblk + blk] : 127u;
+        if (++blk == a.nblk) {
+            blk = 0;
+            ++r;
+        }
     }
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-        const uint64_t item = first + i;
-        if (item >= (uint64_t)a.items) continue;
-        const uint32_t it = (uint32_t)item, row = it / a.nblk, blk = it - row * a.nblk;
-        const uint32_t c0 = blk * kBlk + sub * kPer;
-        const int valid = min(max((int)a.cols - (int)c0, 0), kPer);
         // byte 0 stands for 2^-127, a subnormal float; byte 255 for NaN
         const float s = __uint_as_float(b[i] == 0 ? 0x00400000u : b[i] == 255 ? 0x7fffffffu : b[i] << 23);
         float f[kPer];
@@ -274,26 +327,28 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(Unpack8Args a) {
             f[2 * j] = d.x * s;
             f[2 * j + 1] = d.y * s;
         }
-        T* o = out + (uint64_t)row * a.ldo + c0;
+        T* o = out + row[i] * a.ldo + col[i];
+        const bool whole = VEC && left[i] >= (int)(sub + 1) * kPer;
         if constexpr (sizeof(T) == 4) {
-            if (VEC && valid == kPer) {
-                reinterpret_cast<float4*>(o)[0] = make_float4(f[0], f[1], f[2], f[3]);
-                reinterpret_cast<float4*>(o)[1] = make_float4(f[4], f[5], f[6], f[7]);
+            if (whole) {
+                float4* q = reinterpret_cast<float4*>(o + sub * kPer);
+                q[0] = make_float4(f[0], f[1], f[2], f[3]);
+                q[1] = make_float4(f[4], f[5], f[6], f[7]);
             } else {
 #pragma unroll
                 for (int j = 0; j < kPer; ++j)
-                    if (j < valid) o[j] = f[j];
+                    if ((int)column<VEC>(sub, j) < left[i]) o[column<VEC>(sub, j)] = f[j];
             }
         } else {
             uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) w[j] = bf16x2(f[2 * j], f[2 * j + 1]);
-            if (VEC && valid == kPer) {
-                *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (whole) {
+                *reinterpret_cast<uint4*>(o + sub * kPer) = make_uint4(w[0], w[1], w[2], w[3]);
             } else {
 #pragma unroll
                 for (int j = 0; j < kPer; ++j)
-                    if (j < valid) o[j] = (uint16_t)(w[j / 2] >> (16 * (j % 2)));
+                    if ((int)column<VEC>(sub, j) < left[i]) o[column<VEC>(sub, j)] = (uint16_t)(w[j / 2] >> (16 * (j % 2)));
             }
         }
     }
