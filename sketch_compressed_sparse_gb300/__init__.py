@@ -412,28 +412,35 @@ S2_SCALE_ROWS, S2_SCALE_TILES = 0, 1
 _LAYOUTS = {"rows": S2_SCALE_ROWS, "tiles": S2_SCALE_TILES}
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 _BYTES = (torch.uint8,)
+_BF16 = (torch.bfloat16,)
 
 
 def _mat(t: torch.Tensor, name: str, dtypes, rows: int = -1, cols: int = -1):
     """Pointer, shape and row stride of a matrix whose rows are contiguous."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be a matrix")
+    if not t.is_cuda or t.dtype not in dtypes or t.dim() != 2:
+        _refuse_mat(t, name, dtypes)
     r, c = t.shape
-    if (rows >= 0 and r != rows) or (cols >= 0 and c != cols):
-        raise ValueError(f"{name} is {r} x {c}, expected {rows if rows >= 0 else r} x {cols if cols >= 0 else c}")
     ld, one = t.stride()
+    if (r != rows and rows >= 0) or (c != cols and cols >= 0):
+        raise ValueError(f"{name} is {r} x {c}, expected {rows if rows >= 0 else r} x {cols if cols >= 0 else c}")
     if one != 1 and c > 1:
         raise ValueError(f"{name} must have contiguous rows")
     return t.data_ptr(), r, c, ld
 
 
+def _refuse_mat(t: torch.Tensor, name: str, dtypes):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    raise ValueError(f"{name} must be a matrix")
+
+
 def _scales(t: torch.Tensor, name: str, rows: int, cols: int, layout: int):
-    n = ((rows + 127) // 128 if layout else rows) * ((cols + 127) // 128)
-    return _dev(t, name, _BYTES, n)
+    need = (((rows + 127) >> 7) if layout else rows) * ((cols + 127) >> 7)
+    if t.is_cuda and t.dtype is torch.uint8 and t.numel() >= need and t.is_contiguous():
+        return t.data_ptr()
+    return _dev(t, name, _BYTES, need)  # says what is wrong
 
 
 def _layout(layout) -> int:
@@ -452,8 +459,10 @@ def s2_pack8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, layout=
         pt, _, _, ldt = _mat(codes_t, "codes_t", _CODES, cols, rows)
     if scales_t is not None:
         pst = _scales(scales_t, "scales_t", cols, rows, lay)
-    _check(_f("s2_pack8")(px, _dtype_code(x), rows, cols, ldx, lay, pc, ldc, _scales(scales, "scales", rows, cols, lay),
-                          pt, ldt, pst, _stream(stream)), "s2_pack8")
+    st = _f("s2_pack8")(px, S2_F32 if x.dtype is torch.float32 else S2_BF16, rows, cols, ldx, lay, pc, ldc,
+                        _scales(scales, "scales", rows, cols, lay), pt, ldt, pst, _stream(stream))
+    if st:
+        raise S2Error(st, "s2_pack8")
 
 
 def s2_unpack8(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor, layout="rows", stream=None) -> None:
@@ -461,8 +470,10 @@ def s2_unpack8(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor, lay
     lay = _layout(layout)
     pc, rows, cols, ldc = _mat(codes, "codes", _CODES)
     po, _, _, ldo = _mat(out, "out", _GRAD, rows, cols)
-    _check(_f("s2_unpack8")(pc, ldc, _scales(scales, "scales", rows, cols, lay), lay, rows, cols, po, _dtype_code(out),
-                            ldo, _stream(stream)), "s2_unpack8")
+    st = _f("s2_unpack8")(pc, ldc, _scales(scales, "scales", rows, cols, lay), lay, rows, cols, po,
+                          S2_F32 if out.dtype is torch.float32 else S2_BF16, ldo, _stream(stream))
+    if st:
+        raise S2Error(st, "s2_unpack8")
 
 
 def s2_matmul8(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, y: torch.Tensor,
@@ -472,19 +483,23 @@ def s2_matmul8(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
     px, M, K, ldx = _mat(x, "x", _CODES)
     pw, N, _, ldw = _mat(w, "w", _CODES, -1, K)
     py, _, _, ldy = _mat(y, "y", _GRAD, M, N)
-    _check(_f("s2_matmul8")(px, ldx, _scales(x_scales, "x_scales", M, K, 0), pw, ldw,
-                            _scales(w_scales, "w_scales", N, K, lay), lay, M, N, K, py, _dtype_code(y), ldy,
-                            _stream(stream)), "s2_matmul8")
+    st = _f("s2_matmul8")(px, ldx, _scales(x_scales, "x_scales", M, K, 0), pw, ldw,
+                          _scales(w_scales, "w_scales", N, K, lay), lay, M, N, K, py,
+                          S2_F32 if y.dtype is torch.float32 else S2_BF16, ldy, _stream(stream))
+    if st:
+        raise S2Error(st, "s2_matmul8")
 
 
 def s2_wgrad8(dy: torch.Tensor, x: torch.Tensor, x_scales: torch.Tensor, dw: torch.Tensor, accumulate: bool = False,
               stream=None) -> None:
     """dw [N, K] = dY^T X (or += with accumulate) of dy [T, N] bfloat16 and packed X [T, K] (layout "rows")."""
-    py, T, N, ldy = _mat(dy, "dy", (torch.bfloat16,))
+    py, T, N, ldy = _mat(dy, "dy", _BF16)
     px, _, K, ldx = _mat(x, "x", _CODES, T)
     pw, _, _, ldw = _mat(dw, "dw", _GRAD, N, K)
-    _check(_f("s2_wgrad8")(py, ldy, px, ldx, _scales(x_scales, "x_scales", T, K, 0), T, N, K, pw, _dtype_code(dw), ldw,
-                           1 if accumulate else 0, _stream(stream)), "s2_wgrad8")
+    st = _f("s2_wgrad8")(py, ldy, px, ldx, _scales(x_scales, "x_scales", T, K, 0), T, N, K, pw,
+                         S2_F32 if dw.dtype is torch.float32 else S2_BF16, ldw, 1 if accumulate else 0, _stream(stream))
+    if st:
+        raise S2Error(st, "s2_wgrad8")
 
 
 def s2_wait_faults() -> int:

@@ -323,7 +323,7 @@ cudaError_t launch(const Matmul8Args& m, Args a, cudaStream_t s) {
     a.split = 1;
     while (a.split < 8 && tiles * a.split * 2 <= (uint64_t)di.sms && a.split * 2 <= a.nblk) a.split *= 2;
     auto kernel = matmul8_kernel<NT>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+    e = allow_smem(reinterpret_cast<const void*>(kernel), S::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(a.split > 1 ? tiles * a.split : tiles < (uint64_t)di.sms ? tiles : di.sms));

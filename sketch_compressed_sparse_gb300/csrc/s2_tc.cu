@@ -61,6 +61,25 @@ cudaError_t wait_fault_word(uint32_t** word) {
     return cudaSuccess;
 }
 
+cudaError_t allow_smem(const void* fn, size_t smem) {
+    struct Entry {
+        int dev;
+        const void* fn;
+    };
+    static std::mutex mu;
+    static Entry table[256];
+    static int used = 0;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < used; ++i)
+        if (table[i].dev == dev && table[i].fn == fn) return cudaSuccess;
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess && used < 256) table[used++] = {dev, fn};
+    return e;
+}
+
 cudaError_t max_pairs(const void* fn, int threads, size_t smem, int* pairs) {
     struct Entry {
         int dev;

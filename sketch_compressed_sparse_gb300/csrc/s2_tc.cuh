@@ -247,6 +247,9 @@ __device__ __forceinline__ float ld_peer(uint32_t addr, uint32_t rank) {
 cudaError_t make_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t cols, uint64_t rows,
                      uint64_t stride, uint32_t box_cols, uint32_t box_rows, bool swizzle = true);
 
+// Lets kernel `fn` use `smem` bytes of dynamic shared memory (set once per device).
+cudaError_t allow_smem(const void* fn, size_t smem);
+
 // Pairs of blocks of kernel `fn` that the device holds at once (cached); also
 // lets the kernel use `smem` bytes of dynamic shared memory.
 cudaError_t max_pairs(const void* fn, int threads, size_t smem, int* pairs);

@@ -420,7 +420,7 @@ cudaError_t launch(const Wgrad8Args& m, Args a, int sms, cudaStream_t s) {
     a.split = 1;
     while (a.split < 8 && tiles * a.split * 2 <= (uint64_t)sms && a.split * 2 <= tblocks) a.split *= 2;
     auto kernel = wgrad8_kernel<NT, TMA>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), S::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(a.split > 1 ? tiles * a.split : tiles < (uint64_t)sms ? tiles : sms));
