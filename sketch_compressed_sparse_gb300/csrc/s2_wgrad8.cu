@@ -7,13 +7,13 @@
 // half the activation's bytes. Both operands are read as they lie, rows along
 // the outputs' axes (tokens are the summed axis), so nothing is transposed.
 //
-// A tile is 128 features of X (the accumulator's lanes) by NT outputs
-// (columns): neighbouring lanes hold neighbouring k, so stores run along dW's
-// rows whatever its alignment. A block of 128 features shares one scale per
-// token. dY comes by tiled copies where its rows start on 16 bytes; else
-// (an odd vocabulary) eight warps fetch it, each the rows t = w mod 8, whose
-// misalignment is the same for the whole call, so that a row is shifted into
-// place by a constant amount.
+// Features of X are the accumulator's lanes and outputs its columns:
+// neighbouring lanes hold neighbouring k, so stores run along dW's rows
+// whatever its alignment. A block of 128 features shares one scale per token.
+// dY comes by tiled copies where its rows start on 16 bytes. Else (an odd
+// vocabulary) the rows t = r mod 8 are one matrix whose rows all miss 16 bytes
+// by the same amount; each r is copied from the boundary before and its warp
+// shifts the rows into place.
 #include "s2_internal.h"
 #include "s2_tc.cuh"
 
@@ -26,7 +26,7 @@ constexpr int kBT = 64;                    // tokens per stage
 constexpr int kBF = 128;                   // features per tile
 constexpr uint32_t kGroupBytes = kBT * 128;  // 64 outputs or features by kBT tokens
 constexpr uint32_t kABytes = 2 * kGroupBytes;
-constexpr int kLoaders = 8;                // warps that fetch a misaligned dY
+constexpr int kLoaders = 8;                // warps that shift a misaligned dY into place
 
 struct Args {
     const uint16_t* dy;
@@ -39,20 +39,9 @@ struct Args {
     uint32_t T, N, K, nblk;
     uint32_t tiles_k, tiles_n;
     uint32_t split;
-    uint32_t nt;  // outputs per tile of the wide form, a multiple of 32
+    uint32_t nt;  // outputs per tile, a multiple of 32
     int dtype, accumulate;
     uint32_t* faults;
-};
-
-template <int NT, bool TMA>
-struct Shape {
-    static constexpr uint32_t kStage = kABytes + NT / 64 * kGroupBytes;
-    static constexpr int kStages = (int)(200 * 1024 / kStage) < 8 ? (int)(200 * 1024 / kStage) : 8;
-    static constexpr int kAcc = 2;
-    static constexpr uint32_t kCols = kAcc * NT;  // a power of two
-    static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
-    static constexpr int kWarps = TMA ? 10 : 10 + kLoaders;
-    static_assert((size_t)NT * kBF * 4 <= (size_t)kStages * kStage, "a partial tile fits where the stages were");
 };
 
 // The scale 2^(b - 127) as a bfloat16, twice in a word (the byte 0 is a
@@ -122,20 +111,6 @@ __device__ __forceinline__ void store16(const Args& a, uint32_t n, uint32_t k, c
     }
 }
 
-// Eight elements of dY from p on, which lies `shift` bytes past a 16-byte
-// boundary; `lo` and `hi` bound the array. Sixteen aligned bytes that the
-// array does not hold whole are read element by element.
-__device__ __forceinline__ uint4 load_piece(const uint8_t* q, const uint8_t* lo, const uint8_t* hi) {
-    if (q >= lo && q + 16 <= hi) return ld_stream_u4(q);
-    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint8_t* e = q + 2 * i;
-        if (e >= lo && e + 2 <= hi) w[i / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(e) << (16 * (i % 2));
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // Sixteen bytes from byte `shift` (even, below 16) of a and b on: whole words
 // by the (warp-uniform) branch, half a word by the funnel.
 template <int WORDS>
@@ -149,301 +124,11 @@ __device__ __forceinline__ uint4 from_word(const uint4& a, const uint4& b, uint3
     return o;
 }
 
-struct Ring {
-    uint32_t base, bar0, first, step, tiles;
-    uint32_t tb0, tb1;  // this block's token blocks
-};
-
-// One loader warp's rows of every tile: t = w mod 8, `shift` bytes past a boundary.
-template <int NT>
-__device__ __forceinline__ void load_rows(const Args& a, const Ring& g, const Wait& wt, uint32_t w, uint32_t lane,
-                                          uint32_t shift) {
-    using S = Shape<NT, false>;
-    constexpr int kChunks = NT / 8;               // 16-byte pieces of a row
-    constexpr int kRows = 32 / kChunks;           // rows of one load
-    constexpr int kLoads = kBT / 8 / kRows;       // loads per stage
-    const uint8_t* lo = reinterpret_cast<const uint8_t*>(a.dy);
-    const uint8_t* hi = lo + ((uint64_t)(a.T - 1) * a.lddy + a.N) * 2;
-    const uint32_t piece = lane % kChunks, sub = lane / kChunks;
-    uint32_t it = 0;
-    for (uint32_t tile = g.first; tile < g.tiles; tile += g.step) {
-        const uint32_t n = tile / a.tiles_k * NT + piece * 8;
-        for (uint32_t tb = g.tb0; tb < g.tb1; ++tb, ++it) {
-            uint4 v[kLoads];
-#pragma unroll
-            for (int j = 0; j < kLoads; ++j) {
-                const uint32_t t = tb * kBT + w + 8 * (j * kRows + sub);
-                v[j] = make_uint4(0, 0, 0, 0);
-                if (t < a.T && n < a.N) {
-                    const uint8_t* q = lo + ((uint64_t)t * a.lddy + n) * 2 - shift;
-                    const uint4 b0 = load_piece(q, lo, hi);
-                    const uint4 b1 = shift ? load_piece(q + 16, lo, hi) : b0;
-                    const uint32_t bits = shift % 4 * 8;
-                    switch (shift / 4) {
-                        case 0: v[j] = from_word<0>(b0, b1, bits); break;
-                        case 1: v[j] = from_word<1>(b0, b1, bits); break;
-                        case 2: v[j] = from_word<2>(b0, b1, bits); break;
-                        default: v[j] = from_word<3>(b0, b1, bits); break;
-                    }
-                }
-            }
-            const int s = it % S::kStages;
-            if (!bar_wait(g.bar0 + 8u * (S::kStages + s), ((it / S::kStages) & 1) ^ 1, wt)) return;
-#pragma unroll
-            for (int j = 0; j < kLoads; ++j) {
-                const uint32_t t = w + 8 * (j * kRows + sub);  // t % 8 == w
-                st_shared(g.base + s * S::kStage + kABytes + piece / 8 * kGroupBytes + t * 128 + ((piece % 8) ^ w) * 16, v[j]);
-            }
-            fence_async();
-            __syncwarp();
-            if (lane == 0) bar_arrive(g.bar0 + 8u * s);
-        }
-    }
-}
-
-template <int NT, bool TMA>
-__global__ void __launch_bounds__(Shape<NT, TMA>::kWarps * 32, 1)
-    wgrad8_kernel(const __grid_constant__ CUtensorMap ymap, const Args a) {
-    using S = Shape<NT, TMA>;
-    extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t bars[3 * S::kStages + 2 * S::kAcc + 1];
-    __shared__ uint32_t tmem_slot;
-    __shared__ uint32_t dead;
-
-    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const uint32_t bar0 = smem_u32(bars);
-    auto full = [&](int s) { return bar0 + 8u * s; };
-    auto empty = [&](int s) { return bar0 + 8u * (S::kStages + s); };
-    auto acc_full = [&](int s) { return bar0 + 8u * (2 * S::kStages + s); };
-    auto acc_empty = [&](int s) { return bar0 + 8u * (2 * S::kStages + S::kAcc + s); };
-    const uint32_t drain = bar0 + 8u * (2 * S::kStages + 2 * S::kAcc);
-    auto copied = [&](int s) { return drain + 8u * (1 + s); };  // dY's part of a stage, by tiled copy
-
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < S::kStages; ++s) {
-            bar_init(full(s), TMA ? 4 : 4 + kLoaders);
-            bar_init(empty(s), 1);
-            bar_init(copied(s), 1);
-        }
-        for (int s = 0; s < S::kAcc; ++s) {
-            bar_init(acc_full(s), 1);
-            bar_init(acc_empty(s), 4);
-        }
-        bar_init(drain, 1);
-        dead = 0;
-        bar_fence_init();
-    }
-    if (warp == 9) tmem_alloc(smem_u32(&tmem_slot), S::kCols);
-    fence_before();
-    __syncthreads();
-    fence_after();
-    const uint32_t tmem = tmem_slot;
-    const Wait wt{&dead, a.faults};
-
-    const uint32_t rank = a.split > 1 ? cluster_rank() : 0;
-    const uint32_t tblocks = (a.T + kBT - 1) / kBT;
-    Ring g;
-    g.base = base;
-    g.bar0 = bar0;
-    g.first = blockIdx.x / a.split;
-    g.step = gridDim.x / a.split;
-    g.tiles = a.tiles_k * a.tiles_n;
-    g.tb0 = (uint32_t)((uint64_t)tblocks * rank / a.split);
-    g.tb1 = (uint32_t)((uint64_t)tblocks * (rank + 1) / a.split);
-
-    if (warp == 8) {
-        if (TMA) {
-            const bool leader = elect();
-            uint32_t it = 0;
-            bool ok = true;
-            for (uint32_t tile = g.first; ok && tile < g.tiles; tile += g.step) {
-                const uint32_t n0 = tile / a.tiles_k * NT;
-                for (uint32_t tb = g.tb0; tb < g.tb1; ++tb, ++it) {
-                    const int s = it % S::kStages;
-                    if (!(ok = bar_wait(empty(s), ((it / S::kStages) & 1) ^ 1, wt))) break;
-                    if (leader) {
-                        bar_expect(copied(s), NT / 64 * kGroupBytes);
-#pragma unroll
-                        for (int c = 0; c < NT / 64; ++c)
-                            tma_2d(base + s * S::kStage + kABytes + c * kGroupBytes, &ymap, copied(s), (int)(n0 + 64 * c),
-                                   (int)(tb * kBT));
-                    }
-                }
-            }
-            // nothing of this block's may still be on its way when it ends
-            if (dead)
-                for (uint32_t j = it > (uint32_t)S::kStages ? it - S::kStages : 0; j < it; ++j)
-                    bar_drain(copied(j % S::kStages), (j / S::kStages) & 1);
-        }
-    } else if (warp == 9) {
-        {
-            const bool leader = elect();  // the thread that issues the products also commits them
-            // D float32, A and B bfloat16, both with rows along M and N
-            const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | 1u << 15 | 1u << 16 | (uint32_t)(NT / 8) << 17 |
-                                   (uint32_t)(kBF / 16) << 24;
-            uint32_t it = 0, n = 0;
-            bool ok = true;
-            for (uint32_t tile = g.first; ok && tile < g.tiles; tile += g.step, ++n) {
-                const int buf = n % S::kAcc;
-                if (!(ok = bar_wait(acc_empty(buf), ((n / S::kAcc) & 1) ^ 1, wt))) break;
-                fence_after();
-                for (uint32_t tb = g.tb0; tb < g.tb1; ++tb, ++it) {
-                    const int s = it % S::kStages;
-                    if (!(ok = bar_wait(full(s), (it / S::kStages) & 1, wt))) break;
-                    if (TMA && !(ok = bar_wait(copied(s), (it / S::kStages) & 1, wt))) break;
-                    fence_after();
-                    const uint64_t ad = smem_desc(base + s * S::kStage, kGroupBytes, 1024);
-                    const uint64_t bd = smem_desc(base + s * S::kStage + kABytes, kGroupBytes, 1024);
-                    if (leader) {
-#pragma unroll
-                        for (int j = 0; j < kBT / 16; ++j)  // 16 tokens: two groups of eight rows
-                            mma_bf16(tmem + buf * NT, ad + 128 * j, bd + 128 * j, idesc, tb > g.tb0 || j > 0);
-                        mma_commit(empty(s));
-                    }
-                }
-                if (ok && leader) mma_commit(acc_full(buf));
-            }
-            if (dead && leader) {
-                mma_commit(drain);
-                bar_drain(drain, 0);
-            }
-        }
-    } else if (warp >= 10) {
-        // the same shift for every row t = w mod 8 and every tile: 8 rows and 8 outputs are multiples of 16 bytes
-        const uint32_t w = warp - 10;
-        load_rows<NT>(a, g, wt, w, lane, (uint32_t)((reinterpret_cast<uintptr_t>(a.dy) + (uint64_t)w * a.lddy * 2) % 16));
-    } else if (warp >= 4) {
-        // widen X: a warp takes eight tokens by 64 features at a time, four lanes a token
-        constexpr int kPieces = 4;
-        const uint32_t w = warp - 4, tsub = lane / 4, piece = lane % 4;
-        uint32_t it = 0;
-        bool ok = true;
-        for (uint32_t tile = g.first; ok && tile < g.tiles; tile += g.step) {
-            const uint32_t kb = tile % a.tiles_k;
-            for (uint32_t tb = g.tb0; tb < g.tb1; ++tb, ++it) {
-                uint4 c[kPieces];
-                uint32_t sc[kPieces];
-#pragma unroll
-                for (int i = 0; i < kPieces; ++i) {
-                    const uint32_t t = tb * kBT + (w * 2 + i / 2) * 8 + tsub, k = kb * kBF + (i % 2) * 64 + piece * 16;
-                    c[i] = make_uint4(0, 0, 0, 0);
-                    sc[i] = 127;
-                    if (t < a.T) {
-                        const uint8_t* p = a.x + (uint64_t)t * a.ldx + k;
-                        sc[i] = __ldg(a.xs + (uint64_t)t * a.nblk + kb);
-                        if (k + 16 <= a.K) {
-                            c[i] = __ldg(reinterpret_cast<const uint4*>(p));
-                        } else {
-                            uint32_t v[4] = {0, 0, 0, 0};
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                if (k + j < a.K) v[j / 4] |= (uint32_t)p[j] << (8 * (j % 4));
-                            c[i] = make_uint4(v[0], v[1], v[2], v[3]);
-                        }
-                    }
-                }
-                const int s = it % S::kStages;
-                if (!(ok = bar_wait(empty(s), ((it / S::kStages) & 1) ^ 1, wt))) break;
-#pragma unroll
-                for (int i = 0; i < kPieces; ++i) {
-                    const uint32_t row = (w * 2 + i / 2) * 8 + tsub;  // row % 8 == tsub
-                    const uint32_t at = base + s * S::kStage + (i % 2) * kGroupBytes + row * 128;
-                    uint4 lo, up;
-                    widen16(c[i], factor_of(sc[i]), lo, up);
-                    st_shared(at + ((2 * piece) ^ tsub) * 16, lo);
-                    st_shared(at + ((2 * piece + 1) ^ tsub) * 16, up);
-                }
-                fence_async();
-                __syncwarp();
-                if (lane == 0) bar_arrive(full(s));
-            }
-        }
-    } else {
-        uint32_t n = 0;
-        for (uint32_t tile = g.first; tile < g.tiles; tile += g.step, ++n) {
-            const int buf = n % S::kAcc;
-            if (!bar_wait(acc_full(buf), (n / S::kAcc) & 1, wt)) break;
-            fence_after();
-            const uint32_t k = tile % a.tiles_k * kBF + warp * 32 + lane, n0 = tile / a.tiles_k * NT;
-#pragma unroll 1
-            for (int c = 0; c < NT; c += 16) {
-                uint32_t r[16];
-                tmem_ld16(tmem + ((uint32_t)warp << 21) + buf * NT + c, r);
-                wait_ld();
-                if (a.split > 1) {
-                    float* part = reinterpret_cast<float*>(raw + (base - smem_u32(raw)));
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) part[(c + j) * kBF + warp * 32 + lane] = __uint_as_float(r[j]);
-                } else if (k < a.K) {
-                    store16(a, n0 + c, k, r);
-                }
-            }
-            fence_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive(acc_empty(buf));
-        }
-    }
-
-    __syncwarp();
-    if (a.split > 1) {
-        // one tile per cluster: parts are added in the order of the ranks
-        cluster_sync();
-        const uint32_t k = g.first % a.tiles_k * kBF + threadIdx.x % kBF, n0 = g.first / a.tiles_k * NT;
-        const uint32_t c0 = NT * rank / a.split, c1 = NT * (rank + 1) / a.split;
-        if (!dead && threadIdx.x < 2 * kBF) {
-            for (uint32_t c = c0 + threadIdx.x / kBF; c < c1 && n0 + c < a.N; c += 2) {
-                float v = 0.0f;
-                for (uint32_t r = 0; r < a.split; ++r) v += ld_peer(base + (c * kBF + threadIdx.x % kBF) * 4, r);
-                if (k < a.K) store(a, n0 + c, k, v);
-            }
-        }
-        cluster_sync();
-    }
-    fence_before();
-    __syncthreads();
-    if (warp == 9) tmem_free(tmem, S::kCols);
-}
-
-template <int NT, bool TMA>
-cudaError_t launch(const Wgrad8Args& m, Args a, int sms, cudaStream_t s) {
-    using S = Shape<NT, TMA>;
-    CUtensorMap ymap{};
-    if (TMA) {
-        const cudaError_t e = make_map(&ymap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, m.dy, m.N, m.T, m.lddy * 2, 64, kBT);
-        if (e != cudaSuccess) return e;
-    }
-    a.tiles_n = (m.N + NT - 1) / NT;
-    const uint64_t tiles = (uint64_t)a.tiles_k * a.tiles_n;
-    if (tiles > 0x7fffffffull) return cudaErrorInvalidValue;
-    const uint32_t tblocks = (m.T + kBT - 1) / kBT;
-    a.split = 1;
-    while (a.split < 8 && tiles * a.split * 2 <= (uint64_t)sms && a.split * 2 <= tblocks) a.split *= 2;
-    auto kernel = wgrad8_kernel<NT, TMA>;
-    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), S::kSmem);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(a.split > 1 ? tiles * a.split : tiles < (uint64_t)sms ? tiles : sms));
-    cfg.blockDim = dim3(S::kWarps * 32);
-    cfg.dynamicSmemBytes = S::kSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = a.split;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = a.split > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, ymap, a);
-}
-
-// ---- the wide form: a pair of blocks per tile ----------------------------------
-
-// A tile is 256 features by 256 outputs on two SMs: each block widens its own
-// 128 features and fetches 128 of the outputs, and the pair's product reads
-// both blocks' shared memory, so dY's part of a stage is half of what one
-// block would need for tiles of the same size.
-constexpr int kPairN = 256;            // outputs per tile, at most (Args::nt)
-constexpr int kHalfN = kPairN / 2;     // of which a block fetches half
+// A tile is 128 features by 128 outputs on one SM, or twice that each way on a
+// pair of SMs (CTAS = 2): each block widens its own 128 features and fetches
+// 128 of the outputs, and the pair's product reads both blocks' shared memory,
+// so it does four times the products of one block's on twice the loads.
+constexpr int kHalfN = 128;            // outputs that a block fetches
 constexpr uint32_t kXRaw = kBT * kBF;  // 8-bit part of a stage
 constexpr uint32_t kBBytes = kHalfN / 64 * kGroupBytes;
 constexpr uint32_t kRowRaw = (kHalfN + 8) * 2;     // a misaligned row's piece: 8 elements more
@@ -456,8 +141,8 @@ struct YMaps {
 // Four rings in shared memory: 8-bit rows of X, widened X (A), dY in place (B)
 // and, for misaligned rows, dY as it lies. B and the raw rows are the deeper
 // ones: they wait for HBM, A only for the arithmetic.
-template <bool ALIGNED>
-struct Pair {
+template <bool ALIGNED, int CTAS>
+struct Form {
     // Teams of four warps widen X, a stage each in turn. A has a slot per team
     // and the raw rows of X kXs, so that a team meets every use of its own
     // slots and can tell their phases by one bit.
@@ -466,14 +151,27 @@ struct Pair {
     static constexpr uint32_t kBAt = kA * kABytes, kXAt = kBAt + kB * kBBytes, kYAt = kXAt + kX * kXRaw;
     static constexpr size_t kSmem = kYAt + kY * kYRaw + 1024;
     static constexpr int kAcc = 2;
-    static constexpr uint32_t kCols = kAcc * kPairN;
+    static constexpr uint32_t kTileN = CTAS * kHalfN, kCols = kAcc * kTileN;
     static constexpr int kWideners = 4 * kTeams;
     static constexpr int kWarps = 4 + kWideners + 2 + (ALIGNED ? 0 : kLoaders);
     static constexpr int kBars = 2 * kX + 2 * kA + 3 * kB + 2 * kY + 2 * kAcc + 1;
     static_assert(kYRaw % 1024 == 0, "rings start on the swizzle's period");
     static_assert(kB >= kA, "a stage's B outlives its A");
     static_assert(kSmem <= 226 * 1024, "shared memory");
+    static_assert((size_t)kTileN * kBF * 4 <= kSmem - 1024 || CTAS == 2, "a partial tile fits where the rings were");
 };
+
+// Arrives at a barrier of the block that issues the products.
+template <int CTAS>
+__device__ __forceinline__ void arrive_issuer(uint32_t bar) {
+    if constexpr (CTAS == 2) bar_arrive_first(bar);
+    else bar_arrive(bar);
+}
+template <int CTAS>
+__device__ __forceinline__ void commit(uint32_t bar) {
+    if constexpr (CTAS == 2) mma_commit_pair(bar);
+    else mma_commit(bar);
+}
 
 __device__ __forceinline__ uint4 ld_shared(uint32_t addr) {
     uint4 v;
@@ -485,10 +183,11 @@ __device__ __forceinline__ uint4 ld_shared(uint32_t addr) {
 // row 8r + (q ^ r % 2) of the operand (the tokens of a stage may lie in any
 // order as long as both operands agree), which keeps this warp's and the
 // wideners' stores free of bank conflicts.
+template <int CTAS>
 __device__ __forceinline__ void realign(uint32_t stages, uint32_t y0, uint32_t b0, uint32_t yfull, uint32_t yempty,
                                         uint32_t bfull, uint32_t bempty, const Wait& wt, uint32_t r, uint32_t lane,
                                         uint32_t shift) {
-    using P = Pair<false>;
+    using P = Form<false, CTAS>;
     const uint32_t q = lane % 8, c0 = lane / 8 * 4, row = q ^ (r % 2), bits = shift % 4 * 8;
     Slot<P::kY> ys;
     Slot<P::kB> bs;
@@ -528,15 +227,15 @@ __device__ __forceinline__ void realign(uint32_t stages, uint32_t y0, uint32_t b
         }
         fence_async();
         __syncwarp();
-        if (lane == 0) bar_arrive_first(bfull + 8 * bs.at);
+        if (lane == 0) arrive_issuer<CTAS>(bfull + 8 * bs.at);
         bs.next();
     }
 }
 
-template <bool ALIGNED>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarps * 32, 1)
-    wgrad8_pair_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ YMaps ymaps, const Args a) {
-    using P = Pair<ALIGNED>;
+template <bool ALIGNED, int CTAS>
+__global__ void __launch_bounds__(Form<ALIGNED, CTAS>::kWarps * 32, 1)
+    wgrad8_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ YMaps ymaps, const Args a) {
+    using P = Form<ALIGNED, CTAS>;
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t bars[P::kBars];
     __shared__ uint32_t tmem_slot;
@@ -544,7 +243,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
 
     const uint32_t a0 = (smem_u32(raw) + 1023u) & ~1023u, b0 = a0 + P::kBAt, x0 = a0 + P::kXAt, y0 = a0 + P::kYAt;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const uint32_t rank = cluster_rank();
+    // the block's place in its pair, and (CTAS = 1) its part of the tokens
+    const uint32_t rank = CTAS == 2 ? cluster_rank() : 0, part = CTAS == 1 && a.split > 1 ? cluster_rank() : 0;
     const uint32_t xfull = smem_u32(bars), xempty = xfull + 8 * P::kX;
     const uint32_t afull = xempty + 8 * P::kX, aempty = afull + 8 * P::kA;       // the first block's afull counts
     const uint32_t bfull = aempty + 8 * P::kA, bempty = bfull + 8 * P::kB;       // both; the same for bfull
@@ -558,11 +258,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
             bar_init(xempty + 8 * s, 4);
         }
         for (int s = 0; s < P::kA; ++s) {
-            bar_init(afull + 8 * s, 2 * 4);
+            bar_init(afull + 8 * s, CTAS * 4);
             bar_init(aempty + 8 * s, 1);
         }
         for (int s = 0; s < P::kB; ++s) {
-            bar_init(bfull + 8 * s, 2 * kLoaders);
+            bar_init(bfull + 8 * s, CTAS * kLoaders);
             bar_init(bempty + 8 * s, 1);
             bar_init(copied + 8 * s, 1);
         }
@@ -572,21 +272,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
         }
         for (int s = 0; s < P::kAcc; ++s) {
             bar_init(acc_full + 8 * s, 1);
-            bar_init(acc_empty + 8 * s, 8);
+            bar_init(acc_empty + 8 * s, CTAS * 4);
         }
         bar_init(drain, 1);
         dead = 0;
         bar_fence_init();
     }
     constexpr int kCopier = 4 + P::kWideners, kIssuer = kCopier + 1;
-    if (warp == kIssuer) tmem_alloc_pair(smem_u32(&tmem_slot), P::kCols);
+    if (warp == kIssuer) {
+        if constexpr (CTAS == 2) tmem_alloc_pair(smem_u32(&tmem_slot), P::kCols);
+        else tmem_alloc(smem_u32(&tmem_slot), P::kCols);
+    }
     fence_before();
-    cluster_sync();
+    if constexpr (CTAS == 2) cluster_sync();
+    else __syncthreads();
     fence_after();
     const uint32_t tmem = tmem_slot;
     const Wait wt{&dead, a.faults};
-    const uint32_t first = blockIdx.x / 2, step = gridDim.x / 2, tiles = a.tiles_k * a.tiles_n;
-    const uint32_t tblocks = (a.T + kBT - 1) / kBT;
+    const uint32_t group = CTAS == 2 ? 2 : a.split;  // blocks that work on one tile
+    const uint32_t first = blockIdx.x / group, step = gridDim.x / group, tiles = a.tiles_k * a.tiles_n;
+    const uint32_t all_tb = (a.T + kBT - 1) / kBT, tb0 = (uint32_t)((uint64_t)all_tb * part / a.split);
+    const uint32_t tblocks = (uint32_t)((uint64_t)all_tb * (part + 1) / a.split) - tb0;
     const uint32_t mine = first < tiles ? (tiles - first - 1) / step + 1 : 0, stages = mine * tblocks;
 
     if (warp == kCopier) {
@@ -596,13 +302,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
         uint32_t nx = 0, ny = 0;  // copies issued
         bool ok = true;
         for (uint32_t tile = first; ok && tile < tiles; tile += step) {
-            const int k0 = (int)((tile % a.tiles_k * 2 + rank) * kBF);
-            const int n0 = (int)(tile / a.tiles_k * a.nt + rank * (a.nt / 2));
+            const int k0 = (int)((tile % a.tiles_k * CTAS + rank) * kBF);
+            const int n0 = (int)(tile / a.tiles_k * a.nt + rank * (a.nt / CTAS));
             for (uint32_t tb = 0; tb < tblocks; ++tb) {
                 if (!(ok = bar_wait(xempty + 8 * xs.at, xs.phase ^ 1, wt))) break;
                 if (leader) {
                     bar_expect(xfull + 8 * xs.at, kXRaw);
-                    tma_2d(x0 + xs.at * kXRaw, &xmap, xfull + 8 * xs.at, k0, (int)(tb * kBT));
+                    tma_2d(x0 + xs.at * kXRaw, &xmap, xfull + 8 * xs.at, k0, (int)((tb0 + tb) * kBT));
                 }
                 xs.next();
                 ++nx;
@@ -613,13 +319,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
 #pragma unroll
                         for (int c = 0; c < kHalfN / 64; ++c)
                             tma_2d(b0 + ys.at * kBBytes + c * kGroupBytes, &ymaps.m[0], copied + 8 * ys.at, n0 + 64 * c,
-                                   (int)(tb * kBT));
+                                   (int)((tb0 + tb) * kBT));
                     } else {
                         bar_expect(yfull + 8 * ys.at, kYRaw);
 #pragma unroll
                         for (int r = 0; r < 8; ++r)
                             tma_2d(y0 + ys.at * kYRaw + r * 8 * kRowRaw, &ymaps.m[r], yfull + 8 * ys.at, n0,
-                                   (int)(tb * kBT / 8));
+                                   (int)((tb0 + tb) * kBT / 8) + (r < (int)a.T ? 0 : 8));
                     }
                 }
                 ys.next();
@@ -637,9 +343,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
     } else if (warp == kIssuer) {
         if (rank == 0) {
             const bool leader = elect();  // the thread that issues the products also commits them
-            // D float32, A and B bfloat16, both with rows along M (256) and N
+            // D float32, A and B bfloat16, both with rows along M and N
             const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | 1u << 15 | 1u << 16 | (a.nt / 8) << 17 |
-                                   (2 * kBF / 16) << 24;
+                                   (uint32_t)(CTAS * kBF / 16) << 24;
             Slot<P::kA> as;
             Slot<P::kB> bs;
             Slot<P::kAcc> acc;
@@ -655,25 +361,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
                     const uint64_t bd = smem_desc(b0 + bs.at * kBBytes, kGroupBytes, 1024);
                     if (leader) {
 #pragma unroll
-                        for (int j = 0; j < kBT / 16; ++j)
-                            mma_bf16_pair(tmem + acc.at * kPairN, ad + 128 * j, bd + 128 * j, idesc, tb > 0 || j > 0);
-                        mma_commit_pair(aempty + 8 * as.at);
-                        mma_commit_pair(bempty + 8 * bs.at);
+                        for (int j = 0; j < kBT / 16; ++j) {  // 16 tokens: two groups of eight rows
+                            const uint32_t d = tmem + acc.at * P::kTileN;
+                            if constexpr (CTAS == 2) mma_bf16_pair(d, ad + 128 * j, bd + 128 * j, idesc, tb > 0 || j > 0);
+                            else mma_bf16(d, ad + 128 * j, bd + 128 * j, idesc, tb > 0 || j > 0);
+                        }
+                        commit<CTAS>(aempty + 8 * as.at);
+                        commit<CTAS>(bempty + 8 * bs.at);
                     }
                     as.next();
                     bs.next();
                 }
-                if (ok && leader) mma_commit_pair(acc_full + 8 * acc.at);
+                if (ok && leader) commit<CTAS>(acc_full + 8 * acc.at);
                 acc.next();
             }
             if (dead && leader) {
-                mma_commit_pair(drain);
+                commit<CTAS>(drain);
                 bar_drain(drain, 0);
             }
         }
     } else if (warp > kIssuer) {
         const uint32_t r = warp - kIssuer - 1;
-        realign(stages, y0, b0, yfull, yempty, bfull, bempty, wt, r, lane,
+        realign<CTAS>(stages, y0, b0, yfull, yempty, bfull, bempty, wt, r, lane,
                 (uint32_t)((reinterpret_cast<uintptr_t>(a.dy) + (uint64_t)r * a.lddy * 2) % 16));
     } else if (warp >= 4) {
         // Widen X: a warp takes sixteen tokens, eight tokens by 64 features at a
@@ -693,16 +402,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
         }
         bool ok = true;
         // scale bytes are fetched one turn ahead
-        uint32_t ahead = first, ahead_tb = team, kb = first % a.tiles_k * 2 + rank;
+        uint32_t ahead = first, ahead_tb = team, kb = first % a.tiles_k * CTAS + rank;
         auto next_scales = [&](uint32_t* b) {
             while (ahead_tb >= tblocks && ahead < tiles) {
                 ahead_tb -= tblocks;
                 ahead += step;
-                kb = ahead % a.tiles_k * 2 + rank;
+                kb = ahead % a.tiles_k * CTAS + rank;
             }
             b[0] = b[1] = 127;
             if (ahead < tiles && kb < a.nblk) {
-                const uint32_t t = ahead_tb * kBT + w * 16 + sub;
+                const uint32_t t = (tb0 + ahead_tb) * kBT + w * 16 + sub;
                 const uint8_t* p = a.xs + (uint64_t)t * a.nblk + kb;
                 if (t < a.T) b[0] = __ldg(p);
                 if (t + 8 < a.T) b[1] = __ldg(p + 8 * a.nblk);
@@ -742,7 +451,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
             // this arrival also tells the first block that this block's B has come
             if (ALIGNED && !(ok = bar_wait(copied + 8 * bs.at, bs.phase, wt))) break;
             __syncwarp();
-            if (lane == 0) bar_arrive_first(afull + 8 * team);
+            if (lane == 0) arrive_issuer<CTAS>(afull + 8 * team);
 #pragma unroll
             for (int i = 0; i < P::kTeams; ++i) bs.next();
         }
@@ -751,30 +460,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<ALIGNED>::kWarp
         for (uint32_t tile = first; tile < tiles; tile += step) {
             if (!bar_wait(acc_full + 8 * acc.at, acc.phase, wt)) break;
             fence_after();
-            const uint32_t k = (tile % a.tiles_k * 2 + rank) * kBF + warp * 32 + lane, n0 = tile / a.tiles_k * a.nt;
+            const uint32_t k = (tile % a.tiles_k * CTAS + rank) * kBF + warp * 32 + lane, n0 = tile / a.tiles_k * a.nt;
 #pragma unroll 1
             for (uint32_t c = 0; c < a.nt; c += 16) {
                 uint32_t r[16];
-                tmem_ld16(tmem + ((uint32_t)warp << 21) + acc.at * kPairN + c, r);
+                tmem_ld16(tmem + ((uint32_t)warp << 21) + acc.at * P::kTileN + c, r);
                 wait_ld();
-                if (k < a.K) store16(a, n0 + c, k, r);
+                if (CTAS == 1 && a.split > 1) {
+                    // this block's part of the sums, where the rings were
+                    float* sums = reinterpret_cast<float*>(raw + (a0 - smem_u32(raw)));
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) sums[(c + j) * kBF + warp * 32 + lane] = __uint_as_float(r[j]);
+                } else if (k < a.K) {
+                    store16(a, n0 + c, k, r);
+                }
             }
             fence_before();
             __syncwarp();
-            if (lane == 0) bar_arrive_first(acc_empty + 8 * acc.at);
+            if (lane == 0) arrive_issuer<CTAS>(acc_empty + 8 * acc.at);
             acc.next();
         }
     }
 
     __syncwarp();
+    if (CTAS == 1 && a.split > 1) {
+        // one tile per cluster: each block adds the parts of its own columns,
+        // in the order of the parts, so the sums do not depend on timing
+        cluster_sync();
+        const uint32_t k = first % a.tiles_k * kBF + threadIdx.x % kBF, n0 = first / a.tiles_k * a.nt;
+        const uint32_t c0 = a.nt * part / a.split, c1 = a.nt * (part + 1) / a.split, rows = blockDim.x / kBF;
+        if (!dead && threadIdx.x < rows * kBF) {
+            for (uint32_t c = c0 + threadIdx.x / kBF; c < c1 && n0 + c < a.N; c += rows) {
+                float v[8];
+#pragma unroll
+                for (uint32_t r = 0; r < 8; ++r)
+                    v[r] = r < a.split ? ld_peer(a0 + (c * kBF + threadIdx.x % kBF) * 4, r) : 0.0f;
+                float sum = v[0];
+#pragma unroll
+                for (uint32_t r = 1; r < 8; ++r) sum += v[r];
+                if (k < a.K) store(a, n0 + c, k, sum);
+            }
+        }
+    }
     fence_before();
-    cluster_sync();  // the other block's products and arrivals reach into this one
-    if (warp == kIssuer) tmem_free_pair(tmem, P::kCols);
+    // the others' products, arrivals and loads reach into this block
+    if (group > 1) cluster_sync();
+    else __syncthreads();
+    if (warp == kIssuer) {
+        if constexpr (CTAS == 2) tmem_free_pair(tmem, P::kCols);
+        else tmem_free(tmem, P::kCols);
+    }
 }
 
-template <bool ALIGNED>
-cudaError_t launch_pair(const Wgrad8Args& m, Args a, cudaStream_t s) {
-    using P = Pair<ALIGNED>;
+template <bool ALIGNED, int CTAS>
+cudaError_t launch(const Wgrad8Args& m, Args a, int sms, cudaStream_t s) {
+    using P = Form<ALIGNED, CTAS>;
     CUtensorMap xmap;
     YMaps ymaps{};
     cudaError_t e = make_map(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, m.x, m.K, m.T, m.ldx, kBF, kBT);
@@ -784,37 +524,62 @@ cudaError_t launch_pair(const Wgrad8Args& m, Args a, cudaStream_t s) {
         if (e != cudaSuccess) return e;
     } else {
         for (uint32_t r = 0; r < 8; ++r) {
-            // row r rounded down to 16 bytes and every eighth row from there: the same shift in all of them
-            const uintptr_t row = reinterpret_cast<uintptr_t>(m.dy) + (uint64_t)r * m.lddy * 2;
+            // row r rounded down to 16 bytes and every eighth row from there:
+            // the same shift in all of them. A residue without rows (T < 8) gets
+            // the first row's map and is read past its end, which gives zeros.
+            const uint32_t row0 = r < m.T ? r : 0;
+            const uintptr_t row = reinterpret_cast<uintptr_t>(m.dy) + (uint64_t)row0 * m.lddy * 2;
             const uint32_t shift = row % 16;
             e = make_map(&ymaps.m[r], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, reinterpret_cast<const void*>(row - shift),
-                         m.N + shift / 2, (m.T - r + 7) / 8, m.lddy * 16, kHalfN + 8, kBT / 8, false);
+                         m.N + shift / 2, (m.T - row0 + 7) / 8, m.lddy * 16, kHalfN + 8, kBT / 8, false);
             if (e != cudaSuccess) return e;
         }
     }
-    a.tiles_k = (m.K + 2 * kBF - 1) / (2 * kBF);
-    auto kernel = wgrad8_pair_kernel<ALIGNED>;
-    int pairs = 0;
-    e = max_pairs(reinterpret_cast<const void*>(kernel), P::kWarps * 32, P::kSmem, &pairs);
+    a.tiles_k = (m.K + CTAS * kBF - 1) / (CTAS * kBF);
+    const void* kernel = reinterpret_cast<const void*>(wgrad8_kernel<ALIGNED, CTAS>);
+    int groups = sms;
+    if (CTAS == 2) e = max_pairs(kernel, P::kWarps * 32, P::kSmem, &groups);
+    else e = allow_smem(kernel, P::kSmem);
     if (e != cudaSuccess) return e;
-    // The width that leaves the least of the last round of tiles idle: time
-    // goes as rounds * (width + 40), the widening of X not getting shorter with
-    // the width (256 x 256 tiles of 4096 x 4096 fill 3.4 of 4 rounds, tiles of
-    // 224 all 4: 213 us became 207 us; 160 took longer wherever it was chosen).
-    uint64_t best = ~0ull;
-    for (uint32_t nt = kPairN; nt >= 224; nt -= 32) {
-        const uint64_t rounds = ((uint64_t)a.tiles_k * ((m.N + nt - 1) / nt) + pairs - 1) / pairs;
-        if (rounds * (nt + 40) < best) {
-            best = rounds * (nt + 40);
-            a.nt = nt;
+    a.nt = P::kTileN;
+    if (CTAS == 2) {
+        // The width that leaves the least of the last round of tiles idle: time
+        // goes as rounds * (width + 40), the widening of X not getting shorter
+        // with the width (256 x 256 tiles of 4096 x 4096 fill 3.4 of 4 rounds,
+        // tiles of 224 all 4: 213 us became 207 us; 160 took longer wherever
+        // it was chosen).
+        uint64_t best = ~0ull;
+        for (uint32_t nt = P::kTileN; nt >= 224; nt -= 32) {
+            const uint64_t rounds = ((uint64_t)a.tiles_k * ((m.N + nt - 1) / nt) + groups - 1) / groups;
+            if (rounds * (nt + 40) < best) {
+                best = rounds * (nt + 40);
+                a.nt = nt;
+            }
         }
     }
     a.tiles_n = (m.N + a.nt - 1) / a.nt;
     const uint64_t tiles = (uint64_t)a.tiles_k * a.tiles_n;
-    if (tiles * ((m.T + kBT - 1) / kBT) > 0xffffffffull) return cudaErrorInvalidValue;
-    const uint32_t grid = 2 * (uint32_t)(tiles < (uint64_t)pairs ? tiles : pairs);
-    kernel<<<grid, P::kWarps * 32, P::kSmem, s>>>(xmap, ymaps, a);
-    return cudaGetLastError();
+    const uint32_t tblocks = (m.T + kBT - 1) / kBT;
+    if (tiles * tblocks > 0xffffffffull) return cudaErrorInvalidValue;
+    // Few tiles: the tokens are split among up to eight blocks of a cluster,
+    // where each keeps at least four stages (adding up the parts takes about
+    // as long as four).
+    a.split = 1;
+    if (CTAS == 1)
+        while (a.split < 8 && tiles * a.split * 2 <= (uint64_t)sms && a.split * 8 <= tblocks) a.split *= 2;
+    const uint32_t size = CTAS == 2 ? 2 : a.split;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(size * (unsigned)(a.split > 1 || tiles < (uint64_t)groups ? tiles : groups));
+    cfg.blockDim = dim3(P::kWarps * 32);
+    cfg.dynamicSmemBytes = P::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = size;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = size > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, wgrad8_kernel<ALIGNED, CTAS>, xmap, ymaps, a);
 }
 
 }  // namespace
@@ -834,15 +599,16 @@ cudaError_t launch_wgrad8(const Wgrad8Args& m, cudaStream_t s) {
     a.T = m.T;
     a.N = m.N;
     a.K = m.K;
-    a.nblk = a.tiles_k = (m.K + kBF - 1) / kBF;
+    a.nblk = (m.K + kBF - 1) / kBF;
     a.dtype = m.dtype;
     a.accumulate = m.accumulate;
     e = tc::wait_fault_word(&a.faults);
     if (e != cudaSuccess) return e;
     const bool tma = reinterpret_cast<uintptr_t>(m.dy) % 16 == 0 && m.lddy % 8 == 0;
-    const bool wide = (uint64_t)((m.K + 255) / 256) * ((m.N + 255) / 256) * 2 >= (uint64_t)di.sms && m.T >= 8;
-    if (wide) return tma ? launch_pair<true>(m, a, s) : launch_pair<false>(m, a, s);
-    return tma ? launch<64, true>(m, a, di.sms, s) : launch<64, false>(m, a, di.sms, s);
+    // Pairs of blocks where their tiles fill the SMs; they have the fewest loads and conversions per product.
+    const bool wide = (uint64_t)((m.K + 255) / 256) * ((m.N + 255) / 256) * 2 >= (uint64_t)di.sms;
+    if (wide) return tma ? launch<true, 2>(m, a, di.sms, s) : launch<false, 2>(m, a, di.sms, s);
+    return tma ? launch<true, 1>(m, a, di.sms, s) : launch<false, 1>(m, a, di.sms, s);
 }
 
 }  // namespace s2

@@ -316,6 +316,28 @@ def test_wgrad_types(N, accumulate, dtype):
     check_wgrad(300, N, 250, dtype, accumulate=accumulate)
 
 
+@pytest.mark.parametrize("T", [1, 3, 7, 8, 9, 70, 600])
+@pytest.mark.parametrize("N", [129, 20001])
+def test_wgrad_few_tokens_unaligned(T, N):
+    """Fewer tokens than residues, and first rows that are not finite where no token follows."""
+    check_wgrad(T, N, 100)
+    xc, xs, _ = packed(make(T, 100, 1), "rows")
+    dy = make(T, N, 2, "bf16").to(DEV)
+    dy[0, 5] = float("inf")
+    dw = torch.empty((N, 100), device=DEV)
+    s2.s2_wgrad8(dy, xc, xs, dw)
+    bad = ~torch.isfinite(dw)
+    assert bool(bad[5].any()) and int(bad.any(1).sum()) == 1
+
+
+@pytest.mark.parametrize("T", [513, 1100, 2100, 4500])
+@pytest.mark.parametrize("N,extra", [(128, 0), (130, 1)])
+def test_wgrad_split_tokens(T, N, extra):
+    """Few tiles and many tokens: every size of cluster."""
+    check_wgrad(T, N, 130, dy_extra=extra)
+    check_wgrad(T, N, 130, "bf16", dy_extra=extra, accumulate=True)
+
+
 @pytest.mark.parametrize("N,extra", [(2500, 0), (2501, 0), (2049, 3)])
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_wgrad_many_tiles(N, extra, accumulate):
