@@ -212,6 +212,9 @@ def test_matmul_many_tiles():
     check_matmul(3, 40000, 200, "bf16", "tiles")
     check_matmul(2000, 2100, 300, "f32", "tiles")
     check_matmul(5000, 700, 256, "bf16", "tiles")
+    check_matmul(20000, 250, 384, "f32", "rows", kind="mixed")
+    check_matmul(230, 40001, 650, "bf16", "tiles", kind="mixed")
+    check_matmul(9001, 1030, 700, "f32", "rows", kind="mixed")
 
 
 def test_matmul_empty():
