@@ -26,6 +26,14 @@ constexpr int kBT = 64;                    // tokens per stage
 constexpr int kBF = 128;                   // features per tile
 constexpr uint32_t kGroupBytes = kBT * 128;  // 64 outputs or features by kBT tokens
 constexpr uint32_t kABytes = 2 * kGroupBytes;
+// The tensor cores add to their float32 sums with truncation, which loses
+// 2e-8 of the sum for every 16 tokens on average (2.4e-6 at 2048 tokens, where
+// a float32 matrix product loses 4e-7). So a float32 result is taken in chunks
+// of at most kChunk stages that are added up with rounding: 8e-7 at any length.
+// The sum stays in tensor memory, in the accumulator of the tile's first chunk;
+// later chunks use the other one, and the products wait only while it is added
+// (additions in L2 or through registers took twice as long in all).
+constexpr uint32_t kChunk = 11;
 constexpr int kLoaders = 8;                // warps that shift a misaligned dY into place
 
 struct Args {
@@ -294,6 +302,7 @@ __global__ void __launch_bounds__(Form<ALIGNED, CTAS>::kWarps * 32, 1)
     const uint32_t all_tb = (a.T + kBT - 1) / kBT, tb0 = (uint32_t)((uint64_t)all_tb * part / a.split);
     const uint32_t tblocks = (uint32_t)((uint64_t)all_tb * (part + 1) / a.split) - tb0;
     const uint32_t mine = first < tiles ? (tiles - first - 1) / step + 1 : 0, stages = mine * tblocks;
+    const uint32_t chunks = a.dtype == 0 ? (tblocks + kChunk - 1) / kChunk : 1;
 
     if (warp == kCopier) {
         const bool leader = elect();
@@ -348,32 +357,34 @@ __global__ void __launch_bounds__(Form<ALIGNED, CTAS>::kWarps * 32, 1)
                                    (uint32_t)(CTAS * kBF / 16) << 24;
             Slot<P::kA> as;
             Slot<P::kB> bs;
-            Slot<P::kAcc> acc;
+            uint32_t acc = 0, uses[P::kAcc] = {};  // how often each accumulator was taken
             bool ok = true;
-            for (uint32_t tile = first; ok && tile < tiles; tile += step) {
-                if (!(ok = bar_wait(acc_empty + 8 * acc.at, acc.phase ^ 1, wt))) break;
-                fence_after();
-                for (uint32_t tb = 0; tb < tblocks; ++tb) {
-                    if (!ALIGNED && !(ok = bar_wait(bfull + 8 * bs.at, bs.phase, wt))) break;
-                    if (!(ok = bar_wait(afull + 8 * as.at, as.phase, wt))) break;
+            for (uint32_t tile = first; ok && tile < tiles; tile += step, acc ^= 1) {
+                for (uint32_t c = 0, tb = 0; ok && c < chunks; ++c) {
+                    const uint32_t at = c ? acc ^ 1 : acc, from = tb, end = tblocks * (c + 1) / chunks;
+                    if (!(ok = bar_wait(acc_empty + 8 * at, (uses[at]++ & 1) ^ 1, wt))) break;
                     fence_after();
-                    const uint64_t ad = smem_desc(a0 + as.at * kABytes, kGroupBytes, 1024);
-                    const uint64_t bd = smem_desc(b0 + bs.at * kBBytes, kGroupBytes, 1024);
-                    if (leader) {
+                    for (; tb < end; ++tb) {
+                        if (!ALIGNED && !(ok = bar_wait(bfull + 8 * bs.at, bs.phase, wt))) break;
+                        if (!(ok = bar_wait(afull + 8 * as.at, as.phase, wt))) break;
+                        fence_after();
+                        const uint64_t ad = smem_desc(a0 + as.at * kABytes, kGroupBytes, 1024);
+                        const uint64_t bd = smem_desc(b0 + bs.at * kBBytes, kGroupBytes, 1024);
+                        if (leader) {
 #pragma unroll
-                        for (int j = 0; j < kBT / 16; ++j) {  // 16 tokens: two groups of eight rows
-                            const uint32_t d = tmem + acc.at * P::kTileN;
-                            if constexpr (CTAS == 2) mma_bf16_pair(d, ad + 128 * j, bd + 128 * j, idesc, tb > 0 || j > 0);
-                            else mma_bf16(d, ad + 128 * j, bd + 128 * j, idesc, tb > 0 || j > 0);
+                            for (int j = 0; j < kBT / 16; ++j) {  // 16 tokens: two groups of eight rows
+                                const uint32_t d = tmem + at * P::kTileN;
+                                if constexpr (CTAS == 2) mma_bf16_pair(d, ad + 128 * j, bd + 128 * j, idesc, tb > from || j > 0);
+                                else mma_bf16(d, ad + 128 * j, bd + 128 * j, idesc, tb > from || j > 0);
+                            }
+                            commit<CTAS>(aempty + 8 * as.at);
+                            commit<CTAS>(bempty + 8 * bs.at);
                         }
-                        commit<CTAS>(aempty + 8 * as.at);
-                        commit<CTAS>(bempty + 8 * bs.at);
+                        as.next();
+                        bs.next();
                     }
-                    as.next();
-                    bs.next();
+                    if (ok && leader) commit<CTAS>(acc_full + 8 * at);
                 }
-                if (ok && leader) commit<CTAS>(acc_full + 8 * acc.at);
-                acc.next();
             }
             if (dead && leader) {
                 commit<CTAS>(drain);
@@ -456,29 +467,50 @@ __global__ void __launch_bounds__(Form<ALIGNED, CTAS>::kWarps * 32, 1)
             for (int i = 0; i < P::kTeams; ++i) bs.next();
         }
     } else {
-        Slot<P::kAcc> acc;
-        for (uint32_t tile = first; tile < tiles; tile += step) {
-            if (!bar_wait(acc_full + 8 * acc.at, acc.phase, wt)) break;
+        uint32_t acc = 0, uses[P::kAcc] = {};
+        bool ok = true;
+        const uint32_t mine0 = tmem + ((uint32_t)warp << 21);
+        for (uint32_t tile = first; ok && tile < tiles; tile += step, acc ^= 1) {
+            const uint32_t sum = mine0 + acc * P::kTileN, other = mine0 + (acc ^ 1) * P::kTileN;
+            if (!(ok = bar_wait(acc_full + 8 * acc, uses[acc]++ & 1, wt))) break;
+            for (uint32_t i = 1; i < chunks; ++i) {
+                if (!(ok = bar_wait(acc_full + 8 * (acc ^ 1), uses[acc ^ 1]++ & 1, wt))) break;
+                fence_after();
+#pragma unroll 1
+                for (uint32_t c = 0; c < a.nt; c += 16) {
+                    uint32_t r[16], v[16];
+                    tmem_ld16(sum + c, r);
+                    tmem_ld16(other + c, v);
+                    wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(v[j]));
+                    tmem_st16(sum + c, r);
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_issuer<CTAS>(acc_empty + 8 * (acc ^ 1));
+                wait_st();
+            }
+            if (!ok) break;
             fence_after();
             const uint32_t k = (tile % a.tiles_k * CTAS + rank) * kBF + warp * 32 + lane, n0 = tile / a.tiles_k * a.nt;
 #pragma unroll 1
             for (uint32_t c = 0; c < a.nt; c += 16) {
                 uint32_t r[16];
-                tmem_ld16(tmem + ((uint32_t)warp << 21) + acc.at * P::kTileN + c, r);
+                tmem_ld16(sum + c, r);
                 wait_ld();
                 if (CTAS == 1 && a.split > 1) {
                     // this block's part of the sums, where the rings were
-                    float* sums = reinterpret_cast<float*>(raw + (a0 - smem_u32(raw)));
+                    float* part_sums = reinterpret_cast<float*>(raw + (a0 - smem_u32(raw)));
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) sums[(c + j) * kBF + warp * 32 + lane] = __uint_as_float(r[j]);
+                    for (int j = 0; j < 16; ++j) part_sums[(c + j) * kBF + warp * 32 + lane] = __uint_as_float(r[j]);
                 } else if (k < a.K) {
                     store16(a, n0 + c, k, r);
                 }
             }
             fence_before();
             __syncwarp();
-            if (lane == 0) arrive_issuer<CTAS>(acc_empty + 8 * acc.at);
-            acc.next();
+            if (lane == 0) arrive_issuer<CTAS>(acc_empty + 8 * acc);
         }
     }
 

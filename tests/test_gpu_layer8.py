@@ -349,6 +349,21 @@ def test_wgrad_many_tiles(N, extra, accumulate):
     check_wgrad(70, 40 * N, 128, "bf16", dy_extra=extra, accumulate=accumulate)
 
 
+@pytest.mark.parametrize("N", [264, 301])
+def test_wgrad_long_sums(N):
+    """A long float32 sum loses no more than one of 704 tokens: each of its 44 additions of 16
+    tokens drops on average half a unit, at most 2^-24 of the sum so far, which is at most the
+    chunk's own on average; the chunks are added with rounding (another 2^-24 each, of random sign)."""
+    T, K = 6000, 260
+    xc, xs, xv = packed(make(T, K, 1), "rows")
+    dy = make(T, N, 2, "bf16")
+    dw = torch.empty((N, K), device=DEV)
+    s2.s2_wgrad8(dy.to(DEV), xc, xs, dw)
+    want = dy.double().numpy().T @ xv
+    err = np.linalg.norm(dw.double().cpu().numpy() - want) / np.linalg.norm(want)
+    assert err <= (44 + 9 ** 0.5) * 2.0 ** -24
+
+
 def test_wgrad_empty():
     dw = torch.full((5, 7), 2.0, device=DEV)[:, :6]
     dy = torch.zeros((0, 5), dtype=torch.bfloat16, device=DEV)
