@@ -287,13 +287,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         cluster_sync();
         uint32_t f0, t0;
         place(first, f0, t0);
-        const uint32_t f = f0 + threadIdx.x % kBF;
-        const uint32_t c0 = NT * rank / a.split, c1 = NT * (rank + 1) / a.split;
-        if (!dead && threadIdx.x < 2 * kBF) {
-            for (uint32_t c = c0 + threadIdx.x / kBF; c < c1 && t0 + c < a.M; c += 2) {
-                float v = 0.0f;
-                for (uint32_t r = 0; r < a.split; ++r) v += ld_peer(base + (c * kBF + threadIdx.x % kBF) * 4, r);
-                if (f < a.N) store(a, t0 + c, f, v);
+        const uint32_t c0 = NT * rank / a.split, c1 = NT * (rank + 1) / a.split, q = lane * 4;
+        if (!dead) {
+            for (uint32_t c = c0 + warp; c < c1 && t0 + c < a.M; c += kWarps) {  // a warp per token, four features a lane
+                const float4 v = sum_of_peers(base + (c * kBF + q) * 4, a.split);
+                const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (f0 + q + j < a.N) store(a, t0 + c, f0 + q + j, e[j]);
             }
         }
         cluster_sync();
@@ -320,8 +321,6 @@ cudaError_t launch(const Matmul8Args& m, Args a, cudaStream_t s) {
     if (tiles > 0x7fffffffull) return cudaErrorInvalidValue;
     // the operand with the fewer bytes is the one that tiles in a row re-read
     a.tokens_inner = m.M <= m.N;
-    a.split = 1;
-    while (a.split < 8 && tiles * a.split * 2 <= (uint64_t)di.sms && a.split * 2 <= a.nblk) a.split *= 2;
     auto kernel = matmul8_kernel<NT>;
     e = allow_smem(reinterpret_cast<const void*>(kernel), S::kSmem);
     if (e != cudaSuccess) return e;
@@ -536,22 +535,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWarps * 32, 1)
     if (warp == 9) tmem_free_pair(tmem, S::kCols);
 }
 
-cudaError_t launch_pair(const Matmul8Args& m, Args a, int pairs, cudaStream_t s) {
-    // the width that leaves the least of the last round of tiles idle
-    uint64_t best = ~0ull;
-    a.tiles_f = (m.N + 2 * kBF - 1) / (2 * kBF);
-    for (uint32_t nt = kMaxNT; nt >= 160; nt -= 32) {
-        const uint64_t rounds = ((uint64_t)a.tiles_f * ((m.M + nt - 1) / nt) + pairs - 1) / pairs;
-        if (rounds * (nt + 16) < best) {
-            best = rounds * (nt + 16);
-            a.nt = nt;
+// Estimated times in nanoseconds, fitted to products of 1 to 2048 tokens by 500
+// to 4096 features and 512 to 4096 of K (most within 10 %): what a launch and a
+// tile's first and last steps take, a stage (128 of K), the stores of a tile,
+// and adding up the parts of a tile that is split. The rounds of tiles overlap
+// their stores with the next round's products.
+struct Plan {
+    int nt;  // tokens per tile
+    int split;
+    bool pair;
+    uint64_t ns;
+};
+
+inline uint64_t rounds_ns(uint64_t rounds, uint64_t stages_ns, uint64_t store_ns) {
+    return (rounds - 1) * (stages_ns > store_ns ? stages_ns : store_ns) + stages_ns + store_ns;
+}
+
+Plan choose(uint32_t M, uint32_t N, uint32_t nblk, int sms, int pairs) {
+    Plan best{16, 1, false, ~0ull};
+    const uint64_t tf = (N + kBF - 1) / kBF;
+    for (int nt : {16, 32, 64, 128, 224}) {
+        if (nt > 16 && (uint32_t)nt >= 2 * M) break;
+        const uint64_t tiles = tf * ((M + nt - 1) / nt);
+        for (int split = 1; split <= 8 && (uint32_t)split <= nblk; split *= 2) {
+            // clusters of four and eight do not fill every SM
+            if (split > 1 && tiles * split > (uint64_t)(split == 2 ? sms : split == 4 ? sms - 8 : sms - 32)) break;
+            const uint64_t rounds = split > 1 ? 1 : (tiles + sms - 1) / sms, kb = (nblk + split - 1) / split;
+            const uint64_t ns = 2900 + rounds_ns(rounds, kb * (200 + nt * 7 / 10), 300 + 9 * nt) + (split > 1 ? 600 + 7 * nt : 0);
+            if (ns < best.ns) best = {nt, split, false, ns};
         }
     }
+    const uint64_t pf = (N + 2 * kBF - 1) / (2 * kBF);
+    for (int nt = kMaxNT; nt >= 160; nt -= 32) {
+        const uint64_t rounds = (pf * ((M + nt - 1) / nt) + pairs - 1) / pairs;
+        const uint64_t ns = 4500 + rounds_ns(rounds, (uint64_t)nblk * (60 + nt), 9 * nt);
+        if (ns < best.ns) best = {nt, 1, true, ns};
+    }
+    return best;
+}
+
+cudaError_t launch_pair(const Matmul8Args& m, Args a, int pairs, cudaStream_t s) {
+    a.tiles_f = (m.N + 2 * kBF - 1) / (2 * kBF);
     a.tiles_t = (m.M + a.nt - 1) / a.nt;
     const uint64_t tiles = (uint64_t)a.tiles_f * a.tiles_t;
     if (tiles > 0x7fffffffull) return cudaErrorInvalidValue;
     a.tokens_inner = m.M <= m.N;
-    a.split = 1;
     CUtensorMap wmap, xmap;
     cudaError_t e = make_map(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, m.w, m.K, m.N, m.ldw, kBK, kBF);
     if (e != cudaSuccess) return e;
@@ -577,16 +605,23 @@ cudaError_t launch_matmul8(const Matmul8Args& m, cudaStream_t s) {
     a.dtype = m.dtype;
     cudaError_t e = wait_fault_word(&a.faults);
     if (e != cudaSuccess) return e;
-    if (m.M <= 16) return launch<16>(m, a, s);
-    if (m.M <= 32) return launch<32>(m, a, s);
-    if (m.M <= 64) return launch<64>(m, a, s);
-    if (m.M <= 128) return launch<128>(m, a, s);
+    DeviceInfo di{};
+    e = device_info(&di);
+    if (e != cudaSuccess) return e;
     int pairs = 0;
     e = max_pairs(reinterpret_cast<const void*>(matmul8_pair_kernel), kWarps * 32, Pair::kSmem, &pairs);
     if (e != cudaSuccess) return e;
-    const uint64_t wide = (uint64_t)((m.N + 2 * kBF - 1) / (2 * kBF)) * ((m.M + kMaxNT - 1) / kMaxNT);
-    if (wide >= (uint64_t)pairs) return launch_pair(m, a, pairs, s);
-    return launch<224>(m, a, s);
+    const Plan plan = choose(m.M, m.N, a.nblk, di.sms, pairs);
+    a.split = (uint32_t)plan.split;
+    a.nt = (uint32_t)plan.nt;
+    if (plan.pair) return launch_pair(m, a, pairs, s);
+    switch (plan.nt) {
+        case 16: return launch<16>(m, a, s);
+        case 32: return launch<32>(m, a, s);
+        case 64: return launch<64>(m, a, s);
+        case 128: return launch<128>(m, a, s);
+        default: return launch<224>(m, a, s);
+    }
 }
 
 }  // namespace s2

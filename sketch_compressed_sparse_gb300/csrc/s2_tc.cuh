@@ -238,12 +238,31 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float ld_peer(uint32_t addr, uint32_t rank) {
-    uint32_t p;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(p) : "memory");
-    return v;
+// The sum, in the order of the ranks, of the four floats at `addr` of blocks
+// 0..blocks-1 (at most 8). All loads are on their way before the first addition.
+__device__ __forceinline__ float4 sum_of_peers(uint32_t addr, uint32_t blocks) {
+    float4 v[8];
+#pragma unroll
+    for (uint32_t r = 0; r < 8; ++r) {
+        v[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (r < blocks) {
+            uint32_t p;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(addr), "r"(r));
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(v[r].x), "=f"(v[r].y), "=f"(v[r].z), "=f"(v[r].w)
+                         : "r"(p)
+                         : "memory");
+        }
+    }
+    float4 s = v[0];
+#pragma unroll
+    for (uint32_t r = 1; r < 8; ++r) {
+        s.x += v[r].x;
+        s.y += v[r].y;
+        s.z += v[r].z;
+        s.w += v[r].w;
+    }
+    return s;
 }
 
 // ---- host: tensor maps -------------------------------------------------------

@@ -519,18 +519,15 @@ __global__ void __launch_bounds__(Form<ALIGNED, CTAS>::kWarps * 32, 1)
         // one tile per cluster: each block adds the parts of its own columns,
         // in the order of the parts, so the sums do not depend on timing
         cluster_sync();
-        const uint32_t k = first % a.tiles_k * kBF + threadIdx.x % kBF, n0 = first / a.tiles_k * a.nt;
-        const uint32_t c0 = a.nt * part / a.split, c1 = a.nt * (part + 1) / a.split, rows = blockDim.x / kBF;
-        if (!dead && threadIdx.x < rows * kBF) {
-            for (uint32_t c = c0 + threadIdx.x / kBF; c < c1 && n0 + c < a.N; c += rows) {
-                float v[8];
+        const uint32_t k = first % a.tiles_k * kBF + lane * 4, n0 = first / a.tiles_k * a.nt;
+        const uint32_t c0 = a.nt * part / a.split, c1 = a.nt * (part + 1) / a.split;
+        if (!dead) {
+            for (uint32_t c = c0 + warp; c < c1 && n0 + c < a.N; c += P::kWarps) {  // a warp per output, four features a lane
+                const float4 v = sum_of_peers(a0 + (c * kBF + lane * 4) * 4, a.split);
+                const float e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (uint32_t r = 0; r < 8; ++r)
-                    v[r] = r < a.split ? ld_peer(a0 + (c * kBF + threadIdx.x % kBF) * 4, r) : 0.0f;
-                float sum = v[0];
-#pragma unroll
-                for (uint32_t r = 1; r < 8; ++r) sum += v[r];
-                if (k < a.K) store(a, n0 + c, k, sum);
+                for (int j = 0; j < 4; ++j)
+                    if (k + j < a.K) store(a, n0 + c, k + j, e[j]);
             }
         }
     }
