@@ -205,9 +205,6 @@ __device__ __forceinline__ void realign(uint32_t stages, uint32_t y0, uint32_t b
         uint4 v[5];
 #pragma unroll
         for (int i = 0; i < 5; ++i) v[i] = ld_shared(src + 16 * i);
-        __syncwarp();
-        if (lane == 0) bar_arrive(yempty + 8 * ys.at);
-        ys.next();
         uint4 o[4];
         switch (shift / 4) {
             case 0:
@@ -233,9 +230,17 @@ __device__ __forceinline__ void realign(uint32_t stages, uint32_t y0, uint32_t b
             const uint32_t c = c0 + i;
             st_shared(dst + c / 8 * kGroupBytes + ((c % 8) ^ row) * 16, o[i]);
         }
+        // The raw slot is released only here: the stores above have the loaded
+        // values, and the fence orders the loads before the next copy into the
+        // slot. (An arrival right after the loads were issued let that copy
+        // overtake them.)
         fence_async();
         __syncwarp();
-        if (lane == 0) arrive_issuer<CTAS>(bfull + 8 * bs.at);
+        if (lane == 0) {
+            bar_arrive(yempty + 8 * ys.at);
+            arrive_issuer<CTAS>(bfull + 8 * bs.at);
+        }
+        ys.next();
         bs.next();
     }
 }
@@ -443,8 +448,6 @@ __global__ void __launch_bounds__(Form<ALIGNED, CTAS>::kWarps * 32, 1)
             uint4 c[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) c[i] = ld_shared((src ^ (i % 2 * 64)) + i / 2 * 1024);
-            __syncwarp();
-            if (lane == 0) bar_arrive(xempty + 8 * x);  // the raw rows are in registers
             xs.next();
             // all the arithmetic before the wait: only the stores lie between a
             // slot's release and its next product
@@ -462,7 +465,10 @@ __global__ void __launch_bounds__(Form<ALIGNED, CTAS>::kWarps * 32, 1)
             // this arrival also tells the first block that this block's B has come
             if (ALIGNED && !(ok = bar_wait(copied + 8 * bs.at, bs.phase, wt))) break;
             __syncwarp();
-            if (lane == 0) arrive_issuer<CTAS>(afull + 8 * team);
+            if (lane == 0) {
+                bar_arrive(xempty + 8 * x);  // as in realign(): not before the loaded values are stored
+                arrive_issuer<CTAS>(afull + 8 * team);
+            }
 #pragma unroll
             for (int i = 0; i < P::kTeams; ++i) bs.next();
         }
@@ -541,6 +547,44 @@ __global__ void __launch_bounds__(Form<ALIGNED, CTAS>::kWarps * 32, 1)
     }
 }
 
+// Estimated times in nanoseconds, fitted to 1 to 8192 tokens and layers of 512
+// to 4096 (most within 10 %): what a launch and a tile's first and last steps
+// take, a stage (64 tokens; widening X does not get shorter with the tile), the
+// stores of a tile, and adding up the parts of a tile whose tokens are split.
+// The rounds of tiles overlap their stores with the next round's products. At
+// 4096 x 4096 tiles of 224 outputs fill 4 rounds of pairs where 256 fill 3.4.
+struct Plan {
+    uint32_t nt, split;
+    int ctas;
+    uint64_t ns;
+};
+
+inline uint64_t rounds_ns(uint64_t rounds, uint64_t stages_ns, uint64_t store_ns) {
+    return (rounds - 1) * (stages_ns > store_ns ? stages_ns : store_ns) + stages_ns + store_ns;
+}
+
+Plan choose(uint32_t T, uint32_t N, uint32_t K, bool aligned, int sms, int pairs) {
+    Plan best{32, 1, 1, ~0ull};
+    const uint64_t stages = (T + kBT - 1) / kBT, shift = aligned ? 0 : 190;
+    const uint64_t tk = (K + kBF - 1) / kBF, pk = (K + 2 * kBF - 1) / (2 * kBF);
+    for (uint32_t nt = 32; nt <= 128; nt *= 2) {
+        const uint64_t tiles = tk * ((N + nt - 1) / nt);
+        for (uint32_t split = 1; split <= 8 && split <= stages; split *= 2) {
+            // clusters of four and eight do not fill every SM
+            if (split > 1 && tiles * split > (uint64_t)(split == 2 ? sms : split == 4 ? sms - 8 : sms - 32)) break;
+            const uint64_t rounds = split > 1 ? 1 : (tiles + sms - 1) / sms, tb = (stages + split - 1) / split;
+            const uint64_t ns = 3600 + rounds_ns(rounds, tb * (260 + nt / 2 + shift), 300 + 9 * nt) + (split > 1 ? 600 + 7 * nt : 0);
+            if (ns < best.ns) best = {nt, split, 1, ns};
+        }
+    }
+    for (uint32_t nt = 256; nt >= 160; nt -= 32) {
+        const uint64_t rounds = (pk * ((N + nt - 1) / nt) + pairs - 1) / pairs;
+        const uint64_t ns = 5200 + rounds_ns(rounds, stages * (200 + nt * 2 / 3 + shift), 300 + 9 * nt);
+        if (ns < best.ns) best = {nt, 1, 2, ns};
+    }
+    return best;
+}
+
 template <bool ALIGNED, int CTAS>
 cudaError_t launch(const Wgrad8Args& m, Args a, int sms, cudaStream_t s) {
     using P = Form<ALIGNED, CTAS>;
@@ -570,32 +614,10 @@ cudaError_t launch(const Wgrad8Args& m, Args a, int sms, cudaStream_t s) {
     if (CTAS == 2) e = max_pairs(kernel, P::kWarps * 32, P::kSmem, &groups);
     else e = allow_smem(kernel, P::kSmem);
     if (e != cudaSuccess) return e;
-    a.nt = P::kTileN;
-    if (CTAS == 2) {
-        // The width that leaves the least of the last round of tiles idle: time
-        // goes as rounds * (width + 40), the widening of X not getting shorter
-        // with the width (256 x 256 tiles of 4096 x 4096 fill 3.4 of 4 rounds,
-        // tiles of 224 all 4: 213 us became 207 us; 160 took longer wherever
-        // it was chosen).
-        uint64_t best = ~0ull;
-        for (uint32_t nt = P::kTileN; nt >= 224; nt -= 32) {
-            const uint64_t rounds = ((uint64_t)a.tiles_k * ((m.N + nt - 1) / nt) + groups - 1) / groups;
-            if (rounds * (nt + 40) < best) {
-                best = rounds * (nt + 40);
-                a.nt = nt;
-            }
-        }
-    }
     a.tiles_n = (m.N + a.nt - 1) / a.nt;
     const uint64_t tiles = (uint64_t)a.tiles_k * a.tiles_n;
     const uint32_t tblocks = (m.T + kBT - 1) / kBT;
     if (tiles * tblocks > 0xffffffffull) return cudaErrorInvalidValue;
-    // Few tiles: the tokens are split among up to eight blocks of a cluster,
-    // where each keeps at least four stages (adding up the parts takes about
-    // as long as four).
-    a.split = 1;
-    if (CTAS == 1)
-        while (a.split < 8 && tiles * a.split * 2 <= (uint64_t)sms && a.split * 8 <= tblocks) a.split *= 2;
     const uint32_t size = CTAS == 2 ? 2 : a.split;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(size * (unsigned)(a.split > 1 || tiles < (uint64_t)groups ? tiles : groups));
@@ -634,9 +656,14 @@ cudaError_t launch_wgrad8(const Wgrad8Args& m, cudaStream_t s) {
     e = tc::wait_fault_word(&a.faults);
     if (e != cudaSuccess) return e;
     const bool tma = reinterpret_cast<uintptr_t>(m.dy) % 16 == 0 && m.lddy % 8 == 0;
-    // Pairs of blocks where their tiles fill the SMs; they have the fewest loads and conversions per product.
-    const bool wide = (uint64_t)((m.K + 255) / 256) * ((m.N + 255) / 256) * 2 >= (uint64_t)di.sms;
-    if (wide) return tma ? launch<true, 2>(m, a, di.sms, s) : launch<false, 2>(m, a, di.sms, s);
+    int pairs = 0;
+    using P = Form<true, 2>;
+    e = tc::max_pairs(reinterpret_cast<const void*>(wgrad8_kernel<true, 2>), P::kWarps * 32, P::kSmem, &pairs);
+    if (e != cudaSuccess) return e;
+    const Plan plan = choose(m.T, m.N, m.K, tma, di.sms, pairs);
+    a.nt = plan.nt;
+    a.split = plan.split;
+    if (plan.ctas == 2) return tma ? launch<true, 2>(m, a, di.sms, s) : launch<false, 2>(m, a, di.sms, s);
     return tma ? launch<true, 1>(m, a, di.sms, s) : launch<false, 1>(m, a, di.sms, s);
 }
 

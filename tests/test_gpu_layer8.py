@@ -457,6 +457,40 @@ def test_wgrad_repeats_and_streams(N):
     assert all(torch.equal(o, outs[0]) for o in outs)
 
 
+@pytest.mark.parametrize("T,N,K", [(600, 20001, 100), (640, 20000, 100), (2000, 20001, 128), (700, 9001, 520)])
+def test_wgrad_same_bits_from_cold_caches(T, N, K):
+    """Copies that come late and early, in every order, give the same bits: L2 flushed before every other run."""
+    xc, xs, xv = packed(make(T, K, 1), "rows")
+    dy = make(T, N, 2, "bf16").to(DEV)
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device=DEV)
+    first, dw = torch.empty((N, K), device=DEV), torch.empty((N, K), device=DEV)
+    s2.s2_wgrad8(dy, xc, xs, first)
+    yv = dy.double().cpu().numpy()
+    tol = (17 / 16 * T + 27) * 2.0 ** -23 * (np.abs(yv).T @ np.abs(xv)) + 2.0 ** -149
+    assert (np.abs(first.double().cpu().numpy() - yv.T @ xv) <= tol).all()
+    for i in range(100):
+        if i % 2:
+            flush.fill_(i)
+        dw.fill_(7.0)
+        s2.s2_wgrad8(dy, xc, xs, dw)
+        assert torch.equal(dw, first), f"run {i}"
+
+
+@pytest.mark.parametrize("M,N,K", [(24, 20001, 1024), (100, 20000, 700), (500, 9001, 2048)])
+def test_matmul_same_bits_from_cold_caches(M, N, K):
+    xc, xs, _ = packed(make(M, K, 1), "rows")
+    wc, ws, _ = packed(make(N, K, 2), "tiles")
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device=DEV)
+    first, y = torch.empty((M, N), device=DEV), torch.empty((M, N), device=DEV)
+    s2.s2_matmul8(xc, xs, wc, ws, first)
+    for i in range(100):
+        if i % 2:
+            flush.fill_(i)
+        y.fill_(7.0)
+        s2.s2_matmul8(xc, xs, wc, ws, y)
+        assert torch.equal(y, first), f"run {i}"
+
+
 def test_wgrad_against_differences():
     """L(W) = sum(G * (X W^T)) is linear in W: its central difference along a direction D of packed
     weights is <dL/dW, D>. Both sides in float64 from the operators' float32 outputs:
