@@ -192,7 +192,12 @@ __device__ __forceinline__ void transpose4(uint32_t& r0, uint32_t& r1, uint32_t&
     r3 = __byte_perm(c, d, 0x7632);
 }
 
-constexpr int kTileLd = kBlk + 16;  // row length of the transposed tile in shared memory, in bytes
+// Place of the 16 bytes of rows 16 u to 16 u + 15 of column col in the
+// transposed tile in shared memory: shifted among the eight of a column so
+// that lanes that hold columns 8 or 1 apart meet different banks.
+__device__ __forceinline__ uint32_t turned_at(uint32_t col, uint32_t u) {
+    return col * kBlk + ((u ^ col ^ (col / 8)) % 8) * 16;
+}
 
 // One block of threads per 128 x 128 tile: each half-warp holds eight whole
 // rows of it in registers, so the tile is read once; the transposed codes
@@ -200,7 +205,7 @@ constexpr int kTileLd = kBlk + 16;  // row length of the transposed tile in shar
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) pack_tiles_kernel(Pack8Args a) {
     __shared__ uint32_t warp_max[kThreads / 32];
-    __shared__ __align__(16) uint8_t turned[kBlk * kTileLd];
+    __shared__ __align__(16) uint8_t turned[kBlk * kBlk];
     const uint32_t sub = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
     const uint32_t trow = blockIdx.x / a.nblk, tcol = blockIdx.x - trow * a.nblk;
     const uint64_t r0 = (uint64_t)trow * kBlk + grp * kPer;
@@ -253,7 +258,7 @@ __global__ void __launch_bounds__(kThreads) pack_tiles_kernel(Pack8Args a) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         const uint2 w = j < 4 ? make_uint2(c[j].x, c[j + 4].x) : make_uint2(c[j - 4].y, c[j].y);
-        *reinterpret_cast<uint2*>(turned + column<VEC>(sub, j) * kTileLd + grp * kPer) = w;
+        *reinterpret_cast<uint2*>(turned + turned_at(column<VEC>(sub, j), grp / 2) + grp % 2 * 8) = w;
     }
     __syncthreads();
     const int down = (int)min((uint64_t)kBlk, a.rows - (uint64_t)trow * kBlk);
@@ -261,7 +266,7 @@ __global__ void __launch_bounds__(kThreads) pack_tiles_kernel(Pack8Args a) {
     for (int i = 0; i < kBlk * kBlk / 16 / kThreads; ++i) {
         const uint32_t t = threadIdx.x + i * kThreads, col = t / 8, at = (t % 8) * 16;
         if (tcol * kBlk + col >= a.cols) continue;
-        const uint8_t* s = turned + col * kTileLd + at;
+        const uint8_t* s = turned + turned_at(col, t % 8);
         uint8_t* d = a.codes_t + (uint64_t)(tcol * kBlk + col) * a.ldct + (uint64_t)trow * kBlk + at;
         if ((int)at + 16 <= down) {
             *reinterpret_cast<uint4*>(d) = *reinterpret_cast<const uint4*>(s);
