@@ -384,8 +384,10 @@ S2_API s2_status s2_pipeline_dense_host(const void *host_grad, s2_dtype dt, uint
  *                   (activations, gradients of outputs);
  *   S2_SCALE_TILES: scales [ceil(rows/128)][nblk], a block is 128 x 128
  *                   elements (weights: the transpose has the same values).
- * Sizes up to 2^31 - 1 (S2_ERR_UNSUPPORTED). Row strides of the other
- * matrices are in elements and need only cover a row. A size of zero is valid.
+ * Sizes up to 2^31 - 1, row strides below 2^35 (S2_ERR_UNSUPPORTED). Row
+ * strides of the other matrices are in elements and need only cover a row. A
+ * size of zero is valid. The first s2_matmul8 and s2_wgrad8 on a device look up
+ * an address there: make them before any stream capture.
  */
 typedef enum {
     S2_SCALE_ROWS = 0,
@@ -397,7 +399,9 @@ typedef enum {
  * is the least 2^e, e >= -117, with no finite element above 448 * 2^e; a code
  * is its element divided by the scale, rounded to nearest, ties to even. NaN
  * and infinities become NaN codes and leave their block's scale alone. (So
- * the bytes are 10..247 and code * scale is exact in float32 and bfloat16.)
+ * the bytes are 10..247 and code * scale is exact in float32 and bfloat16,
+ * except that an element above (1 - 2^-5) * 2^128 rounds up to 2^128, which
+ * neither type holds: infinity.)
  * codes_t / scales_t (both or neither; S2_SCALE_TILES only): also the
  * transposed matrix, codes_t [cols][rows] with row stride ldct, scales_t
  * [ceil(cols/128)][ceil(rows/128)], for the product with the weight's
@@ -430,7 +434,8 @@ S2_API s2_status s2_matmul8(const uint8_t *x, uint64_t ldx, const uint8_t *x_sca
  *   with S2_SCALE_ROWS. X's values are exact in bfloat16 (scale bytes 10 to
  *   247, as s2_pack8 writes them; others are rounded), the sums are float32.
  *   accumulate != 0: dw += the sum instead (one more rounding), for a
- *   gradient taken over several batches. The result does not depend on
+ *   gradient taken over several batches. Long float32 sums are taken in
+ *   chunks of at most 704 tokens. The result does not depend on
  *   timing. dw may be a worker's row of grad[W][n], which s2_encode_batched
  *   and s2_block_topk read. Where base or row stride of dy misses 16 bytes
  *   the rows are fetched through registers (slower than aligned rows).

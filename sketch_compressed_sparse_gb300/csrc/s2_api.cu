@@ -315,7 +315,7 @@ inline uint64_t extent(uint64_t rows, uint64_t cols, uint64_t ld, uint64_t esz) 
 
 // A matrix argument: its row stride covers a row and its bytes are addressable.
 inline s2_status check_matrix(uint64_t rows, uint64_t cols, uint64_t ld) {
-    if (rows > kMaxDim8 || cols > kMaxDim8 || ld >= (1ull << 38)) return S2_ERR_UNSUPPORTED;
+    if (rows > kMaxDim8 || cols > kMaxDim8 || ld >= (1ull << 35)) return S2_ERR_UNSUPPORTED;  // tensor maps: 2^40 bytes
     return rows > 1 && ld < cols ? S2_ERR_INVALID_ARG : S2_OK;
 }
 

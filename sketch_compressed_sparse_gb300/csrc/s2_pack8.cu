@@ -12,7 +12,10 @@
 // Both directions are bound by HBM: an element is read once and written once.
 // They come near it only with few instructions per element, so the special
 // numbers cost nothing where there are none: maxima ignore NaN, and only a
-// block whose maximum is infinite goes through its elements again.
+// block whose maximum is infinite goes through its elements again. Measured, of
+// the 6.79 TB/s of a plain copy: packing 8192 x 4096 bfloat16 20.2 us (5.0 TB/s,
+// 0.74), unpacking it 18.5 us (0.80), packing 33278 x 512 float32 in both orders
+// 22.9 us (0.66; its 1040 tiles are 2.3 rounds of the 456 that are resident).
 //
 // Sixteen lanes hold one row's block. Where rows start on 16 bytes a lane holds
 // eight neighbouring elements, else every sixteenth one, so that its accesses
@@ -139,8 +142,9 @@ __device__ __forceinline__ void store_codes(uint8_t* p, uint2 c, uint32_t sub, i
         if ((int)column<VEC>(sub, i) < left) p[column<VEC>(sub, i)] = byte_of(c, i);
 }
 
-// Blocks of a row in flight per half-warp. 8192 x 4096 bfloat16, times with L2
-// flushed: 31 us with two, 37 with four, 33 with one.
+// Blocks of a row in flight per half-warp. 8192 x 4096 bfloat16 with L2 flushed:
+// packing 23 us with two or four, 27 with one; unpacking 21, 21 and 25; rows of
+// 4095 33, 44 and 36 (unpacking).
 constexpr int kItems = 2;
 
 // One half-warp per block of a row, kItems of them in flight.

@@ -115,6 +115,7 @@ def test_matmul_refusals(lib):
     assert call(y=A + 2 * G + 512) == INVALID    # over W
     assert call(y=A + G) == INVALID and call(y=A + 3 * G) == INVALID
     assert call(M=1 << 31) == UNSUP and call(N=1 << 31, ldy=1 << 31) == UNSUP
+    assert call(ldw=1 << 35) == UNSUP and call(ldy=1 << 35) == UNSUP
     assert call(M=0) == OK and call(N=0) == OK
 
 
