@@ -13,13 +13,14 @@
 // They come near it only with few instructions per element, so the special
 // numbers cost nothing where there are none: maxima ignore NaN, and only a
 // block whose maximum is infinite goes through its elements again. Measured, of
-// the 6.79 TB/s of a plain copy: packing 8192 x 4096 bfloat16 20.2 us (5.0 TB/s,
-// 0.74), unpacking it 18.5 us (0.80), packing 33278 x 512 float32 in both orders
-// 22.9 us (0.66; its 1040 tiles are 2.3 rounds of the 456 that are resident).
+// the 6.79 TB/s of a plain copy: 8192 x 4096 bfloat16 packed in 19.1 us (0.78),
+// unpacked in 18.5 us (0.80); float32 27.2 us (0.91) and 28.7 us (0.86); rows of
+// 4095 bfloat16 32 and 31 us; 33278 x 512 float32 in both orders 22.5 us (0.67;
+// its 1040 tiles are 2.3 rounds of the 456 that are resident).
 //
-// Sixteen lanes hold one row's block. Where rows start on 16 bytes a lane holds
-// eight neighbouring elements, else every sixteenth one, so that its accesses
-// of two or four bytes still run along the row together with its neighbours'.
+// Sixteen lanes hold one row's block (see column()); where rows do not start on
+// 16 bytes a lane holds every sixteenth element, so that its accesses of two or
+// four bytes still run along the row together with its neighbours'.
 #include <cuda_bf16.h>
 
 #include "s2_internal.h"
@@ -47,10 +48,17 @@ __device__ __forceinline__ float value(const Raw<uint16_t>& r, int i) {
 __device__ __forceinline__ void put(Raw<float>& r, int i, float x) { r.w[i] = __float_as_uint(x); }
 __device__ __forceinline__ void put(Raw<uint16_t>& r, int i, uint16_t x) { r.w[i / 2] |= (uint32_t)x << (16 * (i % 2)); }
 
-// Column of a lane's element i within its block.
-template <bool VEC>
+// Column of a lane's element i within its block, and whether all of a lane's
+// columns lie before `left`. VEC: rows start on 16 bytes, and a lane holds
+// eight neighbours of 16 bits or twice four of 32 bits, so that each 16-byte
+// access of the half-warp is 256 bytes of a row.
+template <typename T, bool VEC>
 __device__ __forceinline__ uint32_t column(uint32_t sub, int i) {
-    return VEC ? sub * kPer + i : sub + i * kLanes;
+    return !VEC ? sub + i * kLanes : sizeof(T) == 2 ? sub * 8 + i : sub * 4 + i % 4 + i / 4 * 64;
+}
+template <typename T>
+__device__ __forceinline__ bool whole(uint32_t sub, int left) {
+    return left > (int)column<T, true>(sub, kPer - 1);
 }
 
 // A lane's elements of the block of a row that begins at p; `left` columns
@@ -58,10 +66,10 @@ __device__ __forceinline__ uint32_t column(uint32_t sub, int i) {
 template <typename T, bool VEC>
 __device__ __forceinline__ Raw<T> load8(const T* p, uint32_t sub, int left) {
     Raw<T> r;
-    if (VEC && left >= (int)(sub + 1) * kPer) {
+    if (VEC && whole<T>(sub, left)) {
 #pragma unroll
         for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-            const uint4 a = ld_stream_u4(reinterpret_cast<const uint4*>(p + sub * kPer) + i);
+            const uint4 a = *reinterpret_cast<const uint4*>(p + column<T, true>(sub, 4 * i));
             r.w[4 * i] = a.x;
             r.w[4 * i + 1] = a.y;
             r.w[4 * i + 2] = a.z;
@@ -73,7 +81,7 @@ __device__ __forceinline__ Raw<T> load8(const T* p, uint32_t sub, int left) {
     for (int i = 0; i < (int)(2 * sizeof(T)); ++i) r.w[i] = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-        if ((int)column<VEC>(sub, i) < left) put(r, i, p[column<VEC>(sub, i)]);
+        if ((int)column<T, VEC>(sub, i) < left) put(r, i, p[column<T, VEC>(sub, i)]);
     return r;
 }
 
@@ -130,21 +138,38 @@ __device__ __forceinline__ uint2 codes8(const Raw<T>& r, uint32_t b, bool specia
 
 __device__ __forceinline__ uint8_t byte_of(uint2 c, int i) { return (uint8_t)((i < 4 ? c.x : c.y) >> (8 * (i % 4))); }
 
-// A lane's codes to the block that begins at p (8-byte aligned).
-template <bool VEC>
+// A lane's codes to the block that begins at p (8-byte aligned), and from there.
+template <typename T, bool VEC>
 __device__ __forceinline__ void store_codes(uint8_t* p, uint2 c, uint32_t sub, int left) {
-    if (VEC && left >= (int)(sub + 1) * kPer) {
-        *reinterpret_cast<uint2*>(p + sub * kPer) = c;
+    if (VEC && whole<T>(sub, left)) {
+        if constexpr (sizeof(T) == 2) {
+            *reinterpret_cast<uint2*>(p + column<T, true>(sub, 0)) = c;
+        } else {
+            *reinterpret_cast<uint32_t*>(p + column<T, true>(sub, 0)) = c.x;
+            *reinterpret_cast<uint32_t*>(p + column<T, true>(sub, 4)) = c.y;
+        }
         return;
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-        if ((int)column<VEC>(sub, i) < left) p[column<VEC>(sub, i)] = byte_of(c, i);
+        if ((int)column<T, VEC>(sub, i) < left) p[column<T, VEC>(sub, i)] = byte_of(c, i);
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ uint2 load_codes(const uint8_t* p, uint32_t sub, int left) {
+    if (VEC && whole<T>(sub, left)) {
+        if constexpr (sizeof(T) == 2) return *reinterpret_cast<const uint2*>(p + column<T, true>(sub, 0));
+        return make_uint2(*reinterpret_cast<const uint32_t*>(p + column<T, true>(sub, 0)),
+                          *reinterpret_cast<const uint32_t*>(p + column<T, true>(sub, 4)));
+    }
+    uint2 c = make_uint2(0, 0);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        if ((int)column<T, VEC>(sub, i) < left) (i < 4 ? c.x : c.y) |= (uint32_t)p[column<T, VEC>(sub, i)] << (8 * (i % 4));
+    return c;
 }
 
-// Blocks of a row in flight per half-warp. 8192 x 4096 bfloat16 with L2 flushed:
-// packing 23 us with two or four, 27 with one; unpacking 21, 21 and 25; rows of
-// 4095 33, 44 and 36 (unpacking).
+// Blocks of a row in flight per half-warp: 8192 x 4096 bfloat16 packed in 19.2 us
+// with two, 20.6 with four; rows of 4095 unpacked in 31 and 40 us.
 constexpr int kItems = 2;
 
 // One half-warp per block of a row, kItems of them in flight.
@@ -181,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) pack_rows_kernel(Pack8Args a) {
             for (int o = kLanes / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
         }
         const uint32_t b = scale_byte(m);
-        store_codes<VEC>(a.codes + row[i] * a.ldc + col[i], codes8(v[i], b, special), sub, left[i]);
+        store_codes<T, VEC>(a.codes + row[i] * a.ldc + col[i], codes8(v[i], b, special), sub, left[i]);
         if (sub == 0 && left[i]) a.scales[first + i] = (uint8_t)b;
     }
 }
@@ -248,7 +273,7 @@ __global__ void __launch_bounds__(kThreads) pack_tiles_kernel(Pack8Args a) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         c[i] = codes8(v[i], b, special);
-        if (i < rvalid) store_codes<VEC>(a.codes + (r0 + i) * a.ldc + tcol * kBlk, c[i], sub, left);
+        if (i < rvalid) store_codes<T, VEC>(a.codes + (r0 + i) * a.ldc + tcol * kBlk, c[i], sub, left);
     }
     if (threadIdx.x == 0) {
         a.scales[(uint64_t)trow * a.nblk + tcol] = (uint8_t)b;
@@ -262,7 +287,7 @@ __global__ void __launch_bounds__(kThreads) pack_tiles_kernel(Pack8Args a) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         const uint2 w = j < 4 ? make_uint2(c[j].x, c[j + 4].x) : make_uint2(c[j - 4].y, c[j].y);
-        *reinterpret_cast<uint2*>(turned + turned_at(column<VEC>(sub, j), grp / 2) + grp % 2 * 8) = w;
+        *reinterpret_cast<uint2*>(turned + turned_at(column<T, VEC>(sub, j), grp / 2) + grp % 2 * 8) = w;
     }
     __syncthreads();
     const int down = (int)min((uint64_t)kBlk, a.rows - (uint64_t)trow * kBlk);
@@ -311,14 +336,7 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(Unpack8Args a) {
         col[i] = blk * kBlk;
         left[i] = first + i < a.items ? (int)(a.cols - col[i]) : 0;
         const uint8_t* p = a.codes + row[i] * a.ldc + col[i];
-        c[i] = make_uint2(0, 0);
-        if (VEC && left[i] >= (int)(sub + 1) * kPer) {
-            c[i] = *reinterpret_cast<const uint2*>(p + sub * kPer);
-        } else {
-#pragma unroll
-            for (int j = 0; j < kPer; ++j)
-                if ((int)column<VEC>(sub, j) < left[i]) (j < 4 ? c[i].x : c[i].y) |= (uint32_t)p[column<VEC>(sub, j)] << (8 * (j % 4));
-        }
+        c[i] = load_codes<T, VEC>(p, sub, left[i]);
         b[i] = left[i] ? a.scales[(row[i] >> a.row_shift) * a.nblk + blk] : 127u;
         if (++blk == a.nblk) {
             blk = 0;
@@ -337,27 +355,26 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(Unpack8Args a) {
             f[2 * j + 1] = d.y * s;
         }
         T* o = out + row[i] * a.ldo + col[i];
-        const bool whole = VEC && left[i] >= (int)(sub + 1) * kPer;
+        const bool all = VEC && whole<T>(sub, left[i]);
         if constexpr (sizeof(T) == 4) {
-            if (whole) {
-                float4* q = reinterpret_cast<float4*>(o + sub * kPer);
-                q[0] = make_float4(f[0], f[1], f[2], f[3]);
-                q[1] = make_float4(f[4], f[5], f[6], f[7]);
+            if (all) {
+                *reinterpret_cast<float4*>(o + column<T, true>(sub, 0)) = make_float4(f[0], f[1], f[2], f[3]);
+                *reinterpret_cast<float4*>(o + column<T, true>(sub, 4)) = make_float4(f[4], f[5], f[6], f[7]);
             } else {
 #pragma unroll
                 for (int j = 0; j < kPer; ++j)
-                    if ((int)column<VEC>(sub, j) < left[i]) o[column<VEC>(sub, j)] = f[j];
+                    if ((int)column<T, VEC>(sub, j) < left[i]) o[column<T, VEC>(sub, j)] = f[j];
             }
         } else {
             uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) w[j] = bf16x2(f[2 * j], f[2 * j + 1]);
-            if (whole) {
-                *reinterpret_cast<uint4*>(o + sub * kPer) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (all) {
+                *reinterpret_cast<uint4*>(o + column<T, true>(sub, 0)) = make_uint4(w[0], w[1], w[2], w[3]);
             } else {
 #pragma unroll
                 for (int j = 0; j < kPer; ++j)
-                    if ((int)column<VEC>(sub, j) < left[i]) o[column<VEC>(sub, j)] = (uint16_t)(w[j / 2] >> (16 * (j % 2)));
+                    if ((int)column<T, VEC>(sub, j) < left[i]) o[column<T, VEC>(sub, j)] = (uint16_t)(w[j / 2] >> (16 * (j % 2)));
             }
         }
     }
