@@ -581,6 +581,7 @@ Plan choose(uint32_t M, uint32_t N, uint32_t nblk, int sms, int pairs) {
             if (ns < best.ns) best = {nt, split, false, ns};
         }
     }
+    if (M <= 64) return best;  // pairs' tiles are at least 160 tokens wide
     const uint64_t pf = (N + 2 * kBF - 1) / (2 * kBF);
     for (int nt = kMaxNT; nt >= 160; nt -= 32) {
         const uint64_t rounds = (pf * ((M + nt - 1) / nt) + pairs - 1) / pairs;
