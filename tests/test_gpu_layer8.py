@@ -515,6 +515,50 @@ def test_wgrad_against_differences():
     assert abs((loss[0] - loss[1]) - (dw.double().cpu().numpy() * step).sum()) <= room
 
 
+@pytest.mark.parametrize("off", [0, 1, 3, 8])
+@pytest.mark.parametrize("T", [1, 2, 9])
+def test_wgrad_one_row_anywhere(T, off):
+    check_wgrad(T, 77, 140, dy_off=off)
+
+
+def test_offsets_past_32_bits():
+    """Rows so far apart that every array's last offset passes 2^32 elements or bytes."""
+    far = (1 << 31) + 16
+    T, N, K = 3, 150, 200
+    x, w, g = make(T, K, 1), make(N, K, 2), make(T, N, 3, "bf16")
+    wide = torch.empty((T - 1) * far + K, dtype=torch.float32, device=DEV).as_strided((T, K), (far, 1))
+    wide.copy_(x)
+    codes = torch.empty((T - 1) * far + K, dtype=torch.uint8, device=DEV).as_strided((T, K), (far, 1))
+    scales = torch.empty((T, 2), dtype=torch.uint8, device=DEV)
+    s2.s2_pack8(wide, codes, scales)
+    want, want_s = ref.pack(x.double().numpy(), False)
+    np.testing.assert_array_equal(codes.cpu().numpy(), want)
+    np.testing.assert_array_equal(scales.cpu().numpy(), want_s)
+    xv = ref.unpack(want, want_s, False)
+    s2.s2_unpack8(codes, scales, wide)
+    np.testing.assert_array_equal(wide.double().cpu().numpy(), xv)
+    del wide
+    wc, ws, wv = packed(w, "tiles")
+    y = torch.empty((T - 1) * far + N, dtype=torch.bfloat16, device=DEV).as_strided((T, N), (far, 1))
+    y32 = torch.empty((T, N), device=DEV)
+    s2.s2_matmul8(codes, scales, wc, ws, y)
+    s2.s2_matmul8(codes, scales, wc, ws, y32)
+    assert torch.equal(y, y32.to(torch.bfloat16))
+    assert (np.abs(y32.double().cpu().numpy() - xv @ wv.T) <= bound(K, np.abs(xv) @ np.abs(wv).T)).all()
+    y.copy_(g)
+    dw = torch.empty((N, K), device=DEV)
+    for dy in (y, torch.empty((T - 1) * (far + 1) + N, dtype=torch.bfloat16, device=DEV).as_strided((T, N), (far + 1, 1))):
+        dy.copy_(g)
+        s2.s2_wgrad8(dy, codes, scales, dw)
+        yv = g.double().numpy()
+        tol = (17 / 16 * T + 27) * 2.0 ** -23 * (np.abs(yv).T @ np.abs(xv)) + 2.0 ** -149
+        assert (np.abs(dw.double().cpu().numpy() - yv.T @ xv) <= tol).all()
+        del dy
+    far_dw = torch.empty((N - 1) * (1 << 25) + K, device=DEV).as_strided((N, K), (1 << 25, 1))
+    s2.s2_wgrad8(g.to(DEV), codes, scales, far_dw)
+    assert torch.equal(far_dw, dw)
+
+
 def test_binding_refusals():
     codes, scales = s2.alloc_pack8(8, 64)
     x = torch.zeros((8, 64), device=DEV)
