@@ -15,7 +15,7 @@
 // pipeline's fill and 16.8 MB that come from L2); 24 tokens by 267735 x 1024
 // into float32 52.7 us, 0.84 of a copy's rate for its 300 MB; 500 x 2000 x 1024
 // 5.7 us; 8192 x 4096 x 4096 97 us in a long loop (2.8 PFLOP/s, power-capped)
-// and 80 us for ten in a row (3.4); 2048 x 267735 x 1024 into bfloat16 550 us.
+// and 80 us for ten in a row (3.4); 2048 x 267735 x 1024 into bfloat16 540 us.
 #include "s2_internal.h"
 #include "s2_tc.cuh"
 
@@ -30,6 +30,18 @@ constexpr int kGroup = 4;                // K blocks whose scale bytes share a 3
 constexpr int kWarps = 10;               // 0-3 store, 4-7 scales, 8 copies, 9 products
 constexpr uint32_t kABytes = kBF * kBK;  // W part of a stage
 
+// The tensor cores cut off what they add to a float32 sum, so a long sum drifts
+// towards zero: by 4e-7 of itself at K = 4096, 3e-6 at 16384 and 1.3e-5 at
+// 65536. A float32 result is therefore taken in chunks of 32 blocks of K (4e-7
+// at any length; a float32 product of the unpacked values is off by 3.5e-7 and
+// 8e-7 at the longer two), and the sum of chunks stays in tensor memory beside
+// the two accumulators. That leaves a pair 160 tokens a tile where it has 224:
+// 2048 x 1024 x 267735 505 -> 513 us, 8192 x 4096 x 16384 336 -> 369 us. Adding
+// to Y in global memory kept the 224 and took 592 and 367. A bfloat16 result
+// drops all of it in its own rounding and is taken in one chunk.
+constexpr uint32_t kChunk = 32;
+static_assert(kChunk % kGroup == 0, "chunks end between two scale words");
+
 struct Args {
     const uint8_t *xs, *ws;
     void* y;
@@ -43,7 +55,7 @@ struct Args {
     uint32_t* faults;
 };
 
-template <int NT>
+template <int NT, bool CHUNKS>
 struct Shape {
     static constexpr uint32_t kStage = kABytes + NT * kBK;
     static constexpr int kStages = (int)(200 * 1024 / kStage) < 10 ? (int)(200 * 1024 / kStage) : 10;
@@ -51,7 +63,8 @@ struct Shape {
     static constexpr int kScaleB = (NT + 127) / 128 * 4;    // columns of X's scales, in fours
     static constexpr int kScaleCols = 4 + kScaleB;          // columns of one group's scales
     static constexpr int kRing = 2;                         // groups of scales in tensor memory
-    static constexpr uint32_t kUsed = kAcc * NT + kRing * kScaleCols;
+    static constexpr uint32_t kSumAt = kAcc * NT + kRing * kScaleCols;
+    static constexpr uint32_t kUsed = kSumAt + (CHUNKS ? NT : 0);
     static constexpr uint32_t kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
     static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
     static_assert(kUsed <= 512, "tensor memory");
@@ -87,6 +100,15 @@ __device__ __forceinline__ void store16(const Args& a, uint32_t t, uint32_t f, c
     }
 }
 
+// Adds the sum of the chunks before to 16 columns of an accumulator that are being read.
+__device__ __forceinline__ void add_sum16(uint32_t sum, uint32_t* r) {
+    uint32_t q[16];
+    tmem_ld16(sum, q);
+    wait_ld();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(q[j]) + __uint_as_float(r[j]));
+}
+
 // The scale bytes of K blocks kb..kb+3 of one row as a word; blocks past the
 // end repeat 1.0, which no product uses. Words: rows of bytes start on four
 // bytes and their number is a multiple of four.
@@ -101,10 +123,10 @@ __device__ __forceinline__ bool in_words(const uint8_t* s, uint32_t nblk) {
     return nblk % kGroup == 0 && reinterpret_cast<uintptr_t>(s) % kGroup == 0;
 }
 
-template <int NT>
+template <int NT, bool CHUNKS>
 __global__ void __launch_bounds__(kWarps * 32, 1)
     matmul8_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, const Args a) {
-    using S = Shape<NT>;
+    using S = Shape<NT, CHUNKS>;
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t bars[2 * S::kStages + 2 * S::kRing + 2 * S::kAcc + 1];
     __shared__ uint32_t tmem_slot;
@@ -190,32 +212,35 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             const uint32_t idesc = (uint32_t)(NT / 8) << 17 | 1u << 23 | (uint32_t)(kBF / 16) << 24;
             uint32_t it = 0, grp = 0, n = 0;
             bool ok = true;
-            for (uint32_t tile = first; ok && tile < tiles; tile += step, ++n) {
-                const int buf = n % S::kAcc;
-                if (!(ok = bar_wait(acc_empty(buf), ((n / S::kAcc) & 1) ^ 1, wt))) break;
-                fence_after();
-                const uint32_t d = tmem + buf * NT;
-                for (uint32_t kb = kb0; kb < kb1; ++kb, ++it) {
-                    const uint32_t i = kb - kb0;
-                    const uint32_t sf = tmem + S::kAcc * NT + (grp % S::kRing) * S::kScaleCols;
-                    if (i % kGroup == 0 && !(ok = bar_wait(sf_full(grp % S::kRing), (grp / S::kRing) & 1, wt))) break;
-                    const int s = it % S::kStages;
-                    if (!(ok = bar_wait(full(s), (it / S::kStages) & 1, wt))) break;
+            for (uint32_t tile = first; ok && tile < tiles; tile += step) {
+                for (uint32_t from = kb0, end; ok && from < kb1; from = end, ++n) {
+                    const int buf = n % S::kAcc;
+                    if (!(ok = bar_wait(acc_empty(buf), ((n / S::kAcc) & 1) ^ 1, wt))) break;
                     fence_after();
-                    const uint64_t ad = smem_desc(base + s * S::kStage, 16, 1024);
-                    const uint64_t bd = smem_desc(base + s * S::kStage + kABytes, 16, 1024);
-                    const uint32_t id = idesc | (i % kGroup) << 4 | (i % kGroup) << 29;
-                    const bool last = i % kGroup == kGroup - 1 || kb + 1 == kb1;
-                    if (leader) {
+                    const uint32_t d = tmem + buf * NT;
+                    end = CHUNKS && kb1 - from > kChunk ? from + kChunk : kb1;
+                    for (uint32_t kb = from; kb < end; ++kb, ++it) {
+                        const uint32_t i = (kb - from) % kGroup;
+                        const uint32_t sf = tmem + S::kAcc * NT + (grp % S::kRing) * S::kScaleCols;
+                        if (i == 0 && !(ok = bar_wait(sf_full(grp % S::kRing), (grp / S::kRing) & 1, wt))) break;
+                        const int s = it % S::kStages;
+                        if (!(ok = bar_wait(full(s), (it / S::kStages) & 1, wt))) break;
+                        fence_after();
+                        const uint64_t ad = smem_desc(base + s * S::kStage, 16, 1024);
+                        const uint64_t bd = smem_desc(base + s * S::kStage + kABytes, 16, 1024);
+                        const uint32_t id = idesc | i << 4 | i << 29;
+                        const bool last = i == kGroup - 1 || kb + 1 == end;
+                        if (leader) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)  // 32 bytes of K each
-                            mma_mx8(d, ad + 2 * j, bd + 2 * j, id, sf, sf + 4, i > 0 || j > 0);
-                        mma_commit(empty(s));
-                        if (last) mma_commit(sf_empty(grp % S::kRing));
+                            for (int j = 0; j < 4; ++j)  // 32 bytes of K each
+                                mma_mx8(d, ad + 2 * j, bd + 2 * j, id, sf, sf + 4, kb > from || j > 0);
+                            mma_commit(empty(s));
+                            if (last) mma_commit(sf_empty(grp % S::kRing));
+                        }
+                        if (last) ++grp;
                     }
-                    if (last) ++grp;
+                    if (ok && leader) mma_commit(acc_full(buf));
                 }
-                if (ok && leader) mma_commit(acc_full(buf));
             }
             if (dead && leader) {  // products in flight still read this block's memory
                 mma_commit(drain);
@@ -258,20 +283,26 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             }
         }
     } else {
-        uint32_t n = 0;
-        for (uint32_t tile = first; tile < tiles; tile += step, ++n) {
+        uint32_t n = 0, kb = kb0;  // kb: where the chunk begins
+        const uint32_t mine = tmem + ((uint32_t)warp << 21);
+        for (uint32_t tile = first; tile < tiles; ++n) {
             const int buf = n % S::kAcc;
             if (!bar_wait(acc_full(buf), (n / S::kAcc) & 1, wt)) break;
             fence_after();
             uint32_t f0, t0;
             place(tile, f0, t0);
             const uint32_t f = f0 + warp * 32 + lane;
+            const bool more = CHUNKS && kb1 - kb > kChunk;
 #pragma unroll 1
             for (int c = 0; c < NT; c += 16) {
                 uint32_t r[16];
-                tmem_ld16(tmem + ((uint32_t)warp << 21) + buf * NT + c, r);
+                tmem_ld16(mine + buf * NT + c, r);
+                if (CHUNKS && kb > kb0) add_sum16(mine + S::kSumAt + c, r);
                 wait_ld();
-                if (a.split > 1) {
+                if (more) {
+                    tmem_st16(mine + S::kSumAt + c, r);
+                    wait_st();
+                } else if (a.split > 1) {
                     // this block's part of the sums, where the stages were
                     float* part = reinterpret_cast<float*>(raw + (base - smem_u32(raw)));
 #pragma unroll
@@ -283,6 +314,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive(acc_empty(buf));
+            kb += kChunk;
+            if (!more) {
+                tile += step;
+                kb = kb0;
+            }
         }
     }
 
@@ -310,9 +346,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     if (warp == 9) tmem_free(tmem, S::kCols);
 }
 
-template <int NT>
+template <int NT, bool CHUNKS>
 cudaError_t launch(const Matmul8Args& m, Args a, cudaStream_t s) {
-    using S = Shape<NT>;
+    using S = Shape<NT, CHUNKS>;
     DeviceInfo di{};
     cudaError_t e = device_info(&di);
     if (e != cudaSuccess) return e;
@@ -327,7 +363,7 @@ cudaError_t launch(const Matmul8Args& m, Args a, cudaStream_t s) {
     if (tiles > 0x7fffffffull) return cudaErrorInvalidValue;
     // the operand with the fewer bytes is the one that tiles in a row re-read
     a.tokens_inner = m.M <= m.N;
-    auto kernel = matmul8_kernel<NT>;
+    auto kernel = matmul8_kernel<NT, CHUNKS>;
     e = allow_smem(reinterpret_cast<const void*>(kernel), S::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
@@ -361,25 +397,28 @@ cudaError_t launch(const Matmul8Args& m, Args a, cudaStream_t s) {
 // into bfloat16 and 533 us into twice the bytes in as many requests, 371 us
 // without stores; turning bfloat16 through shared memory for longer requests
 // took more time than it saved.
-constexpr int kMaxNT = 224;
-
+template <bool CHUNKS>
 struct Pair {
+    static constexpr int kMaxNT = CHUNKS ? 160 : 224;    // the sum of chunks takes as many columns again
     static constexpr uint32_t kHalf = kMaxNT / 2 * kBK;  // X part of a stage
     static constexpr uint32_t kStage = kABytes + kHalf;
-    static constexpr int kStages = 7;
+    static constexpr int kStages = CHUNKS ? 8 : 7;
     static constexpr int kAcc = 2;
     static constexpr int kScaleCols = 12;  // 4 of W, 8 of X
-    static constexpr int kRing = 4;
-    static constexpr uint32_t kScaleAt = kAcc * kMaxNT;
+    static constexpr int kRing = CHUNKS ? 2 : 4;
+    static constexpr uint32_t kSumAt = kAcc * kMaxNT;
+    static constexpr uint32_t kScaleAt = kSumAt + (CHUNKS ? kMaxNT : 0);
     static constexpr uint32_t kCols = 512;
     static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
     static_assert(kScaleAt + kRing * kScaleCols <= kCols, "tensor memory");
+    static_assert(kSmem <= 227 * 1024 - 1024, "shared memory");
     static_assert(kHalf % 1024 == 0, "stages start on the swizzle's period");
 };
 
+template <bool CHUNKS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWarps * 32, 1)
     matmul8_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, const Args a) {
-    using S = Pair;
+    using S = Pair<CHUNKS>;
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t bars[2 * S::kStages + 2 * S::kRing + 2 * S::kAcc + 1];
     __shared__ uint32_t tmem_slot;
@@ -459,30 +498,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWarps * 32, 1)
             Slot<S::kAcc> acc;
             bool ok = true;
             for (uint32_t tile = first; ok && tile < tiles; tile += step) {
-                if (!(ok = bar_wait(acc_empty + 8 * acc.at, acc.phase ^ 1, wt))) break;
-                fence_after();
-                const uint32_t d = tmem + acc.at * kMaxNT;
-                for (uint32_t kb = 0; kb < a.nblk; ++kb) {
-                    const uint32_t i = kb % kGroup;
-                    if (i == 0 && !(ok = bar_wait(sf_full + 8 * g.at, g.phase, wt))) break;
-                    if (!(ok = bar_wait(full + 8 * s.at, s.phase, wt))) break;
+                for (uint32_t from = 0, end; ok && from < a.nblk; from = end) {
+                    if (!(ok = bar_wait(acc_empty + 8 * acc.at, acc.phase ^ 1, wt))) break;
                     fence_after();
-                    const uint64_t ad = smem_desc(base + s.at * S::kStage, 16, 1024);
-                    const uint64_t bd = smem_desc(base + s.at * S::kStage + kABytes, 16, 1024);
-                    const uint32_t id = idesc | i << 4 | i << 29, sf = tmem + S::kScaleAt + g.at * S::kScaleCols;
-                    const bool last = i == kGroup - 1 || kb + 1 == a.nblk;
-                    if (leader) {
+                    const uint32_t d = tmem + acc.at * S::kMaxNT;
+                    end = CHUNKS && a.nblk - from > kChunk ? from + kChunk : a.nblk;
+                    for (uint32_t kb = from; kb < end; ++kb) {
+                        const uint32_t i = kb % kGroup;
+                        if (i == 0 && !(ok = bar_wait(sf_full + 8 * g.at, g.phase, wt))) break;
+                        if (!(ok = bar_wait(full + 8 * s.at, s.phase, wt))) break;
+                        fence_after();
+                        const uint64_t ad = smem_desc(base + s.at * S::kStage, 16, 1024);
+                        const uint64_t bd = smem_desc(base + s.at * S::kStage + kABytes, 16, 1024);
+                        const uint32_t id = idesc | i << 4 | i << 29, sf = tmem + S::kScaleAt + g.at * S::kScaleCols;
+                        const bool last = i == kGroup - 1 || kb + 1 == end;
+                        if (leader) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            mma_mx8_pair(d, ad + 2 * j, bd + 2 * j, id, sf, sf + 4, kb > 0 || j > 0);
-                        mma_commit_pair(empty + 8 * s.at);
-                        if (last) mma_commit_pair(sf_empty + 8 * g.at);
+                            for (int j = 0; j < 4; ++j)
+                                mma_mx8_pair(d, ad + 2 * j, bd + 2 * j, id, sf, sf + 4, kb > from || j > 0);
+                            mma_commit_pair(empty + 8 * s.at);
+                            if (last) mma_commit_pair(sf_empty + 8 * g.at);
+                        }
+                        if (last) g.next();
+                        s.next();
                     }
-                    if (last) g.next();
-                    s.next();
+                    if (ok && leader) mma_commit_pair(acc_full + 8 * acc.at);
+                    acc.next();
                 }
-                if (ok && leader) mma_commit_pair(acc_full + 8 * acc.at);
-                acc.next();
             }
             if (dead && leader) {
                 mma_commit_pair(drain);
@@ -525,23 +567,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWarps * 32, 1)
         }
     } else {
         Slot<S::kAcc> acc;
-        for (uint32_t tile = first; tile < tiles; tile += step) {
+        uint32_t kb = 0;  // where the chunk begins
+        const uint32_t mine = tmem + ((uint32_t)warp << 21);
+        for (uint32_t tile = first; tile < tiles;) {
             if (!bar_wait(acc_full + 8 * acc.at, acc.phase, wt)) break;
             fence_after();
             uint32_t f0, t0;
             place(tile, f0, t0);
             const uint32_t f = f0 + warp * 32 + lane;
+            const bool more = CHUNKS && a.nblk - kb > kChunk;
 #pragma unroll 1
             for (uint32_t c = 0; c < a.nt; c += 16) {
                 uint32_t r[16];
-                tmem_ld16(tmem + ((uint32_t)warp << 21) + acc.at * kMaxNT + c, r);
+                tmem_ld16(mine + acc.at * S::kMaxNT + c, r);
+                if (CHUNKS && kb > 0) add_sum16(mine + S::kSumAt + c, r);
                 wait_ld();
-                if (f < a.N) store16(a, t0 + c, f, r);
+                if (more) {
+                    tmem_st16(mine + S::kSumAt + c, r);
+                    wait_st();
+                } else if (f < a.N) {
+                    store16(a, t0 + c, f, r);
+                }
             }
             fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive_first(acc_empty + 8 * acc.at);
             acc.next();
+            kb += kChunk;
+            if (!more) {
+                tile += step;
+                kb = 0;
+            }
         }
     }
 
@@ -567,11 +623,11 @@ inline uint64_t rounds_ns(uint64_t rounds, uint64_t stages_ns, uint64_t store_ns
     return (rounds - 1) * (stages_ns > store_ns ? stages_ns : store_ns) + stages_ns + store_ns;
 }
 
-Plan choose(uint32_t M, uint32_t N, uint32_t nblk, int sms, int pairs) {
+Plan choose(uint32_t M, uint32_t N, uint32_t nblk, bool chunks, int sms, int pairs) {
     Plan best{16, 1, false, ~0ull};
     const uint64_t tf = (N + kBF - 1) / kBF;
     for (int nt : {16, 32, 64, 128, 224}) {
-        if (nt > 16 && (uint32_t)nt >= 2 * M) break;
+        if ((nt > 16 && (uint32_t)nt >= 2 * M) || (chunks && nt > 128)) break;
         const uint64_t tiles = tf * ((M + nt - 1) / nt);
         for (int split = 1; split <= 8 && (uint32_t)split <= nblk; split *= 2) {
             // clusters of four and eight do not fill every SM
@@ -583,7 +639,7 @@ Plan choose(uint32_t M, uint32_t N, uint32_t nblk, int sms, int pairs) {
     }
     if (M <= 64) return best;  // pairs' tiles are at least 160 tokens wide
     const uint64_t pf = (N + 2 * kBF - 1) / (2 * kBF);
-    for (int nt = kMaxNT; nt >= 160; nt -= 32) {
+    for (int nt = chunks ? Pair<true>::kMaxNT : Pair<false>::kMaxNT; nt >= 160; nt -= 32) {
         const uint64_t rounds = (pf * ((M + nt - 1) / nt) + pairs - 1) / pairs;
         const uint64_t ns = 4500 + rounds_ns(rounds, (uint64_t)nblk * (60 + nt), 9 * nt);
         if (ns < best.ns) best = {nt, 1, true, ns};
@@ -591,6 +647,7 @@ Plan choose(uint32_t M, uint32_t N, uint32_t nblk, int sms, int pairs) {
     return best;
 }
 
+template <bool CHUNKS>
 cudaError_t launch_pair(const Matmul8Args& m, Args a, int pairs, cudaStream_t s) {
     a.tiles_f = (m.N + 2 * kBF - 1) / (2 * kBF);
     a.tiles_t = (m.M + a.nt - 1) / a.nt;
@@ -603,8 +660,27 @@ cudaError_t launch_pair(const Matmul8Args& m, Args a, int pairs, cudaStream_t s)
     e = make_map(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, m.x, m.K, m.M, m.ldx, kBK, a.nt / 2);
     if (e != cudaSuccess) return e;
     const uint32_t grid = 2 * (uint32_t)(tiles < (uint64_t)pairs ? tiles : pairs);
-    matmul8_pair_kernel<<<grid, kWarps * 32, Pair::kSmem, s>>>(wmap, xmap, a);
+    matmul8_pair_kernel<CHUNKS><<<grid, kWarps * 32, Pair<CHUNKS>::kSmem, s>>>(wmap, xmap, a);
     return cudaGetLastError();
+}
+
+template <bool CHUNKS>
+cudaError_t plan_and_launch(const Matmul8Args& m, Args a, int sms, cudaStream_t s) {
+    int pairs = 0;
+    const cudaError_t e = max_pairs(reinterpret_cast<const void*>(matmul8_pair_kernel<CHUNKS>), kWarps * 32, Pair<CHUNKS>::kSmem, &pairs);
+    if (e != cudaSuccess) return e;
+    const Plan plan = choose(m.M, m.N, a.nblk, CHUNKS, sms, pairs);
+    a.split = (uint32_t)plan.split;
+    a.nt = (uint32_t)plan.nt;
+    if (plan.pair) return launch_pair<CHUNKS>(m, a, pairs, s);
+    switch (plan.nt) {
+        case 16: return launch<16, CHUNKS>(m, a, s);
+        case 32: return launch<32, CHUNKS>(m, a, s);
+        case 64: return launch<64, CHUNKS>(m, a, s);
+        case 128: return launch<128, CHUNKS>(m, a, s);
+    }
+    if constexpr (CHUNKS) return cudaErrorInvalidValue;  // (not chosen: no room for the sum of chunks)
+    else return launch<224, false>(m, a, s);
 }
 
 }  // namespace
@@ -625,20 +701,8 @@ cudaError_t launch_matmul8(const Matmul8Args& m, cudaStream_t s) {
     DeviceInfo di{};
     e = device_info(&di);
     if (e != cudaSuccess) return e;
-    int pairs = 0;
-    e = max_pairs(reinterpret_cast<const void*>(matmul8_pair_kernel), kWarps * 32, Pair::kSmem, &pairs);
-    if (e != cudaSuccess) return e;
-    const Plan plan = choose(m.M, m.N, a.nblk, di.sms, pairs);
-    a.split = (uint32_t)plan.split;
-    a.nt = (uint32_t)plan.nt;
-    if (plan.pair) return launch_pair(m, a, pairs, s);
-    switch (plan.nt) {
-        case 16: return launch<16>(m, a, s);
-        case 32: return launch<32>(m, a, s);
-        case 64: return launch<64>(m, a, s);
-        case 128: return launch<128>(m, a, s);
-        default: return launch<224>(m, a, s);
-    }
+    if (m.dtype == 0 && a.nblk > kChunk) return plan_and_launch<true>(m, a, di.sms, s);
+    return plan_and_launch<false>(m, a, di.sms, s);
 }
 
 }  // namespace s2

@@ -217,6 +217,41 @@ def test_matmul_many_tiles():
     check_matmul(9001, 1030, 700, "f32", "rows", kind="mixed")
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 256, 66000), (40, 700, 33001), (64, 20000, 8200), (300, 1000, 65536),
+                                   (1100, 1100, 65536), (700, 1601, 65000)])
+def test_matmul_long_sums(M, N, K):
+    """A long float32 sum loses no more than one of 4096 products: each of its 128 additions of 32
+    products drops on average half a unit, at most 2^-24 of the sum so far, which is at most the
+    chunk's own on average; the chunks and a split sum's parts are added with rounding (another 2^-24
+    each, of random sign). A bfloat16 result is one sum: 2^-24 for each of its additions, and its own
+    rounding, half of 2^-8."""
+    codes, scales, values = [], [], []
+    for rows, lay, step in ((M, "rows", 1 + M // 40), (N, "tiles", 1 + N // 40)):
+        g = torch.Generator(device=DEV).manual_seed(rows + K)
+        c, b = s2.alloc_pack8(rows, K, lay)
+        s2.s2_pack8(torch.randn((rows, K), device=DEV, generator=g), c, b, lay)
+        some = torch.arange(0, rows, step)
+        codes.append(c)
+        scales.append(b)
+        of = some // 128 if lay == "tiles" else some
+        v = ref.VALUES[c[some].cpu().numpy()] * ref.spread(b[of].cpu().numpy(), len(some), K, False)
+        values.append((some, v))
+    (i, xv), (j, wv) = values
+    want = xv @ wv.T
+    for dtype, tol in (("f32", (128 + (K / 4096 + 9) ** 0.5) * 2.0 ** -24), ("bf16", K / 32 * 2.0 ** -24 + 2.0 ** -9)):
+        y = torch.full((M, N + 1), 3.0, dtype=DT[dtype], device=DEV)
+        s2.s2_matmul8(codes[0], scales[0], codes[1], scales[1], y[:, :N])
+        got = y.double().cpu().numpy()
+        assert (got[:, N] == 3.0).all()
+        err = np.linalg.norm(got[np.ix_(i.numpy(), j.numpy())] - want) / np.linalg.norm(want)
+        assert err <= tol, (dtype, err)
+        again = torch.empty((M, N), dtype=DT[dtype], device=DEV)
+        for _ in range(5):
+            s2.s2_matmul8(codes[0], scales[0], codes[1], scales[1], again)
+            assert torch.equal(again, y[:, :N])
+    assert s2.s2_wait_faults() == 0
+
+
 def test_matmul_empty():
     codes = torch.zeros((4, 16), dtype=torch.uint8, device=DEV)
     none = codes[:, :0]
