@@ -11,12 +11,13 @@
 // stores to Y run along its rows whatever its alignment, and few tokens cost a
 // small NT instead of an idle part of the tile.
 //
-// Measured: one token by 4096 x 4096 5.4 us in a CUDA graph (a launch, the
+// Measured: one token by 4096 x 4096 5.1 us in a CUDA graph (a launch, the
 // pipeline's fill and 16.8 MB that come from L2); 24 tokens by 267735 x 1024
-// into float32 52.7 us, 0.84 of a copy's rate for its 300 MB; 500 x 2000 x 1024
-// 5.7 us; 8192 x 4096 x 4096 97 us in a long loop (2.8 PFLOP/s, power-capped)
+// into float32 50.0 us, 0.88 of a copy's rate for its 300 MB; 500 x 2000 x 1024
+// 4.8 us; 8192 x 4096 x 4096 96 us in a long loop (2.8 PFLOP/s, power-capped)
 // and 80 us for ten in a row (3.4); 2048 x 267735 x 1024 into bfloat16 540 us.
 #include "s2_internal.h"
+#include "s2_launch.cuh"
 #include "s2_tc.cuh"
 
 namespace s2 {
@@ -113,10 +114,10 @@ __device__ __forceinline__ void add_sum16(uint32_t sum, uint32_t* r) {
 // end repeat 1.0, which no product uses. Words: rows of bytes start on four
 // bytes and their number is a multiple of four.
 __device__ __forceinline__ uint32_t scale_word(const uint8_t* s, uint32_t kb, uint32_t nblk, bool words) {
-    if (words) return __ldg(reinterpret_cast<const uint32_t*>(s + kb));
+    if (words) return *reinterpret_cast<const uint32_t*>(s + kb);
     uint32_t w = 0;
 #pragma unroll
-    for (int i = 0; i < kGroup; ++i) w |= (kb + i < nblk ? (uint32_t)__ldg(s + kb + i) : 127u) << (8 * i);
+    for (int i = 0; i < kGroup; ++i) w |= (kb + i < nblk ? (uint32_t)s[kb + i] : 127u) << (8 * i);
     return w;
 }
 __device__ __forceinline__ bool in_words(const uint8_t* s, uint32_t nblk) {
@@ -168,6 +169,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     fence_before();
     __syncthreads();
     fence_after();
+    stream_order();
     const uint32_t tmem = tmem_slot;
     const Wait wt{&dead, a.faults};
 
@@ -366,18 +368,8 @@ cudaError_t launch(const Matmul8Args& m, Args a, cudaStream_t s) {
     auto kernel = matmul8_kernel<NT, CHUNKS>;
     e = allow_smem(reinterpret_cast<const void*>(kernel), S::kSmem);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(a.split > 1 ? tiles * a.split : tiles < (uint64_t)di.sms ? tiles : di.sms));
-    cfg.blockDim = dim3(kWarps * 32);
-    cfg.dynamicSmemBytes = S::kSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = a.split;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = a.split > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, a);
+    const uint32_t grid = (uint32_t)(a.split > 1 ? tiles * a.split : tiles < (uint64_t)di.sms ? tiles : di.sms);
+    return launch_early(kernel, grid, kWarps * 32, S::kSmem, a.split > 1 ? a.split : 0, s, wmap, xmap, a);
 }
 
 // ---- a pair of blocks per tile ---------------------------------------------------
@@ -453,6 +445,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWarps * 32, 1)
     fence_before();
     cluster_sync();
     fence_after();
+    stream_order();
     const uint32_t tmem = tmem_slot;
     const Wait wt{&dead, a.faults};
     const uint32_t first = blockIdx.x / 2, step = gridDim.x / 2, tiles = a.tiles_f * a.tiles_t;
@@ -660,8 +653,7 @@ cudaError_t launch_pair(const Matmul8Args& m, Args a, int pairs, cudaStream_t s)
     e = make_map(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, m.x, m.K, m.M, m.ldx, kBK, a.nt / 2);
     if (e != cudaSuccess) return e;
     const uint32_t grid = 2 * (uint32_t)(tiles < (uint64_t)pairs ? tiles : pairs);
-    matmul8_pair_kernel<CHUNKS><<<grid, kWarps * 32, Pair<CHUNKS>::kSmem, s>>>(wmap, xmap, a);
-    return cudaGetLastError();
+    return launch_early(matmul8_pair_kernel<CHUNKS>, grid, kWarps * 32, Pair<CHUNKS>::kSmem, 0, s, wmap, xmap, a);
 }
 
 template <bool CHUNKS>

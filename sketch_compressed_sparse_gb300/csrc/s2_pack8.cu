@@ -13,9 +13,9 @@
 // They come near it only with few instructions per element, so the special
 // numbers cost nothing where there are none: maxima ignore NaN, and only a
 // block whose maximum is infinite goes through its elements again. Measured, of
-// the 6.79 TB/s of a plain copy: 8192 x 4096 bfloat16 packed in 19.1 us (0.78),
-// unpacked in 18.5 us (0.80); float32 27.2 us (0.91) and 28.7 us (0.86); rows of
-// 4095 bfloat16 32 and 31 us; 33278 x 512 float32 in both orders 22.5 us (0.67;
+// the 6.79 TB/s of a plain copy: 8192 x 4096 bfloat16 packed in 17.6 us (0.85),
+// unpacked in 17.0 us (0.88); float32 25.2 us (0.98) and 26.0 us (0.95); rows of
+// 4095 bfloat16 30 and 29 us; 33278 x 512 float32 in both orders 19.7 us (0.77;
 // its 1040 tiles are 2.3 rounds of the 456 that are resident).
 //
 // Sixteen lanes hold one row's block (see column()); where rows do not start on
@@ -24,6 +24,7 @@
 #include <cuda_bf16.h>
 
 #include "s2_internal.h"
+#include "s2_launch.cuh"
 
 namespace s2 {
 namespace {
@@ -169,12 +170,13 @@ __device__ __forceinline__ uint2 load_codes(const uint8_t* p, uint32_t sub, int 
 }
 
 // Blocks of a row in flight per half-warp: 8192 x 4096 bfloat16 packed in 19.2 us
-// with two, 20.6 with four; rows of 4095 unpacked in 31 and 40 us.
+// with two, 20.6 with four; rows of 4095 unpacked in 31 and 40 us (launches one after the other).
 constexpr int kItems = 2;
 
 // One half-warp per block of a row, kItems of them in flight.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) pack_rows_kernel(Pack8Args a) {
+    stream_order();
     const uint32_t sub = threadIdx.x % kLanes;
     const uint64_t first = ((uint64_t)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes) * kItems;
     const T* x = static_cast<const T*>(a.x);
@@ -233,6 +235,7 @@ __device__ __forceinline__ uint32_t turned_at(uint32_t col, uint32_t u) {
 // turn 8 x 8 bytes in registers and pass through shared memory.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) pack_tiles_kernel(Pack8Args a) {
+    stream_order();
     __shared__ uint32_t warp_max[kThreads / 32];
     __shared__ __align__(16) uint8_t turned[kBlk * kBlk];
     const uint32_t sub = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
@@ -322,6 +325,7 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) unpack_kernel(Unpack8Args a) {
+    stream_order();
     const uint32_t sub = threadIdx.x % kLanes;
     const uint64_t first = ((uint64_t)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes) * kItems;
     T* out = static_cast<T*>(a.out);
@@ -388,39 +392,20 @@ inline bool vec16(const void* p, uint64_t ld, size_t esz) {
 
 cudaError_t launch_pack8(const Pack8Args& a, int dtype, bool tiles, cudaStream_t s) {
     const bool vec = vec16(a.x, a.ldx, dtype == 0 ? 4 : 2);
-    if (tiles) {
-        const uint32_t grid = a.nrow_blk * a.nblk;
-        if (dtype == 0) {
-            if (vec) pack_tiles_kernel<float, true><<<grid, kThreads, 0, s>>>(a);
-            else pack_tiles_kernel<float, false><<<grid, kThreads, 0, s>>>(a);
-        } else {
-            if (vec) pack_tiles_kernel<uint16_t, true><<<grid, kThreads, 0, s>>>(a);
-            else pack_tiles_kernel<uint16_t, false><<<grid, kThreads, 0, s>>>(a);
-        }
-        return cudaGetLastError();
-    }
-    const uint32_t per = (uint32_t)(kThreads / kLanes * kItems), grid = (a.items - 1) / per + 1;
-    if (dtype == 0) {
-        if (vec) pack_rows_kernel<float, true><<<grid, kThreads, 0, s>>>(a);
-        else pack_rows_kernel<float, false><<<grid, kThreads, 0, s>>>(a);
-    } else {
-        if (vec) pack_rows_kernel<uint16_t, true><<<grid, kThreads, 0, s>>>(a);
-        else pack_rows_kernel<uint16_t, false><<<grid, kThreads, 0, s>>>(a);
-    }
-    return cudaGetLastError();
+    const uint32_t per = (uint32_t)(kThreads / kLanes * kItems), grid = tiles ? a.nrow_blk * a.nblk : (a.items - 1) / per + 1;
+    auto launch = [&](auto kernel) { return launch_early(kernel, grid, kThreads, 0, 0, s, a); };
+    if (tiles && dtype == 0) return vec ? launch(pack_tiles_kernel<float, true>) : launch(pack_tiles_kernel<float, false>);
+    if (tiles) return vec ? launch(pack_tiles_kernel<uint16_t, true>) : launch(pack_tiles_kernel<uint16_t, false>);
+    if (dtype == 0) return vec ? launch(pack_rows_kernel<float, true>) : launch(pack_rows_kernel<float, false>);
+    return vec ? launch(pack_rows_kernel<uint16_t, true>) : launch(pack_rows_kernel<uint16_t, false>);
 }
 
 cudaError_t launch_unpack8(const Unpack8Args& a, int dtype, cudaStream_t s) {
     const bool vec = vec16(a.out, a.ldo, dtype == 0 ? 4 : 2);
     const uint32_t per = (uint32_t)(kThreads / kLanes * kItems), grid = (a.items - 1) / per + 1;
-    if (dtype == 0) {
-        if (vec) unpack_kernel<float, true><<<grid, kThreads, 0, s>>>(a);
-        else unpack_kernel<float, false><<<grid, kThreads, 0, s>>>(a);
-    } else {
-        if (vec) unpack_kernel<uint16_t, true><<<grid, kThreads, 0, s>>>(a);
-        else unpack_kernel<uint16_t, false><<<grid, kThreads, 0, s>>>(a);
-    }
-    return cudaGetLastError();
+    auto launch = [&](auto kernel) { return launch_early(kernel, grid, kThreads, 0, 0, s, a); };
+    if (dtype == 0) return vec ? launch(unpack_kernel<float, true>) : launch(unpack_kernel<float, false>);
+    return vec ? launch(unpack_kernel<uint16_t, true>) : launch(unpack_kernel<uint16_t, false>);
 }
 
 }  // namespace s2

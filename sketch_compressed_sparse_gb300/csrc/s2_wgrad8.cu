@@ -16,11 +16,12 @@
 // piece that holds the row's first element) and its warp shifts the rows into
 // place.
 //
-// Measured: 200 tokens, 512 x 512 5.0 us in a CUDA graph; 8192 tokens, 4096 x 4096
+// Measured: 200 tokens, 512 x 512 4.4 us in a CUDA graph; 8192 tokens, 4096 x 4096
 // into bfloat16 195 us in a long loop (1.41 PFLOP/s, 0.73 of a cuBLAS product at
 // its burst rate) and 170 us for ten in a row; 2048 tokens, 267735 x 1024, odd
 // rows, into float32 1.05 ms (1.07 PFLOP/s).
 #include "s2_internal.h"
+#include "s2_launch.cuh"
 #include "s2_tc.cuh"
 
 namespace s2 {
@@ -318,6 +319,7 @@ __global__ void __launch_bounds__(Form<ALIGNED, CTAS>::kWarps * 32, 1)
     if constexpr (CTAS == 2) cluster_sync();
     else __syncthreads();
     fence_after();
+    stream_order();
     const uint32_t tmem = tmem_slot;
     const Wait wt{&dead, a.faults};
     const uint32_t group = CTAS == 2 ? 2 : a.split;  // blocks that work on one tile
@@ -447,8 +449,8 @@ __global__ void __launch_bounds__(Form<ALIGNED, CTAS>::kWarps * 32, 1)
             if (ahead < tiles && kb < a.nblk) {
                 const uint32_t t = (tb0 + ahead_tb) * kBT + w * 16 + sub;
                 const uint8_t* p = a.xs + (uint64_t)t * a.nblk + kb;
-                if (t < a.T) b[0] = __ldg(p);
-                if (t + 8 < a.T) b[1] = __ldg(p + 8 * a.nblk);
+                if (t < a.T) b[0] = *p;
+                if (t + 8 < a.T) b[1] = p[8 * a.nblk];
             }
             ahead_tb += P::kTeams;
         };
@@ -637,18 +639,8 @@ cudaError_t launch(const Wgrad8Args& m, Args a, int sms, cudaStream_t s) {
     const uint32_t tblocks = (m.T + kBT - 1) / kBT;
     if (tiles * tblocks > 0xffffffffull) return cudaErrorInvalidValue;
     const uint32_t size = CTAS == 2 ? 2 : a.split;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(size * (unsigned)(a.split > 1 || tiles < (uint64_t)groups ? tiles : groups));
-    cfg.blockDim = dim3(P::kWarps * 32);
-    cfg.dynamicSmemBytes = P::kSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = size;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = size > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, wgrad8_kernel<ALIGNED, CTAS>, xmap, ymaps, a);
+    const uint32_t grid = size * (uint32_t)(a.split > 1 || tiles < (uint64_t)groups ? tiles : groups);
+    return launch_early(wgrad8_kernel<ALIGNED, CTAS>, grid, P::kWarps * 32, P::kSmem, size > 1 ? size : 0, s, xmap, ymaps, a);
 }
 
 }  // namespace

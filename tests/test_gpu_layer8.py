@@ -526,6 +526,49 @@ def test_matmul_same_bits_from_cold_caches(M, N, K):
         assert torch.equal(y, first), f"run {i}"
 
 
+@pytest.mark.parametrize("rows,width", [(1, 512), (200, 700), (2500, 1536)])
+def test_stream_order(rows, width):
+    """Every kernel reads what the one before it wrote and overwrites what an earlier one read, 40
+    times without a wait, also as a graph and between other kernels: the bits of the same calls
+    with a wait after each."""
+    wc, ws, _ = packed(make(width, width, 1) / width ** 0.5, "tiles")
+    start = make(rows, width, 2, "bf16").to(DEV)
+    pad = -(-width // 8) * 8
+    x = torch.zeros((rows, pad), dtype=torch.bfloat16, device=DEV)[:, :width]
+    codes, scales = s2.alloc_pack8(rows, width)
+    back, dw = torch.zeros((rows, width), device=DEV), torch.zeros((width, width), device=DEV)
+
+    def chain(between):
+        x.copy_(start)
+        dw.zero_()
+        for i in range(40):
+            s2.s2_pack8(x, codes, scales)
+            between()
+            s2.s2_matmul8(codes, scales, wc, ws, x)
+            between()
+            s2.s2_wgrad8(x, codes, scales, dw, accumulate=True)
+            between()
+            s2.s2_unpack8(codes, scales, back)
+            between()
+            if i % 4 == 3:  # another library's kernels on both sides
+                x.add_(back.to(torch.bfloat16))
+                between()
+
+    chain(torch.cuda.synchronize)
+    want = [t.clone() for t in (x, back, dw, codes, scales)]
+    for _ in range(5):
+        chain(lambda: None)
+        assert all(torch.equal(a, b) for a, b in zip(want, (x, back, dw, codes, scales)))
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        chain(lambda: None)
+    for _ in range(3):
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(want, (x, back, dw, codes, scales)))
+    assert s2.s2_wait_faults() == 0
+
+
 def test_wgrad_against_differences():
     """L(W) = sum(G * (X W^T)) is linear in W: its central difference along a direction D of packed
     weights is <dL/dW, D>. Both sides in float64 from the operators' float32 outputs:
