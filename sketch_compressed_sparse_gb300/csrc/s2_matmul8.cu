@@ -387,8 +387,9 @@ cudaError_t launch(const Matmul8Args& m, Args a, cudaStream_t s) {
 // warps, nor with clusters of two pairs that share the tokens' copies (23 KB a
 // block and stage). With K = 1024 the stores bind: 2048 x 267735 takes 453 us
 // into bfloat16 and 533 us into twice the bytes in as many requests, 371 us
-// without stores; turning bfloat16 through shared memory for longer requests
-// took more time than it saved.
+// without stores; at K = 128 the stores alone take 393. Turning bfloat16 through
+// shared memory for longer requests, or for whole 32-byte sectors where rows
+// start on odd addresses, took more time than it saved.
 template <bool CHUNKS>
 struct Pair {
     static constexpr int kMaxNT = CHUNKS ? 160 : 224;    // the sum of chunks takes as many columns again

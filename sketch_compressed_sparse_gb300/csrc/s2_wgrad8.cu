@@ -55,7 +55,7 @@ struct Args {
     uint32_t tiles_k, tiles_n;
     uint32_t split;
     uint32_t nt;  // outputs per tile, a multiple of 32
-    int dtype, accumulate;
+    int dtype;
     uint32_t* faults;
 };
 
@@ -98,31 +98,57 @@ __device__ __forceinline__ void st_shared(uint32_t addr, uint4 v) {
 // Makes this thread's shared-memory stores visible to the tensor cores.
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// Sixteen neighbouring outputs of feature k, from n on.
-__device__ __forceinline__ void store(const Args& a, uint32_t n, uint32_t k, float v) {
-    const uint64_t at = (uint64_t)n * a.lddw + k;
-    if (a.dtype == 0) {
-        float* p = static_cast<float*>(a.dw) + at;
-        *p = a.accumulate ? *p + v : v;
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(uint16_t* p, float v) {
+    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(*p) : "f"(v));  // the one rounding to 16 bits: dW's own type
+}
+__device__ __forceinline__ float value(float v) { return v; }
+__device__ __forceinline__ float value(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+
+// Sixteen sums of a feature to the outputs from p on, `step` apart, of which
+// the first `count` exist.
+template <typename T>
+__device__ __forceinline__ void store16(T* p, uint64_t step, int count, const uint32_t* r) {
+    if (count >= 16) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j, p += step) put(p, __uint_as_float(r[j]));
     } else {
-        uint16_t* p = static_cast<uint16_t*>(a.dw) + at;
-        if (a.accumulate) v += __uint_as_float((uint32_t)*p << 16);
-        asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(*p) : "f"(v));  // the one rounding to 16 bits: dW's own type
+#pragma unroll
+        for (int j = 0; j < 16; ++j, p += step)
+            if (j < count) put(p, __uint_as_float(r[j]));
     }
 }
-__device__ __forceinline__ void store16(const Args& a, uint32_t n, uint32_t k, const uint32_t* r) {
-    if (a.accumulate || n + 16 > a.N) {
+template <typename T>
+__device__ __forceinline__ void load16(const T* p, uint64_t step, int count, T* v) {
+    if (count >= 16) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (n + j < a.N) store(a, n + j, k, __uint_as_float(r[j]));
-    } else if (a.dtype == 0) {
-        float* p = static_cast<float*>(a.dw) + (uint64_t)n * a.lddw + k;
-#pragma unroll
-        for (int j = 0; j < 16; ++j, p += a.lddw) *p = __uint_as_float(r[j]);
+        for (int j = 0; j < 16; ++j, p += step) v[j] = *p;
     } else {
-        uint16_t* p = static_cast<uint16_t*>(a.dw) + (uint64_t)n * a.lddw + k;
 #pragma unroll
-        for (int j = 0; j < 16; ++j, p += a.lddw) asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(*p) : "f"(__uint_as_float(r[j])));
+        for (int j = 0; j < 16; ++j, p += step) v[j] = j < count ? *p : T(0);
+    }
+}
+
+// dW += a tile's sums. A thread's sixteen old values are loaded together, and
+// before the stores of the sixteen before: one by one, 12000 x 2944 of them
+// took 843 us, so 77 (12 tokens, float32; 3.7 TB/s). Adding in memory took 56,
+// but turns subnormal numbers into zeros. A kernel of its own (ADD): in one with
+// the plain stores the old values cost those registers, 33 -> 45 us.
+template <typename T>
+__device__ __forceinline__ void add_tile(T* p, uint64_t step, int count, uint32_t nt, uint32_t sum) {
+    T old[16];
+    load16(p, step, count, old);
+#pragma unroll 1
+    for (uint32_t c = 0; c < nt; c += 16, p += 16 * step, count -= 16) {
+        uint32_t r[16];
+        tmem_ld16(sum + c, r);
+        wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(value(old[j]) + __uint_as_float(r[j]));
+        if (c + 16 < nt) load16(p + 16 * step, step, count - 16, old);
+        store16(p, step, count, r);
     }
 }
 
@@ -264,7 +290,7 @@ __device__ __forceinline__ void realign(uint32_t stages, uint32_t y0, uint32_t b
     }
 }
 
-template <bool ALIGNED, int CTAS>
+template <bool ALIGNED, int CTAS, bool ADD>
 __global__ void __launch_bounds__(Form<ALIGNED, CTAS>::kWarps * 32, 1)
     wgrad8_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ YMaps ymaps, const Args a) {
     using P = Form<ALIGNED, CTAS>;
@@ -498,6 +524,12 @@ __global__ void __launch_bounds__(Form<ALIGNED, CTAS>::kWarps * 32, 1)
         const uint32_t mine0 = tmem + ((uint32_t)warp << 21);
         for (uint32_t tile = first; ok && tile < tiles; tile += step, acc ^= 1) {
             const uint32_t sum = mine0 + acc * P::kTileN, other = mine0 + (acc ^ 1) * P::kTileN;
+            if (ADD && (CTAS == 2 || a.split == 1)) {
+                // the old values on their way to L2 while the products run (8192 x 8192, 12 tokens: 199 -> 131 us)
+                const uint32_t pk = (tile % a.tiles_k * CTAS + rank) * kBF + warp * 32, pn = tile / a.tiles_k * a.nt;
+                for (uint32_t c = lane; pk < a.K && c < a.nt && pn + c < a.N; c += 32)
+                    prefetch_l2(static_cast<const uint8_t*>(a.dw) + ((uint64_t)(pn + c) * a.lddw + pk) * (a.dtype == 0 ? 4 : 2));
+            }
             if (!(ok = bar_wait(acc_full + 8 * acc, uses[acc]++ & 1, wt))) break;
             for (uint32_t i = 1; i < chunks; ++i) {
                 if (!(ok = bar_wait(acc_full + 8 * (acc ^ 1), uses[acc ^ 1]++ & 1, wt))) break;
@@ -520,18 +552,29 @@ __global__ void __launch_bounds__(Form<ALIGNED, CTAS>::kWarps * 32, 1)
             if (!ok) break;
             fence_after();
             const uint32_t k = (tile % a.tiles_k * CTAS + rank) * kBF + warp * 32 + lane, n0 = tile / a.tiles_k * a.nt;
+            const uint64_t at = (uint64_t)n0 * a.lddw + k;
+            const int rows = n0 < a.N ? (int)min(a.N - n0, a.nt) : 0;
+            if (ADD && (CTAS == 2 || a.split == 1)) {
+                // (features past the end add nothing, but read their part of the accumulator with the others)
+                const int count = k < a.K ? rows : 0;
+                if (a.dtype == 0) add_tile(static_cast<float*>(a.dw) + at, a.lddw, count, a.nt, sum);
+                else add_tile(static_cast<uint16_t*>(a.dw) + at, a.lddw, count, a.nt, sum);
+            } else {
 #pragma unroll 1
-            for (uint32_t c = 0; c < a.nt; c += 16) {
-                uint32_t r[16];
-                tmem_ld16(sum + c, r);
-                wait_ld();
-                if (CTAS == 1 && a.split > 1) {
-                    // this block's part of the sums, where the rings were
-                    float* part_sums = reinterpret_cast<float*>(raw + (a0 - smem_u32(raw)));
+                for (uint32_t c = 0; c < a.nt; c += 16) {
+                    uint32_t r[16];
+                    tmem_ld16(sum + c, r);
+                    wait_ld();
+                    if (CTAS == 1 && a.split > 1) {
+                        // this block's part of the sums, where the rings were
+                        float* part_sums = reinterpret_cast<float*>(raw + (a0 - smem_u32(raw)));
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) part_sums[(c + j) * kBF + warp * 32 + lane] = __uint_as_float(r[j]);
-                } else if (k < a.K) {
-                    store16(a, n0 + c, k, r);
+                        for (int j = 0; j < 16; ++j) part_sums[(c + j) * kBF + warp * 32 + lane] = __uint_as_float(r[j]);
+                    } else if (k < a.K) {
+                        const uint64_t to = at + (uint64_t)c * a.lddw;
+                        if (a.dtype == 0) store16(static_cast<float*>(a.dw) + to, a.lddw, rows - (int)c, r);
+                        else store16(static_cast<uint16_t*>(a.dw) + to, a.lddw, rows - (int)c, r);
+                    }
                 }
             }
             fence_before();
@@ -550,10 +593,21 @@ __global__ void __launch_bounds__(Form<ALIGNED, CTAS>::kWarps * 32, 1)
         if (!dead) {
             for (uint32_t c = c0 + warp; c < c1 && n0 + c < a.N; c += P::kWarps) {  // a warp per output, four features a lane
                 const float4 v = sum_of_peers(a0 + (c * kBF + lane * 4) * 4, a.split);
-                const float e[4] = {v.x, v.y, v.z, v.w};
+                float e[4] = {v.x, v.y, v.z, v.w};
+                float* p = static_cast<float*>(a.dw) + (uint64_t)(n0 + c) * a.lddw + k;
+                uint16_t* q = static_cast<uint16_t*>(a.dw) + (uint64_t)(n0 + c) * a.lddw + k;
+                if (ADD) {
+                    float old[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (k + j < a.K) store(a, n0 + c, k + j, e[j]);
+                    for (int j = 0; j < 4; ++j) old[j] = k + j >= a.K ? 0.0f : a.dtype == 0 ? p[j] : value(q[j]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) e[j] += old[j];
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (k + j < a.K && a.dtype == 0) put(p + j, e[j]);
+                    if (k + j < a.K && a.dtype != 0) put(q + j, e[j]);
+                }
             }
         }
     }
@@ -629,10 +683,10 @@ cudaError_t launch(const Wgrad8Args& m, Args a, int sms, cudaStream_t s) {
         }
     }
     a.tiles_k = (m.K + CTAS * kBF - 1) / (CTAS * kBF);
-    const void* kernel = reinterpret_cast<const void*>(wgrad8_kernel<ALIGNED, CTAS>);
+    const auto kernel = m.accumulate ? wgrad8_kernel<ALIGNED, CTAS, true> : wgrad8_kernel<ALIGNED, CTAS, false>;
     int groups = sms;
-    if (CTAS == 2) e = max_pairs(kernel, P::kWarps * 32, P::kSmem, &groups);
-    else e = allow_smem(kernel, P::kSmem);
+    if (CTAS == 2) e = max_pairs(reinterpret_cast<const void*>(kernel), P::kWarps * 32, P::kSmem, &groups);
+    else e = allow_smem(reinterpret_cast<const void*>(kernel), P::kSmem);
     if (e != cudaSuccess) return e;
     a.tiles_n = (m.N + a.nt - 1) / a.nt;
     const uint64_t tiles = (uint64_t)a.tiles_k * a.tiles_n;
@@ -640,7 +694,7 @@ cudaError_t launch(const Wgrad8Args& m, Args a, int sms, cudaStream_t s) {
     if (tiles * tblocks > 0xffffffffull) return cudaErrorInvalidValue;
     const uint32_t size = CTAS == 2 ? 2 : a.split;
     const uint32_t grid = size * (uint32_t)(a.split > 1 || tiles < (uint64_t)groups ? tiles : groups);
-    return launch_early(wgrad8_kernel<ALIGNED, CTAS>, grid, P::kWarps * 32, P::kSmem, size > 1 ? size : 0, s, xmap, ymaps, a);
+    return launch_early(kernel, grid, P::kWarps * 32, P::kSmem, size > 1 ? size : 0, s, xmap, ymaps, a);
 }
 
 }  // namespace
@@ -662,13 +716,12 @@ cudaError_t launch_wgrad8(const Wgrad8Args& m, cudaStream_t s) {
     a.K = m.K;
     a.nblk = (m.K + kBF - 1) / kBF;
     a.dtype = m.dtype;
-    a.accumulate = m.accumulate;
     e = tc::wait_fault_word(&a.faults);
     if (e != cudaSuccess) return e;
     const bool tma = reinterpret_cast<uintptr_t>(m.dy) % 16 == 0 && m.lddy % 8 == 0;
     int pairs = 0;
     using P = Form<true, 2>;
-    e = tc::max_pairs(reinterpret_cast<const void*>(wgrad8_kernel<true, 2>), P::kWarps * 32, P::kSmem, &pairs);
+    e = tc::max_pairs(reinterpret_cast<const void*>(wgrad8_kernel<true, 2, false>), P::kWarps * 32, P::kSmem, &pairs);
     if (e != cudaSuccess) return e;
     const Plan plan = choose(m.T, m.N, m.K, tma, di.sms, pairs);
     a.nt = plan.nt;

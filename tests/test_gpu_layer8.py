@@ -384,6 +384,26 @@ def test_wgrad_many_tiles(N, extra, accumulate):
     check_wgrad(70, 40 * N, 128, "bf16", dy_extra=extra, accumulate=accumulate)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,N,K", [(1, 131, 259), (5, 16, 128), (40, 4500, 1001), (300, 2001, 2500), (900, 100, 70)])
+def test_wgrad_accumulate(T, N, K, dtype):
+    """dw += over single blocks, pairs and split tokens, with columns and rows past the last tile."""
+    check_wgrad(T, N, K, dtype, dy_extra=-N % 8, dw_extra=3, accumulate=True)
+    check_wgrad(T, N, K, dtype, dw_extra=1, accumulate=True)
+
+
+@pytest.mark.parametrize("T,N,K", [(2, 40, 200), (500, 64, 128), (300, 2001, 2500)])
+def test_wgrad_accumulate_keeps_subnormals(T, N, K):
+    """Adding zeros leaves every number as it is, those below the least normal one too."""
+    xc, xs, _ = packed(make(T, K, 1), "rows")
+    dy = torch.zeros((T, N), dtype=torch.bfloat16, device=DEV)
+    for dtype, bits in ((torch.float32, torch.int32), (torch.bfloat16, torch.int16)):
+        dw = torch.arange(1, N * K + 1, dtype=torch.int32, device=DEV).remainder(127).to(bits).reshape(N, K).contiguous()
+        want = dw.clone()
+        s2.s2_wgrad8(dy, xc, xs, dw.view(dtype), accumulate=True)
+        assert torch.equal(dw, want)
+
+
 @pytest.mark.parametrize("N", [264, 301])
 def test_wgrad_long_sums(N):
     """A long float32 sum loses no more than one of 704 tokens: each of its 44 additions of 16
