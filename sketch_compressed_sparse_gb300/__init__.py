@@ -13,7 +13,9 @@ PyTorch is used for device memory and streams only.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
+import sysconfig
 from typing import Optional, Tuple
 
 import torch
@@ -61,6 +63,7 @@ __all__ = [
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_lib", "libs2.so")
+_CALLS_PATH = os.path.join(_HERE, "_lib", "_s2calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 S2_OK, S2_ERR_INVALID_ARG, S2_ERR_ALIGNMENT, S2_ERR_UNSUPPORTED, S2_ERR_CUDA = range(5)
 S2_F32, S2_BF16 = 0, 1
@@ -121,6 +124,13 @@ def _load():
         f.argtypes = args
         f.restype = res
         _fns[name] = f
+    if os.path.exists(_CALLS_PATH):  # the same functions of the same library, without ctypes' conversions
+        spec = importlib.util.spec_from_file_location("_s2calls", _CALLS_PATH)
+        calls = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(calls)
+        names = ("s2_pack8", "s2_unpack8", "s2_matmul8", "s2_wgrad8")
+        calls.bind(*(ctypes.cast(_fns[n], _vp).value for n in names))
+        _fns.update((n, getattr(calls, n)) for n in names)
     return _fns
 
 

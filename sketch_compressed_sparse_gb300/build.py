@@ -1,8 +1,10 @@
 """Build libs2.so (the sm_103a kernels and the C ABI) in-tree with nvcc.
 
 Each .cu file compiles to an object in parallel, then nvcc links the shared
-library into ``sketch_compressed_sparse_gb300/_lib/libs2.so``. The build is
-skipped when the library is newer than every source and header.
+library into ``sketch_compressed_sparse_gb300/_lib/libs2.so``. Where Python's
+headers are installed, ``_s2calls`` (a shorter way from Python to the 8-bit
+layer's calls) is built beside it. The build is skipped when the library is
+newer than every source and header.
 
 Usage: ``python -m sketch_compressed_sparse_gb300.build [--force] [--verbose]``.
 """
@@ -14,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +24,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "_lib")
 OBJDIR = os.path.join(LIBDIR, "obj")
 LIB = os.path.join(LIBDIR, "libs2.so")
+CALLS_SRC = os.path.join(CSRC, "s2_calls.cpp")
+CALLS = os.path.join(LIBDIR, "_s2calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 HEADER = os.path.join(ROOT, "include", "s2.h")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -39,12 +44,31 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _python_headers():
+    """Directory of Python.h, or None."""
+    inc = sysconfig.get_paths()["include"]
+    return inc if os.path.exists(os.path.join(inc, "Python.h")) else None
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or (_python_headers() and not os.path.exists(CALLS)):
         return True
     t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + [HEADER]
+    deps = sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + [CALLS_SRC, HEADER]
     return any(os.path.getmtime(p) > t for p in deps)
+
+
+def _build_calls() -> None:
+    inc = _python_headers()
+    if not inc:
+        return
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I", inc,
+           "-I", os.path.join(ROOT, "include"), CALLS_SRC, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on s2_calls.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -64,7 +88,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         return obj, r.stdout + r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+        calls = ex.submit(_build_calls)
         results = list(ex.map(compile_one, sources()))
+        calls.result()
     if verbose or ptxas_info:
         for _, log in results:
             if log.strip():

@@ -148,3 +148,41 @@ def test_binding_checks():
         s2.s2_matmul8(cpu, cpu, cpu, cpu, torch.zeros((4, 4)))
     f = _fn(ctypes.CDLL(s2.lib_path()), "s2_wait_faults", [VP])
     assert f(None) == INVALID
+
+
+def test_calls_without_ctypes():
+    """The extension's calls are the library's: the statuses that ctypes gets, None as a null
+    pointer, and errors for what is no argument list."""
+    import os
+
+    import sketch_compressed_sparse_gb300 as s2
+    from sketch_compressed_sparse_gb300 import build
+
+    if not os.path.exists(build.CALLS):
+        pytest.skip("built without Python's headers")
+    lib = ctypes.CDLL(s2.lib_path())
+    cases = {
+        "s2_pack8": [(None, 0, 0, 5, 5, 0, None, 16, None, None, 0, None, None),
+                     (None, 0, 3, 5, 5, 0, None, 16, None, None, 0, None, None),
+                     (16, 7, 3, 5, 5, 0, 32, 16, 64, None, 0, None, None),
+                     (16, 0, 3, 5, 4, 0, 32, 16, 64, None, 0, None, None)],
+        "s2_unpack8": [(None, 16, None, 0, 0, 5, None, 0, 5, None), (None, 16, None, 0, 3, 5, None, 0, 5, None),
+                       (16, 16, 64, 9, 3, 5, 128, 0, 5, None)],
+        "s2_matmul8": [(None, 16, None, None, 16, None, 1, 0, 4, 5, None, 0, 4, None),
+                       (16, 16, 32, 64, 16, 96, 1, 2, 4, 5, 130, 0, 4, None),
+                       (16, 16, 32, 64, 16, 96, 1, 2, 4, 5, None, 0, 4, 2 ** 63)],
+        "s2_wgrad8": [(None, 4, None, 16, None, 2, 0, 5, None, 0, 5, 0, None),
+                      (16, 4, 32, 16, 64, 2, 4, 5, None, 0, 5, 1, None),
+                      (17, 4, 32, 16, 64, 2, 4, 5, 128, 0, 5, 1, None)],
+    }
+    for name, calls in cases.items():
+        f = _fn(lib, name, s2._SIGS[name][0])
+        for args in calls:
+            assert s2._f(name)(*args) == f(*args), (name, args)
+        n = len(s2._SIGS[name][0])
+        with pytest.raises(TypeError):
+            s2._f(name)(*(0,) * (n - 1))
+        with pytest.raises(TypeError):
+            s2._f(name)(*("x",) * n)
+        with pytest.raises(OverflowError):
+            s2._f(name)(*(2 ** 64,) * n)
