@@ -589,6 +589,43 @@ def test_stream_order(rows, width):
     assert s2.s2_wait_faults() == 0
 
 
+def test_waits_for_other_streams():
+    """A call after a wait for another stream's event reads what that stream wrote, although the
+    kernel before it in its own stream lets it start early; also over the legacy default stream."""
+    rows, width = 300, 640
+    wc, ws, _ = packed(make(512, width, 1), "tiles")
+    busy = torch.randn((4096, 4096), device=DEV)
+    inputs = [make(rows, width, 10 + i).to(DEV) for i in range(8)]
+    want = []
+    for v in inputs:
+        c, b = s2.alloc_pack8(rows, width)
+        s2.s2_pack8(v, c, b)
+        y = torch.empty((rows, 512), device=DEV)
+        s2.s2_matmul8(c, b, wc, ws, y)
+        want.append((c.clone(), y))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for own in (torch.cuda.current_stream(), torch.cuda.Stream()):
+        x = torch.zeros((rows, width), device=DEV)
+        c, b = s2.alloc_pack8(rows, width)
+        other = s2.alloc_pack8(rows, width)
+        y = torch.empty((rows, 512), device=DEV)
+        torch.cuda.synchronize()
+        for v, (codes, out) in zip(inputs, want):
+            with torch.cuda.stream(side):
+                side.wait_stream(own)
+                for _ in range(3):
+                    busy.mm(busy)
+                x.copy_(v)
+            with torch.cuda.stream(own):
+                s2.s2_pack8(inputs[0], *other, stream=own)
+                own.wait_stream(side)
+                s2.s2_pack8(x, c, b, stream=own)
+                s2.s2_matmul8(c, b, wc, ws, y, stream=own)
+                own.synchronize()
+            assert torch.equal(c, codes) and torch.equal(y, out)
+
+
 def test_wgrad_against_differences():
     """L(W) = sum(G * (X W^T)) is linear in W: its central difference along a direction D of packed
     weights is <dL/dW, D>. Both sides in float64 from the operators' float32 outputs:
