@@ -435,9 +435,10 @@ S2_API s2_status s2_matmul8(const uint8_t *x, uint64_t ldx, const uint8_t *x_sca
  *   with S2_SCALE_ROWS. X's values are exact in bfloat16 (scale bytes 10 to
  *   247, as s2_pack8 writes them; others are rounded), the sums are float32.
  *   accumulate != 0: dw += the sum instead (one more rounding), for a
- *   gradient taken over several batches. Long float32 sums are taken in
- *   chunks of at most 704 tokens. The result does not depend on
- *   timing. dw may be a worker's row of grad[W][n], which s2_encode_batched
+ *   gradient taken over several batches. Long sums are taken in chunks of
+ *   at most 704 tokens (float32 results) or 2048 (bfloat16), which are
+ *   added up in float32. The result does not depend on timing.
+ *   dw may be a worker's row of grad[W][n], which s2_encode_batched
  *   and s2_block_topk read. Where base or row stride of dy misses 16 bytes
  *   the rows are fetched through registers (slower than aligned rows).
  */

@@ -17,8 +17,8 @@
 // place.
 //
 // Measured: 200 tokens, 512 x 512 4.4 us in a CUDA graph; 8192 tokens, 4096 x 4096
-// into bfloat16 195 us in a long loop (1.41 PFLOP/s, 0.73 of a cuBLAS product at
-// its burst rate) and 170 us for ten in a row; 2048 tokens, 267735 x 1024, odd
+// into bfloat16 196 us in a long loop (1.40 PFLOP/s, 0.73 of a cuBLAS product at
+// its burst rate) and 177 us for ten in a row; 2048 tokens, 267735 x 1024, odd
 // rows, into float32 1.05 ms (1.07 PFLOP/s).
 #include "s2_internal.h"
 #include "s2_launch.cuh"
@@ -41,6 +41,11 @@ constexpr uint32_t kABytes = 2 * kGroupBytes;
 // later chunks use the other one, and the products wait only while it is added
 // (additions in L2 or through registers took twice as long in all).
 constexpr uint32_t kChunk = 11;
+// A bfloat16 result is rounded by up to 2^-9 of itself, so its chunks are longer:
+// 2048 tokens lose 2.4e-6, an 800th of that, at any number of tokens. (One chunk
+// lost 9.5e-6 at 8192 tokens, growing with their number and always towards zero;
+// 8192 x 4096 x 4096, ten in a row: one chunk 172 us, chunks of 32 stages 177, of 11 198.)
+constexpr uint32_t kChunk16 = 32;
 constexpr int kLoaders = 8;                // warps that shift a misaligned dY into place
 
 struct Args {
@@ -373,7 +378,7 @@ __global__ void __launch_bounds__(Form<ALIGNED, CTAS>::kWarps * 32, 1)
     const uint32_t all_tb = (a.T + kBT - 1) / kBT, tb0 = (uint32_t)((uint64_t)all_tb * part / a.split);
     const uint32_t tblocks = (uint32_t)((uint64_t)all_tb * (part + 1) / a.split) - tb0;
     const uint32_t mine = first < tiles ? (tiles - first - 1) / step + 1 : 0, stages = mine * tblocks;
-    const uint32_t chunks = a.dtype == 0 ? (tblocks + kChunk - 1) / kChunk : 1;
+    const uint32_t chunk = a.dtype == 0 ? kChunk : kChunk16, chunks = (tblocks + chunk - 1) / chunk;
 
     if (warp == kCopier) {
         const bool leader = elect();

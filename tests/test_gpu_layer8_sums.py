@@ -1,0 +1,61 @@
+"""GPU tests of the 8-bit layer's long sums, in every form that its planners choose: sums split over
+a cluster, tiles of one block, pairs of blocks, aligned and misaligned rows.
+
+The tensor cores cut off what they add, on average half a unit, at most 2^-24 of a chunk's own sum,
+for each of the chunk's additions: always towards zero, so that a bfloat16 result's own rounding
+(at most 2^-9 of the value, of either sign) hides it in one output and not in the mean of many. With
+n outputs the mean of sign(exact) (y - exact) over the mean of |exact| is therefore at most
+    additions of a chunk * 2^-24 + 6 * 2^-9 / sqrt(n)
+in magnitude, with six standard deviations (each below 2^-9) for the roundings, whose sizes grow with
+the outputs as |exact| does (their mean square over their squared mean is below 2: n is halved).
+"""
+import pytest
+import torch
+
+from tests import _layer8 as ref
+from tests.test_gpu_layer8 import DEV
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import sketch_compressed_sparse_gb300 as s2
+
+
+def packed_here(rows, cols, seed, lay="rows"):
+    """A packed normal matrix and its values in float64, all on the GPU."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    codes, scales = s2.alloc_pack8(rows, cols, lay)
+    s2.s2_pack8(torch.randn((rows, cols), generator=g, device=DEV), codes, scales, lay)
+    table = torch.from_numpy(ref.VALUES).to(DEV)
+    s = torch.exp2(scales.double() - 127).repeat_interleave(128, 1)[:, :cols]
+    if lay == "tiles":
+        s = s.repeat_interleave(128, 0)[:rows]
+    return codes, scales, table[codes.int()] * s
+
+
+def normal(rows, cols, seed, dtype):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.randn((rows, cols), generator=g, device=DEV).to(dtype)
+
+
+def drift(got, want):
+    return abs(float(((got.double() - want) * want.sign()).mean() / want.abs().mean()))
+
+
+def drift_bound(additions, n):
+    return additions * 2.0 ** -24 + 6 * 2.0 ** -9 / (n / 2) ** 0.5
+
+
+# split over a cluster, one block a tile, pairs; aligned and misaligned rows (on 152 SMs)
+@pytest.mark.parametrize("T,N,K", [(1600000, 264, 260), (1600000, 263, 260), (60000, 9600, 256), (60000, 9601, 256),
+                                   (48000, 4096, 1024), (48000, 4097, 1024)])
+def test_wgrad_bfloat16_does_not_drift(T, N, K):
+    """A bfloat16 result's chunks are 2048 tokens at most, 128 additions of 16."""
+    xc, xs, xv = packed_here(T, K, 1)
+    dy = normal(T, N, 2, torch.bfloat16)
+    dw = torch.empty((N, K), dtype=torch.bfloat16, device=DEV)
+    s2.s2_wgrad8(dy, xc, xs, dw)
+    want = dy.double().T @ xv
+    assert drift(dw, want) <= drift_bound(128, N * K)
+    assert float((dw.double() - want).norm() / want.norm()) <= 128 * 2.0 ** -24 + 2.0 ** -9
+    assert s2.s2_wait_faults() == 0
