@@ -20,6 +20,7 @@
 // into bfloat16 196 us in a long loop (1.40 PFLOP/s, 0.73 of a cuBLAS product at
 // its burst rate) and 177 us for ten in a row; 2048 tokens, 267735 x 1024, odd
 // rows, into float32 1.05 ms (1.07 PFLOP/s).
+#include "s2_chunks.h"
 #include "s2_internal.h"
 #include "s2_launch.cuh"
 #include "s2_tc.cuh"
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(Form<ALIGNED, CTAS>::kWarps * 32, 1)
     const uint32_t all_tb = (a.T + kBT - 1) / kBT, tb0 = (uint32_t)((uint64_t)all_tb * part / a.split);
     const uint32_t tblocks = (uint32_t)((uint64_t)all_tb * (part + 1) / a.split) - tb0;
     const uint32_t mine = first < tiles ? (tiles - first - 1) / step + 1 : 0, stages = mine * tblocks;
-    const uint32_t chunk = a.dtype == 0 ? kChunk : kChunk16, chunks = (tblocks + chunk - 1) / chunk;
+    const uint32_t chunks = chunk_count(tblocks, a.dtype == 0 ? kChunk : kChunk16);
 
     if (warp == kCopier) {
         const bool leader = elect();
@@ -437,7 +438,7 @@ __global__ void __launch_bounds__(Form<ALIGNED, CTAS>::kWarps * 32, 1)
             bool ok = true;
             for (uint32_t tile = first; ok && tile < tiles; tile += step, acc ^= 1) {
                 for (uint32_t c = 0, tb = 0; ok && c < chunks; ++c) {
-                    const uint32_t at = c ? acc ^ 1 : acc, from = tb, end = tblocks * (c + 1) / chunks;
+                    const uint32_t at = c ? acc ^ 1 : acc, from = tb, end = chunk_end(tblocks, chunks, c);
                     if (!(ok = bar_wait(acc_empty + 8 * at, (uses[at]++ & 1) ^ 1, wt))) break;
                     fence_after();
                     for (; tb < end; ++tb) {
