@@ -420,8 +420,9 @@ S2_API s2_status s2_unpack8(const uint8_t *codes, uint64_t ldc, const uint8_t *s
  * s2_matmul8 -- y[m][n] = sum over k of X[m][k] * W[n][k], of type dt, with
  *   X [M][K] packed with S2_SCALE_ROWS (a layer's input, or the gradient of
  *   its output) and W [N][K] packed with either layout (its weight, or the
- *   transposed weight). Sums are float32, a float32 result's in chunks of
- *   at most 4096 k; one rounding to dt. The result does not depend on timing.
+ *   transposed weight). Sums are float32, in chunks of at most 4096 k that
+ *   are added up in float32 (a bfloat16 result's only where K > 65536); one
+ *   rounding to dt. The result does not depend on timing.
  *   Serves one token (M = 1) as well as a batch.
  */
 S2_API s2_status s2_matmul8(const uint8_t *x, uint64_t ldx, const uint8_t *x_scales, const uint8_t *w, uint64_t ldw,

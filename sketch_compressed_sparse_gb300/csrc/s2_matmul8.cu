@@ -38,9 +38,15 @@ constexpr uint32_t kABytes = kBF * kBK;  // W part of a stage
 // 8e-7 at the longer two), and the sum of chunks stays in tensor memory beside
 // the two accumulators. That leaves a pair 160 tokens a tile where it has 224:
 // 2048 x 1024 x 267735 505 -> 513 us, 8192 x 4096 x 16384 336 -> 369 us. Adding
-// to Y in global memory kept the 224 and took 592 and 367. A bfloat16 result
-// drops all of it in its own rounding and is taken in one chunk.
+// to Y in global memory kept the 224 and took 592 and 367.
 constexpr uint32_t kChunk = 32;
+// A bfloat16 result is rounded by up to 2^-9 of itself. Up to this many blocks of
+// K it is taken in one chunk, which loses at most 1.6e-5, a 120th of that, and
+// keeps the 224 tokens (8192 x 4096 x 8192 150 us, in chunks 180; 2048 x 8192 x
+// 28672 352 and 426). Beyond, the loss would go on growing with K, always towards
+// zero (4e-5 at 267735), and chunks are taken: 2048 x 4096 x 66048 367 -> 374 us,
+// 8192 x 4096 x 66048 1.28 -> 1.55 ms.
+constexpr uint32_t kLong16 = 512;
 static_assert(kChunk % kGroup == 0, "chunks end between two scale words");
 
 struct Args {
@@ -694,7 +700,7 @@ cudaError_t launch_matmul8(const Matmul8Args& m, cudaStream_t s) {
     DeviceInfo di{};
     e = device_info(&di);
     if (e != cudaSuccess) return e;
-    if (m.dtype == 0 && a.nblk > kChunk) return plan_and_launch<true>(m, a, di.sms, s);
+    if (a.nblk > (m.dtype == 0 ? kChunk : kLong16)) return plan_and_launch<true>(m, a, di.sms, s);
     return plan_and_launch<false>(m, a, di.sms, s);
 }
 

@@ -22,15 +22,20 @@ if torch.cuda.is_available():
 
 
 def packed_here(rows, cols, seed, lay="rows"):
-    """A packed normal matrix and its values in float64, all on the GPU."""
+    """A packed normal matrix, on the GPU."""
     g = torch.Generator(device=DEV).manual_seed(seed)
     codes, scales = s2.alloc_pack8(rows, cols, lay)
     s2.s2_pack8(torch.randn((rows, cols), generator=g, device=DEV), codes, scales, lay)
-    table = torch.from_numpy(ref.VALUES).to(DEV)
+    return codes, scales
+
+
+def values(codes, scales, lay="rows"):
+    """The values of a packed matrix in float64."""
+    rows, cols = codes.shape
     s = torch.exp2(scales.double() - 127).repeat_interleave(128, 1)[:, :cols]
     if lay == "tiles":
         s = s.repeat_interleave(128, 0)[:rows]
-    return codes, scales, table[codes.int()] * s
+    return torch.from_numpy(ref.VALUES).to(DEV)[codes.int()] * s
 
 
 def normal(rows, cols, seed, dtype):
@@ -51,11 +56,28 @@ def drift_bound(additions, n):
                                    (48000, 4096, 1024), (48000, 4097, 1024)])
 def test_wgrad_bfloat16_does_not_drift(T, N, K):
     """A bfloat16 result's chunks are 2048 tokens at most, 128 additions of 16."""
-    xc, xs, xv = packed_here(T, K, 1)
+    xc, xs = packed_here(T, K, 1)
     dy = normal(T, N, 2, torch.bfloat16)
     dw = torch.empty((N, K), dtype=torch.bfloat16, device=DEV)
     s2.s2_wgrad8(dy, xc, xs, dw)
-    want = dy.double().T @ xv
+    want = dy.double().T @ values(xc, xs)
     assert drift(dw, want) <= drift_bound(128, N * K)
     assert float((dw.double() - want).norm() / want.norm()) <= 128 * 2.0 ** -24 + 2.0 ** -9
+    assert s2.s2_wait_faults() == 0
+
+
+# one block a tile, pairs (on 152 SMs)
+@pytest.mark.parametrize("M,N,K", [(64, 20000, 131072), (2048, 1024, 267735)])
+def test_matmul_bfloat16_does_not_drift(M, N, K):
+    """Beyond 65536 of K a bfloat16 result's chunks are 4096 at most, 128 additions of 32."""
+    xc, xs = packed_here(M, K, 1)
+    wc, ws = packed_here(N, K, 2, "tiles")
+    y = torch.empty((M, N), dtype=torch.bfloat16, device=DEV)
+    s2.s2_matmul8(xc, xs, wc, ws, y)
+    want = torch.zeros((M, N), dtype=torch.float64, device=DEV)
+    for k in range(0, K, 16384):
+        b = slice(k // 128, (k + 16384) // 128)
+        want += values(xc[:, k:k + 16384], xs[:, b]) @ values(wc[:, k:k + 16384], ws[:, b], "tiles").T
+    assert drift(y, want) <= drift_bound(128, M * N)
+    assert float((y.double() - want).norm() / want.norm()) <= 128 * 2.0 ** -24 + 2.0 ** -9
     assert s2.s2_wait_faults() == 0
