@@ -107,13 +107,17 @@ __device__ __forceinline__ void store16(const Args& a, uint32_t t, uint32_t f, c
     }
 }
 
-// Adds the sum of the chunks before to 16 columns of an accumulator that are being read.
-__device__ __forceinline__ void add_sum16(uint32_t sum, uint32_t* r) {
+// 16 columns of an accumulator and, if there are any, of the sum of the chunks before.
+__device__ __forceinline__ void load_sums16(uint32_t acc, uint32_t sum, bool before, uint32_t* r) {
     uint32_t q[16];
-    tmem_ld16(sum, q);
-    wait_ld();
+    tmem_ld16(acc, r);
+    if (before) tmem_ld16(sum, q);
+    wait_ld16(r);
+    if (before) {
+        wait_ld16(q);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(q[j]) + __uint_as_float(r[j]));
+        for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(q[j]) + __uint_as_float(r[j]));
+    }
 }
 
 // The scale bytes of K blocks kb..kb+3 of one row as a word; blocks past the
@@ -304,9 +308,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll 1
             for (int c = 0; c < NT; c += 16) {
                 uint32_t r[16];
-                tmem_ld16(mine + buf * NT + c, r);
-                if (CHUNKS && kb > kb0) add_sum16(mine + S::kSumAt + c, r);
-                wait_ld();
+                load_sums16(mine + buf * NT + c, mine + S::kSumAt + c, CHUNKS && kb > kb0, r);
                 if (more) {
                     tmem_st16(mine + S::kSumAt + c, r);
                     wait_st();
@@ -579,9 +581,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWarps * 32, 1)
 #pragma unroll 1
             for (uint32_t c = 0; c < a.nt; c += 16) {
                 uint32_t r[16];
-                tmem_ld16(mine + acc.at * S::kMaxNT + c, r);
-                if (CHUNKS && kb > 0) add_sum16(mine + S::kSumAt + c, r);
-                wait_ld();
+                load_sums16(mine + acc.at * S::kMaxNT + c, mine + S::kSumAt + c, CHUNKS && kb > 0, r);
                 if (more) {
                     tmem_st16(mine + S::kSumAt + c, r);
                     wait_st();

@@ -123,7 +123,6 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 16 or 32 neighbouring columns of the warp's 32 lanes.
@@ -135,6 +134,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
         : "r"(addr));
 }
 // Waits for the loads in flight, one of which fills r: r is not touched before.
+// (A wait that does not name the registers would not keep their uses behind it.)
 __device__ __forceinline__ void wait_ld16(uint32_t* r) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),

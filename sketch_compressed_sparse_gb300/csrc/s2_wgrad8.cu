@@ -170,7 +170,7 @@ __device__ __forceinline__ void add_tile(T* p, uint64_t step, int count, uint32_
     for (uint32_t c = 0; c < nt; c += 16, p += 16 * step, count -= 16) {
         uint32_t r[16];
         tmem_ld16(sum + c, r);
-        wait_ld();
+        wait_ld16(r);
 #pragma unroll
         for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(value(old[j]) + __uint_as_float(r[j]));
         if (c + 16 < nt) load16(p + 16 * step, step, count - 16, old);
@@ -565,7 +565,8 @@ __global__ void __launch_bounds__(Form<ALIGNED, CTAS>::kWarps * 32, 1)
                     uint32_t r[16], v[16];
                     tmem_ld16(sum + c, r);
                     tmem_ld16(other + c, v);
-                    wait_ld();
+                    wait_ld16(r);
+                    wait_ld16(v);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(v[j]));
                     tmem_st16(sum + c, r);
@@ -592,7 +593,7 @@ __global__ void __launch_bounds__(Form<ALIGNED, CTAS>::kWarps * 32, 1)
                 for (uint32_t c = 0; c < a.nt; c += 16) {
                     uint32_t r[16];
                     tmem_ld16(sum + c, r);
-                    wait_ld();
+                    wait_ld16(r);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) part_sums[(c + j) * kBF + warp * 32 + lane] = __uint_as_float(r[j]);
                 }
