@@ -327,6 +327,9 @@ inline s2_status check_codes(const void* codes, uint64_t rows, uint64_t cols, ui
     return aligned(codes, 16) && (rows <= 1 || ld % 16 == 0) ? S2_OK : S2_ERR_ALIGNMENT;
 }
 
+// Row stride of codes for their tensor map, which wants a multiple of 16; that of a single row is free.
+inline uint64_t stride16(uint64_t rows, uint64_t cols, uint64_t ld) { return rows > 1 ? ld : (cols + 15) / 16 * 16; }
+
 inline s2_status first_error(std::initializer_list<s2_status> all) {
     for (s2_status st : all)
         if (st != S2_OK) return st;
@@ -771,7 +774,7 @@ s2_status s2_matmul8(const uint8_t* x, uint64_t ldx, const uint8_t* x_scales, co
     if (clash({{y, extent(M, N, ldy, esz)}, {x, extent(M, K, ldx, 1)}, {x_scales, M * nblk}, {w, extent(N, K, ldw, 1)},
                {w_scales, (w_layout == S2_SCALE_TILES ? blocks8(N) : N) * nblk}}, 1))
         return S2_ERR_INVALID_ARG;
-    Matmul8Args a{x, x_scales, w, w_scales, y, M > 1 ? ldx : (K + 15) / 16 * 16, N > 1 ? ldw : (K + 15) / 16 * 16, ldy,
+    Matmul8Args a{x, x_scales, w, w_scales, y, stride16(M, K, ldx), stride16(N, K, ldw), ldy,
                   (uint32_t)M, (uint32_t)N, (uint32_t)K, w_layout == S2_SCALE_TILES ? 7u : 0u, dt == S2_F32 ? 0 : 1};
     return cuda_status(launch_matmul8(a, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -796,7 +799,7 @@ s2_status s2_wgrad8(const void* dy, uint64_t lddy, const uint8_t* x, uint64_t ld
     if (clash({{dw, extent(N, K, lddw, esz)}, {dy, extent(T, N, lddy, 2)}, {x, extent(T, K, ldx, 1)},
                {x_scales, T * blocks8(K)}}, 1))
         return S2_ERR_INVALID_ARG;
-    Wgrad8Args a{dy, x, x_scales, dw, T > 1 ? lddy : (N + 7) / 8 * 8, ldx, lddw, (uint32_t)T, (uint32_t)N, (uint32_t)K,
+    Wgrad8Args a{dy, x, x_scales, dw, T > 1 ? lddy : (N + 7) / 8 * 8, stride16(T, K, ldx), lddw, (uint32_t)T, (uint32_t)N, (uint32_t)K,
                  dt == S2_F32 ? 0 : 1, accumulate != 0};
     return cuda_status(launch_wgrad8(a, reinterpret_cast<cudaStream_t>(stream)));
 }

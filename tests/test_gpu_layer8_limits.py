@@ -1,9 +1,11 @@
 """GPU tests of the 8-bit layer at the edges of what its calls take: the longest
-sums."""
+sums and single rows of any stride."""
+import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_layer8 import DEV
+from tests import _layer8 as ref
+from tests.test_gpu_layer8 import DEV, make
 
 pytestmark = pytest.mark.gpu
 
@@ -25,3 +27,35 @@ def test_wgrad_of_many_tokens():
         s2.s2_wgrad8(dy, codes, scales, dw)
         assert torch.equal(dw.float(), want)
     assert s2.s2_wait_faults() == 0
+
+
+def one_row(codes, ld):
+    """The same single row, as a matrix whose row stride is ld."""
+    return codes.reshape(-1).as_strided((1, codes.shape[1]), (ld, 1))
+
+
+@pytest.mark.parametrize("ld", [0, 1, 140, 141, 144])
+def test_single_rows_of_any_stride(ld):
+    """A matrix of one row has no next row: its row stride does not matter, as a contiguous [1, 140]
+    has it. The products with one of 1.0 as the other factor are exact."""
+    K = 140
+    x = make(1, K, 1)
+    want, want_s = ref.pack(x.double().numpy(), False)
+    values = ref.unpack(want, want_s, False)
+    room = torch.zeros((1, 256), dtype=torch.uint8, device=DEV)
+    codes = one_row(room[:, :K], ld)
+    scales = torch.empty((1, 2), dtype=torch.uint8, device=DEV)
+    s2.s2_pack8(one_row(x.to(DEV), ld), codes, scales)
+    np.testing.assert_array_equal(codes.cpu().numpy(), want)
+    out = one_row(torch.empty((1, 256), device=DEV)[:, :K], ld)
+    s2.s2_unpack8(codes, scales, out)
+    np.testing.assert_array_equal(out.double().cpu().numpy(), values)
+    for N in (1, 24):
+        dw = torch.empty((N, K), device=DEV)
+        dy = one_row(torch.ones((1, 64), dtype=torch.bfloat16, device=DEV)[:, :N], ld)
+        s2.s2_wgrad8(dy, codes, scales, dw)
+        np.testing.assert_array_equal(dw.double().cpu().numpy(), np.repeat(values, N, 0))
+    y = one_row(torch.empty((1, 256), device=DEV)[:, :1], ld)
+    s2.s2_matmul8(codes, scales, codes, scales, y, "rows")
+    sq = (values * values).sum()
+    assert abs(y.item() - sq) <= (K + 41) * 2.0 ** -23 * sq
