@@ -123,7 +123,9 @@ cudaError_t max_pairs(const void* fn, int threads, size_t smem, int* pairs) {
 
 cudaError_t read_wait_faults(uint32_t* count) {
     uint32_t* word = nullptr;
-    const cudaError_t e = tc::wait_fault_word(&word);
+    cudaError_t e = tc::wait_fault_word(&word);
+    // the copy alone would not wait for streams that do not synchronise with the default one
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
     return e == cudaSuccess ? cudaMemcpy(count, word, sizeof(*count), cudaMemcpyDeviceToHost) : e;
 }
 

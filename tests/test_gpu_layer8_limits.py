@@ -1,5 +1,5 @@
 """GPU tests of the 8-bit layer at the edges of what its calls take: the longest
-sums and single rows of any stride."""
+sums, single rows of any stride, and the count of waits that ran out."""
 import numpy as np
 import pytest
 import torch
@@ -59,3 +59,17 @@ def test_single_rows_of_any_stride(ld):
     s2.s2_matmul8(codes, scales, codes, scales, y, "rows")
     sq = (values * values).sum()
     assert abs(y.item() - sq) <= (K + 41) * 2.0 ** -23 * sq
+
+
+def test_wait_faults_waits_for_every_stream():
+    """The count covers every call made before: also those on streams that do not wait for the default stream."""
+    busy = torch.randn((8192, 8192), device=DEV)
+    out = busy @ busy
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    assert s2.s2_wait_faults() == 0
+    with torch.cuda.stream(side):
+        for _ in range(30):
+            torch.mm(busy, busy, out=out)
+    assert s2.s2_wait_faults() == 0
+    assert side.query()
