@@ -167,13 +167,16 @@ def _check(status: int, where: str):
         raise S2Error(status, where)
 
 
-_raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+# (absent from a torch built for the CPU)
+_raw_stream, _device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
 
 
 def _stream(stream: Optional[torch.cuda.Stream]) -> int:
     if stream is not None:
         return stream.cuda_stream
-    # torch.cuda.current_stream().cuda_stream without building a Stream object (0.2 us instead of 2.9 us)
+    if _raw_stream is None or _device is None:
+        return torch.cuda.current_stream().cuda_stream
+    # the same without building a Stream object (0.2 us instead of 2.9 us)
     return _raw_stream(_device())
 
 
