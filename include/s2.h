@@ -384,7 +384,8 @@ S2_API s2_status s2_pipeline_dense_host(const void *host_grad, s2_dtype dt, uint
  *                   (activations, gradients of outputs);
  *   S2_SCALE_TILES: scales [ceil(rows/128)][nblk], a block is 128 x 128
  *                   elements (weights: the transpose has the same values).
- * Sizes up to 2^31 - 1, row strides below 2^35 (S2_ERR_UNSUPPORTED). Row
+ * Sizes up to 2^31 - 1, row strides below 2^35, at most 2^48 elements
+ * from a matrix's first to its last row (S2_ERR_UNSUPPORTED). Row
  * strides of the other matrices are in elements and need only cover a row. A
  * size of zero is valid. The first s2_matmul8 and s2_wgrad8 on a device look up
  * an address there: make them before any stream capture.
@@ -423,7 +424,8 @@ S2_API s2_status s2_unpack8(const uint8_t *codes, uint64_t ldc, const uint8_t *s
  *   transposed weight). Sums are float32, in chunks of at most 4096 k that
  *   are added up in float32 (a bfloat16 result's only where K > 65536); one
  *   rounding to dt. The result does not depend on timing.
- *   Serves one token (M = 1) as well as a batch.
+ *   Serves one token (M = 1) as well as a batch. ceil(M/16) * ceil(N/128)
+ *   must be below 2^31 (S2_ERR_UNSUPPORTED).
  */
 S2_API s2_status s2_matmul8(const uint8_t *x, uint64_t ldx, const uint8_t *x_scales, const uint8_t *w, uint64_t ldw,
                             const uint8_t *w_scales, s2_scale_layout w_layout, uint64_t M, uint64_t N, uint64_t K,
@@ -442,6 +444,8 @@ S2_API s2_status s2_matmul8(const uint8_t *x, uint64_t ldx, const uint8_t *x_sca
  *   dw may be a worker's row of grad[W][n], which s2_encode_batched
  *   and s2_block_topk read. Where base or row stride of dy misses 16 bytes
  *   the rows are fetched through registers (slower than aligned rows).
+ *   ceil(N/32) * ceil(K/128) must be below 2^31, and times ceil(T/64) below
+ *   2^36 (S2_ERR_UNSUPPORTED).
  */
 S2_API s2_status s2_wgrad8(const void *dy, uint64_t lddy, const uint8_t *x, uint64_t ldx, const uint8_t *x_scales,
                            uint64_t T, uint64_t N, uint64_t K, void *dw, s2_dtype dt, uint64_t lddw, int accumulate,

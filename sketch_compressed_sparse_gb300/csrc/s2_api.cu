@@ -301,7 +301,8 @@ PipelineLayout pipeline_layout(s2_dtype dt, uint32_t W, uint64_t n, s2_params p)
 }
 
 // ---- 8-bit layer ----
-constexpr uint64_t kMaxDim8 = 0x7fffffffull;  // sizes travel as 32-bit coordinates
+constexpr uint64_t kMaxDim8 = 0x7fffffffull;   // sizes travel as 32-bit coordinates
+constexpr uint64_t kMaxSpan8 = 1ull << 48;     // elements from a matrix's first to its last row
 
 inline uint64_t blocks8(uint64_t n) { return (n + 127) / 128; }
 inline uint64_t size_of(s2_dtype dt) { return dt == S2_F32 ? 4 : 2; }
@@ -316,6 +317,7 @@ inline uint64_t extent(uint64_t rows, uint64_t cols, uint64_t ld, uint64_t esz) 
 // A matrix argument: its row stride covers a row and its bytes are addressable.
 inline s2_status check_matrix(uint64_t rows, uint64_t cols, uint64_t ld) {
     if (rows > kMaxDim8 || cols > kMaxDim8 || ld >= (1ull << 35)) return S2_ERR_UNSUPPORTED;  // tensor maps: 2^40 bytes
+    if (rows > 1 && ld && rows - 1 > kMaxSpan8 / ld) return S2_ERR_UNSUPPORTED;
     return rows > 1 && ld < cols ? S2_ERR_INVALID_ARG : S2_OK;
 }
 
@@ -760,6 +762,7 @@ s2_status s2_matmul8(const uint8_t* x, uint64_t ldx, const uint8_t* x_scales, co
     if (!dtype_ok(dt) || !layout_ok(w_layout)) return S2_ERR_INVALID_ARG;
     s2_status st = first_error({check_matrix(M, N, ldy), check_matrix(M, K, ldx), check_matrix(N, K, ldw)});
     if (st != S2_OK) return st;
+    if ((M + 15) / 16 * blocks8(N) > 0x7fffffffull) return S2_ERR_UNSUPPORTED;  // the smallest tiles are counted in 32 bits
     if (M == 0 || N == 0) return S2_OK;
     if (!y) return S2_ERR_INVALID_ARG;
     const uint64_t esz = size_of(dt);
@@ -784,6 +787,9 @@ s2_status s2_wgrad8(const void* dy, uint64_t lddy, const uint8_t* x, uint64_t ld
     if (!dtype_ok(dt)) return S2_ERR_INVALID_ARG;
     s2_status st = first_error({check_matrix(T, N, lddy), check_matrix(T, K, ldx), check_matrix(N, K, lddw)});
     if (st != S2_OK) return st;
+    // the smallest tiles are counted in 32 bits, and so are the stages of one of the device's blocks or pairs (at least 64)
+    const uint64_t tiles = (N + 31) / 32 * blocks8(K);
+    if (tiles > 0x7fffffffull || tiles * ((T + 63) / 64) >= (1ull << 36)) return S2_ERR_UNSUPPORTED;
     if (N == 0 || K == 0) return S2_OK;
     if (!dw) return S2_ERR_INVALID_ARG;
     const uint64_t esz = size_of(dt);

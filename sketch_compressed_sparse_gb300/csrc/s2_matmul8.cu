@@ -370,7 +370,6 @@ cudaError_t launch(const Matmul8Args& m, Args a, cudaStream_t s) {
     a.tiles_f = (m.N + kBF - 1) / kBF;
     a.tiles_t = (m.M + NT - 1) / NT;
     const uint64_t tiles = (uint64_t)a.tiles_f * a.tiles_t;
-    if (tiles > 0x7fffffffull) return cudaErrorInvalidValue;
     // the operand with the fewer bytes is the one that tiles in a row re-read
     a.tokens_inner = m.M <= m.N;
     auto kernel = matmul8_kernel<NT, CHUNKS>;
@@ -652,7 +651,6 @@ cudaError_t launch_pair(const Matmul8Args& m, Args a, int pairs, cudaStream_t s)
     a.tiles_f = (m.N + 2 * kBF - 1) / (2 * kBF);
     a.tiles_t = (m.M + a.nt - 1) / a.nt;
     const uint64_t tiles = (uint64_t)a.tiles_f * a.tiles_t;
-    if (tiles > 0x7fffffffull) return cudaErrorInvalidValue;
     a.tokens_inner = m.M <= m.N;
     CUtensorMap wmap, xmap;
     cudaError_t e = make_map(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, m.w, m.K, m.N, m.ldw, kBK, kBF);

@@ -715,8 +715,6 @@ cudaError_t launch(const Wgrad8Args& m, Args a, int sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     a.tiles_n = (m.N + a.nt - 1) / a.nt;
     const uint64_t tiles = (uint64_t)a.tiles_k * a.tiles_n;
-    const uint32_t tblocks = (m.T + kBT - 1) / kBT;
-    if (tiles * tblocks > 0xffffffffull) return cudaErrorInvalidValue;
     const uint32_t size = CTAS == 2 ? 2 : a.split;
     const uint32_t grid = size * (uint32_t)(a.split > 1 || tiles < (uint64_t)groups ? tiles : groups);
     return launch_early(kernel, grid, P::kWarps * 32, P::kSmem, size > 1 ? size : 0, s, xmap, ymaps, a);
