@@ -462,7 +462,7 @@ S2_API s2_status s2_wait_faults(uint32_t *host_count);
 /* Human-readable name of a status code (static string). */
 S2_API const char *s2_status_string(s2_status st);
 
-/* Library version string (static). */
+/* Library version string (static); its last word stands for the contents of the s2.h it was built from. */
 S2_API const char *s2_version(void);
 
 #ifdef __cplusplus

@@ -110,6 +110,25 @@ _SIGS = {
 _fns = {}
 
 
+def _short_calls():
+    """The 8-bit layer's calls without ctypes' conversions: the same functions of the same library. Empty
+    where the extension is missing or was compiled from another s2.h than the library."""
+    if not os.path.exists(_CALLS_PATH):
+        return {}
+    spec = importlib.util.spec_from_file_location("_s2calls", _CALLS_PATH)
+    try:
+        calls = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(calls)
+    except ImportError:
+        return {}
+    header = getattr(calls, "header", "unknown")
+    if header == "unknown" or not _fns["s2_version"]().decode().endswith(header):
+        return {}
+    names = ("s2_pack8", "s2_unpack8", "s2_matmul8", "s2_wgrad8")
+    calls.bind(*(ctypes.cast(_fns[n], _vp).value for n in names))
+    return {n: getattr(calls, n) for n in names}
+
+
 def _load():
     """Load libs2.so once; raise ImportError if it has not been built."""
     if _fns:
@@ -124,13 +143,7 @@ def _load():
         f.argtypes = args
         f.restype = res
         _fns[name] = f
-    if os.path.exists(_CALLS_PATH):  # the same functions of the same library, without ctypes' conversions
-        spec = importlib.util.spec_from_file_location("_s2calls", _CALLS_PATH)
-        calls = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(calls)
-        names = ("s2_pack8", "s2_unpack8", "s2_matmul8", "s2_wgrad8")
-        calls.bind(*(ctypes.cast(_fns[n], _vp).value for n in names))
-        _fns.update((n, getattr(calls, n)) for n in names)
+    _fns.update(_short_calls())
     return _fns
 
 

@@ -3,8 +3,8 @@
 Each .cu file compiles to an object in parallel, then nvcc links the shared
 library into ``sketch_compressed_sparse_gb300/_lib/libs2.so``. Where Python's
 headers and a host compiler are installed, ``_s2calls`` (a shorter way from
-Python to the 8-bit layer's calls) is built beside it. The build is skipped
-when the library is newer than every source and header.
+Python to the 8-bit layer's calls) is built beside it. Each is skipped where
+it is newer than its sources and headers.
 
 Usage: ``python -m sketch_compressed_sparse_gb300.build [--force] [--verbose]``.
 """
@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import hashlib
 import os
 import shutil
 import subprocess
@@ -50,12 +51,22 @@ def _python_headers():
     return inc if os.path.exists(os.path.join(inc, "Python.h")) else None
 
 
+def header_flags():
+    """Says in a binary which s2.h it was compiled from: the extension is used only with a library of the same."""
+    with open(HEADER, "rb") as f:
+        return [f"-DS2_HEADER_ID=h{hashlib.sha256(f.read()).hexdigest()[:16]}"]
+
+
+def _older(target, deps) -> bool:
+    return not os.path.exists(target) or any(os.path.getmtime(p) > os.path.getmtime(target) for p in deps)
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB) or (_python_headers() and not os.path.exists(CALLS)):
-        return True
-    t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + [CALLS_SRC, HEADER]
-    return any(os.path.getmtime(p) > t for p in deps)
+    return _older(LIB, sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + [HEADER])
+
+
+def _calls_stale() -> bool:
+    return _python_headers() is not None and _older(CALLS, [CALLS_SRC, os.path.join(CSRC, "s2_header_id.h"), HEADER])
 
 
 def _build_calls() -> None:
@@ -64,7 +75,7 @@ def _build_calls() -> None:
         return
     tmp = CALLS + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I", inc,
-           "-I", os.path.join(ROOT, "include"), CALLS_SRC, "-o", tmp]
+           "-I", os.path.join(ROOT, "include"), *header_flags(), CALLS_SRC, "-o", tmp]
     try:
         r = subprocess.run(cmd, capture_output=True, text=True)
         log = "" if r.returncode == 0 else r.stdout + r.stderr or f"{cmd[0]} failed"
@@ -82,6 +93,8 @@ def _build_calls() -> None:
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile every kernel for sm_103a and link libs2.so; returns its path."""
     if not force and not _stale():
+        if _calls_stale():
+            _build_calls()
         return LIB
     os.makedirs(OBJDIR, exist_ok=True)
     cc = nvcc()
@@ -89,7 +102,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
 
     def compile_one(src):
         obj = os.path.join(OBJDIR, os.path.basename(src).replace(".cu", ".o"))
-        cmd = [cc, *ARCH, *NVCC_FLAGS, *extra, "-I", os.path.join(ROOT, "include"), "-c", src, "-o", obj]
+        cmd = [cc, *ARCH, *NVCC_FLAGS, *header_flags(), *extra, "-I", os.path.join(ROOT, "include"), "-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")

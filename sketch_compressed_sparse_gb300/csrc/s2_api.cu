@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "s2.h"  // include/ is on the include path
+#include "s2_header_id.h"
 #include "s2_internal.h"
 
 namespace s2 {
@@ -826,6 +827,6 @@ const char* s2_status_string(s2_status st) {
     return "S2_UNKNOWN_STATUS";
 }
 
-const char* s2_version(void) { return "libs2 0.1 (sm_103a)"; }
+const char* s2_version(void) { return "libs2 0.1 (sm_103a), s2.h " S2_HEADER_WORD; }
 
 }  // extern "C"

@@ -6,6 +6,7 @@
 #include <Python.h>
 
 #include "s2.h"
+#include "s2_header_id.h"
 
 namespace {
 
@@ -139,4 +140,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_s2calls", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__s2calls() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__s2calls() {
+    PyObject* m = PyModule_Create(&module);
+    // the library's version ends with the same word where both are of one header
+    if (m && PyModule_AddStringConstant(m, "header", S2_HEADER_WORD) < 0) Py_CLEAR(m);
+    return m;
+}
