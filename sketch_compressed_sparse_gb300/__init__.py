@@ -438,7 +438,7 @@ def s2_pipeline_dense_host(host_grad: torch.Tensor, d: int, w: int, seed: int, h
 # ---- the 8-bit layer ----
 
 S2_SCALE_ROWS, S2_SCALE_TILES = 0, 1
-_LAYOUTS = {"rows": S2_SCALE_ROWS, "tiles": S2_SCALE_TILES}
+_LAYOUTS = {"rows": S2_SCALE_ROWS, "tiles": S2_SCALE_TILES, S2_SCALE_ROWS: S2_SCALE_ROWS, S2_SCALE_TILES: S2_SCALE_TILES}
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 _U8, _F32T = torch.uint8, torch.float32
 _BYTES = (_U8,)
@@ -477,7 +477,10 @@ def _scales(t: torch.Tensor, name: str, rows: int, cols: int, layout: int):
 
 
 def _layout(layout) -> int:
-    return _LAYOUTS[layout] if isinstance(layout, str) else int(layout)
+    try:
+        return _LAYOUTS[layout]
+    except (KeyError, TypeError):
+        raise ValueError(f"layout is {layout!r}, expected one of {tuple(_LAYOUTS)}") from None
 
 
 def s2_pack8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, layout="rows",

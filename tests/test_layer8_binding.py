@@ -4,6 +4,8 @@ import os
 import subprocess
 import sys
 
+import pytest
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
@@ -23,3 +25,14 @@ def test_import_without_cuda_in_torch():
             "torch.cuda.current_stream = lambda: type('Stream', (), {'cuda_stream': 7})\n"
             "assert s2._stream(None) == 7\n")
     assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("layout", ["row", "", None, 2, -1, 1 << 32, 1.5])
+def test_unknown_layouts(layout):
+    """A layout is "rows", "tiles" or their constants; nothing is taken for one of them."""
+    import sketch_compressed_sparse_gb300 as s2
+
+    with pytest.raises(ValueError, match="layout"):
+        s2.alloc_pack8(4, 4, layout, device="cpu")
+    for known in ("rows", "tiles", s2.S2_SCALE_ROWS, s2.S2_SCALE_TILES):
+        s2.alloc_pack8(4, 4, known, device="cpu")
