@@ -81,3 +81,28 @@ def test_matmul_bfloat16_does_not_drift(M, N, K):
     assert drift(y, want) <= drift_bound(128, M * N)
     assert float((y.double() - want).norm() / want.norm()) <= 128 * 2.0 ** -24 + 2.0 ** -9
     assert s2.s2_wait_faults() == 0
+
+
+# clusters of two to eight, one block a tile, pairs; aligned and misaligned rows (on 152 SMs)
+@pytest.mark.parametrize("T,N,K", [(6000, 264, 260), (6000, 301, 260), (2100, 130, 130), (4500, 128, 130), (2000, 640, 520),
+                                   (2000, 641, 520), (3000, 1496, 700), (3000, 1497, 700), (3000, 1200, 1100), (3000, 1201, 1100),
+                                   (2000, 2504, 4000), (2000, 2501, 4000), (6000, 4096, 1024), (6000, 4097, 1024)])
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_wgrad_sums(T, N, K, accumulate, dtype):
+    """44 additions of 16 in a chunk of a float32 result, 128 of a bfloat16 one; T/704 + 1 chunks, eight
+    parts and what was there before at most, each added with a rounding; the last one 2^-9 in bfloat16.
+    A token that is left out or taken twice is off by about 1 / sqrt(T), 4000 times the float32 bound."""
+    xc, xs = packed_here(T, K, 1)
+    dy = normal(T, N, 2, torch.bfloat16)
+    dw = normal(N, K, 3, dtype)
+    want = dy.double().T @ values(xc, xs)
+    size = want.norm()
+    if accumulate:
+        want += dw.double()
+        size = size + dw.double().norm()
+    s2.s2_wgrad8(dy, xc, xs, dw, accumulate)
+    additions = 44 if dtype == torch.float32 else 128
+    bound = (additions + (T / 704 + 1 + 8 + 1) ** 0.5) * 2.0 ** -24 + (2.0 ** -9 if dtype == torch.bfloat16 else 0)
+    assert float((dw.double() - want).norm() / size) <= bound
+    assert s2.s2_wait_faults() == 0
