@@ -102,8 +102,12 @@ def batches(vocab, hidden, tokens, workers, steps, device="cuda", seed=1):
 def train(vocab=1003, hidden=256, tokens=512, workers=4, steps=20, lr=20.0):
     layer = SoftmaxLayer(vocab, hidden, tokens, workers)
     dhidden = torch.empty((workers, tokens, hidden), device="cuda")
+    before = s2.s2_wait_faults()
     losses = [layer.step(h, t, dhidden, lr) for h, t in batches(vocab, hidden, tokens, workers, steps)]
-    return [float(v) for v in losses]
+    losses = [float(v) for v in losses]
+    if s2.s2_wait_faults() != before:  # a kernel gave up a wait: what it wrote is not valid
+        raise RuntimeError("a wait in the layer's kernels ran out")
+    return losses
 
 
 if __name__ == "__main__":

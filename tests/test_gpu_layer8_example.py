@@ -51,3 +51,13 @@ def test_gradients_of_a_step(example):
         gv = ref.unpack(gc, gs, False)
         got = dhidden[k].double().cpu().numpy()
         assert (np.abs(got - gv @ wv) <= (V + 41) * 2.0 ** -23 * (np.abs(gv) @ np.abs(wv))).all()
+
+
+def test_waits_that_ran_out_end_the_training(example, monkeypatch):
+    """The count is asked before and after the steps; one that rises is an error and no list of losses."""
+    counts = iter([3, 3])
+    monkeypatch.setattr(example.s2, "s2_wait_faults", lambda: next(counts))
+    assert len(example.train(steps=1)) == 1
+    counts = iter([3, 4])
+    with pytest.raises(RuntimeError):
+        example.train(steps=1)
