@@ -436,7 +436,8 @@ S2_API s2_status s2_matmul8(const uint8_t *x, uint64_t ldx, const uint8_t *x_sca
  *   dw[n][k] = sum over t of dy[t][n] * X[t][k], of type dt, with
  *   dy [T][N] bfloat16 (row stride lddy, any alignment) and X [T][K] packed
  *   with S2_SCALE_ROWS. X's values are exact in bfloat16 (scale bytes 10 to
- *   247, as s2_pack8 writes them; others are rounded), the sums are float32.
+ *   247, as s2_pack8 writes them, values below 2^128; smaller ones are
+ *   rounded, larger ones are infinite), the sums are float32.
  *   accumulate != 0: dw += the sum instead (one more rounding), for a
  *   gradient taken over several batches. Long sums are taken in chunks of
  *   at most 704 tokens (float32 results) or 2048 (bfloat16), which are

@@ -14,7 +14,7 @@
 // Measured: one token by 4096 x 4096 5.1 us in a CUDA graph (a launch, the
 // pipeline's fill and 16.8 MB that come from L2); 24 tokens by 267735 x 1024
 // into float32 50.0 us, 0.88 of a copy's rate for its 300 MB; 500 x 2000 x 1024
-// 4.8 us; 8192 x 4096 x 4096 96 us in a long loop (2.8 PFLOP/s, power-capped)
+// 4.8 us; 8192 x 4096 x 4096 95 us in a long loop (2.9 PFLOP/s, power-capped)
 // and 80 us for ten in a row (3.4); 2048 x 267735 x 1024 into bfloat16 540 us.
 #include "s2_internal.h"
 #include "s2_launch.cuh"
@@ -32,16 +32,19 @@ constexpr int kWarps = 10;               // 0-3 store, 4-7 scales, 8 copies, 9 p
 constexpr uint32_t kABytes = kBF * kBK;  // W part of a stage
 
 // The tensor cores cut off what they add to a float32 sum, so a long sum drifts
-// towards zero: by 4e-7 of itself at K = 4096, 3e-6 at 16384 and 1.3e-5 at
-// 65536. A float32 result is therefore taken in chunks of 32 blocks of K (4e-7
-// at any length; a float32 product of the unpacked values is off by 3.5e-7 and
-// 8e-7 at the longer two), and the sum of chunks stays in tensor memory beside
-// the two accumulators. That leaves a pair 160 tokens a tile where it has 224:
+// towards zero. Normal inputs, relative error of one sum: 2.2e-7 at K = 4096,
+// 1.2e-6 at 16384, 7.7e-6 at 65536, 1.9e-5 at 131072 (a float32 product of the
+// unpacked values: 8e-8, 1.9e-7, 4.9e-7, 7.9e-7); twice that where a few
+// channels are far larger. A float32 result is therefore taken in chunks of 32
+// blocks of K that are added with rounding: 2.2e-7 at 16384, 2.3e-7 at 65536 (the
+// additions' own roundings grow with the root of their number: 3.1e-7 at K = 2^22,
+// in eight parts). The sum of chunks stays in tensor memory beside the two
+// accumulators. That leaves a pair 160 tokens a tile where it has 224:
 // 2048 x 1024 x 267735 505 -> 513 us, 8192 x 4096 x 16384 336 -> 369 us. Adding
 // to Y in global memory kept the 224 and took 592 and 367.
 constexpr uint32_t kChunk = 32;
 // A bfloat16 result is rounded by up to 2^-9 of itself. Up to this many blocks of
-// K it is taken in one chunk, which loses at most 1.6e-5, a 120th of that, and
+// K it is taken in one chunk, which loses 7.7e-6 to 1.6e-5, a 120th of that, and
 // keeps the 224 tokens (8192 x 4096 x 8192 150 us, in chunks 180; 2048 x 8192 x
 // 28672 352 and 426). Beyond, the loss would go on growing with K, always towards
 // zero (4e-5 at 267735), and chunks are taken: 2048 x 4096 x 66048 367 -> 374 us,
@@ -392,9 +395,10 @@ cudaError_t launch(const Matmul8Args& m, Args a, cudaStream_t s) {
 // active 0.80 of the time). It did not get shorter with a copying warp for each
 // operand, with scale words fetched a group ahead, with twice the storing
 // warps, nor with clusters of two pairs that share the tokens' copies (23 KB a
-// block and stage). With K = 1024 the stores bind: 2048 x 267735 takes 453 us
-// into bfloat16 and 533 us into twice the bytes in as many requests, 371 us
-// without stores; at K = 128 the stores alone take 393. Turning bfloat16 through
+// block and stage). With K = 1024 the stores bind: 2048 x 267735 takes, ten in a
+// row, 453 us into bfloat16 and 533 us into twice the bytes in as many requests,
+// 371 us without stores (540 into bfloat16 in a long loop, at a lower clock); at
+// K = 128 the stores alone take 393. Turning bfloat16 through
 // shared memory for longer requests, or for whole 32-byte sectors where rows
 // start on odd addresses, took more time than it saved.
 template <bool CHUNKS>

@@ -19,7 +19,7 @@
 // Measured: 200 tokens, 512 x 512 4.4 us in a CUDA graph; 8192 tokens, 4096 x 4096
 // into bfloat16 196 us in a long loop (1.40 PFLOP/s, 0.73 of a cuBLAS product at
 // its burst rate) and 177 us for ten in a row; 2048 tokens, 267735 x 1024, odd
-// rows, into float32 1.05 ms (1.07 PFLOP/s).
+// rows, into float32 1.03 ms (1.09 PFLOP/s).
 #include "s2_chunks.h"
 #include "s2_internal.h"
 #include "s2_launch.cuh"
@@ -34,17 +34,20 @@ constexpr int kBT = 64;                    // tokens per stage
 constexpr int kBF = 128;                   // features per tile
 constexpr uint32_t kGroupBytes = kBT * 128;  // 64 outputs or features by kBT tokens
 constexpr uint32_t kABytes = 2 * kGroupBytes;
-// The tensor cores add to their float32 sums with truncation, which loses
-// 2e-8 of the sum for every 16 tokens on average (2.4e-6 at 2048 tokens, where
-// a float32 matrix product loses 4e-7). So a float32 result is taken in chunks
-// of at most kChunk stages that are added up with rounding: 8e-7 at any length.
+// The tensor cores add to their float32 sums with truncation. Normal inputs,
+// relative error of one sum: 6.4e-7 at 2048 tokens, 3.7e-6 at 8192, 4.8e-5 at
+// 65536 (a float32 matrix product: 1.5e-7, 3.6e-7, 1.5e-6); 2.4e-6 and 9.5e-6 at
+// the first two with heavy-tailed gradients. So a float32 result is taken in
+// chunks of at most kChunk stages that are added up with rounding: 1.9e-7 up to
+// 8192 tokens, 2.6e-7 at 65536, 4.0e-7 at 262144 (the additions' own roundings
+// grow with the root of their number); heavy-tailed 8e-7 at 2048.
 // The sum stays in tensor memory, in the accumulator of the tile's first chunk;
 // later chunks use the other one, and the products wait only while it is added
 // (additions in L2 or through registers took twice as long in all).
 constexpr uint32_t kChunk = 11;
 // A bfloat16 result is rounded by up to 2^-9 of itself, so its chunks are longer:
-// 2048 tokens lose 2.4e-6, an 800th of that, at any number of tokens. (One chunk
-// lost 9.5e-6 at 8192 tokens, growing with their number and always towards zero;
+// 2048 tokens lose 6e-7 to 2.4e-6, at most an 800th of that, whatever the number
+// of chunks. (One chunk went on growing with the tokens, always towards zero;
 // 8192 x 4096 x 4096, ten in a row: one chunk 172 us, chunks of 32 stages 177, of 11 198.)
 constexpr uint32_t kChunk16 = 32;
 constexpr int kLoaders = 8;                // warps that shift a misaligned dY into place

@@ -8,6 +8,9 @@ n outputs the mean of sign(exact) (y - exact) over the mean of |exact| is theref
     additions of a chunk * 2^-24 + 6 * 2^-9 / sqrt(n)
 in magnitude, with six standard deviations (each below 2^-9) for the roundings, whose sizes grow with
 the outputs as |exact| does (their mean square over their squared mean is below 2: n is halved).
+
+A float32 and a bfloat16 result are the same sums, rounded once more, only where both are one chunk
+(up to 704 tokens in a block, up to 4096 of K); beyond, their chunks differ.
 """
 import pytest
 import torch
