@@ -43,12 +43,12 @@ constexpr uint32_t kABytes = kBF * kBK;  // W part of a stage
 // 2048 x 1024 x 267735 505 -> 513 us, 8192 x 4096 x 16384 336 -> 369 us. Adding
 // to Y in global memory kept the 224 and took 592 and 367.
 constexpr uint32_t kChunk = 32;
-// A bfloat16 result is rounded by up to 2^-9 of itself. Up to this many blocks of
-// K it is taken in one chunk, which loses 7.7e-6 to 1.6e-5, a 120th of that, and
-// keeps the 224 tokens (8192 x 4096 x 8192 150 us, in chunks 180; 2048 x 8192 x
-// 28672 352 and 426). Beyond, the loss would go on growing with K, always towards
-// zero (4e-5 at 267735), and chunks are taken: 2048 x 4096 x 66048 367 -> 374 us,
-// 8192 x 4096 x 66048 1.28 -> 1.55 ms.
+// A bfloat16 result is rounded by up to 2^-8 of itself, 1.7e-3 in the mean square.
+// Up to this many blocks of K it is taken in one chunk, which loses 7.7e-6 to
+// 1.6e-5, a 100th of that, and keeps the 224 tokens (8192 x 4096 x 8192 150 us, in
+// chunks 180; 2048 x 8192 x 28672 352 and 426). Beyond, the loss would go on growing
+// with K, always towards zero (4e-5 at 267735), and chunks are taken: 2048 x 4096 x
+// 66048 367 -> 374 us, 8192 x 4096 x 66048 1.28 -> 1.55 ms.
 constexpr uint32_t kLong16 = 512;
 static_assert(kChunk % kGroup == 0, "chunks end between two scale words");
 

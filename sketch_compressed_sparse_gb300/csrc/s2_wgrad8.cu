@@ -45,10 +45,11 @@ constexpr uint32_t kABytes = 2 * kGroupBytes;
 // later chunks use the other one, and the products wait only while it is added
 // (additions in L2 or through registers took twice as long in all).
 constexpr uint32_t kChunk = 11;
-// A bfloat16 result is rounded by up to 2^-9 of itself, so its chunks are longer:
-// 2048 tokens lose 6e-7 to 2.4e-6, at most an 800th of that, whatever the number
-// of chunks. (One chunk went on growing with the tokens, always towards zero;
-// 8192 x 4096 x 4096, ten in a row: one chunk 172 us, chunks of 32 stages 177, of 11 198.)
+// A bfloat16 result is rounded by up to 2^-8 of itself, 1.7e-3 in the mean square,
+// so its chunks are longer: 2048 tokens lose 6e-7 to 2.4e-6, at most a 700th of
+// that, whatever the number of chunks. (One chunk went on growing with the tokens,
+// always towards zero; 8192 x 4096 x 4096, ten in a row: one chunk 172 us, chunks of
+// 32 stages 177, of 11 198.)
 constexpr uint32_t kChunk16 = 32;
 constexpr int kLoaders = 8;                // warps that shift a misaligned dY into place
 

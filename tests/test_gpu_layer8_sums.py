@@ -3,10 +3,10 @@ a cluster, tiles of one block, pairs of blocks, aligned and misaligned rows.
 
 The tensor cores cut off what they add, on average half a unit, at most 2^-24 of a chunk's own sum,
 for each of the chunk's additions: always towards zero, so that a bfloat16 result's own rounding
-(at most 2^-9 of the value, of either sign) hides it in one output and not in the mean of many. With
+(2^-9 of the value in the mean square, of either sign) hides it in one output and not in the mean of many. With
 n outputs the mean of sign(exact) (y - exact) over the mean of |exact| is therefore at most
     additions of a chunk * 2^-24 + 6 * 2^-9 / sqrt(n)
-in magnitude, with six standard deviations (each below 2^-9) for the roundings, whose sizes grow with
+in magnitude, with six standard deviations (each below 2^-9 on average) for the roundings, whose sizes grow with
 the outputs as |exact| does (their mean square over their squared mean is below 2: n is halved).
 
 A float32 and a bfloat16 result are the same sums, rounded once more, only where both are one chunk
@@ -94,7 +94,8 @@ def test_matmul_bfloat16_does_not_drift(M, N, K):
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_wgrad_sums(T, N, K, accumulate, dtype):
     """44 additions of 16 in a chunk of a float32 result, 128 of a bfloat16 one; T/704 + 1 chunks, eight
-    parts and what was there before at most, each added with a rounding; the last one 2^-9 in bfloat16.
+    parts and what was there before at most, each added with a rounding; the last one 2^-9 in
+    the mean square in bfloat16.
     A token that is left out or taken twice is off by about 1 / sqrt(T), 4000 times the float32 bound."""
     xc, xs = packed_here(T, K, 1)
     dy = normal(T, N, 2, torch.bfloat16)
