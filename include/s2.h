@@ -453,8 +453,60 @@ S2_API s2_status s2_wgrad8(const void *dy, uint64_t lddy, const uint8_t *x, uint
                            s2_stream_t stream);
 
 /*
- * s2_wait_faults -- how many waits inside s2_matmul8 and s2_wgrad8 kernels
- * ran out on the current device since the library was loaded (0 unless
+ * The 4-bit layer -- a layer that is only read: a trained layer that serves,
+ * or a teacher. Its weights and the activations that meet them are kept in
+ * microscaled 4-bit floating point (MXFP4) and multiplied in 4 bits.
+ *
+ * Packed matrix [rows][cols]: codes, two to a byte, the earlier element in the
+ * low half (the unused half of an odd row's last byte is 0); row stride ldc in
+ * bytes, base 16-byte aligned and ldc a multiple of 16 (S2_ERR_ALIGNMENT;
+ * bytes between a row's end and the next row are neither read nor written).
+ * A code is an e2m1 number: sign, then 0, 0.5, 1, 1.5, 2, 3, 4 or 6. Each 32
+ * elements of a row share a scale byte: b stands for 2^(b - 127), 255 for NaN.
+ * Scale bytes lie in tiles of 512, one for each 128 rows by 128 columns, tile
+ * row after tile row, in the order in which the tensor cores take them: row
+ * r's byte for block j is byte (r%32)*16 + (r%128)/32*4 + j%4 of tile
+ * (r/128) * ceil(cols/128) + j/4. Bytes of rows and blocks past the end exist
+ * and are not 255 (s2_pack4 writes 127). s2_pack4_scales_size gives their
+ * number, 512 * ceil(rows/128) * ceil(cols/128); base 16-byte aligned.
+ * Sizes up to 2^31 - 1, strides as in the 8-bit layer. A size of zero is valid.
+ * Make the first s2_matmul4 on a device before any stream capture (it looks up
+ * an address there).
+ */
+S2_API s2_status s2_pack4_scales_size(uint64_t rows, uint64_t cols, size_t *bytes);
+
+/*
+ * s2_pack4 -- x [rows][cols] of type dt (row stride ldx in elements) to codes
+ * and scales. A block's scale is the least 2^e, e >= -125, with no element
+ * above 6 * 2^e; a code is its element divided by the scale, rounded to
+ * nearest, ties to the even code, the sign kept. A block that holds a NaN or
+ * an infinity gets the scale byte 255 and codes of 0: all its values are NaN
+ * (4 bits hold neither). So the bytes are 2..253, or 255, and code * scale is
+ * exact in float32 and bfloat16, except that an element above 1.75 * 2^127
+ * rounds up to 2^128, which neither type holds: infinity.
+ */
+S2_API s2_status s2_pack4(const void *x, s2_dtype dt, uint64_t rows, uint64_t cols, uint64_t ldx, uint8_t *codes,
+                          uint64_t ldc, uint8_t *scales, s2_stream_t stream);
+
+/* s2_unpack4 -- the values of a packed matrix: out [rows][cols] of type dt, row stride ldo. */
+S2_API s2_status s2_unpack4(const uint8_t *codes, uint64_t ldc, const uint8_t *scales, uint64_t rows, uint64_t cols,
+                            void *out, s2_dtype dt, uint64_t ldo, s2_stream_t stream);
+
+/*
+ * s2_matmul4 -- y[m][n] = sum over k of X[m][k] * W[n][k], of type dt, with X
+ *   [M][K] (a layer's input) and W [N][K] (its weight) packed by s2_pack4.
+ *   Sums are float32, in chunks of at most 8192 k that are added up in float32
+ *   (a bfloat16 result's only where K > 131072); one rounding to dt. The
+ *   result does not depend on timing. Serves one token (M = 1) as well as a
+ *   batch. ceil(M/16) * ceil(N/128) must be below 2^31 (S2_ERR_UNSUPPORTED).
+ */
+S2_API s2_status s2_matmul4(const uint8_t *x, uint64_t ldx, const uint8_t *x_scales, const uint8_t *w, uint64_t ldw,
+                            const uint8_t *w_scales, uint64_t M, uint64_t N, uint64_t K, void *y, s2_dtype dt,
+                            uint64_t ldy, s2_stream_t stream);
+
+/*
+ * s2_wait_faults -- how many waits inside s2_matmul8, s2_wgrad8 and
+ * s2_matmul4 kernels ran out on the current device since the library was loaded (0 unless
  * something is broken; outputs of the call concerned are not valid then).
  * host_count is HOST memory; this call, a diagnostic, waits for the device.
  */

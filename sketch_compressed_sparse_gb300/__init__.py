@@ -52,6 +52,10 @@ __all__ = [
     "s2_unpack8",
     "s2_matmul8",
     "s2_wgrad8",
+    "s2_pack4_scales_size",
+    "s2_pack4",
+    "s2_unpack4",
+    "s2_matmul4",
     "s2_wait_faults",
     "S2_SCALE_ROWS",
     "S2_SCALE_TILES",
@@ -103,6 +107,10 @@ _SIGS = {
     "s2_unpack8": ([_vp, _u64, _vp, _i32, _u64, _u64, _vp, _i32, _u64, _vp], _i32),
     "s2_matmul8": ([_vp, _u64, _vp, _vp, _u64, _vp, _i32, _u64, _u64, _u64, _vp, _i32, _u64, _vp], _i32),
     "s2_wgrad8": ([_vp, _u64, _vp, _u64, _vp, _u64, _u64, _u64, _vp, _i32, _u64, _i32, _vp], _i32),
+    "s2_pack4_scales_size": ([_u64, _u64, ctypes.POINTER(_sz)], _i32),
+    "s2_pack4": ([_vp, _i32, _u64, _u64, _u64, _vp, _u64, _vp, _vp], _i32),
+    "s2_unpack4": ([_vp, _u64, _vp, _u64, _u64, _vp, _i32, _u64, _vp], _i32),
+    "s2_matmul4": ([_vp, _u64, _vp, _vp, _u64, _vp, _u64, _u64, _u64, _vp, _i32, _u64, _vp], _i32),
     "s2_wait_faults": ([ctypes.POINTER(_u32)], _i32),
     "s2_status_string": ([_i32], ctypes.c_char_p),
     "s2_version": ([], ctypes.c_char_p),
@@ -552,6 +560,67 @@ def s2_wgrad8(dy: torch.Tensor, x: torch.Tensor, x_scales: torch.Tensor, dw: tor
         raise S2Error(st, "s2_wgrad8")
 
 
+# ---- the 4-bit layer ----
+
+def s2_pack4_scales_size(rows: int, cols: int) -> int:
+    """Scale bytes of a 4-bit matrix."""
+    b = _sz()
+    _check(_f("s2_pack4_scales_size")(rows, cols, ctypes.byref(b)), "s2_pack4_scales_size")
+    return int(b.value)
+
+
+def _scales4(t: torch.Tensor, name: str, rows: int, cols: int):
+    """(16 bytes alignment is checked by the library)"""
+    need = ((rows + 127) >> 7) * ((cols + 127) >> 7) << 9
+    if t.is_cuda and t.dtype is _U8 and t.numel() >= need and t.is_contiguous():
+        return t.data_ptr()
+    return _dev(t, name, _BYTES, need)  # says what is wrong
+
+
+def s2_pack4(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
+    """x [rows, cols] -> codes [rows, ceil(cols / 2)] (two elements a byte, rows on 16 bytes) and scale bytes
+    (s2_pack4_scales_size of them, in tiles of 512)."""
+    px, rows, cols, ldx = _mat(x, "x", _GRAD)
+    pc, r, c, ldc = _mat(codes, "codes", _BYTES)
+    if r != rows or c != (cols + 1) >> 1:
+        _refuse_shape(codes, "codes", rows, (cols + 1) >> 1)
+    st = _f("s2_pack4")(px, S2_F32 if x.dtype is _F32T else S2_BF16, rows, cols, ldx, pc, ldc,
+                        _scales4(scales, "scales", rows, cols), _stream(stream))
+    if st:
+        raise S2Error(st, "s2_pack4")
+
+
+def s2_unpack4(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor, stream=None) -> None:
+    """The values of a 4-bit matrix: codes [rows, ceil(cols / 2)] and scale bytes -> out [rows, cols]."""
+    po, rows, cols, ldo = _mat(out, "out", _GRAD)
+    pc, r, c, ldc = _mat(codes, "codes", _BYTES)
+    if r != rows or c != (cols + 1) >> 1:
+        _refuse_shape(codes, "codes", rows, (cols + 1) >> 1)
+    st = _f("s2_unpack4")(pc, ldc, _scales4(scales, "scales", rows, cols), rows, cols, po,
+                          S2_F32 if out.dtype is _F32T else S2_BF16, ldo, _stream(stream))
+    if st:
+        raise S2Error(st, "s2_unpack4")
+
+
+def s2_matmul4(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, y: torch.Tensor,
+               stream=None) -> None:
+    """y [M, N] = X W^T of 4-bit X [M, K] and W [N, K], given by their codes of K / 2 bytes a row (K odd: the
+    last half byte is 0 in both, and adds nothing)."""
+    px, M, c, ldx = _mat(x, "x", _BYTES)
+    pw, N, cw, ldw = _mat(w, "w", _BYTES)
+    if cw != c:
+        _refuse_shape(w, "w", N, c)
+    py, r, cy, ldy = _mat(y, "y", _GRAD)
+    if r != M or cy != N:
+        _refuse_shape(y, "y", M, N)
+    K = 2 * c
+    st = _f("s2_matmul4")(px, ldx, _scales4(x_scales, "x_scales", M, K), pw, ldw,
+                          _scales4(w_scales, "w_scales", N, K), M, N, K, py, S2_F32 if y.dtype is _F32T else S2_BF16,
+                          ldy, _stream(stream))
+    if st:
+        raise S2Error(st, "s2_matmul4")
+
+
 def s2_wait_faults() -> int:
     """Waits of the tensor-core kernels that ran out on the current device (waits for the device)."""
     c = _u32()
@@ -572,3 +641,10 @@ def alloc_pack8(rows: int, cols: int, layout="rows", device="cuda") -> Tuple[tor
     codes = torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.uint8, device=device)[:, :cols]
     srows = (rows + 127) // 128 if _layout(layout) == S2_SCALE_TILES else rows
     return codes, torch.empty((srows, (cols + 127) // 128), dtype=torch.uint8, device=device)
+
+
+def alloc_pack4(rows: int, cols: int, device="cuda") -> Tuple[torch.Tensor, torch.Tensor]:
+    """Codes [rows, ceil(cols / 2)] whose rows start on 16 bytes, and scale bytes, for s2_pack4."""
+    codes = torch.empty((rows, (cols + 31) // 32 * 16), dtype=torch.uint8, device=device)[:, :(cols + 1) // 2]
+    n = (rows + 127) // 128 * ((cols + 127) // 128) * 512
+    return codes, torch.empty(n, dtype=torch.uint8, device=device)

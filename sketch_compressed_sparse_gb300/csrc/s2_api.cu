@@ -330,6 +330,20 @@ inline s2_status check_codes(const void* codes, uint64_t rows, uint64_t cols, ui
     return aligned(codes, 16) && (rows <= 1 || ld % 16 == 0) ? S2_OK : S2_ERR_ALIGNMENT;
 }
 
+// ---- 4-bit layer ----
+constexpr uint64_t kMaxItems4 = 0x7fffffffull * 8;  // a warp each, eight warps a block
+
+inline uint64_t bytes4(uint64_t cols) { return (cols + 1) / 2; }
+inline uint64_t scales4(uint64_t rows, uint64_t cols) { return blocks8(rows) * blocks8(cols) * 512; }
+
+// A packed matrix: rows of codes start on 16 bytes, and so do the scales.
+inline s2_status check_packed4(const void* codes, uint64_t rows, uint64_t cols, uint64_t ldc, const void* scales) {
+    if (!scales) return S2_ERR_INVALID_ARG;
+    const s2_status st = check_codes(codes, rows, bytes4(cols), ldc);
+    if (st != S2_OK) return st;
+    return aligned(scales, 16) ? S2_OK : S2_ERR_ALIGNMENT;
+}
+
 // Row stride of codes for their tensor map, which wants a multiple of 16; that of a single row is free.
 inline uint64_t stride16(uint64_t rows, uint64_t cols, uint64_t ld) { return rows > 1 ? ld : (cols + 15) / 16 * 16; }
 
@@ -809,6 +823,76 @@ s2_status s2_wgrad8(const void* dy, uint64_t lddy, const uint8_t* x, uint64_t ld
     Wgrad8Args a{dy, x, x_scales, dw, T > 1 ? lddy : (N + 7) / 8 * 8, stride16(T, K, ldx), lddw, (uint32_t)T, (uint32_t)N, (uint32_t)K,
                  dt == S2_F32 ? 0 : 1, accumulate != 0};
     return cuda_status(launch_wgrad8(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+s2_status s2_pack4_scales_size(uint64_t rows, uint64_t cols, size_t* bytes) {
+    if (!bytes) return S2_ERR_INVALID_ARG;
+    if (rows > kMaxDim8 || cols > kMaxDim8) return S2_ERR_UNSUPPORTED;
+    *bytes = scales4(rows, cols);
+    return S2_OK;
+}
+
+s2_status s2_pack4(const void* x, s2_dtype dt, uint64_t rows, uint64_t cols, uint64_t ldx, uint8_t* codes, uint64_t ldc,
+                   uint8_t* scales, s2_stream_t stream) {
+    if (!dtype_ok(dt)) return S2_ERR_INVALID_ARG;
+    s2_status st = check_matrix(rows, cols, ldx);
+    if (st != S2_OK) return st;
+    const uint64_t items = blocks8(rows) * blocks8(cols) * 16;
+    if (items > kMaxItems4) return S2_ERR_UNSUPPORTED;
+    if (rows == 0 || cols == 0) return S2_OK;
+    if (!x) return S2_ERR_INVALID_ARG;
+    st = check_packed4(codes, rows, cols, ldc, scales);
+    if (st != S2_OK) return st;
+    if (!aligned(x, size_of(dt))) return S2_ERR_ALIGNMENT;
+    if (clash({{codes, extent(rows, bytes4(cols), ldc, 1)}, {scales, scales4(rows, cols)},
+               {x, extent(rows, cols, ldx, size_of(dt))}}, 2))
+        return S2_ERR_INVALID_ARG;
+    Pack4Args a{x, ldx, codes, ldc, scales, rows, (uint32_t)cols, (uint32_t)blocks8(cols), items};
+    return cuda_status(launch_pack4(a, dt == S2_F32 ? 0 : 1, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+s2_status s2_unpack4(const uint8_t* codes, uint64_t ldc, const uint8_t* scales, uint64_t rows, uint64_t cols, void* out,
+                     s2_dtype dt, uint64_t ldo, s2_stream_t stream) {
+    if (!dtype_ok(dt)) return S2_ERR_INVALID_ARG;
+    s2_status st = check_matrix(rows, cols, ldo);
+    if (st != S2_OK) return st;
+    const uint64_t items = blocks8(rows) * blocks8(cols) * 16;
+    if (items > kMaxItems4) return S2_ERR_UNSUPPORTED;
+    if (rows == 0 || cols == 0) return S2_OK;
+    if (!out) return S2_ERR_INVALID_ARG;
+    st = check_packed4(codes, rows, cols, ldc, scales);
+    if (st != S2_OK) return st;
+    if (!aligned(out, size_of(dt))) return S2_ERR_ALIGNMENT;
+    if (clash({{out, extent(rows, cols, ldo, size_of(dt))}, {codes, extent(rows, bytes4(cols), ldc, 1)},
+               {scales, scales4(rows, cols)}}, 1))
+        return S2_ERR_INVALID_ARG;
+    Unpack4Args a{codes, ldc, scales, out, ldo, rows, (uint32_t)cols, (uint32_t)blocks8(cols), items};
+    return cuda_status(launch_unpack4(a, dt == S2_F32 ? 0 : 1, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+s2_status s2_matmul4(const uint8_t* x, uint64_t ldx, const uint8_t* x_scales, const uint8_t* w, uint64_t ldw,
+                     const uint8_t* w_scales, uint64_t M, uint64_t N, uint64_t K, void* y, s2_dtype dt, uint64_t ldy,
+                     s2_stream_t stream) {
+    if (!dtype_ok(dt)) return S2_ERR_INVALID_ARG;
+    s2_status st = first_error({check_matrix(M, N, ldy), check_matrix(M, bytes4(K), ldx), check_matrix(N, bytes4(K), ldw)});
+    if (st != S2_OK) return st;
+    // the smallest tiles are counted in 32 bits; K as a size has the limit of the others
+    if (K > kMaxDim8 || (M + 15) / 16 * blocks8(N) > 0x7fffffffull) return S2_ERR_UNSUPPORTED;
+    if (M == 0 || N == 0) return S2_OK;
+    if (!y) return S2_ERR_INVALID_ARG;
+    const uint64_t esz = size_of(dt);
+    if (!aligned(y, esz)) return S2_ERR_ALIGNMENT;
+    if (K == 0)  // an empty sum
+        return cuda_status(cudaMemset2DAsync(y, (M > 1 ? ldy : N) * esz, 0, N * esz, M,
+                                             reinterpret_cast<cudaStream_t>(stream)));
+    st = first_error({check_packed4(x, M, K, ldx, x_scales), check_packed4(w, N, K, ldw, w_scales)});
+    if (st != S2_OK) return st;
+    if (clash({{y, extent(M, N, ldy, esz)}, {x, extent(M, bytes4(K), ldx, 1)}, {x_scales, scales4(M, K)},
+               {w, extent(N, bytes4(K), ldw, 1)}, {w_scales, scales4(N, K)}}, 1))
+        return S2_ERR_INVALID_ARG;
+    Matmul4Args a{x, x_scales, w, w_scales, y, stride16(M, bytes4(K), ldx), stride16(N, bytes4(K), ldw), ldy,
+                  (uint32_t)M, (uint32_t)N, (uint32_t)K, dt == S2_F32 ? 0 : 1};
+    return cuda_status(launch_matmul4(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 s2_status s2_wait_faults(uint32_t* host_count) {

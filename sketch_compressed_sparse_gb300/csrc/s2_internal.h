@@ -185,6 +185,45 @@ struct Wgrad8Args {
 };
 cudaError_t launch_wgrad8(const Wgrad8Args& a, cudaStream_t s);
 
+// ---- 4-bit layer: packing, product of packed matrices ------------------------
+struct Pack4Args {
+    const void* x;
+    uint64_t ldx;
+    uint8_t* codes;
+    uint64_t ldc;
+    uint8_t* scales;  // tiles of 512 bytes
+    uint64_t rows;
+    uint32_t cols;
+    uint32_t tcols;  // tiles per row of tiles
+    uint64_t items;  // 16 per tile
+};
+struct Unpack4Args {
+    const uint8_t* codes;
+    uint64_t ldc;
+    const uint8_t* scales;
+    void* out;
+    uint64_t ldo;
+    uint64_t rows;
+    uint32_t cols;
+    uint32_t tcols;
+    uint64_t items;
+};
+// dtype: 0 = f32, 1 = bf16; at least one element.
+cudaError_t launch_pack4(const Pack4Args& a, int dtype, cudaStream_t s);
+cudaError_t launch_unpack4(const Unpack4Args& a, int dtype, cudaStream_t s);
+
+struct Matmul4Args {
+    const uint8_t* x;  // [M][K] codes, row stride ldx bytes
+    const uint8_t* xs;
+    const uint8_t* w;  // [N][K] codes, row stride ldw bytes
+    const uint8_t* ws;
+    void* y;  // [M][N], row stride ldy
+    uint64_t ldx, ldw, ldy;
+    uint32_t M, N, K;
+    int dtype;  // of y: 0 = f32, 1 = bf16
+};
+cudaError_t launch_matmul4(const Matmul4Args& a, cudaStream_t s);
+
 // Waits of the tensor-core kernels that ran out on the current device.
 cudaError_t read_wait_faults(uint32_t* count);
 
