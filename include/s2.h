@@ -504,6 +504,47 @@ S2_API s2_status s2_matmul4(const uint8_t *x, uint64_t ldx, const uint8_t *x_sca
                             const uint8_t *w_scales, uint64_t M, uint64_t N, uint64_t K, void *y, s2_dtype dt,
                             uint64_t ldy, s2_stream_t stream);
 
+/* Weights and temperature of s2_distill. */
+typedef struct {
+    float temperature; /* of the teacher's and the student's softmax in the soft term; above 0, and 1 / temperature finite */
+    float soft;        /* weight of the soft term (temperature^2 keeps its gradient's size) */
+    float hard;        /* weight of the cross entropy with the targets */
+    float scale;       /* of the gradient alone, 1 / tokens for a mean */
+} s2_distill_params;
+
+/*
+ * s2_distill -- a softmax layer's loss against a teacher's top logits, and its
+ * gradient, which s2_wgrad8 and s2_pack8 take on to the layer.
+ *   logits [T][V] of type dt, row stride ld: the student's.
+ *   teacher_idx [T][K] int32 and teacher [T][K] float32: indices and logits of
+ *   the teacher's largest, contiguous, in any order. Entries whose index is
+ *   not in [0, V) do not count (a shorter list); an index that stands there
+ *   twice counts twice. q = softmax(teacher / temperature) over a row's entries.
+ *   targets [T] int32: the words that followed; one outside [0, V) has no
+ *   cross entropy. Null (with hard = 0 or not): none has.
+ *   row_weight [T] float32, or null for 1: multiplies the row's loss and
+ *   gradient. Where it is 0 both are 0, whatever the row holds (padding).
+ *   loss [T] float32 out: row_weight * (soft * sum over k of q_k * (log q_k -
+ *   log softmax(logits / temperature)[idx_k]) + hard * -log softmax(logits)[target]).
+ *   A row without entries of weight has no soft term, in the gradient neither.
+ *   dlogits [T][V] of type ddt, row stride ldd, out, or null for the loss
+ *   alone: scale times the derivative of loss[t] by logits[t], rounded once.
+ *   A logit of -infinity has probability 0 (a mask): its gradient is 0, and a
+ *   teacher's entry or target there makes the loss infinite. A row of nothing
+ *   else has probability 0 everywhere. NaN and +infinity make a row NaN (the
+ *   teacher's: its loss, and the gradient at its entries).
+ *   A term of weight 0 is left out. Sums are float32; the result does not
+ *   depend on timing. K at most
+ *   S2_DISTILL_MAX_ENTRIES, T and V below 2^31 (S2_ERR_UNSUPPORTED).
+ *   dlogits may not overlap logits. Fastest where logits and dlogits start on
+ *   32 bytes and have the same row stride.
+ */
+#define S2_DISTILL_MAX_ENTRIES 8192u
+S2_API s2_status s2_distill(const void *logits, s2_dtype dt, uint64_t T, uint64_t V, uint64_t ld,
+                            const int32_t *teacher_idx, const float *teacher, uint64_t K, const int32_t *targets,
+                            const float *row_weight, s2_distill_params p, float *loss, void *dlogits, s2_dtype ddt,
+                            uint64_t ldd, s2_stream_t stream);
+
 /*
  * s2_wait_faults -- how many waits inside s2_matmul8, s2_wgrad8 and
  * s2_matmul4 kernels ran out on the current device since the library was loaded (0 unless

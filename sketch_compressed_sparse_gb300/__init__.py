@@ -56,6 +56,8 @@ __all__ = [
     "s2_pack4",
     "s2_unpack4",
     "s2_matmul4",
+    "s2_distill",
+    "S2_DISTILL_MAX_ENTRIES",
     "s2_wait_faults",
     "S2_SCALE_ROWS",
     "S2_SCALE_TILES",
@@ -75,6 +77,10 @@ S2_F32, S2_BF16 = 0, 1
 
 class Params(ctypes.Structure):
     _fields_ = [("d", ctypes.c_uint32), ("w", ctypes.c_uint32), ("seed", ctypes.c_uint32)]
+
+
+class DistillParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_float) for n in ("temperature", "soft", "hard", "scale")]
 
 
 _u32, _u64, _i32, _f32, _vp, _sz = (ctypes.c_uint32, ctypes.c_uint64, ctypes.c_int, ctypes.c_float,
@@ -111,6 +117,7 @@ _SIGS = {
     "s2_pack4": ([_vp, _i32, _u64, _u64, _u64, _vp, _u64, _vp, _vp], _i32),
     "s2_unpack4": ([_vp, _u64, _vp, _u64, _u64, _vp, _i32, _u64, _vp], _i32),
     "s2_matmul4": ([_vp, _u64, _vp, _vp, _u64, _vp, _u64, _u64, _u64, _vp, _i32, _u64, _vp], _i32),
+    "s2_distill": ([_vp, _i32, _u64, _u64, _u64, _vp, _vp, _u64, _vp, _vp, DistillParams, _vp, _vp, _i32, _u64, _vp], _i32),
     "s2_wait_faults": ([ctypes.POINTER(_u32)], _i32),
     "s2_status_string": ([_i32], ctypes.c_char_p),
     "s2_version": ([], ctypes.c_char_p),
@@ -619,6 +626,49 @@ def s2_matmul4(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
                           ldy, _stream(stream))
     if st:
         raise S2Error(st, "s2_matmul4")
+
+
+# ---- a softmax layer's loss against a teacher ----
+
+S2_DISTILL_MAX_ENTRIES = 8192
+_I32T = (torch.int32,)
+_F32S = (torch.float32,)
+
+
+def _rows(t: Optional[torch.Tensor], name: str, dtypes, rows: int):
+    """One value for each row, or None."""
+    if t is not None and t.dim() != 1:
+        raise ValueError(f"{name} must have one value for each row")
+    return _dev(t, name, dtypes, rows)
+
+
+def s2_distill(logits: torch.Tensor, teacher_idx: Optional[torch.Tensor], teacher: Optional[torch.Tensor],
+               loss: torch.Tensor, dlogits: Optional[torch.Tensor] = None, targets: Optional[torch.Tensor] = None,
+               row_weight: Optional[torch.Tensor] = None, temperature: float = 1.0, soft: float = 1.0,
+               hard: float = 0.0, scale: float = 1.0, stream=None) -> None:
+    """loss [T] of logits [T, V] against a teacher's top logits (teacher_idx [T, K] int32, teacher [T, K]
+    float32) and targets [T] int32, and scale times its gradient in dlogits [T, V]:
+    row_weight * (soft * KL(teacher || logits, both at temperature) + hard * cross entropy)."""
+    pz, T, V, ld = _mat(logits, "logits", _GRAD)
+    K = 0
+    if teacher is not None or teacher_idx is not None:
+        if teacher is None or teacher_idx is None:
+            raise ValueError("teacher_idx and teacher go together")
+        if teacher.dim() != 2 or teacher.shape != teacher_idx.shape or teacher.shape[0] != T:
+            raise ValueError(f"teacher_idx {tuple(teacher_idx.shape)} and teacher {tuple(teacher.shape)} must be [{T}, K]")
+        K = teacher.shape[1]
+    pd, ldd, ddt = None, 0, S2_F32
+    if dlogits is not None:
+        pd, r, c, ldd = _mat(dlogits, "dlogits", _GRAD)
+        if r != T or c != V:
+            _refuse_shape(dlogits, "dlogits", T, V)
+        ddt = _dtype_code(dlogits)
+    st = _f("s2_distill")(pz, _dtype_code(logits), T, V, ld, _dev(teacher_idx, "teacher_idx", _I32T, T * K),
+                          _dev(teacher, "teacher", _F32S, T * K), K, _rows(targets, "targets", _I32T, T),
+                          _rows(row_weight, "row_weight", _F32S, T), DistillParams(temperature, soft, hard, scale),
+                          _rows(loss, "loss", _F32S, T), pd, ddt, ldd, _stream(stream))
+    if st:
+        raise S2Error(st, "s2_distill")
 
 
 def s2_wait_faults() -> int:

@@ -1,6 +1,7 @@
 // C ABI of libs2: argument validation and dispatch to the kernels. Every
 // entry point checks its arguments completely before anything is launched,
 // then queues its kernels on the caller's stream and returns.
+#include <cmath>
 #include <cstring>
 #include <initializer_list>
 #include <mutex>
@@ -893,6 +894,54 @@ s2_status s2_matmul4(const uint8_t* x, uint64_t ldx, const uint8_t* x_scales, co
     Matmul4Args a{x, x_scales, w, w_scales, y, stride16(M, bytes4(K), ldx), stride16(N, bytes4(K), ldw), ldy,
                   (uint32_t)M, (uint32_t)N, (uint32_t)K, dt == S2_F32 ? 0 : 1};
     return cuda_status(launch_matmul4(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+s2_status s2_distill(const void* logits, s2_dtype dt, uint64_t T, uint64_t V, uint64_t ld, const int32_t* teacher_idx,
+                     const float* teacher, uint64_t K, const int32_t* targets, const float* row_weight,
+                     s2_distill_params p, float* loss, void* dlogits, s2_dtype ddt, uint64_t ldd, s2_stream_t stream) {
+    if (!dtype_ok(dt) || (dlogits && !dtype_ok(ddt))) return S2_ERR_INVALID_ARG;
+    const float ct = (float)(1.44269504088896340736 / p.temperature), inv_t = (float)(1.0 / p.temperature);
+    if (!(p.temperature > 0.0f) || !std::isfinite(p.temperature) || !std::isfinite(ct) || !std::isfinite(p.soft) ||
+        !std::isfinite(p.hard) || !std::isfinite(p.scale))
+        return S2_ERR_INVALID_ARG;
+    s2_status st = first_error({check_matrix(T, V, ld), dlogits ? check_matrix(T, V, ldd) : S2_OK});
+    if (st != S2_OK) return st;
+    if (K > S2_DISTILL_MAX_ENTRIES) return S2_ERR_UNSUPPORTED;
+    if (T == 0) return S2_OK;
+    if (!loss || (K > 0 && (!teacher_idx || !teacher))) return S2_ERR_INVALID_ARG;
+    if (!aligned(loss, 4) || !aligned(teacher_idx, 4) || !aligned(teacher, 4) || !aligned(targets, 4) || !aligned(row_weight, 4))
+        return S2_ERR_ALIGNMENT;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (V == 0) return cuda_status(cudaMemsetAsync(loss, 0, T * 4, s));  // no logits, no terms
+    if (!logits) return S2_ERR_INVALID_ARG;
+    const uint64_t esz = size_of(dt), dsz = size_of(ddt);
+    if (!aligned(logits, esz) || !aligned(dlogits, dsz)) return S2_ERR_ALIGNMENT;
+    if (clash({{loss, T * 4}, {dlogits, dlogits ? extent(T, V, ldd, dsz) : 0}, {logits, extent(T, V, ld, esz)},
+               {teacher_idx, T * K * 4}, {teacher, T * K * 4}, {targets, T * 4}, {row_weight, T * 4}}, 2))
+        return S2_ERR_INVALID_ARG;
+    DistillArgs a{};
+    a.z = logits;
+    a.ld = ld;
+    a.idx = teacher_idx;
+    a.t = teacher;
+    a.K = (uint32_t)K;
+    a.targets = targets;
+    a.row_weight = row_weight;
+    a.soft = p.soft;
+    a.hard = p.hard;
+    a.scale = p.scale;
+    a.loss = loss;
+    a.dz = dlogits;
+    a.ldd = ldd;
+    a.T = (uint32_t)T;
+    a.V = (uint32_t)V;
+    a.wide = dlogits && (reinterpret_cast<uintptr_t>(logits) / esz - reinterpret_cast<uintptr_t>(dlogits) / dsz) % 8 == 0 &&
+             (T == 1 || (ld - ldd) % 8 == 0);
+    a.use_soft = K > 0 && p.soft != 0.0f;
+    a.use_hard = targets && p.hard != 0.0f;
+    a.ct = ct;
+    a.inv_t = inv_t;
+    return cuda_status(launch_distill(a, dt == S2_F32 ? 0 : 1, ddt == S2_F32 ? 0 : 1, s));
 }
 
 s2_status s2_wait_faults(uint32_t* host_count) {

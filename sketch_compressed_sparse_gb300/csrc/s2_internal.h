@@ -224,6 +224,27 @@ struct Matmul4Args {
 };
 cudaError_t launch_matmul4(const Matmul4Args& a, cudaStream_t s);
 
+// ---- a softmax layer's loss against a teacher ---------------------------------
+struct DistillArgs {
+    const void* z;  // [T][V] logits, row stride ld
+    uint64_t ld;
+    const int32_t* idx;  // [T][K]
+    const float* t;      // [T][K]
+    uint32_t K;
+    const int32_t* targets;
+    const float* row_weight;
+    float soft, hard, scale;
+    float* loss;
+    void* dz;  // [T][V], row stride ldd, or nullptr
+    uint64_t ldd;
+    uint32_t T, V;
+    bool wide;                // element addresses of z and dz agree modulo eight, in every row
+    bool use_soft, use_hard;  // the term has a weight and its inputs
+    float ct, inv_t;          // log2(e) / temperature, 1 / temperature
+};
+// dtype of z and ddtype of dz: 0 = f32, 1 = bf16; at least one logit.
+cudaError_t launch_distill(const DistillArgs& a, int dtype, int ddtype, cudaStream_t s);
+
 // Waits of the tensor-core kernels that ran out on the current device.
 cudaError_t read_wait_faults(uint32_t* count);
 
