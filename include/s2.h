@@ -504,6 +504,35 @@ S2_API s2_status s2_matmul4(const uint8_t *x, uint64_t ldx, const uint8_t *x_sca
                             const uint8_t *w_scales, uint64_t M, uint64_t N, uint64_t K, void *y, s2_dtype dt,
                             uint64_t ldy, s2_stream_t stream);
 
+/*
+ * s2_sample -- the next token of each of T rows of logits [T][V] of type dt
+ * (row stride ld), drawn with one given random number per row.
+ *   u [T] float32 in [0, 1) (larger ones are taken for the largest below 1;
+ *   negative ones and NaN for 0).
+ *   Settings of each row, arrays of T, or null where no row uses one:
+ *   temperature float32 (null: 1; 0, negative, NaN or below 2^-126: the row's
+ *   largest logit is taken, the lowest index of equals), top_k int32 (below 1: off), top_p
+ *   float32 (1 or more, or NaN: off; 0 or less: one token), min_p float32 (0
+ *   or less, or NaN: off; more than 1: 1).
+ *   With l_max the row's largest logit a token's weight is exp((l - l_max) /
+ *   temperature). The tokens are ordered by logit, the largest first, equal
+ *   ones by index; top-k keeps the first top_k; top-p keeps the shortest
+ *   beginning of what is left whose weights sum to top_p of their sum or
+ *   more; min-p drops weights below min_p. tokens [T] int32 out: the first
+ *   kept index, in ascending order, at which the sum of the kept weights up to
+ *   and including it exceeds u times their sum.
+ *   A logit that is -infinity or NaN is never drawn (a mask). A row with no
+ *   other gives -1. Where a row holds +infinity those tokens alone have
+ *   weight, 1 each.
+ *   Weights are right to about 2^-35 of themselves and summed as integers, so
+ *   the token does not depend on timing, nor, but for borders that close, on
+ *   the arithmetic. logits need the alignment of their type only. T and V
+ *   below 2^31; V = 0 gives -1.
+ */
+S2_API s2_status s2_sample(const void *logits, s2_dtype dt, uint64_t T, uint64_t V, uint64_t ld,
+                           const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                           const float *u, int32_t *tokens, s2_stream_t stream);
+
 /* Weights and temperature of s2_distill. */
 typedef struct {
     float temperature; /* of the teacher's and the student's softmax in the soft term; above 0, and 1 / temperature finite */

@@ -56,6 +56,7 @@ __all__ = [
     "s2_pack4",
     "s2_unpack4",
     "s2_matmul4",
+    "s2_sample",
     "s2_distill",
     "S2_DISTILL_MAX_ENTRIES",
     "s2_wait_faults",
@@ -117,6 +118,7 @@ _SIGS = {
     "s2_pack4": ([_vp, _i32, _u64, _u64, _u64, _vp, _u64, _vp, _vp], _i32),
     "s2_unpack4": ([_vp, _u64, _vp, _u64, _u64, _vp, _i32, _u64, _vp], _i32),
     "s2_matmul4": ([_vp, _u64, _vp, _vp, _u64, _vp, _u64, _u64, _u64, _vp, _i32, _u64, _vp], _i32),
+    "s2_sample": ([_vp, _i32, _u64, _u64, _u64, _vp, _vp, _vp, _vp, _vp, _vp, _vp], _i32),
     "s2_distill": ([_vp, _i32, _u64, _u64, _u64, _vp, _vp, _u64, _vp, _vp, DistillParams, _vp, _vp, _i32, _u64, _vp], _i32),
     "s2_wait_faults": ([ctypes.POINTER(_u32)], _i32),
     "s2_status_string": ([_i32], ctypes.c_char_p),
@@ -628,9 +630,8 @@ def s2_matmul4(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
         raise S2Error(st, "s2_matmul4")
 
 
-# ---- a softmax layer's loss against a teacher ----
+# ---- the next token of rows of logits ----
 
-S2_DISTILL_MAX_ENTRIES = 8192
 _I32T = (torch.int32,)
 _F32S = (torch.float32,)
 
@@ -640,6 +641,25 @@ def _rows(t: Optional[torch.Tensor], name: str, dtypes, rows: int):
     if t is not None and t.dim() != 1:
         raise ValueError(f"{name} must have one value for each row")
     return _dev(t, name, dtypes, rows)
+
+
+def s2_sample(logits: torch.Tensor, u: torch.Tensor, tokens: torch.Tensor, temperature: Optional[torch.Tensor] = None,
+              top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+              min_p: Optional[torch.Tensor] = None, stream=None) -> None:
+    """tokens [T] int32 drawn from logits [T, V] with the random numbers u [T] in [0, 1); temperature, top_p and
+    min_p [T] float32 and top_k [T] int32 are each row's settings (None: not used)."""
+    pz, T, V, ld = _mat(logits, "logits", _GRAD)
+    st = _f("s2_sample")(pz, _dtype_code(logits), T, V, ld, _rows(temperature, "temperature", _F32S, T),
+                         _rows(top_k, "top_k", _I32T, T), _rows(top_p, "top_p", _F32S, T),
+                         _rows(min_p, "min_p", _F32S, T), _rows(u, "u", _F32S, T), _rows(tokens, "tokens", _I32T, T),
+                         _stream(stream))
+    if st:
+        raise S2Error(st, "s2_sample")
+
+
+# ---- a softmax layer's loss against a teacher ----
+
+S2_DISTILL_MAX_ENTRIES = 8192
 
 
 def s2_distill(logits: torch.Tensor, teacher_idx: Optional[torch.Tensor], teacher: Optional[torch.Tensor],

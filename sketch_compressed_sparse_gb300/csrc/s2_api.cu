@@ -896,6 +896,28 @@ s2_status s2_matmul4(const uint8_t* x, uint64_t ldx, const uint8_t* x_scales, co
     return cuda_status(launch_matmul4(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+s2_status s2_sample(const void* logits, s2_dtype dt, uint64_t T, uint64_t V, uint64_t ld, const float* temperature,
+                    const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int32_t* tokens,
+                    s2_stream_t stream) {
+    if (!dtype_ok(dt)) return S2_ERR_INVALID_ARG;
+    const s2_status st = check_matrix(T, V, ld);
+    if (st != S2_OK) return st;
+    if (T == 0) return S2_OK;
+    if (!tokens || !u) return S2_ERR_INVALID_ARG;
+    if (!aligned(tokens, 4) || !aligned(u, 4) || !aligned(temperature, 4) || !aligned(top_k, 4) || !aligned(top_p, 4) ||
+        !aligned(min_p, 4))
+        return S2_ERR_ALIGNMENT;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (V > 0 && !logits) return S2_ERR_INVALID_ARG;
+    if (!aligned(logits, size_of(dt))) return S2_ERR_ALIGNMENT;
+    if (clash({{tokens, T * 4}, {logits, extent(T, V, ld, size_of(dt))}, {temperature, T * 4}, {top_k, T * 4},
+               {top_p, T * 4}, {min_p, T * 4}, {u, T * 4}}, 1))
+        return S2_ERR_INVALID_ARG;
+    if (V == 0) return cuda_status(cudaMemsetAsync(tokens, 0xff, T * 4, s));  // -1: nothing to draw
+    SampleArgs a{logits, ld, (uint32_t)T, (uint32_t)V, temperature, top_k, top_p, min_p, u, tokens};
+    return cuda_status(launch_sample(a, dt == S2_F32 ? 0 : 1, s));
+}
+
 s2_status s2_distill(const void* logits, s2_dtype dt, uint64_t T, uint64_t V, uint64_t ld, const int32_t* teacher_idx,
                      const float* teacher, uint64_t K, const int32_t* targets, const float* row_weight,
                      s2_distill_params p, float* loss, void* dlogits, s2_dtype ddt, uint64_t ldd, s2_stream_t stream) {

@@ -262,7 +262,7 @@ cudaError_t launch(const DistillArgs& a, cudaStream_t s) {
     int clusters = 0;
     for (;; blocks /= 2) {
         const uint64_t need = (groups + blocks - 1) / blocks + 1;
-        const bool fits = kGrad && need * kGroupBytes <= 200 * 1024;
+        const bool fits = kGrad && need * kGroupBytes <= kRowSmem;
         kernel = fits ? distill_kernel<TI, TO, TWO, kGrad> : distill_kernel<TI, TO, TWO, false>;
         room = fits ? (uint32_t)need : 0;
         smem = fits ? need * kGroupBytes : 0;

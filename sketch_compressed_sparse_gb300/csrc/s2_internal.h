@@ -245,6 +245,21 @@ struct DistillArgs {
 // dtype of z and ddtype of dz: 0 = f32, 1 = bf16; at least one logit.
 cudaError_t launch_distill(const DistillArgs& a, int dtype, int ddtype, cudaStream_t s);
 
+// ---- the next token of rows of logits ------------------------------------------
+struct SampleArgs {
+    const void* z;  // [T][V], row stride ld
+    uint64_t ld;
+    uint32_t T, V;
+    const float* temperature;  // [T] or nullptr, as the next three
+    const int32_t* top_k;
+    const float* top_p;
+    const float* min_p;
+    const float* u;
+    int32_t* tokens;
+};
+// dtype: 0 = f32, 1 = bf16; at least one logit.
+cudaError_t launch_sample(const SampleArgs& a, int dtype, cudaStream_t s);
+
 // Waits of the tensor-core kernels that ran out on the current device.
 cudaError_t read_wait_faults(uint32_t* count);
 

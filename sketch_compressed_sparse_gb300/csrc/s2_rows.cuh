@@ -19,6 +19,7 @@ namespace rows {
 constexpr int kRowThreads = 512;
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr uint32_t kAll = 0xffffffffu;
+constexpr int kRowSmem = 204 * 1024;  // beside up to 22 KB of a kernel's own
 
 __device__ __forceinline__ float minus_inf() { return __uint_as_float(0xff800000u); }
 
@@ -182,7 +183,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 
 // Clusters of `blocks` blocks of kernel `fn` that the device holds at once, 0 if
-// none (cached); also lets the kernel use `smem` bytes of dynamic shared memory.
+// none (cached); also lets the kernel use kRowSmem bytes of dynamic shared memory.
 inline cudaError_t resident_clusters(const void* fn, uint32_t blocks, size_t smem, int* clusters) {
     struct Entry {
         int dev;
@@ -203,7 +204,7 @@ inline cudaError_t resident_clusters(const void* fn, uint32_t blocks, size_t sme
             *clusters = table[i].clusters;
             return cudaSuccess;
         }
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowSmem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
