@@ -4,8 +4,8 @@
 // The row is cut into groups of eight elements whose addresses are multiples of
 // eight elements, so that every group but the first and the last of a row is
 // read in 16-byte accesses whatever the row's own alignment (rows of an odd
-// length start anywhere). Block `rank` of C owns the groups [NG*rank/C,
-// NG*(rank+1)/C). Elements outside the row read as -infinity.
+// length start anywhere). Block `rank` of C, a power of two, owns the
+// groups [NG*rank/C, NG*(rank+1)/C). Elements outside the row read as -infinity.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -16,32 +16,40 @@
 namespace s2 {
 namespace rows {
 
-constexpr int kRowThreads = 512;
-constexpr int kRowWarps = kRowThreads / 32;
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kRowSmem = 204 * 1024;  // beside up to 22 KB of a kernel's own
 
 __device__ __forceinline__ float minus_inf() { return __uint_as_float(0xff800000u); }
 
-struct Part {
-    uint32_t off;    // elements between the address of group 0 and the row's first
-    uint32_t first;  // first group of this block
-    uint32_t count;  // groups of this block
-    __device__ __forceinline__ uint32_t groups(uint32_t V) const { return (uint32_t)(((uint64_t)V + off + 7) / 8); }
-};
-// Element i of the row lies in group (i + off) / 8, at place (i + off) % 8.
 template <typename T>
-__device__ __forceinline__ Part part_of(const T* row, uint32_t V, uint32_t rank, uint32_t blocks) {
-    Part p;
+struct Part {
+    const T* base;   // address of this block's first group
+    uint32_t off;    // elements between the address of the row's group 0 and its first element
+    uint32_t first;  // this block's first group
+    uint32_t count;  // its groups
+    uint32_t lo, n;  // its groups lo..lo+n-1 lie in the row as a whole
+    __device__ __forceinline__ bool inner(uint32_t l) const { return l - lo < n; }
+    // index in the row of element j of local group l (beyond the row's ends: below 0 or not below V)
+    __device__ __forceinline__ int64_t index(uint32_t l, int j) const { return (int64_t)(first + l) * 8 + j - off; }
+    // the row's element i lies in this block
+    __device__ __forceinline__ bool holds(uint32_t i, uint32_t V) const {
+        return i < V && (uint32_t)(((uint64_t)i + off) / 8) - first < count;
+    }
+};
+// The groups of block `rank` of 2^log2_blocks.
+template <typename T>
+__device__ __forceinline__ Part<T> part_of(const T* row, uint32_t V, uint32_t rank, uint32_t log2_blocks) {
+    Part<T> p;
     p.off = (uint32_t)(reinterpret_cast<uintptr_t>(row) / sizeof(T)) % 8;
-    const uint64_t n = p.groups(V);
-    p.first = (uint32_t)(n * rank / blocks);
-    p.count = (uint32_t)(n * (rank + 1) / blocks) - p.first;
+    const uint64_t end = (uint64_t)V + p.off, n = (end + 7) / 8;
+    p.first = (uint32_t)(n * rank >> log2_blocks);
+    p.count = (uint32_t)(n * (rank + 1) >> log2_blocks) - p.first;
+    p.base = row + ((int64_t)p.first * 8 - p.off);
+    const uint32_t whole = (uint32_t)(end / 8);  // groups before this one end in the row
+    p.lo = p.first == 0 && p.off && p.count ? 1 : 0;
+    const uint32_t last = whole < p.first + p.count ? whole : p.first + p.count;
+    p.n = last > p.first + p.lo ? last - p.first - p.lo : 0;
     return p;
-}
-// All eight elements of group g belong to the row.
-__device__ __forceinline__ bool inner(const Part& p, uint32_t g, uint32_t V) {
-    return (g > 0 || p.off == 0) && (uint64_t)g * 8 + 8 <= (uint64_t)V + p.off;
 }
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
@@ -61,15 +69,16 @@ __device__ __forceinline__ float element(const Raw<T>& r, int j) {
         return __uint_as_float(j % 2 ? w & 0xffff0000u : w << 16);
     }
 }
+// A group at one of the row's ends.
 template <typename T>
-__device__ __forceinline__ Raw<T> edge_group(const T* row, const Part& p, uint32_t g, uint32_t V) {
+__device__ __noinline__ Raw<T> edge_group(const Part<T> p, uint32_t l, uint32_t V) {
     uint32_t e[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const int64_t i = (int64_t)g * 8 + j - p.off;
+        const int64_t i = p.index(l, j);
         const bool there = i >= 0 && i < (int64_t)V;
-        if constexpr (sizeof(T) == 4) e[j] = there ? __float_as_uint(row[i]) : 0xff800000u;
-        else e[j] = there ? row[i] : 0xff80u;
+        if constexpr (sizeof(T) == 4) e[j] = there ? __float_as_uint(p.base[l * 8 + j]) : 0xff800000u;
+        else e[j] = there ? p.base[l * 8 + j] : 0xff80u;
     }
     Raw<T> r;
     if constexpr (sizeof(T) == 4) {
@@ -81,10 +90,10 @@ __device__ __forceinline__ Raw<T> edge_group(const T* row, const Part& p, uint32
     return r;
 }
 template <typename T>
-__device__ __forceinline__ Raw<T> load_group(const T* row, const Part& p, uint32_t g, uint32_t V) {
-    if (!inner(p, g, V)) return edge_group(row, p, g, V);
+__device__ __forceinline__ Raw<T> load_group(const Part<T>& p, uint32_t l, uint32_t V) {
+    if (!p.inner(l)) return edge_group(p, l, V);
     Raw<T> r;
-    const uint4* q = reinterpret_cast<const uint4*>(row + ((int64_t)g * 8 - p.off));
+    const uint4* q = reinterpret_cast<const uint4*>(p.base + (uint64_t)l * 8);
 #pragma unroll
     for (int h = 0; h < (int)sizeof(T) / 2; ++h) r.w[h] = q[h];
     return r;
@@ -96,24 +105,34 @@ __device__ __forceinline__ Raw<T> load_group(const T* row, const Part& p, uint32
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void copy4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// Starts this thread's copies: groups threadIdx.x, threadIdx.x + kRowThreads, ...
+// Starts the copy of local group l, one in the midst of the row, to its place, which only this thread reads.
 template <typename T>
-__device__ __forceinline__ void stage(uint4* room, uint32_t size, const T* row, const Part& p, uint32_t V) {
-    const uint32_t base = (uint32_t)__cvta_generic_to_shared(room);
-    for (uint32_t l = threadIdx.x; l < p.count; l += kRowThreads) {
-        const uint32_t g = p.first + l;
-        if (inner(p, g, V)) {
-            const T* q = row + ((int64_t)g * 8 - p.off);
+__device__ __forceinline__ void stage_inner(uint4* room, uint32_t size, const Part<T>& p, uint32_t l) {
+    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(room + l);
+    const T* q = p.base + (uint64_t)l * 8;
 #pragma unroll
-            for (int h = 0; h < (int)sizeof(T) / 2; ++h) copy16(base + (h * size + l) * 16, q + h * 16 / sizeof(T));
-        } else {
-            const Raw<T> r = edge_group(row, p, g, V);
+    for (int h = 0; h < (int)sizeof(T) / 2; ++h) copy16(dst + h * size * 16, q + h * 16 / sizeof(T));
+}
+// Any group.
+template <typename T>
+__device__ __forceinline__ void stage_group(uint4* room, uint32_t size, const Part<T>& p, uint32_t l, uint32_t V) {
+    if (p.inner(l)) {
+        stage_inner(room, size, p, l);
+    } else {
+        const Raw<T> r = edge_group(p, l, V);
 #pragma unroll
-            for (int h = 0; h < (int)sizeof(T) / 2; ++h) room[h * size + l] = r.w[h];
-        }
+        for (int h = 0; h < (int)sizeof(T) / 2; ++h) room[h * size + l] = r.w[h];
     }
+}
+// Starts a thread's copies: groups `from`, from + step, ...
+template <typename T>
+__device__ __forceinline__ void stage(uint4* room, uint32_t size, const Part<T>& p, uint32_t V, uint32_t from, uint32_t step) {
+    for (uint32_t l = from; l < p.count; l += step) stage_group(room, size, p, l, V);
 }
 template <typename T>
 __device__ __forceinline__ Raw<T> staged(const uint4* room, uint32_t size, uint32_t l) {
@@ -122,18 +141,60 @@ __device__ __forceinline__ Raw<T> staged(const uint4* room, uint32_t size, uint3
     for (int h = 0; h < (int)sizeof(T) / 2; ++h) r.w[h] = room[h * size + l];
     return r;
 }
-// Element at place j of local group l.
+// ---- two floats in one instruction ----------------------------------------------
+struct Two {
+    uint64_t b;
+};
+__device__ __forceinline__ Two two(float x, float y) {
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.b) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 apart(Two a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.b));
+    return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.b) : "l"(a.b), "l"(b.b), "l"(c.b));
+    return r;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+    Two r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(a.b), "l"(b.b));
+    return r;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(a.b), "l"(b.b));
+    return r;
+}
+// Elements 2j and 2j + 1 of a group.
 template <typename T>
-__device__ __forceinline__ float staged_at(const uint4* room, uint32_t size, uint32_t l, uint32_t j) {
-    if constexpr (sizeof(T) == 4) return reinterpret_cast<const float*>(room + (j / 4 * size + l))[j % 4];
-    else return to_float(reinterpret_cast<const uint16_t*>(room + l)[j]);
+__device__ __forceinline__ Two element2(const Raw<T>& r, int j) {
+    return two(element(r, 2 * j), element(r, 2 * j + 1));
+}
+// The largest of a group, NaN aside.
+__device__ __forceinline__ float group_max(const Raw<float>& r) {
+    return fmaxf(fmaxf(fmaxf(element(r, 0), element(r, 1)), fmaxf(element(r, 2), element(r, 3))),
+                 fmaxf(fmaxf(element(r, 4), element(r, 5)), fmaxf(element(r, 6), element(r, 7))));
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float group_max(const Raw<uint16_t>& r) {
+    const uint32_t m = max_bf16x2(max_bf16x2(r.w[0].x, r.w[0].y), max_bf16x2(r.w[0].z, r.w[0].w));
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
 }
 
 // ---- reductions --------------------------------------------------------------------
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-    return v;
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 // The same bits in every lane: each step adds the same two numbers in both.
 __device__ __forceinline__ float warp_sum(float v) {
@@ -171,6 +232,10 @@ __device__ __forceinline__ uint64_t peer_u64(uint32_t a) {
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The two halves of it; relaxed: what this warp wrote need not be seen by the others.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t cluster_size() {
     uint32_t r;
     asm volatile("mov.u32 %0, %cluster_nctaid.x;" : "=r"(r));
@@ -182,9 +247,12 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     return r;
 }
 
+// Shared memory for a slice, in few different sizes: what follows keeps an answer for each.
+inline uint64_t smem_of(uint64_t bytes) { return (bytes + 2047) / 2048 * 2048; }
+
 // Clusters of `blocks` blocks of kernel `fn` that the device holds at once, 0 if
 // none (cached); also lets the kernel use kRowSmem bytes of dynamic shared memory.
-inline cudaError_t resident_clusters(const void* fn, uint32_t blocks, size_t smem, int* clusters) {
+inline cudaError_t resident_clusters(const void* fn, int threads, uint32_t blocks, size_t smem, int* clusters) {
     struct Entry {
         int dev;
         const void* fn;
@@ -209,7 +277,7 @@ inline cudaError_t resident_clusters(const void* fn, uint32_t blocks, size_t sme
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(kRowThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;

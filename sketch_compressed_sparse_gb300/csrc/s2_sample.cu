@@ -33,6 +33,8 @@ namespace {
 
 using namespace rows;
 
+constexpr int kRowThreads = 512;
+constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kBins = kRowThreads;   // one per thread
 constexpr int kChunks = kRowThreads; // runs of tokens, one per thread
 constexpr uint32_t kList = 256;      // tokens that are ranked against one another
@@ -118,8 +120,7 @@ template <typename TI, bool STAGED>
 struct Row {
     const uint4* slice;
     uint32_t room;
-    const TI* z;
-    Part p;
+    Part<TI> p;
     uint32_t V;
     uint32_t span;    // 256-token steps per run
     uint32_t chunks;  // runs of this block
@@ -127,7 +128,7 @@ struct Row {
     // f(values of eight neighbours) of local group l
     template <typename F>
     __device__ __forceinline__ void one(uint32_t l, F f) const {
-        const Raw<TI> r = STAGED ? staged<TI>(slice, room, l) : load_group(z, p, p.first + l, V);
+        const Raw<TI> r = STAGED ? staged<TI>(slice, room, l) : load_group(p, l, V);
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = element(r, j);
@@ -146,7 +147,7 @@ struct Row {
     __device__ __forceinline__ void each(F f) const {
         for (uint32_t c = threadIdx.x / 32; c < chunks; c += kRowWarps) run(c, f);
     }
-    __device__ __forceinline__ uint32_t index(uint32_t l, int j) const { return (p.first + l) * 8 + j - p.off; }
+    __device__ __forceinline__ uint32_t index(uint32_t l, int j) const { return (uint32_t)p.index(l, j); }
 };
 
 // What is kept: logits above v, and those equal to it with an index below i.
@@ -407,25 +408,24 @@ __device__ Border narrow(Shared& sh, const R& row, Border from, uint32_t& turn, 
 }
 
 template <typename TI, bool STAGED>
-__global__ void __launch_bounds__(kRowThreads, 2) sample_kernel(const SampleArgs a, uint32_t room, int shift) {
+__global__ void __launch_bounds__(kRowThreads, 2) sample_kernel(const SampleArgs a, uint32_t room, uint32_t log2_blocks, int shift) {
     extern __shared__ uint4 slice[];
     __shared__ Shared sh;
     stream_order();
-    const uint32_t blocks = cluster_size(), rank = cluster_rank();
+    const uint32_t blocks = 1u << log2_blocks, rank = cluster_rank();
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (threadIdx.x < 32) sh.roots[threadIdx.x] = kRoots[threadIdx.x];
     uint32_t turn = 0, parity = 0;
-    for (uint64_t at = blockIdx.x / blocks; at < a.T; at += gridDim.x / blocks, parity ^= 1) {
+    for (uint64_t at = blockIdx.x / blocks; at < a.T; at += gridDim.x >> log2_blocks, parity ^= 1) {
         Row<TI, STAGED> row;
         row.slice = slice;
         row.room = room;
-        row.z = static_cast<const TI*>(a.z) + at * a.ld;
-        row.p = part_of(row.z, a.V, rank, blocks);
+        row.p = part_of(static_cast<const TI*>(a.z) + at * a.ld, a.V, rank, log2_blocks);
         row.V = a.V;
         row.span = (row.p.count + 32 * kChunks - 1) / (32 * kChunks);
         if (row.span == 0) row.span = 1;
         row.chunks = (row.p.count + 32 * row.span - 1) / (32 * row.span);
-        if (STAGED) stage(slice, room, row.z, row.p, a.V);
+        if (STAGED) stage(slice, room, row.p, a.V, threadIdx.x, kRowThreads);
         if (threadIdx.x == kRowThreads - 1) {
             Settings s;
             const float t = a.temperature ? a.temperature[at] : 1.0f;
@@ -594,19 +594,21 @@ cudaError_t launch(const SampleArgs& a, cudaStream_t s) {
     int clusters = 0;
     for (;; blocks /= 2) {
         const uint64_t need = (groups + blocks - 1) / blocks + 1;
-        const bool fits = need * kGroupBytes <= kRowSmem && need <= 32ull * kChunks;
+        const bool fits = smem_of(need * kGroupBytes) <= kRowSmem && need <= 32ull * kChunks;
         kernel = fits ? sample_kernel<TI, true> : sample_kernel<TI, false>;
         room = fits ? (uint32_t)need : 0;
-        smem = fits ? need * kGroupBytes : 0;
-        e = resident_clusters(reinterpret_cast<const void*>(kernel), blocks, smem, &clusters);
+        smem = fits ? smem_of(need * kGroupBytes) : 0;
+        e = resident_clusters(reinterpret_cast<const void*>(kernel), kRowThreads, blocks, smem, &clusters);
         if (e != cudaSuccess) return e;
         if (clusters > 0 || blocks == 1) break;
     }
+    uint32_t log2_blocks = 0;
+    while ((1u << log2_blocks) < blocks) ++log2_blocks;
     int shift = 0;  // sums of V weights stay below 2^63
     while ((1ull << (62 - kBits + shift)) < a.V) ++shift;
     const uint64_t most = 0x7fffffffull / 16;
     const uint32_t grid = (uint32_t)(a.T < most ? a.T : most) * blocks;
-    return launch_early(kernel, grid, kRowThreads, smem, blocks, s, a, room, shift);
+    return launch_early(kernel, grid, kRowThreads, smem, blocks, s, a, room, log2_blocks, shift);
 }
 
 }  // namespace

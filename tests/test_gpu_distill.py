@@ -172,6 +172,20 @@ def test_not_finite(V):
     check(z, idx, t, y, w, hard=0.5)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_nothing_is_left_from_rows_before(dtype):
+    """Rows whose ends lie inside a group, in few and many blocks, right after rows of NaN in every block."""
+    bad = torch.full((2000, 30001), float("nan"), dtype=DT[dtype], device=DEV)
+    bi = torch.arange(100, dtype=torch.int32, device=DEV).repeat(2000, 1)
+    bt, bl, bd = torch.full((2000, 100), float("nan"), device=DEV), torch.empty(2000, device=DEV), torch.empty_like(bad)
+    for T, V, K in [(6, 50, 40), (9, 333, 0), (30, 5003, 20), (3, 100001, 9), (700, 3001, 5)]:
+        z, idx, t, y, w = make(T, V, K, repeat=True, missing=True)
+        w[::4] = 0
+        for hard in (0.0, 0.4):
+            s2.s2_distill(bad, bi, bt, bl, bd, targets=bi[:, 0].contiguous(), hard=0.5, temperature=2.0)
+            check(z, idx, t, y, w, dtype, dtype, temperature=1.5, hard=hard)
+
+
 def test_no_teacher_and_nothing():
     """Cross entropy alone, and rows without any term."""
     z, _, _, y, w = make(9, 777, 3, missing=True)
