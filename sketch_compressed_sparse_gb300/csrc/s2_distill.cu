@@ -10,31 +10,35 @@
 // The teacher's entries and the target are put right afterwards, one by one: the
 // dense part is the same for every element.
 //
-// A thread reads only what it copied itself, so it asks for the next row's
-// groups as soon as it has taken a group for the last time: loads go on while
-// sums are joined and gradients stored.
-//
-// Bound by HBM (a logit is read once, its gradient written once) and near it by
-// instructions: two exponentials a logit and pass, in pairs of floats.
+// Bound by HBM (a logit is read once, its gradient written once), near it by
+// exponentials (two a logit and pass), and by the time that a row's sums take to
+// be joined, so every kind of work has warps of its own: most go over the logits
+// and copy the next row's groups to the places of those that they took for the
+// last time (a thread reads only what it copied, so no barrier is needed for
+// that); one joins the sums and hands them to the cluster's other blocks; two see
+// to the teacher's entries, every second row each, so that these have the time of
+// two rows for loads that depend on one another.
 #include <cfloat>
 #include <type_traits>
 
 #include "s2_internal.h"
 #include "s2_launch.cuh"
 #include "s2_rows.cuh"
+#include "s2_tc.cuh"
 
 namespace s2 {
 namespace {
 
 using namespace rows;
 
-constexpr int kRowThreads = 384;
-constexpr int kRowWarps = kRowThreads / 32;
-constexpr int kResident = 3;  // blocks on an SM
+constexpr int kMaxThreads = 1024;
+constexpr uint32_t kMaxBlocks = 16;  // of a cluster
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr double kLn2 = 0.69314718055994530942;
-constexpr int kSlots = 4;             // teacher's entries of a lane of the first warp
-constexpr uint32_t kFew = 32 * kSlots;  // up to here that warp sees to them by itself
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// The exponentials of a logit: one where one sum is enough; two; or, where the
+// temperature is 2, the one at that temperature and its square.
+enum { kOne, kSquare, kBoth };
 
 // exp2(z * c - k) with k = max * c rounded needs one rounding; where max is near
 // the end of the floats (a row of nothing but a type's lowest value) the product
@@ -43,6 +47,7 @@ struct Base {
     float max, k;
     bool plain;
 };
+// limit: below it a logit's product with c and with log2(e) is far from infinite.
 __device__ __forceinline__ Base base_of(float max, float c, float limit) {
     const bool plain = fabsf(max) < limit;
     return {max, plain ? __fmul_rn(max, c) : 0.0f, plain};  // (k as it is: not fused into a difference)
@@ -54,20 +59,20 @@ __device__ __forceinline__ float factor(const Base& from, const Base& to, float 
     return from.plain ? ex2(from.k - to.k) : 0.0f;
 }
 // log of the sum of exp((z - max) / T) from that of the powers: k is not max * c exactly.
-__device__ __forceinline__ double log_sum(float sum, const Base& b, float c) {
-    if (sum == 0.0f) return 0.0;  // a row of nothing: its loss is infinite already
-    return (double)logf(sum) - (b.plain ? (double)fmaf(b.max, c, -b.k) * kLn2 : 0.0);
+__device__ __forceinline__ float log_sum(float sum, const Base& b, float c) {
+    if (sum == 0.0f) return 0.0f;  // a row of nothing: its loss is infinite already
+    return logf(sum) - (b.plain ? fmaf(b.max, c, -b.k) * kLn2 : 0.0f);
 }
 
-// What a block knows of its part of a row.
-struct Record {
-    float max;         // of its logits (lowest finite number where it has none)
+// What a block knows of its part of a row: 32 bytes, two stores to another block.
+struct __align__(16) Record {
+    float max;         // base of its logits' sums (lowest finite number where it has none)
     float soft, hard;  // sums of the powers of (z - max) / T, z - max
+    uint32_t flags;    // 1: the target is here, 2: the row has a soft term, 4: a hard one
     float cross;       // sum of q (log q - (z - ref) / T) over the teacher's entries here
     float mass;        // sum of their q
     float ref;         // what stands for max in `cross`
-    float target;      // the target's logit
-    uint32_t flags;    // 1: the target is here, 2: the row has a soft term, 4: a hard one
+    float target;      // the target's logit, where it is here
 };
 
 struct Sums {
@@ -75,28 +80,12 @@ struct Sums {
 };
 
 // Joins the sums of the lanes of a warp.
-template <bool TWO>
+template <int EXPS>
 __device__ __forceinline__ Sums join(const Sums& s, float c, float limit) {
     Sums r;
     r.max = warp_max(s.max);
     r.a = warp_sum(s.a * factor(base_of(s.max, c, limit), base_of(r.max, c, limit), c));
-    r.b = TWO ? warp_sum(s.b * factor(base_of(s.max, kLog2e, limit), base_of(r.max, kLog2e, limit), kLog2e)) : r.a;
-    return r;
-}
-
-// The teacher's entries of one row that a thread has seen: largest logit, sum of powers over it.
-struct Teacher {
-    float max, sum;
-};
-__device__ __forceinline__ void see(Teacher& t, float v, float ct) {
-    const float m = fmaxf(t.max, v);
-    t.sum = t.sum * ex2((t.max - m) * ct) + ex2((v - m) * ct);
-    t.max = m;
-}
-__device__ __forceinline__ Teacher join(const Teacher& t, float ct) {
-    Teacher r;
-    r.max = warp_max(t.max);
-    r.sum = warp_sum(t.sum * ex2((t.max - r.max) * ct));
+    r.b = EXPS != kOne ? warp_sum(s.b * factor(base_of(s.max, kLog2e, limit), base_of(r.max, kLog2e, limit), kLog2e)) : r.a;
     return r;
 }
 
@@ -131,491 +120,743 @@ __device__ __forceinline__ void store_group(TO* dz, const Part<TI>& p, uint32_t 
     }
 }
 
-// A row's entries as they lie in memory, fetched two rows ahead. A lane reads
-// what it copied itself: entries lane, lane + 32, ...
-struct Fetched {
-    uint32_t i[kFew];
-    float t[kFew];
-    uint32_t y[32];
-};
-__device__ __forceinline__ void fetch(Fetched& f, const DistillArgs& a, uint64_t row, bool few) {
-    const uint32_t lane = threadIdx.x % 32;
-    if (row >= a.T) return;
-    if (few)
-        for (uint32_t k = lane; k < a.K; k += 32) {
-            copy4(f.i + k, a.idx + row * a.K + k);
-            copy4(f.t + k, a.t + row * a.K + k);
+// A thread's sums over the groups that it takes, over a base that its warp shares
+// at first. What is read again later is not known to be below it: a logit 2^kFar
+// times as likely moves the sums to another base (a float holds sums that far
+// above 1, so nearer ones need not).
+constexpr float kFar = 60.0f;
+template <int EXPS>
+struct Taken {
+    float max, ka, kb;  // of the bases; both are plain or none is
+    bool plain;
+    Two sa, sb;
+    __device__ __forceinline__ void rest_on(float m, float c, float limit) {
+        const Base a = base_of(m, c, limit), b = base_of(m, kLog2e, limit);
+        max = m;
+        ka = a.k;
+        kb = b.k;
+        plain = a.plain;
+    }
+    __device__ __forceinline__ Taken(float m, float c, float limit) : sa(two(0.0f, 0.0f)), sb(sa) { rest_on(m, c, limit); }
+    // a base is plain
+    template <typename TI>
+    __device__ __forceinline__ void add(const Raw<TI>& r, float c) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const Two v = element2(r, j);
+            const float2 x = apart(fma2(v, two(c, c), two(-ka, -ka)));
+            const Two e = two(ex2(x.x), ex2(x.y));
+            sa = add2(sa, e);
+            if (EXPS == kSquare) sb = fma2(e, e, sb);
+            if (EXPS == kBoth) {
+                const float2 w = apart(fma2(v, two(kLog2e, kLog2e), two(-kb, -kb)));
+                sb = add2(sb, two(ex2(w.x), ex2(w.y)));
+            }
         }
-    if (a.use_hard) copy4(f.y + lane, a.targets + row);
+    }
+    template <typename TI>
+    __device__ __forceinline__ void add_any(const Raw<TI>& r, float c) {
+        if (plain) return add(r, c);
+#pragma unroll 1
+        for (int j = 0; j < 8; ++j) {
+            const float x = element(r, j) - max;
+            sa = add2(sa, two(ex2(x * c), 0.0f));
+            if (EXPS != kOne) sb = add2(sb, two(ex2(x * kLog2e), 0.0f));
+        }
+    }
+    __device__ __noinline__ void move(float m, float c, float limit) {
+        const Base a{max, ka, plain}, b{max, kb, plain};
+        rest_on(m, c, limit);
+        const float fa = factor(a, {max, ka, plain}, c), fb = factor(b, {max, kb, plain}, kLog2e);
+        sa = mul2(sa, two(fa, fa));
+        if (EXPS != kOne) sb = mul2(sb, two(fb, fb));
+    }
+    __device__ __forceinline__ Sums sums() const {
+        const float2 x = apart(sa), y = apart(sb);
+        return {max, x.x + x.y, y.x + y.y};
+    }
+};
+
+// What is the same for all of a launch, and for all of a row.
+template <typename TI>
+struct Rows {
+    const DistillArgs& a;
+    uint32_t rank, log2_blocks, room;
+    float c, limit;  // c: of the first sum
+    uint64_t row, step;
+    __device__ __forceinline__ const TI* logits(uint64_t r) const { return static_cast<const TI*>(a.z) + r * a.ld; }
+    __device__ __forceinline__ bool there(uint64_t r) const { return r < a.T; }
+    __device__ __forceinline__ float weight(uint64_t r) const { return !there(r) ? 0.0f : a.row_weight ? a.row_weight[r] : 1.0f; }
+    __device__ __forceinline__ Part<TI> part(uint64_t r) const { return part_of(logits(there(r) ? r : 0), a.V, rank, log2_blocks); }
+    // groups of part p that stay in shared memory
+    __device__ __forceinline__ uint32_t kept(const Part<TI>& p, float weight) const { return weight != 0.0f ? min(p.count, room) : 0; }
+};
+
+// The factors of a row's gradient, from the joined sums.
+template <int EXPS>
+struct Factors {
+    Base ba, bb;
+    float ca, cb, gq, gy;  // of the powers; of the teacher's probabilities and the target
+    bool some;             // the row has a term
+    __device__ __forceinline__ Factors(const Sums& w, bool soft, bool hard, float weight, const DistillArgs& a, float c, float limit)
+        : ba(base_of(w.max, c, limit)), bb(base_of(w.max, kLog2e, limit)), some(soft || hard) {
+        const float g = weight * a.scale;
+        gq = soft ? g * a.soft * a.inv_t : 0.0f;
+        gy = hard ? g * a.hard : 0.0f;
+        ca = w.a == 0.0f ? 0.0f : gq / w.a;
+        cb = w.b == 0.0f ? 0.0f : gy / w.b;
+        if (EXPS == kOne) ca += cb;
+    }
+    __device__ __forceinline__ float dense(float v, float c) const {
+        const float e = power(ba, v, c);
+        if (EXPS == kSquare) return e * fmaf(cb, e, ca);
+        return EXPS == kBoth ? fmaf(cb, power(bb, v, kLog2e), ca * e) : ca * e;
+    }
+    // the same for a group, where the bases are plain
+    template <typename TI>
+    __device__ __forceinline__ void dense8(const Raw<TI>& q, float c, float2* v) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const Two x = element2(q, j);
+            const float2 u = apart(fma2(x, two(c, c), two(-ba.k, -ba.k)));
+            const Two e = two(ex2(u.x), ex2(u.y));
+            Two d = mul2(e, EXPS == kSquare ? fma2(two(cb, cb), e, two(ca, ca)) : two(ca, ca));
+            if (EXPS == kBoth) {
+                const float2 f = apart(fma2(x, two(kLog2e, kLog2e), two(-bb.k, -bb.k)));
+                d = fma2(two(cb, cb), two(ex2(f.x), ex2(f.y)), d);
+            }
+            v[j] = apart(d);
+        }
+    }
+};
+
+// A thread's sums over its groups first, first + step, ... of part p, joined in
+// its warp. FREE: this is the last use of the groups in shared memory, and the
+// next row's (part np) take their places.
+//
+// The base of the sums need not be the largest logit: any number serves for which
+// they neither overflow nor vanish. It is `guess`, the log-sum of the row before;
+// only where the sums come out far from 1 is the largest logit looked for.
+template <typename TI, int EXPS, bool FREE>
+__device__ __forceinline__ Sums sums_of(uint4* slice, const Rows<TI>& rw, const Part<TI>& p, uint32_t kept, const Part<TI>& np,
+                                        uint32_t next_kept, float guess, uint32_t first, uint32_t step) {
+    const float c = rw.c;
+    const uint32_t room = rw.room;
+    constexpr float kLarge = 0x1p80f, kSmall = 0x1p-60f;
+    auto fine = [](float v) { return v > kSmall && v < kLarge; };
+    Taken<EXPS> sum(guess, c, rw.limit);
+    Sums s{guess, 0.0f, 0.0f};
+    bool good = sum.plain;
+    if (good) {
+#pragma unroll 2
+        for (uint32_t l = first; l < kept; l += step) sum.add(staged<TI>(slice, room, l), c);
+        s = sum.sums();
+        s.a = warp_sum(s.a);
+        s.b = EXPS != kOne ? warp_sum(s.b) : s.a;
+        good = fine(s.a) && fine(s.b);
+    }
+    if (!good) {
+        float m = -FLT_MAX;
+#pragma unroll 4
+        for (uint32_t l = first; l < kept; l += step) m = fmaxf(m, group_max(staged<TI>(slice, room, l)));
+        sum = Taken<EXPS>(warp_max(m), c, rw.limit);
+        if (sum.plain) {
+#pragma unroll 2
+            for (uint32_t l = first; l < kept; l += step) sum.add(staged<TI>(slice, room, l), c);
+        } else {
+            for (uint32_t l = first; l < kept; l += step) sum.add_any(staged<TI>(slice, room, l), c);
+        }
+        s = sum.sums();
+        s.a = warp_sum(s.a);
+        s.b = EXPS != kOne ? warp_sum(s.b) : s.a;
+    }
+    if (FREE) {
+        uint32_t l = first;
+        if (l == 0 && np.lo && l < next_kept) {
+            stage_group(slice, room, np, l, rw.a.V);
+            l += step;
+        }
+        const uint32_t fast = min(next_kept, np.lo + np.n);
+#pragma unroll 4
+        for (; l < fast; l += step) stage_inner(slice, room, np, l);
+        for (; l < next_kept; l += step) stage_group(slice, room, np, l, rw.a.V);
+    }
+    if (p.count > room) {  // what does not stay in shared memory
+        const float far = kFar / (EXPS == kBoth ? fmaxf(c, kLog2e) : EXPS == kSquare ? kLog2e : c);
+        float above = sum.plain ? sum.max + far : sum.max;
+        uint32_t r = first;
+        if (first < kept) r += (kept - first + step - 1) / step * step;
+#pragma unroll 2
+        for (; r < p.count; r += step) {
+            const Raw<TI> g = load_group(p, r, rw.a.V);
+            const float m = group_max(g);
+            if (m > above) {
+                sum.move(m, c, rw.limit);
+                above = sum.plain ? m + far : m;
+            }
+            sum.add_any(g, c);
+        }
+        s = join<EXPS>(sum.sums(), c, rw.limit);
+    }
+    return s;
 }
 
-// What a lane of the last warp knows of a row's entries and target before the
-// row's sums. In shared memory, a lane's own (21 words: no two lanes meet a
-// bank): in registers it would be carried through the other warps' loops.
+// The base for the next row: this one's log-sum.
+__device__ __forceinline__ float guess_from(const Sums& w, float c, float old) {
+    const float g = w.max + __log2f(w.a) / c;
+    return w.a > 0.0f && fabsf(g) < FLT_MAX ? g : old;
+}
+
+// Stores a thread's groups of the gradient's dense part; the next row's take the
+// places of those in shared memory.
+template <typename TI, typename TO, int EXPS>
+__device__ __forceinline__ void store_dense(TO* dz, uint4* slice, const Rows<TI>& rw, const Factors<EXPS>& f, const Part<TI>& p, uint32_t kept,
+                                            const Part<TI>& np, uint32_t next_kept, uint32_t first, uint32_t step) {
+    const uint32_t V = rw.a.V, room = rw.room;
+    const float c = rw.c;
+    const bool plain = f.ba.plain && f.some, wide = rw.a.wide;
+    auto any = [&](uint32_t l) {  // any group of this row or the next
+        if (l < p.count) {
+            float2 v[4] = {};
+            if (f.some) {
+                const Raw<TI> q = l < kept ? staged<TI>(slice, room, l) : load_group(p, l, V);
+                if (plain) {
+                    f.dense8(q, c, v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] = make_float2(f.dense(element(q, 2 * j), c), f.dense(element(q, 2 * j + 1), c));
+                }
+            }
+            store_group(dz, p, l, V, wide, v);
+        }
+        if (l < next_kept) stage_group(slice, room, np, l, V);
+    };
+    const uint32_t both = max(p.count, next_kept);
+    uint32_t l = first;
+    if (plain && wide) {  // groups in the midst of both rows
+        if (l == 0 && (p.lo | np.lo) && l < both) {
+            any(l);
+            l += step;
+        }
+        TO* at = dz + p.index(0, 0);
+        const uint32_t mid = p.lo + p.n, here = min(mid, kept), fast = next_kept ? min(here, min(np.lo + np.n, next_kept)) : 0;
+#pragma unroll 2
+        for (; l < fast; l += step) {
+            float2 v[4];
+            f.dense8(staged<TI>(slice, room, l), c, v);
+            stage_inner(slice, room, np, l);
+            put8(at + (uint64_t)l * 8, v);
+        }
+        if (!next_kept) {
+#pragma unroll 2
+            for (; l < here; l += step) {
+                float2 v[4];
+                f.dense8(staged<TI>(slice, room, l), c, v);
+                put8(at + (uint64_t)l * 8, v);
+            }
+        }
+        const uint32_t rest = max(kept, next_kept);
+        for (; l < rest; l += step) any(l);
+#pragma unroll 2
+        for (; l < mid; l += step) {
+            float2 v[4];
+            f.dense8(load_inner(p, l), c, v);
+            put8(at + (uint64_t)l * 8, v);
+        }
+    }
+    for (; l < both; l += step) any(l);
+}
+
+// The row's loss, from what the lanes' blocks know; in lane 0.
+template <int EXPS>
+__device__ __forceinline__ float loss_of(const Record& r, const Sums& w, bool mine, bool soft, float weight, const DistillArgs& a, float c, float limit) {
+    const Base ba = base_of(w.max, c, limit), bb = base_of(w.max, kLog2e, limit);
+    float sum = 0.0f;
+    if (mine) {
+        if (soft) sum += a.soft * (r.cross + (r.mass == 0.0f ? 0.0f : r.mass * ((w.max - r.ref) * a.inv_t + log_sum(w.a, ba, c))));
+        if (r.flags & 1) sum += a.hard * ((w.max - r.target) + log_sum(w.b, EXPS != kOne ? bb : ba, EXPS != kOne ? kLog2e : c));
+    }
+    return warp_sum(sum) * weight;
+}
+
+// ---- up to 256 entries -----------------------------------------------------------
+
+constexpr int kSlots = 8;               // entries of a lane
+constexpr uint32_t kFew = 32 * kSlots;
+constexpr uint32_t kPlaces = 512;       // of the table that finds indices that stand twice
+constexpr uint32_t kNone = 0xffffffffu;
+constexpr uint32_t kHelpers = 96;       // threads that do not go over the logits
+
+struct Shared {
+    Record records[2][kMaxBlocks];  // of this row and the next, from every block
+    Sums sums[kMaxThreads / 32];
+    float4 entries[2];              // cross, mass, ref, target
+    uint32_t flags[2];
+    uint32_t table[2][kPlaces];
+    uint64_t full[2];               // the records are here
+    uint32_t dead;
+};
+
+__device__ __forceinline__ void arrive(uint32_t barrier, uint32_t threads) {
+    __syncwarp();  // the whole warp at once
+    asm volatile("bar.arrive %0, %1;" ::"r"(barrier), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void wait(uint32_t barrier, uint32_t threads) {
+    __syncwarp();
+    asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(threads) : "memory");
+}
+// 16 bytes to another block's shared memory; its barrier counts them.
+__device__ __forceinline__ void push16(uint32_t to, uint32_t barrier, const uint4& v) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to), "r"(v.x), "r"(v.y),
+                 "r"(v.z), "r"(v.w), "r"(barrier)
+                 : "memory");
+}
+
+// Barriers of a block: kSums: a row's sums and entries are there, and the records
+// of the row before have been read (all threads; the joining warp alone waits);
+// kStored + parity: the row's dense part is stored (the entries' warp waits).
+constexpr uint32_t kSums = 1, kStored = 2;
+
+// The rows of an entries' warp: what it holds of one.
+template <typename TI>
 struct Entries {
     uint32_t i[kSlots];
-    float t[kSlots], z[kSlots];  // z: of those in this block
-    Teacher all;
-    float inv_sum;  // 1 / all.sum
-    float ref;      // the largest z here
-    float cross, mass;
-    float target;   // the target's logit, where it is here
-    uint32_t y;
-    uint32_t flags;  // as in a record
+    float q[kSlots], z[kSlots];  // q: logits, then probabilities; z: of those in this block
+    float target;
+    uint32_t y, flags;
+    bool twice, listed;
 
-    __device__ __forceinline__ float prob(int s, float ct) const { return ex2((t[s] - all.max) * ct) * inv_sum; }
-    // The loads of what `f` names; finish() is called after a while.
-    template <typename TI>
-    __device__ __forceinline__ void begin(const Fetched& f, const DistillArgs& a, bool alive, const TI* zr, const Part<TI>& p, bool few) {
+    __device__ __forceinline__ void fetch(const Rows<TI>& rw, uint64_t row) {
+        const DistillArgs& a = rw.a;
         const uint32_t lane = threadIdx.x % 32;
-        y = alive && a.use_hard ? f.y[lane] : 0xffffffffu;
-        const bool has = p.holds(y, a.V);
-        flags = (uint32_t)has | (y < a.V ? 4u : 0u);
-        float v[kSlots + 1];
-        v[kSlots] = has ? to_float(zr[y]) : 0.0f;
-        uint32_t at[kSlots];
+        const bool there = rw.there(row);
+        y = there && a.use_hard ? (uint32_t)a.targets[row] : kNone;
 #pragma unroll
         for (int s = 0; s < kSlots; ++s) {
             const uint32_t k = s * 32 + lane;
-            const bool there = alive && few && k < a.K;
-            at[s] = there ? f.i[k] : 0xffffffffu;
-            t[s] = there ? f.t[k] : 0.0f;
-            v[s] = p.holds(at[s], a.V) ? to_float(zr[at[s]]) : -FLT_MAX;
+            const bool some = there && a.use_soft && k < a.K;
+            i[s] = some ? (uint32_t)a.idx[row * a.K + k] : kNone;
+            q[s] = some ? a.t[row * a.K + k] : 0.0f;
         }
-#pragma unroll
-        for (int s = 0; s < kSlots; ++s) {
-            i[s] = at[s];
-            z[s] = v[s];
-        }
-        target = v[kSlots];
     }
-    template <typename TI>
-    __device__ __forceinline__ void finish(const DistillArgs& a, bool alive, const Part<TI>& p, bool few) {
-        cross = mass = ref = 0.0f;
-        if (!alive || !few) return;
-        Teacher sum{-FLT_MAX, 0.0f};
-        float top = -FLT_MAX, part = 0.0f, weight = 0.0f;
+    // The logits that belong to what fetch() brought.
+    __device__ __forceinline__ void gather(const Rows<TI>& rw, uint64_t row, const Part<TI>& p) {
+        const TI* zr = rw.logits(row);
+        const bool has = p.holds(y, rw.a.V);
+        flags = (uint32_t)has | (y < rw.a.V ? 4u : 0u);
+        target = has ? to_float(zr[y]) : 0.0f;
+#pragma unroll
+        for (int s = 0; s < kSlots; ++s) z[s] = p.holds(i[s], rw.a.V) ? to_float(zr[i[s]]) : -FLT_MAX;
+    }
+    // Probabilities, and this block's part of the soft term: cross, mass, ref, target.
+    __device__ __forceinline__ float4 finish(const Rows<TI>& rw, const Part<TI>& p, uint32_t* table, bool grad) {
+        const DistillArgs& a = rw.a;
+        const uint32_t lane = threadIdx.x % 32, V = a.V;
+        twice = listed = false;
+        if (!a.use_soft) return make_float4(0.0f, 0.0f, 0.0f, target);
+        float most = -FLT_MAX, top = -FLT_MAX, sum = 0.0f, cross = 0.0f, mass = 0.0f;
 #pragma unroll
         for (int s = 0; s < kSlots; ++s) {
-            if (i[s] < a.V) see(sum, t[s], a.ct);
+            if (i[s] < V) most = fmaxf(most, q[s]);
             top = fmaxf(top, z[s]);
         }
-        sum = join(sum, a.ct);
+        most = warp_max(most);
         top = warp_max(top);
-        const float inv = 1.0f / sum.sum, log_sum = logf(sum.sum);
+        float x[kSlots];
 #pragma unroll
         for (int s = 0; s < kSlots; ++s) {
-            const float q = ex2((t[s] - sum.max) * a.ct) * inv;
-            if (!p.holds(i[s], a.V) || q == 0.0f) continue;
-            part += q * ((t[s] - sum.max) * a.inv_t - log_sum - (z[s] - top) * a.inv_t);
-            weight += q;
+            x[s] = q[s] - most;
+            q[s] = i[s] < V ? ex2(x[s] * a.ct) : 0.0f;
+            sum += q[s];
+            listed |= i[s] == y && i[s] < V;
         }
-        all = sum;
-        inv_sum = inv;
-        ref = top;
-        if (sum.sum == 0.0f) return;  // no entry of weight
-        cross = warp_sum(part);
-        mass = warp_sum(weight);
-        flags |= 2u;
-    }
-};
-
-// All warps but the last go over the logits; the last one sees to the teacher's
-// entries and the target, joins the block's sums and passes them on.
-constexpr uint32_t kDense = kRowThreads - 32;
-constexpr uint32_t kLast = kRowWarps - 1;
-
-// The last warp waits until the others have stored a row; they go on.
-__device__ __forceinline__ void stored() { asm volatile("bar.arrive 1, %0;" ::"n"(kRowThreads) : "memory"); }
-__device__ __forceinline__ void stored_wait() { asm volatile("bar.sync 1, %0;" ::"n"(kRowThreads) : "memory"); }
-
-// TO: the gradient's type, void for the loss alone. TWO: both sums are needed
-// and differ. STAGED: the block's part of a row fits in shared memory (`room`
-// groups); else it is read again from global memory.
-template <typename TI, typename TO, bool TWO, bool STAGED>
-__global__ void __launch_bounds__(kRowThreads, kResident) distill_kernel(const DistillArgs a, uint32_t room, uint32_t log2_blocks, float limit) {
-    constexpr bool kGrad = !std::is_same<TO, void>::value;
-    extern __shared__ uint4 slice[];
-    __shared__ Sums warp_sums[kRowWarps];
-    __shared__ Teacher warp_teacher[kRowWarps];
-    __shared__ float2 warp_cross[kRowWarps];
-    __shared__ Record records[2];
-    __shared__ Entries entries[2][32];
-    __shared__ Fetched fetched[2];
-    stream_order();
-    const uint32_t blocks = 1u << log2_blocks, rank = blocks > 1 ? cluster_rank() : 0;
-    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const float c = a.use_soft ? a.ct : kLog2e;  // of the first sum
-    const bool many = a.use_soft && a.K > kFew, few = a.use_soft && !many;
-    const uint64_t rows = gridDim.x >> log2_blocks;
-    auto row_at = [&](uint64_t row) { return static_cast<const TI*>(a.z) + row * a.ld; };
-    auto weight_of = [&](uint64_t row) { return a.row_weight ? a.row_weight[row] : 1.0f; };
-
-    uint64_t row = blockIdx.x >> log2_blocks;
-    float weight = row < a.T ? weight_of(row) : 0.0f;
-    Part<TI> p = part_of(row_at(row < a.T ? row : 0), a.V, rank, log2_blocks);
-    if (warp == kLast) {
-        fetch(fetched[0], a, row, few);
-        copies_done();
-        if (row < a.T) {
-            entries[0][lane].begin(fetched[0], a, weight != 0.0f, row_at(row), p, few);
-            entries[0][lane].finish(a, weight != 0.0f, p, few);
-        }
-        fetch(fetched[1], a, row + rows, few);
-    } else if (STAGED && weight != 0.0f) {
-        stage(slice, room, p, a.V, threadIdx.x, kDense);
-    }
-    for (uint32_t turn = 0; row < a.T; row += rows, turn ^= 1) {
-        const bool alive = weight != 0.0f;
-        Entries& e = entries[turn][lane];  // the last warp's
-        // the row after this one
-        const uint64_t next = row + rows;
-        const float next_weight = next < a.T ? weight_of(next) : 0.0f;
-        const TI* z = row_at(row);
-        Part<TI> np = part_of(row_at(next < a.T ? next : row), a.V, rank, log2_blocks);
-        const uint32_t next_count = next_weight != 0.0f ? np.count : 0;
-
-        Sums s{-FLT_MAX, 0.0f, 0.0f};
-        if (warp != kLast) {
-            if (STAGED) copies_done();
-            if (alive) {
-                // the warp's largest first: its lanes then share a base, and no sum is ever moved to another
-                auto group = [&](uint32_t l) { return STAGED ? staged<TI>(slice, room, l) : load_group(p, l, a.V); };
-#pragma unroll 4
-                for (uint32_t l = threadIdx.x; l < p.count; l += kDense) s.max = fmaxf(s.max, group_max(group(l)));
-                s.max = warp_max(s.max);
-                const Base ba = base_of(s.max, c, limit), bb = base_of(s.max, kLog2e, limit);
-                Two sa = two(0.0f, 0.0f), sb = sa;
-                auto add = [&](const Raw<TI>& r) {
+        sum = warp_sum(sum);
+        if (!(sum == 0.0f)) {
+            flags |= 2u;
+            const float inv = 1.0f / sum, log_all = logf(sum);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const Two v = element2(r, j);
-                        const float2 x = apart(fma2(v, two(c, c), two(-ba.k, -ba.k)));
-                        sa = add2(sa, two(ex2(x.x), ex2(x.y)));
-                        if (TWO) {
-                            const float2 w = apart(fma2(v, two(kLog2e, kLog2e), two(-bb.k, -bb.k)));
-                            sb = add2(sb, two(ex2(w.x), ex2(w.y)));
-                        }
-                    }
-                };
-                uint32_t l = threadIdx.x;
-                if (ba.plain && bb.plain) {
-                    if (!kGrad && STAGED) {  // a group is taken for the last time: the next row's takes its place
-                        if (l == 0 && np.lo && l < p.count) {
-                            add(group(l));
-                            if (l < next_count) stage_group(slice, room, np, l, a.V);
-                            l += kDense;
-                        }
-                        const uint32_t fast = min(p.count, next_count ? np.lo + np.n : 0);
-#pragma unroll 2
-                        for (; l < fast; l += kDense) {
-                            add(group(l));
-                            stage_inner(slice, room, np, l);
-                        }
-                    }
-#pragma unroll 2
-                    for (; l < p.count; l += kDense) {
-                        add(group(l));
-                        if (!kGrad && STAGED && l < next_count) stage_group(slice, room, np, l, a.V);
-                    }
-                } else {
-                    for (; l < p.count; l += kDense) {
-                        const Raw<TI> r = group(l);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float x = element(r, 2 * j), w = element(r, 2 * j + 1);
-                            sa = add2(sa, two(power(ba, x, c), power(ba, w, c)));
-                            if (TWO) sb = add2(sb, two(power(bb, x, kLog2e), power(bb, w, kLog2e)));
-                        }
-                        if (!kGrad && STAGED && l < next_count) stage_group(slice, room, np, l, a.V);
-                    }
-                }
-                const float2 ha = apart(sa), hb = apart(sb);
-                s.a = ha.x + ha.y;
-                s.b = hb.x + hb.y;
-            }
-            if (!kGrad && STAGED)  // (a part may have a group more than the one before it)
-                for (uint32_t l = threadIdx.x; l < next_count; l += kDense)
-                    if (!alive || l >= p.count) stage_group(slice, room, np, l, a.V);
-            s.a = warp_sum(s.a);
-            s.b = TWO ? warp_sum(s.b) : s.a;
-            if (lane == 0) warp_sums[warp] = s;
-        }
-        const int32_t* idx = a.idx + row * a.K;
-        const float* t = a.t + row * a.K;
-        Teacher tea{-FLT_MAX, 0.0f};
-        if (many && alive) {
-            for (uint32_t k = threadIdx.x; k < a.K; k += kRowThreads)
-                if ((uint32_t)idx[k] < a.V) see(tea, t[k], a.ct);
-            tea = join(tea, a.ct);
-            if (lane == 0) warp_teacher[warp] = tea;
-        }
-        __syncthreads();
-        if (warp == kLast || many) {  // the block's
-            s = lane < kLast ? warp_sums[lane] : Sums{-FLT_MAX, 0.0f, 0.0f};
-            s = join<TWO>(s, c, limit);
-        }
-        float inv_tsum = 0.0f;
-        auto prob = [&](float v) { return ex2((v - tea.max) * a.ct) * inv_tsum; };
-        if (many) {  // every warp has a share of the entries
-            float cross = 0.0f, mass = 0.0f;
-            if (alive) tea = join(lane < kRowWarps ? warp_teacher[lane] : Teacher{-FLT_MAX, 0.0f}, a.ct);
-            const bool some = !(tea.sum == 0.0f);
-            inv_tsum = 1.0f / tea.sum;
-            if (some) {
-                const float log_tsum = logf(tea.sum);
-                for (uint32_t k = threadIdx.x; k < a.K; k += kRowThreads) {
-                    const uint32_t i = (uint32_t)idx[k];
-                    const float q = prob(t[k]);
-                    if (!p.holds(i, a.V) || q == 0.0f) continue;
-                    cross += q * ((t[k] - tea.max) * a.inv_t - log_tsum - (to_float(z[i]) - s.max) * a.inv_t);
-                    mass += q;
-                }
+            for (int s = 0; s < kSlots; ++s) {
+                q[s] *= inv;
+                if (!p.holds(i[s], V) || q[s] == 0.0f) continue;
+                cross += q[s] * (x[s] * a.inv_t - log_all - (z[s] - top) * a.inv_t);
+                mass += q[s];
             }
             cross = warp_sum(cross);
             mass = warp_sum(mass);
-            if (lane == 0) warp_cross[warp] = make_float2(cross, mass);
-            __syncthreads();
-            if (warp == kLast) {
-                const float2 w = lane < kRowWarps ? warp_cross[lane] : make_float2(0.0f, 0.0f);
-                e.cross = warp_sum(w.x);
-                e.mass = warp_sum(w.y);
-                e.ref = s.max;
-                e.flags |= some ? 2u : 0u;
-            }
         }
-        if (warp == kLast && lane == 0)
-            records[turn] = {s.max, s.a, s.b, e.cross, e.mass, e.ref, e.target, e.flags};
-        // (only the last warp has something to hand over: the others' stores need not be waited for)
-        if (blocks == 1) {
-            __syncthreads();
-        } else {
-            if (warp == kLast) cluster_arrive();
-            else cluster_arrive_relaxed();
-            cluster_wait();
-        }
-        // of the row, in every warp: a lane reads a block's record
-        Sums r{-FLT_MAX, 0.0f, 0.0f};
-        uint32_t flags = 0;
-        const uint32_t from = peer(&records[turn], lane < blocks ? lane : 0);
-        if (lane < blocks) {
-            r = {peer_float(from), peer_float(from + 4), peer_float(from + 8)};
-            flags = peer_u32(from + 28);
-        }
-        const bool soft = __any_sync(kAll, flags & 2), hard = __any_sync(kAll, flags & 4);  // (every block says the same)
-        const Sums w = join<TWO>(r, c, limit);
-        const Base ba = base_of(w.max, c, limit), bb = base_of(w.max, kLog2e, limit);
-        if (warp == kLast && rank == 0) {
-            double sum = 0.0;
-            if (lane < blocks) {
-                const float rc = peer_float(from + 12), rm = peer_float(from + 16), rr = peer_float(from + 20), rt = peer_float(from + 24);
-                if (soft) sum += (double)a.soft * ((double)rc + (rm == 0.0f ? 0.0 : (double)rm * (((double)w.max - rr) * a.inv_t + log_sum(w.a, ba, c))));
-                if (flags & 1) sum += (double)a.hard * ((double)w.max - rt + log_sum(w.b, TWO ? bb : ba, TWO ? kLog2e : c));
-            }
+        listed = __any_sync(kAll, listed) && (flags & 2u);
+        if (grad) {  // each index into a table of its own, where another of the same would be found
+            for (uint32_t t = lane; t < kPlaces; t += 32) table[t] = kNone;
+            __syncwarp();
 #pragma unroll
-            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-            if (lane == 0) a.loss[row] = soft || hard ? (float)(sum * weight) : 0.0f;
-        }
-        auto ahead = [&] {  // the last warp's: the next row's entries, and the fetching of those of the row after it
-            copies_done();
-            if (next < a.T) entries[turn ^ 1][lane].begin(fetched[turn ^ 1], a, next_weight != 0.0f, row_at(next), np, few);
-            fetch(fetched[turn], a, next + rows, few);
-        };
-        if constexpr (kGrad) {
-            TO* dz = static_cast<TO*>(a.dz) + row * a.ldd;
-            const float g = weight * a.scale;
-            const float gq = soft ? g * a.soft * a.inv_t : 0.0f, gy = hard ? g * a.hard : 0.0f;
-            float ca = w.a == 0.0f ? 0.0f : gq / w.a, cb = w.b == 0.0f ? 0.0f : gy / w.b;
-            if (!TWO) ca += cb;
-            const bool some = soft || hard;
-            auto dense = [&](float v) {
-                const float x = ca * power(ba, v, c);
-                return TWO ? fmaf(cb, power(bb, v, kLog2e), x) : x;
-            };
-            if (warp == kLast) {
-                ahead();
-            } else {
-                auto dense8 = [&](const Raw<TI>& q, float2* v) {  // where both bases are plain
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const Two x = element2(q, j);
-                        const float2 u = apart(fma2(x, two(c, c), two(-ba.k, -ba.k)));
-                        Two d = mul2(two(ca, ca), two(ex2(u.x), ex2(u.y)));
-                        if (TWO) {
-                            const float2 f = apart(fma2(x, two(kLog2e, kLog2e), two(-bb.k, -bb.k)));
-                            d = fma2(two(cb, cb), two(ex2(f.x), ex2(f.y)), d);
-                        }
-                        v[j] = apart(d);
+            for (int s = 0; s < kSlots; ++s) {
+                if (i[s] >= V) continue;
+                uint32_t at = (i[s] * 0x9E3779B1u) >> 23;  // (half full at most)
+                for (uint32_t tries = 0; tries < kPlaces; ++tries) {
+                    const uint32_t old = atomicCAS(table + at, kNone, i[s]);
+                    if (old == kNone) break;
+                    if (old == i[s]) {
+                        twice = true;
+                        break;
                     }
-                };
-                const bool plain = ba.plain && bb.plain && some;
-                auto any = [&](uint32_t l) {  // any group of this row or the next
-                    if (l < p.count) {
-                        float2 v[4] = {};
-                        if (some) {
-                            const Raw<TI> q = STAGED ? staged<TI>(slice, room, l) : load_group(p, l, a.V);
-                            if (plain) {
-                                dense8(q, v);
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) v[j] = make_float2(dense(element(q, 2 * j)), dense(element(q, 2 * j + 1)));
-                            }
-                        }
-                        store_group(dz, p, l, a.V, a.wide, v);
-                    }
-                    if (STAGED && l < next_count) stage_group(slice, room, np, l, a.V);
-                };
-                const uint32_t both = max(p.count, STAGED ? next_count : 0);
-                uint32_t l = threadIdx.x;
-                if (STAGED && plain && a.wide) {  // groups in the midst of both rows
-                    if (l == 0 && (p.lo | np.lo) && l < both) {
-                        any(l);
-                        l += kDense;
-                    }
-                    TO* at = dz + p.index(0, 0);
-                    const uint32_t mid = p.lo + p.n, fast = next_count ? min(mid, np.lo + np.n) : 0;
-#pragma unroll 2
-                    for (; l < fast; l += kDense) {
-                        float2 v[4];
-                        dense8(staged<TI>(slice, room, l), v);
-                        stage_inner(slice, room, np, l);
-                        put8(at + (uint64_t)l * 8, v);
-                    }
-                    if (!next_count) {
-#pragma unroll 2
-                        for (; l < mid; l += kDense) {
-                            float2 v[4];
-                            dense8(staged<TI>(slice, room, l), v);
-                            put8(at + (uint64_t)l * 8, v);
-                        }
-                    }
+                    at = (at + 1) % kPlaces;
                 }
-                for (; l < both; l += kDense) any(l);
             }
-            // the elements of the entries and the target are stored again, behind the dense ones
-            if (many || warp == kLast) stored_wait();
-            else stored();
-            if (many && soft) {
-                for (uint32_t k = warp; k < a.K; k += kRowWarps) {  // a warp each
-                    const uint32_t i = (uint32_t)idx[k];
-                    if (!p.holds(i, a.V)) continue;
-                    const uint32_t y = a.use_hard ? (uint32_t)a.targets[row] : 0xffffffffu;
+            twice = __any_sync(kAll, twice);
+        }
+        return make_float4(cross, mass, top, target);
+    }
+    // The gradient's elements at the entries and the target, over their dense part.
+    template <typename TO, int EXPS>
+    __device__ __forceinline__ void correct(TO* dz, const Rows<TI>& rw, const Factors<EXPS>& f, const Part<TI>& p, bool soft) const {
+        const uint32_t lane = threadIdx.x % 32, V = rw.a.V;
+        if (soft && !twice) {
+#pragma unroll
+            for (int s = 0; s < kSlots; ++s)
+                if (p.holds(i[s], V)) put(dz + i[s], f.dense(z[s], rw.c) - f.gq * q[s] - (i[s] == y ? f.gy : 0.0f));
+        } else if (soft) {
+#pragma unroll
+            for (int s = 0; s < kSlots; ++s) {
+                uint32_t todo = __ballot_sync(kAll, p.holds(i[s], V));
+                while (todo) {
+                    const int at = __ffs(todo) - 1;
+                    todo &= todo - 1;
+                    const uint32_t which = __shfl_sync(kAll, i[s], at);
+                    // an entry that stands before it sees to the others of its index
                     float sum = 0.0f;
                     bool first = true;
-                    for (uint32_t j = lane; j < a.K; j += 32) {
-                        if ((uint32_t)idx[j] != i) continue;
-                        sum += prob(t[j]);
-                        first &= j >= k;
+#pragma unroll
+                    for (int o = 0; o < kSlots; ++o) {
+                        const uint32_t same = __ballot_sync(kAll, i[o] == which);
+                        if (o < s) first &= same == 0;
+                        if (o == s) first &= (same & ((1u << at) - 1)) == 0;
+                        if (i[o] == which) sum += q[o];
                     }
-                    if (!__all_sync(kAll, first)) continue;
+                    if (!first) continue;
                     sum = warp_sum(sum);
-                    if (lane == 0) put(dz + i, dense(to_float(z[i])) - gq * sum - (i == y ? gy : 0.0f));
+                    if ((int)lane == at) put(dz + which, f.dense(z[s], rw.c) - f.gq * sum - (which == y ? f.gy : 0.0f));
                 }
             }
-            if (warp == kLast) {
-                if (few && soft) {
-#pragma unroll
-                    for (int k = 0; k < kSlots; ++k) {
-                        uint32_t todo = __ballot_sync(kAll, p.holds(e.i[k], a.V));
-                        while (todo) {
-                            const int at = __ffs(todo) - 1;
-                            todo &= todo - 1;
-                            const uint32_t i = __shfl_sync(kAll, e.i[k], at);
-                            // an entry that stands before it sees to the others of its index
-                            float sum = 0.0f;
-                            bool first = true;
-#pragma unroll
-                            for (int o = 0; o < kSlots; ++o) {
-                                const uint32_t same = __ballot_sync(kAll, e.i[o] == i);
-                                if (o < k) first &= same == 0;
-                                if (o == k) first &= (same & ((1u << at) - 1)) == 0;
-                                if (e.i[o] == i) sum += e.prob(o, a.ct);
-                            }
-                            if (!first) continue;
-                            sum = warp_sum(sum);
-                            if ((int)lane == at) put(dz + i, dense(e.z[k]) - gq * sum - (i == e.y ? gy : 0.0f));
-                        }
-                    }
-                }
-                if (e.flags & 1) {  // the target, where no entry has seen to it
-                    bool listed = false;
-                    if (few && soft) {
-#pragma unroll
-                        for (int k = 0; k < kSlots; ++k) listed |= e.i[k] == e.y;
-                    } else if (many && soft) {
-                        for (uint32_t j = lane; j < a.K; j += 32) listed |= (uint32_t)idx[j] == e.y;
-                    }
-                    if (!__any_sync(kAll, listed) && lane == 0) put(dz + e.y, dense(e.target) - gy);
-                }
-                if (next < a.T) entries[turn ^ 1][lane].finish(a, next_weight != 0.0f, np, few);
-            }
-        } else if (warp == kLast) {
-            ahead();
-            if (next < a.T) entries[turn ^ 1][lane].finish(a, next_weight != 0.0f, np, few);
         }
-        weight = next_weight;
-        p = np;
+        if ((flags & 1u) && !listed && lane == 0) put(dz + y, f.dense(target, rw.c) - f.gy);
     }
-    if (blocks > 1) cluster_barrier();  // no block ends while another reads its record
+};
+
+// TO: the gradient's type, void for the loss alone. EXPS: a logit's
+// exponentials. `room` groups of the block's part of a row stay in shared memory;
+// what lies behind them is read again.
+template <typename TI, typename TO, int EXPS>
+__global__ void __launch_bounds__(kMaxThreads, 1) distill_kernel(const DistillArgs a, uint32_t room, uint32_t log2_blocks, float limit, uint32_t* faults) {
+    constexpr bool kGrad = !std::is_same<TO, void>::value;
+    extern __shared__ uint4 slice[];
+    __shared__ Shared sh;
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, threads = blockDim.x, dense_threads = threads - kHelpers;
+    const uint32_t blocks = 1u << log2_blocks;
+    if (threadIdx.x == 0) {
+        tc::bar_init(tc::smem_u32(&sh.full[0]), 1);
+        tc::bar_init(tc::smem_u32(&sh.full[1]), 1);
+        tc::bar_fence_init();
+        sh.dead = 0;
+    }
+    if (blocks > 1) cluster_barrier();  // before another block's records come
+    else __syncthreads();
+    stream_order();
+    Rows<TI> rw{a, blocks > 1 ? cluster_rank() : 0, log2_blocks, room, a.use_soft ? a.ct : kLog2e, limit, blockIdx.x >> log2_blocks, gridDim.x >> log2_blocks};
+    const tc::Wait wt{&sh.dead, faults};
+    // Waits for the records of the cluster's n-th row and joins them. (Should a
+    // wait run out, the rows go on with what is there: nothing else depends on it.)
+    auto joined = [&](uint32_t n, Record& r, bool& soft, bool& hard) {
+        __syncwarp();
+        tc::bar_wait(tc::smem_u32(&sh.full[n & 1]), (n >> 1) & 1, wt);
+        r = {-FLT_MAX, 0.0f, 0.0f, 0u, 0.0f, 0.0f, 0.0f, 0.0f};
+        if (lane < blocks) r = sh.records[n & 1][lane];
+        soft = __any_sync(kAll, r.flags & 2u);  // (every block says the same)
+        hard = __any_sync(kAll, r.flags & 4u);
+        return join<EXPS>({r.max, r.soft, r.hard}, rw.c, limit);
+    };
+
+    if (threadIdx.x < dense_threads) {
+        float weight = rw.weight(rw.row), next_weight = rw.weight(rw.row + rw.step);
+        Part<TI> p = rw.part(rw.row);
+        float guess = FLT_MAX;  // none yet
+        for (uint32_t l = threadIdx.x, n = rw.kept(p, weight); l < n; l += dense_threads) stage_group(slice, room, p, l, a.V);
+        for (uint32_t n = 0; rw.there(rw.row); ++n, rw.row += rw.step) {
+            const float after = rw.weight(rw.row + 2 * rw.step);
+            const Part<TI> np = rw.part(rw.row + rw.step);
+            const uint32_t kept = rw.kept(p, weight), next_kept = rw.kept(np, next_weight);
+            Sums s{-FLT_MAX, 0.0f, 0.0f};
+            copies_done();
+            if (weight != 0.0f) {
+                s = sums_of<TI, EXPS, !kGrad>(slice, rw, p, kept, np, next_kept, guess, threadIdx.x, dense_threads);
+            } else if (!kGrad) {
+                for (uint32_t l = threadIdx.x; l < next_kept; l += dense_threads) stage_group(slice, room, np, l, a.V);
+            }
+            if (lane == 0) sh.sums[warp] = s;
+            arrive(kSums, threads);
+            Record r;
+            bool soft, hard;
+            const Sums w = joined(n, r, soft, hard);
+            guess = guess_from(w, rw.c, guess);
+            if constexpr (kGrad) {
+                const Factors<EXPS> f(w, soft, hard, weight, a, rw.c, limit);
+                store_dense(static_cast<TO*>(a.dz) + rw.row * a.ldd, slice, rw, f, p, kept, np, next_kept, threadIdx.x, dense_threads);
+                arrive(kStored + (n & 1), dense_threads + 32);
+            }
+            weight = next_weight;
+            next_weight = after;
+            p = np;
+        }
+    } else if (threadIdx.x < dense_threads + 32) {  // joins
+        for (uint32_t n = 0; rw.there(rw.row); ++n, rw.row += rw.step) {
+            const float weight = rw.weight(rw.row);
+            wait(kSums, threads);
+            Sums s = lane < dense_threads / 32 ? sh.sums[lane] : Sums{-FLT_MAX, 0.0f, 0.0f};
+            s = join<EXPS>(s, rw.c, limit);
+            const float4 e = sh.entries[n & 1];
+            const uint32_t at = tc::smem_u32(&sh.records[n & 1][rw.rank]), bar = tc::smem_u32(&sh.full[n & 1]);
+            if (lane == 0) tc::bar_expect(bar, blocks * (uint32_t)sizeof(Record));
+            __syncwarp();
+            if (lane < blocks) {
+                uint32_t to, of;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(at), "r"(lane));
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(of) : "r"(bar), "r"(lane));
+                push16(to, of, make_uint4(__float_as_uint(s.max), __float_as_uint(s.a), __float_as_uint(s.b), sh.flags[n & 1]));
+                push16(to + 16, of, make_uint4(__float_as_uint(e.x), __float_as_uint(e.y), __float_as_uint(e.z), __float_as_uint(e.w)));
+            }
+            Record r;
+            bool soft, hard;
+            const Sums w = joined(n, r, soft, hard);
+            if (rw.rank == 0) {
+                const float loss = loss_of<EXPS>(r, w, lane < blocks, soft, weight, a, rw.c, limit);
+                if (lane == 0) a.loss[rw.row] = soft || hard ? loss : 0.0f;
+            }
+        }
+    } else {  // entries of every second row
+        const uint32_t parity = warp - dense_threads / 32 - 1;
+        const uint64_t first = rw.row;
+        Entries<TI> e;
+        if (parity == 1 && rw.there(first)) arrive(kSums, threads);
+        rw.row += parity * rw.step;
+        e.fetch(rw, rw.row);
+        for (uint32_t n = parity; rw.there(rw.row); n += 2, rw.row += 2 * rw.step) {
+            const float weight = rw.weight(rw.row);
+            const Part<TI> p = rw.part(rw.row);
+            float4 own = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (weight != 0.0f) {
+                e.gather(rw, rw.row, p);
+                own = e.finish(rw, p, sh.table[parity], kGrad);
+            } else {
+                e.flags = 0;
+                e.listed = e.twice = false;
+            }
+            if (lane == 0) {
+                sh.entries[parity] = own;
+                sh.flags[parity] = e.flags;
+            }
+            __syncwarp();
+            if (n > 0) tc::bar_wait(tc::smem_u32(&sh.full[(n - 1) & 1]), ((n - 1) >> 1) & 1, wt);  // kSums of that row is over
+            arrive(kSums, threads);
+            Record r;
+            bool soft, hard;
+            const Sums w = joined(n, r, soft, hard);
+            if (rw.there(rw.row + rw.step)) arrive(kSums, threads);
+            if constexpr (kGrad) {
+                const Factors<EXPS> f(w, soft, hard, weight, a, rw.c, limit);
+                wait(kStored + parity, dense_threads + 32);
+                if (f.some) e.correct(static_cast<TO*>(a.dz) + rw.row * a.ldd, rw, f, p, soft);
+            }
+            e.fetch(rw, rw.row + 2 * rw.step);
+        }
+    }
+    __syncwarp();
+    if (blocks > 1) cluster_barrier();  // no block ends while another's records are on their way to it
 }
 
-template <typename TI, typename TO, bool TWO>
-cudaError_t launch(const DistillArgs& a, cudaStream_t s) {
+// ---- more entries ------------------------------------------------------------------
+
+// Every warp has a share of the entries, row by row: no table holds them, and an
+// index that stands twice is found by going through the list for each.
+template <typename TI, typename TO, int EXPS>
+__global__ void __launch_bounds__(kMaxThreads, 1) distill_many_kernel(const DistillArgs a, uint32_t room, uint32_t log2_blocks, float limit, uint32_t*) {
+    constexpr bool kGrad = !std::is_same<TO, void>::value;
+    extern __shared__ uint4 slice[];
+    __shared__ Sums warp_sums[kMaxThreads / 32];
+    __shared__ float2 warp_teacher[kMaxThreads / 32], warp_cross[kMaxThreads / 32];
+    __shared__ Record records[2];
+    stream_order();
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, threads = blockDim.x, warps = threads / 32;
+    const uint32_t blocks = 1u << log2_blocks;
+    const Rows<TI> rw{a, blocks > 1 ? cluster_rank() : 0, log2_blocks, room, a.ct, limit, blockIdx.x >> log2_blocks, gridDim.x >> log2_blocks};
+    uint32_t turn = 0;
+    for (uint64_t row = rw.row; rw.there(row); row += rw.step, turn ^= 1) {
+        const float weight = rw.weight(row);
+        const bool alive = weight != 0.0f;
+        const Part<TI> p = rw.part(row);
+        const TI* z = rw.logits(row);
+        const uint32_t kept = rw.kept(p, weight);
+        const int32_t* idx = a.idx + row * a.K;
+        const float* t = a.t + row * a.K;
+        const uint32_t y = alive && a.use_hard ? (uint32_t)a.targets[row] : kNone;
+        for (uint32_t l = threadIdx.x; l < kept; l += threads) stage_group(slice, room, p, l, a.V);
+        // log-sum of the entries: largest, and sum over it
+        float most = -FLT_MAX, sum = 0.0f;
+        if (alive)
+            for (uint32_t k = threadIdx.x; k < a.K; k += threads)
+                if ((uint32_t)idx[k] < a.V) {
+                    const float m = fmaxf(most, t[k]);
+                    sum = sum * ex2((most - m) * a.ct) + ex2((t[k] - m) * a.ct);
+                    most = m;
+                }
+        auto join_teacher = [&](float& m, float& v) {
+            const float to = warp_max(m);
+            v = warp_sum(v * ex2((m - to) * a.ct));
+            m = to;
+        };
+        join_teacher(most, sum);
+        copies_done();
+        Sums s{-FLT_MAX, 0.0f, 0.0f};
+        if (alive) s = sums_of<TI, EXPS, false>(slice, rw, p, kept, p, 0, FLT_MAX, threadIdx.x, threads);
+        if (lane == 0) {
+            warp_sums[warp] = s;
+            warp_teacher[warp] = make_float2(most, sum);
+        }
+        __syncthreads();
+        s = join<EXPS>(lane < warps ? warp_sums[lane] : Sums{-FLT_MAX, 0.0f, 0.0f}, rw.c, limit);
+        most = lane < warps ? warp_teacher[lane].x : -FLT_MAX;
+        sum = lane < warps ? warp_teacher[lane].y : 0.0f;
+        join_teacher(most, sum);
+        const bool some = !(sum == 0.0f);
+        const float inv = 1.0f / sum, log_all = logf(sum);
+        auto prob = [&](uint32_t k) { return ex2((t[k] - most) * a.ct) * inv; };
+        float cross = 0.0f, mass = 0.0f;
+        if (some)
+            for (uint32_t k = threadIdx.x; k < a.K; k += threads) {
+                const uint32_t i = (uint32_t)idx[k];
+                if (!p.holds(i, a.V)) continue;
+                const float q = prob(k);
+                if (q == 0.0f) continue;
+                cross += q * ((t[k] - most) * a.inv_t - log_all - (to_float(z[i]) - s.max) * a.inv_t);
+                mass += q;
+            }
+        cross = warp_sum(cross);
+        mass = warp_sum(mass);
+        if (lane == 0) warp_cross[warp] = make_float2(cross, mass);
+        __syncthreads();
+        const bool has = p.holds(y, a.V);
+        if (warp == 0) {
+            cross = warp_sum(lane < warps ? warp_cross[lane].x : 0.0f);
+            mass = warp_sum(lane < warps ? warp_cross[lane].y : 0.0f);
+            if (lane == 0)
+                records[turn] = {s.max, s.a, s.b, (uint32_t)has | (some ? 2u : 0u) | (y < a.V ? 4u : 0u), cross, mass, s.max, has ? to_float(z[y]) : 0.0f};
+        }
+        cluster_barrier();
+        Record r{-FLT_MAX, 0.0f, 0.0f, 0u, 0.0f, 0.0f, 0.0f, 0.0f};
+        if (lane < blocks) {
+            const uint32_t at = peer(&records[turn], lane);
+            r = {peer_float(at), peer_float(at + 4), peer_float(at + 8), peer_u32(at + 12), peer_float(at + 16), peer_float(at + 20), peer_float(at + 24), peer_float(at + 28)};
+        }
+        const bool hard = y < a.V;
+        const Sums w = join<EXPS>({r.max, r.soft, r.hard}, rw.c, limit);
+        if (rw.rank == 0 && warp == 0) {
+            const float loss = loss_of<EXPS>(r, w, lane < blocks, some, weight, a, rw.c, limit);
+            if (lane == 0) a.loss[row] = some || hard ? loss : 0.0f;
+        }
+        if constexpr (kGrad) {
+            TO* dz = static_cast<TO*>(a.dz) + row * a.ldd;
+            const Factors<EXPS> f(w, some, hard, weight, a, rw.c, limit);
+            store_dense(dz, slice, rw, f, p, kept, p, 0, threadIdx.x, threads);
+            __syncthreads();  // the elements below are stored again
+            for (uint32_t k = warp; k <= a.K; k += warps) {  // a warp each, the target behind the entries
+                if (k == a.K ? !has : !some) continue;
+                const uint32_t i = k == a.K ? y : (uint32_t)idx[k];
+                if (!p.holds(i, a.V)) continue;
+                float q = 0.0f;
+                bool first = true;
+                for (uint32_t j = lane; some && j < a.K; j += 32) {
+                    if ((uint32_t)idx[j] != i) continue;
+                    q += prob(j);
+                    first &= j >= k;
+                }
+                if (!__all_sync(kAll, first)) continue;  // an entry before it has seen to it
+                q = warp_sum(q);
+                if (lane == 0) put(dz + i, f.dense(to_float(z[i]), rw.c) - f.gq * q - (i == y ? f.gy : 0.0f));
+            }
+            __syncthreads();
+        }
+    }
+    cluster_barrier();  // no block ends while another reads its record
+}
+
+// How a row is spread: threads of a block, blocks on an SM, shared memory of a
+// block's part of a row. Estimated nanoseconds of a round of rows, fitted to rows
+// of 33278 and 267735 in every spread (2048 x 267735 bfloat16 with its gradient:
+// three blocks of an SM and eight of a row 434 us; two and eight 472, two and four
+// 506, one and two 516, three and sixteen 664; one and one 680): joining its sums, 62 bytes of
+// logits and gradient a nanosecond on an SM, 16 where the logits are read again.
+struct Spread {
+    uint32_t threads, per_sm, smem;
+};
+constexpr Spread kSpreads[3] = {{1024, 1, 208 * 1024}, {512, 2, 104 * 1024}, {320, 3, 66 * 1024}};
+constexpr double kJoinNs = 4500.0, kBytesNs = 62.0, kAgainNs = 16.0;
+
+template <typename TI, typename TO, int EXPS>
+cudaError_t launch(const DistillArgs& a, uint32_t* faults, cudaStream_t s) {
     const uint64_t groups = ((uint64_t)a.V + 14) / 8;  // whatever the row's alignment
     constexpr uint64_t kGroupBytes = 8 * sizeof(TI);
-    // The number of blocks that share a row: the fewest groups that a block goes
-    // through in all, a row counting kRowCost of them more for the joining of its sums.
-    constexpr uint64_t kRowCost = 1000;
-    uint64_t best = ~0ull;
-    uint32_t blocks = 0, room = 0, clusters = 0, log2_blocks = 0;
-    auto kernel = distill_kernel<TI, TO, TWO, false>;
-    for (uint32_t b = 1; b <= 16; b *= 2) {
-        const uint64_t need = (groups + b - 1) / b + 1;
-        const uint64_t smem = smem_of(need * kGroupBytes);
-        const bool fits = smem <= 66 * 1024;  // kResident times in an SM, beside 8 KB of the kernel's own
-        if (!fits && b < 16) continue;
-        if (b > 1 && groups < b * (uint64_t)kRowThreads / 2) break;  // too little for so many
-        auto k = fits ? distill_kernel<TI, TO, TWO, true> : distill_kernel<TI, TO, TWO, false>;
-        int n = 0;
-        const cudaError_t e = resident_clusters(reinterpret_cast<const void*>(k), kRowThreads, b, fits ? smem : 0, &n);
-        if (e != cudaSuccess) return e;
-        if (n < 1) continue;
-        const uint64_t cost = ((uint64_t)a.T + n - 1) / n * (need + kRowCost);
-        if (cost >= best) continue;
-        best = cost;
-        blocks = b;
-        room = fits ? (uint32_t)need : 0;
-        clusters = (uint32_t)n;
-        kernel = k;
+    constexpr double kMoved = kGroupBytes + (std::is_same<TO, void>::value ? 0.0 : std::is_same<TO, float>::value ? 32.0 : 16.0);
+    DeviceInfo di{};
+    cudaError_t e = device_info(&di);
+    if (e != cudaSuccess) return e;
+    auto kernel = a.use_soft && a.K > kFew ? distill_many_kernel<TI, TO, EXPS> : distill_kernel<TI, TO, EXPS>;
+    double best = 0.0;
+    uint32_t blocks = 0, log2_blocks = 0, room = 0, clusters = 0, threads = 0, smem = 0;
+    for (const Spread& w : kSpreads) {
+        for (uint32_t b = 1, log2 = 0; b <= kMaxBlocks; b *= 2, ++log2) {
+            if (b > 1 && groups < b * (uint64_t)w.threads / 2) break;  // too little for so many
+            const uint64_t need = (groups + b - 1) / b + 1, most = w.smem / kGroupBytes, keep = need < most ? need : most;
+            const uint32_t bytes = (uint32_t)smem_of(keep * kGroupBytes);
+            int n = 0;
+            e = resident_clusters(reinterpret_cast<const void*>(kernel), w.threads, b, bytes, &n);
+            if (e != cudaSuccess) return e;
+            if (n < 1) continue;
+            const uint64_t rounds = ((uint64_t)a.T + n - 1) / n, all = ((uint64_t)a.T * b + di.sms - 1) / di.sms;
+            const double per_sm = (double)(all < w.per_sm ? all : w.per_sm);
+            const double ns = (double)rounds * (kJoinNs + per_sm * kMoved * ((double)keep / kBytesNs + (double)(need - keep) / kAgainNs));
+            if (blocks && ns >= best) continue;
+            best = ns;
+            blocks = b;
+            log2_blocks = log2;
+            room = (uint32_t)keep;
+            clusters = (uint32_t)n;
+            threads = w.threads;
+            smem = bytes;
+        }
     }
-    if (blocks == 0) {  // clusters of sixteen do not fit on this device: rows are read again
-        int n = 0;
-        blocks = 8;
-        const cudaError_t e = resident_clusters(reinterpret_cast<const void*>(kernel), kRowThreads, blocks, 0, &n);
-        if (e != cudaSuccess) return e;
-        clusters = n > 0 ? n : 1;
-    }
-    while ((1u << log2_blocks) < blocks) ++log2_blocks;
+    if (blocks == 0) return cudaErrorInvalidConfiguration;
     const float c = a.use_soft ? a.ct : kLog2e;
     const float limit = 1e30f / (c > kLog2e ? c : kLog2e);
     const uint32_t grid = (a.T < clusters ? a.T : clusters) * blocks;
-    return launch_early(kernel, grid, kRowThreads, smem_of(room * kGroupBytes), blocks, s, a, room, log2_blocks, limit);
+    return launch_early(kernel, grid, threads, smem, blocks, s, a, room, log2_blocks, limit, faults);
 }
 
 template <typename TI, typename TO>
-cudaError_t launch_two(const DistillArgs& a, cudaStream_t s) {
-    return a.use_soft && a.use_hard && a.ct != kLog2e ? launch<TI, TO, true>(a, s) : launch<TI, TO, false>(a, s);
+cudaError_t launch_two(const DistillArgs& a, uint32_t* faults, cudaStream_t s) {
+    if (!a.use_soft || !a.use_hard || a.ct == kLog2e) return launch<TI, TO, kOne>(a, faults, s);
+    return 2.0f * a.ct == kLog2e ? launch<TI, TO, kSquare>(a, faults, s) : launch<TI, TO, kBoth>(a, faults, s);
 }
 template <typename TI>
-cudaError_t launch_type(const DistillArgs& a, int ddtype, cudaStream_t s) {
-    if (!a.dz) return launch_two<TI, void>(a, s);
-    return ddtype == 0 ? launch_two<TI, float>(a, s) : launch_two<TI, uint16_t>(a, s);
+cudaError_t launch_type(const DistillArgs& a, int ddtype, uint32_t* faults, cudaStream_t s) {
+    if (!a.dz) return launch_two<TI, void>(a, faults, s);
+    return ddtype == 0 ? launch_two<TI, float>(a, faults, s) : launch_two<TI, uint16_t>(a, faults, s);
 }
 
 }  // namespace
 
 cudaError_t launch_distill(const DistillArgs& a, int dtype, int ddtype, cudaStream_t s) {
-    return dtype == 0 ? launch_type<float>(a, ddtype, s) : launch_type<uint16_t>(a, ddtype, s);
+    uint32_t* faults = nullptr;
+    const cudaError_t e = tc::wait_fault_word(&faults);
+    if (e != cudaSuccess) return e;
+    return dtype == 0 ? launch_type<float>(a, ddtype, faults, s) : launch_type<uint16_t>(a, ddtype, faults, s);
 }
 
 }  // namespace s2

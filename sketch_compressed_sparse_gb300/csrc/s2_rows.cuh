@@ -17,7 +17,7 @@ namespace s2 {
 namespace rows {
 
 constexpr uint32_t kAll = 0xffffffffu;
-constexpr int kRowSmem = 204 * 1024;  // beside up to 22 KB of a kernel's own
+constexpr int kRowSmem = 208 * 1024;  // beside up to 18 KB of a kernel's own
 
 __device__ __forceinline__ float minus_inf() { return __uint_as_float(0xff800000u); }
 
@@ -90,13 +90,16 @@ __device__ __noinline__ Raw<T> edge_group(const Part<T> p, uint32_t l, uint32_t 
     return r;
 }
 template <typename T>
-__device__ __forceinline__ Raw<T> load_group(const Part<T>& p, uint32_t l, uint32_t V) {
-    if (!p.inner(l)) return edge_group(p, l, V);
+__device__ __forceinline__ Raw<T> load_inner(const Part<T>& p, uint32_t l) {
     Raw<T> r;
     const uint4* q = reinterpret_cast<const uint4*>(p.base + (uint64_t)l * 8);
 #pragma unroll
     for (int h = 0; h < (int)sizeof(T) / 2; ++h) r.w[h] = q[h];
     return r;
+}
+template <typename T>
+__device__ __forceinline__ Raw<T> load_group(const Part<T>& p, uint32_t l, uint32_t V) {
+    return p.inner(l) ? load_inner(p, l) : edge_group(p, l, V);
 }
 
 // ---- a block's groups in shared memory -------------------------------------------
@@ -256,6 +259,7 @@ inline cudaError_t resident_clusters(const void* fn, int threads, uint32_t block
     struct Entry {
         int dev;
         const void* fn;
+        int threads;
         uint32_t blocks;
         size_t smem;
         int clusters;
@@ -268,7 +272,7 @@ inline cudaError_t resident_clusters(const void* fn, int threads, uint32_t block
     if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lock(mu);
     for (int i = 0; i < used; ++i)
-        if (table[i].dev == dev && table[i].fn == fn && table[i].blocks == blocks && table[i].smem == smem) {
+        if (table[i].dev == dev && table[i].fn == fn && table[i].threads == threads && table[i].blocks == blocks && table[i].smem == smem) {
             *clusters = table[i].clusters;
             return cudaSuccess;
         }
@@ -290,7 +294,7 @@ inline cudaError_t resident_clusters(const void* fn, int threads, uint32_t block
         cudaGetLastError();  // a failed query is not a launch error
         n = 0;
     }
-    if (used < 256) table[used++] = {dev, fn, blocks, smem, n};
+    if (used < 256) table[used++] = {dev, fn, threads, blocks, smem, n};
     *clusters = n;
     return cudaSuccess;
 }

@@ -107,7 +107,7 @@ def test_alignments(ld, off, ldd, offd, dtype, ddtype):
     check(z, idx, t, y, w, dtype, ddtype, temperature=2.0, hard=0.3, ld=ld, off=off, ldd=ldd, offd=offd)
 
 
-@pytest.mark.parametrize("V,K", [(50, 40), (5000, 300), (70000, 1000)])
+@pytest.mark.parametrize("V,K", [(50, 40), (700, 128), (900, 256), (5000, 257), (5000, 300), (70000, 1000)])
 def test_repeated_and_missing_entries(V, K):
     """An index twice counts twice; one outside the row not at all; targets among the entries and not."""
     for kw in (dict(repeat=True), dict(missing=True), dict(repeat=True, missing=True)):
