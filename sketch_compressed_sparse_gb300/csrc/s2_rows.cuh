@@ -232,6 +232,21 @@ __device__ __forceinline__ uint64_t peer_u64(uint32_t a) {
     asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
     return v;
 }
+// Sum of the words at `p` in the blocks of the cluster (sixteen at most): the
+// loads do not wait for one another.
+__device__ __forceinline__ uint64_t sum_of_blocks(const void* p, uint32_t blocks) {
+    uint64_t sum = 0;
+#pragma unroll
+    for (uint32_t half = 0; half < 16; half += 8) {
+        if (half && blocks <= 8) break;
+        uint64_t v[8];
+#pragma unroll
+        for (uint32_t r = 0; r < 8; ++r) v[r] = half + r < blocks ? peer_u64(peer(p, half + r)) : 0;
+#pragma unroll
+        for (uint32_t r = 0; r < 8; ++r) sum += v[r];
+    }
+    return sum;
+}
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }

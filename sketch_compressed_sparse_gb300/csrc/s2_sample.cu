@@ -15,13 +15,15 @@
 // largest (fewer bits where V is above 2^19), and weights are added as 64-bit
 // integers: sums are exact and do not depend on their order.
 //
-// A cluster of blocks keeps the row in shared memory (or reads it again where it
-// does not fit) and goes over it a few times: for the maximum; for each of top-k
-// and top-p a histogram of counts or weights over 512 ranges of logits, one of 512
+// A cluster of blocks keeps the row in shared memory (what does not fit is read
+// again) and goes over it a few times: for the maximum; for each of top-k and
+// top-p a histogram of counts or weights over 256 ranges of logits, one of 256
 // parts of the range that holds the border, and a list of the few tokens in that
 // part, which are ranked against one another; and for the token the sums of its
-// runs of 256 tokens. Where many tokens fall into one part (equal logits, a range
-// without end) the border's bits are found nine at a time.
+// runs of tokens. Where many tokens fall into one part (equal logits, a range
+// without end) the border's bits are found eight at a time. The passes behind the
+// first ones look at the largest of eight neighbours and leave most of them alone.
+// Bound by instructions: a weight takes about 35.
 #include <cfloat>
 
 #include "s2_internal.h"
@@ -33,24 +35,27 @@ namespace {
 
 using namespace rows;
 
-constexpr int kRowThreads = 512;
-constexpr int kRowWarps = kRowThreads / 32;
-constexpr int kBins = kRowThreads;   // one per thread
-constexpr int kChunks = kRowThreads; // runs of tokens, one per thread
-constexpr uint32_t kList = 256;      // tokens that are ranked against one another
-constexpr float kPerOctave = 16.0f;  // ranges of logits per factor of two of weight
-constexpr int kBits = 43;            // of a weight of 1
+constexpr int kMaxThreads = 1024;
+constexpr uint32_t kMinThreads = 320;
+constexpr uint32_t kBins = 256;     // a thread each
+constexpr uint32_t kList = 128;     // tokens that are ranked against one another
+constexpr float kPerOctave = 8.0f;  // ranges of logits per factor of two of weight
+constexpr int kBits = 43;           // of a weight of 1
+static_assert(kBins <= kMinThreads && kList <= kMinThreads, "a thread for each");
 
-// 2^(j/32) * 2^43, rounded
-__device__ const uint64_t kRoots[32] = {
-    0x80000000000ull, 0x82cd8698ac3ull, 0x85aac367cc5ull, 0x88980e8092eull,
-    0x8b95c1e3ea9ull, 0x8ea4398b45dull, 0x91c3d373ab1ull, 0x94f4efa8fefull,
-    0x9837f0518dcull, 0x9b8d39b9d55ull, 0x9ef5326091aull, 0xa27043030c5ull,
-    0xa5fed6a9b15ull, 0xa9a15ab4ea8ull, 0xad583eea42aull, 0xb123f581d2bull,
-    0xb504f333f9eull, 0xb8fbaf47630ull, 0xbd08a39f581ull, 0xc12c4cca667ull,
-    0xc5672a11550ull, 0xc9b9bd866e3ull, 0xce248c151f8ull, 0xd2a81d91f13ull,
-    0xd744fccad6aull, 0xdbfbb797dafull, 0xe0ccdeec2a9ull, 0xe5b906e77c8ull,
-    0xeac0c6e7dd2ull, 0xefe4b99bdceull, 0xf5257d15248ull, 0xfa83b2db723ull,
+// 2^(j/32) in two floats
+__device__ const float2 kRoots[32] = {
+    {0x1.0000000000000p+0f, 0x0.0p+0f}, {0x1.059b0e0000000p+0f, -0x1.9d4f520000000p-25f}, {0x1.0b55860000000p+0f, 0x1.9f31220000000p-25f},
+    {0x1.11301e0000000p+0f, -0x1.fdb4960000000p-25f}, {0x1.172b840000000p+0f, -0x1.c157420000000p-27f}, {0x1.1d48740000000p+0f, -0x1.d2e8ca0000000p-25f},
+    {0x1.2387a60000000p+0f, 0x1.ceac480000000p-25f}, {0x1.29e9e00000000p+0f, -0x1.5c04240000000p-25f}, {0x1.306fe00000000p+0f, 0x1.4636e20000000p-25f},
+    {0x1.371a740000000p+0f, -0x1.18aac60000000p-25f}, {0x1.3dea640000000p+0f, 0x1.8246840000000p-25f}, {0x1.44e0860000000p+0f, 0x1.8624b40000000p-30f},
+    {0x1.4bfdae0000000p+0f, -0x1.593abc0000000p-25f}, {0x1.5342b60000000p+0f, -0x1.2c56100000000p-25f}, {0x1.5ab07e0000000p+0f, -0x1.5bd5ec0000000p-27f},
+    {0x1.6247ec0000000p+0f, -0x1.f8b5500000000p-25f}, {0x1.6a09e60000000p+0f, 0x1.9fcef40000000p-26f}, {0x1.71f75e0000000p+0f, 0x1.1d8bee0000000p-25f},
+    {0x1.7a11480000000p+0f, -0x1.829fd00000000p-25f}, {0x1.82589a0000000p+0f, -0x1.accc7c0000000p-26f}, {0x1.8ace540000000p+0f, 0x1.15506e0000000p-27f},
+    {0x1.93737c0000000p+0f, -0x1.e647440000000p-25f}, {0x1.9c49180000000p+0f, 0x1.51f8480000000p-27f}, {0x1.a5503c0000000p+0f, -0x1.b83b540000000p-25f},
+    {0x1.ae89fa0000000p+0f, -0x1.a94b140000000p-26f}, {0x1.b7f7700000000p+0f, -0x1.a094380000000p-25f}, {0x1.c199be0000000p+0f, -0x1.3d56b20000000p-27f},
+    {0x1.cb720e0000000p+0f, -0x1.8837cc0000000p-27f}, {0x1.d5818e0000000p+0f, -0x1.822dbc0000000p-27f}, {0x1.dfc9740000000p+0f, -0x1.908c940000000p-25f},
+    {0x1.ea4afa0000000p+0f, 0x1.52486c0000000p-27f}, {0x1.f507660000000p+0f, -0x1.246eb00000000p-26f},
 };
 
 // A row's settings, and what follows from them.
@@ -67,25 +72,23 @@ struct Settings {
 struct Listed {
     float v;
     uint32_t i;
-    uint64_t w;
 };
 
 struct Shared {
-    uint64_t roots[32];
+    float2 roots[32];
     uint64_t hist[2][kBins];
     Listed list[kList], all[kList];
-    uint64_t scan[kRowWarps];
-    uint64_t best[2];    // largest logit's key and the complement of its index
-    uint32_t finite[2];  // tokens above -infinity
+    uint64_t weight[kList];
+    uint64_t scan[kMaxThreads / 32];
+    float warp_max[kMaxThreads / 32];
+    float top[2];        // this block's largest logit
+    uint32_t lowest[2];  // the lowest index of the row's largest
     uint32_t listed;
     uint64_t total;      // weight kept in this block
-    uint64_t warp_best[kRowWarps];
-    uint32_t warp_finite[kRowWarps];
     Settings set;
     uint64_t before;     // of the bin that was found
     uint32_t bin;
-    float border_v;
-    uint32_t border_i;
+    Listed border;
 };
 
 // Bits in the order of the numbers; both zeros are one.
@@ -101,7 +104,7 @@ __device__ __forceinline__ float of_key(uint32_t k) {
 __device__ uint64_t times(float f, uint64_t z, bool up) {
     const uint32_t b = __float_as_uint(f), e = b >> 23;
     const uint64_t m = e ? (b & 0x7fffffu) | 0x800000u : b & 0x7fffffu;
-    const uint32_t s = 150 - (e ? e : 1);  // f = m * 2^-s, 24 < s
+    const uint32_t s = 150 - (e ? e : 1);  // f = m * 2^-s, 24 <= s
     const uint64_t lo = z * m, hi = __umul64hi(z, m);
     uint64_t q = 0;
     bool rest = (lo | hi) != 0;
@@ -115,41 +118,6 @@ __device__ uint64_t times(float f, uint64_t z, bool up) {
     return q + (up && rest);
 }
 
-// A row as the blocks of a cluster share it.
-template <typename TI, bool STAGED>
-struct Row {
-    const uint4* slice;
-    uint32_t room;
-    Part<TI> p;
-    uint32_t V;
-    uint32_t span;    // 256-token steps per run
-    uint32_t chunks;  // runs of this block
-
-    // f(values of eight neighbours) of local group l
-    template <typename F>
-    __device__ __forceinline__ void one(uint32_t l, F f) const {
-        const Raw<TI> r = STAGED ? staged<TI>(slice, room, l) : load_group(p, l, V);
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = element(r, j);
-        f(v);
-    }
-    // f(values, local group) for every group of run `chunk` that this lane holds
-    template <typename F>
-    __device__ __forceinline__ void run(uint32_t chunk, F f) const {
-        for (uint32_t s = 0; s < span; ++s) {
-            const uint32_t l = (chunk * span + s) * 32 + threadIdx.x % 32;
-            if (l < p.count) one(l, [&](const float* v) { f(v, l); });
-        }
-    }
-    // for every group of the block, each once
-    template <typename F>
-    __device__ __forceinline__ void each(F f) const {
-        for (uint32_t c = threadIdx.x / 32; c < chunks; c += kRowWarps) run(c, f);
-    }
-    __device__ __forceinline__ uint32_t index(uint32_t l, int j) const { return (uint32_t)p.index(l, j); }
-};
-
 // What is kept: logits above v, and those equal to it with an index below i.
 struct Border {
     float v;
@@ -157,44 +125,118 @@ struct Border {
     __device__ __forceinline__ bool keeps(float x, uint32_t at) const { return x > v || (x == v && at < i); }
 };
 
-// A token's weight, to about 2^-35 of itself. (d, dl) is l - l_max exactly, (y, e)
-// that times log2(e) / T, and y = (32 n + j) / 32 + r with |r| <= 1/64, so that
-//   2^(y + e) = 2^n * 2^(j/32) * exp(ln 2 * (r + e)).
+// A row as the blocks of a cluster share it.
+template <typename TI>
+struct Row {
+    const uint4* slice;
+    uint32_t room, kept;  // groups of the block's part in shared memory
+    Part<TI> p;
+    uint32_t V;
+    uint32_t span;    // 256-token steps per run
+    uint32_t chunks;  // runs of this block, at most kBins
+
+    __device__ __forceinline__ Raw<TI> group(uint32_t l) const { return l < kept ? staged<TI>(slice, room, l) : load_group(p, l, V); }
+    // f(group, local index) for every group of the block, each once
+    template <typename F>
+    __device__ __forceinline__ void each(F f) const {
+#pragma unroll 2
+        for (uint32_t l = threadIdx.x; l < kept; l += blockDim.x) f(staged<TI>(slice, room, l), l);
+        uint32_t l = threadIdx.x;
+        if (l < kept) l += (kept - l + blockDim.x - 1) / blockDim.x * blockDim.x;
+        for (; l < p.count; l += blockDim.x) f(load_group(p, l, V), l);
+    }
+    // for every group that may hold a logit above `least` or equal to it
+    template <typename F>
+    __device__ __forceinline__ void above(float least, F f) const {
+        each([&](const Raw<TI>& r, uint32_t l) {
+            if (group_max(r) >= least) f(r, l);
+        });
+    }
+    // f(group, local index) for the groups of run `chunk`: each lane holds one of `span` steps
+    template <typename F>
+    __device__ __forceinline__ void run(uint32_t chunk, F f) const {
+        for (uint32_t s = 0; s < span; ++s) {
+            const uint32_t l = (chunk * span + s) * 32 + threadIdx.x % 32;
+            if (l < p.count) f(group(l), l);
+        }
+    }
+    __device__ __forceinline__ uint32_t index(uint32_t l, int j) const { return (uint32_t)p.index(l, j); }
+};
+
+// Weights, to about 2^-35 of themselves. (D, Dl) is l_max - l exactly, (PY, -e)
+// that times log2(e) / T, and -PY = (32 n + j) / 32 - R with |R| <= 1/64, so that
+//   2^(-PY + e) = 2^n * 2^(j/32) * exp(ln 2 * (e - R)).
 // Adding a float whose last place is the wanted unit turns a float into a whole
-// number of those units. (The products and sums are spelt out so that none is fused.)
+// number of those units: a weight is hi * 2^-22 + lo * 2^-43. Two tokens at a time.
+// (Products and sums are single instructions: none is fused into another.)
 struct Weigher {
-    const uint64_t* roots;
+    const float2* roots;
     float max, ch, cl;
     int shift;  // bits fewer than kBits
-    __device__ __forceinline__ uint64_t operator()(float l) const {
-        constexpr float kStep32 = 1.5f * 262144.0f;      // last place 2^-5
-        constexpr float kStep28 = 1.5f / 32.0f;          // last place 2^-28
-        constexpr float kStep35 = 1.5f / 4096.0f;        // last place 2^-35
+    float none;  // down to it weights are below 2^-40
+
+    __device__ __forceinline__ void pair(float l0, float l1, int* hi, int* lo) const {
+        constexpr float kStep32 = 1.5f * 262144.0f;   // last place 2^-5
+        constexpr float kStep22 = 3.0f;               // last place 2^-22
+        constexpr float kStep43 = 1.5f / 1048576.0f;  // last place 2^-43
         constexpr double kLn2 = 0.69314718055994530942;
         constexpr float kLnHi = (float)kLn2, kLnLo = (float)(kLn2 - (double)kLnHi);
         constexpr float c2 = (float)(kLn2 * kLn2 / 2), c3 = (float)(kLn2 * kLn2 * kLn2 / 6),
                         c4 = (float)(kLn2 * kLn2 * kLn2 * kLn2 / 24), c5 = (float)(kLn2 * kLn2 * kLn2 * kLn2 * kLn2 / 120);
+        auto both = [](float v) { return two(v, v); };
+        const Two minus = both(-1.0f), M = both(max);
+        // (what is not kept, NaN and -infinity among it, is moved to where it does no harm)
+        const Two l = two(fmaxf(l0, none), fmaxf(l1, none));
+        const Two D = fma2(l, minus, M), back = add2(D, both(-max));
+        const Two Dl = fma2(add2(l, back), minus, fma2(fma2(back, minus, D), minus, M));
+        const Two PY = mul2(D, both(ch));
+        const Two e = fma2(Dl, both(-ch), fma2(D, both(-cl), fma2(D, both(-ch), PY)));
+        const Two t = fma2(PY, minus, both(kStep32));
+        const Two R = add2(PY, add2(t, both(-kStep32)));
+        const Two na = mul2(R, both(kLnHi)), a = mul2(R, both(-kLnHi)), x = fma2(R, minus, e);
+        Two small = fma2(e, both(kLnHi), fma2(R, both(-kLnLo), fma2(R, both(-kLnHi), na)));
+        small = fma2(mul2(x, x), fma2(x, fma2(x, fma2(x, both(c5), both(c4)), both(c3)), both(c2)), small);
+        const float2 ft = apart(t);
+        const int n0 = __float_as_int(ft.x) - __float_as_int(kStep32), n1 = __float_as_int(ft.y) - __float_as_int(kStep32);
+        const float2 r0 = roots[n0 & 31], r1 = roots[n1 & 31];
+        const Two by = two(__int_as_float(((n0 >> 5) + 127 - shift) << 23), __int_as_float(((n1 >> 5) + 127 - shift) << 23));
+        const Two root = mul2(two(r0.x, r1.x), by), rest = mul2(two(r0.y, r1.y), by);
+        const Two p = mul2(root, a), pe = fma2(root, a, mul2(root, na)), s = add2(root, p);
+        const Two wl = add2(add2(fma2(rest, a, fma2(root, small, pe)), rest), fma2(fma2(root, minus, s), minus, p));
+        const Two v = add2(s, wl), under = fma2(fma2(s, minus, v), minus, wl);
+        const Two th = add2(v, both(kStep22));
+        const Two tl = add2(add2(fma2(add2(th, both(-kStep22)), minus, v), under), both(kStep43));
+        const float2 h = apart(th), w = apart(tl);
+        hi[0] = __float_as_int(h.x) - __float_as_int(kStep22);
+        hi[1] = __float_as_int(h.y) - __float_as_int(kStep22);
+        lo[0] = __float_as_int(w.x) - __float_as_int(kStep43);
+        lo[1] = __float_as_int(w.y) - __float_as_int(kStep43);
+    }
+    __device__ __forceinline__ static uint64_t whole(int hi, int lo) { return (uint64_t)(((int64_t)hi << 21) + lo); }
+    // A weight by itself, of a logit that is not below `none`.
+    __device__ __forceinline__ uint64_t operator()(float l) const {
         if (max == __uint_as_float(0x7f800000u)) return l == max ? 1ull << (kBits - shift) : 0;
-        const float d = __fadd_rn(l, -max);
-        const float y = __fmul_rn(d, ch);
-        if (!(y > -(float)(kBits + 2))) return 0;  // (-infinity and NaN too)
-        const float back = __fadd_rn(d, -l);  // what d took for -max
-        const float dl = __fadd_rn(__fadd_rn(l, -__fadd_rn(d, -back)), __fadd_rn(-max, -back));
-        const float e = __fmaf_rn(dl, ch, __fmaf_rn(d, cl, __fmaf_rn(d, ch, -y)));
-        const float t = __fadd_rn(y, kStep32);
-        const int n = __float_as_int(t) - __float_as_int(kStep32);
-        const float r = __fadd_rn(y, -__fadd_rn(t, -kStep32));
-        const float x = __fadd_rn(r, e);
-        const float a = __fmul_rn(r, kLnHi);
-        float small = __fmaf_rn(e, kLnHi, __fmaf_rn(r, kLnLo, __fmaf_rn(r, kLnHi, -a)));
-        small = __fmaf_rn(__fmul_rn(x, x), __fmaf_rn(x, __fmaf_rn(x, __fmaf_rn(x, c5, c4), c3), c2), small);
-        const float ta = __fadd_rn(a, kStep28);
-        const float tb = __fadd_rn(__fadd_rn(small, __fadd_rn(a, -__fadd_rn(ta, -kStep28))), kStep35);
-        const int q = (__float_as_int(ta) - __float_as_int(kStep28)) * 128 + (__float_as_int(tb) - __float_as_int(kStep35));
-        const uint64_t root = roots[n & 31];
-        const uint64_t w = root + (uint64_t)(((int64_t)(uint32_t)(root >> 12) * q) >> 23);  // q is in units of 2^-35
-        const int s = shift - (n >> 5);
-        return s ? (w + (1ull << (s - 1))) >> s : w;
+        int hi[2], lo[2];
+        pair(l, l, hi, lo);
+        return whole(hi[0], lo[0]);
+    }
+    // Of a group: f(element, weight) where use(element) holds.
+    template <typename TI, typename Use, typename F>
+    __device__ __forceinline__ void group(const Raw<TI>& r, Use use, F f) const {
+        if (max == __uint_as_float(0x7f800000u)) {
+#pragma unroll 1
+            for (int j = 0; j < 8; ++j)
+                if (use(element(r, j), j)) f(element(r, j), j, (*this)(element(r, j)));
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            int hi[2], lo[2];
+            const float v0 = element(r, j), v1 = element(r, j + 1);
+            pair(v0, v1, hi, lo);
+            if (use(v0, j)) f(v0, j, whole(hi[0], lo[0]));
+            if (use(v1, j + 1)) f(v1, j + 1, whole(hi[1], lo[1]));
+        }
     }
 };
 
@@ -212,14 +254,9 @@ __device__ __forceinline__ uint64_t block_scan(Shared& sh, uint64_t v, uint64_t*
     __syncthreads();  // the last scan's sums have been read
     if (threadIdx.x % 32 == 31) sh.scan[threadIdx.x / 32] = v;
     __syncthreads();
-    uint64_t before = 0, all = 0;
-#pragma unroll
-    for (uint32_t i = 0; i < kRowWarps; ++i) {
-        const uint64_t s = sh.scan[i];
-        if (i < threadIdx.x / 32) before += s;
-        all += s;
-    }
-    *total = all;
+    const uint64_t mine = threadIdx.x % 32 < blockDim.x / 32 ? sh.scan[threadIdx.x % 32] : 0, upto = warp_scan(mine);
+    *total = __shfl_sync(kAll, upto, 31);
+    const uint64_t before = __shfl_sync(kAll, upto - mine, threadIdx.x / 32);
     return before + v;
 }
 
@@ -230,146 +267,211 @@ __device__ __forceinline__ void add64(uint64_t* at, uint64_t v) {
     if (hi) atomicAdd(w + 1, hi);
 }
 
-// Finds the bin in which the sum over the bins of all blocks reaches `target`
-// (from 1 to that sum), and takes off what lies before it. bin_of(v) is a
-// group's element's bin, or kBins; measure(v) what it counts. `target_of(total)`
-// gives the target. The same answer in every block.
-template <typename R, typename BinOf, typename Measure, typename TargetOf>
-__device__ __forceinline__ uint32_t find_bin(Shared& sh, const R& row, const Border& from, uint32_t& turn, uint32_t blocks, BinOf bin_of,
-                                             Measure measure, TargetOf target_of, uint64_t* target) {
-    uint64_t* hist = sh.hist[turn++ & 1];
-    hist[threadIdx.x] = 0;
-    __syncthreads();
-    row.each([&](const float* v, uint32_t l) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (!from.keeps(v[j], row.index(l, j))) continue;
-            const uint32_t b = bin_of(v[j]);
-            if (b < kBins) {
-                const uint64_t m = measure(v[j]);
-                if (m) add64(hist + b, m);
-            }
+// What a row's threads share and agree on.
+template <typename TI>
+struct Team {
+    Shared& sh;
+    const Row<TI>& row;
+    uint32_t blocks, rank;
+    float top;  // the row's largest logit
+    uint32_t& turn;
+
+    // Finds the bin in which the sum over the bins of all blocks reaches the goal
+    // goal_of(total), from 1 to that sum; *goal: what is left of it in that bin.
+    // fill(hist) adds this block's part. The same answer in every block.
+    template <typename Fill, typename GoalOf>
+    __device__ __forceinline__ uint32_t find_bin(Fill fill, GoalOf goal_of, uint64_t* goal) const {
+        uint64_t* hist = sh.hist[turn++ & 1];
+        if (threadIdx.x < kBins) hist[threadIdx.x] = 0;
+        __syncthreads();
+        fill(hist);
+        cluster_barrier();
+        const uint64_t sum = threadIdx.x < kBins ? sum_of_blocks(hist + threadIdx.x, blocks) : 0;
+        uint64_t total;
+        const uint64_t upto = block_scan(sh, sum, &total);
+        const uint64_t want = goal_of(total);
+        if (upto >= want && upto - sum < want) {
+            sh.bin = threadIdx.x;
+            sh.before = upto - sum;
         }
-    });
-    cluster_barrier();
-    uint64_t sum = 0;
-    for (uint32_t r = 0; r < blocks; ++r) sum += peer_u64(peer(hist + threadIdx.x, r));
-    uint64_t total;
-    const uint64_t upto = block_scan(sh, sum, &total);
-    const uint64_t goal = target_of(total);
-    if (upto >= goal && upto - sum < goal) {
-        sh.bin = threadIdx.x;
-        sh.before = upto - sum;
+        __syncthreads();
+        *goal = want - sh.before;
+        return sh.bin;
     }
-    __syncthreads();
-    *target = goal - sh.before;
-    return sh.bin;
+    // The sum of the blocks' totals, and of those before this one. (A lane reads a block's.)
+    __device__ __forceinline__ void totals(uint64_t* before, uint64_t* all) const {
+        const uint32_t lane = threadIdx.x % 32;
+        const uint64_t mine = lane < blocks ? peer_u64(peer(&sh.total, lane)) : 0;
+        uint64_t upto = mine;
+#pragma unroll
+        for (int o = 1; o < 16; o *= 2) {
+            const uint64_t u = __shfl_up_sync(kAll, upto, o);
+            if (lane >= o) upto += u;
+        }
+        *all = __shfl_sync(kAll, upto, 15);
+        *before = __shfl_sync(kAll, upto - mine, rank);
+    }
+};
+
+// How tokens are measured: counted, or weighed.
+struct Count {
+    static constexpr bool kWeighed = false;
+    __device__ __forceinline__ uint64_t operator()(float) const { return 1; }
+    template <typename TI, typename Use, typename F>
+    __device__ __forceinline__ void group(const Raw<TI>& r, Use use, F f) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (use(element(r, j), j)) f(element(r, j), j, (uint64_t)1);
+    }
+};
+struct Weigh : Weigher {
+    static constexpr bool kWeighed = true;
+};
+template <typename Measure>
+__device__ __forceinline__ void count_in(uint64_t* at, uint64_t m) {
+    if (Measure::kWeighed) {
+        if (m) add64(at, m);
+    } else {
+        atomicAdd(reinterpret_cast<uint32_t*>(at), 1u);  // (a block has fewer than 2^32)
+    }
 }
 
 // The border of the shortest beginning of what `from` keeps that measures
-// target_of(what all of it measures) or more. `scale`: ranges per unit of logit.
-template <typename R, typename Measure, typename TargetOf>
-__device__ Border narrow(Shared& sh, const R& row, Border from, uint32_t& turn, uint32_t blocks, float top, float scale, Measure measure,
-                         TargetOf target_of) {
-    uint64_t target;
+// goal_of(what all of it measures) or more. `scale`: ranges per unit of logit.
+// `least`: no token below it belongs to that beginning.
+template <typename TI, typename Measure, typename GoalOf>
+__device__ Border narrow(const Team<TI>& team, Border from, float scale, float least, const Measure& measure, GoalOf goal_of) {
+    Shared& sh = team.sh;
+    const Row<TI>& row = team.row;
+    const float top = team.top;
+    uint64_t goal;
     auto range = [&](float v) { return fminf((top - v) * scale, (float)(kBins - 1)); };  // larger logits first
-    const uint32_t bin = find_bin(sh, row, from, turn, blocks,
-                                  [&](float v) { return (uint32_t)__float2int_rn(range(v)); }, measure, target_of, &target);
-    auto left = [&](uint64_t) { return target; };
+    auto range_of = [&](float v) { return (uint32_t)__float2int_rn(range(v)); };
+    auto kept = [&](uint32_t l) { return [&row, &from, l](float v, int j) { return from.keeps(v, row.index(l, j)); }; };
+    const uint32_t bin = team.find_bin(
+        [&](uint64_t* hist) {
+            row.above(fmaxf(least, from.v), [&](const Raw<TI>& r, uint32_t l) {
+                measure.group(r, kept(l), [&](float v, int, uint64_t m) { count_in<Measure>(hist + range_of(v), m); });
+            });
+        },
+        goal_of, &goal);
+    auto left = [&](uint64_t) { return goal; };
     // a part of the range; the last range has no end
     uint32_t part = kBins;
     auto part_of_range = [&](float v) { return (uint32_t)__float2int_rn(fminf(fmaxf((range(v) - (float)bin + 0.5f) * (kBins - 1), 0.0f), kBins - 1)); };
-    auto in_range = [&](float v) { return (uint32_t)__float2int_rn(range(v)) == bin; };
+    // (a little below the range's end, whatever the rounding)
+    const float low = bin < kBins - 1 ? fmaxf(from.v, top - ((float)bin + 0.75f) / scale) : from.v;
     if (bin < kBins - 1)
-        part = find_bin(sh, row, from, turn, blocks, [&](float v) { return in_range(v) ? part_of_range(v) : kBins; }, measure, left, &target);
-    auto member = [&](float v) { return in_range(v) && (part == kBins || part_of_range(v) == part); };
+        part = team.find_bin(
+            [&](uint64_t* hist) {
+                row.above(low, [&](const Raw<TI>& r, uint32_t l) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float v = element(r, j);
+                        if (from.keeps(v, row.index(l, j)) && range_of(v) == bin) count_in<Measure>(hist + part_of_range(v), measure(v));
+                    }
+                });
+            },
+            left, &goal);
+    auto member = [&](float v) { return range_of(v) == bin && (part == kBins || part_of_range(v) == part); };
 
     // few: rank them against one another
     if (part < kBins) {
         if (threadIdx.x == 0) sh.listed = 0;
         __syncthreads();
-        row.each([&](const float* v, uint32_t l) {
+        row.above(low, [&](const Raw<TI>& r, uint32_t l) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
+                const float v = element(r, j);
                 const uint32_t i = row.index(l, j);
-                if (!from.keeps(v[j], i) || !member(v[j])) continue;
+                if (!from.keeps(v, i) || !member(v)) continue;
                 const uint32_t at = atomicAdd(&sh.listed, 1u);
-                if (at < kList) sh.list[at] = {v[j], i, measure(v[j])};
+                if (at < kList) sh.list[at] = {v, i};
             }
         });
         cluster_barrier();
-        uint32_t n = 0, most = 0;
-        for (uint32_t r = 0; r < blocks; ++r) {
-            const uint32_t c = peer_u32(peer(&sh.listed, r));
-            if (c <= kList && n + c <= kList)
-                for (uint32_t k = threadIdx.x; k < c; k += kRowThreads) {
-                    const uint32_t at = peer(sh.list + k, r);
-                    sh.all[n + k] = {peer_float(at), peer_u32(at + 4), peer_u64(at + 8)};
-                }
-            n = c > kList || n > kList ? kList + 1 : n + c;
-            most = n;
+        // each warp takes some blocks' lists to their places behind one another
+        const uint32_t lane = threadIdx.x % 32, c = min(lane < team.blocks ? peer_u32(peer(&sh.listed, lane)) : 0, kList + 1);
+        uint32_t upto = c;
+#pragma unroll
+        for (int o = 1; o < 16; o *= 2) {
+            const uint32_t u = __shfl_up_sync(kAll, upto, o);
+            if (lane >= o) upto += u;
         }
+        const uint32_t n = __shfl_sync(kAll, upto, 15);
+        if (n <= kList)
+            for (uint32_t r = threadIdx.x / 32; r < team.blocks; r += blockDim.x / 32) {
+                const uint32_t many = __shfl_sync(kAll, c, r), first = __shfl_sync(kAll, upto - c, r);
+                for (uint32_t k = lane; k < many; k += 32) {
+                    const uint32_t at = peer(sh.list + k, r);
+                    const Listed e{peer_float(at), peer_u32(at + 4)};
+                    sh.all[first + k] = e;
+                    sh.weight[first + k] = measure(e.v);
+                }
+            }
         __syncthreads();
-        if (most <= kList) {
-            for (uint32_t k = threadIdx.x; k < n; k += kRowThreads) {
-                const Listed me = sh.all[k];
+        if (n <= kList) {
+            if (threadIdx.x < n) {
+                const Listed me = sh.all[threadIdx.x];
                 uint64_t before = 0;
                 for (uint32_t j = 0; j < n; ++j) {
                     const Listed o = sh.all[j];
-                    if (o.v > me.v || (o.v == me.v && o.i < me.i)) before += o.w;
+                    if (o.v > me.v || (o.v == me.v && o.i < me.i)) before += sh.weight[j];
                 }
-                if (before < target && before + me.w >= target) {
-                    sh.border_v = me.v;
-                    sh.border_i = me.i + 1;
-                }
+                if (before < goal && before + sh.weight[threadIdx.x] >= goal) sh.border = {me.v, me.i + 1};
             }
             __syncthreads();
-            const Border b{sh.border_v, sh.border_i};
+            const Border b{sh.border.v, sh.border.i};
             __syncthreads();
             return b;
         }
     }
-    // many: the border's key, nine bits at a time
+    // many: the border's key, eight bits at a time
     uint32_t prefix = 0;
-    constexpr int kShift[4] = {23, 14, 5, 0};
 #pragma unroll 1
-    for (int s = 0; s < 4; ++s) {
-        const int shift = kShift[s], bits = s < 3 ? 9 : 5;
-        const uint32_t found = find_bin(sh, row, from, turn, blocks,
-                                        [&](float v) {
-                                            const uint32_t k = key_of(v);
-                                            // (a shift of 32 bits would be none)
-                                            if (!member(v) || (s > 0 && k >> (shift + bits) != prefix)) return (uint32_t)kBins;
-                                            return ((1u << bits) - 1) - ((k >> shift) & ((1u << bits) - 1));
-                                        },
-                                        measure, left, &target);
-        prefix = prefix << bits | (((1u << bits) - 1) - found);
+    for (int shift = 24; shift >= 0; shift -= 8) {
+        const uint32_t found = team.find_bin(
+            [&](uint64_t* hist) {
+                row.above(low, [&](const Raw<TI>& r, uint32_t l) {
+#pragma unroll 1
+                    for (int j = 0; j < 8; ++j) {
+                        const float v = element(r, j);
+                        const uint32_t k = key_of(v);
+                        if (!from.keeps(v, row.index(l, j)) || !member(v) || (shift < 24 && k >> (shift + 8) != prefix)) continue;
+                        count_in<Measure>(hist + (255u - (k >> shift & 255u)), measure(v));
+                    }
+                });
+            },
+            left, &goal);
+        prefix = prefix << 8 | (255u - found);
     }
     // `need` of the equal logits, by index
     const float v = of_key(prefix);
-    const uint64_t each = measure(v), need = (target + each - 1) / each;
-    uint64_t count = 0;
-    for (uint32_t c = threadIdx.x / 32; c < row.chunks; c += kRowWarps) {
-        uint32_t mine = 0;
-        row.run(c, [&](const float* x, uint32_t l) {
+    const uint64_t each = measure(v), need = (goal + each - 1) / each;
+    uint64_t* counts = sh.hist[team.turn++ & 1];
+    auto hits = [&](const Raw<TI>& r, uint32_t l) {
+        uint32_t hit = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) mine += x[j] == v && from.keeps(x[j], row.index(l, j));
-        });
+        for (int j = 0; j < 8; ++j) hit |= (uint32_t)(element(r, j) == v && from.keeps(v, row.index(l, j))) << j;
+        return hit;
+    };
+    for (uint32_t c = threadIdx.x / 32; c < row.chunks; c += blockDim.x / 32) {
+        uint32_t mine = 0;
+        row.run(c, [&](const Raw<TI>& r, uint32_t l) { mine += __popc(hits(r, l)); });
         mine = __reduce_add_sync(kAll, mine);
-        if (threadIdx.x % 32 == 0) sh.hist[turn & 1][c] = mine;
+        if (threadIdx.x % 32 == 0) counts[c] = mine;
     }
     __syncthreads();
-    uint64_t* counts = sh.hist[turn++ & 1];
-    count = threadIdx.x < row.chunks ? counts[threadIdx.x] : 0;
+    const uint64_t count = threadIdx.x < row.chunks ? counts[threadIdx.x] : 0;
     uint64_t total;
     const uint64_t upto = block_scan(sh, count, &total);
     if (threadIdx.x == 0) {
         sh.total = total;
-        sh.border_i = 0;
+        sh.border.i = 0;
     }
     cluster_barrier();
-    uint64_t before = 0;
-    for (uint32_t r = 0; r < cluster_rank(); ++r) before += peer_u64(peer(&sh.total, r));
+    uint64_t before, all;
+    team.totals(&before, &all);
     const uint64_t want = need > before ? need - before : 0;  // of this block
     if (want > upto - count && want <= upto) {
         sh.bin = threadIdx.x;
@@ -378,55 +480,71 @@ __device__ Border narrow(Shared& sh, const R& row, Border from, uint32_t& turn, 
     __syncthreads();
     if (want > 0 && want <= total && threadIdx.x < 32) {
         uint64_t seen = 0;
-        const uint64_t goal = sh.before;
-        // (every lane of the warp takes every step)
-        for (uint32_t s = 0; s < row.span; ++s) {
+        const uint64_t goal_here = sh.before;
+        for (uint32_t s = 0; s < row.span; ++s) {  // (every lane takes every step)
             const uint32_t l = (sh.bin * row.span + s) * 32 + threadIdx.x;
-            uint32_t hit = 0;
-            if (l < row.p.count) {
-                row.one(l, [&](const float* x) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) hit |= (uint32_t)(x[j] == v && from.keeps(x[j], row.index(l, j))) << j;
-                });
-            }
+            const uint32_t hit = l < row.p.count ? hits(row.group(l), l) : 0;
             const uint64_t mine = warp_scan((uint64_t)__popc(hit));
             const uint64_t first = seen + mine - __popc(hit);
-            if (goal > first && goal <= first + __popc(hit)) {
-                uint32_t k = (uint32_t)(goal - first);
+            if (goal_here > first && goal_here <= first + __popc(hit)) {
+                uint32_t k = (uint32_t)(goal_here - first);
                 for (int j = 0; j < 8; ++j)
-                    if (hit >> j & 1 && --k == 0) sh.border_i = row.index(l, j) + 1;
+                    if (hit >> j & 1 && --k == 0) sh.border.i = row.index(l, j) + 1;
             }
             seen += __shfl_sync(kAll, mine, 31);
         }
     }
     cluster_barrier();
     // one block has found it
-    uint32_t i = 0;
-    for (uint32_t r = 0; r < blocks; ++r) i = max(i, peer_u32(peer(&sh.border_i, r)));
+    const uint32_t lane = threadIdx.x % 32;
+    const uint32_t i = __reduce_max_sync(kAll, lane < team.blocks ? peer_u32(peer(&sh.border.i, lane)) : 0);
     cluster_barrier();  // read by all before it is written again
     return {v, i};
 }
 
-template <typename TI, bool STAGED>
-__global__ void __launch_bounds__(kRowThreads, 2) sample_kernel(const SampleArgs a, uint32_t room, uint32_t log2_blocks, int shift) {
+// A logit that at least `k` of the row's are not below, from the largest of eight
+// neighbours each (one atomic instead of eight); -infinity where that is not known.
+template <typename TI>
+__device__ __forceinline__ float at_least(const Team<TI>& team, uint64_t k, float scale) {
+    const Row<TI>& row = team.row;
+    const float top = team.top;
+    if (k > row.V / 16) return minus_inf();  // too near to all of them
+    uint64_t goal, groups = 0;
+    const uint32_t bin = team.find_bin(
+        [&](uint64_t* hist) {
+            row.each([&](const Raw<TI>& r, uint32_t) {
+                const float m = group_max(r);
+                if (m > minus_inf()) atomicAdd(reinterpret_cast<uint32_t*>(hist + __float2int_rn(fminf((top - m) * scale, (float)(kBins - 1)))), 1u);
+            });
+        },
+        [&](uint64_t total) {
+            groups = total;
+            return total < k ? total : k;
+        },
+        &goal);
+    return bin < kBins - 1 && groups >= k ? top - ((float)bin + 0.75f) / scale : minus_inf();
+}
+
+template <typename TI>
+__global__ void __launch_bounds__(kMaxThreads, 1) sample_kernel(const SampleArgs a, uint32_t room, uint32_t log2_blocks, int shift) {
     extern __shared__ uint4 slice[];
     __shared__ Shared sh;
     stream_order();
-    const uint32_t blocks = 1u << log2_blocks, rank = cluster_rank();
-    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t blocks = 1u << log2_blocks, rank = blocks > 1 ? cluster_rank() : 0;
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
     if (threadIdx.x < 32) sh.roots[threadIdx.x] = kRoots[threadIdx.x];
     uint32_t turn = 0, parity = 0;
-    for (uint64_t at = blockIdx.x / blocks; at < a.T; at += gridDim.x >> log2_blocks, parity ^= 1) {
-        Row<TI, STAGED> row;
+    for (uint64_t at = blockIdx.x >> log2_blocks; at < a.T; at += gridDim.x >> log2_blocks, parity ^= 1) {
+        Row<TI> row;
         row.slice = slice;
         row.room = room;
         row.p = part_of(static_cast<const TI*>(a.z) + at * a.ld, a.V, rank, log2_blocks);
+        row.kept = min(row.p.count, room);
         row.V = a.V;
-        row.span = (row.p.count + 32 * kChunks - 1) / (32 * kChunks);
-        if (row.span == 0) row.span = 1;
+        row.span = max(1u, (row.p.count + 32 * kBins - 1) / (32 * kBins));
         row.chunks = (row.p.count + 32 * row.span - 1) / (32 * row.span);
-        if (STAGED) stage(slice, room, row.p, a.V, threadIdx.x, kRowThreads);
-        if (threadIdx.x == kRowThreads - 1) {
+        for (uint32_t l = threadIdx.x; l < row.kept; l += blockDim.x) stage_group(slice, room, row.p, l, a.V);
+        if (threadIdx.x == blockDim.x - 1) {
             Settings s;
             const float t = a.temperature ? a.temperature[at] : 1.0f;
             s.greedy = !(t >= FLT_MIN);
@@ -444,99 +562,92 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_kernel(const SampleArgs
             s.u = u > 0.0f ? fminf(u, 1.0f - FLT_EPSILON / 2) : 0.0f;
             sh.set = s;
         }
-        if (STAGED) copies_done();
+        copies_done();
 
-        // the largest logit, the first of equals; how many tokens there are
-        uint64_t best = 0;
-        uint32_t finite = 0;
-        row.each([&](const float* v, uint32_t l) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (!(v[j] > minus_inf())) continue;
-                ++finite;
-                const uint64_t k = (uint64_t)key_of(v[j]) << 32 | (uint32_t)~row.index(l, j);
-                best = k > best ? k : best;
-            }
-        });
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            const uint64_t other = __shfl_xor_sync(kAll, best, o);
-            best = other > best ? other : best;
-        }
-        finite = __reduce_add_sync(kAll, finite);
-        if (lane == 0) {
-            sh.warp_best[warp] = best;
-            sh.warp_finite[warp] = finite;
-        }
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            for (uint32_t w = 1; w < kRowWarps; ++w) {
-                best = sh.warp_best[w] > best ? sh.warp_best[w] : best;
-                finite += sh.warp_finite[w];
-            }
-            sh.best[parity] = best;
-            sh.finite[parity] = finite;
+        // the largest logit
+        float top = minus_inf();
+        row.each([&](const Raw<TI>& r, uint32_t) { top = fmaxf(top, group_max(r)); });
+        top = rows::warp_max(top);
+        if (lane == 0) sh.warp_max[warp] = top;
+        __syncthreads();  // (and what every thread copied is there for all)
+        if (warp == 0) {
+            top = rows::warp_max(lane < warps ? sh.warp_max[lane] : minus_inf());
+            if (lane == 0) sh.top[parity] = top;
         }
         cluster_barrier();
-        best = 0;
-        finite = 0;
-        for (uint32_t r = 0; r < blocks; ++r) {
-            const uint64_t b = peer_u64(peer(&sh.best[parity], r));
-            best = b > best ? b : best;
-            finite += peer_u32(peer(&sh.finite[parity], r));
-        }
+        top = rows::warp_max(lane < blocks ? peer_float(peer(&sh.top[parity], lane)) : minus_inf());
         const Settings set = sh.set;
-        const bool first = finite == 0 || set.greedy || set.top_k == 1 || set.top_p == 0.0f;
-        if (first) {  // nothing to draw; the same in every block
-            if (rank == 0 && threadIdx.x == 0) a.tokens[at] = finite ? (int32_t)~(uint32_t)best : -1;
+        if (top == minus_inf() || set.greedy || set.top_k == 1 || set.top_p == 0.0f) {  // nothing to draw; the same in every block
+            if (threadIdx.x == 0) sh.lowest[parity] = 0xffffffffu;
+            __syncthreads();
+            if (top > minus_inf())
+                row.above(top, [&](const Raw<TI>& r, uint32_t l) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (element(r, j) == top) atomicMin(&sh.lowest[parity], row.index(l, j));
+                });
+            cluster_barrier();
+            if (rank == 0 && warp == 0) {
+                const uint32_t i = __reduce_min_sync(kAll, lane < blocks ? peer_u32(peer(&sh.lowest[parity], lane)) : 0xffffffffu);
+                if (lane == 0) a.tokens[at] = (int32_t)i;  // -1 where there is none
+            }
             __syncthreads();
             continue;
         }
-        const float max = of_key((uint32_t)(best >> 32));
-        const Weigher weigh{sh.roots, max, set.ch, set.cl, shift};
-        Border border{minus_inf(), 0};
-        if (set.top_k && set.top_k < finite)
-            border = narrow(sh, row, border, turn, blocks, max, kPerOctave * 1.44269504f, [](float) { return (uint64_t)1; },
-                            [&](uint64_t) { return (uint64_t)set.top_k; });
+        const Team<TI> team{sh, row, blocks, rank, top, turn};
+        Weigh weigh;
+        weigh.roots = sh.roots;
+        weigh.max = top;
+        weigh.ch = set.ch;
+        weigh.cl = set.cl;
+        weigh.shift = shift;
+        weigh.none = fmaxf(top - fminf(60.0f / set.ch, FLT_MAX), -FLT_MAX);
+        // What weighs next to nothing is left out from the start; where the floats
+        // below the largest do (a tiny temperature), so is all but that.
+        Border border = weigh.none < top ? Border{weigh.none, 0} : Border{top, 0xffffffffu};
+        if (set.top_k && set.top_k < a.V) {
+            const float scale = kPerOctave * 1.44269504f;
+            const float least = at_least(team, set.top_k, scale);
+            border = narrow(team, border, scale, least, Count{}, [&](uint64_t total) { return total < set.top_k ? total : (uint64_t)set.top_k; });
+        }
         if (set.top_p < 1.0f)
-            border = narrow(sh, row, border, turn, blocks, max, set.bins, weigh, [&](uint64_t total) {
+            border = narrow(team, border, set.bins, minus_inf(), weigh, [&](uint64_t total) {
                 const uint64_t goal = times(set.top_p, total, true);
                 return goal ? goal : 1;
             });
         if (set.use_min_p) {  // weight >= min_p: l >= l_max + T log(min_p), from the next float on
-            const double least = (double)max + set.min_p;
-            float f = (float)least;
-            if ((double)f < least) f = of_key(key_of(f) + 1);
-            const uint32_t k = key_of(f) - 1;
-            const float below = of_key(k == 0x7fffffffu ? k - 1 : k);  // (that key would be the other zero)
+            if (threadIdx.x == 0) {
+                const double least = (double)top + set.min_p;
+                float f = (float)least;
+                if ((double)f < least) f = of_key(key_of(f) + 1);
+                const uint32_t k = key_of(f) - 1;
+                sh.border.v = of_key(k == 0x7fffffffu ? k - 1 : k);  // (that key would be the other zero)
+            }
+            __syncthreads();
+            const float below = sh.border.v;
             if (below > border.v || (below == border.v && border.i > 0)) border = {below, 0};
         }
 
         // the sums of this block's runs
-        for (uint32_t c = warp; c < row.chunks; c += kRowWarps) {
+        uint64_t* sums = sh.hist[turn++ & 1];
+        for (uint32_t c = warp; c < row.chunks; c += warps) {
             uint64_t w = 0;
-            row.run(c, [&](const float* v, uint32_t l) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (border.keeps(v[j], row.index(l, j))) w += weigh(v[j]);
+            row.run(c, [&](const Raw<TI>& r, uint32_t l) {
+                if (group_max(r) >= border.v)
+                    weigh.group(r, [&](float v, int j) { return border.keeps(v, row.index(l, j)); }, [&](float, int, uint64_t m) { w += m; });
             });
 #pragma unroll
             for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(kAll, w, o);
-            if (lane == 0) sh.hist[turn & 1][c] = w;
+            if (lane == 0) sums[c] = w;
         }
         __syncthreads();
-        const uint64_t mine = threadIdx.x < row.chunks ? sh.hist[turn & 1][threadIdx.x] : 0;
-        ++turn;
+        const uint64_t mine = threadIdx.x < row.chunks ? sums[threadIdx.x] : 0;
         uint64_t total;
         const uint64_t upto = block_scan(sh, mine, &total);
         if (threadIdx.x == 0) sh.total = total;
         cluster_barrier();
-        uint64_t before = 0, all = 0;
-        for (uint32_t r = 0; r < blocks; ++r) {
-            const uint64_t t = peer_u64(peer(&sh.total, r));
-            if (r < rank) before += t;
-            all += t;
-        }
+        uint64_t before, all;
+        team.totals(&before, &all);
         const uint64_t goal = times(set.u, all, false);  // the token: the first whose running sum passes it
         const bool here = goal >= before && goal - before < total;
         if (here && goal - before >= upto - mine && goal - before < upto) {
@@ -553,13 +664,11 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_kernel(const SampleArgs
 #pragma unroll
                 for (int j = 0; j < 8; ++j) w[j] = 0;
                 if (l < row.p.count)
-                    row.one(l, [&](const float* v) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            w[j] = border.keeps(v[j], row.index(l, j)) ? weigh(v[j]) : 0;
-                            sum += w[j];
-                        }
-                    });
+                    weigh.group(row.group(l), [&](float v, int j) { return border.keeps(v, row.index(l, j)); },
+                                [&](float, int j, uint64_t m) {
+                                    w[j] = m;
+                                    sum += m;
+                                });
                 const uint64_t scan = warp_scan(sum);
                 uint64_t run = seen + scan - sum;
                 if (left >= run && left < run + sum) {
@@ -577,6 +686,15 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_kernel(const SampleArgs
     cluster_barrier();  // no block ends while another reads its shared memory
 }
 
+// How a row is spread: threads of a block, blocks on an SM, shared memory of a
+// block's part of a row. A round of rows costs kRoundNs, and a group kGroupNs of
+// its SM, kAgain times as much where it is read again in every pass.
+struct Spread {
+    uint32_t threads, per_sm, smem;
+};
+constexpr Spread kSpreads[3] = {{1024, 1, 200 * 1024}, {512, 2, 100 * 1024}, {320, 3, 66 * 1024}};
+constexpr double kRoundNs = 12000.0, kGroupNs = 2.0, kAgain = 2.0;
+
 template <typename TI>
 cudaError_t launch(const SampleArgs& a, cudaStream_t s) {
     DeviceInfo di{};
@@ -584,31 +702,36 @@ cudaError_t launch(const SampleArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const uint64_t groups = ((uint64_t)a.V + 14) / 8;  // whatever the row's alignment
     constexpr uint64_t kGroupBytes = 8 * sizeof(TI);
-    // as many blocks as let a few of them share an SM, more where the rows do not fill the GPU
-    uint32_t blocks = 1;
-    while (blocks < 16 && groups * kGroupBytes > blocks * 80ull * 1024) blocks *= 2;
-    while (blocks < 16 && (uint64_t)a.T * blocks * 2 <= (uint64_t)di.sms * 2 && groups >= blocks * 2ull * kRowThreads) blocks *= 2;
-    auto kernel = sample_kernel<TI, false>;
-    size_t smem = 0;
-    uint32_t room = 0;
-    int clusters = 0;
-    for (;; blocks /= 2) {
-        const uint64_t need = (groups + blocks - 1) / blocks + 1;
-        const bool fits = smem_of(need * kGroupBytes) <= kRowSmem && need <= 32ull * kChunks;
-        kernel = fits ? sample_kernel<TI, true> : sample_kernel<TI, false>;
-        room = fits ? (uint32_t)need : 0;
-        smem = fits ? smem_of(need * kGroupBytes) : 0;
-        e = resident_clusters(reinterpret_cast<const void*>(kernel), kRowThreads, blocks, smem, &clusters);
-        if (e != cudaSuccess) return e;
-        if (clusters > 0 || blocks == 1) break;
+    const void* kernel = reinterpret_cast<const void*>(sample_kernel<TI>);
+    double best = 0.0;
+    uint32_t blocks = 0, log2_blocks = 0, room = 0, clusters = 0, threads = 0, smem = 0;
+    for (const Spread& w : kSpreads) {
+        for (uint32_t b = 1, log2 = 0; b <= 16; b *= 2, ++log2) {
+            if (b > 1 && groups < b * (uint64_t)w.threads / 2) break;  // too little for so many
+            const uint64_t need = (groups + b - 1) / b + 1, most = w.smem / kGroupBytes, keep = need < most ? need : most;
+            const uint32_t bytes = (uint32_t)smem_of(keep * kGroupBytes);
+            int n = 0;
+            e = resident_clusters(kernel, w.threads, b, bytes, &n);
+            if (e != cudaSuccess) return e;
+            if (n < 1) continue;
+            const uint64_t rounds = ((uint64_t)a.T + n - 1) / n, on = ((uint64_t)a.T * b + di.sms - 1) / di.sms;
+            const double per_sm = (double)(on < w.per_sm ? on : w.per_sm);
+            const double ns = (double)rounds * (kRoundNs + per_sm * kGroupNs * ((double)keep + kAgain * (double)(need - keep)));
+            if (blocks && ns >= best) continue;
+            best = ns;
+            blocks = b;
+            log2_blocks = log2;
+            room = (uint32_t)keep;
+            clusters = (uint32_t)n;
+            threads = w.threads;
+            smem = bytes;
+        }
     }
-    uint32_t log2_blocks = 0;
-    while ((1u << log2_blocks) < blocks) ++log2_blocks;
+    if (blocks == 0) return cudaErrorInvalidConfiguration;
     int shift = 0;  // sums of V weights stay below 2^63
     while ((1ull << (62 - kBits + shift)) < a.V) ++shift;
-    const uint64_t most = 0x7fffffffull / 16;
-    const uint32_t grid = (uint32_t)(a.T < most ? a.T : most) * blocks;
-    return launch_early(kernel, grid, kRowThreads, smem, blocks, s, a, room, log2_blocks, shift);
+    const uint32_t grid = (a.T < clusters ? a.T : clusters) * blocks;
+    return launch_early(sample_kernel<TI>, grid, threads, smem, blocks, s, a, room, log2_blocks, shift);
 }
 
 }  // namespace
