@@ -848,7 +848,7 @@ s2_status s2_pack4(const void* x, s2_dtype dt, uint64_t rows, uint64_t cols, uin
     if (clash({{codes, extent(rows, bytes4(cols), ldc, 1)}, {scales, scales4(rows, cols)},
                {x, extent(rows, cols, ldx, size_of(dt))}}, 2))
         return S2_ERR_INVALID_ARG;
-    Pack4Args a{x, ldx, codes, ldc, scales, rows, (uint32_t)cols, (uint32_t)blocks8(cols), items};
+    Pack4Args a{x, ldx, codes, ldc, scales, rows, (uint32_t)cols, (uint32_t)blocks8(cols), items / 16, 0};
     return cuda_status(launch_pack4(a, dt == S2_F32 ? 0 : 1, reinterpret_cast<cudaStream_t>(stream)));
 }
 

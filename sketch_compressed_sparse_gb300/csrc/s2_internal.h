@@ -195,7 +195,8 @@ struct Pack4Args {
     uint64_t rows;
     uint32_t cols;
     uint32_t tcols;  // tiles per row of tiles
-    uint64_t items;  // 16 per tile
+    uint64_t tiles;
+    uint64_t items;  // what a warp takes (set by the launch)
 };
 struct Unpack4Args {
     const uint8_t* codes;
@@ -206,7 +207,7 @@ struct Unpack4Args {
     uint64_t rows;
     uint32_t cols;
     uint32_t tcols;
-    uint64_t items;
+    uint64_t items;  // 16 per tile
 };
 // dtype: 0 = f32, 1 = bf16; at least one element.
 cudaError_t launch_pack4(const Pack4Args& a, int dtype, cudaStream_t s);

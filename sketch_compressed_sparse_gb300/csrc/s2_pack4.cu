@@ -9,10 +9,11 @@
 // element, and code * 2^e is exact in float32 and in bfloat16.
 //
 // Both directions are bound by HBM: an element is read once and written once.
-// A warp holds eight rows of a tile of 128 x 128 elements, r and r + 1 for r
-// ahead by 0, 32, 64 and 96: their scale words are then 32 neighbouring bytes of
-// the tile, one sector, and every lane has four independent loads in flight.
-// A row's 128 elements are 16 lanes of eight neighbours, whose codes are a word.
+// A lane holds neighbours of four rows of a tile of 128 x 128 elements, 32 rows
+// apart: their scale words are then 16 neighbouring bytes of the tile, and it has
+// four or eight independent loads in flight. Packing takes 32 bytes of a row a
+// lane, eight floats or sixteen bfloat16 (with eight bfloat16 twice the shuffles
+// and addresses, 267735 x 1024 in 202 us instead of 101).
 #include "s2_internal.h"
 #include "s2_launch.cuh"
 
@@ -20,59 +21,81 @@ namespace s2 {
 namespace {
 
 constexpr int kTile = 128;           // rows and columns of a tile of scales
-constexpr int kPer = 8;              // elements per lane
-constexpr int kLanes = kTile / kPer; // lanes per row of a tile
 constexpr int kRows = 4;             // rows of a lane
 constexpr uint32_t kTileBytes = 512;
 constexpr uint32_t kMinByte = 2;     // e >= -125
 constexpr uint32_t kInf = 0x7f800000u;
 
-// What a warp works on: eight rows of one tile.
+// What a warp works on: rows of one tile, LANES lanes and 128 / LANES elements a
+// lane to a row, 32 / LANES rows at a time.
 struct Item {
-    uint64_t row;    // the half-warp's first row; the others are 32, 64 and 96 below
+    uint64_t row;    // the lane's first row; the others are 32, 64 and 96 below
     uint32_t col;    // the lane's first column
     int left;        // columns from there to the row's end
-    uint64_t scale;  // the half-warp's four words of scale bytes
+    uint64_t scale;  // the four words of scale bytes of the lane's rows
 };
+template <int LANES>
 __device__ __forceinline__ Item item(uint64_t at, uint32_t tcols, uint32_t cols) {
-    const uint32_t lane = threadIdx.x % 32, half = lane / kLanes, sub = lane % kLanes;
+    constexpr uint32_t kAtOnce = 32 / LANES, kBands = 32 / kAtOnce;  // of a tile's first 32 rows
+    const uint32_t lane = threadIdx.x % 32, sub = lane % LANES;
     // neighbouring warps take neighbouring tiles of the same rows
     const uint64_t band = at / tcols;
     const uint32_t tcol = (uint32_t)(at - band * tcols);
-    const uint64_t trow = band / 16;
-    const uint32_t r = (uint32_t)(band % 16) * 2 + half;
+    const uint64_t trow = band / kBands;
+    const uint32_t r = (uint32_t)(band % kBands) * kAtOnce + lane / LANES;
     Item it;
     it.row = trow * kTile + r;
-    it.col = tcol * kTile + sub * kPer;
+    it.col = tcol * kTile + sub * (kTile / LANES);
     it.left = (int)cols - (int)it.col;
     it.scale = (trow * tcols + tcol) * kTileBytes + r * 16;
     return it;
 }
 
-// A lane's eight elements of a row as floats' bits; those past the end are 0.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* p, int left, uint32_t* v) {
-    if (VEC && left >= kPer) {
+// A lane's elements of a row, eight words as they lie in memory: eight floats or
+// sixteen bfloat16. Those past the row's end are 0.
+template <typename T>
+struct Raw {
+    static constexpr int kPer = 32 / sizeof(T);
+    uint32_t w[8];
+    __device__ __forceinline__ float value(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else return __uint_as_float(i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    }
+    // Bits of the largest magnitude as a float's; above every number's where there is a NaN.
+    __device__ __forceinline__ uint32_t amax() const {
+        uint32_t m = 0;
         if constexpr (sizeof(T) == 4) {
-            const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
+            return m;
         } else {
-            const uint4 a = *reinterpret_cast<const uint4*>(p);
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+            m = w[0] & 0x7fff7fffu;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[2 * i] = w[i] << 16;
-                v[2 * i + 1] = w[i] & 0xffff0000u;
-            }
+            for (int i = 1; i < 8; ++i) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i] & 0x7fff7fffu));
+            return max(m & 0xffff0000u, m << 16);
         }
-        return;
+    }
+};
+template <typename T, bool VEC>
+__device__ __forceinline__ Raw<T> load(const T* p, int left) {
+    Raw<T> r;
+    if (VEC && left >= Raw<T>::kPer) {
+        const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
+        r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
+        r.w[4] = b.x, r.w[5] = b.y, r.w[6] = b.z, r.w[7] = b.w;
+        return r;
     }
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        v[i] = 0;
-        if (i < left) v[i] = sizeof(T) == 4 ? (uint32_t)p[i] : (uint32_t)p[i] << 16;
+    for (int i = 0; i < 8; ++i) {
+        r.w[i] = 0;
+        if constexpr (sizeof(T) == 4) {
+            if (i < left) r.w[i] = p[i];
+        } else {
+            if (2 * i < left) r.w[i] = p[2 * i];
+            if (2 * i + 1 < left) r.w[i] |= (uint32_t)p[2 * i + 1] << 16;
+        }
     }
+    return r;
 }
 
 // Eight codes as a word, the first in the lowest half byte: to nearest, ties to
@@ -92,54 +115,58 @@ __device__ __forceinline__ uint32_t codes8(const float* q) {
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) pack4_kernel(Pack4Args a) {
+    constexpr int kPer = Raw<T>::kPer, kLanes = kTile / kPer, kBlock = 32 / kPer;  // lanes of a row, of a block
     stream_order();
     const uint64_t at = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) / 32;
     if (at >= a.items) return;  // whole warps
-    const Item it = item(at, a.tcols, a.cols);
+    const Item it = item<kLanes>(at, a.tcols, a.cols);
     const T* x = static_cast<const T*>(a.x);
-    uint32_t v[kRows][kPer], word[kRows];
+    Raw<T> v[kRows];
+    uint32_t word[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         const uint64_t row = it.row + 32 * i;
         const bool there = row < a.rows && it.left > 0;
-        load8<T, VEC>(x + (there ? row * a.ldx + it.col : 0), there ? it.left : 0, v[i]);
+        v[i] = load<T, VEC>(x + (there ? row * a.ldx + it.col : 0), there ? it.left : 0);
     }
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         const uint64_t row = it.row + 32 * i;
-        uint32_t m = 0;
+        uint32_t m = v[i].amax();
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) m = max(m, v[i][j] & 0x7fffffffu);  // above every number where there is a NaN
-        m = max(m, __shfl_xor_sync(kFull, m, 1));
-        m = max(m, __shfl_xor_sync(kFull, m, 2));
+        for (int o = 1; o < kBlock; o *= 2) m = max(m, __shfl_xor_sync(kFull, m, o));
         const bool special = m >= kInf;
         uint32_t b = (uint32_t)max((int)((m + 0x3fffffu) >> 23) - 2, (int)kMinByte);
         const float inv = special ? 0.0f : __uint_as_float((254u - b) << 23);
-        float q[kPer];
+        uint32_t c[kPer / 8];
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) q[j] = __uint_as_float(v[i][j]) * inv;
-        uint32_t c = codes8(q);
+        for (int h = 0; h < kPer / 8; ++h) {
+            float q[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) q[j] = v[i].value(8 * h + j) * inv;
+            c[h] = codes8(q);
+        }
         if (special) {
             b = 255;
-            c = 0;
+#pragma unroll
+            for (int h = 0; h < kPer / 8; ++h) c[h] = 0;
         }
         const bool there = row < a.rows && it.left > 0;
         if (!there) b = 127;  // past the end
         if (there) {
             uint8_t* p = a.codes + row * a.ldc + it.col / 2;
             if (it.left >= kPer) {
-                *reinterpret_cast<uint32_t*>(p) = c;
+                if constexpr (kPer == 16) *reinterpret_cast<uint2*>(p) = make_uint2(c[0], c[1]);
+                else *reinterpret_cast<uint32_t*>(p) = c[0];
             } else {
-                for (int j = 0; 2 * j < it.left; ++j) p[j] = (uint8_t)(c >> (8 * j));
+                for (int j = 0; 2 * j < it.left; ++j) p[j] = (uint8_t)(c[j / 4] >> (8 * (j % 4)));
             }
         }
-        // four lanes' bytes in lanes 0, 4, 8 and 12 of the half-warp: one word
+        // the bytes of the row's four blocks, kBlock lanes apart, as one word in its first lane
         uint32_t w = b;
-        w |= __shfl_xor_sync(kFull, b, 4) << 8;
-        w = __byte_perm(w, __shfl_xor_sync(kFull, w, 8), 0x5410);
-        word[i] = w;
+        w |= __shfl_xor_sync(kFull, b, kBlock) << 8;
+        word[i] = __byte_perm(w, __shfl_xor_sync(kFull, w, 2 * kBlock), 0x5410);
     }
-    // (lane 0's word holds the bytes in ascending order)
     if (threadIdx.x % kLanes == 0)
         *reinterpret_cast<uint4*>(a.scales + it.scale) = make_uint4(word[0], word[1], word[2], word[3]);
 }
@@ -165,12 +192,19 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     return r;
 }
 
-template <typename T, bool VEC>
+__device__ __forceinline__ float scale_of(uint32_t b) {
+    // byte 0 stands for 2^-127, a subnormal float; byte 255 for NaN
+    return __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7fffffffu : b << 23);
+}
+
+// Rows on 16 bytes: eight neighbours a lane.
+template <typename T>
 __global__ void __launch_bounds__(kThreads) unpack4_kernel(Unpack4Args a) {
+    constexpr int kLanes = 16, kPer = 8;
     stream_order();
     const uint64_t at = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) / 32;
     if (at >= a.items) return;
-    const Item it = item(at, a.tcols, a.cols);
+    const Item it = item<kLanes>(at, a.tcols, a.cols);
     if (it.left <= 0) return;
     uint32_t c[kRows];
     const uint4 s4 = *reinterpret_cast<const uint4*>(a.scales + it.scale);
@@ -192,16 +226,14 @@ __global__ void __launch_bounds__(kThreads) unpack4_kernel(Unpack4Args a) {
     for (int i = 0; i < kRows; ++i) {
         const uint64_t row = it.row + 32 * i;
         if (row >= a.rows) break;
-        const uint32_t b = (s[i] >> (8 * (threadIdx.x % kLanes / 4))) & 255u;
-        // byte 0 stands for 2^-127, a subnormal float; byte 255 for NaN
-        const float f = __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7fffffffu : b << 23);
+        const float f = scale_of((s[i] >> (8 * (threadIdx.x % kLanes / 4))) & 255u);
         float v[kPer];
         values8(c[i], v);
 #pragma unroll
         for (int j = 0; j < kPer; ++j) v[j] *= f;
         T* o = out + row * a.ldo + it.col;
         if constexpr (sizeof(T) == 4) {
-            if (VEC && it.left >= kPer) {
+            if (it.left >= kPer) {
                 reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
                 reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
             } else {
@@ -211,7 +243,7 @@ __global__ void __launch_bounds__(kThreads) unpack4_kernel(Unpack4Args a) {
             }
         } else {
             const uint4 w = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
-            if (VEC && it.left >= kPer) {
+            if (it.left >= kPer) {
                 *reinterpret_cast<uint4*>(o) = w;
             } else {
                 const uint32_t h[4] = {w.x, w.y, w.z, w.w};
@@ -219,6 +251,42 @@ __global__ void __launch_bounds__(kThreads) unpack4_kernel(Unpack4Args a) {
                 for (int j = 0; j < kPer; ++j)
                     if (j < it.left) o[j] = (uint16_t)(h[j / 2] >> (16 * (j % 2)));
             }
+        }
+    }
+}
+
+// Rows that start anywhere: every sixteenth element a lane, so that the half-warp's
+// stores of two or four bytes still run along the row (20000 x 4095 bfloat16 in
+// 65 us; with eight neighbours a lane 227).
+template <typename T>
+__global__ void __launch_bounds__(kThreads) unpack4_any_kernel(Unpack4Args a) {
+    constexpr int kLanes = 16, kPer = 8;
+    stream_order();
+    const uint64_t at = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) / 32;
+    if (at >= a.items) return;
+    const Item it = item<kLanes>(at, a.tcols, a.cols);
+    const uint32_t sub = threadIdx.x % kLanes, tile = it.col - sub * kPer;  // the tile's first column
+    const uint4 s4 = *reinterpret_cast<const uint4*>(a.scales + it.scale);
+    const uint32_t s[kRows] = {s4.x, s4.y, s4.z, s4.w};
+    T* out = static_cast<T*>(a.out);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const uint64_t row = it.row + 32 * i;
+        if (row >= a.rows) break;
+        const uint8_t* p = a.codes + row * a.ldc + tile / 2 + sub / 2;
+        T* o = out + row * a.ldo + tile + sub;
+        uint32_t c = 0;  // the lane's eight codes
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+            if (tile + sub + j * kLanes < a.cols) c |= ((uint32_t)p[j * (kLanes / 2)] >> (4 * (sub % 2)) & 15u) << (4 * j);
+        float v[kPer];
+        values8(c, v);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            if (tile + sub + j * kLanes >= a.cols) continue;
+            const float q = v[j] * scale_of(s[i] >> (8 * (j / 2)) & 255u);  // two steps of sixteen are a block
+            if constexpr (sizeof(T) == 4) o[j * kLanes] = q;
+            else o[j * kLanes] = (uint16_t)bf16x2(q, 0.0f);
         }
     }
 }
@@ -231,7 +299,9 @@ inline uint32_t blocks_of(uint64_t items) { return (uint32_t)((items + kThreads 
 
 }  // namespace
 
-cudaError_t launch_pack4(const Pack4Args& a, int dtype, cudaStream_t s) {
+cudaError_t launch_pack4(const Pack4Args& m, int dtype, cudaStream_t s) {
+    Pack4Args a = m;
+    a.items = a.tiles * (dtype == 0 ? 16 : 8);
     const bool vec = vector_rows(a.x, a.ldx, a.rows, dtype == 0 ? 4 : 2);
     auto kernel = dtype == 0 ? (vec ? pack4_kernel<uint32_t, true> : pack4_kernel<uint32_t, false>)
                              : (vec ? pack4_kernel<uint16_t, true> : pack4_kernel<uint16_t, false>);
@@ -240,8 +310,8 @@ cudaError_t launch_pack4(const Pack4Args& a, int dtype, cudaStream_t s) {
 
 cudaError_t launch_unpack4(const Unpack4Args& a, int dtype, cudaStream_t s) {
     const bool vec = vector_rows(a.out, a.ldo, a.rows, dtype == 0 ? 4 : 2);
-    if (dtype == 0) return launch_early(vec ? unpack4_kernel<float, true> : unpack4_kernel<float, false>, blocks_of(a.items), kThreads, 0, 0, s, a);
-    return launch_early(vec ? unpack4_kernel<uint16_t, true> : unpack4_kernel<uint16_t, false>, blocks_of(a.items), kThreads, 0, 0, s, a);
+    if (dtype == 0) return launch_early(vec ? unpack4_kernel<float> : unpack4_any_kernel<float>, blocks_of(a.items), kThreads, 0, 0, s, a);
+    return launch_early(vec ? unpack4_kernel<uint16_t> : unpack4_any_kernel<uint16_t>, blocks_of(a.items), kThreads, 0, 0, s, a);
 }
 
 }  // namespace s2

@@ -29,6 +29,7 @@ struct Part {
     uint32_t count;  // its groups
     uint32_t lo, n;  // its groups lo..lo+n-1 lie in the row as a whole
     __device__ __forceinline__ bool inner(uint32_t l) const { return l - lo < n; }
+    __device__ __forceinline__ uint64_t groups(uint32_t V) const { return ((uint64_t)V + off + 7) / 8; }
     // index in the row of element j of local group l (beyond the row's ends: below 0 or not below V)
     __device__ __forceinline__ int64_t index(uint32_t l, int j) const { return (int64_t)(first + l) * 8 + j - off; }
     // the row's element i lies in this block

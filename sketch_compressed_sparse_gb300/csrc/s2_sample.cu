@@ -83,10 +83,10 @@ struct Shared {
     float warp_max[kMaxThreads / 32];
     float top[2];        // this block's largest logit
     uint32_t lowest[2];  // the lowest index of the row's largest
-    uint32_t listed;
+    uint32_t listed, lowest_key, highest_key;  // of the tokens that are ranked
     uint64_t total;      // weight kept in this block
     Settings set;
-    uint64_t before;     // of the bin that was found
+    uint64_t before, inside;  // of the bin that was found
     uint32_t bin;
     Listed border;
 };
@@ -99,6 +99,10 @@ __device__ __forceinline__ uint32_t key_of(float v) {
 __device__ __forceinline__ float of_key(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
+
+// The nearest whole number of a float from 0 to 2^22 (adding 1.5 * 2^23 leaves it in
+// the low bits; the conversion takes four times as long).
+__device__ __forceinline__ uint32_t whole_of(float v) { return (uint32_t)(__float_as_int(__fadd_rn(v, 12582912.0f)) - 0x4b400000); }
 
 // floor(f * z), or the ceiling, for a float f in [0, 1).
 __device__ uint64_t times(float f, uint64_t z, bool up) {
@@ -229,14 +233,12 @@ struct Weigher {
                 if (use(element(r, j), j)) f(element(r, j), j, (*this)(element(r, j)));
             return;
         }
+        int hi[8], lo[8];
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            int hi[2], lo[2];
-            const float v0 = element(r, j), v1 = element(r, j + 1);
-            pair(v0, v1, hi, lo);
-            if (use(v0, j)) f(v0, j, whole(hi[0], lo[0]));
-            if (use(v1, j + 1)) f(v1, j + 1, whole(hi[1], lo[1]));
-        }
+        for (int j = 0; j < 8; j += 2) pair(element(r, j), element(r, j + 1), hi + j, lo + j);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (use(element(r, j), j)) f(element(r, j), j, whole(hi[j], lo[j]));
     }
 };
 
@@ -280,7 +282,8 @@ struct Team {
     // goal_of(total), from 1 to that sum; *goal: what is left of it in that bin.
     // fill(hist) adds this block's part. The same answer in every block.
     template <typename Fill, typename GoalOf>
-    __device__ __forceinline__ uint32_t find_bin(Fill fill, GoalOf goal_of, uint64_t* goal) const {
+    // *inside: what lies in it.
+    __device__ __forceinline__ uint32_t find_bin(Fill fill, GoalOf goal_of, uint64_t* goal, uint64_t* inside = nullptr) const {
         uint64_t* hist = sh.hist[turn++ & 1];
         if (threadIdx.x < kBins) hist[threadIdx.x] = 0;
         __syncthreads();
@@ -293,9 +296,11 @@ struct Team {
         if (upto >= want && upto - sum < want) {
             sh.bin = threadIdx.x;
             sh.before = upto - sum;
+            sh.inside = sum;
         }
         __syncthreads();
         *goal = want - sh.before;
+        if (inside) *inside = sh.inside;
         return sh.bin;
     }
     // The sum of the blocks' totals, and of those before this one. (A lane reads a block's.)
@@ -338,57 +343,76 @@ __device__ __forceinline__ void count_in(uint64_t* at, uint64_t m) {
 
 // The border of the shortest beginning of what `from` keeps that measures
 // goal_of(what all of it measures) or more. `scale`: ranges per unit of logit.
-// `least`: no token below it belongs to that beginning.
+// `least`: no token below it belongs to that beginning. `kept_most`: `from` keeps
+// no more tokens than this (so few that they are all ranked).
 template <typename TI, typename Measure, typename GoalOf>
-__device__ Border narrow(const Team<TI>& team, Border from, float scale, float least, const Measure& measure, GoalOf goal_of) {
+__device__ Border narrow(const Team<TI>& team, Border from, float scale, float least, uint64_t kept_most, const Measure& measure, GoalOf goal_of) {
     Shared& sh = team.sh;
     const Row<TI>& row = team.row;
     const float top = team.top;
-    uint64_t goal;
+    uint64_t goal = 0, inside = 0;
+    const bool rank_all = kept_most <= kList;
     auto range = [&](float v) { return fminf((top - v) * scale, (float)(kBins - 1)); };  // larger logits first
-    auto range_of = [&](float v) { return (uint32_t)__float2int_rn(range(v)); };
+    auto range_of = [&](float v) { return whole_of(range(v)); };
     auto kept = [&](uint32_t l) { return [&row, &from, l](float v, int j) { return from.keeps(v, row.index(l, j)); }; };
-    const uint32_t bin = team.find_bin(
-        [&](uint64_t* hist) {
-            row.above(fmaxf(least, from.v), [&](const Raw<TI>& r, uint32_t l) {
-                measure.group(r, kept(l), [&](float v, int, uint64_t m) { count_in<Measure>(hist + range_of(v), m); });
-            });
-        },
-        goal_of, &goal);
+    uint32_t bin = 0;
+    if (!rank_all)
+        bin = team.find_bin(
+            [&](uint64_t* hist) {
+                row.above(fmaxf(least, from.v), [&](const Raw<TI>& r, uint32_t l) {
+                    measure.group(r, kept(l), [&](float v, int, uint64_t m) { count_in<Measure>(hist + range_of(v), m); });
+                });
+            },
+            goal_of, &goal, &inside);
     auto left = [&](uint64_t) { return goal; };
     // a part of the range; the last range has no end
     uint32_t part = kBins;
-    auto part_of_range = [&](float v) { return (uint32_t)__float2int_rn(fminf(fmaxf((range(v) - (float)bin + 0.5f) * (kBins - 1), 0.0f), kBins - 1)); };
+    auto part_of_range = [&](float v) { return whole_of(fminf(fmaxf((range(v) - (float)bin + 0.5f) * (kBins - 1), 0.0f), kBins - 1)); };
     // (a little below the range's end, whatever the rounding)
-    const float low = bin < kBins - 1 ? fmaxf(from.v, top - ((float)bin + 0.75f) / scale) : from.v;
-    if (bin < kBins - 1)
+    const float low = bin < kBins - 1 && !rank_all ? fmaxf(from.v, top - ((float)bin + 0.75f) / scale) : from.v;
+    const bool few = rank_all || (!Measure::kWeighed && inside <= kList);
+    if (bin < kBins - 1 && !few)
         part = team.find_bin(
             [&](uint64_t* hist) {
                 row.above(low, [&](const Raw<TI>& r, uint32_t l) {
+                    uint32_t here = 0;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float v = element(r, j);
-                        if (from.keeps(v, row.index(l, j)) && range_of(v) == bin) count_in<Measure>(hist + part_of_range(v), measure(v));
-                    }
+                    for (int j = 0; j < 8; ++j) here |= (uint32_t)(from.keeps(element(r, j), row.index(l, j)) && range_of(element(r, j)) == bin) << j;
+                    if (here)
+                        measure.group(r, [&](float, int j) { return here >> j & 1; },
+                                      [&](float v, int, uint64_t m) { count_in<Measure>(hist + part_of_range(v), m); });
                 });
             },
             left, &goal);
-    auto member = [&](float v) { return range_of(v) == bin && (part == kBins || part_of_range(v) == part); };
+    auto member = [&](float v) { return rank_all || (range_of(v) == bin && (part == kBins || part_of_range(v) == part)); };
 
     // few: rank them against one another
-    if (part < kBins) {
-        if (threadIdx.x == 0) sh.listed = 0;
+    if (part < kBins || few) {
+        if (threadIdx.x == 0) {
+            sh.listed = 0;
+            sh.lowest_key = 0xffffffffu;
+            sh.highest_key = 0;
+        }
         __syncthreads();
+        uint32_t lowest = 0xffffffffu, highest = 0;
         row.above(low, [&](const Raw<TI>& r, uint32_t l) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float v = element(r, j);
                 const uint32_t i = row.index(l, j);
                 if (!from.keeps(v, i) || !member(v)) continue;
-                const uint32_t at = atomicAdd(&sh.listed, 1u);
+                const uint32_t at = atomicAdd(&sh.listed, 1u), k = key_of(v);
                 if (at < kList) sh.list[at] = {v, i};
+                lowest = min(lowest, k);
+                highest = max(highest, k);
             }
         });
+        lowest = __reduce_min_sync(kAll, lowest);
+        highest = __reduce_max_sync(kAll, highest);
+        if (threadIdx.x % 32 == 0 && lowest <= highest) {
+            atomicMin(&sh.lowest_key, lowest);
+            atomicMax(&sh.highest_key, highest);
+        }
         cluster_barrier();
         // each warp takes some blocks' lists to their places behind one another
         const uint32_t lane = threadIdx.x % 32, c = min(lane < team.blocks ? peer_u32(peer(&sh.listed, lane)) : 0, kList + 1);
@@ -411,12 +435,20 @@ __device__ Border narrow(const Team<TI>& team, Border from, float scale, float l
             }
         __syncthreads();
         if (n <= kList) {
+            if (rank_all) {
+                uint64_t total = 0;
+#pragma unroll 8
+                for (uint32_t j = 0; j < n; ++j) total += sh.weight[j];
+                goal = goal_of(total);
+            }
             if (threadIdx.x < n) {
                 const Listed me = sh.all[threadIdx.x];
                 uint64_t before = 0;
+#pragma unroll 8
                 for (uint32_t j = 0; j < n; ++j) {
                     const Listed o = sh.all[j];
-                    if (o.v > me.v || (o.v == me.v && o.i < me.i)) before += sh.weight[j];
+                    const uint64_t w = sh.weight[j];
+                    before += o.v > me.v || (o.v == me.v && o.i < me.i) ? w : 0;
                 }
                 if (before < goal && before + sh.weight[threadIdx.x] >= goal) sh.border = {me.v, me.i + 1};
             }
@@ -426,10 +458,18 @@ __device__ Border narrow(const Team<TI>& team, Border from, float scale, float l
             return b;
         }
     }
-    // many: the border's key, eight bits at a time
+    // many: the border's key, eight bits at a time, unless all have the same
     uint32_t prefix = 0;
+    int shift = 24;
+    if (part < kBins || few) {
+        const uint32_t lane = threadIdx.x % 32;
+        const uint32_t lowest = __reduce_min_sync(kAll, lane < team.blocks ? peer_u32(peer(&sh.lowest_key, lane)) : 0xffffffffu);
+        prefix = __reduce_max_sync(kAll, lane < team.blocks ? peer_u32(peer(&sh.highest_key, lane)) : 0u);
+        if (lowest == prefix) shift = -8;
+        else prefix = 0;
+    }
 #pragma unroll 1
-    for (int shift = 24; shift >= 0; shift -= 8) {
+    for (; shift >= 0; shift -= 8) {
         const uint32_t found = team.find_bin(
             [&](uint64_t* hist) {
                 row.above(low, [&](const Raw<TI>& r, uint32_t l) {
@@ -508,13 +548,14 @@ template <typename TI>
 __device__ __forceinline__ float at_least(const Team<TI>& team, uint64_t k, float scale) {
     const Row<TI>& row = team.row;
     const float top = team.top;
-    if (k > row.V / 16) return minus_inf();  // too near to all of them
+    // (too near to all of them; and where a thread has few groups, a pass for this takes longer than it spares)
+    if (k > row.V / 16 || row.p.groups(row.V) < 8ull * blockDim.x * team.blocks) return minus_inf();
     uint64_t goal, groups = 0;
     const uint32_t bin = team.find_bin(
         [&](uint64_t* hist) {
             row.each([&](const Raw<TI>& r, uint32_t) {
                 const float m = group_max(r);
-                if (m > minus_inf()) atomicAdd(reinterpret_cast<uint32_t*>(hist + __float2int_rn(fminf((top - m) * scale, (float)(kBins - 1)))), 1u);
+                if (m > minus_inf()) atomicAdd(reinterpret_cast<uint32_t*>(hist + whole_of(fminf((top - m) * scale, (float)(kBins - 1)))), 1u);
             });
         },
         [&](uint64_t total) {
@@ -548,9 +589,11 @@ __global__ void __launch_bounds__(kMaxThreads, 1) sample_kernel(const SampleArgs
             Settings s;
             const float t = a.temperature ? a.temperature[at] : 1.0f;
             s.greedy = !(t >= FLT_MIN);
-            const double c = 1.4426950408889634074 / (double)t;
-            s.ch = (float)c;
-            s.cl = (float)(c - (double)s.ch);
+            // log2(e) / t in two floats: a quotient, and that of its remainder (64-bit division is slow here)
+            constexpr double kLog2e = 1.4426950408889634074;
+            constexpr float kHigh = (float)kLog2e, kLow = (float)(kLog2e - (double)kHigh);
+            s.ch = __fdiv_rn(kHigh, t);
+            s.cl = t < 0x1p100f ? __fdiv_rn(__fmaf_rn(-s.ch, t, kHigh) + kLow, t) : 0.0f;  // (beyond, a remainder below the floats)
             s.bins = kPerOctave * s.ch;
             s.top_k = a.top_k && a.top_k[at] > 0 ? (uint32_t)a.top_k[at] : 0;
             const float p = a.top_p ? a.top_p[at] : 1.0f;
@@ -608,10 +651,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1) sample_kernel(const SampleArgs
         if (set.top_k && set.top_k < a.V) {
             const float scale = kPerOctave * 1.44269504f;
             const float least = at_least(team, set.top_k, scale);
-            border = narrow(team, border, scale, least, Count{}, [&](uint64_t total) { return total < set.top_k ? total : (uint64_t)set.top_k; });
+            border = narrow(team, border, scale, least, ~0ull, Count{}, [&](uint64_t total) { return total < set.top_k ? total : (uint64_t)set.top_k; });
         }
         if (set.top_p < 1.0f)
-            border = narrow(team, border, set.bins, minus_inf(), weigh, [&](uint64_t total) {
+            border = narrow(team, border, set.bins, minus_inf(), set.top_k ? set.top_k : ~0ull, weigh, [&](uint64_t total) {
                 const uint64_t goal = times(set.top_p, total, true);
                 return goal ? goal : 1;
             });
@@ -688,12 +731,16 @@ __global__ void __launch_bounds__(kMaxThreads, 1) sample_kernel(const SampleArgs
 
 // How a row is spread: threads of a block, blocks on an SM, shared memory of a
 // block's part of a row. A round of rows costs kRoundNs, and a group kGroupNs of
-// its SM, kAgain times as much where it is read again in every pass.
+// its SM, kAgain times as much where it is read again in every pass. Rows of all
+// kinds of settings, 256 x 267735 float32: two blocks of an SM and eight of a row
+// 445 us, two and four 439, three and eight 447, one and four 460, two and sixteen
+// 680, one and one 709; 24 rows: 84, 114, 96, 91, 81 and 294; a row of 33278 in one
+// block 60 us, in sixteen 21.
 struct Spread {
     uint32_t threads, per_sm, smem;
 };
 constexpr Spread kSpreads[3] = {{1024, 1, 200 * 1024}, {512, 2, 100 * 1024}, {320, 3, 66 * 1024}};
-constexpr double kRoundNs = 12000.0, kGroupNs = 2.0, kAgain = 2.0;
+constexpr double kRoundNs = 9000.0, kGroupNs = 6.5, kAgain = 2.0;
 
 template <typename TI>
 cudaError_t launch(const SampleArgs& a, cudaStream_t s) {
