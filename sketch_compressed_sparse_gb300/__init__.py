@@ -128,8 +128,9 @@ _fns = {}
 
 
 def _short_calls():
-    """The 8-bit layer's calls without ctypes' conversions: the same functions of the same library. Empty
-    where the extension is missing or was compiled from another s2.h than the library."""
+    """The layers' calls, sampling and distillation without ctypes' conversions: the same functions of the
+    same library (s2_distill's parameters as four numbers). Empty where the extension is missing or was
+    compiled from another s2.h than the library."""
     if not os.path.exists(_CALLS_PATH):
         return {}
     spec = importlib.util.spec_from_file_location("_s2calls", _CALLS_PATH)
@@ -141,7 +142,8 @@ def _short_calls():
     header = getattr(calls, "header", "unknown")
     if header == "unknown" or not _fns["s2_version"]().decode().endswith(header):
         return {}
-    names = ("s2_pack8", "s2_unpack8", "s2_matmul8", "s2_wgrad8")
+    names = ("s2_pack8", "s2_unpack8", "s2_matmul8", "s2_wgrad8", "s2_pack4", "s2_unpack4", "s2_matmul4", "s2_sample",
+             "s2_distill")
     calls.bind(*(ctypes.cast(_fns[n], _vp).value for n in names))
     return {n: getattr(calls, n) for n in names}
 
@@ -160,7 +162,11 @@ def _load():
         f.argtypes = args
         f.restype = res
         _fns[name] = f
-    _fns.update(_short_calls())
+    calls = _short_calls()
+    if not calls:
+        by_ctypes = _fns["s2_distill"]
+        calls = {"s2_distill": lambda *a: by_ctypes(*a[:10], DistillParams(*a[10:14]), *a[14:])}
+    _fns.update(calls)
     return _fns
 
 
@@ -685,7 +691,7 @@ def s2_distill(logits: torch.Tensor, teacher_idx: Optional[torch.Tensor], teache
         ddt = _dtype_code(dlogits)
     st = _f("s2_distill")(pz, _dtype_code(logits), T, V, ld, _dev(teacher_idx, "teacher_idx", _I32T, T * K),
                           _dev(teacher, "teacher", _F32S, T * K), K, _rows(targets, "targets", _I32T, T),
-                          _rows(row_weight, "row_weight", _F32S, T), DistillParams(temperature, soft, hard, scale),
+                          _rows(row_weight, "row_weight", _F32S, T), temperature, soft, hard, scale,
                           _rows(loss, "loss", _F32S, T), pd, ddt, ldd, _stream(stream))
     if st:
         raise S2Error(st, "s2_distill")

@@ -1,6 +1,9 @@
 """s2_distill without a GPU: the plain implementation that the GPU tests compare with, against torch's
 own functions and differences, and the refusals of the entry point (no call here reaches a kernel)."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -8,6 +11,7 @@ import torch
 
 from tests import _distill as ref
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 VP, U64, I32 = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_int
 OK, INVALID, ALIGN, UNSUP = 0, 1, 2, 3
 A = 0x10000000  # fake, aligned device addresses; never dereferenced
@@ -90,3 +94,16 @@ def test_binding_refusals():
     z = torch.zeros(2, 8)
     with pytest.raises(ValueError, match="CUDA"):
         s2.s2_distill(z, None, None, torch.zeros(2))
+
+
+def test_both_ways_of_calling_agree():
+    """The extension's call and that by ctypes refuse the same: the parameters arrive."""
+    code = ("import sketch_compressed_sparse_gb300 as s2\n"
+            "if {0}: s2._CALLS_PATH = '/nowhere'\n"
+            "f = s2._f('s2_distill')\n"
+            "one = lambda t, so, h, sc: f(None, 0, 0, 5, 5, None, None, 0, None, None, t, so, h, sc, None, None, 0, 0, None)\n"
+            "inf = float('inf')\n"
+            "print([one(*v) for v in ((1.0, 1, 0.0, 2.0), (0.0, 1.0, 0.0, 1.0), (1.0, inf, 0.0, 1.0), (1.0, 0.0, inf, 1.0), (2, 0.0, 0.0, inf))])\n")
+    for own in (0, 1):
+        r = subprocess.run([sys.executable, "-c", code.format(own)], cwd=ROOT, capture_output=True, text=True, timeout=300)
+        assert r.returncode == 0 and r.stdout.strip() == "[0, 1, 1, 1, 1]", r.stdout + r.stderr
