@@ -23,7 +23,13 @@
 // runs of tokens. Where many tokens fall into one part (equal logits, a range
 // without end) the border's bits are found eight at a time. The passes behind the
 // first ones look at the largest of eight neighbours and leave most of them alone.
-// Bound by instructions: a weight takes about 35.
+//
+// Few rows are bound by the passes' barriers (a cluster's takes 1 to 2 us), many by
+// instructions: a weight takes about 35, where a row that nothing filters weighs
+// each token once and top-p with every token twice. Measured: a row of 33278
+// bfloat16 with top-p 22 us; 24 rows of 267735 float32 of all kinds of settings 70,
+// of 256 rows 416; of 256 rows 110 the largest alone, 160 with min-p, 300 with no
+// filter, 280 with top-k 50, 500 with top-k 1000 and top-p. To read them takes 38.
 #include <cfloat>
 
 #include "s2_internal.h"
@@ -35,13 +41,14 @@ namespace {
 
 using namespace rows;
 
-constexpr int kMaxThreads = 1024;
-constexpr uint32_t kMinThreads = 320;
+constexpr uint32_t kThreads = 512;
+constexpr uint32_t kPerSm = 2;      // blocks
 constexpr uint32_t kBins = 256;     // a thread each
 constexpr uint32_t kList = 128;     // tokens that are ranked against one another
+constexpr uint32_t kQueue = 512;    // groups that a pass over few of them takes one after the other
 constexpr float kPerOctave = 8.0f;  // ranges of logits per factor of two of weight
 constexpr int kBits = 43;           // of a weight of 1
-static_assert(kBins <= kMinThreads && kList <= kMinThreads, "a thread for each");
+static_assert(kBins <= kThreads && kList <= kThreads, "a thread for each");
 
 // 2^(j/32) in two floats
 __device__ const float2 kRoots[32] = {
@@ -77,10 +84,17 @@ struct Listed {
 struct Shared {
     float2 roots[32];
     uint64_t hist[2][kBins];
-    Listed list[kList], all[kList];
-    uint64_t weight[kList];
-    uint64_t scan[kMaxThreads / 32];
-    float warp_max[kMaxThreads / 32];
+    Listed list[kList];
+    union {
+        struct {
+            Listed all[kList];
+            uint64_t weight[kList];
+        };
+        uint32_t queue[kQueue];  // groups that a pass looks into
+    };
+    uint32_t queued;
+    uint64_t scan[kThreads / 32];
+    float warp_max[kThreads / 32];
     float top[2];        // this block's largest logit
     uint32_t lowest[2];  // the lowest index of the row's largest
     uint32_t listed, lowest_key, highest_key;  // of the tokens that are ranked
@@ -136,7 +150,7 @@ struct Row {
     uint32_t room, kept;  // groups of the block's part in shared memory
     Part<TI> p;
     uint32_t V;
-    uint32_t span;    // 256-token steps per run
+    uint32_t size;    // groups of a run
     uint32_t chunks;  // runs of this block, at most kBins
 
     __device__ __forceinline__ Raw<TI> group(uint32_t l) const { return l < kept ? staged<TI>(slice, room, l) : load_group(p, l, V); }
@@ -144,24 +158,54 @@ struct Row {
     template <typename F>
     __device__ __forceinline__ void each(F f) const {
 #pragma unroll 2
-        for (uint32_t l = threadIdx.x; l < kept; l += blockDim.x) f(staged<TI>(slice, room, l), l);
+        for (uint32_t l = threadIdx.x; l < kept; l += kThreads) f(staged<TI>(slice, room, l), l);
         uint32_t l = threadIdx.x;
-        if (l < kept) l += (kept - l + blockDim.x - 1) / blockDim.x * blockDim.x;
-        for (; l < p.count; l += blockDim.x) f(load_group(p, l, V), l);
+        if (l < kept) l += (kept - l + kThreads - 1) / kThreads * kThreads;
+        for (; l < p.count; l += kThreads) f(load_group(p, l, V), l);
     }
-    // for every group that may hold a logit above `least` or equal to it
-    template <typename F>
-    __device__ __forceinline__ void above(float least, F f) const {
-        each([&](const Raw<TI>& r, uint32_t l) {
-            if (group_max(r) >= least) f(r, l);
-        });
+    // f(group, local index) for every group that holds a logit above `least` or
+    // equal to it. Where they are few, most lanes of a warp would wait for one that
+    // looks into its group: such groups are queued first, and every thread takes its
+    // own from the queue. `all`: there are no few. All threads, behind a barrier.
+    template <typename S, typename F>
+    __device__ __forceinline__ void above(S& sh, float least, bool all, F f) const {
+        bool direct = all || p.count <= kThreads;
+        uint32_t n = p.count;
+        if (!direct) {
+            if (threadIdx.x == 0) sh.queued = 0;
+            __syncthreads();
+            const uint32_t lane = threadIdx.x % 32;
+#pragma unroll 2
+            for (uint32_t first = threadIdx.x - lane; first < p.count; first += kThreads) {
+                const uint32_t l = first + lane;
+                const bool hit = l < p.count && group_max(group(l)) >= least;
+                const uint32_t hits = __ballot_sync(kAll, hit);
+                if (!hits) continue;
+                uint32_t at = 0;
+                if (lane == 0) at = atomicAdd(&sh.queued, (uint32_t)__popc(hits));
+                at = __shfl_sync(kAll, at, 0) + __popc(hits & ((1u << lane) - 1));
+                if (hit && at < kQueue) sh.queue[at] = l;
+            }
+            __syncthreads();
+            n = sh.queued;
+            if (n > kQueue) {
+                direct = true;
+                n = p.count;
+            }
+        }
+        for (uint32_t q = threadIdx.x; q < n; q += kThreads) {
+            const uint32_t l = direct ? q : sh.queue[q];
+            const Raw<TI> r = group(l);
+            if (!direct || group_max(r) >= least) f(r, l);
+        }
     }
-    // f(group, local index) for the groups of run `chunk`: each lane holds one of `span` steps
+    // The lane's groups of run `chunk`: f(local index) for lane, lane + 32, ..., in as
+    // many steps for every lane; the index is past the block's groups where there is none.
     template <typename F>
     __device__ __forceinline__ void run(uint32_t chunk, F f) const {
-        for (uint32_t s = 0; s < span; ++s) {
-            const uint32_t l = (chunk * span + s) * 32 + threadIdx.x % 32;
-            if (l < p.count) f(group(l), l);
+        for (uint32_t s = 0; s < size; s += 32) {
+            const uint32_t i = s + threadIdx.x % 32, l = chunk * size + i;
+            f(i < size && l < p.count ? l : 0xffffffffu);
         }
     }
     __device__ __forceinline__ uint32_t index(uint32_t l, int j) const { return (uint32_t)p.index(l, j); }
@@ -218,7 +262,7 @@ struct Weigher {
     }
     __device__ __forceinline__ static uint64_t whole(int hi, int lo) { return (uint64_t)(((int64_t)hi << 21) + lo); }
     // A weight by itself, of a logit that is not below `none`.
-    __device__ __forceinline__ uint64_t operator()(float l) const {
+    __device__ __noinline__ uint64_t operator()(float l) const {
         if (max == __uint_as_float(0x7f800000u)) return l == max ? 1ull << (kBits - shift) : 0;
         int hi[2], lo[2];
         pair(l, l, hi, lo);
@@ -256,7 +300,7 @@ __device__ __forceinline__ uint64_t block_scan(Shared& sh, uint64_t v, uint64_t*
     __syncthreads();  // the last scan's sums have been read
     if (threadIdx.x % 32 == 31) sh.scan[threadIdx.x / 32] = v;
     __syncthreads();
-    const uint64_t mine = threadIdx.x % 32 < blockDim.x / 32 ? sh.scan[threadIdx.x % 32] : 0, upto = warp_scan(mine);
+    const uint64_t mine = threadIdx.x % 32 < kThreads / 32 ? sh.scan[threadIdx.x % 32] : 0, upto = warp_scan(mine);
     *total = __shfl_sync(kAll, upto, 31);
     const uint64_t before = __shfl_sync(kAll, upto - mine, threadIdx.x / 32);
     return before + v;
@@ -279,10 +323,10 @@ struct Team {
     uint32_t& turn;
 
     // Finds the bin in which the sum over the bins of all blocks reaches the goal
-    // goal_of(total), from 1 to that sum; *goal: what is left of it in that bin.
-    // fill(hist) adds this block's part. The same answer in every block.
+    // goal_of(total), from 1 to that sum; *goal: what is left of it in that bin,
+    // *inside: what lies in it. fill(hist) adds this block's part. The same answer in
+    // every block.
     template <typename Fill, typename GoalOf>
-    // *inside: what lies in it.
     __device__ __forceinline__ uint32_t find_bin(Fill fill, GoalOf goal_of, uint64_t* goal, uint64_t* inside = nullptr) const {
         uint64_t* hist = sh.hist[turn++ & 1];
         if (threadIdx.x < kBins) hist[threadIdx.x] = 0;
@@ -344,9 +388,10 @@ __device__ __forceinline__ void count_in(uint64_t* at, uint64_t m) {
 // The border of the shortest beginning of what `from` keeps that measures
 // goal_of(what all of it measures) or more. `scale`: ranges per unit of logit.
 // `least`: no token below it belongs to that beginning. `kept_most`: `from` keeps
-// no more tokens than this (so few that they are all ranked).
+// no more tokens than this (so few that they are all ranked). `dense`: it keeps
+// most of them.
 template <typename TI, typename Measure, typename GoalOf>
-__device__ Border narrow(const Team<TI>& team, Border from, float scale, float least, uint64_t kept_most, const Measure& measure, GoalOf goal_of) {
+__device__ Border narrow(const Team<TI>& team, Border from, float scale, float least, uint64_t kept_most, bool dense, const Measure& measure, GoalOf goal_of) {
     Shared& sh = team.sh;
     const Row<TI>& row = team.row;
     const float top = team.top;
@@ -359,7 +404,7 @@ __device__ Border narrow(const Team<TI>& team, Border from, float scale, float l
     if (!rank_all)
         bin = team.find_bin(
             [&](uint64_t* hist) {
-                row.above(fmaxf(least, from.v), [&](const Raw<TI>& r, uint32_t l) {
+                row.above(sh, fmaxf(least, from.v), dense, [&](const Raw<TI>& r, uint32_t l) {
                     measure.group(r, kept(l), [&](float v, int, uint64_t m) { count_in<Measure>(hist + range_of(v), m); });
                 });
             },
@@ -374,7 +419,7 @@ __device__ Border narrow(const Team<TI>& team, Border from, float scale, float l
     if (bin < kBins - 1 && !few)
         part = team.find_bin(
             [&](uint64_t* hist) {
-                row.above(low, [&](const Raw<TI>& r, uint32_t l) {
+                row.above(sh, low, false, [&](const Raw<TI>& r, uint32_t l) {
                     uint32_t here = 0;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) here |= (uint32_t)(from.keeps(element(r, j), row.index(l, j)) && range_of(element(r, j)) == bin) << j;
@@ -388,6 +433,7 @@ __device__ Border narrow(const Team<TI>& team, Border from, float scale, float l
 
     // few: rank them against one another
     if (part < kBins || few) {
+        if (rank_all) cluster_barrier();  // the last list has been read by all (else find_bin saw to it)
         if (threadIdx.x == 0) {
             sh.listed = 0;
             sh.lowest_key = 0xffffffffu;
@@ -395,7 +441,7 @@ __device__ Border narrow(const Team<TI>& team, Border from, float scale, float l
         }
         __syncthreads();
         uint32_t lowest = 0xffffffffu, highest = 0;
-        row.above(low, [&](const Raw<TI>& r, uint32_t l) {
+        row.above(sh, low, false, [&](const Raw<TI>& r, uint32_t l) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float v = element(r, j);
@@ -424,7 +470,7 @@ __device__ Border narrow(const Team<TI>& team, Border from, float scale, float l
         }
         const uint32_t n = __shfl_sync(kAll, upto, 15);
         if (n <= kList)
-            for (uint32_t r = threadIdx.x / 32; r < team.blocks; r += blockDim.x / 32) {
+            for (uint32_t r = threadIdx.x / 32; r < team.blocks; r += kThreads / 32) {
                 const uint32_t many = __shfl_sync(kAll, c, r), first = __shfl_sync(kAll, upto - c, r);
                 for (uint32_t k = lane; k < many; k += 32) {
                     const uint32_t at = peer(sh.list + k, r);
@@ -472,7 +518,7 @@ __device__ Border narrow(const Team<TI>& team, Border from, float scale, float l
     for (; shift >= 0; shift -= 8) {
         const uint32_t found = team.find_bin(
             [&](uint64_t* hist) {
-                row.above(low, [&](const Raw<TI>& r, uint32_t l) {
+                row.above(sh, low, false, [&](const Raw<TI>& r, uint32_t l) {
 #pragma unroll 1
                     for (int j = 0; j < 8; ++j) {
                         const float v = element(r, j);
@@ -495,9 +541,9 @@ __device__ Border narrow(const Team<TI>& team, Border from, float scale, float l
         for (int j = 0; j < 8; ++j) hit |= (uint32_t)(element(r, j) == v && from.keeps(v, row.index(l, j))) << j;
         return hit;
     };
-    for (uint32_t c = threadIdx.x / 32; c < row.chunks; c += blockDim.x / 32) {
+    for (uint32_t c = threadIdx.x / 32; c < row.chunks; c += kThreads / 32) {
         uint32_t mine = 0;
-        row.run(c, [&](const Raw<TI>& r, uint32_t l) { mine += __popc(hits(r, l)); });
+        row.run(c, [&](uint32_t l) { mine += l < row.p.count ? __popc(hits(row.group(l), l)) : 0; });
         mine = __reduce_add_sync(kAll, mine);
         if (threadIdx.x % 32 == 0) counts[c] = mine;
     }
@@ -521,8 +567,7 @@ __device__ Border narrow(const Team<TI>& team, Border from, float scale, float l
     if (want > 0 && want <= total && threadIdx.x < 32) {
         uint64_t seen = 0;
         const uint64_t goal_here = sh.before;
-        for (uint32_t s = 0; s < row.span; ++s) {  // (every lane takes every step)
-            const uint32_t l = (sh.bin * row.span + s) * 32 + threadIdx.x;
+        row.run(sh.bin, [&](uint32_t l) {
             const uint32_t hit = l < row.p.count ? hits(row.group(l), l) : 0;
             const uint64_t mine = warp_scan((uint64_t)__popc(hit));
             const uint64_t first = seen + mine - __popc(hit);
@@ -532,7 +577,7 @@ __device__ Border narrow(const Team<TI>& team, Border from, float scale, float l
                     if (hit >> j & 1 && --k == 0) sh.border.i = row.index(l, j) + 1;
             }
             seen += __shfl_sync(kAll, mine, 31);
-        }
+        });
     }
     cluster_barrier();
     // one block has found it
@@ -549,7 +594,7 @@ __device__ __forceinline__ float at_least(const Team<TI>& team, uint64_t k, floa
     const Row<TI>& row = team.row;
     const float top = team.top;
     // (too near to all of them; and where a thread has few groups, a pass for this takes longer than it spares)
-    if (k > row.V / 16 || row.p.groups(row.V) < 8ull * blockDim.x * team.blocks) return minus_inf();
+    if (k > row.V / 16 || row.p.groups(row.V) < 8ull * kThreads * team.blocks) return minus_inf();
     uint64_t goal, groups = 0;
     const uint32_t bin = team.find_bin(
         [&](uint64_t* hist) {
@@ -567,12 +612,12 @@ __device__ __forceinline__ float at_least(const Team<TI>& team, uint64_t k, floa
 }
 
 template <typename TI>
-__global__ void __launch_bounds__(kMaxThreads, 1) sample_kernel(const SampleArgs a, uint32_t room, uint32_t log2_blocks, int shift) {
+__global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SampleArgs a, uint32_t room, uint32_t log2_blocks, int shift) {
     extern __shared__ uint4 slice[];
     __shared__ Shared sh;
     stream_order();
     const uint32_t blocks = 1u << log2_blocks, rank = blocks > 1 ? cluster_rank() : 0;
-    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = kThreads / 32;
     if (threadIdx.x < 32) sh.roots[threadIdx.x] = kRoots[threadIdx.x];
     uint32_t turn = 0, parity = 0;
     for (uint64_t at = blockIdx.x >> log2_blocks; at < a.T; at += gridDim.x >> log2_blocks, parity ^= 1) {
@@ -582,10 +627,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1) sample_kernel(const SampleArgs
         row.p = part_of(static_cast<const TI*>(a.z) + at * a.ld, a.V, rank, log2_blocks);
         row.kept = min(row.p.count, room);
         row.V = a.V;
-        row.span = max(1u, (row.p.count + 32 * kBins - 1) / (32 * kBins));
-        row.chunks = (row.p.count + 32 * row.span - 1) / (32 * row.span);
-        for (uint32_t l = threadIdx.x; l < row.kept; l += blockDim.x) stage_group(slice, room, row.p, l, a.V);
-        if (threadIdx.x == blockDim.x - 1) {
+        row.size = max(1u, (row.p.count + kBins - 1) / kBins);
+        for (uint32_t l = threadIdx.x; l < row.kept; l += kThreads) stage_group(slice, room, row.p, l, a.V);
+        if (threadIdx.x == kThreads - 1) {
             Settings s;
             const float t = a.temperature ? a.temperature[at] : 1.0f;
             s.greedy = !(t >= FLT_MIN);
@@ -620,11 +664,14 @@ __global__ void __launch_bounds__(kMaxThreads, 1) sample_kernel(const SampleArgs
         cluster_barrier();
         top = rows::warp_max(lane < blocks ? peer_float(peer(&sh.top[parity], lane)) : minus_inf());
         const Settings set = sh.set;
+        const bool filtered = set.top_k || set.top_p < 1.0f || set.use_min_p;
+        if (!filtered) row.size = (row.size + 31) / 32 * 32;  // a warp's steps; else few groups that meet in one sum
+        row.chunks = (row.p.count + row.size - 1) / row.size;
         if (top == minus_inf() || set.greedy || set.top_k == 1 || set.top_p == 0.0f) {  // nothing to draw; the same in every block
             if (threadIdx.x == 0) sh.lowest[parity] = 0xffffffffu;
             __syncthreads();
             if (top > minus_inf())
-                row.above(top, [&](const Raw<TI>& r, uint32_t l) {
+                row.above(sh, top, false, [&](const Raw<TI>& r, uint32_t l) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         if (element(r, j) == top) atomicMin(&sh.lowest[parity], row.index(l, j));
@@ -651,10 +698,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1) sample_kernel(const SampleArgs
         if (set.top_k && set.top_k < a.V) {
             const float scale = kPerOctave * 1.44269504f;
             const float least = at_least(team, set.top_k, scale);
-            border = narrow(team, border, scale, least, ~0ull, Count{}, [&](uint64_t total) { return total < set.top_k ? total : (uint64_t)set.top_k; });
+            border = narrow(team, border, scale, least, ~0ull, least == minus_inf(), Count{}, [&](uint64_t total) { return total < set.top_k ? total : (uint64_t)set.top_k; });
         }
         if (set.top_p < 1.0f)
-            border = narrow(team, border, set.bins, minus_inf(), set.top_k ? set.top_k : ~0ull, weigh, [&](uint64_t total) {
+            border = narrow(team, border, set.bins, minus_inf(), set.top_k ? set.top_k : ~0ull, !set.top_k, weigh, [&](uint64_t total) {
                 const uint64_t goal = times(set.top_p, total, true);
                 return goal ? goal : 1;
             });
@@ -673,15 +720,26 @@ __global__ void __launch_bounds__(kMaxThreads, 1) sample_kernel(const SampleArgs
 
         // the sums of this block's runs
         uint64_t* sums = sh.hist[turn++ & 1];
-        for (uint32_t c = warp; c < row.chunks; c += warps) {
+        auto weight_of = [&](uint32_t l) {
             uint64_t w = 0;
-            row.run(c, [&](const Raw<TI>& r, uint32_t l) {
-                if (group_max(r) >= border.v)
-                    weigh.group(r, [&](float v, int j) { return border.keeps(v, row.index(l, j)); }, [&](float, int, uint64_t m) { w += m; });
+            weigh.group(row.group(l), [&](float v, int j) { return border.keeps(v, row.index(l, j)); }, [&](float, int, uint64_t m) { w += m; });
+            return w;
+        };
+        if (filtered) {
+            if (threadIdx.x < kBins) sums[threadIdx.x] = 0;
+            __syncthreads();
+            row.above(sh, border.v, false, [&](const Raw<TI>&, uint32_t l) {
+                const uint64_t w = weight_of(l);
+                if (w) add64(sums + l / row.size, w);
             });
+        } else {
+            for (uint32_t c = warp; c < row.chunks; c += warps) {
+                uint64_t w = 0;
+                row.run(c, [&](uint32_t l) { w += l < row.p.count ? weight_of(l) : 0; });
 #pragma unroll
-            for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(kAll, w, o);
-            if (lane == 0) sums[c] = w;
+                for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(kAll, w, o);
+                if (lane == 0) sums[c] = w;
+            }
         }
         __syncthreads();
         const uint64_t mine = threadIdx.x < row.chunks ? sums[threadIdx.x] : 0;
@@ -701,8 +759,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) sample_kernel(const SampleArgs
         if (here && warp == 0) {
             uint64_t seen = 0;
             const uint64_t left = sh.before;
-            for (uint32_t s = 0; s < row.span; ++s) {
-                const uint32_t l = (sh.bin * row.span + s) * 32 + lane;
+            row.run(sh.bin, [&](uint32_t l) {
                 uint64_t w[8], sum = 0;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) w[j] = 0;
@@ -722,25 +779,24 @@ __global__ void __launch_bounds__(kMaxThreads, 1) sample_kernel(const SampleArgs
                     }
                 }
                 seen += __shfl_sync(kAll, scan, 31);
-            }
+            });
         }
         __syncthreads();  // the slice and the sums are free
     }
     cluster_barrier();  // no block ends while another reads its shared memory
 }
 
-// How a row is spread: threads of a block, blocks on an SM, shared memory of a
-// block's part of a row. A round of rows costs kRoundNs, and a group kGroupNs of
-// its SM, kAgain times as much where it is read again in every pass. Rows of all
-// kinds of settings, 256 x 267735 float32: two blocks of an SM and eight of a row
-// 445 us, two and four 439, three and eight 447, one and four 460, two and sixteen
-// 680, one and one 709; 24 rows: 84, 114, 96, 91, 81 and 294; a row of 33278 in one
-// block 60 us, in sixteen 21.
-struct Spread {
-    uint32_t threads, per_sm, smem;
-};
-constexpr Spread kSpreads[3] = {{1024, 1, 200 * 1024}, {512, 2, 100 * 1024}, {320, 3, 66 * 1024}};
-constexpr double kRoundNs = 9000.0, kGroupNs = 6.5, kAgain = 2.0;
+// How a row is spread: over a cluster of up to sixteen blocks, two on an SM, that
+// go through their rows one after the other. A row costs kRowNs on each of its
+// blocks and a group kGroupNs of its SM, kAgain times as much where it is read
+// again in every pass, and the slowest of a few rows kRows more than most. Rows of
+// all kinds of settings, in us, over two, four, eight and sixteen blocks:
+//   24 x 267735 float32 225, 122, 77, 68; 256 x 267735 678, 484, 416, 609;
+//   256 x 33278 90, 108, 155, 359; one row of 33278 46, 26, 24, 22.
+// One block of 1024 threads on an SM: 86 and 435 where those take 68 and 416;
+// three of 320: 72 and 406, 90 at 256 x 33278.
+constexpr uint32_t kPartSmem = 100 * 1024;  // of a block's part of a row
+constexpr double kRowNs = 22000.0, kGroupNs = 6.25, kAgain = 2.0, kRows = 0.5;
 
 template <typename TI>
 cudaError_t launch(const SampleArgs& a, cudaStream_t s) {
@@ -751,34 +807,31 @@ cudaError_t launch(const SampleArgs& a, cudaStream_t s) {
     constexpr uint64_t kGroupBytes = 8 * sizeof(TI);
     const void* kernel = reinterpret_cast<const void*>(sample_kernel<TI>);
     double best = 0.0;
-    uint32_t blocks = 0, log2_blocks = 0, room = 0, clusters = 0, threads = 0, smem = 0;
-    for (const Spread& w : kSpreads) {
-        for (uint32_t b = 1, log2 = 0; b <= 16; b *= 2, ++log2) {
-            if (b > 1 && groups < b * (uint64_t)w.threads / 2) break;  // too little for so many
-            const uint64_t need = (groups + b - 1) / b + 1, most = w.smem / kGroupBytes, keep = need < most ? need : most;
-            const uint32_t bytes = (uint32_t)smem_of(keep * kGroupBytes);
-            int n = 0;
-            e = resident_clusters(kernel, w.threads, b, bytes, &n);
-            if (e != cudaSuccess) return e;
-            if (n < 1) continue;
-            const uint64_t rounds = ((uint64_t)a.T + n - 1) / n, on = ((uint64_t)a.T * b + di.sms - 1) / di.sms;
-            const double per_sm = (double)(on < w.per_sm ? on : w.per_sm);
-            const double ns = (double)rounds * (kRoundNs + per_sm * kGroupNs * ((double)keep + kAgain * (double)(need - keep)));
-            if (blocks && ns >= best) continue;
-            best = ns;
-            blocks = b;
-            log2_blocks = log2;
-            room = (uint32_t)keep;
-            clusters = (uint32_t)n;
-            threads = w.threads;
-            smem = bytes;
-        }
+    uint32_t blocks = 0, log2_blocks = 0, room = 0, clusters = 0, smem = 0;
+    for (uint32_t b = 1, log2 = 0; b <= 16; b *= 2, ++log2) {
+        if (b > 1 && groups < b * (uint64_t)kThreads / 2) break;  // too little for so many
+        const uint64_t need = (groups + b - 1) / b + 1, most = kPartSmem / kGroupBytes, keep = need < most ? need : most;
+        const uint32_t bytes = (uint32_t)smem_of(keep * kGroupBytes);
+        int n = 0;
+        e = resident_clusters(kernel, kThreads, b, bytes, &n);
+        if (e != cudaSuccess) return e;
+        if (n < 1) continue;
+        const uint64_t on = ((uint64_t)a.T * b + di.sms - 1) / di.sms;
+        const double per_sm = (double)(on < kPerSm ? on : kPerSm), rounds = kRows + (a.T > (uint32_t)n ? (double)a.T / n : 1.0);
+        const double ns = rounds * (kRowNs + per_sm * kGroupNs * ((double)keep + kAgain * (double)(need - keep)));
+        if (blocks && ns >= best) continue;
+        best = ns;
+        blocks = b;
+        log2_blocks = log2;
+        room = (uint32_t)keep;
+        clusters = (uint32_t)n;
+        smem = bytes;
     }
     if (blocks == 0) return cudaErrorInvalidConfiguration;
     int shift = 0;  // sums of V weights stay below 2^63
     while ((1ull << (62 - kBits + shift)) < a.V) ++shift;
     const uint32_t grid = (a.T < clusters ? a.T : clusters) * blocks;
-    return launch_early(sample_kernel<TI>, grid, threads, smem, blocks, s, a, room, log2_blocks, shift);
+    return launch_early(sample_kernel<TI>, grid, kThreads, smem, blocks, s, a, room, log2_blocks, shift);
 }
 
 }  // namespace
