@@ -469,7 +469,9 @@ S2_API s2_status s2_wgrad8(const void *dy, uint64_t lddy, const uint8_t *x, uint
  * (r/128) * ceil(cols/128) + j/4. Bytes of rows and blocks past the end exist
  * and are not 255 (s2_pack4 writes 127). s2_pack4_scales_size gives their
  * number, 512 * ceil(rows/128) * ceil(cols/128); base 16-byte aligned.
- * Sizes up to 2^31 - 1, strides as in the 8-bit layer. A size of zero is valid.
+ * Sizes up to 2^31 - 1, strides as in the 8-bit layer; fewer than 2^30 tiles to
+ * a matrix that is packed or unpacked (S2_ERR_UNSUPPORTED). A size of zero is
+ * valid.
  * Make the first s2_matmul4 on a device before any stream capture (it looks up
  * an address there).
  */
@@ -511,9 +513,9 @@ S2_API s2_status s2_matmul4(const uint8_t *x, uint64_t ldx, const uint8_t *x_sca
  *   negative ones and NaN for 0).
  *   Settings of each row, arrays of T, or null where no row uses one:
  *   temperature float32 (null: 1; 0, negative, NaN or below 2^-126: the row's
- *   largest logit is taken, the lowest index of equals), top_k int32 (below 1: off), top_p
- *   float32 (1 or more, or NaN: off; 0 or less: one token), min_p float32 (0
- *   or less, or NaN: off; more than 1: 1).
+ *   largest logit is taken, the lowest index of equals), top_k int32 (below 1:
+ *   off), top_p float32 (1 or more, or NaN: off; 0 or less: one token), min_p
+ *   float32 (0 or less, or NaN: off; more than 1: 1).
  *   With l_max the row's largest logit a token's weight is exp((l - l_max) /
  *   temperature). The tokens are ordered by logit, the largest first, equal
  *   ones by index; top-k keeps the first top_k; top-p keeps the shortest
@@ -563,10 +565,12 @@ typedef struct {
  *   else has probability 0 everywhere. NaN and +infinity make a row NaN (the
  *   teacher's: its loss, and the gradient at its entries).
  *   A term of weight 0 is left out. Sums are float32; the result does not
- *   depend on timing. K at most
- *   S2_DISTILL_MAX_ENTRIES, T and V below 2^31 (S2_ERR_UNSUPPORTED).
- *   dlogits may not overlap logits. Fastest where logits and dlogits start on
- *   32 bytes and have the same row stride.
+ *   depend on timing (a row's last bits do on its address modulo eight
+ *   elements, on its place among the others and on T). K at most S2_DISTILL_MAX_ENTRIES (fastest up to 256), T
+ *   and V below 2^31 (S2_ERR_UNSUPPORTED). dlogits may not overlap logits.
+ *   Fastest where logits and dlogits start on 32 bytes and have the same row
+ *   stride. Make the first call on a device before any stream capture (it
+ *   looks up an address there).
  */
 #define S2_DISTILL_MAX_ENTRIES 8192u
 S2_API s2_status s2_distill(const void *logits, s2_dtype dt, uint64_t T, uint64_t V, uint64_t ld,
@@ -575,9 +579,10 @@ S2_API s2_status s2_distill(const void *logits, s2_dtype dt, uint64_t T, uint64_
                             uint64_t ldd, s2_stream_t stream);
 
 /*
- * s2_wait_faults -- how many waits inside s2_matmul8, s2_wgrad8 and
- * s2_matmul4 kernels ran out on the current device since the library was loaded (0 unless
- * something is broken; outputs of the call concerned are not valid then).
+ * s2_wait_faults -- how many waits inside s2_matmul8, s2_wgrad8, s2_matmul4
+ * and s2_distill kernels ran out on the current device since the library was
+ * loaded (0 unless something is broken; outputs of the call concerned are not
+ * valid then).
  * host_count is HOST memory; this call, a diagnostic, waits for the device.
  */
 S2_API s2_status s2_wait_faults(uint32_t *host_count);
