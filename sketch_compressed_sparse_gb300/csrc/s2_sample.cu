@@ -45,10 +45,10 @@ constexpr uint32_t kThreads = 512;
 constexpr uint32_t kPerSm = 2;      // blocks
 constexpr uint32_t kBins = 256;     // a thread each
 constexpr uint32_t kList = 128;     // tokens that are ranked against one another
-constexpr uint32_t kQueue = 512;    // groups that a pass over few of them takes one after the other
+constexpr uint32_t kQueue = 512;    // groups that a pass over few of them takes
 constexpr float kPerOctave = 8.0f;  // ranges of logits per factor of two of weight
 constexpr int kBits = 43;           // of a weight of 1
-static_assert(kBins <= kThreads && kList <= kThreads, "a thread for each");
+static_assert(kBins <= kThreads && kList <= kThreads && kQueue <= kThreads, "a thread for each");
 
 // 2^(j/32) in two floats
 __device__ const float2 kRoots[32] = {
@@ -91,6 +91,7 @@ struct Shared {
             uint64_t weight[kList];
         };
         uint32_t queue[kQueue];  // groups that a pass looks into
+        float picked[kThreads / 32][64];
     };
     uint32_t queued;
     uint64_t scan[kThreads / 32];
@@ -99,7 +100,7 @@ struct Shared {
     uint32_t lowest[2];  // the lowest index of the row's largest
     uint32_t listed, lowest_key, highest_key;  // of the tokens that are ranked
     uint64_t total;      // weight kept in this block
-    Settings set;
+    Settings set[2];     // of this row and the next
     uint64_t before, inside;  // of the bin that was found
     uint32_t bin;
     Listed border;
@@ -140,7 +141,7 @@ __device__ uint64_t times(float f, uint64_t z, bool up) {
 struct Border {
     float v;
     uint32_t i;
-    __device__ __forceinline__ bool keeps(float x, uint32_t at) const { return x > v || (x == v && at < i); }
+    __device__ __forceinline__ bool keeps(float x, uint32_t at) const { return (x > v) | ((x == v) & (at < i)); }
 };
 
 // A row as the blocks of a cluster share it.
@@ -163,6 +164,28 @@ struct Row {
         if (l < kept) l += (kept - l + kThreads - 1) / kThreads * kThreads;
         for (; l < p.count; l += kThreads) f(load_group(p, l, V), l);
     }
+    // Queues the groups that hold a logit above `least` or equal to it; their
+    // number, more than kQueue where not all have a place. All threads, behind a
+    // barrier.
+    template <typename S>
+    __device__ __forceinline__ uint32_t queue_up(S& sh, float least) const {
+        if (threadIdx.x == 0) sh.queued = 0;
+        __syncthreads();
+        const uint32_t lane = threadIdx.x % 32;
+#pragma unroll 2
+        for (uint32_t first = threadIdx.x - lane; first < p.count; first += kThreads) {
+            const uint32_t l = first + lane;
+            const bool hit = l < p.count && group_max(group(l)) >= least;
+            const uint32_t hits = __ballot_sync(kAll, hit);
+            if (!hits) continue;
+            uint32_t at = 0;
+            if (lane == 0) at = atomicAdd(&sh.queued, (uint32_t)__popc(hits));
+            at = __shfl_sync(kAll, at, 0) + __popc(hits & ((1u << lane) - 1));
+            if (hit && at < kQueue) sh.queue[at] = l;
+        }
+        __syncthreads();
+        return sh.queued;
+    }
     // f(group, local index) for every group that holds a logit above `least` or
     // equal to it. Where they are few, most lanes of a warp would wait for one that
     // looks into its group: such groups are queued first, and every thread takes its
@@ -170,34 +193,52 @@ struct Row {
     template <typename S, typename F>
     __device__ __forceinline__ void above(S& sh, float least, bool all, F f) const {
         bool direct = all || p.count <= kThreads;
-        uint32_t n = p.count;
-        if (!direct) {
-            if (threadIdx.x == 0) sh.queued = 0;
-            __syncthreads();
-            const uint32_t lane = threadIdx.x % 32;
-#pragma unroll 2
-            for (uint32_t first = threadIdx.x - lane; first < p.count; first += kThreads) {
-                const uint32_t l = first + lane;
-                const bool hit = l < p.count && group_max(group(l)) >= least;
-                const uint32_t hits = __ballot_sync(kAll, hit);
-                if (!hits) continue;
-                uint32_t at = 0;
-                if (lane == 0) at = atomicAdd(&sh.queued, (uint32_t)__popc(hits));
-                at = __shfl_sync(kAll, at, 0) + __popc(hits & ((1u << lane) - 1));
-                if (hit && at < kQueue) sh.queue[at] = l;
-            }
-            __syncthreads();
-            n = sh.queued;
-            if (n > kQueue) {
-                direct = true;
-                n = p.count;
-            }
-        }
+        uint32_t n = direct ? 0 : queue_up(sh, least);
+        if (n > kQueue) direct = true;
+        if (direct) n = p.count;
         for (uint32_t q = threadIdx.x; q < n; q += kThreads) {
             const uint32_t l = direct ? q : sh.queue[q];
             const Raw<TI> r = group(l);
             if (!direct || group_max(r) >= least) f(r, l);
         }
+    }
+    // f(logit) for every one of the block's for which pick(logit, index) holds, all of
+    // them at `least` or above: where they are some in a hundred and f takes long, 32
+    // are collected at a time. All threads.
+    template <typename S, typename Pick, typename F>
+    __device__ __forceinline__ void picked(S& sh, float least, Pick pick, F f) const {
+        const uint32_t lane = threadIdx.x % 32;
+        float* mine = sh.picked[threadIdx.x / 32];
+        uint32_t n = 0;
+        for (uint32_t first = threadIdx.x - lane; first < p.count; first += kThreads) {
+            const uint32_t l = first + lane;
+            Raw<TI> r{};
+            uint32_t here = 0;
+            if (l < p.count) {
+                r = group(l);
+                if (group_max(r) >= least) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) here |= (uint32_t)pick(element(r, j), index(l, j)) << j;
+                }
+            }
+            if (!__any_sync(kAll, here)) continue;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const bool hit = here >> j & 1;
+                const uint32_t hits = __ballot_sync(kAll, hit);
+                if (hit) mine[n + __popc(hits & ((1u << lane) - 1))] = element(r, j);
+                n += __popc(hits);
+                if (n < 32) continue;
+                __syncwarp();
+                f(mine[lane]);
+                const float rest = mine[32 + lane];
+                __syncwarp();
+                n -= 32;
+                if (lane < n) mine[lane] = rest;
+            }
+        }
+        __syncwarp();
+        if (lane < n) f(mine[lane]);
     }
     // The lane's groups of run `chunk`: f(local index) for lane, lane + 32, ..., in as
     // many steps for every lane; the index is past the block's groups where there is none.
@@ -268,7 +309,7 @@ struct Weigher {
         pair(l, l, hi, lo);
         return whole(hi[0], lo[0]);
     }
-    // Of a group: f(element, weight) where use(element) holds.
+    // Of a group: f(element, its number, weight), a weight of 0 where use(element, number) does not hold.
     template <typename TI, typename Use, typename F>
     __device__ __forceinline__ void group(const Raw<TI>& r, Use use, F f) const {
         if (max == __uint_as_float(0x7f800000u)) {
@@ -282,7 +323,7 @@ struct Weigher {
         for (int j = 0; j < 8; j += 2) pair(element(r, j), element(r, j + 1), hi + j, lo + j);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (use(element(r, j), j)) f(element(r, j), j, whole(hi[j], lo[j]));
+            f(element(r, j), j, use(element(r, j), j) ? whole(hi[j], lo[j]) : 0);
     }
 };
 
@@ -306,11 +347,27 @@ __device__ __forceinline__ uint64_t block_scan(Shared& sh, uint64_t v, uint64_t*
     return before + v;
 }
 
+// Adds to a sum in shared memory, nothing where v is 0. (No branches: most lanes add.)
 __device__ __forceinline__ void add64(uint64_t* at, uint64_t v) {
-    uint32_t* w = reinterpret_cast<uint32_t*>(at);
-    const uint32_t lo = (uint32_t)v, old = atomicAdd(w, lo);
-    const uint32_t hi = (uint32_t)(v >> 32) + (old + lo < old);
-    if (hi) atomicAdd(w + 1, hi);
+    asm volatile(
+        "{.reg .pred p; .reg .u32 lo, hi, old, sum;\n"
+        "mov.b64 {lo, hi}, %1;\n"
+        "setp.ne.u32 p, lo, 0;\n"
+        "mov.u32 old, 0;\n"
+        "@p atom.shared.add.u32 old, [%0], lo;\n"
+        "add.cc.u32 sum, old, lo;\n"
+        "addc.u32 hi, hi, 0;\n"
+        "setp.ne.u32 p, hi, 0;\n"
+        "@p red.shared.add.u32 [%0 + 4], hi;}" ::"r"((uint32_t)__cvta_generic_to_shared(at)),
+        "l"(v)
+        : "memory");
+}
+__device__ __forceinline__ void count32(uint64_t* at, uint32_t v) {  // (a block has fewer than 2^32)
+    asm volatile(
+        "{.reg .pred p; setp.ne.u32 p, %1, 0;\n"
+        "@p red.shared.add.u32 [%0], %1;}" ::"r"((uint32_t)__cvta_generic_to_shared(at)),
+        "r"(v)
+        : "memory");
 }
 
 // What a row's threads share and agree on.
@@ -370,7 +427,7 @@ struct Count {
     __device__ __forceinline__ void group(const Raw<TI>& r, Use use, F f) const {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (use(element(r, j), j)) f(element(r, j), j, (uint64_t)1);
+            f(element(r, j), j, (uint64_t)use(element(r, j), j));
     }
 };
 struct Weigh : Weigher {
@@ -378,11 +435,8 @@ struct Weigh : Weigher {
 };
 template <typename Measure>
 __device__ __forceinline__ void count_in(uint64_t* at, uint64_t m) {
-    if (Measure::kWeighed) {
-        if (m) add64(at, m);
-    } else {
-        atomicAdd(reinterpret_cast<uint32_t*>(at), 1u);  // (a block has fewer than 2^32)
-    }
+    if (Measure::kWeighed) add64(at, m);
+    else count32(at, (uint32_t)m);
 }
 
 // The border of the shortest beginning of what `from` keeps that measures
@@ -419,17 +473,12 @@ __device__ Border narrow(const Team<TI>& team, Border from, float scale, float l
     if (bin < kBins - 1 && !few)
         part = team.find_bin(
             [&](uint64_t* hist) {
-                row.above(sh, low, false, [&](const Raw<TI>& r, uint32_t l) {
-                    uint32_t here = 0;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) here |= (uint32_t)(from.keeps(element(r, j), row.index(l, j)) && range_of(element(r, j)) == bin) << j;
-                    if (here)
-                        measure.group(r, [&](float, int j) { return here >> j & 1; },
-                                      [&](float v, int, uint64_t m) { count_in<Measure>(hist + part_of_range(v), m); });
-                });
+                auto in_bin = [&](float v, uint32_t i) { return from.keeps(v, i) & (range_of(v) == bin); };
+                auto add = [&](float v) { count_in<Measure>(hist + part_of_range(v), measure(v)); };
+                row.picked(sh, low, in_bin, add);
             },
             left, &goal);
-    auto member = [&](float v) { return rank_all || (range_of(v) == bin && (part == kBins || part_of_range(v) == part)); };
+    auto member = [&](float v) { return rank_all | ((range_of(v) == bin) & ((part == kBins) | (part_of_range(v) == part))); };
 
     // few: rank them against one another
     if (part < kBins || few) {
@@ -446,7 +495,7 @@ __device__ Border narrow(const Team<TI>& team, Border from, float scale, float l
             for (int j = 0; j < 8; ++j) {
                 const float v = element(r, j);
                 const uint32_t i = row.index(l, j);
-                if (!from.keeps(v, i) || !member(v)) continue;
+                if (!(from.keeps(v, i) & member(v))) continue;
                 const uint32_t at = atomicAdd(&sh.listed, 1u), k = key_of(v);
                 if (at < kList) sh.list[at] = {v, i};
                 lowest = min(lowest, k);
@@ -620,15 +669,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SampleAr
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = kThreads / 32;
     if (threadIdx.x < 32) sh.roots[threadIdx.x] = kRoots[threadIdx.x];
     uint32_t turn = 0, parity = 0;
-    for (uint64_t at = blockIdx.x >> log2_blocks; at < a.T; at += gridDim.x >> log2_blocks, parity ^= 1) {
-        Row<TI> row;
-        row.slice = slice;
-        row.room = room;
-        row.p = part_of(static_cast<const TI*>(a.z) + at * a.ld, a.V, rank, log2_blocks);
-        row.kept = min(row.p.count, room);
-        row.V = a.V;
-        row.size = max(1u, (row.p.count + kBins - 1) / kBins);
-        for (uint32_t l = threadIdx.x; l < row.kept; l += kThreads) stage_group(slice, room, row.p, l, a.V);
+    const uint64_t step = gridDim.x >> log2_blocks;
+    auto part = [&](uint64_t at) { return part_of(static_cast<const TI*>(a.z) + at * a.ld, a.V, rank, log2_blocks); };
+    // Row `at` on its way to shared memory, and its settings.
+    auto begin = [&](uint64_t at, uint32_t slot) {
+        if (at >= a.T) return;
+        const Part<TI> p = part(at);
+        const uint32_t kept = min(p.count, room);
+        for (uint32_t l = threadIdx.x; l < kept; l += kThreads) stage_group(slice, room, p, l, a.V);
         if (threadIdx.x == kThreads - 1) {
             Settings s;
             const float t = a.temperature ? a.temperature[at] : 1.0f;
@@ -647,8 +695,18 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SampleAr
             s.min_p = s.use_min_p ? (double)t * log((double)fminf(m, 1.0f)) : 0.0;
             const float u = a.u[at];
             s.u = u > 0.0f ? fminf(u, 1.0f - FLT_EPSILON / 2) : 0.0f;
-            sh.set = s;
+            sh.set[slot] = s;
         }
+    };
+    begin(blockIdx.x >> log2_blocks, 0);
+    for (uint64_t at = blockIdx.x >> log2_blocks; at < a.T; at += step, parity ^= 1) {
+        Row<TI> row;
+        row.slice = slice;
+        row.room = room;
+        row.p = part(at);
+        row.kept = min(row.p.count, room);
+        row.V = a.V;
+        row.size = max(1u, (row.p.count + kBins - 1) / kBins);
         copies_done();
 
         // the largest logit
@@ -663,9 +721,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SampleAr
         }
         cluster_barrier();
         top = rows::warp_max(lane < blocks ? peer_float(peer(&sh.top[parity], lane)) : minus_inf());
-        const Settings set = sh.set;
+        const Settings set = sh.set[parity];
         const bool filtered = set.top_k || set.top_p < 1.0f || set.use_min_p;
-        if (!filtered) row.size = (row.size + 31) / 32 * 32;  // a warp's steps; else few groups that meet in one sum
         row.chunks = (row.p.count + row.size - 1) / row.size;
         if (top == minus_inf() || set.greedy || set.top_k == 1 || set.top_p == 0.0f) {  // nothing to draw; the same in every block
             if (threadIdx.x == 0) sh.lowest[parity] = 0xffffffffu;
@@ -677,6 +734,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SampleAr
                         if (element(r, j) == top) atomicMin(&sh.lowest[parity], row.index(l, j));
                 });
             cluster_barrier();
+            begin(at + step, parity ^ 1);
             if (rank == 0 && warp == 0) {
                 const uint32_t i = __reduce_min_sync(kAll, lane < blocks ? peer_u32(peer(&sh.lowest[parity], lane)) : 0xffffffffu);
                 if (lane == 0) a.tokens[at] = (int32_t)i;  // -1 where there is none
@@ -720,28 +778,39 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SampleAr
 
         // the sums of this block's runs
         uint64_t* sums = sh.hist[turn++ & 1];
-        auto weight_of = [&](uint32_t l) {
+        auto sum_of = [&](const Raw<TI>& r, auto use) {
             uint64_t w = 0;
-            weigh.group(row.group(l), [&](float v, int j) { return border.keeps(v, row.index(l, j)); }, [&](float, int, uint64_t m) { w += m; });
+            weigh.group(r, use, [&](float, int, uint64_t m) { w += m; });
             return w;
         };
-        if (filtered) {
+        auto kept = [&](uint32_t l) { return [&row, &border, l](float v, int j) { return border.keeps(v, row.index(l, j)); }; };
+        const bool small = row.p.count <= kThreads;
+        const uint32_t few = small ? row.p.count : filtered ? row.queue_up(sh, border.v) : kQueue + 1;
+        if (few <= kQueue) {
             if (threadIdx.x < kBins) sums[threadIdx.x] = 0;
             __syncthreads();
-            row.above(sh, border.v, false, [&](const Raw<TI>&, uint32_t l) {
-                const uint64_t w = weight_of(l);
-                if (w) add64(sums + l / row.size, w);
-            });
-        } else {
-            for (uint32_t c = warp; c < row.chunks; c += warps) {
-                uint64_t w = 0;
-                row.run(c, [&](uint32_t l) { w += l < row.p.count ? weight_of(l) : 0; });
-#pragma unroll
-                for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(kAll, w, o);
-                if (lane == 0) sums[c] = w;
+            if (threadIdx.x < few) {
+                const uint32_t l = small ? threadIdx.x : sh.queue[threadIdx.x];
+                add64(sums + l / row.size, sum_of(row.group(l), kept(l)));
             }
+        } else {  // many groups that would meet in one sum: a warp's steps are a run's
+            row.size = (row.size + 31) / 32 * 32;
+            row.chunks = (row.p.count + row.size - 1) / row.size;
+            auto runs = [&](auto use) {
+                for (uint32_t c = warp; c < row.chunks; c += warps) {
+                    uint64_t w = 0;
+                    row.run(c, [&](uint32_t l) { w += l < row.p.count ? sum_of(row.group(l), use(l)) : 0; });
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(kAll, w, o);
+                    if (lane == 0) sums[c] = w;
+                }
+            };
+            const float least = border.i ? border.v : of_key(key_of(border.v) + 1);
+            if (border.i == 0 || border.i == 0xffffffffu) runs([&](uint32_t) { return [&](float v, int) { return v >= least; }; });
+            else runs(kept);
         }
         __syncthreads();
+        begin(at + step, parity ^ 1);  // (what follows reads few of this row's logits once more)
         const uint64_t mine = threadIdx.x < row.chunks ? sums[threadIdx.x] : 0;
         uint64_t total;
         const uint64_t upto = block_scan(sh, mine, &total);
@@ -764,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SampleAr
 #pragma unroll
                 for (int j = 0; j < 8; ++j) w[j] = 0;
                 if (l < row.p.count)
-                    weigh.group(row.group(l), [&](float v, int j) { return border.keeps(v, row.index(l, j)); },
+                    weigh.group(load_group(row.p, l, a.V), [&](float v, int j) { return border.keeps(v, row.index(l, j)); },
                                 [&](float, int j, uint64_t m) {
                                     w[j] = m;
                                     sum += m;
@@ -781,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SampleAr
                 seen += __shfl_sync(kAll, scan, 31);
             });
         }
-        __syncthreads();  // the slice and the sums are free
+        __syncthreads();  // the sums are free
     }
     cluster_barrier();  // no block ends while another reads its shared memory
 }
