@@ -180,7 +180,9 @@ struct Row {
             if (!hits) continue;
             uint32_t at = 0;
             if (lane == 0) at = atomicAdd(&sh.queued, (uint32_t)__popc(hits));
-            at = __shfl_sync(kAll, at, 0) + __popc(hits & ((1u << lane) - 1));
+            at = __shfl_sync(kAll, at, 0);
+            if (at > kQueue) break;  // too many already
+            at += __popc(hits & ((1u << lane) - 1));
             if (hit && at < kQueue) sh.queue[at] = l;
         }
         __syncthreads();
@@ -439,6 +441,13 @@ __device__ __forceinline__ void count_in(uint64_t* at, uint64_t m) {
     else count32(at, (uint32_t)m);
 }
 
+// A float not above any logit of range `bin` or one before it: that range ends half a
+// range on, and a difference is rounded by 2^-24 of the larger of its numbers.
+__device__ __forceinline__ float below_range(float top, uint32_t bin, float scale) {
+    const float by = ((float)bin + 0.75f) / scale;
+    return (top - by) - (fabsf(top) + by) * 0x1p-21f;
+}
+
 // The border of the shortest beginning of what `from` keeps that measures
 // goal_of(what all of it measures) or more. `scale`: ranges per unit of logit.
 // `least`: no token below it belongs to that beginning. `kept_most`: `from` keeps
@@ -467,8 +476,7 @@ __device__ Border narrow(const Team<TI>& team, Border from, float scale, float l
     // a part of the range; the last range has no end
     uint32_t part = kBins;
     auto part_of_range = [&](float v) { return whole_of(fminf(fmaxf((range(v) - (float)bin + 0.5f) * (kBins - 1), 0.0f), kBins - 1)); };
-    // (a little below the range's end, whatever the rounding)
-    const float low = bin < kBins - 1 && !rank_all ? fmaxf(from.v, top - ((float)bin + 0.75f) / scale) : from.v;
+    const float low = bin < kBins - 1 && !rank_all ? fmaxf(from.v, below_range(top, bin, scale)) : from.v;
     const bool few = rank_all || (!Measure::kWeighed && inside <= kList);
     if (bin < kBins - 1 && !few)
         part = team.find_bin(
@@ -657,7 +665,7 @@ __device__ __forceinline__ float at_least(const Team<TI>& team, uint64_t k, floa
             return total < k ? total : k;
         },
         &goal);
-    return bin < kBins - 1 && groups >= k ? top - ((float)bin + 0.75f) / scale : minus_inf();
+    return bin < kBins - 1 && groups >= k ? below_range(top, bin, scale) : minus_inf();
 }
 
 template <typename TI>
@@ -796,18 +804,28 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SampleAr
         } else {  // many groups that would meet in one sum: a warp's steps are a run's
             row.size = (row.size + 31) / 32 * 32;
             row.chunks = (row.p.count + row.size - 1) / row.size;
-            auto runs = [&](auto use) {
-                for (uint32_t c = warp; c < row.chunks; c += warps) {
-                    uint64_t w = 0;
-                    row.run(c, [&](uint32_t l) { w += l < row.p.count ? sum_of(row.group(l), use(l)) : 0; });
-#pragma unroll
-                    for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(kAll, w, o);
-                    if (lane == 0) sums[c] = w;
-                }
-            };
             const float least = border.i ? border.v : of_key(key_of(border.v) + 1);
-            if (border.i == 0 || border.i == 0xffffffffu) runs([&](uint32_t) { return [&](float v, int) { return v >= least; }; });
-            else runs(kept);
+            const bool tied = border.i - 1 < 0xfffffffeu;  // the index decides between those equal to border.v
+            for (uint32_t c = warp; c < row.chunks; c += warps) {
+                uint64_t w = 0;
+                row.run(c, [&](uint32_t l) {
+                    if (l >= row.p.count) return;
+                    const Raw<TI> r = row.group(l);
+                    bool equal = false;
+                    w += sum_of(r, [&](float v, int) {
+                        equal |= v == border.v;
+                        return v >= least;
+                    });
+                    if (tied && equal) {  // those behind the border, taken off again
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (element(r, j) == border.v && row.index(l, j) >= border.i) w -= weigh(border.v);
+                    }
+                });
+#pragma unroll
+                for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(kAll, w, o);
+                if (lane == 0) sums[c] = w;
+            }
         }
         __syncthreads();
         begin(at + step, parity ^ 1);  // (what follows reads few of this row's logits once more)

@@ -157,6 +157,18 @@ def test_extreme_settings():
     check(z * 1e-4, u, top_p=np.full(T, 0.9, np.float32), top_k=np.full(T, 900, np.int32))
 
 
+@pytest.mark.parametrize("T,V,base,temperature", [(40, 4099, 1e6, 1.0), (40, 4099, -1e6, 0.3), (150, 140001, 1e6, 1.0),
+                                                  (150, 140001, -3e6, 2.0), (40, 33278, 2e5, 0.05)])
+def test_logits_far_from_zero(T, V, base, temperature):
+    """Logits whose floats lie as far apart as the ranges in which a border is looked for: what a range or a
+    part of it holds may not be judged by a rounded edge."""
+    rng = np.random.default_rng([T, V, 5])
+    z = base + rng.normal(size=(T, V)) * 2
+    kw = dict(temperature=np.full(T, temperature, np.float32), top_k=rng.choice([0, 3, 40, 200, 999, 3000, V // 20], T).astype(np.int32),
+              top_p=rng.choice([1.0, 0.97, 0.9, 0.6, 0.2], T).astype(np.float32))
+    check(z, rng.random(T), "f32", **kw)
+
+
 def test_every_token_can_be_drawn():
     """Over an even grid of u each of the kept tokens comes as often as its probability says."""
     V, T = 300, 20000
