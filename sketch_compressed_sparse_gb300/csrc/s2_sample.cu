@@ -27,9 +27,12 @@
 // Few rows are bound by the passes' barriers (a cluster's takes 1 to 2 us), many by
 // instructions: a weight takes about 35, where a row that nothing filters weighs
 // each token once and top-p with every token twice. Measured: a row of 33278
-// bfloat16 with top-p 22 us; 24 rows of 267735 float32 of all kinds of settings 70,
-// of 256 rows 416; of 256 rows 110 the largest alone, 160 with min-p, 300 with no
-// filter, 280 with top-k 50, 500 with top-k 1000 and top-p. To read them takes 38.
+// bfloat16 with top-p 22 us; 24 rows of 267735 float32 of all kinds of settings 69,
+// of 256 rows 390; of 256 rows 110 the largest alone, 140 with min-p, 290 with no
+// filter, 255 with top-k 50, 475 with top-k 1000 and top-p, 760 with top-p alone.
+// To read them takes 38. (There a third is issued, a fifth waits at barriers; exact
+// ends of ranges as floats, found once, spare top-p alone 70 us and cost every row
+// with top-k and every single row more.)
 #include <cfloat>
 
 #include "s2_internal.h"
@@ -878,10 +881,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SampleAr
 // blocks and a group kGroupNs of its SM, kAgain times as much where it is read
 // again in every pass, and the slowest of a few rows kRows more than most. Rows of
 // all kinds of settings, in us, over two, four, eight and sixteen blocks:
-//   24 x 267735 float32 225, 122, 77, 68; 256 x 267735 678, 484, 416, 609;
-//   256 x 33278 90, 108, 155, 359; one row of 33278 46, 26, 24, 22.
-// One block of 1024 threads on an SM: 86 and 435 where those take 68 and 416;
-// three of 320: 72 and 406, 90 at 256 x 33278.
+//   24 x 267735 float32 213, 95, 68, 69; 256 x 267735 536, 406, 392, 598;
+//   256 x 33278 84, 105, 155, 367; one row of 33278 40, 26, 24, 23.
+// (Before the passes were last shortened one block of 1024 threads on an SM took 86
+// and 435 where these took 68 and 416; three of 320 72 and 406.)
 constexpr uint32_t kPartSmem = 100 * 1024;  // of a block's part of a row
 constexpr double kRowNs = 22000.0, kGroupNs = 6.25, kAgain = 2.0, kRows = 0.5;
 
