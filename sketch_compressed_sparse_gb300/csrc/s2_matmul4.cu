@@ -15,7 +15,9 @@
 // Measured in CUDA graphs: one token by 4096 x 4096 4.2 us (a launch, the
 // pipeline's fill and 8.9 MB from L2); 24 tokens by 267735 x 1024 into float32
 // 29.2 us, 5.9 TB/s of its 171 MB (0.88 of a copy's rate), 64 into bfloat16 29.3;
-// 8192 x 4096 x 4096 44 us (6.2 PFLOP/s), 4096 x 4096 x 16384 87 us (6.4); 2048 x
+// 8192 x 4096 x 4096 44 us (6.2 PFLOP/s), 4096 x 4096 x 16384 87 us (6.4), bound by
+// shared memory: for a product of 64 k an SM reads 10 KB of it and copies write 7.7
+// KB, 139 clocks at 128 bytes a clock, where the tensor cores would take 101; 2048 x
 // 267735 x 1024 into bfloat16 385 us, which its stores take (2 bytes of 548 million
 // elements in rows that start on odd addresses, three sectors to a request).
 #include "s2_internal.h"
