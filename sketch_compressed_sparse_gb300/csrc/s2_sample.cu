@@ -27,11 +27,11 @@
 // Few rows are bound by the passes' barriers (a cluster's takes 1 to 2 us), many by
 // instructions: a weight takes about 35, where a row that nothing filters weighs
 // each token once and top-p with every token twice. Measured: a row of 33278
-// bfloat16 with top-p 22 us; 24 rows of 267735 float32 of all kinds of settings 69,
-// of 256 rows 390; of 256 rows 110 the largest alone, 140 with min-p, 290 with no
-// filter, 255 with top-k 50, 475 with top-k 1000 and top-p, 760 with top-p alone.
-// To read them takes 38. (There a third is issued, a fifth waits at barriers; exact
-// ends of ranges as floats, found once, spare top-p alone 70 us and cost every row
+// bfloat16 with top-p 20 us; 24 rows of 267735 float32 of all kinds of settings 66,
+// of 256 rows 363; of 256 rows 120 the largest alone, 140 with min-p, 270 with no
+// filter, 250 with top-k 50, 470 with top-k 1000 and top-p, 735 with top-p alone.
+// To read them takes 38. (There half is issued, a fifth waits at barriers; exact
+// ends of ranges as floats, found once, spare top-p alone 10 % and cost every row
 // with top-k and every single row more.)
 #include <cfloat>
 
@@ -44,14 +44,14 @@ namespace {
 
 using namespace rows;
 
-constexpr uint32_t kThreads = 512;
+constexpr uint32_t kThreads = 384;
 constexpr uint32_t kPerSm = 2;      // blocks
 constexpr uint32_t kBins = 256;     // a thread each
 constexpr uint32_t kList = 128;     // tokens that are ranked against one another
-constexpr uint32_t kQueue = 512;    // groups that a pass over few of them takes
+constexpr uint32_t kQueue = 768;    // groups that a pass over few of them takes
 constexpr float kPerOctave = 8.0f;  // ranges of logits per factor of two of weight
 constexpr int kBits = 43;           // of a weight of 1
-static_assert(kBins <= kThreads && kList <= kThreads && kQueue <= kThreads, "a thread for each");
+static_assert(kBins <= kThreads && kList <= kThreads, "a thread for each");
 
 // 2^(j/32) in two floats
 __device__ const float2 kRoots[32] = {
@@ -800,8 +800,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SampleAr
         if (few <= kQueue) {
             if (threadIdx.x < kBins) sums[threadIdx.x] = 0;
             __syncthreads();
-            if (threadIdx.x < few) {
-                const uint32_t l = small ? threadIdx.x : sh.queue[threadIdx.x];
+            for (uint32_t q = threadIdx.x; q < few; q += kThreads) {
+                const uint32_t l = small ? q : sh.queue[q];
                 add64(sums + l / row.size, sum_of(row.group(l), kept(l)));
             }
         } else {  // many groups that would meet in one sum: a warp's steps are a run's
@@ -881,10 +881,11 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SampleAr
 // blocks and a group kGroupNs of its SM, kAgain times as much where it is read
 // again in every pass, and the slowest of a few rows kRows more than most. Rows of
 // all kinds of settings, in us, over two, four, eight and sixteen blocks:
-//   24 x 267735 float32 213, 95, 68, 69; 256 x 267735 536, 406, 392, 598;
-//   256 x 33278 84, 105, 155, 367; one row of 33278 40, 26, 24, 23.
-// (Before the passes were last shortened one block of 1024 threads on an SM took 86
-// and 435 where these took 68 and 416; three of 320 72 and 406.)
+//   24 x 267735 float32 222, 103, 66, 63; 256 x 267735 582, 410, 379, 558;
+//   256 x 33278 91, 94, 137, 328; one row of 33278 41, 29, 22, 21.
+// Blocks of 512 threads, with fewer registers each, 68, 390, 84 and 23; of 320 64,
+// 420, 93 and 21; three of 320 with less shared memory 70, 375, 92 and 22; one of 640
+// 78, 404, 104 and 21.
 constexpr uint32_t kPartSmem = 100 * 1024;  // of a block's part of a row
 constexpr double kRowNs = 22000.0, kGroupNs = 6.25, kAgain = 2.0, kRows = 0.5;
 
