@@ -525,7 +525,7 @@ S2_API s2_status s2_matmul4(const uint8_t *x, uint64_t ldx, const uint8_t *x_sca
  *   and including it exceeds u times their sum.
  *   A logit that is -infinity or NaN is never drawn (a mask). A row with no
  *   other gives -1. Where a row holds +infinity those tokens alone have
- *   weight, 1 each.
+ *   weight, 1 each. A logit more than 3.4e38 below the largest has none.
  *   Weights are right to about 2^-35 of themselves and summed as integers, so
  *   the token does not depend on timing, nor, but for borders that close, on
  *   the arithmetic. logits need the alignment of their type only. T and V
@@ -566,11 +566,11 @@ typedef struct {
  *   teacher's: its loss, and the gradient at its entries).
  *   A term of weight 0 is left out. Sums are float32; the result does not
  *   depend on timing (a row's last bits do on its address modulo eight
- *   elements, on its place among the others and on T). K at most S2_DISTILL_MAX_ENTRIES (fastest up to 256), T
- *   and V below 2^31 (S2_ERR_UNSUPPORTED). dlogits may not overlap logits.
- *   Fastest where logits and dlogits start on 32 bytes and have the same row
- *   stride. Make the first call on a device before any stream capture (it
- *   looks up an address there).
+ *   elements, on its place among the others and on T). K at most
+ *   S2_DISTILL_MAX_ENTRIES (fastest up to 256), T and V below 2^31
+ *   (S2_ERR_UNSUPPORTED). dlogits may not overlap logits. Fastest where logits
+ *   and dlogits start on 32 bytes and have the same row stride. Make the first
+ *   call on a device before any stream capture (it looks up an address there).
  */
 #define S2_DISTILL_MAX_ENTRIES 8192u
 S2_API s2_status s2_distill(const void *logits, s2_dtype dt, uint64_t T, uint64_t V, uint64_t ld,

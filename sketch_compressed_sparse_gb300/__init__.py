@@ -698,7 +698,7 @@ def s2_distill(logits: torch.Tensor, teacher_idx: Optional[torch.Tensor], teache
 
 
 def s2_wait_faults() -> int:
-    """Waits of the tensor-core kernels that ran out on the current device (waits for the device)."""
+    """Waits of the tensor-core and the distillation kernels that ran out on the current device (waits for the device)."""
     c = _u32()
     _check(_f("s2_wait_faults")(ctypes.byref(c)), "s2_wait_faults")
     return int(c.value)

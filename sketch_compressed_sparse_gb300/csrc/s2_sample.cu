@@ -30,7 +30,7 @@
 // bfloat16 with top-p 20 us; 24 rows of 267735 float32 of all kinds of settings 66,
 // of 256 rows 363; of 256 rows 120 the largest alone, 140 with min-p, 270 with no
 // filter, 250 with top-k 50, 470 with top-k 1000 and top-p, 735 with top-p alone.
-// To read them takes 38. (There half is issued, a fifth waits at barriers; exact
+// To read them takes 38. (Two fifths of the issue slots are used; exact
 // ends of ranges as floats, found once, spare top-p alone 10 % and cost every row
 // with top-k and every single row more.)
 #include <cfloat>
