@@ -18,7 +18,7 @@
 // that); one joins the sums and hands them to the cluster's other blocks; two see
 // to the teacher's entries, every second row each, so that these have the time of
 // two rows for loads that depend on one another. Measured: 2048 rows of 267735
-// bfloat16 with 64 entries, a target and a bfloat16 gradient 438 us (5.0 TB/s of its
+// bfloat16 with 64 entries, a target and a bfloat16 gradient 434 us (5.1 TB/s of its
 // 2.2 GB, 0.75 of a copy's rate); 2048 rows of 33278 bfloat16, the loss alone, 37 us
 // (3.7 TB/s); 200 rows of 33278 float32 with a float32 gradient 21 us, where one
 // round of rows is loaded, summed and stored with nothing beside it.
@@ -35,7 +35,7 @@ namespace {
 
 using namespace rows;
 
-constexpr int kMaxThreads = 1024;
+constexpr int kMaxThreads = 512;
 constexpr uint32_t kMaxBlocks = 16;  // of a cluster
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -389,6 +389,7 @@ constexpr int kSlots = 8;               // entries of a lane
 constexpr uint32_t kFew = 32 * kSlots;
 constexpr uint32_t kPlaces = 512;       // of the table that finds indices that stand twice
 constexpr uint32_t kNone = 0xffffffffu;
+constexpr uint32_t kRepeated = 0x80000000u;  // beside an index of the table (below 2^31)
 constexpr uint32_t kHelpers = 96;       // threads that do not go over the logits
 
 struct Shared {
@@ -427,7 +428,7 @@ struct Entries {
     uint32_t i[kSlots];
     float q[kSlots], z[kSlots];  // q: logits, then probabilities; z: of those in this block
     float target;
-    uint32_t y, flags;
+    uint32_t y, flags, repeated;  // repeated: a bit for each slot whose index stands twice
     bool twice, listed;
 
     __device__ __forceinline__ void fetch(const Rows<TI>& rw, uint64_t row) {
@@ -457,6 +458,7 @@ struct Entries {
         const DistillArgs& a = rw.a;
         const uint32_t lane = threadIdx.x % 32, V = a.V;
         twice = listed = false;
+        repeated = 0;
         if (!a.use_soft) return make_float4(0.0f, 0.0f, 0.0f, target);
         float most = -FLT_MAX, top = -FLT_MAX, sum = 0.0f, cross = 0.0f, mass = 0.0f;
 #pragma unroll
@@ -499,7 +501,8 @@ struct Entries {
                 for (uint32_t tries = 0; tries < kPlaces; ++tries) {
                     const uint32_t old = atomicCAS(table + at, kNone, i[s]);
                     if (old == kNone) break;
-                    if (old == i[s]) {
+                    if ((old & ~kRepeated) == i[s]) {
+                        atomicOr(table + at, kRepeated);
                         twice = true;
                         break;
                     }
@@ -507,6 +510,15 @@ struct Entries {
                 }
             }
             twice = __any_sync(kAll, twice);
+            if (twice) {  // all entries of such an index have to know
+#pragma unroll
+                for (int s = 0; s < kSlots; ++s) {
+                    if (i[s] >= V) continue;
+                    uint32_t at = (i[s] * 0x9E3779B1u) >> 23;
+                    for (uint32_t tries = 0; tries < kPlaces && (table[at] & ~kRepeated) != i[s]; ++tries) at = (at + 1) % kPlaces;
+                    repeated |= (table[at] >> 31) << s;
+                }
+            }
         }
         return make_float4(cross, mass, top, target);
     }
@@ -514,14 +526,15 @@ struct Entries {
     template <typename TO, int EXPS>
     __device__ __forceinline__ void correct(TO* dz, const Rows<TI>& rw, const Factors<EXPS>& f, const Part<TI>& p, bool soft) const {
         const uint32_t lane = threadIdx.x % 32, V = rw.a.V;
-        if (soft && !twice) {
+        if (soft) {
 #pragma unroll
             for (int s = 0; s < kSlots; ++s)
-                if (p.holds(i[s], V)) put(dz + i[s], f.dense(z[s], rw.c) - f.gq * q[s] - (i[s] == y ? f.gy : 0.0f));
-        } else if (soft) {
+                if (p.holds(i[s], V) && !(repeated >> s & 1)) put(dz + i[s], f.dense(z[s], rw.c) - f.gq * q[s] - (i[s] == y ? f.gy : 0.0f));
+        }
+        if (soft && twice) {
 #pragma unroll
             for (int s = 0; s < kSlots; ++s) {
-                uint32_t todo = __ballot_sync(kAll, p.holds(i[s], V));
+                uint32_t todo = __ballot_sync(kAll, p.holds(i[s], V) && (repeated >> s & 1));
                 while (todo) {
                     const int at = __ffs(todo) - 1;
                     todo &= todo - 1;
@@ -550,7 +563,7 @@ struct Entries {
 // exponentials. `room` groups of the block's part of a row stay in shared memory;
 // what lies behind them is read again.
 template <typename TI, typename TO, int EXPS>
-__global__ void __launch_bounds__(kMaxThreads, 1) distill_kernel(const DistillArgs a, uint32_t room, uint32_t log2_blocks, float limit, uint32_t* faults) {
+__global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const DistillArgs a, uint32_t room, uint32_t log2_blocks, float limit, uint32_t* faults) {
     constexpr bool kGrad = !std::is_same<TO, void>::value;
     extern __shared__ uint4 slice[];
     __shared__ Shared sh;
@@ -650,7 +663,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) distill_kernel(const DistillAr
                 e.gather(rw, rw.row, p);
                 own = e.finish(rw, p, sh.table[parity], kGrad);
             } else {
-                e.flags = 0;
+                e.flags = e.repeated = 0;
                 e.listed = e.twice = false;
             }
             if (lane == 0) {
@@ -681,7 +694,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) distill_kernel(const DistillAr
 // Every warp has a share of the entries, row by row: no table holds them, and an
 // index that stands twice is found by going through the list for each.
 template <typename TI, typename TO, int EXPS>
-__global__ void __launch_bounds__(kMaxThreads, 1) distill_many_kernel(const DistillArgs a, uint32_t room, uint32_t log2_blocks, float limit, uint32_t*) {
+__global__ void __launch_bounds__(kMaxThreads, 2) distill_many_kernel(const DistillArgs a, uint32_t room, uint32_t log2_blocks, float limit, uint32_t*) {
     constexpr bool kGrad = !std::is_same<TO, void>::value;
     extern __shared__ uint4 slice[];
     __shared__ Sums warp_sums[kMaxThreads / 32];
@@ -793,15 +806,18 @@ __global__ void __launch_bounds__(kMaxThreads, 1) distill_many_kernel(const Dist
 
 // How a row is spread: threads of a block, blocks on an SM, shared memory of a
 // block's part of a row. Estimated nanoseconds of a round of rows, fitted to rows
-// of 33278 and 267735 in every spread (2048 x 267735 bfloat16 with its gradient:
-// three blocks of an SM and eight of a row 434 us; two and eight 472, two and four
-// 506, one and two 516, three and sixteen 664; one and one 680): joining its sums, 62 bytes of
+// of 1000 to 267735 in every spread: launching and joining the sums, then 62 bytes of
 // logits and gradient a nanosecond on an SM, 16 where the logits are read again.
+// (2048 x 267735 bfloat16 with its gradient: three blocks of an SM and eight of a row
+// 434 us; two and eight 472, two and four 506. 300 x 60000 bfloat16, the loss alone:
+// two of an SM and one of a row 11, three and two 18. One row of 1000: 288 threads a
+// block 3.8 us, 1024 5.3, and such blocks were the best nowhere.)
 struct Spread {
     uint32_t threads, per_sm, smem;
+    double join_ns;
 };
-constexpr Spread kSpreads[3] = {{1024, 1, 208 * 1024}, {512, 2, 104 * 1024}, {320, 3, 66 * 1024}};
-constexpr double kJoinNs = 4500.0, kBytesNs = 62.0, kAgainNs = 16.0;
+constexpr Spread kSpreads[2] = {{512, 2, 104 * 1024, 5500.0}, {288, 3, 66 * 1024, 4500.0}};
+constexpr double kBytesNs = 62.0, kAgainNs = 16.0;
 
 template <typename TI, typename TO, int EXPS>
 cudaError_t launch(const DistillArgs& a, uint32_t* faults, cudaStream_t s) {
@@ -825,7 +841,7 @@ cudaError_t launch(const DistillArgs& a, uint32_t* faults, cudaStream_t s) {
             if (n < 1) continue;
             const uint64_t rounds = ((uint64_t)a.T + n - 1) / n, all = ((uint64_t)a.T * b + di.sms - 1) / di.sms;
             const double per_sm = (double)(all < w.per_sm ? all : w.per_sm);
-            const double ns = (double)rounds * (kJoinNs + per_sm * kMoved * ((double)keep / kBytesNs + (double)(need - keep) / kAgainNs));
+            const double ns = (double)rounds * (w.join_ns + per_sm * kMoved * ((double)keep / kBytesNs + (double)(need - keep) / kAgainNs));
             if (blocks && ns >= best) continue;
             best = ns;
             blocks = b;
