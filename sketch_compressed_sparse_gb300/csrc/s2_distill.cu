@@ -18,9 +18,9 @@
 // that); one joins the sums and hands them to the cluster's other blocks; two see
 // to the teacher's entries, every second row each, so that these have the time of
 // two rows for loads that depend on one another. Measured: 2048 rows of 267735
-// bfloat16 with 64 entries, a target and a bfloat16 gradient 434 us (5.1 TB/s of its
-// 2.2 GB, 0.75 of a copy's rate); 2048 rows of 33278 bfloat16, the loss alone, 37 us
-// (3.7 TB/s); 200 rows of 33278 float32 with a float32 gradient 21 us, where one
+// bfloat16 with 64 entries, a target and a bfloat16 gradient 430 us (5.1 TB/s of its
+// 2.2 GB, 0.76 of a copy's rate); 2048 rows of 33278 bfloat16, the loss alone, 36 us
+// (3.8 TB/s); 200 rows of 33278 float32 with a float32 gradient 21 us, where one
 // round of rows is loaded, summed and stored with nothing beside it.
 #include <cfloat>
 #include <type_traits>
