@@ -68,10 +68,11 @@ __device__ __forceinline__ float log_sum(float sum, const Base& b, float c) {
     return logf(sum) - (b.plain ? fmaf(b.max, c, -b.k) * kLn2 : 0.0f);
 }
 
-// What a block knows of its part of a row: 32 bytes, two stores to another block.
+// What a block knows of its part of a row: 32 bytes, two stores to another block
+// (a third brings bmax, where that is not max).
 struct __align__(16) Record {
     float max;         // base of its logits' sums (lowest finite number where it has none)
-    float soft, hard;  // sums of the powers of (z - max) / T, z - max
+    float soft, hard;  // sums of the powers of (z - max) / T, z - max (z - bmax)
     uint32_t flags;    // 1: the target is here, 2: the row has a soft term, 4: a hard one
     float cross;       // sum of q (log q - (z - ref) / T) over the teacher's entries here
     float mass;        // sum of their q
@@ -79,7 +80,13 @@ struct __align__(16) Record {
     float target;      // the target's logit, where it is here
 };
 
+// Sums over a base. A log-sum at temperature T lies up to (T - 1) log V above the
+// one at 1, so two sums that have nothing to do with one another have a base each.
 struct Sums {
+    float max, a, b;
+    float bmax;  // of b; max but for kBoth
+};
+struct Three {  // all but bmax
     float max, a, b;
 };
 
@@ -89,7 +96,8 @@ __device__ __forceinline__ Sums join(const Sums& s, float c, float limit) {
     Sums r;
     r.max = warp_max(s.max);
     r.a = warp_sum(s.a * factor(base_of(s.max, c, limit), base_of(r.max, c, limit), c));
-    r.b = EXPS != kOne ? warp_sum(s.b * factor(base_of(s.max, kLog2e, limit), base_of(r.max, kLog2e, limit), kLog2e)) : r.a;
+    r.bmax = EXPS == kBoth ? warp_max(s.bmax) : r.max;
+    r.b = EXPS != kOne ? warp_sum(s.b * factor(base_of(s.bmax, kLog2e, limit), base_of(r.bmax, kLog2e, limit), kLog2e)) : r.a;
     return r;
 }
 
@@ -130,18 +138,31 @@ __device__ __forceinline__ void store_group(TO* dz, const Part<TI>& p, uint32_t 
 // above 1, so nearer ones need not).
 constexpr float kFar = 60.0f;
 template <int EXPS>
+struct Second {  // base of the second sum
+    __device__ __forceinline__ void put(float) {}
+    __device__ __forceinline__ float get(float first) const { return first; }
+};
+template <>
+struct Second<kBoth> {
+    float max;
+    __device__ __forceinline__ void put(float m) { max = m; }
+    __device__ __forceinline__ float get(float) const { return max; }
+};
+template <int EXPS>
 struct Taken {
-    float max, ka, kb;  // of the bases; both are plain or none is
+    float max, ka, kb;  // of the bases; both are plain, or none is and they are the same
     bool plain;
+    Second<EXPS> second;
     Two sa, sb;
-    __device__ __forceinline__ void rest_on(float m, float c, float limit) {
-        const Base a = base_of(m, c, limit), b = base_of(m, kLog2e, limit);
+    __device__ __forceinline__ void rest_on(float m, float mb, float c, float limit) {
+        const Base a = base_of(m, c, limit), b = base_of(mb, kLog2e, limit);
         max = m;
+        second.put(mb);
         ka = a.k;
         kb = b.k;
-        plain = a.plain;
+        plain = a.plain && b.plain;
     }
-    __device__ __forceinline__ Taken(float m, float c, float limit) : sa(two(0.0f, 0.0f)), sb(sa) { rest_on(m, c, limit); }
+    __device__ __forceinline__ Taken(float m, float mb, float c, float limit) : sa(two(0.0f, 0.0f)), sb(sa) { rest_on(m, mb, c, limit); }
     // a base is plain
     template <typename TI>
     __device__ __forceinline__ void add(const Raw<TI>& r, float c) {
@@ -169,15 +190,15 @@ struct Taken {
         }
     }
     __device__ __noinline__ void move(float m, float c, float limit) {
-        const Base a{max, ka, plain}, b{max, kb, plain};
-        rest_on(m, c, limit);
+        const Base a{max, ka, plain}, b{second.get(max), kb, plain};
+        rest_on(m, m, c, limit);
         const float fa = factor(a, {max, ka, plain}, c), fb = factor(b, {max, kb, plain}, kLog2e);
         sa = mul2(sa, two(fa, fa));
         if (EXPS != kOne) sb = mul2(sb, two(fb, fb));
     }
     __device__ __forceinline__ Sums sums() const {
         const float2 x = apart(sa), y = apart(sb);
-        return {max, x.x + x.y, y.x + y.y};
+        return {max, x.x + x.y, y.x + y.y, second.get(max)};
     }
 };
 
@@ -203,7 +224,7 @@ struct Factors {
     float ca, cb, gq, gy;  // of the powers; of the teacher's probabilities and the target
     bool some;             // the row has a term
     __device__ __forceinline__ Factors(const Sums& w, bool soft, bool hard, float weight, const DistillArgs& a, float c, float limit)
-        : ba(base_of(w.max, c, limit)), bb(base_of(w.max, kLog2e, limit)), some(soft || hard) {
+        : ba(base_of(w.max, c, limit)), bb(base_of(w.bmax, kLog2e, limit)), some(soft || hard) {
         const float g = weight * a.scale;
         gq = soft ? g * a.soft * a.inv_t : 0.0f;
         gy = hard ? g * a.hard : 0.0f;
@@ -239,17 +260,19 @@ struct Factors {
 // next row's (part np) take their places.
 //
 // The base of the sums need not be the largest logit: any number serves for which
-// they neither overflow nor vanish. It is `guess`, the log-sum of the row before;
-// only where the sums come out far from 1 is the largest logit looked for.
+// they neither overflow nor vanish. It is `guess` (and `guess_b`), the log-sum of
+// the row before; only where the sums come out far from 1 is the largest logit
+// looked for. (With one base for both sums that was every row from temperature 5
+// on: 2048 x 267735 bfloat16 with a gradient in 780 us instead of 545.)
 template <typename TI, int EXPS, bool FREE>
 __device__ __forceinline__ Sums sums_of(uint4* slice, const Rows<TI>& rw, const Part<TI>& p, uint32_t kept, const Part<TI>& np,
-                                        uint32_t next_kept, float guess, uint32_t first, uint32_t step) {
+                                        uint32_t next_kept, float guess, float guess_b, uint32_t first, uint32_t step) {
     const float c = rw.c;
     const uint32_t room = rw.room;
     constexpr float kLarge = 0x1p80f, kSmall = 0x1p-60f;
     auto fine = [](float v) { return v > kSmall && v < kLarge; };
-    Taken<EXPS> sum(guess, c, rw.limit);
-    Sums s{guess, 0.0f, 0.0f};
+    Taken<EXPS> sum(guess, EXPS == kBoth ? guess_b : guess, c, rw.limit);
+    Sums s{};
     bool good = sum.plain;
     if (good) {
 #pragma unroll 2
@@ -263,7 +286,8 @@ __device__ __forceinline__ Sums sums_of(uint4* slice, const Rows<TI>& rw, const 
         float m = -FLT_MAX;
 #pragma unroll 4
         for (uint32_t l = first; l < kept; l += step) m = fmaxf(m, group_max(staged<TI>(slice, room, l)));
-        sum = Taken<EXPS>(warp_max(m), c, rw.limit);
+        m = warp_max(m);
+        sum = Taken<EXPS>(m, m, c, rw.limit);
         if (sum.plain) {
 #pragma unroll 2
             for (uint32_t l = first; l < kept; l += step) sum.add(staged<TI>(slice, room, l), c);
@@ -286,8 +310,12 @@ __device__ __forceinline__ Sums sums_of(uint4* slice, const Rows<TI>& rw, const 
         for (; l < next_kept; l += step) stage_group(slice, room, np, l, rw.a.V);
     }
     if (p.count > room) {  // what does not stay in shared memory
-        const float far = kFar / (EXPS == kBoth ? fmaxf(c, kLog2e) : EXPS == kSquare ? kLog2e : c);
-        float above = sum.plain ? sum.max + far : sum.max;
+        const float far = kFar / (EXPS == kSquare ? kLog2e : c);
+        auto limit_of = [&] {
+            if (!sum.plain) return sum.max;
+            return EXPS == kBoth ? fminf(sum.max + far, sum.second.get(sum.max) + kFar / kLog2e) : sum.max + far;
+        };
+        float above = limit_of();
         uint32_t r = first;
         if (first < kept) r += (kept - first + step - 1) / step * step;
 #pragma unroll 2
@@ -296,7 +324,7 @@ __device__ __forceinline__ Sums sums_of(uint4* slice, const Rows<TI>& rw, const 
             const float m = group_max(g);
             if (m > above) {
                 sum.move(m, c, rw.limit);
-                above = sum.plain ? m + far : m;
+                above = limit_of();
             }
             sum.add_any(g, c);
         }
@@ -305,10 +333,10 @@ __device__ __forceinline__ Sums sums_of(uint4* slice, const Rows<TI>& rw, const 
     return s;
 }
 
-// The base for the next row: this one's log-sum.
-__device__ __forceinline__ float guess_from(const Sums& w, float c, float old) {
-    const float g = w.max + __log2f(w.a) / c;
-    return w.a > 0.0f && fabsf(g) < FLT_MAX ? g : old;
+// The base for the next row: this one's log-sum, from a sum over base `max`.
+__device__ __forceinline__ float guess_from(float max, float sum, float c, float old) {
+    const float g = max + __log2f(sum) / c;
+    return sum > 0.0f && fabsf(g) < FLT_MAX ? g : old;
 }
 
 // Stores a thread's groups of the gradient's dense part; the next row's take the
@@ -318,7 +346,7 @@ __device__ __forceinline__ void store_dense(TO* dz, uint4* slice, const Rows<TI>
                                             const Part<TI>& np, uint32_t next_kept, uint32_t first, uint32_t step) {
     const uint32_t V = rw.a.V, room = rw.room;
     const float c = rw.c;
-    const bool plain = f.ba.plain && f.some, wide = rw.a.wide;
+    const bool plain = f.ba.plain && (EXPS != kBoth || f.bb.plain) && f.some, wide = rw.a.wide;
     auto any = [&](uint32_t l) {  // any group of this row or the next
         if (l < p.count) {
             float2 v[4] = {};
@@ -374,11 +402,11 @@ __device__ __forceinline__ void store_dense(TO* dz, uint4* slice, const Rows<TI>
 // The row's loss, from what the lanes' blocks know; in lane 0.
 template <int EXPS>
 __device__ __forceinline__ float loss_of(const Record& r, const Sums& w, bool mine, bool soft, float weight, const DistillArgs& a, float c, float limit) {
-    const Base ba = base_of(w.max, c, limit), bb = base_of(w.max, kLog2e, limit);
+    const Base ba = base_of(w.max, c, limit), bb = base_of(w.bmax, kLog2e, limit);
     float sum = 0.0f;
     if (mine) {
         if (soft) sum += a.soft * (r.cross + (r.mass == 0.0f ? 0.0f : r.mass * ((w.max - r.ref) * a.inv_t + log_sum(w.a, ba, c))));
-        if (r.flags & 1) sum += a.hard * ((w.max - r.target) + log_sum(w.b, EXPS != kOne ? bb : ba, EXPS != kOne ? kLog2e : c));
+        if (r.flags & 1) sum += a.hard * ((w.bmax - r.target) + log_sum(w.b, EXPS != kOne ? bb : ba, EXPS != kOne ? kLog2e : c));
     }
     return warp_sum(sum) * weight;
 }
@@ -392,9 +420,17 @@ constexpr uint32_t kNone = 0xffffffffu;
 constexpr uint32_t kRepeated = 0x80000000u;  // beside an index of the table (below 2^31)
 constexpr uint32_t kHelpers = 96;       // threads that do not go over the logits
 
-struct Shared {
+template <int EXPS>
+struct SharedBases {};
+template <>
+struct SharedBases<kBoth> {  // bmax of the records and of the warps' sums
+    float4 bases[2][kMaxBlocks];
+    float sum_bases[kMaxThreads / 32];
+};
+template <int EXPS>
+struct Shared : SharedBases<EXPS> {
     Record records[2][kMaxBlocks];  // of this row and the next, from every block
-    Sums sums[kMaxThreads / 32];
+    Three sums[kMaxThreads / 32];
     float4 entries[2];              // cross, mass, ref, target
     uint32_t flags[2];
     uint32_t table[2][kPlaces];
@@ -566,7 +602,7 @@ template <typename TI, typename TO, int EXPS>
 __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const DistillArgs a, uint32_t room, uint32_t log2_blocks, float limit, uint32_t* faults) {
     constexpr bool kGrad = !std::is_same<TO, void>::value;
     extern __shared__ uint4 slice[];
-    __shared__ Shared sh;
+    __shared__ Shared<EXPS> sh;
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, threads = blockDim.x, dense_threads = threads - kHelpers;
     const uint32_t blocks = 1u << log2_blocks;
     if (threadIdx.x == 0) {
@@ -587,33 +623,39 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const DistillAr
         tc::bar_wait(tc::smem_u32(&sh.full[n & 1]), (n >> 1) & 1, wt);
         r = {-FLT_MAX, 0.0f, 0.0f, 0u, 0.0f, 0.0f, 0.0f, 0.0f};
         if (lane < blocks) r = sh.records[n & 1][lane];
+        float bmax = r.max;
+        if constexpr (EXPS == kBoth) bmax = lane < blocks ? sh.bases[n & 1][lane].x : bmax;
         soft = __any_sync(kAll, r.flags & 2u);  // (every block says the same)
         hard = __any_sync(kAll, r.flags & 4u);
-        return join<EXPS>({r.max, r.soft, r.hard}, rw.c, limit);
+        return join<EXPS>({r.max, r.soft, r.hard, bmax}, rw.c, limit);
     };
 
     if (threadIdx.x < dense_threads) {
         float weight = rw.weight(rw.row), next_weight = rw.weight(rw.row + rw.step);
         Part<TI> p = rw.part(rw.row);
-        float guess = FLT_MAX;  // none yet
+        float guess = FLT_MAX, guess_b = FLT_MAX;  // none yet
         for (uint32_t l = threadIdx.x, n = rw.kept(p, weight); l < n; l += dense_threads) stage_group(slice, room, p, l, a.V);
         for (uint32_t n = 0; rw.there(rw.row); ++n, rw.row += rw.step) {
             const float after = rw.weight(rw.row + 2 * rw.step);
             const Part<TI> np = rw.part(rw.row + rw.step);
             const uint32_t kept = rw.kept(p, weight), next_kept = rw.kept(np, next_weight);
-            Sums s{-FLT_MAX, 0.0f, 0.0f};
+            Sums s{-FLT_MAX, 0.0f, 0.0f, -FLT_MAX};
             copies_done();
             if (weight != 0.0f) {
-                s = sums_of<TI, EXPS, !kGrad>(slice, rw, p, kept, np, next_kept, guess, threadIdx.x, dense_threads);
+                s = sums_of<TI, EXPS, !kGrad>(slice, rw, p, kept, np, next_kept, guess, guess_b, threadIdx.x, dense_threads);
             } else if (!kGrad) {
                 for (uint32_t l = threadIdx.x; l < next_kept; l += dense_threads) stage_group(slice, room, np, l, a.V);
             }
-            if (lane == 0) sh.sums[warp] = s;
+            if (lane == 0) {
+                sh.sums[warp] = {s.max, s.a, s.b};
+                if constexpr (EXPS == kBoth) sh.sum_bases[warp] = s.bmax;
+            }
             arrive(kSums, threads);
             Record r;
             bool soft, hard;
             const Sums w = joined(n, r, soft, hard);
-            guess = guess_from(w, rw.c, guess);
+            guess = guess_from(w.max, w.a, rw.c, guess);
+            if (EXPS == kBoth) guess_b = guess_from(w.bmax, w.b, kLog2e, guess_b);
             if constexpr (kGrad) {
                 const Factors<EXPS> f(w, soft, hard, weight, a, rw.c, limit);
                 store_dense(static_cast<TO*>(a.dz) + rw.row * a.ldd, slice, rw, f, p, kept, np, next_kept, threadIdx.x, dense_threads);
@@ -627,11 +669,14 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const DistillAr
         for (uint32_t n = 0; rw.there(rw.row); ++n, rw.row += rw.step) {
             const float weight = rw.weight(rw.row);
             wait(kSums, threads);
-            Sums s = lane < dense_threads / 32 ? sh.sums[lane] : Sums{-FLT_MAX, 0.0f, 0.0f};
-            s = join<EXPS>(s, rw.c, limit);
+            const bool some = lane < dense_threads / 32;
+            const Three mine = some ? sh.sums[lane] : Three{-FLT_MAX, 0.0f, 0.0f};
+            float bmax = mine.max;
+            if constexpr (EXPS == kBoth) bmax = some ? sh.sum_bases[lane] : bmax;
+            const Sums s = join<EXPS>({mine.max, mine.a, mine.b, bmax}, rw.c, limit);
             const float4 e = sh.entries[n & 1];
             const uint32_t at = tc::smem_u32(&sh.records[n & 1][rw.rank]), bar = tc::smem_u32(&sh.full[n & 1]);
-            if (lane == 0) tc::bar_expect(bar, blocks * (uint32_t)sizeof(Record));
+            if (lane == 0) tc::bar_expect(bar, blocks * (uint32_t)(sizeof(Record) + (EXPS == kBoth ? sizeof(float4) : 0)));
             __syncwarp();
             if (lane < blocks) {
                 uint32_t to, of;
@@ -639,6 +684,10 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const DistillAr
                 asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(of) : "r"(bar), "r"(lane));
                 push16(to, of, make_uint4(__float_as_uint(s.max), __float_as_uint(s.a), __float_as_uint(s.b), sh.flags[n & 1]));
                 push16(to + 16, of, make_uint4(__float_as_uint(e.x), __float_as_uint(e.y), __float_as_uint(e.z), __float_as_uint(e.w)));
+                if constexpr (EXPS == kBoth) {
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(tc::smem_u32(&sh.bases[n & 1][rw.rank])), "r"(lane));
+                    push16(to, of, make_uint4(__float_as_uint(s.bmax), 0, 0, 0));
+                }
             }
             Record r;
             bool soft, hard;
@@ -700,6 +749,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_many_kernel(const Dist
     __shared__ Sums warp_sums[kMaxThreads / 32];
     __shared__ float2 warp_teacher[kMaxThreads / 32], warp_cross[kMaxThreads / 32];
     __shared__ Record records[2];
+    __shared__ float bases[2];
     stream_order();
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, threads = blockDim.x, warps = threads / 32;
     const uint32_t blocks = 1u << log2_blocks;
@@ -731,14 +781,14 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_many_kernel(const Dist
         };
         join_teacher(most, sum);
         copies_done();
-        Sums s{-FLT_MAX, 0.0f, 0.0f};
-        if (alive) s = sums_of<TI, EXPS, false>(slice, rw, p, kept, p, 0, FLT_MAX, threadIdx.x, threads);
+        Sums s{-FLT_MAX, 0.0f, 0.0f, -FLT_MAX};
+        if (alive) s = sums_of<TI, EXPS, false>(slice, rw, p, kept, p, 0, FLT_MAX, FLT_MAX, threadIdx.x, threads);
         if (lane == 0) {
             warp_sums[warp] = s;
             warp_teacher[warp] = make_float2(most, sum);
         }
         __syncthreads();
-        s = join<EXPS>(lane < warps ? warp_sums[lane] : Sums{-FLT_MAX, 0.0f, 0.0f}, rw.c, limit);
+        s = join<EXPS>(lane < warps ? warp_sums[lane] : Sums{-FLT_MAX, 0.0f, 0.0f, -FLT_MAX}, rw.c, limit);
         most = lane < warps ? warp_teacher[lane].x : -FLT_MAX;
         sum = lane < warps ? warp_teacher[lane].y : 0.0f;
         join_teacher(most, sum);
@@ -763,17 +813,21 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_many_kernel(const Dist
         if (warp == 0) {
             cross = warp_sum(lane < warps ? warp_cross[lane].x : 0.0f);
             mass = warp_sum(lane < warps ? warp_cross[lane].y : 0.0f);
-            if (lane == 0)
+            if (lane == 0) {
                 records[turn] = {s.max, s.a, s.b, (uint32_t)has | (some ? 2u : 0u) | (y < a.V ? 4u : 0u), cross, mass, s.max, has ? to_float(z[y]) : 0.0f};
+                bases[turn] = s.bmax;
+            }
         }
         cluster_barrier();
         Record r{-FLT_MAX, 0.0f, 0.0f, 0u, 0.0f, 0.0f, 0.0f, 0.0f};
+        float bmax = r.max;
         if (lane < blocks) {
             const uint32_t at = peer(&records[turn], lane);
             r = {peer_float(at), peer_float(at + 4), peer_float(at + 8), peer_u32(at + 12), peer_float(at + 16), peer_float(at + 20), peer_float(at + 24), peer_float(at + 28)};
+            bmax = EXPS == kBoth ? peer_float(peer(&bases[turn], lane)) : r.max;
         }
         const bool hard = y < a.V;
-        const Sums w = join<EXPS>({r.max, r.soft, r.hard}, rw.c, limit);
+        const Sums w = join<EXPS>({r.max, r.soft, r.hard, bmax}, rw.c, limit);
         if (rw.rank == 0 && warp == 0) {
             const float loss = loss_of<EXPS>(r, w, lane < blocks, some, weight, a, rw.c, limit);
             if (lane == 0) a.loss[row] = some || hard ? loss : 0.0f;
