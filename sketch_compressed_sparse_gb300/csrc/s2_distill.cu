@@ -44,7 +44,7 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // temperature is 2, the one at that temperature and its square.
 enum { kOne, kSquare, kBoth };
 
-// exp2(z * c - k) with k = max * c rounded needs one rounding; where max is near
+// exp2(z * c - k) with k close to max * c needs one rounding; where max is near
 // the end of the floats (a row of nothing but a type's lowest value) the product
 // may be infinite, and (z - max) * c is taken instead.
 struct Base {
@@ -132,11 +132,52 @@ __device__ __forceinline__ void store_group(TO* dz, const Part<TI>& p, uint32_t 
     }
 }
 
+// A whole row's sums, moved to bases at its log-sums. A power is off by 2^-24 of
+// its exponent, which is small for the logits that matter only there, and what is
+// left of a sum is one to two: neither the gradient nor the loss depends on where
+// the sums were taken. The moves are by whole factors of two, hence exact.
+template <int EXPS>
+struct Settled {
+    Base a, b;
+    float sa, sb;
+    bool moved;  // a and, where it has a base of its own, b
+
+    __device__ __forceinline__ Settled(const Sums& w, float c, float inv_c, float limit)
+        : a(base_of(w.max, c, limit)), b(base_of(w.bmax, kLog2e, limit)), sa(w.a), sb(w.b) {
+        auto fit = [](const Base& x, float s) { return x.plain && s > 0x1p-100f && s < 0x1p100f; };
+        moved = fit(a, sa) && (EXPS != kBoth || fit(b, sb));
+        if (!moved) return;
+        const float by = move(a, sa, inv_c);
+        if (EXPS == kSquare) {
+            const float down = __uint_as_float((254u << 23) - (__float_as_uint(w.a) & 0x7f800000u));  // 2^-n
+            sb *= down;
+            sb *= down;
+            sb = fmaf(sb, 2.0f * by, sb);
+            b.max = a.max;
+            b.k = 2.0f * a.k;
+        } else if (EXPS == kBoth) {
+            move(b, sb, kLn2);
+        } else {
+            sb = sa;
+        }
+    }
+    // s = 2^n t: t over the base k + n; that number's rounding goes to the sum.
+    static __device__ __forceinline__ float move(Base& x, float& s, float inv_c) {
+        const uint32_t bits = __float_as_uint(s);
+        const float n = (float)((int)(bits >> 23) - 127), k = __fadd_rn(x.k, n), t = __fsub_rn(k, x.k);
+        const float by = kLn2 * __fadd_rn(__fsub_rn(x.k, __fsub_rn(k, t)), __fsub_rn(n, t));
+        s = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+        s = fmaf(s, by, s);
+        x.k = k;
+        x.max = k * inv_c;  // (nearly)
+        return by;
+    }
+};
+
 // A thread's sums over the groups that it takes, over a base that its warp shares
 // at first. What is read again later is not known to be below it: a logit 2^kFar
-// times as likely moves the sums to another base (a float holds sums that far
-// above 1, so nearer ones need not).
-constexpr float kFar = 60.0f;
+// times as likely moves the sums to another base.
+constexpr float kFar = 16.0f;
 template <int EXPS>
 struct Second {  // base of the second sum
     __device__ __forceinline__ void put(float) {}
@@ -155,7 +196,7 @@ struct Taken {
     Second<EXPS> second;
     Two sa, sb;
     __device__ __forceinline__ void rest_on(float m, float mb, float c, float limit) {
-        const Base a = base_of(m, c, limit), b = base_of(mb, kLog2e, limit);
+        const Base a = base_of(m, c, limit), b = base_of(EXPS == kBoth ? mb : m, kLog2e, limit);
         max = m;
         second.put(mb);
         ka = a.k;
@@ -207,7 +248,7 @@ template <typename TI>
 struct Rows {
     const DistillArgs& a;
     uint32_t rank, log2_blocks, room;
-    float c, limit;  // c: of the first sum
+    float c, inv_c, limit;  // c: of the first sum
     uint64_t row, step;
     __device__ __forceinline__ const TI* logits(uint64_t r) const { return static_cast<const TI*>(a.z) + r * a.ld; }
     __device__ __forceinline__ bool there(uint64_t r) const { return r < a.T; }
@@ -223,13 +264,13 @@ struct Factors {
     Base ba, bb;
     float ca, cb, gq, gy;  // of the powers; of the teacher's probabilities and the target
     bool some;             // the row has a term
-    __device__ __forceinline__ Factors(const Sums& w, bool soft, bool hard, float weight, const DistillArgs& a, float c, float limit)
-        : ba(base_of(w.max, c, limit)), bb(base_of(w.bmax, kLog2e, limit)), some(soft || hard) {
+    __device__ __forceinline__ Factors(const Settled<EXPS>& w, bool soft, bool hard, float weight, const DistillArgs& a)
+        : ba(w.a), bb(w.b), some(soft || hard) {
         const float g = weight * a.scale;
         gq = soft ? g * a.soft * a.inv_t : 0.0f;
         gy = hard ? g * a.hard : 0.0f;
-        ca = w.a == 0.0f ? 0.0f : gq / w.a;
-        cb = w.b == 0.0f ? 0.0f : gy / w.b;
+        ca = w.sa == 0.0f ? 0.0f : gq / w.sa;
+        cb = w.sb == 0.0f ? 0.0f : gy / w.sb;
         if (EXPS == kOne) ca += cb;
     }
     __device__ __forceinline__ float dense(float v, float c) const {
@@ -259,20 +300,24 @@ struct Factors {
 // its warp. FREE: this is the last use of the groups in shared memory, and the
 // next row's (part np) take their places.
 //
-// The base of the sums need not be the largest logit: any number serves for which
-// they neither overflow nor vanish. It is `guess` (and `guess_b`), the log-sum of
-// the row before; only where the sums come out far from 1 is the largest logit
-// looked for. (With one base for both sums that was every row from temperature 5
-// on: 2048 x 267735 bfloat16 with a gradient in 780 us instead of 545.)
+// The base of the sums need not be the largest logit: any number near it serves.
+// It is `guess` (and `guess_b`), the log-sum of the row before. Where the sums come
+// out above 2^16 or below 2^-30 (a warp has a hundredth of a row's words, and far
+// less of its probability where one word has nearly all) they are taken again, over
+// the log-sum that they give; where they say nothing, over the largest logit. An
+// exponent that matters is so below 32, and off by half of 2^-19 at most. (Taken as
+// far away as floats reach, a row 40 below the one before it had its loss off by up
+// to 6e-6. With one base for both sums every row was gone over three times from
+// temperature 5 on: 2048 x 267735 bfloat16 with a gradient in 780 us instead of 548.)
 template <typename TI, int EXPS, bool FREE>
 __device__ __forceinline__ Sums sums_of(uint4* slice, const Rows<TI>& rw, const Part<TI>& p, uint32_t kept, const Part<TI>& np,
                                         uint32_t next_kept, float guess, float guess_b, uint32_t first, uint32_t step) {
     const float c = rw.c;
     const uint32_t room = rw.room;
-    constexpr float kLarge = 0x1p80f, kSmall = 0x1p-60f;
-    auto fine = [](float v) { return v > kSmall && v < kLarge; };
-    Taken<EXPS> sum(guess, EXPS == kBoth ? guess_b : guess, c, rw.limit);
-    Sums s{};
+    auto near = [](float v) { return v > 0x1p-30f && v < 0x1p16f; };
+    auto known = [](float v) { return v > 0x1p-100f && v < 0x1p100f; };
+    Taken<EXPS> sum(guess, guess_b, c, rw.limit);
+    Sums s{guess, 0.0f, 0.0f, guess};
     bool good = sum.plain;
     if (good) {
 #pragma unroll 2
@@ -280,14 +325,19 @@ __device__ __forceinline__ Sums sums_of(uint4* slice, const Rows<TI>& rw, const 
         s = sum.sums();
         s.a = warp_sum(s.a);
         s.b = EXPS != kOne ? warp_sum(s.b) : s.a;
-        good = fine(s.a) && fine(s.b);
+        good = near(s.a) && (EXPS == kBoth ? near(s.b) : known(s.b));
     }
     if (!good) {
-        float m = -FLT_MAX;
+        const bool some = known(s.a) && (EXPS != kBoth || known(s.b));
+        if (some) sum.rest_on(s.max + __log2f(s.a) / c, EXPS == kBoth ? s.bmax + __log2f(s.b) / kLog2e : 0.0f, c, rw.limit);
+        if (!some || !sum.plain) {
+            float m = -FLT_MAX;
 #pragma unroll 4
-        for (uint32_t l = first; l < kept; l += step) m = fmaxf(m, group_max(staged<TI>(slice, room, l)));
-        m = warp_max(m);
-        sum = Taken<EXPS>(m, m, c, rw.limit);
+            for (uint32_t l = first; l < kept; l += step) m = fmaxf(m, group_max(staged<TI>(slice, room, l)));
+            m = warp_max(m);
+            sum.rest_on(m, m, c, rw.limit);
+        }
+        sum.sa = sum.sb = two(0.0f, 0.0f);
         if (sum.plain) {
 #pragma unroll 2
             for (uint32_t l = first; l < kept; l += step) sum.add(staged<TI>(slice, room, l), c);
@@ -310,7 +360,7 @@ __device__ __forceinline__ Sums sums_of(uint4* slice, const Rows<TI>& rw, const 
         for (; l < next_kept; l += step) stage_group(slice, room, np, l, rw.a.V);
     }
     if (p.count > room) {  // what does not stay in shared memory
-        const float far = kFar / (EXPS == kSquare ? kLog2e : c);
+        const float far = kFar / c;
         auto limit_of = [&] {
             if (!sum.plain) return sum.max;
             return EXPS == kBoth ? fminf(sum.max + far, sum.second.get(sum.max) + kFar / kLog2e) : sum.max + far;
@@ -331,12 +381,6 @@ __device__ __forceinline__ Sums sums_of(uint4* slice, const Rows<TI>& rw, const 
         s = join<EXPS>(sum.sums(), c, rw.limit);
     }
     return s;
-}
-
-// The base for the next row: this one's log-sum, from a sum over base `max`.
-__device__ __forceinline__ float guess_from(float max, float sum, float c, float old) {
-    const float g = max + __log2f(sum) / c;
-    return sum > 0.0f && fabsf(g) < FLT_MAX ? g : old;
 }
 
 // Stores a thread's groups of the gradient's dense part; the next row's take the
@@ -401,12 +445,12 @@ __device__ __forceinline__ void store_dense(TO* dz, uint4* slice, const Rows<TI>
 
 // The row's loss, from what the lanes' blocks know; in lane 0.
 template <int EXPS>
-__device__ __forceinline__ float loss_of(const Record& r, const Sums& w, bool mine, bool soft, float weight, const DistillArgs& a, float c, float limit) {
-    const Base ba = base_of(w.max, c, limit), bb = base_of(w.bmax, kLog2e, limit);
+__device__ __forceinline__ float loss_of(const Record& r, const Settled<EXPS>& w, bool mine, bool soft, float weight, const DistillArgs& a, float c) {
     float sum = 0.0f;
     if (mine) {
-        if (soft) sum += a.soft * (r.cross + (r.mass == 0.0f ? 0.0f : r.mass * ((w.max - r.ref) * a.inv_t + log_sum(w.a, ba, c))));
-        if (r.flags & 1) sum += a.hard * ((w.bmax - r.target) + log_sum(w.b, EXPS != kOne ? bb : ba, EXPS != kOne ? kLog2e : c));
+        if (soft) sum += a.soft * (r.cross + (r.mass == 0.0f ? 0.0f : r.mass * ((w.a.max - r.ref) * a.inv_t + log_sum(w.sa, w.a, c))));
+        const Base& b = EXPS != kOne ? w.b : w.a;
+        if (r.flags & 1) sum += a.hard * ((b.max - r.target) + log_sum(w.sb, b, EXPS != kOne ? kLog2e : c));
     }
     return warp_sum(sum) * weight;
 }
@@ -614,7 +658,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const DistillAr
     if (blocks > 1) cluster_barrier();  // before another block's records come
     else __syncthreads();
     stream_order();
-    Rows<TI> rw{a, blocks > 1 ? cluster_rank() : 0, log2_blocks, room, a.use_soft ? a.ct : kLog2e, limit, blockIdx.x >> log2_blocks, gridDim.x >> log2_blocks};
+    Rows<TI> rw{a, blocks > 1 ? cluster_rank() : 0, log2_blocks, room, a.use_soft ? a.ct : kLog2e, a.use_soft ? 1.0f / a.ct : kLn2, limit, blockIdx.x >> log2_blocks, gridDim.x >> log2_blocks};
     const tc::Wait wt{&sh.dead, faults};
     // Waits for the records of the cluster's n-th row and joins them. (Should a
     // wait run out, the rows go on with what is there: nothing else depends on it.)
@@ -627,7 +671,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const DistillAr
         if constexpr (EXPS == kBoth) bmax = lane < blocks ? sh.bases[n & 1][lane].x : bmax;
         soft = __any_sync(kAll, r.flags & 2u);  // (every block says the same)
         hard = __any_sync(kAll, r.flags & 4u);
-        return join<EXPS>({r.max, r.soft, r.hard, bmax}, rw.c, limit);
+        return Settled<EXPS>(join<EXPS>({r.max, r.soft, r.hard, bmax}, rw.c, limit), rw.c, rw.inv_c, limit);
     };
 
     if (threadIdx.x < dense_threads) {
@@ -653,11 +697,13 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const DistillAr
             arrive(kSums, threads);
             Record r;
             bool soft, hard;
-            const Sums w = joined(n, r, soft, hard);
-            guess = guess_from(w.max, w.a, rw.c, guess);
-            if (EXPS == kBoth) guess_b = guess_from(w.bmax, w.b, kLog2e, guess_b);
+            const Settled<EXPS> w = joined(n, r, soft, hard);
+            if (w.moved) {  // the next row's
+                guess = w.a.max;
+                guess_b = w.b.max;
+            }
             if constexpr (kGrad) {
-                const Factors<EXPS> f(w, soft, hard, weight, a, rw.c, limit);
+                const Factors<EXPS> f(w, soft, hard, weight, a);
                 store_dense(static_cast<TO*>(a.dz) + rw.row * a.ldd, slice, rw, f, p, kept, np, next_kept, threadIdx.x, dense_threads);
                 arrive(kStored + (n & 1), dense_threads + 32);
             }
@@ -691,9 +737,9 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const DistillAr
             }
             Record r;
             bool soft, hard;
-            const Sums w = joined(n, r, soft, hard);
+            const Settled<EXPS> w = joined(n, r, soft, hard);
             if (rw.rank == 0) {
-                const float loss = loss_of<EXPS>(r, w, lane < blocks, soft, weight, a, rw.c, limit);
+                const float loss = loss_of<EXPS>(r, w, lane < blocks, soft, weight, a, rw.c);
                 if (lane == 0) a.loss[rw.row] = soft || hard ? loss : 0.0f;
             }
         }
@@ -724,10 +770,10 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_kernel(const DistillAr
             arrive(kSums, threads);
             Record r;
             bool soft, hard;
-            const Sums w = joined(n, r, soft, hard);
+            const Settled<EXPS> w = joined(n, r, soft, hard);
             if (rw.there(rw.row + rw.step)) arrive(kSums, threads);
             if constexpr (kGrad) {
-                const Factors<EXPS> f(w, soft, hard, weight, a, rw.c, limit);
+                const Factors<EXPS> f(w, soft, hard, weight, a);
                 wait(kStored + parity, dense_threads + 32);
                 if (f.some) e.correct(static_cast<TO*>(a.dz) + rw.row * a.ldd, rw, f, p, soft);
             }
@@ -753,7 +799,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_many_kernel(const Dist
     stream_order();
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, threads = blockDim.x, warps = threads / 32;
     const uint32_t blocks = 1u << log2_blocks;
-    const Rows<TI> rw{a, blocks > 1 ? cluster_rank() : 0, log2_blocks, room, a.ct, limit, blockIdx.x >> log2_blocks, gridDim.x >> log2_blocks};
+    const Rows<TI> rw{a, blocks > 1 ? cluster_rank() : 0, log2_blocks, room, a.ct, 1.0f / a.ct, limit, blockIdx.x >> log2_blocks, gridDim.x >> log2_blocks};
     uint32_t turn = 0;
     for (uint64_t row = rw.row; rw.there(row); row += rw.step, turn ^= 1) {
         const float weight = rw.weight(row);
@@ -827,14 +873,14 @@ __global__ void __launch_bounds__(kMaxThreads, 2) distill_many_kernel(const Dist
             bmax = EXPS == kBoth ? peer_float(peer(&bases[turn], lane)) : r.max;
         }
         const bool hard = y < a.V;
-        const Sums w = join<EXPS>({r.max, r.soft, r.hard, bmax}, rw.c, limit);
+        const Settled<EXPS> w(join<EXPS>({r.max, r.soft, r.hard, bmax}, rw.c, limit), rw.c, rw.inv_c, limit);
         if (rw.rank == 0 && warp == 0) {
-            const float loss = loss_of<EXPS>(r, w, lane < blocks, some, weight, a, rw.c, limit);
+            const float loss = loss_of<EXPS>(r, w, lane < blocks, some, weight, a, rw.c);
             if (lane == 0) a.loss[row] = some || hard ? loss : 0.0f;
         }
         if constexpr (kGrad) {
             TO* dz = static_cast<TO*>(a.dz) + row * a.ldd;
-            const Factors<EXPS> f(w, some, hard, weight, a, rw.c, limit);
+            const Factors<EXPS> f(w, some, hard, weight, a);
             store_dense(dz, slice, rw, f, p, kept, p, 0, threadIdx.x, threads);
             __syncthreads();  // the elements below are stored again
             for (uint32_t k = warp; k <= a.K; k += warps) {  // a warp each, the target behind the entries
