@@ -144,8 +144,11 @@ struct Settled {
 
     __device__ __forceinline__ Settled(const Sums& w, float c, float inv_c, float limit)
         : a(base_of(w.max, c, limit)), b(base_of(w.bmax, kLog2e, limit)), sa(w.a), sb(w.b) {
-        auto fit = [](const Base& x, float s) { return x.plain && s > 0x1p-100f && s < 0x1p100f; };
-        moved = fit(a, sa) && (EXPS != kBoth || fit(b, sb));
+        // (at a temperature of 10^37 a factor of two is more than the floats)
+        auto fit = [](const Base& x, float s, float inv_c) {
+            return x.plain && s > 0x1p-100f && s < 0x1p100f && (fabsf(x.k) + 100.0f) * inv_c < FLT_MAX;
+        };
+        moved = fit(a, sa, inv_c) && (EXPS != kBoth || fit(b, sb, kLn2));
         if (!moved) return;
         const float by = move(a, sa, inv_c);
         if (EXPS == kSquare) {

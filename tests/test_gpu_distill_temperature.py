@@ -1,4 +1,6 @@
-"""s2_distill with a teacher and targets, at temperatures where its two sums have nothing to do with one another."""
+"""s2_distill at temperatures where its two sums have nothing to do with one another, and where logits hardly differ."""
+import math
+
 import pytest
 import torch
 
@@ -35,3 +37,21 @@ def test_time_does_not_depend_on_the_temperature():
     times = [(ms(3.0), ms(8.0)) for _ in range(8)][2:]
     near, far = (min(x) for x in zip(*times))
     assert far <= near * 4 / 3, (near, far)
+
+
+@pytest.mark.parametrize("V", [1003, 2000003])
+@pytest.mark.parametrize("temperature", [1e30, 8e36, 1e37, 3e38])
+def test_huge_temperatures(temperature, V):
+    """Every finite distance is next to nothing: a row is uniform, its loss log V, each probability 1 / V. (A sum of V
+    ones, V / 1000 in each of a thread's, and the twenty that join them: off by 2^-24 (V / 1000 + 20) of itself at most;
+    the exponent of the sum, log2 V, is off by 2^-22 of itself.)"""
+    z = torch.randn((40, V), generator=torch.Generator(device=DEV).manual_seed(1), device=DEV)
+    idx, t = torch.full((40, 1), 7, dtype=torch.int32, device=DEV), torch.zeros((40, 1), device=DEV)
+    loss, d = torch.empty(40, device=DEV), torch.empty((40, V), device=DEV)
+    s2.s2_distill(z, idx, t, loss, d, temperature=temperature, soft=1e30)
+    off = 2.0 ** -24 * (V / 1000 + 20 + 4 * math.log2(V))
+    assert (loss.double() / 1e30 - math.log(V)).abs().max().item() <= off * 2
+    d = d.double() * (temperature / 1e30 * V)
+    d[:, 7] += V
+    assert (d - 1).abs().max(dim=0)[0][torch.arange(V, device=DEV) != 7].max().item() <= off * 2
+    assert (d[:, 7] - 1).abs().max().item() <= off * 2 + V * 2.0 ** -23
