@@ -364,9 +364,9 @@ __device__ __forceinline__ Sums sums_of(uint4* slice, const Rows<TI>& rw, const 
     }
     if (p.count > room) {  // what does not stay in shared memory
         const float far = kFar / c;
-        auto limit_of = [&] {
+        auto limit_of = [&] {  // (finite: an infinite logit has to be seen)
             if (!sum.plain) return sum.max;
-            return EXPS == kBoth ? fminf(sum.max + far, sum.second.get(sum.max) + kFar / kLog2e) : sum.max + far;
+            return fminf(EXPS == kBoth ? fminf(sum.max + far, sum.second.get(sum.max) + kFar / kLog2e) : sum.max + far, FLT_MAX);
         };
         float above = limit_of();
         uint32_t r = first;

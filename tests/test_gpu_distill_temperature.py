@@ -55,3 +55,16 @@ def test_huge_temperatures(temperature, V):
     d[:, 7] += V
     assert (d - 1).abs().max(dim=0)[0][torch.arange(V, device=DEV) != 7].max().item() <= off * 2
     assert (d[:, 7] - 1).abs().max().item() <= off * 2 + V * 2.0 ** -23
+
+
+@pytest.mark.parametrize("temperature", [1.0, 1e30, 8e36, 1e37, 3e38])
+def test_infinite_logit_behind_what_is_kept(temperature):
+    """+infinity makes a row NaN also where it lies behind what a cluster keeps of the row."""
+    V = 2000003
+    z = torch.randn((2, V), generator=torch.Generator(device=DEV).manual_seed(1), device=DEV)
+    z[0, V - 5] = float("inf")
+    idx, t = torch.full((2, 1), 7, dtype=torch.int32, device=DEV), torch.zeros((2, 1), device=DEV)
+    loss, d = torch.empty(2, device=DEV), torch.empty((2, V), device=DEV)
+    s2.s2_distill(z, idx, t, loss, d, temperature=temperature)
+    assert bool(torch.isnan(loss[0])) and bool(torch.isnan(d[0]).all())
+    assert bool(torch.isfinite(loss[1])) and bool(torch.isfinite(d[1]).all())
