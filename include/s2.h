@@ -526,9 +526,13 @@ S2_API s2_status s2_matmul4(const uint8_t *x, uint64_t ldx, const uint8_t *x_sca
  *   A logit that is -infinity or NaN is never drawn (a mask). A row with no
  *   other gives -1. Where a row holds +infinity those tokens alone have
  *   weight, 1 each. A logit more than 3.4e38 below the largest has none.
- *   Weights are right to about 2^-35 of themselves and summed as integers, so
- *   the token does not depend on timing, nor, but for borders that close, on
- *   the arithmetic. logits need the alignment of their type only. T and V
+ *   Weights are counted in whole units of 2^-43 of the largest weight (twice
+ *   that for each factor of two of V above 2^19: at V = 2^31 2^-31), rounded to
+ *   nearest from values that are right to about 2^-35 of themselves. One below
+ *   half a unit counts as 0: such a token is not drawn, not even with u = 0, and
+ *   adds nothing to what top-p sums. The sums of units are exact, so the token
+ *   does not depend on timing; half a unit for each token is the most by which
+ *   rounding moves a sum. logits need the alignment of their type only. T and V
  *   below 2^31; V = 0 gives -1.
  */
 S2_API s2_status s2_sample(const void *logits, s2_dtype dt, uint64_t T, uint64_t V, uint64_t ld,

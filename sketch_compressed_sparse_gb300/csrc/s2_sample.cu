@@ -13,7 +13,9 @@
 // of itself moves every third border past its neighbour. A weight is therefore
 // computed to about 2^-35 of itself and rounded to a multiple of 2^-43 of the
 // largest (fewer bits where V is above 2^19), and weights are added as 64-bit
-// integers: sums are exact and do not depend on their order.
+// integers: sums are exact and do not depend on their order. A token below half
+// of that unit weighs 0 and is not drawn, not even with u = 0: among the words of a
+// row at a low temperature most are like that, and no user means one of them.
 //
 // A cluster of blocks keeps the row in shared memory (what does not fit is read
 // again) and goes over it a few times: for the maximum; for each of top-k and
