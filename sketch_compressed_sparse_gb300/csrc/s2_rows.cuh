@@ -13,6 +13,8 @@
 #include <cstdint>
 #include <mutex>
 
+#include "s2_remember.h"
+
 namespace s2 {
 namespace rows {
 
@@ -269,29 +271,30 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 // Shared memory for a slice, in few different sizes: what follows keeps an answer for each.
 inline uint64_t smem_of(uint64_t bytes) { return (bytes + 2047) / 2048 * 2048; }
 
+// A question of resident_clusters.
+struct Residency {
+    const void* fn;
+    uint64_t smem;
+    uint32_t blocks;
+    int dev, threads;
+    bool operator==(const Residency& o) const {
+        return fn == o.fn && smem == o.smem && blocks == o.blocks && dev == o.dev && threads == o.threads;
+    }
+    uint64_t hash() const {
+        return spread(spread(reinterpret_cast<uintptr_t>(fn) + smem) + (uint64_t)blocks * 4096 * 256 + (uint64_t)threads * 256 + (uint64_t)dev);
+    }
+};
+
 // Clusters of `blocks` blocks of kernel `fn` that the device holds at once, 0 if
-// none (cached); also lets the kernel use kRowSmem bytes of dynamic shared memory.
+// none (kept); also lets the kernel use kRowSmem bytes of dynamic shared memory.
 inline cudaError_t resident_clusters(const void* fn, int threads, uint32_t blocks, size_t smem, int* clusters) {
-    struct Entry {
-        int dev;
-        const void* fn;
-        int threads;
-        uint32_t blocks;
-        size_t smem;
-        int clusters;
-    };
     static std::mutex mu;
-    static Entry table[256];
-    static int used = 0;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    static Remembered<Residency, int, 512> kept;
+    Residency q{fn, smem, blocks, 0, threads};
+    cudaError_t e = cudaGetDevice(&q.dev);
     if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lock(mu);
-    for (int i = 0; i < used; ++i)
-        if (table[i].dev == dev && table[i].fn == fn && table[i].threads == threads && table[i].blocks == blocks && table[i].smem == smem) {
-            *clusters = table[i].clusters;
-            return cudaSuccess;
-        }
+    if (kept.find(q, clusters)) return cudaSuccess;
     e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowSmem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
@@ -310,7 +313,7 @@ inline cudaError_t resident_clusters(const void* fn, int threads, uint32_t block
         cudaGetLastError();  // a failed query is not a launch error
         n = 0;
     }
-    if (used < 256) table[used++] = {dev, fn, threads, blocks, smem, n};
+    kept.put(q, n);
     *clusters = n;
     return cudaSuccess;
 }
