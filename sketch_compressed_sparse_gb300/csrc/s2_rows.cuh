@@ -111,9 +111,6 @@ __device__ __forceinline__ Raw<T> load_group(const Part<T>& p, uint32_t l, uint3
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void copy4(void* dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
-}
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Starts the copy of local group l, one in the midst of the row, to its place, which only this thread reads.
@@ -134,11 +131,6 @@ __device__ __forceinline__ void stage_group(uint4* room, uint32_t size, const Pa
 #pragma unroll
         for (int h = 0; h < (int)sizeof(T) / 2; ++h) room[h * size + l] = r.w[h];
     }
-}
-// Starts a thread's copies: groups `from`, from + step, ...
-template <typename T>
-__device__ __forceinline__ void stage(uint4* room, uint32_t size, const Part<T>& p, uint32_t V, uint32_t from, uint32_t step) {
-    for (uint32_t l = from; l < p.count; l += step) stage_group(room, size, p, l, V);
 }
 template <typename T>
 __device__ __forceinline__ Raw<T> staged(const uint4* room, uint32_t size, uint32_t l) {
@@ -252,15 +244,6 @@ __device__ __forceinline__ uint64_t sum_of_blocks(const void* p, uint32_t blocks
 }
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The two halves of it; relaxed: what this warp wrote need not be seen by the others.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %cluster_nctaid.x;" : "=r"(r));
-    return r;
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;

@@ -63,7 +63,7 @@ def check(z, idx, t, y, w, dtype, ddtype, temperature, soft, hard, ld):
         losses.append(got)
         same = np.isfinite(want)
         np.testing.assert_array_equal(got[~same], want[~same])
-        np.testing.assert_array_less(np.abs(got - want)[same], (E * room + 2.0 ** -24 * np.abs(want))[same] + 1e-37)
+        np.testing.assert_array_less(np.abs(got[same] - want[same]), (E * room + 2.0 ** -24 * np.abs(want))[same] + 1e-37)
     dgot = d.double().cpu().numpy()
     np.testing.assert_array_equal(np.isnan(dgot), np.isnan(dwant))
     for r in range(T):

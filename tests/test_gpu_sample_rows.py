@@ -5,8 +5,6 @@ import pytest
 
 from tests.test_gpu_sample import check, normal, settings
 
-import torch
-
 pytestmark = pytest.mark.gpu
 
 
