@@ -541,7 +541,7 @@ S2_API s2_status s2_sample(const void *logits, s2_dtype dt, uint64_t T, uint64_t
 
 /* Weights and temperature of s2_distill. */
 typedef struct {
-    float temperature; /* of the teacher's and the student's softmax in the soft term; above 0, and 1 / temperature finite */
+    float temperature; /* of the teacher's and the student's softmax in the soft term; above 0, and log2(e) / temperature finite */
     float soft;        /* weight of the soft term (temperature^2 keeps its gradient's size) */
     float hard;        /* weight of the cross entropy with the targets */
     float scale;       /* of the gradient alone, 1 / tokens for a mean */
@@ -564,16 +564,20 @@ typedef struct {
  *   A row without entries of weight has no soft term, in the gradient neither.
  *   dlogits [T][V] of type ddt, row stride ldd, out, or null for the loss
  *   alone: scale times the derivative of loss[t] by logits[t], rounded once.
- *   A logit of -infinity has probability 0 (a mask): its gradient is 0, and a
- *   teacher's entry or target there makes the loss infinite. A row of nothing
- *   else has probability 0 everywhere. NaN and +infinity make a row NaN (the
- *   teacher's: its loss, and the gradient at its entries).
- *   A term of weight 0 is left out. Sums are float32; the result does not
- *   depend on timing (a row's last bits do on its address modulo eight
- *   elements, on its place among the others and on T). K at most
- *   S2_DISTILL_MAX_ENTRIES (fastest up to 256), T and V below 2^31
- *   (S2_ERR_UNSUPPORTED). dlogits may not overlap logits. Fastest where logits
- *   and dlogits start on 32 bytes and have the same row stride. Make the first
+ *   A logit of -infinity has probability 0 (a mask): its gradient is 0, but for
+ *   what a teacher's entry or target there subtracts, which makes the loss
+ *   infinite. A row of nothing else has probability 0 everywhere. NaN and
+ *   +infinity make a row NaN (the teacher's: its loss, and the gradient at its
+ *   entries).
+ *   A term of weight 0 is left out. Sums are float32; whatever the rows before a
+ *   row hold, an exponential is off by at most 1e-6 of itself where it matters
+ *   (its square at temperature 2 by twice that). The result does not depend on
+ *   timing (a row's last bits do on its address modulo eight elements, on its
+ *   place among the others and on T). K at most S2_DISTILL_MAX_ENTRIES; above 256
+ *   every entry is looked for in the whole list (2048 rows of 267735 bfloat16
+ *   with a gradient: 458 us with 256 entries, 1160 with 257, 4160 with 1000). T and V below 2^31 (S2_ERR_UNSUPPORTED). dlogits may not overlap
+ *   logits. Fastest where logits and dlogits start on 32 bytes and have the same
+ *   row stride; where both terms are used, at temperatures 1 and 2. Make the first
  *   call on a device before any stream capture (it looks up an address there).
  */
 #define S2_DISTILL_MAX_ENTRIES 8192u

@@ -18,10 +18,12 @@
 // that); one joins the sums and hands them to the cluster's other blocks; two see
 // to the teacher's entries, every second row each, so that these have the time of
 // two rows for loads that depend on one another. Measured: 2048 rows of 267735
-// bfloat16 with 64 entries, a target and a bfloat16 gradient 430 us (5.1 TB/s of its
-// 2.2 GB, 0.76 of a copy's rate); 2048 rows of 33278 bfloat16, the loss alone, 36 us
-// (3.8 TB/s); 200 rows of 33278 float32 with a float32 gradient 21 us, where one
-// round of rows is loaded, summed and stored with nothing beside it.
+// bfloat16 with 64 entries, a target and a bfloat16 gradient at temperature 2 432 us
+// (5.1 TB/s of its 2.2 GB, 0.76 of a copy's rate), at 1 425, at any other, where
+// each logit has two exponentials, 546; 2048 rows of 33278 bfloat16, the loss alone,
+// 36 us at temperature 2 (3.8 TB/s), 34 at 1, 42 at others; 200 rows of 33278 float32
+// with a float32 gradient 21.7 us, where one round of rows is loaded, summed and
+// stored with nothing beside it.
 #include <cfloat>
 #include <type_traits>
 
@@ -311,7 +313,10 @@ struct Factors {
 // exponent that matters is so below 32, and off by half of 2^-19 at most. (Taken as
 // far away as floats reach, a row 40 below the one before it had its loss off by up
 // to 6e-6. With one base for both sums every row was gone over three times from
-// temperature 5 on: 2048 x 267735 bfloat16 with a gradient in 780 us instead of 548.)
+// temperature 5 on: 2048 x 267735 bfloat16 with a gradient in 780 us instead of 546.
+// Taking sums again costs rows that lie 35 to 50 apart, 2048 x 33278 loss alone, 40
+// us instead of 35, and rows where one word has all but 2^-24 of the probability
+// 502 instead of 437.)
 template <typename TI, int EXPS, bool FREE>
 __device__ __forceinline__ Sums sums_of(uint4* slice, const Rows<TI>& rw, const Part<TI>& p, uint32_t kept, const Part<TI>& np,
                                         uint32_t next_kept, float guess, float guess_b, uint32_t first, uint32_t step) {

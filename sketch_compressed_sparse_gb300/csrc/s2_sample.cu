@@ -29,10 +29,10 @@
 // Few rows are bound by the passes' barriers (a cluster's takes 1 to 2 us), many by
 // instructions: a weight takes about 35, where a row that nothing filters weighs
 // each token once and top-p with every token twice. Measured: a row of 33278
-// bfloat16 with top-p 20 us; 24 rows of 267735 float32 of all kinds of settings 66,
-// of 256 rows 363; of 256 rows 120 the largest alone, 140 with min-p, 270 with no
-// filter, 250 with top-k 50, 470 with top-k 1000 and top-p, 735 with top-p alone.
-// To read them takes 38. (Two fifths of the issue slots are used; exact
+// bfloat16 with top-p 20 us; 24 rows of 267735 float32 of all kinds of settings 62 to
+// 81, by what the settings are, 256 rows 378 to 385; of 256 rows 113 the largest
+// alone, 141 with min-p, 270 with no filter, 247 with top-k 50, 460 with top-k 1000 and
+// top-p, 739 with top-p alone (460 at temperature 0.6). To read them takes 41. (Two fifths of the issue slots are used; exact
 // ends of ranges as floats, found once, spare top-p alone 10 % and cost every row
 // with top-k and every single row more.)
 #include <cfloat>
