@@ -575,9 +575,10 @@ typedef struct {
  *   timing (a row's last bits do on its address modulo eight elements, on its
  *   place among the others and on T). K at most S2_DISTILL_MAX_ENTRIES; above 256
  *   every entry is looked for in the whole list (2048 rows of 267735 bfloat16
- *   with a gradient: 458 us with 256 entries, 1160 with 257, 4160 with 1000). T and V below 2^31 (S2_ERR_UNSUPPORTED). dlogits may not overlap
- *   logits. Fastest where logits and dlogits start on 32 bytes and have the same
- *   row stride; where both terms are used, at temperatures 1 and 2. Make the first
+ *   with a gradient: 458 us with 256 entries, 1160 with 257, 4160 with 1000).
+ *   T and V below 2^31 (S2_ERR_UNSUPPORTED). dlogits may not overlap logits.
+ *   Fastest where logits and dlogits start on 32 bytes and have the same row
+ *   stride; where both terms are used, at temperatures 1 and 2. Make the first
  *   call on a device before any stream capture (it looks up an address there).
  */
 #define S2_DISTILL_MAX_ENTRIES 8192u

@@ -137,7 +137,8 @@ __device__ __forceinline__ void store_group(TO* dz, const Part<TI>& p, uint32_t 
 // A whole row's sums, moved to bases at its log-sums. A power is off by 2^-24 of
 // its exponent, which is small for the logits that matter only there, and what is
 // left of a sum is one to two: neither the gradient nor the loss depends on where
-// the sums were taken. The moves are by whole factors of two, hence exact.
+// the sums were taken. The moves are by whole factors of two, but for the rounding
+// of the base, which goes to the sum.
 template <int EXPS>
 struct Settled {
     Base a, b;
@@ -146,9 +147,10 @@ struct Settled {
 
     __device__ __forceinline__ Settled(const Sums& w, float c, float inv_c, float limit)
         : a(base_of(w.max, c, limit)), b(base_of(w.bmax, kLog2e, limit)), sa(w.a), sb(w.b) {
-        // (at a temperature of 10^37 a factor of two is more than the floats)
+        // (Bases below 2^20 are rounded by 2^-5 at most. At a temperature of 10^37 a
+        // factor of two is more than the floats. Sums elsewhere stay where they are.)
         auto fit = [](const Base& x, float s, float inv_c) {
-            return x.plain && s > 0x1p-100f && s < 0x1p100f && (fabsf(x.k) + 100.0f) * inv_c < FLT_MAX;
+            return fabsf(x.k) < 0x1p20f - 128.0f && x.plain && s > 0x1p-100f && s < 0x1p100f && (fabsf(x.k) + 100.0f) * inv_c < FLT_MAX;
         };
         moved = fit(a, sa, inv_c) && (EXPS != kBoth || fit(b, sb, kLn2));
         if (!moved) return;
@@ -157,7 +159,8 @@ struct Settled {
             const float down = __uint_as_float((254u << 23) - (__float_as_uint(w.a) & 0x7f800000u));  // 2^-n
             sb *= down;
             sb *= down;
-            sb = fmaf(sb, 2.0f * by, sb);
+            sb = fmaf(sb, by, sb);
+            sb = fmaf(sb, by, sb);
             b.max = a.max;
             b.k = 2.0f * a.k;
         } else if (EXPS == kBoth) {
@@ -166,11 +169,14 @@ struct Settled {
             sb = sa;
         }
     }
-    // s = 2^n t: t over the base k + n; that number's rounding goes to the sum.
+    // s = 2^n t: t over the base k + n. That number is rounded, by -r say, so t becomes
+    // t (1 + p), p = 2^r - 1, the series of the exponential to its fourth term: the next is
+    // below 2^-31 where |r| <= 2^-5.
     static __device__ __forceinline__ float move(Base& x, float& s, float inv_c) {
         const uint32_t bits = __float_as_uint(s);
         const float n = (float)((int)(bits >> 23) - 127), k = __fadd_rn(x.k, n), t = __fsub_rn(k, x.k);
-        const float by = kLn2 * __fadd_rn(__fsub_rn(x.k, __fsub_rn(k, t)), __fsub_rn(n, t));
+        const float r = kLn2 * __fadd_rn(__fsub_rn(x.k, __fsub_rn(k, t)), __fsub_rn(n, t));
+        const float by = fmaf(r * r, fmaf(r, fmaf(r, 1.0f / 24.0f, 1.0f / 6.0f), 0.5f), r);
         s = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
         s = fmaf(s, by, s);
         x.k = k;

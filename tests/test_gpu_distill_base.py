@@ -19,9 +19,11 @@ def dev(a, dtype):
     return torch.from_numpy(np.ascontiguousarray(a)).to(dtype).to(DEV)
 
 
+@pytest.mark.parametrize("level", [0.0, 1e3, 2e4, 3e5, -4e6, 3e7])
 @pytest.mark.parametrize("form", [(1.0, 0.0, 1.0), (1.0, 1.0, 0.0), (2.0, 1.0, 1.0), (3.0, 1.0, 1.0)])
-def test_a_row_does_not_depend_on_the_level_of_the_one_before(form):
-    """Rows that one word (or two of like weight) dominates, at levels 0 to 50 apart. With x the exponent of that
+def test_a_row_does_not_depend_on_the_level_of_the_one_before(form, level):
+    """Rows that one word (or two of like weight) dominates, at levels 0 to 50 apart, around 0 and far from it (a logit
+    is a float exactly there too, and so is its distance from one beside it). With x the exponent of that
     word over the base of its sums, at most 30, its exponential is off by 2^-22 + 2^-20 ln 2 (half a step of numbers below
     32), and 2^-22 more for what follows: 1.15e-6, and a loss (of little more than 0, or log 2) or a probability by no
     more. At temperature 2 the cross entropy's sum is of the squares of those exponentials: twice that."""
@@ -34,7 +36,7 @@ def test_a_row_does_not_depend_on_the_level_of_the_one_before(form):
     z[rows, at[:, 0]] = rng.random(T)
     two = rows % 2 == 0
     z[rows[two], at[two, 1]] = z[rows[two], at[two, 0]]
-    z = (z + rng.uniform(0, 50 * max(1.0, temperature), (T, 1))).astype(np.float32)
+    z = (z + rng.uniform(0, 50 * max(1.0, temperature), (T, 1)) + level).astype(np.float32)
     idx, t = at[:, :1], np.zeros((T, 1))
     teacher = (dev(idx, torch.int32), dev(t, torch.float32)) if soft else (None, None)
     loss, d = torch.empty(T, device=DEV), torch.empty((T, V), device=DEV)

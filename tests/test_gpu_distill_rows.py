@@ -119,6 +119,15 @@ def test_many_rows_of_a_cluster(form, K, ld, dtype, ddtype):
         np.testing.assert_allclose(a, b, rtol=4 * bound(1003), atol=1e-5)
 
 
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("far", [3e3, 1e5, 1e6, 1e8])
+def test_many_rows_far_from_zero(form, far):
+    """Logits of that size, whose sums' bases are floats up to 8 apart: what a base is rounded by is not lost."""
+    temperature, soft, hard = form
+    z, idx, t, y, w = make(2600, 1003, 9, far=far)
+    check(z, idx, t, y, w, "f32", "f32", temperature, soft, hard, 1003)
+
+
 def test_many_rows_without_a_teacher():
     z, _, _, y, w = make(2600, 1003, 0)
     check(z, None, None, y, w, "f32", "f32", 1.0, 0.0, 1.0, 1003)
